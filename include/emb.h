@@ -8,7 +8,8 @@
  * backward pass dedups the batch's rows, reduces their gradients and applies sparse
  * Adagrad to the touched rows only.  Around that path: Adagrad Decay, feature admission
  * and eviction for the hashed table, tiered storage for static tables (host tier plus an
- * HBM row cache), a cross interaction layer and an int8 row codec.
+ * HBM row cache), a cross interaction layer and an int8 row codec.  On top of it: the
+ * operators of an expert tower (rows by expert, gated norms, gradient clipping).
  *
  * Sources (web pages, by title and section):
  *  - HugeCTR interview (zhidx), section 2: embeddings map categorical IDs to vectors that
@@ -275,6 +276,126 @@ emb_status emb_quantize_rows(const float* d_x, int64_t n, int32_t d, int8_t* d_q
                              float* d_scale, void* stream);
 emb_status emb_dequantize_rows(const int8_t* d_q, const float* d_scale, int64_t n, int32_t d,
                                float* d_x, void* stream);
+
+/* ---- expert tower ----
+ * The operators of a sparsely gated mixture-of-experts tower on top of the interaction, and of
+ * its training step: rows sorted by expert and brought back, the norms, gate and scale around
+ * a residual block, and the clipping of the dense gradients.  The source pages name none of
+ * them; the formulas are stated at each call.  They need no context; every buffer is a device
+ * buffer owned by the caller.  Matrices are rows of `dim` elements, fp32 (EMB_F32) or bf16
+ * (EMB_BF16), with a row step (*_ld, in elements): an input may have any step >= 0 (0: one row
+ * for all), an output one of at least dim (any, for a single row).  Any alignment of the
+ * element type serves; bases and steps on 16-byte boundaries are faster.  Sums are fp32 or
+ * wider whatever the type, rounded once on output, and taken in a fixed order: repeated calls
+ * give the same bits.  Outputs must not overlap inputs or each other except where a call says
+ * so.  Workspaces are 16-byte aligned device buffers of at least the size the call's
+ * *_workspace function gives (0: may be NULL; -1: bad sizes); their contents need not be kept
+ * between calls, and calls that may overlap on the GPU need one each. */
+#define EMB_EXPERT_MAX 1024       /* experts */
+#define EMB_EXPERT_MAX_K 16       /* experts of one row */
+#define EMB_EXPERT_MAX_DIM 65536  /* elements of a row */
+
+/* Sort by expert.  d_ids [n][k] int64: the experts row i chose, slot i*k + j.  An id outside
+ * [0, E) drops its slot (E = num_experts).  Stable by (expert, slot), dropped slots last:
+ *   d_order   [n*k] int32: order[p] = the slot at place p
+ *   d_pos     [n*k] int32: pos[slot] = its place p, or -1 - p for a dropped slot
+ *   d_offsets [E+1] int32: offsets[e] = first place of expert e; offsets[E] = kept slots
+ * EMB_EINVAL: n < 0, k outside [1, EMB_EXPERT_MAX_K], E outside [1, EMB_EXPERT_MAX],
+ * n*k >= 2^31, a NULL buffer, a short or misaligned workspace. */
+int64_t emb_expert_sort_workspace(int64_t n, int32_t k, int32_t num_experts);
+emb_status emb_expert_sort(const int64_t* d_ids, int64_t n, int32_t k, int32_t num_experts,
+                           int32_t* d_order, int32_t* d_pos, int32_t* d_offsets, void* d_ws,
+                           int64_t ws_bytes, void* stream);
+
+/* Rows to their sorted places: xs[p] = x[order[p] / k] for p < offsets[E], zero rows after
+ * them.  d_x [n][dim], d_pos [n*k] from emb_expert_sort, d_xs [n*k][dim].  The backward sums
+ * each row's kept places: dx[i] = sum over kept j of dxs[pos[i*k + j]] (what a dropped slot's
+ * place holds is not read).  A place outside [0, n*k) is neither read nor written.
+ * EMB_EINVAL: sizes as above, dim outside [1, EMB_EXPERT_MAX_DIM], a bad dtype or row step, a
+ * NULL buffer. */
+emb_status emb_expert_dispatch(const void* d_x, int64_t x_ld, const int32_t* d_pos, int64_t n,
+                               int32_t k, int32_t dim, int32_t dtype, void* d_xs, int64_t xs_ld,
+                               void* stream);
+emb_status emb_expert_dispatch_backward(const void* d_dxs, int64_t dxs_ld, const int32_t* d_pos,
+                                        int64_t n, int32_t k, int32_t dim, int32_t dtype,
+                                        void* d_dx, int64_t dx_ld, void* stream);
+
+/* Sorted rows back to their rows, weighted: out[i] = sum over kept j of w[i][j] *
+ * ys[pos[i*k + j]] (zero for a row that kept none).  d_ys [n*k][dim], d_w fp32 [n][k],
+ * d_out [n][dim].  Backward: dys[pos] = w * dout[i] at kept places, zero rows at dropped ones
+ * (all n*k rows are written); dw[i][j] = dout[i] . ys[pos], 0 when dropped.  The weight and
+ * the sorted row of a dropped slot are not used (they may be infinite or NaN). */
+emb_status emb_expert_combine(const void* d_ys, int64_t ys_ld, const int32_t* d_pos,
+                              const float* d_w, int64_t n, int32_t k, int32_t dim, int32_t dtype,
+                              void* d_out, int64_t out_ld, void* stream);
+emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, const void* d_ys,
+                                       int64_t ys_ld, const int32_t* d_pos, const float* d_w,
+                                       int64_t n, int32_t k, int32_t dim, int32_t dtype,
+                                       void* d_dys, int64_t dys_ld, float* d_dw, void* stream);
+
+/* Gated norm: the end of one residual block and the start of the next in one pass.  Per row,
+ * with rms(v) = sqrt(mean(v^2) + eps):
+ *   x_out = x + res_scale * sigmoid(gate) * (y / rms(y) * w_post)
+ *   h     = x_out / rms(x_out) * w_pre
+ * x, x_out and their gradients are of x_dtype; y, gate, h and theirs of dtype (x_dtype F32 or,
+ * when dtype is BF16, either); the vectors w_post, res_scale, w_pre and their gradients are
+ * fp32 [dim], and a NULL one counts as ones.  d_gate: gate_cols columns, 1 (one gate for a row)
+ * or dim; NULL: no gate.  d_y NULL: no block, x_out = x (not written), only h.  d_h NULL: only
+ * x_out (h is taken from x_out before its rounding).  x_out may be x itself (same row step).
+ * Backward, from the residual stream's gradient dx_out (NULL: zero) and dh (NULL: no h), x_out
+ * and y as stored, and the same gate and vectors:
+ *   dx = dx_out + the gradient of h through the norm;  dy and dgate from dx;
+ *   dw_post, dres_scale, dw_pre: summed over the rows (fp32 [dim], overwritten).
+ * Any of its outputs may be NULL; dx may be dx_out itself (same row step).  With d_y NULL, dy,
+ * dgate, dw_post and dres_scale are NULL; with d_dh NULL, dw_pre is.
+ * EMB_EINVAL: n < 0, dim outside [1, EMB_NORM_MAX_DIM], bad types, gate_cols or row steps, eps
+ * not a positive finite number, a missing buffer, nothing to compute; the backward also for a
+ * short or misaligned workspace. */
+#define EMB_NORM_MAX_DIM 8192
+typedef struct emb_norm {
+  int64_t n;
+  int32_t dim, x_dtype, dtype, gate_cols;
+  float eps;
+  /* both directions */
+  const void* d_y;
+  const void* d_gate;
+  const float *d_w_post, *d_res_scale, *d_w_pre; /* [dim] */
+  void* d_x_out;                                 /* forward: output; backward: input */
+  int64_t y_ld, gate_ld, x_out_ld;
+  /* forward */
+  const void* d_x;
+  void* d_h;
+  int64_t x_ld, h_ld;
+  /* backward */
+  const void *d_dx_out, *d_dh;
+  void *d_dx, *d_dy, *d_dgate;
+  float *d_dw_post, *d_dres_scale, *d_dw_pre; /* [dim] */
+  int64_t dx_out_ld, dh_ld, dx_ld, dy_ld, dgate_ld;
+} emb_norm;
+emb_status emb_gated_norm(const emb_norm* args, void* stream);
+int64_t emb_gated_norm_backward_workspace(int64_t n, int32_t dim);
+emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_bytes,
+                                   void* stream);
+
+/* Global gradient norm and clipping over `count` tensors: *d_norm = sqrt(sum of g^2 over all
+ * of them), out = g * min(1, max_norm / norm).  The squares' sums are fp64 beyond groups of a
+ * few elements, so neither huge nor tiny finite gradients lose the norm.  A norm that is
+ * infinite or NaN in fp32 clips nothing: the outputs equal the gradients, and the caller sees
+ * the norm.  h_list: host array, read before the call returns; d_out may be d_src (in place) or
+ * a buffer of the same type that overlaps no other.  numel may be 0, and count too (norm 0).
+ * EMB_EINVAL: count < 0 or above EMB_CLIP_MAX_TENSORS, a negative numel, a bad dtype, a NULL or
+ * (for its type) misaligned buffer, max_norm negative or NaN (infinity: only the norm and
+ * copies), a short or misaligned workspace. */
+#define EMB_CLIP_MAX_TENSORS 65536
+typedef struct emb_tensor {
+  const void* d_src;
+  void* d_out;
+  int64_t numel;
+  int32_t dtype; /* EMB_F32 or EMB_BF16, of both buffers */
+} emb_tensor;
+int64_t emb_clip_grads_workspace(int64_t count);
+emb_status emb_clip_grads(const emb_tensor* h_list, int64_t count, float max_norm, float* d_norm,
+                          void* d_ws, int64_t ws_bytes, void* stream);
 
 /* Adagrad Decay.  DeepRec announcement, "Adagrad Decay Optimizer": the accumulator is
  * discounted by period, with one discount for every sample of a period; the rule is not

@@ -41,6 +41,23 @@ class EmbConfig(ctypes.Structure):
                 ("max_batch", ctypes.c_int64), ("max_lookups", ctypes.c_int64)]
 
 
+class EmbNorm(ctypes.Structure):
+    _P, _I64 = ctypes.c_void_p, ctypes.c_int64
+    _fields_ = [("n", _I64), ("dim", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("gate_cols", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("d_y", _P), ("d_gate", _P), ("d_w_post", _P), ("d_res_scale", _P),
+                ("d_w_pre", _P), ("d_x_out", _P), ("y_ld", _I64), ("gate_ld", _I64),
+                ("x_out_ld", _I64), ("d_x", _P), ("d_h", _P), ("x_ld", _I64), ("h_ld", _I64),
+                ("d_dx_out", _P), ("d_dh", _P), ("d_dx", _P), ("d_dy", _P), ("d_dgate", _P),
+                ("d_dw_post", _P), ("d_dres_scale", _P), ("d_dw_pre", _P), ("dx_out_ld", _I64),
+                ("dh_ld", _I64), ("dx_ld", _I64), ("dy_ld", _I64), ("dgate_ld", _I64)]
+
+
+class EmbTensor(ctypes.Structure):
+    _fields_ = [("d_src", ctypes.c_void_p), ("d_out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
 _P, _I64, _I32, _U32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32
 _SIGS = {
     "emb_status_str": ([ctypes.c_int], ctypes.c_char_p),
@@ -75,6 +92,18 @@ _SIGS = {
     "emb_prefetch": ([_P, _P, _P, _I64, _I64, _P], ctypes.c_int),
     "emb_set_tier_watermark": ([_P, _I64, _I64], ctypes.c_int),
     "emb_tier_occupancy": ([_P, ctypes.POINTER(_I64)], ctypes.c_int),
+    "emb_expert_sort_workspace": ([_I64, _I32, _I32], _I64),
+    "emb_expert_sort": ([_P, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _P], ctypes.c_int),
+    "emb_expert_dispatch": ([_P, _I64, _P, _I64, _I32, _I32, _I32, _P, _I64, _P], ctypes.c_int),
+    "emb_expert_dispatch_backward": ([_P, _I64, _P, _I64, _I32, _I32, _I32, _P, _I64, _P], ctypes.c_int),
+    "emb_expert_combine": ([_P, _I64, _P, _P, _I64, _I32, _I32, _I32, _P, _I64, _P], ctypes.c_int),
+    "emb_expert_combine_backward": ([_P, _I64, _P, _I64, _P, _P, _I64, _I32, _I32, _I32, _P, _I64,
+                                     _P, _P], ctypes.c_int),
+    "emb_gated_norm": ([ctypes.POINTER(EmbNorm), _P], ctypes.c_int),
+    "emb_gated_norm_backward_workspace": ([_I64, _I32], _I64),
+    "emb_gated_norm_backward": ([ctypes.POINTER(EmbNorm), _P, _I64, _P], ctypes.c_int),
+    "emb_clip_grads_workspace": ([_I64], _I64),
+    "emb_clip_grads": ([ctypes.POINTER(EmbTensor), _I64, ctypes.c_float, _P, _P, _I64, _P], ctypes.c_int),
     "emb_unique_keys_noalloc": ([_P, _I64, _P, _P, _P, _P], ctypes.c_int),
 }
 NOALLOC_MAX_KEYS = 524288
@@ -196,6 +225,240 @@ def _stream(stream) -> Optional[int]:
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+# ---- expert tower (context-free) ----
+EXPERT_MAX, EXPERT_MAX_K, EXPERT_MAX_DIM, NORM_MAX_DIM = 1024, 16, 65536, 8192
+
+_ROW_TYPES = {}  # torch dtype -> (EMB_F32 or EMB_BF16); filled on first use
+
+
+def _row_type(t, name: str) -> int:
+    if not _ROW_TYPES:
+        import torch
+        _ROW_TYPES[torch.float32], _ROW_TYPES[torch.bfloat16] = F32, BF16
+    code = _ROW_TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _rows(t, code: int, n: int, dim: int, name: str):
+    """(pointer, row step) of a CUDA matrix [n, dim] of the given element type; its rows may lie
+    any number of elements apart."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name}: expected a CUDA matrix")
+    if _row_type(t, name) != code:
+        raise ValueError(f"{name}: expected {'bfloat16' if code == BF16 else 'float32'}, got {t.dtype}")
+    if t.shape[0] != n or t.shape[1] != dim:
+        raise ValueError(f"{name}: {tuple(t.shape)}, expected {(n, dim)}")
+    step, inner = t.stride()
+    if inner != 1 and dim > 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent")
+    return t.data_ptr(), step if n > 1 else dim
+
+
+def _opt_rows(t, code: int, n: int, dim: int, name: str):
+    return (None, 0) if t is None else _rows(t, code, n, dim, name)
+
+
+def _vec(t, dim: int, name: str) -> Optional[int]:
+    if t is not None and t.numel() != dim:
+        raise ValueError(f"{name}: {t.numel()} elements, expected {dim}")
+    return _dptr(t, "f32", dim, name)
+
+
+def _workspace(need: int, workspace, stream, like):
+    """The caller's workspace (any contiguous CUDA tensor of enough bytes), or one from torch's
+    allocator, taken on the call's stream so that its memory is reused in that stream's order."""
+    if need <= 0:
+        return None, 0
+    if workspace is None:
+        import torch
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise ValueError(f"workspace: {have} bytes, at least {need} needed")
+    _dptr(workspace, name="workspace")
+    return workspace, have
+
+
+def expert_sort_workspace(n: int, k: int, num_experts: int) -> int:
+    """Bytes of workspace of expert_sort."""
+    return int(_lib.emb_expert_sort_workspace(n, k, num_experts))
+
+
+def expert_sort(ids, num_experts: int, order, pos, offsets, workspace=None, stream=None):
+    """Sort the slots of `ids` (int64 [n, k]: the experts each row chose; outside
+    [0, num_experts): dropped) stably by expert into `order` (int32 [n*k], slot at each place),
+    `pos` (int32 [n*k], place of each slot, -1 - place when dropped) and `offsets` (int32
+    [num_experts + 1], first place of each expert; the last: kept slots).  Asynchronous."""
+    if ids.dim() != 2:
+        raise ValueError("ids: expected a matrix [n, k]")
+    n, k = ids.shape
+    S = n * k
+    args = (_dptr(ids, "i64", S, "ids"), n, k, num_experts, _dptr(order, "i32", S, "order"),
+            _dptr(pos, "i32", S, "pos"), _dptr(offsets, "i32", num_experts + 1, "offsets"))
+    ws, have = _workspace(_lib.emb_expert_sort_workspace(n, k, num_experts), workspace, stream, ids)
+    _check("emb_expert_sort", _lib.emb_expert_sort(*args, _dptr(ws), have, _stream(stream)))
+
+
+def _slots(pos, n: int) -> int:
+    """Experts of a row: k of a pos with n * k places."""
+    S = pos.numel()
+    if n == 0:
+        if S:
+            raise ValueError(f"pos: {S} elements for no rows")
+        return 1
+    if S % n or not S:
+        raise ValueError(f"pos: {S} elements, expected a multiple of {n} rows")
+    return S // n
+
+
+def expert_dispatch(x, pos, xs, stream=None):
+    """xs[pos[i, j]] = x[i] for the kept slots, zero rows at the dropped ones' places.  x [n, d]
+    and xs [n*k, d] float32 or bfloat16, rows any step apart; pos of expert_sort."""
+    code, (n, d) = _row_type(x, "x"), x.shape
+    k = _slots(pos, n)
+    xp, xl = _rows(x, code, n, d, "x")
+    op, ol = _rows(xs, code, n * k, d, "xs")
+    _check("emb_expert_dispatch",
+           _lib.emb_expert_dispatch(xp, xl, _dptr(pos, "i32", n * k, "pos"), n, k, d, code, op, ol,
+                                    _stream(stream)))
+
+
+def expert_dispatch_backward(dxs, pos, dx, stream=None):
+    """dx[i] = sum of dxs over row i's kept places (dxs [n*k, d], dx [n, d])."""
+    code, (n, d) = _row_type(dx, "dx"), dx.shape
+    k = _slots(pos, n)
+    ip, il = _rows(dxs, code, n * k, d, "dxs")
+    op, ol = _rows(dx, code, n, d, "dx")
+    _check("emb_expert_dispatch_backward",
+           _lib.emb_expert_dispatch_backward(ip, il, _dptr(pos, "i32", n * k, "pos"), n, k, d, code,
+                                             op, ol, _stream(stream)))
+
+
+def expert_combine(ys, pos, w, out, stream=None):
+    """out[i] = sum over row i's kept slots of w[i, j] * ys[place] (ys [n*k, d], w float32
+    [n, k], out [n, d])."""
+    code, (n, d) = _row_type(out, "out"), out.shape
+    k = _slots(pos, n)
+    ip, il = _rows(ys, code, n * k, d, "ys")
+    op, ol = _rows(out, code, n, d, "out")
+    _check("emb_expert_combine",
+           _lib.emb_expert_combine(ip, il, _dptr(pos, "i32", n * k, "pos"),
+                                   _dptr(w, "f32", n * k, "w"), n, k, d, code, op, ol,
+                                   _stream(stream)))
+
+
+def expert_combine_backward(dout, ys, pos, w, dys, dw, stream=None):
+    """Gradients of expert_combine: dys [n*k, d] (zero rows at dropped places) and dw float32
+    [n, k] (0 when dropped)."""
+    code, (n, d) = _row_type(dout, "dout"), dout.shape
+    k = _slots(pos, n)
+    gp, gl = _rows(dout, code, n, d, "dout")
+    yp, yl = _rows(ys, code, n * k, d, "ys")
+    op, ol = _rows(dys, code, n * k, d, "dys")
+    _check("emb_expert_combine_backward",
+           _lib.emb_expert_combine_backward(gp, gl, yp, yl, _dptr(pos, "i32", n * k, "pos"),
+                                            _dptr(w, "f32", n * k, "w"), n, k, d, code, op, ol,
+                                            _dptr(dw, "f32", n * k, "dw"), _stream(stream)))
+
+
+def _norm_args(x, y, gate, h, eps, names):
+    """The sizes and types of a gated-norm call, from the residual stream x and the first of the
+    block's matrices that is there."""
+    code, (n, d) = _row_type(x, names[0]), x.shape
+    block = next((t for t in (y, h) if t is not None), None)
+    bcode = code if block is None else _row_type(block, "y" if y is not None else names[1])
+    a = EmbNorm(n=n, dim=d, x_dtype=code, dtype=bcode, eps=eps)
+    a.d_y, a.y_ld = _opt_rows(y, bcode, n, d, "y")
+    if gate is not None:
+        cols = gate.shape[-1]
+        if cols not in (1, d):
+            raise ValueError(f"gate: {cols} columns, expected 1 or {d}")
+        a.gate_cols = cols
+        a.d_gate, a.gate_ld = _rows(gate, bcode, n, cols, "gate")
+    return a, code, bcode, n, d
+
+
+def gated_norm(x, y, x_out, h, gate=None, w_post=None, res_scale=None, w_pre=None,
+               eps: float = 1e-6, stream=None):
+    """The end of a residual block and the start of the next in one pass:
+    x_out = x + res_scale * sigmoid(gate) * (y / rms(y) * w_post), h = x_out / rms(x_out) * w_pre.
+    x, x_out [n, d] float32 or bfloat16; y, h, gate ([n, d], or [n, 1]: one gate a row) of one
+    type, bfloat16 or as x; vectors float32 [d], None counts as ones.  y None: h from x alone;
+    h None: only x_out.  x_out may be x.  Asynchronous."""
+    a, code, bcode, n, d = _norm_args(x, y, gate, h, eps, ("x", "h"))
+    a.d_x, a.x_ld = _rows(x, code, n, d, "x")
+    a.d_x_out, a.x_out_ld = _opt_rows(x_out, code, n, d, "x_out")
+    a.d_h, a.h_ld = _opt_rows(h, bcode, n, d, "h")
+    a.d_w_post, a.d_res_scale = _vec(w_post, d, "w_post"), _vec(res_scale, d, "res_scale")
+    a.d_w_pre = _vec(w_pre, d, "w_pre")
+    _check("emb_gated_norm", _lib.emb_gated_norm(ctypes.byref(a), _stream(stream)))
+
+
+def gated_norm_backward_workspace(n: int, d: int) -> int:
+    """Bytes of workspace of gated_norm_backward."""
+    return int(_lib.emb_gated_norm_backward_workspace(n, d))
+
+
+def gated_norm_backward(dx_out, dh, x_out, y, dx, dy, gate=None, w_post=None, res_scale=None,
+                        w_pre=None, dgate=None, dw_post=None, dres_scale=None, dw_pre=None,
+                        eps: float = 1e-6, workspace=None, stream=None):
+    """Gradients of gated_norm from dx_out (None: zero) and dh (None: no h), with x_out, y, gate
+    and the vectors of the forward: dx, dy, dgate and the vectors' (float32 [d], overwritten).
+    Outputs may be None; dx may be dx_out.  Asynchronous."""
+    a, code, bcode, n, d = _norm_args(x_out, y, gate, dh, eps, ("x_out", "dh"))
+    a.d_x_out, a.x_out_ld = _rows(x_out, code, n, d, "x_out")
+    a.d_dx_out, a.dx_out_ld = _opt_rows(dx_out, code, n, d, "dx_out")
+    a.d_dh, a.dh_ld = _opt_rows(dh, bcode, n, d, "dh")
+    a.d_dx, a.dx_ld = _opt_rows(dx, code, n, d, "dx")
+    a.d_dy, a.dy_ld = _opt_rows(dy, bcode, n, d, "dy")
+    if dgate is not None:
+        a.d_dgate, a.dgate_ld = _rows(dgate, bcode, n, a.gate_cols if gate is not None else d, "dgate")
+    a.d_w_post, a.d_res_scale = _vec(w_post, d, "w_post"), _vec(res_scale, d, "res_scale")
+    a.d_w_pre, a.d_dw_post = _vec(w_pre, d, "w_pre"), _vec(dw_post, d, "dw_post")
+    a.d_dres_scale, a.d_dw_pre = _vec(dres_scale, d, "dres_scale"), _vec(dw_pre, d, "dw_pre")
+    ws, have = _workspace(_lib.emb_gated_norm_backward_workspace(n, d), workspace, stream, x_out)
+    _check("emb_gated_norm_backward",
+           _lib.emb_gated_norm_backward(ctypes.byref(a), _dptr(ws), have, _stream(stream)))
+
+
+def clip_grads_workspace(count: int) -> int:
+    """Bytes of workspace of clip_grads."""
+    return int(_lib.emb_clip_grads_workspace(count))
+
+
+def clip_grads(grads, max_norm: float, norm, out=None, workspace=None, stream=None):
+    """norm (float32 [1]) = sqrt(sum of squares over all of `grads`), and every gradient times
+    min(1, max_norm / norm), in place or into `out` (contiguous CUDA tensors, float32 or
+    bfloat16, of the gradients' types and sizes).  An infinite or NaN norm clips nothing.
+    Asynchronous."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"out: {len(outs)} tensors for {len(grads)} gradients")
+    lst = (EmbTensor * len(grads))()
+    for e, g, o in zip(lst, grads, outs):
+        if not g.is_cuda or not g.is_contiguous():
+            raise ValueError("grads: expected contiguous CUDA tensors")
+        e.dtype = _row_type(g, "grads")
+        e.numel = g.numel()
+        e.d_src = e.d_out = g.data_ptr()
+        if o is not g:
+            if not o.is_cuda or not o.is_contiguous() or o.dtype != g.dtype or o.numel() != e.numel:
+                raise ValueError("out: expected contiguous CUDA tensors of the gradients' types and sizes")
+            e.d_out = o.data_ptr()
+    np_ = _dptr(norm, "f32", 1, "norm")
+    ws, have = _workspace(_lib.emb_clip_grads_workspace(len(grads)), workspace, stream, norm)
+    _check("emb_clip_grads",
+           _lib.emb_clip_grads(lst, len(grads), float(max_norm), np_, _dptr(ws), have,
+                               _stream(stream)))
 
 
 class EmbCtx:

@@ -1102,6 +1102,164 @@ emb_status emb_dequantize_rows(const int8_t* d_q, const float* d_scale, int64_t 
                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static bool ws_ok(const void* ws, int64_t have, int64_t need) {
+  return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 15) == 0);
+}
+
+// an output's row step: rows must not overlap
+static bool out_ld_ok(int64_t ld, int64_t rows, int64_t dim) { return rows <= 1 || ld >= dim; }
+
+static bool aligned_to(const void* p, int elem) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(elem - 1)) == 0;
+}
+
+static bool expert_slots_ok(int64_t n, int32_t k) {
+  return n >= 0 && k >= 1 && k <= EMB_EXPERT_MAX_K && n <= INT32_MAX / k;
+}
+
+static bool expert_rows_ok(int64_t n, int32_t k, int32_t dim, int32_t dtype) {
+  return expert_slots_ok(n, k) && dim >= 1 && dim <= EMB_EXPERT_MAX_DIM &&
+         (dtype == EMB_F32 || dtype == EMB_BF16);
+}
+
+int64_t emb_expert_sort_workspace(int64_t n, int32_t k, int32_t num_experts) {
+  if (!expert_slots_ok(n, k) || num_experts < 1 || num_experts > EMB_EXPERT_MAX) return -1;
+  return expert_sort_workspace(n * k, num_experts);
+}
+
+emb_status emb_expert_sort(const int64_t* d_ids, int64_t n, int32_t k, int32_t num_experts,
+                           int32_t* d_order, int32_t* d_pos, int32_t* d_offsets, void* d_ws,
+                           int64_t ws_bytes, void* stream) {
+  const int64_t need = emb_expert_sort_workspace(n, k, num_experts);
+  if (need < 0 || !d_offsets || (n > 0 && (!d_ids || !d_order || !d_pos))) return EMB_EINVAL;
+  if (!ws_ok(d_ws, ws_bytes, need)) return EMB_EINVAL;
+  return check_launch(launch_expert_sort(d_ids, n * k, num_experts, d_order, d_pos, d_offsets, d_ws,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+emb_status emb_expert_dispatch(const void* d_x, int64_t x_ld, const int32_t* d_pos, int64_t n,
+                               int32_t k, int32_t dim, int32_t dtype, void* d_xs, int64_t xs_ld,
+                               void* stream) {
+  if (!expert_rows_ok(n, k, dim, dtype) || x_ld < 0 || !out_ld_ok(xs_ld, n * k, dim)) return EMB_EINVAL;
+  const int elem = dtype == EMB_BF16 ? 2 : 4;
+  if (n > 0 && (!d_x || !d_pos || !d_xs)) return EMB_EINVAL;
+  if (!aligned_to(d_x, elem) || !aligned_to(d_xs, elem)) return EMB_EINVAL;
+  return check_launch(launch_expert_dispatch(d_x, x_ld, d_pos, n, k, dim, elem, d_xs, xs_ld,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+emb_status emb_expert_dispatch_backward(const void* d_dxs, int64_t dxs_ld, const int32_t* d_pos,
+                                        int64_t n, int32_t k, int32_t dim, int32_t dtype,
+                                        void* d_dx, int64_t dx_ld, void* stream) {
+  if (!expert_rows_ok(n, k, dim, dtype) || dxs_ld < 0 || !out_ld_ok(dx_ld, n, dim)) return EMB_EINVAL;
+  const int elem = dtype == EMB_BF16 ? 2 : 4;
+  if (n > 0 && (!d_dxs || !d_pos || !d_dx)) return EMB_EINVAL;
+  if (!aligned_to(d_dxs, elem) || !aligned_to(d_dx, elem)) return EMB_EINVAL;
+  return check_launch(launch_expert_combine(d_dxs, dxs_ld, d_pos, nullptr, n, k, dim,
+                                            dtype == EMB_BF16, d_dx, dx_ld,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+emb_status emb_expert_combine(const void* d_ys, int64_t ys_ld, const int32_t* d_pos,
+                              const float* d_w, int64_t n, int32_t k, int32_t dim, int32_t dtype,
+                              void* d_out, int64_t out_ld, void* stream) {
+  if (!expert_rows_ok(n, k, dim, dtype) || ys_ld < 0 || !out_ld_ok(out_ld, n, dim)) return EMB_EINVAL;
+  const int elem = dtype == EMB_BF16 ? 2 : 4;
+  if (n > 0 && (!d_ys || !d_pos || !d_w || !d_out)) return EMB_EINVAL;
+  if (!aligned_to(d_ys, elem) || !aligned_to(d_out, elem)) return EMB_EINVAL;
+  return check_launch(launch_expert_combine(d_ys, ys_ld, d_pos, d_w, n, k, dim, dtype == EMB_BF16,
+                                            d_out, out_ld, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, const void* d_ys,
+                                       int64_t ys_ld, const int32_t* d_pos, const float* d_w,
+                                       int64_t n, int32_t k, int32_t dim, int32_t dtype,
+                                       void* d_dys, int64_t dys_ld, float* d_dw, void* stream) {
+  if (!expert_rows_ok(n, k, dim, dtype) || dout_ld < 0 || ys_ld < 0 || !out_ld_ok(dys_ld, n * k, dim))
+    return EMB_EINVAL;
+  const int elem = dtype == EMB_BF16 ? 2 : 4;
+  if (n > 0 && (!d_dout || !d_ys || !d_pos || !d_w || !d_dys || !d_dw)) return EMB_EINVAL;
+  if (!aligned_to(d_dout, elem) || !aligned_to(d_ys, elem) || !aligned_to(d_dys, elem)) return EMB_EINVAL;
+  return check_launch(launch_expert_combine_bwd(d_dout, dout_ld, d_ys, ys_ld, d_pos, d_w, n, k, dim,
+                                                dtype == EMB_BF16, d_dys, dys_ld, d_dw,
+                                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Sizes, types, steps and alignment of a gated-norm call (the buffers each direction needs are
+// checked by it).
+static bool norm_ok(const emb_norm* p) {
+  if (!p || p->n < 0 || p->dim < 1 || p->dim > EMB_NORM_MAX_DIM) return false;
+  if (p->x_dtype != EMB_F32 && p->x_dtype != EMB_BF16) return false;
+  if (p->dtype != EMB_BF16 && !(p->dtype == EMB_F32 && p->x_dtype == EMB_F32)) return false;
+  if (!(p->eps > 0.f) || !(p->eps <= 3.4028235e38f)) return false;
+  // (the buffers of an empty batch may be NULL and say nothing)
+  if (p->n > 0 && p->d_gate && (!p->d_y || (p->gate_cols != 1 && p->gate_cols != p->dim))) return false;
+  if (p->x_ld < 0 || p->y_ld < 0 || p->gate_ld < 0 || p->x_out_ld < 0 || p->h_ld < 0 ||
+      p->dx_out_ld < 0 || p->dh_ld < 0 || p->dx_ld < 0 || p->dy_ld < 0 || p->dgate_ld < 0)
+    return false;
+  const int xe = p->x_dtype == EMB_BF16 ? 2 : 4, be = p->dtype == EMB_BF16 ? 2 : 4;
+  const void* xs[] = {p->d_x, p->d_x_out, p->d_dx_out, p->d_dx};
+  const void* bs[] = {p->d_y, p->d_gate, p->d_h, p->d_dh, p->d_dy, p->d_dgate};
+  for (const void* q : xs)
+    if (!aligned_to(q, xe)) return false;
+  for (const void* q : bs)
+    if (!aligned_to(q, be)) return false;
+  return true;
+}
+
+emb_status emb_gated_norm(const emb_norm* args, void* stream) {
+  if (!norm_ok(args)) return EMB_EINVAL;
+  const emb_norm& p = *args;
+  if (p.n > 0 && ((!p.d_y && !p.d_h) || !p.d_x || (p.d_y && !p.d_x_out))) return EMB_EINVAL;
+  if (p.d_y && !out_ld_ok(p.x_out_ld, p.n, p.dim)) return EMB_EINVAL;
+  if (p.d_h && !out_ld_ok(p.h_ld, p.n, p.dim)) return EMB_EINVAL;
+  return check_launch(launch_gated_norm(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t emb_gated_norm_backward_workspace(int64_t n, int32_t dim) {
+  if (n < 0 || dim < 1 || dim > EMB_NORM_MAX_DIM) return -1;
+  return gated_norm_bwd_workspace(n, dim);
+}
+
+emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_bytes,
+                                   void* stream) {
+  if (!norm_ok(args)) return EMB_EINVAL;
+  const emb_norm& p = *args;
+  if (p.n > 0) {
+    if (!p.d_dx && !p.d_dy && !p.d_dgate && !p.d_dw_post && !p.d_dres_scale && !p.d_dw_pre)
+      return EMB_EINVAL;
+    if (!p.d_y && (p.d_dy || p.d_dw_post || p.d_dres_scale)) return EMB_EINVAL;
+    if ((!p.d_gate && p.d_dgate) || (!p.d_dh && p.d_dw_pre)) return EMB_EINVAL;
+    if (!p.d_x_out || (!p.d_dx_out && !p.d_dh)) return EMB_EINVAL;
+  }
+  if ((p.d_dx && !out_ld_ok(p.dx_ld, p.n, p.dim)) || (p.d_dy && !out_ld_ok(p.dy_ld, p.n, p.dim)) ||
+      (p.d_dgate && !out_ld_ok(p.dgate_ld, p.n, p.gate_cols)))
+    return EMB_EINVAL;
+  if (!ws_ok(d_ws, ws_bytes, gated_norm_bwd_workspace(p.n, p.dim))) return EMB_EINVAL;
+  return check_launch(launch_gated_norm_bwd(p, d_ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t emb_clip_grads_workspace(int64_t count) {
+  if (count < 0 || count > EMB_CLIP_MAX_TENSORS) return -1;
+  return clip_grads_workspace(count);
+}
+
+emb_status emb_clip_grads(const emb_tensor* h_list, int64_t count, float max_norm, float* d_norm,
+                          void* d_ws, int64_t ws_bytes, void* stream) {
+  const int64_t need = emb_clip_grads_workspace(count);
+  if (need < 0 || (count > 0 && !h_list) || !d_norm || !(max_norm >= 0.f)) return EMB_EINVAL;
+  for (int64_t i = 0; i < count; ++i) {
+    const emb_tensor& t = h_list[i];
+    if (t.numel < 0 || (t.dtype != EMB_F32 && t.dtype != EMB_BF16)) return EMB_EINVAL;
+    const int elem = t.dtype == EMB_BF16 ? 2 : 4;
+    if (t.numel > 0 && (!t.d_src || !t.d_out)) return EMB_EINVAL;
+    if (!aligned_to(t.d_src, elem) || !aligned_to(t.d_out, elem)) return EMB_EINVAL;
+  }
+  if (!ws_ok(d_ws, ws_bytes, need)) return EMB_EINVAL;
+  return check_launch(launch_clip_grads(h_list, count, max_norm, d_norm, d_ws,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int32_t emb_step_tracks_once(const emb_ctx* ctx) {
   if (!ctx) return -1;
   return ctx->once_step ? 1 : 0;

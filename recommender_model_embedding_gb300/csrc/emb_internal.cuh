@@ -302,6 +302,25 @@ cudaError_t launch_quantize_rows(const float* x, int64_t n, int d, int8_t* q, fl
                                  cudaStream_t s);
 cudaError_t launch_dequantize_rows(const int8_t* q, const float* scale, int64_t n, int d,
                                    float* x, cudaStream_t s);
+// expert tower (context-free)
+int64_t expert_sort_workspace(int64_t slots, int E);
+cudaError_t launch_expert_sort(const int64_t* ids, int64_t slots, int E, int32_t* order, int32_t* pos,
+                               int32_t* offsets, void* ws, cudaStream_t s);
+cudaError_t launch_expert_dispatch(const void* x, int64_t x_ld, const int32_t* pos, int64_t n, int k,
+                                   int dim, int elem, void* xs, int64_t xs_ld, cudaStream_t s);
+cudaError_t launch_expert_combine(const void* ys, int64_t ys_ld, const int32_t* pos, const float* w,
+                                  int64_t n, int k, int dim, int bf16, void* out, int64_t out_ld,
+                                  cudaStream_t s);
+cudaError_t launch_expert_combine_bwd(const void* dout, int64_t dout_ld, const void* ys,
+                                      int64_t ys_ld, const int32_t* pos, const float* w, int64_t n,
+                                      int k, int dim, int bf16, void* dys, int64_t dys_ld, float* dw,
+                                      cudaStream_t s);
+cudaError_t launch_gated_norm(const emb_norm& p, cudaStream_t s);
+int64_t gated_norm_bwd_workspace(int64_t n, int dim);
+cudaError_t launch_gated_norm_bwd(const emb_norm& p, void* ws, cudaStream_t s);
+int64_t clip_grads_workspace(int64_t count);
+cudaError_t launch_clip_grads(const emb_tensor* list, int64_t count, float max_norm, float* norm,
+                              void* ws, cudaStream_t s);
 cudaError_t launch_key_stats(Ctx* c, const uint32_t* rows, int64_t n, uint32_t* freq,
                              uint32_t* last, cudaStream_t s);
 

@@ -1,0 +1,239 @@
+// Global gradient norm over a list of tensors, and clipping: norm = sqrt(sum of g^2 over all
+// of them), out = g * min(1, max_norm / norm).
+//
+// Bound by HBM bandwidth: one read for the norm, then one read and one write for the scaled
+// tensors.  The list is cut into tiles of equal size, spread over the CTAs whatever the tensors'
+// sizes; the tensors' addresses travel as kernel parameters, so nothing is staged or kept.
+// Squares are summed in fp32 over at most 32 elements, those sums in fp64: a thread's,
+// the CTA's and the list's, all in a fixed order, so the norm repeats bit for bit.  A group of
+// elements whose fp32 sum overflows, or is so small that squares may have been lost, is summed
+// again in fp64, so the norm is right for gradients of any finite size.
+#include "rows_common.cuh"
+
+namespace emb {
+
+constexpr int kClipThreads = 256;
+constexpr int kClipList = 256;     // tensors of one launch
+constexpr int kClipCtasPerSm = 8;  // CTAs of one launch, at most, per SM
+constexpr int64_t kClipTile = 16384, kClipTileMin = 2048;
+
+struct ClipList {
+  const void* src[kClipList];
+  void* dst[kClipList];
+  int64_t numel[kClipList];
+  int64_t first[kClipList + 1];  // first tile of each tensor
+  uint8_t bf16[kClipList];
+  uint8_t vec[kClipList];  // 16-byte accesses
+  int count;
+  int tile;  // elements
+};
+
+// Sum of squares of N values: fp32 where that is exact enough, else fp64.
+template <int N>
+__device__ __forceinline__ double square_sum(const float (&v)[N]) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s = fmaf(v[i], v[i], s);
+  if (s < 1e37f && s > 1e-30f) return (double)s;
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) any |= __float_as_uint(v[i]) << 1;
+  if (any == 0) return 0.0;
+  double d = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) d += (double)v[i] * (double)v[i];
+  return d;
+}
+
+__device__ __forceinline__ int clip_tensor(const ClipList& l, int64_t tile) {
+  int lo = 0, hi = l.count - 1;  // last tensor whose first tile is at or before `tile`
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.first[mid] <= tile) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <typename T, int EPU>
+__device__ __forceinline__ double tile_squares(const T* p, int64_t n) {
+  constexpr int U = 16 / EPU < 4 ? 16 / EPU < 1 ? 1 : 16 / EPU : 4;
+  double acc = 0.0;
+  const int64_t packs = n / EPU;
+  for (int64_t c0 = threadIdx.x; c0 < packs; c0 += kClipThreads * U) {
+    Pack<T, EPU> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v[u].zero();
+      if (c0 + u * kClipThreads < packs) v[u].load(p + (c0 + u * kClipThreads) * EPU);
+    }
+    float f[U * EPU];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float e[EPU];
+      v[u].get(e);
+#pragma unroll
+      for (int m = 0; m < EPU; ++m) f[u * EPU + m] = e[m];
+    }
+    acc += square_sum(f);
+  }
+  if (EPU > 1)
+    for (int64_t i = packs * EPU + threadIdx.x; i < n; i += kClipThreads) {
+      Pack<T, 1> v;
+      v.load(p + i);
+      float f[1];
+      v.get(f);
+      acc += square_sum(f);
+    }
+  return acc;
+}
+
+// Sum over the CTA, the same in every thread.
+__device__ __forceinline__ double cta_sum(double v) {
+  __shared__ double sh[kClipThreads / 32];
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int w = 0; w < kClipThreads / 32; ++w) v += sh[w];
+  return v;
+}
+
+__global__ void __launch_bounds__(kClipThreads) k_clip_norm(const __grid_constant__ ClipList l,
+                                                            double* part) {
+  double acc = 0.0;
+  const int64_t tiles = l.first[l.count];
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int i = clip_tensor(l, t);
+    const int64_t at = (t - l.first[i]) * l.tile;
+    const int64_t n = l.numel[i] - at < l.tile ? l.numel[i] - at : l.tile;
+    if (l.bf16[i]) {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(l.src[i]) + at;
+      acc += l.vec[i] ? tile_squares<__nv_bfloat16, 8>(p, n) : tile_squares<__nv_bfloat16, 1>(p, n);
+    } else {
+      const float* p = static_cast<const float*>(l.src[i]) + at;
+      acc += l.vec[i] ? tile_squares<float, 4>(p, n) : tile_squares<float, 1>(p, n);
+    }
+  }
+  acc = cta_sum(acc);
+  if (threadIdx.x == 0) part[blockIdx.x] = acc;
+}
+
+template <typename T, int EPU>
+__device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, float c) {
+  constexpr int U = 4;
+  const int64_t packs = n / EPU;
+  for (int64_t c0 = threadIdx.x; c0 < packs; c0 += kClipThreads * U) {
+    Pack<T, EPU> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * kClipThreads < packs) v[u].load(p + (c0 + u * kClipThreads) * EPU);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * kClipThreads < packs) {
+        float f[EPU];
+        v[u].get(f);
+#pragma unroll
+        for (int m = 0; m < EPU; ++m) f[m] *= c;
+        v[u].set(f);
+        v[u].store(o + (c0 + u * kClipThreads) * EPU);
+      }
+  }
+  if (EPU > 1)
+    for (int64_t i = packs * EPU + threadIdx.x; i < n; i += kClipThreads) {
+      Pack<T, 1> v;
+      v.load(p + i);
+      float f[1];
+      v.get(f);
+      f[0] *= c;
+      v.set(f);
+      v.store(o + i);
+    }
+}
+
+// Every CTA adds up all `parts` itself (a few KB from L2).  The tiles are taken from the last to
+// the first: the norm's pass left the last ones in L2.
+__global__ void __launch_bounds__(kClipThreads)
+    k_clip_scale(const __grid_constant__ ClipList l, const double* part, int parts, float max_norm,
+                 float* norm_out, int inplace) {
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < parts; i += kClipThreads) acc += part[i];
+  const double norm = sqrt(cta_sum(acc));
+  const float nf = (float)norm;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = nf;
+  // a norm that is infinite or NaN scales nothing: the caller sees it and drops the step
+  const bool clip = norm > (double)max_norm && isfinite(nf);
+  if (!clip && inplace) return;
+  const float c = clip ? (float)((double)max_norm / norm) : 1.f;
+  const int64_t tiles = l.first[l.count];
+  for (int64_t t = tiles - 1 - blockIdx.x; t >= 0; t -= gridDim.x) {
+    const int i = clip_tensor(l, t);
+    const int64_t at = (t - l.first[i]) * l.tile;
+    const int64_t n = l.numel[i] - at < l.tile ? l.numel[i] - at : l.tile;
+    if (l.bf16[i]) {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(l.src[i]) + at;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(l.dst[i]) + at;
+      if (l.vec[i]) tile_scale<__nv_bfloat16, 8>(p, o, n, c);
+      else tile_scale<__nv_bfloat16, 1>(p, o, n, c);
+    } else {
+      const float* p = static_cast<const float*>(l.src[i]) + at;
+      float* o = static_cast<float*>(l.dst[i]) + at;
+      if (l.vec[i]) tile_scale<float, 4>(p, o, n, c);
+      else tile_scale<float, 1>(p, o, n, c);
+    }
+  }
+}
+
+int64_t clip_grads_workspace(int64_t count) {
+  const int64_t launches = count > 0 ? (count + kClipList - 1) / kClipList : 1;
+  return launches * device_sms() * kClipCtasPerSm * (int64_t)sizeof(double);
+}
+
+cudaError_t launch_clip_grads(const emb_tensor* list, int64_t count, float max_norm, float* norm,
+                              void* ws, cudaStream_t s) {
+  const int64_t cap = (int64_t)device_sms() * kClipCtasPerSm;
+  double* part = static_cast<double*>(ws);
+  int64_t total = 0;
+  int inplace = 1;
+  for (int64_t i = 0; i < count; ++i) {
+    total += list[i].numel;
+    if (list[i].d_out != list[i].d_src) inplace = 0;
+  }
+  // tiles small enough that a short list reaches every SM
+  int64_t tile = kClipTile;
+  while (tile > kClipTileMin && total / tile < cap / 2) tile /= 2;
+  ClipList l{};
+  l.tile = (int)tile;
+  auto fill = [&](int64_t i0) {
+    l.count = (int)(count - i0 < kClipList ? count - i0 : kClipList);
+    l.first[0] = 0;
+    for (int i = 0; i < l.count; ++i) {
+      const emb_tensor& t = list[i0 + i];
+      l.src[i] = t.d_src, l.dst[i] = t.d_out, l.numel[i] = t.numel;
+      l.bf16[i] = t.dtype == EMB_BF16;
+      l.vec[i] = rows16(t.d_src, 0, 1) && rows16(t.d_out, 0, 1);
+      l.first[i + 1] = l.first[i] + (t.numel + tile - 1) / tile;
+    }
+    const int64_t tiles = l.first[l.count];
+    return (int)(tiles < 1 ? 1 : tiles < cap ? tiles : cap);
+  };
+  int parts = 0;
+  int64_t i0 = 0;
+  do {  // an empty list still gives its norm of zero
+    const int grid = fill(i0);
+    k_clip_norm<<<grid, kClipThreads, 0, s>>>(l, part + parts);
+    parts += grid;
+    i0 += kClipList;
+  } while (i0 < count);
+  i0 = 0;
+  do {
+    const int grid = count <= kClipList ? parts : fill(i0);
+    k_clip_scale<<<grid, kClipThreads, 0, s>>>(l, part, parts, max_norm, norm, inplace);
+    i0 += kClipList;
+  } while (i0 < count);
+  return cudaGetLastError();
+}
+
+}  // namespace emb

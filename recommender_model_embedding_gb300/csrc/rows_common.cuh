@@ -1,0 +1,134 @@
+// Row access shared by the expert and gated-norm kernels: packs of EPU consecutive elements
+// of an fp32 or bf16 row (16 bytes and more where everything is 16-byte aligned, one element
+// otherwise), held as loaded and widened to fp32 where they are used.
+#pragma once
+
+#include "emb_internal.cuh"
+
+namespace emb {
+
+template <typename T, int EPU>
+struct Pack;  // raw register image of EPU elements
+
+template <>
+struct Pack<float, 1> {
+  float r;
+  __device__ __forceinline__ void load(const float* p) { r = *p; }
+  __device__ __forceinline__ void zero() { r = 0.f; }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = r; }
+  __device__ __forceinline__ void set(const float (&v)[1]) { r = v[0]; }
+  __device__ __forceinline__ void store(float* p) const { *p = r; }
+};
+
+template <>
+struct Pack<__nv_bfloat16, 1> {
+  __nv_bfloat16 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *p; }
+  __device__ __forceinline__ void zero() { r = __float2bfloat16_rn(0.f); }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = __bfloat162float(r); }
+  __device__ __forceinline__ void set(const float (&v)[1]) { r = __float2bfloat16_rn(v[0]); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *p = r; }
+};
+
+template <>
+struct Pack<float, 4> {
+  float4 r;
+  __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+  }
+  __device__ __forceinline__ void set(const float (&v)[4]) {
+    r = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = r; }
+};
+
+template <>
+struct Pack<float, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+};
+
+template <>
+struct Pack<__nv_bfloat16, 8> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // widening a bf16 is a 16-bit shift
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint4*>(p) = r;
+  }
+};
+
+// Quotient by a divisor fixed at launch: for i < 2^31, i / d = (i * mul) >> sh with
+// sh = 31 + ceil(log2 d) and mul = ceil(2^sh / d) (mul * d - 2^sh < d <= 2^(sh - 31), so the
+// excess i * (mul * d - 2^sh) / 2^sh stays below 1 and the floor is exact).
+struct FastDiv {
+  uint32_t d, mul;
+  int sh;
+  explicit FastDiv(uint32_t d_ = 1) : d(d_) {
+    int l = 0;
+    while ((1ull << l) < d) ++l;
+    sh = 31 + l;
+    mul = (uint32_t)(((1ull << sh) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t i) const {
+    return (uint32_t)(((uint64_t)i * mul) >> sh);
+  }
+};
+
+// Sum over the `tpr` lanes (a power of two <= 32) that share a row.
+__device__ __forceinline__ float lanes_sum(float v, int tpr) {
+  for (int o = tpr >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Multiprocessors of the current device (context-free calls).
+inline int device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    cudaGetLastError();
+  return sms < 1 ? 1 : sms;
+}
+
+// Whether a matrix of rows allows 16-byte accesses: base and row step on 16-byte boundaries.
+inline bool rows16(const void* p, int64_t ld, int elem) {
+  return p == nullptr || (((reinterpret_cast<uintptr_t>(p) | (uint64_t)(ld * elem)) & 15) == 0);
+}
+
+}  // namespace emb
