@@ -348,8 +348,8 @@ emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, cons
  *   dw_post, dres_scale, dw_pre: summed over the rows (fp32 [dim], overwritten).
  * Any of its outputs may be NULL; dx may be dx_out itself (same row step).  With d_y NULL, dy,
  * dgate, dw_post and dres_scale are NULL; with d_dh NULL, dw_pre is.
- * EMB_EINVAL: n < 0, dim outside [1, EMB_NORM_MAX_DIM], bad types, gate_cols or row steps, eps
- * not a positive finite number, a missing buffer, nothing to compute; the backward also for a
+ * EMB_EINVAL: n outside [0, 2^31), dim outside [1, EMB_NORM_MAX_DIM], bad types or gate_cols, a row
+ * step of 2^30 elements or more or (outputs) below dim, eps not a positive finite number, a missing buffer, nothing to compute; the backward also for a
  * short or misaligned workspace. */
 #define EMB_NORM_MAX_DIM 8192
 typedef struct emb_norm {

@@ -1188,15 +1188,15 @@ emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, cons
 // Sizes, types, steps and alignment of a gated-norm call (the buffers each direction needs are
 // checked by it).
 static bool norm_ok(const emb_norm* p) {
-  if (!p || p->n < 0 || p->dim < 1 || p->dim > EMB_NORM_MAX_DIM) return false;
+  if (!p || p->n < 0 || p->n > INT32_MAX || p->dim < 1 || p->dim > EMB_NORM_MAX_DIM) return false;
   if (p->x_dtype != EMB_F32 && p->x_dtype != EMB_BF16) return false;
   if (p->dtype != EMB_BF16 && !(p->dtype == EMB_F32 && p->x_dtype == EMB_F32)) return false;
   if (!(p->eps > 0.f) || !(p->eps <= 3.4028235e38f)) return false;
   // (the buffers of an empty batch may be NULL and say nothing)
   if (p->n > 0 && p->d_gate && (!p->d_y || (p->gate_cols != 1 && p->gate_cols != p->dim))) return false;
-  if (p->x_ld < 0 || p->y_ld < 0 || p->gate_ld < 0 || p->x_out_ld < 0 || p->h_ld < 0 ||
-      p->dx_out_ld < 0 || p->dh_ld < 0 || p->dx_ld < 0 || p->dy_ld < 0 || p->dgate_ld < 0)
-    return false;
+  for (int64_t ld : {p->x_ld, p->y_ld, p->gate_ld, p->x_out_ld, p->h_ld, p->dx_out_ld, p->dh_ld,
+                     p->dx_ld, p->dy_ld, p->dgate_ld})
+    if (ld < 0 || ld >= (1 << 30)) return false;
   const int xe = p->x_dtype == EMB_BF16 ? 2 : 4, be = p->dtype == EMB_BF16 ? 2 : 4;
   const void* xs[] = {p->d_x, p->d_x_out, p->d_dx_out, p->d_dx};
   const void* bs[] = {p->d_y, p->d_gate, p->d_h, p->d_dh, p->d_dy, p->d_dgate};
@@ -1217,7 +1217,7 @@ emb_status emb_gated_norm(const emb_norm* args, void* stream) {
 }
 
 int64_t emb_gated_norm_backward_workspace(int64_t n, int32_t dim) {
-  if (n < 0 || dim < 1 || dim > EMB_NORM_MAX_DIM) return -1;
+  if (n < 0 || n > INT32_MAX || dim < 1 || dim > EMB_NORM_MAX_DIM) return -1;
   return gated_norm_bwd_workspace(n, dim);
 }
 

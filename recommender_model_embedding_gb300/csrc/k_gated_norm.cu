@@ -35,26 +35,79 @@ constexpr int kNormMaxThreads = 512;  // of a row
 constexpr int kStages = 3;            // rows of the ring
 
 struct NormArgs {
-  int64_t n;
+  uint32_t n;
   int dim, packs, tpr;  // packs of EPU elements of a row; threads of a row
   int rpb;              // rows side by side in a CTA
   int stages;           // of the ring: 1 .. kStages
-  int gate_cols;        // 0, 1 or dim
+  int gate_row;         // one gate for a row
   float eps, inv_dim;
-  const void *x, *y, *gate, *dx_out, *dh;
-  void *x_out, *h, *dx, *dy, *dgate;
-  int64_t x_ld, y_ld, gate_ld, dx_out_ld, dh_ld, x_out_ld, h_ld, dx_ld, dy_ld, dgate_ld;
+  const char *x, *y, *gate, *dx_out, *dh;
+  char *x_out, *h, *dx, *dy, *dgate;
+  uint32_t x_st, y_st, gate_st, dx_out_st, dh_st, x_out_st, h_st, dx_st, dy_st, dgate_st;  // bytes
   const float *w_post, *res_scale, *w_pre;
   float* part;  // [CTAs][2][dim] column sums (backward)
 };
 
-// sigmoid(z) and 1 - sigmoid(z), each to a few units in the last place at either end (the
-// smaller of the two is e / (1 + e), not a difference); |z| e^-|z| < 1/2, so the fast
-// exponential's argument error stays below one unit too.
+// ---- arithmetic on N elements a thread: two at a time (fp32 pairs) where N is even ----
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
+                                     float c0, float c1) {
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// d = a * b + c, with b a vector or one factor for all
+template <int N>
+__device__ __forceinline__ void v_fma(float (&d)[N], const float (&a)[N], const float (&b)[N],
+                                      const float (&c)[N]) {
+  if constexpr (N == 1) d[0] = fmaf(a[0], b[0], c[0]);
+  else
+#pragma unroll
+    for (int m = 0; m < N; m += 2)
+      fma2(d[m], d[m + 1], a[m], a[m + 1], b[m], b[m + 1], c[m], c[m + 1]);
+}
+template <int N>
+__device__ __forceinline__ void v_fma(float (&d)[N], const float (&a)[N], float b, const float (&c)[N]) {
+  if constexpr (N == 1) d[0] = fmaf(a[0], b, c[0]);
+  else
+#pragma unroll
+    for (int m = 0; m < N; m += 2) fma2(d[m], d[m + 1], a[m], a[m + 1], b, b, c[m], c[m + 1]);
+}
+template <int N>
+__device__ __forceinline__ void v_mul(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+  if constexpr (N == 1) d[0] = a[0] * b[0];
+  else
+#pragma unroll
+    for (int m = 0; m < N; m += 2) mul2(d[m], d[m + 1], a[m], a[m + 1], b[m], b[m + 1]);
+}
+template <int N>
+__device__ __forceinline__ void v_mul(float (&d)[N], const float (&a)[N], float b) {
+  if constexpr (N == 1) d[0] = a[0] * b;
+  else
+#pragma unroll
+    for (int m = 0; m < N; m += 2) mul2(d[m], d[m + 1], a[m], a[m + 1], b, b);
+}
+// s += sum of a * b, in two halves
+template <int N>
+__device__ __forceinline__ void v_dot(float (&s)[2], const float (&a)[N], const float (&b)[N]) {
+  if constexpr (N == 1) s[0] = fmaf(a[0], b[0], s[0]);
+  else
+#pragma unroll
+    for (int m = 0; m < N; m += 2) fma2(s[0], s[1], a[m], a[m + 1], b[m], b[m + 1], s[0], s[1]);
+}
+
+// g = sigmoid(z) = 1 / (1 + e) and rest = 1 - g, with e = exp(-z), both to a few units in the
+// last place: rest is taken as e g where that difference would cancel (z >= 0).
 __device__ __forceinline__ void sigmoid2(float z, float& g, float& rest) {
-  const float e = __expf(-fabsf(z)), r = __fdividef(1.f, 1.f + e), er = e * r;
-  g = z >= 0.f ? r : er;
-  rest = z >= 0.f ? er : r;
+  float e;  // the product's rounding moves e by less than |z| units, where e is at most that small
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(1.f + e));
+  rest = z < 0.f ? 1.f - g : e * g;
 }
 
 // The ring: one plane of UB bytes a thread for each 16 bytes (or element) of a pack.
@@ -64,21 +117,27 @@ struct Slot {
   static constexpr int UB = kBytes < 16 ? kBytes : 16, kPlanes = kBytes / UB;
 
   // starts the copy of the pack at p to this thread's place of the planes from `to` on
-  static __device__ __forceinline__ void fetch(uint32_t to, uint32_t plane, const T* p) {
-    if constexpr (UB >= 4) {
+  static __device__ __forceinline__ void fetch(uint32_t to, uint32_t plane, const char* p) {
+    if constexpr (UB == 16) {
 #pragma unroll
       for (int i = 0; i < kPlanes; ++i)
-        if constexpr (UB == 16)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * plane),
-                       "l"(reinterpret_cast<const char*>(p) + i * 16) : "memory");
-        else
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * plane), "l"(p + i * 16)
+                     : "memory");
+    } else if constexpr (UB == 4) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
     } else {  // one bf16: too small for an asynchronous copy
       const uint16_t v = *reinterpret_cast<const uint16_t*>(p);
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
     }
   }
-  static __device__ __forceinline__ void read(uint32_t from, uint32_t plane, float (&v)[EPU]) {
+  static __device__ __forceinline__ void zero(uint32_t to, uint32_t plane) {
+#pragma unroll
+    for (int i = 0; i < kPlanes; ++i)
+#pragma unroll
+      for (int b = 0; b < UB; b += 2)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * plane + b), "h"((uint16_t)0) : "memory");
+  }
+  static __device__ __forceinline__ void read(uint32_t from, uint32_t plane, float* v) {
     if constexpr (UB == 16) {
       uint32_t w[4 * kPlanes];
 #pragma unroll
@@ -144,7 +203,7 @@ struct RowGroup {
 };
 
 template <int EPU>
-__device__ __forceinline__ void load_cols(const float* w, int col, float (&v)[EPU]) {
+__device__ __forceinline__ void load_cols(const float* w, int col, float* v) {
   if constexpr (EPU >= 4) {
 #pragma unroll
     for (int m = 0; m < EPU; m += 4) {
@@ -158,31 +217,39 @@ __device__ __forceinline__ void load_cols(const float* w, int col, float (&v)[EP
   }
 }
 
+// How a thread's V packs of EPU elements are taken: in NC chunks of C elements (PP packs), the
+// unit of arithmetic.
+template <int EPU, int V>
+struct Chunks {
+  static constexpr int EPT = V * EPU, C = EPT < 8 ? EPT : 8, NC = EPT / C, PP = C / EPU;
+};
+
 // res_scale * w_post and w_pre of a thread's columns: in registers for all its rows when it has
-// one pack, else loaded where they are used (from L1).
+// one chunk, else loaded where they are used (from L1).  Zero past the row's end.
 template <int EPU, int V>
 struct ColWeights {
-  static constexpr bool kKeep = V == 1 || EPU == 1;
-  static constexpr int N = kKeep ? V : 1;
-  float rw[N][EPU], wq[N][EPU];
-  __device__ __forceinline__ void load(const NormArgs& a, int i, int at) {
-    float wp[EPU];
-    load_cols<EPU>(a.w_post, at, wp);
-    load_cols<EPU>(a.res_scale, at, rw[i]);
-    load_cols<EPU>(a.w_pre, at, wq[i]);
+  using K = Chunks<EPU, V>;
+  float rw[K::C], wq[K::C];
+  __device__ __forceinline__ void load(const NormArgs& a, int sub, int chunk) {
+    float wp[K::C];
 #pragma unroll
-    for (int m = 0; m < EPU; ++m) rw[i][m] *= wp[m];
+    for (int p = 0; p < K::PP; ++p) {
+      const int c = sub + (chunk * K::PP + p) * a.tpr;
+#pragma unroll
+      for (int m = 0; m < EPU; ++m) rw[p * EPU + m] = wq[p * EPU + m] = wp[p * EPU + m] = 0.f;
+      if (c < a.packs) {
+        load_cols<EPU>(a.w_post, c * EPU, wp + p * EPU);
+        load_cols<EPU>(a.res_scale, c * EPU, rw + p * EPU);
+        load_cols<EPU>(a.w_pre, c * EPU, wq + p * EPU);
+      }
+    }
+    v_mul(rw, rw, wp);
   }
   __device__ __forceinline__ void init(const NormArgs& a, int sub) {
-    if constexpr (kKeep)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (sub + i * a.tpr < a.packs) load(a, i, (sub + i * a.tpr) * EPU);
+    if constexpr (K::NC == 1) load(a, sub, 0);
   }
-  __device__ __forceinline__ int use(const NormArgs& a, int i, int at) {
-    if constexpr (kKeep) return i;
-    load(a, 0, at);
-    return 0;
+  __device__ __forceinline__ void use(const NormArgs& a, int sub, int chunk) {
+    if constexpr (K::NC > 1) load(a, sub, chunk);
   }
 };
 
@@ -190,291 +257,310 @@ struct ColWeights {
 template <typename XT, typename BT, int EPU, int V, int XS, int BS>
 constexpr int kRingBytes = V * EPU * (XS * (int)sizeof(XT) + BS * (int)sizeof(BT));
 
+// One matrix's part of the ring, and its rows in memory: offsets and strides in bytes.
+template <typename T, int EPU, int V>
+struct Lane {
+  using S = Slot<T, EPU>;
+  using K = Chunks<EPU, V>;
+  uint32_t at, plane;  // this thread's place of the matrix in stage 0; bytes of a plane
+  __device__ __forceinline__ uint32_t pack(uint32_t stage, int i) const {
+    return at + stage + i * S::kPlanes * plane;
+  }
+  // the thread's packs of a row, into the ring (`left`: packs of the row from this thread's on)
+  __device__ __forceinline__ void fetch(uint32_t stage, const char* row, int left, int tpr) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i * tpr < left) S::fetch(pack(stage, i), plane, row + i * tpr * S::kBytes);
+  }
+  __device__ __forceinline__ void zero_tail(uint32_t stage, int left, int tpr) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i * tpr >= left) S::zero(pack(stage, i), plane);
+  }
+  __device__ __forceinline__ void read(uint32_t stage, int chunk, float (&v)[K::C]) const {
+#pragma unroll
+    for (int p = 0; p < K::PP; ++p) S::read(pack(stage, chunk * K::PP + p), plane, v + p * EPU);
+  }
+  static __device__ __forceinline__ void store(char* row, int chunk, const float (&v)[K::C], int left,
+                                               int tpr) {
+#pragma unroll
+    for (int p = 0; p < K::PP; ++p) {
+      const int i = chunk * K::PP + p;
+      if (i * tpr < left) {
+        float f[EPU];
+#pragma unroll
+        for (int m = 0; m < EPU; ++m) f[m] = v[p * EPU + m];
+        Pack<T, EPU> o;
+        o.set(f);
+        o.store(reinterpret_cast<T*>(row + i * tpr * S::kBytes));
+      }
+    }
+  }
+};
+
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-template <typename XT, typename BT, int EPU, int V>
+__device__ __forceinline__ int64_t at_row(uint32_t row, uint32_t step) {
+  return (int64_t)((uint64_t)row * step);
+}
+
+template <typename BT>
+__device__ __forceinline__ void row_gate(const NormArgs& a, uint32_t row, float& g, float& rest) {
+  Pack<BT, 1> p;
+  float z[1];
+  p.load(reinterpret_cast<const BT*>(a.gate + at_row(row, a.gate_st)));
+  p.get(z);
+  sigmoid2(z[0], g, rest);
+}
+
+// GATE: a gate for each element.
+template <typename XT, typename BT, int EPU, int V, bool GATE>
 __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm(NormArgs a) {
-  using SX = Slot<XT, EPU>;
-  using SB = Slot<BT, EPU>;
+  using K = Chunks<EPU, V>;
+  using LX = Lane<XT, EPU, V>;
+  using LB = Lane<BT, EPU, V>;
   extern __shared__ __align__(16) char ring[];
   __shared__ float red_all[2 * 16 * 16];
-  const uint32_t plx = blockDim.x * SX::UB, plb = blockDim.x * SB::UB;  // bytes of a plane
   const RowGroup grp{a.tpr, (int)threadIdx.x / a.tpr, (int)threadIdx.x % a.tpr};
   float* red = red_all + (a.tpr > 32 ? grp.id : 0) * 2 * 16;
-  const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 1, 2>;
-  const uint32_t ring0 = smem_at(ring);
-  const uint32_t ofs_y = V * SX::kPlanes * plx, ofs_g = ofs_y + V * SB::kPlanes * plb;
-  const uint32_t tx = ring0 + threadIdx.x * SX::UB, tb = ring0 + threadIdx.x * SB::UB;
-  const int64_t step = (int64_t)gridDim.x * a.rpb;
+  const int left = a.packs - grp.sub, tpr = a.tpr;
+  const uint32_t plx = blockDim.x * LX::S::UB, plb = blockDim.x * LB::S::UB;
+  const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>;
+  const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::UB;
+  const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::UB + V * LX::S::kPlanes * plx;
+  const LX lx{tx, plx};
+  const LB ly{tb, plb}, lg{tb + V * LB::S::kPlanes * plb, plb};
+  const int cx = grp.sub * LX::S::kBytes, cb = grp.sub * LB::S::kBytes;
   ColWeights<EPU, V> cw;
   cw.init(a, grp.sub);
+  for (int s = 0; s < a.stages; ++s) {
+    lx.zero_tail(s * stage_bytes, left, tpr);
+    ly.zero_tail(s * stage_bytes, left, tpr);
+    if (GATE) lg.zero_tail(s * stage_bytes, left, tpr);
+  }
 
-  auto fetch = [&](int64_t row, int stage) {
+  auto fetch = [&](uint32_t row, uint32_t stage) {
     if (row < a.n) {
-      const uint32_t sb = stage * stage_bytes;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = grp.sub + i * a.tpr;
-        if (c < a.packs) {
-          const int64_t at = (int64_t)c * EPU;
-          SX::fetch(tx + sb + i * SX::kPlanes * plx, plx, static_cast<const XT*>(a.x) + row * a.x_ld + at);
-          if (a.y)
-            SB::fetch(tb + sb + ofs_y + i * SB::kPlanes * plb, plb,
-                      static_cast<const BT*>(a.y) + row * a.y_ld + at);
-          if (a.gate_cols > 1)
-            SB::fetch(tb + sb + ofs_g + i * SB::kPlanes * plb, plb,
-                      static_cast<const BT*>(a.gate) + row * a.gate_ld + at);
-        }
-      }
+      lx.fetch(stage, a.x + at_row(row, a.x_st) + cx, left, tpr);
+      if (a.y) ly.fetch(stage, a.y + at_row(row, a.y_st) + cb, left, tpr);
+      if (GATE) lg.fetch(stage, a.gate + at_row(row, a.gate_st) + cb, left, tpr);
     }
     ring_commit();
   };
-  int64_t row = (int64_t)blockIdx.x * a.rpb + grp.id;
-  for (int s = 0; s < a.stages - 1; ++s) fetch(row + s * step, s);
-  int st = 0;
+  const uint32_t step = gridDim.x * a.rpb, last = (a.stages - 1) * stage_bytes;
+  uint32_t row = blockIdx.x * a.rpb + grp.id;
+  for (int s = 0; s < a.stages - 1; ++s) fetch(row + s * step, s * stage_bytes);
+  uint32_t st = 0;
   // every group runs as many rounds as the CTA's first: shuffles and barriers stay whole
-  for (int64_t r0 = (int64_t)blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
+  for (uint32_t r0 = blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
     const bool live = row < a.n;
-    fetch(row + (a.stages - 1) * step, st == 0 ? a.stages - 1 : st - 1);
+    fetch(row + (a.stages - 1) * step, st == 0 ? last : st - stage_bytes);
     float g_row = 1.f, rest;
-    if (a.gate_cols == 1 && live) {
-      Pack<BT, 1> p;
-      float z[1];
-      p.load(static_cast<const BT*>(a.gate) + row * a.gate_ld);
-      p.get(z);
-      sigmoid2(z[0], g_row, rest);
-    }
+    if (!GATE && a.gate_row && live) row_gate<BT>(a, row, g_row, rest);
     ring_wait(a.stages);
-    const uint32_t sb = st * stage_bytes;
-    float s[1] = {0.f}, ry = 0.f;
-    float f[V][EPU];  // y, then x_out
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = grp.sub + i * a.tpr;
-#pragma unroll
-      for (int m = 0; m < EPU; ++m) f[i][m] = 0.f;
-      if (a.y && live && c < a.packs) {
-        SB::read(tb + sb + ofs_y + i * SB::kPlanes * plb, plb, f[i]);
-#pragma unroll
-        for (int m = 0; m < EPU; ++m) s[0] = fmaf(f[i][m], f[i][m], s[0]);
-      }
-    }
+    float f[K::NC][K::C];  // x_out
+    float s[1], s2[2] = {0.f, 0.f}, ry = 0.f;
     if (a.y) {
+      if (live)
+#pragma unroll
+        for (int i = 0; i < K::NC; ++i) {
+          ly.read(st, i, f[i]);
+          v_dot(s2, f[i], f[i]);
+        }
+      s[0] = s2[0] + s2[1];
       grp.sum(s, red);
       ry = rsqrtf(s[0] * a.inv_dim + a.eps);
+      s2[0] = s2[1] = 0.f;
     }
-    s[0] = 0.f;
+    if (live)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = grp.sub + i * a.tpr;
-      if (!live || c >= a.packs) continue;
-      float x[EPU], z[EPU];
-      SX::read(tx + sb + i * SX::kPlanes * plx, plx, x);
-      if (a.y) {
-        const int w = cw.use(a, i, c * EPU);
-        if (a.gate_cols > 1) SB::read(tb + sb + ofs_g + i * SB::kPlanes * plb, plb, z);
+      for (int i = 0; i < K::NC; ++i) {
+        float x[K::C];
+        lx.read(st, i, x);
+        if (a.y) {
+          float g[K::C], y[K::C];
+          cw.use(a, grp.sub, i);
+          ly.read(st, i, y);
+          v_mul(y, y, ry);
+          if (GATE) {
+            lg.read(st, i, g);
 #pragma unroll
-        for (int m = 0; m < EPU; ++m) {
-          float g = g_row;
-          if (a.gate_cols > 1) sigmoid2(z[m], g, rest);
-          x[m] = fmaf(cw.rw[w][m] * g, f[i][m] * ry, x[m]);
+            for (int m = 0; m < K::C; ++m) sigmoid2(g[m], g[m], rest);
+            v_mul(g, g, cw.rw);
+          } else {
+            v_mul(g, cw.rw, g_row);
+          }
+          v_fma(x, g, y, x);
+          LX::store(a.x_out + at_row(row, a.x_out_st) + cx, i, x, left, tpr);
         }
-        Pack<XT, EPU> o;
-        o.set(x);
-        o.store(static_cast<XT*>(a.x_out) + row * a.x_out_ld + (int64_t)c * EPU);
-      }
+        v_dot(s2, x, x);
 #pragma unroll
-      for (int m = 0; m < EPU; ++m) {
-        f[i][m] = x[m];
-        s[0] = fmaf(x[m], x[m], s[0]);
+        for (int m = 0; m < K::C; ++m) f[i][m] = x[m];
       }
-    }
     if (a.h) {
+      s[0] = s2[0] + s2[1];
       grp.sum(s, red + 16);
       const float rx = rsqrtf(s[0] * a.inv_dim + a.eps);
+      if (live)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = grp.sub + i * a.tpr;
-        if (!live || c >= a.packs) continue;
-        const int w = cw.use(a, i, c * EPU);
-        float o[EPU];
-#pragma unroll
-        for (int m = 0; m < EPU; ++m) o[m] = f[i][m] * rx * cw.wq[w][m];
-        Pack<BT, EPU> p;
-        p.set(o);
-        p.store(static_cast<BT*>(a.h) + row * a.h_ld + (int64_t)c * EPU);
-      }
+        for (int i = 0; i < K::NC; ++i) {
+          cw.use(a, grp.sub, i);
+          v_mul(f[i], f[i], rx);
+          v_mul(f[i], f[i], cw.wq);
+          LB::store(a.h + at_row(row, a.h_st) + cb, i, f[i], left, tpr);
+        }
     }
     // a call with one sum a row leaves no second barrier between its uses of `red`
-    if ((!a.y || !a.h) && a.tpr > 32)
-      asm volatile("bar.sync %0, %1;" ::"r"(grp.id + 1), "r"(a.tpr) : "memory");
-    st = st + 1 == a.stages ? 0 : st + 1;
+    if ((!a.y || !a.h) && tpr > 32) asm volatile("bar.sync %0, %1;" ::"r"(grp.id + 1), "r"(tpr) : "memory");
+    st = st == last ? 0 : st + stage_bytes;
   }
 }
 
-template <typename XT, typename BT, int EPU, int V>
+template <typename XT, typename BT, int EPU, int V, bool GATE>
 __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm_bwd(NormArgs a) {
-  using SX = Slot<XT, EPU>;
-  using SB = Slot<BT, EPU>;
+  using K = Chunks<EPU, V>;
+  using LX = Lane<XT, EPU, V>;
+  using LB = Lane<BT, EPU, V>;
   extern __shared__ __align__(16) char ring[];
   __shared__ float red_all[4 * 16 * 16];
-  const uint32_t plx = blockDim.x * SX::UB, plb = blockDim.x * SB::UB;
   const RowGroup grp{a.tpr, (int)threadIdx.x / a.tpr, (int)threadIdx.x % a.tpr};
   float* red = red_all + (a.tpr > 32 ? grp.id : 0) * 4 * 16;
-  const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 2, 3>;
-  const uint32_t ring0 = smem_at(ring);
-  const uint32_t ofs_dx = V * SX::kPlanes * plx, ofs_dh = 2 * ofs_dx;
-  const uint32_t ofs_y = ofs_dh + V * SB::kPlanes * plb, ofs_g = ofs_y + V * SB::kPlanes * plb;
-  const uint32_t tx = ring0 + threadIdx.x * SX::UB, tb = ring0 + threadIdx.x * SB::UB;
-  const int64_t step = (int64_t)gridDim.x * a.rpb;
+  const int left = a.packs - grp.sub, tpr = a.tpr;
+  const uint32_t plx = blockDim.x * LX::S::UB, plb = blockDim.x * LB::S::UB;
+  const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>;
+  const uint32_t mx = V * LX::S::kPlanes * plx, mb = V * LB::S::kPlanes * plb;  // of a matrix
+  const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::UB;
+  const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::UB + 2 * mx;
+  const LX lx{tx, plx}, lt{tx + mx, plx};
+  const LB ld{tb, plb}, ly{tb + mb, plb}, lg{tb + 2 * mb, plb};
+  const int cx = grp.sub * LX::S::kBytes, cb = grp.sub * LB::S::kBytes;
   ColWeights<EPU, V> cw;
   cw.init(a, grp.sub);
-  float col_pre[V][EPU], col_t[V][EPU];
+  float col_pre[K::NC][K::C], col_t[K::NC][K::C];
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < K::NC; ++i)
 #pragma unroll
-    for (int m = 0; m < EPU; ++m) col_pre[i][m] = col_t[i][m] = 0.f;
+    for (int m = 0; m < K::C; ++m) col_pre[i][m] = col_t[i][m] = 0.f;
+  for (int s = 0; s < a.stages; ++s) {
+    lx.zero_tail(s * stage_bytes, left, tpr);
+    lt.zero_tail(s * stage_bytes, left, tpr);
+    ld.zero_tail(s * stage_bytes, left, tpr);
+    ly.zero_tail(s * stage_bytes, left, tpr);
+    if (GATE) lg.zero_tail(s * stage_bytes, left, tpr);
+  }
 
-  auto fetch = [&](int64_t row, int stage) {
+  auto fetch = [&](uint32_t row, uint32_t stage) {
     if (row < a.n) {
-      const uint32_t sb = stage * stage_bytes;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = grp.sub + i * a.tpr;
-        if (c < a.packs) {
-          const int64_t at = (int64_t)c * EPU;
-          const uint32_t ix = tx + sb + i * SX::kPlanes * plx, ib = tb + sb + i * SB::kPlanes * plb;
-          SX::fetch(ix, plx, static_cast<const XT*>(a.x_out) + row * a.x_out_ld + at);
-          if (a.dx_out) SX::fetch(ix + ofs_dx, plx, static_cast<const XT*>(a.dx_out) + row * a.dx_out_ld + at);
-          if (a.dh) SB::fetch(ib + ofs_dh, plb, static_cast<const BT*>(a.dh) + row * a.dh_ld + at);
-          if (a.y) SB::fetch(ib + ofs_y, plb, static_cast<const BT*>(a.y) + row * a.y_ld + at);
-          if (a.gate_cols > 1) SB::fetch(ib + ofs_g, plb, static_cast<const BT*>(a.gate) + row * a.gate_ld + at);
-        }
-      }
+      lx.fetch(stage, a.x_out + at_row(row, a.x_out_st) + cx, left, tpr);
+      if (a.dx_out) lt.fetch(stage, a.dx_out + at_row(row, a.dx_out_st) + cx, left, tpr);
+      if (a.dh) ld.fetch(stage, a.dh + at_row(row, a.dh_st) + cb, left, tpr);
+      if (a.y) ly.fetch(stage, a.y + at_row(row, a.y_st) + cb, left, tpr);
+      if (GATE) lg.fetch(stage, a.gate + at_row(row, a.gate_st) + cb, left, tpr);
     }
     ring_commit();
   };
-  int64_t row = (int64_t)blockIdx.x * a.rpb + grp.id;
-  for (int s = 0; s < a.stages - 1; ++s) fetch(row + s * step, s);
-  int st = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
+  const uint32_t step = gridDim.x * a.rpb, last = (a.stages - 1) * stage_bytes;
+  uint32_t row = blockIdx.x * a.rpb + grp.id;
+  for (int s = 0; s < a.stages - 1; ++s) fetch(row + s * step, s * stage_bytes);
+  uint32_t st = 0;
+  for (uint32_t r0 = blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
     const bool live = row < a.n;
-    fetch(row + (a.stages - 1) * step, st == 0 ? a.stages - 1 : st - 1);
+    fetch(row + (a.stages - 1) * step, st == 0 ? last : st - stage_bytes);
     float g_row = 1.f, rest_row = 0.f;
-    if (a.gate_cols == 1 && live) {
-      Pack<BT, 1> p;
-      float z[1];
-      p.load(static_cast<const BT*>(a.gate) + row * a.gate_ld);
-      p.get(z);
-      sigmoid2(z[0], g_row, rest_row);
-    }
+    if (!GATE && a.gate_row && live) row_gate<BT>(a, row, g_row, rest_row);
     ring_wait(a.stages);
-    const uint32_t sb = st * stage_bytes;
-    float s[3] = {0.f, 0.f, 0.f};  // x_out^2, dh w_pre x_out, y^2
+    float sx[2] = {0.f, 0.f}, sd[2] = {0.f, 0.f}, sy[2] = {0.f, 0.f};
+    if (live)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = grp.sub + i * a.tpr;
-      if (!live || c >= a.packs) continue;
-      const uint32_t ix = tx + sb + i * SX::kPlanes * plx, ib = tb + sb + i * SB::kPlanes * plb;
-      float x[EPU], d[EPU];
-      SX::read(ix, plx, x);
-#pragma unroll
-      for (int m = 0; m < EPU; ++m) s[0] = fmaf(x[m], x[m], s[0]);
-      if (a.dh) {
-        const int w = cw.use(a, i, c * EPU);
-        SB::read(ib + ofs_dh, plb, d);
-#pragma unroll
-        for (int m = 0; m < EPU; ++m) s[1] = fmaf(d[m] * cw.wq[w][m], x[m], s[1]);
+      for (int i = 0; i < K::NC; ++i) {
+        float x[K::C], d[K::C];
+        lx.read(st, i, x);
+        v_dot(sx, x, x);
+        if (a.dh) {
+          cw.use(a, grp.sub, i);
+          ld.read(st, i, d);
+          v_mul(d, d, cw.wq);
+          v_dot(sd, d, x);
+        }
+        if (a.y) {
+          ly.read(st, i, d);
+          v_dot(sy, d, d);
+        }
       }
-      if (a.y) {
-        SB::read(ib + ofs_y, plb, d);
-#pragma unroll
-        for (int m = 0; m < EPU; ++m) s[2] = fmaf(d[m], d[m], s[2]);
-      }
-    }
+    float s[3] = {sx[0] + sx[1], sd[0] + sd[1], sy[0] + sy[1]};
     grp.sum(s, red);
     const float rx = rsqrtf(s[0] * a.inv_dim + a.eps), ry = rsqrtf(s[2] * a.inv_dim + a.eps);
-    const float xm = rx * rx * (rx * s[1] * a.inv_dim);  // x_out * xm = q mean(dh w_pre q) / rms
-    float su[1] = {0.f};
-    float u[V][EPU];
+    const float xm = -rx * rx * (rx * s[1] * a.inv_dim);  // x_out * xm = -q mean(dh w_pre q) / rms
+    float su2[2] = {0.f, 0.f}, su[1];
+    float u[K::NC][K::C];
+    if (live)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = grp.sub + i * a.tpr;
-      if (!live || c >= a.packs) continue;
-      const int64_t at = (int64_t)c * EPU;
-      const uint32_t ix = tx + sb + i * SX::kPlanes * plx, ib = tb + sb + i * SB::kPlanes * plb;
-      const int w = cw.use(a, i, c * EPU);
-      float t[EPU];
+      for (int i = 0; i < K::NC; ++i) {
+        float t[K::C];
+        cw.use(a, grp.sub, i);
+        if (a.dx_out) lt.read(st, i, t);
+        else
 #pragma unroll
-      for (int m = 0; m < EPU; ++m) t[m] = 0.f;
-      if (a.dx_out) SX::read(ix + ofs_dx, plx, t);
-      if (a.dh) {
-        float x[EPU], d[EPU];
-        SX::read(ix, plx, x);
-        SB::read(ib + ofs_dh, plb, d);
+          for (int m = 0; m < K::C; ++m) t[m] = 0.f;
+        if (a.dh) {
+          float x[K::C], d[K::C];
+          lx.read(st, i, x);
+          ld.read(st, i, d);
+          v_mul(d, d, rx);
+          v_fma(t, d, cw.wq, t);
+          v_fma(t, x, xm, t);
+          v_fma(col_pre[i], d, x, col_pre[i]);
+        }
+        if (a.dx) LX::store(a.dx + at_row(row, a.dx_st) + cx, i, t, left, tpr);
+        if (a.y) {
+          float y[K::C], rest[K::C];
+          ly.read(st, i, y);
+          v_mul(y, y, ry);
+          if (GATE) {
+            float g[K::C];
+            lg.read(st, i, g);
 #pragma unroll
-        for (int m = 0; m < EPU; ++m) {
-          const float dr = d[m] * rx;
-          t[m] += dr * cw.wq[w][m] - x[m] * xm;
-          col_pre[i][m] = fmaf(dr, x[m], col_pre[i][m]);
+            for (int m = 0; m < K::C; ++m) sigmoid2(g[m], g[m], rest[m]);
+            v_mul(t, t, g);
+          } else {
+            v_mul(t, t, g_row);
+          }
+          v_fma(col_t[i], t, y, col_t[i]);
+          v_mul(u[i], t, cw.rw);
+          v_dot(su2, u[i], y);
+          if (GATE && a.dgate) {
+            v_mul(y, u[i], y);
+            v_mul(y, y, rest);
+            LB::store(a.dgate + at_row(row, a.dgate_st) + cb, i, y, left, tpr);
+          }
         }
       }
-      if (a.dx) {
-        Pack<XT, EPU> o;
-        o.set(t);
-        o.store(static_cast<XT*>(a.dx) + row * a.dx_ld + at);
-      }
-      if (a.y) {
-        float y[EPU], z[EPU];
-        SB::read(ib + ofs_y, plb, y);
-        if (a.gate_cols > 1) SB::read(ib + ofs_g, plb, z);
-#pragma unroll
-        for (int m = 0; m < EPU; ++m) {
-          float g = g_row, rest = 0.f;
-          if (a.gate_cols > 1) sigmoid2(z[m], g, rest);
-          const float yn = y[m] * ry, tg = t[m] * g;
-          col_t[i][m] = fmaf(tg, yn, col_t[i][m]);
-          u[i][m] = tg * cw.rw[w][m];
-          const float uy = u[i][m] * yn;
-          su[0] += uy;
-          z[m] = uy * rest;
-        }
-        if (a.gate_cols > 1 && a.dgate) {
-          Pack<BT, EPU> o;
-          o.set(z);
-          o.store(static_cast<BT*>(a.dgate) + row * a.dgate_ld + at);
-        }
-      }
-    }
     if (a.y) {
+      su[0] = su2[0] + su2[1];
       grp.sum(su, red + 3 * 16);
       // one gate a row: sum of t res_scale w_post a g, times 1 - g
-      if (a.gate_cols == 1 && a.dgate && live && grp.sub == 0) {
+      if (!GATE && a.gate_row && a.dgate && live && grp.sub == 0) {
         Pack<BT, 1> p;
         const float z[1] = {su[0] * rest_row};
         p.set(z);
-        p.store(static_cast<BT*>(a.dgate) + row * a.dgate_ld);
+        p.store(reinterpret_cast<BT*>(a.dgate + at_row(row, a.dgate_st)));
       }
-      const float um = ry * su[0] * a.inv_dim;
-      if (a.dy)
+      const float um = -ry * ry * su[0] * a.inv_dim;
+      if (a.dy && live)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c = grp.sub + i * a.tpr;
-          if (!live || c >= a.packs) continue;
-          float y[EPU];
-          SB::read(tb + sb + i * SB::kPlanes * plb + ofs_y, plb, y);
-#pragma unroll
-          for (int m = 0; m < EPU; ++m) y[m] = ry * (u[i][m] - y[m] * um);
-          Pack<BT, EPU> o;
-          o.set(y);
-          o.store(static_cast<BT*>(a.dy) + row * a.dy_ld + (int64_t)c * EPU);
+        for (int i = 0; i < K::NC; ++i) {
+          float y[K::C];
+          ly.read(st, i, y);
+          v_mul(y, y, um);
+          v_fma(y, u[i], ry, y);
+          LB::store(a.dy + at_row(row, a.dy_st) + cb, i, y, left, tpr);
         }
-    } else if (a.tpr > 32) {  // one sum a row: no second barrier between its uses of `red`
-      asm volatile("bar.sync %0, %1;" ::"r"(grp.id + 1), "r"(a.tpr) : "memory");
+    } else if (tpr > 32) {  // one sum a row: no second barrier between its uses of `red`
+      asm volatile("bar.sync %0, %1;" ::"r"(grp.id + 1), "r"(tpr) : "memory");
     }
-    st = st + 1 == a.stages ? 0 : st + 1;
+    st = st == last ? 0 : st + stage_bytes;
   }
   ring_wait_n<0>();
   // the CTA's column sums: its groups are added one after another in shared memory
@@ -485,12 +571,11 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm_bwd(NormArgs a) 
     if (grp.id != r) continue;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = grp.sub + i * a.tpr;
-      if (c >= a.packs) continue;
+      if (i * tpr >= left) continue;
 #pragma unroll
       for (int m = 0; m < EPU; ++m) {
-        const int k = c * EPU + m;
-        float p = col_pre[i][m], q = col_t[i][m];
+        const int k = (grp.sub + i * tpr) * EPU + m, e = i * EPU + m;
+        float p = col_pre[e / K::C][e % K::C], q = col_t[e / K::C][e % K::C];
         if (r > 0) p += cols[k], q += cols[a.dim + k];
         if (r < a.rpb - 1) cols[k] = p, cols[a.dim + k] = q;
         else out[k] = p, out[a.dim + k] = q;
@@ -542,11 +627,12 @@ static void norm_shape(NormArgs& a, int epu) {
   a.rpb = a.tpr >= kNormThreads ? 1 : kNormThreads / a.tpr;
 }
 
-// Ring stages that fit, and their bytes: up to kStages within a CTA's shared memory.
+// Ring stages and their bytes: up to kStages, but no fewer than two CTAs an SM for it while two
+// stages are left, and at least one.
 static int norm_ring(NormArgs& a, int thread_bytes) {
   const int per = a.rpb * a.tpr * thread_bytes, most = 220 * 1024;
   a.stages = kStages;
-  while (a.stages > 1 && a.stages * per > most) --a.stages;
+  while (a.stages > 1 && a.stages * per > (a.stages > 2 ? most / 2 : most)) --a.stages;
   return a.stages * per;
 }
 
@@ -561,14 +647,20 @@ static int norm_ctas(K kern, int threads, int smem, cudaError_t* e) {
 }
 
 static NormArgs norm_args(const emb_norm& p) {
+  const int xe = p.x_dtype == EMB_BF16 ? 2 : 4, be = p.dtype == EMB_BF16 ? 2 : 4;
+  const auto in = [](const void* q) { return static_cast<const char*>(q); };
+  const auto out = [](void* q) { return static_cast<char*>(q); };
   NormArgs a{};
-  a.n = p.n, a.dim = p.dim, a.gate_cols = p.d_gate ? p.gate_cols : 0;
+  a.n = (uint32_t)p.n, a.dim = p.dim, a.gate_row = p.d_gate && p.gate_cols == 1;
   a.eps = p.eps, a.inv_dim = 1.f / (float)p.dim;
-  a.x = p.d_x, a.y = p.d_y, a.gate = p.d_gate, a.dx_out = p.d_dx_out, a.dh = p.d_dh;
-  a.x_out = p.d_x_out, a.h = p.d_h, a.dx = p.d_dx, a.dy = p.d_dy, a.dgate = p.d_dgate;
-  a.x_ld = p.x_ld, a.y_ld = p.y_ld, a.gate_ld = p.gate_ld, a.dx_out_ld = p.dx_out_ld;
-  a.dh_ld = p.dh_ld, a.x_out_ld = p.x_out_ld, a.h_ld = p.h_ld, a.dx_ld = p.dx_ld;
-  a.dy_ld = p.dy_ld, a.dgate_ld = p.dgate_ld;
+  a.x = in(p.d_x), a.y = in(p.d_y), a.gate = in(p.d_gate), a.dx_out = in(p.d_dx_out), a.dh = in(p.d_dh);
+  a.x_out = out(p.d_x_out), a.h = out(p.d_h), a.dx = out(p.d_dx), a.dy = out(p.d_dy);
+  a.dgate = out(p.d_dgate);
+  a.x_st = (uint32_t)(p.x_ld * xe), a.x_out_st = (uint32_t)(p.x_out_ld * xe);
+  a.dx_out_st = (uint32_t)(p.dx_out_ld * xe), a.dx_st = (uint32_t)(p.dx_ld * xe);
+  a.y_st = (uint32_t)(p.y_ld * be), a.gate_st = (uint32_t)(p.gate_ld * be);
+  a.h_st = (uint32_t)(p.h_ld * be), a.dh_st = (uint32_t)(p.dh_ld * be);
+  a.dy_st = (uint32_t)(p.dy_ld * be), a.dgate_st = (uint32_t)(p.dgate_ld * be);
   a.w_post = p.d_w_post, a.res_scale = p.d_res_scale, a.w_pre = p.d_w_pre;
   return a;
 }
@@ -585,14 +677,14 @@ static bool norm_vec(const emb_norm& p) {
          rows16(p.d_res_scale, 0, 4) && rows16(p.d_w_pre, 0, 4);
 }
 
-template <typename XT, typename BT, int EPU, int V>
+template <typename XT, typename BT, int EPU, int V, bool GATE>
 static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
-  const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, 2>), threads = a.rpb * a.tpr;
+  const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>), threads = a.rpb * a.tpr;
+  const auto kern = k_gated_norm<XT, BT, EPU, V, GATE>;
   cudaError_t e;
-  const int64_t blocks = (a.n + a.rpb - 1) / a.rpb;
-  const int64_t cap = norm_ctas(k_gated_norm<XT, BT, EPU, V>, threads, smem, &e);
+  const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = norm_ctas(kern, threads, smem, &e);
   if (e != cudaSuccess) return e;
-  k_gated_norm<XT, BT, EPU, V><<<(int)(blocks < cap ? blocks : cap), threads, smem, s>>>(a);
+  kern<<<(int)(blocks < cap ? blocks : cap), threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -612,17 +704,18 @@ int64_t gated_norm_bwd_workspace(int64_t n, int dim) {
   return norm_bwd_grid(n, a.rpb, (int64_t)device_sms() * kNormCtasPerSm) * 2 * dim * (int64_t)sizeof(float);
 }
 
-template <typename XT, typename BT, int EPU, int V>
+template <typename XT, typename BT, int EPU, int V, bool GATE>
 static cudaError_t norm_bwd_v(NormArgs& a, int* grid, cudaStream_t s) {
-  int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, 3>);
+  int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>);
   const int threads = a.rpb * a.tpr, cols = a.rpb > 1 ? 2 * a.dim * (int)sizeof(float) : 0;
   if (smem < cols) smem = cols;
+  const auto kern = k_gated_norm_bwd<XT, BT, EPU, V, GATE>;
   cudaError_t e;
-  int64_t cap = norm_ctas(k_gated_norm_bwd<XT, BT, EPU, V>, threads, smem, &e);
+  int64_t cap = norm_ctas(kern, threads, smem, &e);
   if (e != cudaSuccess) return e;
   if (cap > (int64_t)device_sms() * kNormCtasPerSm) cap = (int64_t)device_sms() * kNormCtasPerSm;
   *grid = (int)norm_bwd_grid(a.n, a.rpb, cap);
-  k_gated_norm_bwd<XT, BT, EPU, V><<<*grid, threads, smem, s>>>(a);
+  kern<<<*grid, threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -632,8 +725,11 @@ static cudaError_t norm_t(NormArgs& a, int* grid, cudaStream_t s) {
   if constexpr (V == 1) norm_shape(a, EPU);
   if constexpr (V * EPU < 16)
     if ((a.packs + a.tpr - 1) / a.tpr > V) return norm_t<XT, BT, EPU, BWD, 2 * V>(a, grid, s);
-  if constexpr (BWD) return norm_bwd_v<XT, BT, EPU, V>(a, grid, s);
-  else return norm_fwd_v<XT, BT, EPU, V>(a, s);
+  const bool gate = a.gate && !a.gate_row;
+  if constexpr (BWD)
+    return gate ? norm_bwd_v<XT, BT, EPU, V, true>(a, grid, s) : norm_bwd_v<XT, BT, EPU, V, false>(a, grid, s);
+  else
+    return gate ? norm_fwd_v<XT, BT, EPU, V, true>(a, s) : norm_fwd_v<XT, BT, EPU, V, false>(a, s);
 }
 
 template <bool BWD>
