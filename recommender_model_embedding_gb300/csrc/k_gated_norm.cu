@@ -30,8 +30,8 @@
 
 namespace emb {
 
-constexpr int kNormThreads = 256;     // of a CTA, unless a row takes more
-constexpr int kNormMaxThreads = 512;  // of a row
+constexpr int kNormThreads = 256;  // of a CTA (8 elements a thread)
+constexpr int kNormWide = 512;     // of a CTA whose rows take 16 elements a thread, at most
 constexpr int kStages = 3;            // rows of the ring
 
 struct NormArgs {
@@ -175,28 +175,54 @@ __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_gr
 // The threads of one row: group `id` of the CTA, thread `sub` of tpr.
 struct RowGroup {
   int tpr, id, sub;
-  // Sums of NS values over the group, the same in every thread.  `red`: NS * 16 floats of the
-  // group's own, not used again before another sum of the group has passed its barrier.
+  // Sums of NS (1 or 3) values over the group, the same in every thread.  `red`: the group's own
+  // NS * 16 floats, 16-byte aligned, zero past its warps and not used again before another
+  // sum of the group has passed its barrier.
   template <int NS>
   __device__ __forceinline__ void sum(float (&v)[NS], float* red) const {
-    const int width = tpr < 32 ? tpr : 32;
+    static_assert(NS == 1 || NS == 3, "one or three sums");
+    if (tpr < 32) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) v[i] = lanes_sum(v[i], width);
-    if (tpr > 32) {
-      const int lane = sub & 31, warp = sub >> 5, warps = tpr >> 5;
-      if (lane == 0)
+      for (int i = 0; i < NS; ++i) v[i] = lanes_sum(v[i], tpr);
+      return;
+    }
+    const int lane = threadIdx.x & 31;
+    float r = v[0];
+    if constexpr (NS == 3) {
+      // three sums in one: lanes 0-7, 16-23 and 8-15 (24-31) end with v[0], v[1] and v[2]
+      const bool up = lane & 16, odd = lane & 8;
+      r = (up ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[1], 16);
+      const float c = v[2] + __shfl_xor_sync(0xFFFFFFFFu, v[2], 16);
+      r = (odd ? c : r) + __shfl_xor_sync(0xFFFFFFFFu, odd ? r : c, 8);
+    } else {
+      r += __shfl_xor_sync(0xFFFFFFFFu, r, 16);
+      r += __shfl_xor_sync(0xFFFFFFFFu, r, 8);
+    }
+    r += __shfl_xor_sync(0xFFFFFFFFu, r, 4);
+    r += __shfl_xor_sync(0xFFFFFFFFu, r, 2);
+    r += __shfl_xor_sync(0xFFFFFFFFu, r, 1);
+    if (tpr == 32) {
+      v[0] = __shfl_sync(0xFFFFFFFFu, r, 0);
+      if constexpr (NS == 3) {
+        v[1] = __shfl_sync(0xFFFFFFFFu, r, 16);
+        v[2] = __shfl_sync(0xFFFFFFFFu, r, 8);
+      }
+      return;
+    }
+    if (lane == 0) red[sub >> 5] = r;
+    if constexpr (NS == 3) {
+      if (lane == 16) red[16 + (sub >> 5)] = r;
+      if (lane == 8) red[32 + (sub >> 5)] = r;
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(tpr) : "memory");
 #pragma unroll
-        for (int i = 0; i < NS; ++i) red[i * 16 + warp] = v[i];
-      asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(tpr) : "memory");
-      if (warps <= 4) {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          v[i] = red[i * 16];
-          for (int w = 1; w < warps; ++w) v[i] += red[i * 16 + w];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) v[i] = lanes_sum(lane < warps ? red[i * 16 + lane] : 0.f, 32);
+    for (int i = 0; i < NS; ++i) {
+      const float4* q = reinterpret_cast<const float4*>(red + i * 16);
+      float4 f = q[0];
+      v[i] = (f.x + f.y) + (f.z + f.w);
+      for (int w = 1; w * 128 < tpr; ++w) {
+        f = q[w];
+        v[i] += (f.x + f.y) + (f.z + f.w);
       }
     }
   }
@@ -302,27 +328,30 @@ __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-__device__ __forceinline__ int64_t at_row(uint32_t row, uint32_t step) {
-  return (int64_t)((uint64_t)row * step);
+// a thread's place in a row: base + row * step + ofs (one 32 x 32 + 64-bit multiply-add and a sum)
+template <typename P>
+__device__ __forceinline__ P at_row(P base, uint32_t row, uint32_t step, uint64_t ofs = 0) {
+  return base + ((uint64_t)row * step + ofs);
 }
 
 template <typename BT>
 __device__ __forceinline__ void row_gate(const NormArgs& a, uint32_t row, float& g, float& rest) {
   Pack<BT, 1> p;
   float z[1];
-  p.load(reinterpret_cast<const BT*>(a.gate + at_row(row, a.gate_st)));
+  p.load(reinterpret_cast<const BT*>(at_row(a.gate, row, a.gate_st)));
   p.get(z);
   sigmoid2(z[0], g, rest);
 }
 
 // GATE: a gate for each element.
 template <typename XT, typename BT, int EPU, int V, bool GATE>
-__global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm(NormArgs a) {
+__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EPU > 8 ? 1 : 4) k_gated_norm(NormArgs a) {
   using K = Chunks<EPU, V>;
   using LX = Lane<XT, EPU, V>;
   using LB = Lane<BT, EPU, V>;
   extern __shared__ __align__(16) char ring[];
-  __shared__ float red_all[2 * 16 * 16];
+  __shared__ __align__(16) float red_all[8 * 2 * 16];
+  for (int i = threadIdx.x; i < 8 * 2 * 16; i += blockDim.x) red_all[i] = 0.f;
   const RowGroup grp{a.tpr, (int)threadIdx.x / a.tpr, (int)threadIdx.x % a.tpr};
   float* red = red_all + (a.tpr > 32 ? grp.id : 0) * 2 * 16;
   const int left = a.packs - grp.sub, tpr = a.tpr;
@@ -332,7 +361,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm(NormArgs a) {
   const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::UB + V * LX::S::kPlanes * plx;
   const LX lx{tx, plx};
   const LB ly{tb, plb}, lg{tb + V * LB::S::kPlanes * plb, plb};
-  const int cx = grp.sub * LX::S::kBytes, cb = grp.sub * LB::S::kBytes;
+  const uint64_t cx = (uint32_t)grp.sub * LX::S::kBytes, cb = (uint32_t)grp.sub * LB::S::kBytes;
   ColWeights<EPU, V> cw;
   cw.init(a, grp.sub);
   for (int s = 0; s < a.stages; ++s) {
@@ -340,12 +369,13 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm(NormArgs a) {
     ly.zero_tail(s * stage_bytes, left, tpr);
     if (GATE) lg.zero_tail(s * stage_bytes, left, tpr);
   }
+  __syncthreads();
 
   auto fetch = [&](uint32_t row, uint32_t stage) {
     if (row < a.n) {
-      lx.fetch(stage, a.x + at_row(row, a.x_st) + cx, left, tpr);
-      if (a.y) ly.fetch(stage, a.y + at_row(row, a.y_st) + cb, left, tpr);
-      if (GATE) lg.fetch(stage, a.gate + at_row(row, a.gate_st) + cb, left, tpr);
+      lx.fetch(stage, at_row(a.x, row, a.x_st, cx), left, tpr);
+      if (a.y) ly.fetch(stage, at_row(a.y, row, a.y_st, cb), left, tpr);
+      if (GATE) lg.fetch(stage, at_row(a.gate, row, a.gate_st, cb), left, tpr);
     }
     ring_commit();
   };
@@ -393,7 +423,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm(NormArgs a) {
             v_mul(g, cw.rw, g_row);
           }
           v_fma(x, g, y, x);
-          LX::store(a.x_out + at_row(row, a.x_out_st) + cx, i, x, left, tpr);
+          LX::store(at_row(a.x_out, row, a.x_out_st, cx), i, x, left, tpr);
         }
         v_dot(s2, x, x);
 #pragma unroll
@@ -409,7 +439,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm(NormArgs a) {
           cw.use(a, grp.sub, i);
           v_mul(f[i], f[i], rx);
           v_mul(f[i], f[i], cw.wq);
-          LB::store(a.h + at_row(row, a.h_st) + cb, i, f[i], left, tpr);
+          LB::store(at_row(a.h, row, a.h_st, cb), i, f[i], left, tpr);
         }
     }
     // a call with one sum a row leaves no second barrier between its uses of `red`
@@ -419,12 +449,13 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm(NormArgs a) {
 }
 
 template <typename XT, typename BT, int EPU, int V, bool GATE>
-__global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm_bwd(NormArgs a) {
+__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EPU > 8 ? 1 : 3) k_gated_norm_bwd(NormArgs a) {
   using K = Chunks<EPU, V>;
   using LX = Lane<XT, EPU, V>;
   using LB = Lane<BT, EPU, V>;
   extern __shared__ __align__(16) char ring[];
-  __shared__ float red_all[4 * 16 * 16];
+  __shared__ __align__(16) float red_all[8 * 4 * 16];
+  for (int i = threadIdx.x; i < 8 * 4 * 16; i += blockDim.x) red_all[i] = 0.f;
   const RowGroup grp{a.tpr, (int)threadIdx.x / a.tpr, (int)threadIdx.x % a.tpr};
   float* red = red_all + (a.tpr > 32 ? grp.id : 0) * 4 * 16;
   const int left = a.packs - grp.sub, tpr = a.tpr;
@@ -435,7 +466,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm_bwd(NormArgs a) 
   const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::UB + 2 * mx;
   const LX lx{tx, plx}, lt{tx + mx, plx};
   const LB ld{tb, plb}, ly{tb + mb, plb}, lg{tb + 2 * mb, plb};
-  const int cx = grp.sub * LX::S::kBytes, cb = grp.sub * LB::S::kBytes;
+  const uint64_t cx = (uint32_t)grp.sub * LX::S::kBytes, cb = (uint32_t)grp.sub * LB::S::kBytes;
   ColWeights<EPU, V> cw;
   cw.init(a, grp.sub);
   float col_pre[K::NC][K::C], col_t[K::NC][K::C];
@@ -450,14 +481,15 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm_bwd(NormArgs a) 
     ly.zero_tail(s * stage_bytes, left, tpr);
     if (GATE) lg.zero_tail(s * stage_bytes, left, tpr);
   }
+  __syncthreads();
 
   auto fetch = [&](uint32_t row, uint32_t stage) {
     if (row < a.n) {
-      lx.fetch(stage, a.x_out + at_row(row, a.x_out_st) + cx, left, tpr);
-      if (a.dx_out) lt.fetch(stage, a.dx_out + at_row(row, a.dx_out_st) + cx, left, tpr);
-      if (a.dh) ld.fetch(stage, a.dh + at_row(row, a.dh_st) + cb, left, tpr);
-      if (a.y) ly.fetch(stage, a.y + at_row(row, a.y_st) + cb, left, tpr);
-      if (GATE) lg.fetch(stage, a.gate + at_row(row, a.gate_st) + cb, left, tpr);
+      lx.fetch(stage, at_row(a.x_out, row, a.x_out_st, cx), left, tpr);
+      if (a.dx_out) lt.fetch(stage, at_row(a.dx_out, row, a.dx_out_st, cx), left, tpr);
+      if (a.dh) ld.fetch(stage, at_row(a.dh, row, a.dh_st, cb), left, tpr);
+      if (a.y) ly.fetch(stage, at_row(a.y, row, a.y_st, cb), left, tpr);
+      if (GATE) lg.fetch(stage, at_row(a.gate, row, a.gate_st, cb), left, tpr);
     }
     ring_commit();
   };
@@ -513,7 +545,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm_bwd(NormArgs a) 
           v_fma(t, x, xm, t);
           v_fma(col_pre[i], d, x, col_pre[i]);
         }
-        if (a.dx) LX::store(a.dx + at_row(row, a.dx_st) + cx, i, t, left, tpr);
+        if (a.dx) LX::store(at_row(a.dx, row, a.dx_st, cx), i, t, left, tpr);
         if (a.y) {
           float y[K::C], rest[K::C];
           ly.read(st, i, y);
@@ -533,7 +565,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm_bwd(NormArgs a) 
           if (GATE && a.dgate) {
             v_mul(y, u[i], y);
             v_mul(y, y, rest);
-            LB::store(a.dgate + at_row(row, a.dgate_st) + cb, i, y, left, tpr);
+            LB::store(at_row(a.dgate, row, a.dgate_st, cb), i, y, left, tpr);
           }
         }
       }
@@ -545,7 +577,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm_bwd(NormArgs a) 
         Pack<BT, 1> p;
         const float z[1] = {su[0] * rest_row};
         p.set(z);
-        p.store(reinterpret_cast<BT*>(a.dgate + at_row(row, a.dgate_st)));
+        p.store(reinterpret_cast<BT*>(at_row(a.dgate, row, a.dgate_st)));
       }
       const float um = -ry * ry * su[0] * a.inv_dim;
       if (a.dy && live)
@@ -555,7 +587,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) k_gated_norm_bwd(NormArgs a) 
           ly.read(st, i, y);
           v_mul(y, y, um);
           v_fma(y, u[i], ry, y);
-          LB::store(a.dy + at_row(row, a.dy_st) + cb, i, y, left, tpr);
+          LB::store(at_row(a.dy, row, a.dy_st, cb), i, y, left, tpr);
         }
     } else if (tpr > 32) {  // one sum a row: no second barrier between its uses of `red`
       asm volatile("bar.sync %0, %1;" ::"r"(grp.id + 1), "r"(tpr) : "memory");
@@ -616,15 +648,16 @@ __global__ void __launch_bounds__(1024) k_gated_norm_cols(const float* part, int
 
 // ---- host ----
 
-// Threads of a row: about eight elements each, a power of two up to a warp, whole warps above.
+// Threads of a row: for 8 elements each (16 in rows of more than 2048), a power of two up to a
+// warp, whole warps above.
 static void norm_shape(NormArgs& a, int epu) {
   a.packs = a.dim / epu;
-  const int want = (a.dim + 7) / 8;
+  const int each = a.dim > 8 * kNormThreads ? 16 : 8, want = (a.dim + each - 1) / each;
   int t = 4;
   while (t < want && t < 32) t *= 2;
   if (want > 32) t = (want + 31) / 32 * 32;
-  a.tpr = t < kNormMaxThreads ? t : kNormMaxThreads;
-  a.rpb = a.tpr >= kNormThreads ? 1 : kNormThreads / a.tpr;
+  a.tpr = t;
+  a.rpb = t >= kNormThreads ? 1 : kNormThreads / t;
 }
 
 // Ring stages and their bytes: up to kStages, but no fewer than two CTAs an SM for it while two
