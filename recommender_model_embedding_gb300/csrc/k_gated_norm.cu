@@ -16,8 +16,9 @@
 //   dw_post = res_scale * T, dres_scale = w_post * T
 //
 // Both are bound by HBM bandwidth.  A group of `tpr` threads takes a row, about eight elements a
-// thread (V packs of EPU: 16 bytes a pack where everything is aligned, one element otherwise),
-// so a row costs each thread few shuffles per element.  CTAs are persistent; every thread
+// thread (V packs of EPU: 16 bytes a pack where everything is aligned, one element otherwise;
+// with an fp32 stream beside bf16 blocks 4 elements, 16 and 8 bytes, so that neighbouring
+// threads' accesses of either type are neighbours in memory), so a row costs each thread few shuffles per element.  CTAs are persistent; every thread
 // copies its own packs of the next rows to shared memory asynchronously, kStages rows ahead,
 // and reads back only what it copied itself, so the ring needs no barrier; the groups of
 // a CTA run independently of each other (named barriers for the row sums, and only for rows
@@ -110,48 +111,43 @@ __device__ __forceinline__ void sigmoid2(float z, float& g, float& rest) {
   rest = z < 0.f ? 1.f - g : e * g;
 }
 
-// The ring: one plane of UB bytes a thread for each 16 bytes (or element) of a pack.
+// The ring: for each matrix and pack a plane of one place per thread.
 template <typename T, int EPU>
 struct Slot {
   static constexpr int kBytes = EPU * (int)sizeof(T);
-  static constexpr int UB = kBytes < 16 ? kBytes : 16, kPlanes = kBytes / UB;
+  static_assert(kBytes <= 16, "a pack is one access");
 
-  // starts the copy of the pack at p to this thread's place of the planes from `to` on
-  static __device__ __forceinline__ void fetch(uint32_t to, uint32_t plane, const char* p) {
-    if constexpr (UB == 16) {
-#pragma unroll
-      for (int i = 0; i < kPlanes; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * plane), "l"(p + i * 16)
-                     : "memory");
-    } else if constexpr (UB == 4) {
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
+  // starts the copy of the pack at p to this thread's place `to`
+  static __device__ __forceinline__ void fetch(uint32_t to, const char* p) {
+    if constexpr (kBytes == 16) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+    } else if constexpr (kBytes >= 4) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(p), "n"(kBytes) : "memory");
     } else {  // one bf16: too small for an asynchronous copy
       const uint16_t v = *reinterpret_cast<const uint16_t*>(p);
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
     }
   }
-  static __device__ __forceinline__ void zero(uint32_t to, uint32_t plane) {
+  static __device__ __forceinline__ void zero(uint32_t to) {
 #pragma unroll
-    for (int i = 0; i < kPlanes; ++i)
-#pragma unroll
-      for (int b = 0; b < UB; b += 2)
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i * plane + b), "h"((uint16_t)0) : "memory");
+    for (int b = 0; b < kBytes; b += 2)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + b), "h"((uint16_t)0) : "memory");
   }
-  static __device__ __forceinline__ void read(uint32_t from, uint32_t plane, float* v) {
-    if constexpr (UB == 16) {
-      uint32_t w[4 * kPlanes];
-#pragma unroll
-      for (int i = 0; i < kPlanes; ++i)
+  static __device__ __forceinline__ void read(uint32_t from, float* v) {
+    if constexpr (kBytes >= 4) {
+      uint32_t w[kBytes / 4];
+      if constexpr (kBytes == 16)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
-                     : "r"(from + i * plane) : "memory");
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from) : "memory");
+      else if constexpr (kBytes == 8)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(from) : "memory");
+      else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(from) : "memory");
 #pragma unroll
       for (int i = 0; i < EPU; ++i) {
         if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
         else v[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
       }
-    } else if constexpr (UB == 4) {
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(from) : "memory");
     } else {
       uint16_t w;
       asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(from) : "memory");
@@ -290,22 +286,22 @@ struct Lane {
   using K = Chunks<EPU, V>;
   uint32_t at, plane;  // this thread's place of the matrix in stage 0; bytes of a plane
   __device__ __forceinline__ uint32_t pack(uint32_t stage, int i) const {
-    return at + stage + i * S::kPlanes * plane;
+    return at + stage + i * plane;
   }
   // the thread's packs of a row, into the ring (`left`: packs of the row from this thread's on)
   __device__ __forceinline__ void fetch(uint32_t stage, const char* row, int left, int tpr) const {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i * tpr < left) S::fetch(pack(stage, i), plane, row + i * tpr * S::kBytes);
+      if (i * tpr < left) S::fetch(pack(stage, i), row + i * tpr * S::kBytes);
   }
   __device__ __forceinline__ void zero_tail(uint32_t stage, int left, int tpr) const {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i * tpr >= left) S::zero(pack(stage, i), plane);
+      if (i * tpr >= left) S::zero(pack(stage, i));
   }
   __device__ __forceinline__ void read(uint32_t stage, int chunk, float (&v)[K::C]) const {
 #pragma unroll
-    for (int p = 0; p < K::PP; ++p) S::read(pack(stage, chunk * K::PP + p), plane, v + p * EPU);
+    for (int p = 0; p < K::PP; ++p) S::read(pack(stage, chunk * K::PP + p), v + p * EPU);
   }
   static __device__ __forceinline__ void store(char* row, int chunk, const float (&v)[K::C], int left,
                                                int tpr) {
@@ -355,12 +351,12 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
   const RowGroup grp{a.tpr, (int)threadIdx.x / a.tpr, (int)threadIdx.x % a.tpr};
   float* red = red_all + (a.tpr > 32 ? grp.id : 0) * 2 * 16;
   const int left = a.packs - grp.sub, tpr = a.tpr;
-  const uint32_t plx = blockDim.x * LX::S::UB, plb = blockDim.x * LB::S::UB;
+  const uint32_t plx = blockDim.x * LX::S::kBytes, plb = blockDim.x * LB::S::kBytes;
   const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>;
-  const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::UB;
-  const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::UB + V * LX::S::kPlanes * plx;
+  const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::kBytes;
+  const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::kBytes + V * plx;
   const LX lx{tx, plx};
-  const LB ly{tb, plb}, lg{tb + V * LB::S::kPlanes * plb, plb};
+  const LB ly{tb, plb}, lg{tb + V * plb, plb};
   const uint64_t cx = (uint32_t)grp.sub * LX::S::kBytes, cb = (uint32_t)grp.sub * LB::S::kBytes;
   ColWeights<EPU, V> cw;
   cw.init(a, grp.sub);
@@ -459,11 +455,11 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
   const RowGroup grp{a.tpr, (int)threadIdx.x / a.tpr, (int)threadIdx.x % a.tpr};
   float* red = red_all + (a.tpr > 32 ? grp.id : 0) * 4 * 16;
   const int left = a.packs - grp.sub, tpr = a.tpr;
-  const uint32_t plx = blockDim.x * LX::S::UB, plb = blockDim.x * LB::S::UB;
+  const uint32_t plx = blockDim.x * LX::S::kBytes, plb = blockDim.x * LB::S::kBytes;
   const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>;
-  const uint32_t mx = V * LX::S::kPlanes * plx, mb = V * LB::S::kPlanes * plb;  // of a matrix
-  const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::UB;
-  const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::UB + 2 * mx;
+  const uint32_t mx = V * plx, mb = V * plb;  // of a matrix
+  const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::kBytes;
+  const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::kBytes + 2 * mx;
   const LX lx{tx, plx}, lt{tx + mx, plx};
   const LB ld{tb, plb}, ly{tb + mb, plb}, lg{tb + 2 * mb, plb};
   const uint64_t cx = (uint32_t)grp.sub * LX::S::kBytes, cb = (uint32_t)grp.sub * LB::S::kBytes;
@@ -698,15 +694,16 @@ static NormArgs norm_args(const emb_norm& p) {
   return a;
 }
 
-// Whether every matrix of the call (NULL: none) allows packs of 16 bytes.
+// Whether every matrix of the call (NULL: none) allows packs of more than one element.
 static bool norm_vec(const emb_norm& p) {
   const int xe = p.x_dtype == EMB_BF16 ? 2 : 4, be = p.dtype == EMB_BF16 ? 2 : 4;
-  const int epu = be == 2 ? 8 : 4;
-  return p.dim % epu == 0 && rows16(p.d_x, p.x_ld, xe) && rows16(p.d_y, p.y_ld, be) &&
-         (p.gate_cols == 1 || rows16(p.d_gate, p.gate_ld, be)) && rows16(p.d_x_out, p.x_out_ld, xe) &&
-         rows16(p.d_h, p.h_ld, be) && rows16(p.d_dx_out, p.dx_out_ld, xe) &&
-         rows16(p.d_dh, p.dh_ld, be) && rows16(p.d_dx, p.dx_ld, xe) && rows16(p.d_dy, p.dy_ld, be) &&
-         (p.gate_cols == 1 || rows16(p.d_dgate, p.dgate_ld, be)) && rows16(p.d_w_post, 0, 4) &&
+  const int epu = xe == 2 ? 8 : 4, bb = epu * be;  // elements of a pack, bytes of a block's
+  return p.dim % epu == 0 && rows16(p.d_x, p.x_ld, xe) && rows_on(p.d_y, p.y_ld, be, bb) &&
+         (p.gate_cols == 1 || rows_on(p.d_gate, p.gate_ld, be, bb)) &&
+         rows16(p.d_x_out, p.x_out_ld, xe) && rows_on(p.d_h, p.h_ld, be, bb) &&
+         rows16(p.d_dx_out, p.dx_out_ld, xe) && rows_on(p.d_dh, p.dh_ld, be, bb) &&
+         rows16(p.d_dx, p.dx_ld, xe) && rows_on(p.d_dy, p.dy_ld, be, bb) &&
+         (p.gate_cols == 1 || rows_on(p.d_dgate, p.dgate_ld, be, bb)) && rows16(p.d_w_post, 0, 4) &&
          rows16(p.d_res_scale, 0, 4) && rows16(p.d_w_pre, 0, 4);
 }
 
@@ -772,7 +769,7 @@ static cudaError_t norm_call(const emb_norm& p, NormArgs& a, int* grid, cudaStre
   if (p.dtype == EMB_F32)
     return vec ? norm_t<float, float, 4, BWD>(a, grid, s) : norm_t<float, float, 1, BWD>(a, grid, s);
   if (p.x_dtype == EMB_F32)
-    return vec ? norm_t<float, H, 8, BWD>(a, grid, s) : norm_t<float, H, 1, BWD>(a, grid, s);
+    return vec ? norm_t<float, H, 4, BWD>(a, grid, s) : norm_t<float, H, 1, BWD>(a, grid, s);
   return vec ? norm_t<H, H, 8, BWD>(a, grid, s) : norm_t<H, H, 1, BWD>(a, grid, s);
 }
 

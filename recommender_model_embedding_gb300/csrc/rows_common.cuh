@@ -1,6 +1,6 @@
 // Row access shared by the expert and gated-norm kernels: packs of EPU consecutive elements
-// of an fp32 or bf16 row (16 bytes and more where everything is 16-byte aligned, one element
-// otherwise), held as loaded and widened to fp32 where they are used.
+// of an fp32 or bf16 row (up to 16 bytes, where everything is aligned for it; else one
+// element), held as loaded and widened to fp32 where they are used.
 #pragma once
 
 #include "emb_internal.cuh"
@@ -45,23 +45,18 @@ struct Pack<float, 4> {
 };
 
 template <>
-struct Pack<float, 8> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+struct Pack<__nv_bfloat16, 4> {
+  uint2 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r = *reinterpret_cast<const uint2*>(p);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  __device__ __forceinline__ void zero() { r = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void set(const float (&v)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    r = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
-    a = make_float4(v[0], v[1], v[2], v[3]);
-    b = make_float4(v[4], v[5], v[6], v[7]);
-  }
-  __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    *reinterpret_cast<uint2*>(p) = r;
   }
 };
 
@@ -126,9 +121,12 @@ inline int device_sms() {
   return sms < 1 ? 1 : sms;
 }
 
-// Whether a matrix of rows allows 16-byte accesses: base and row step on 16-byte boundaries.
-inline bool rows16(const void* p, int64_t ld, int elem) {
-  return p == nullptr || (((reinterpret_cast<uintptr_t>(p) | (uint64_t)(ld * elem)) & 15) == 0);
+// Whether a matrix of rows allows accesses of `bytes` (a power of two): base and row step on
+// such boundaries.
+inline bool rows_on(const void* p, int64_t ld, int elem, int bytes) {
+  return p == nullptr ||
+         (((reinterpret_cast<uintptr_t>(p) | (uint64_t)(ld * elem)) & (uint64_t)(bytes - 1)) == 0);
 }
+inline bool rows16(const void* p, int64_t ld, int elem) { return rows_on(p, ld, elem, 16); }
 
 }  // namespace emb
