@@ -283,8 +283,8 @@ emb_status emb_dequantize_rows(const int8_t* d_q, const float* d_scale, int64_t 
  * a residual block, and the clipping of the dense gradients.  The source pages name none of
  * them; the formulas are stated at each call.  They need no context; every buffer is a device
  * buffer owned by the caller.  Matrices are rows of `dim` elements, fp32 (EMB_F32) or bf16
- * (EMB_BF16), with a row step (*_ld, in elements): an input may have any step >= 0 (0: one row
- * for all), an output one of at least dim (any, for a single row).  Any alignment of the
+ * (EMB_BF16), with a row step (*_ld, in elements, below 2^30): an input may have any step >= 0
+ * (0: one row for all), an output one of at least dim (any, for a single row).  Any alignment of the
  * element type serves; bases and steps on 16-byte boundaries are faster.  Sums are fp32 or
  * wider whatever the type, rounded once on output, and taken in a fixed order: repeated calls
  * give the same bits.  Outputs must not overlap inputs or each other except where a call says
@@ -348,8 +348,8 @@ emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, cons
  *   dw_post, dres_scale, dw_pre: summed over the rows (fp32 [dim], overwritten).
  * Any of its outputs may be NULL; dx may be dx_out itself (same row step).  With d_y NULL, dy,
  * dgate, dw_post and dres_scale are NULL; with d_dh NULL, dw_pre is.
- * EMB_EINVAL: n outside [0, 2^31), dim outside [1, EMB_NORM_MAX_DIM], bad types or gate_cols, a row
- * step of 2^30 elements or more or (outputs) below dim, eps not a positive finite number, a missing buffer, nothing to compute; the backward also for a
+ * EMB_EINVAL: n outside [0, 2^31), dim outside [1, EMB_NORM_MAX_DIM], bad types, gate_cols or row
+ * steps, eps not a positive finite number, a missing buffer, nothing to compute; the backward also for a
  * short or misaligned workspace. */
 #define EMB_NORM_MAX_DIM 8192
 typedef struct emb_norm {

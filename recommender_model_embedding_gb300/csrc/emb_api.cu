@@ -1106,8 +1106,11 @@ static bool ws_ok(const void* ws, int64_t have, int64_t need) {
   return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 15) == 0);
 }
 
-// an output's row step: rows must not overlap
-static bool out_ld_ok(int64_t ld, int64_t rows, int64_t dim) { return rows <= 1 || ld >= dim; }
+// row steps: below 2^30 elements, and an output's rows must not overlap
+static bool in_ld_ok(int64_t ld) { return ld >= 0 && ld < (1 << 30); }
+static bool out_ld_ok(int64_t ld, int64_t rows, int64_t dim) {
+  return in_ld_ok(ld) && (rows <= 1 || ld >= dim);
+}
 
 static bool aligned_to(const void* p, int elem) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(elem - 1)) == 0;
@@ -1140,7 +1143,7 @@ emb_status emb_expert_sort(const int64_t* d_ids, int64_t n, int32_t k, int32_t n
 emb_status emb_expert_dispatch(const void* d_x, int64_t x_ld, const int32_t* d_pos, int64_t n,
                                int32_t k, int32_t dim, int32_t dtype, void* d_xs, int64_t xs_ld,
                                void* stream) {
-  if (!expert_rows_ok(n, k, dim, dtype) || x_ld < 0 || !out_ld_ok(xs_ld, n * k, dim)) return EMB_EINVAL;
+  if (!expert_rows_ok(n, k, dim, dtype) || !in_ld_ok(x_ld) || !out_ld_ok(xs_ld, n * k, dim)) return EMB_EINVAL;
   const int elem = dtype == EMB_BF16 ? 2 : 4;
   if (n > 0 && (!d_x || !d_pos || !d_xs)) return EMB_EINVAL;
   if (!aligned_to(d_x, elem) || !aligned_to(d_xs, elem)) return EMB_EINVAL;
@@ -1151,7 +1154,7 @@ emb_status emb_expert_dispatch(const void* d_x, int64_t x_ld, const int32_t* d_p
 emb_status emb_expert_dispatch_backward(const void* d_dxs, int64_t dxs_ld, const int32_t* d_pos,
                                         int64_t n, int32_t k, int32_t dim, int32_t dtype,
                                         void* d_dx, int64_t dx_ld, void* stream) {
-  if (!expert_rows_ok(n, k, dim, dtype) || dxs_ld < 0 || !out_ld_ok(dx_ld, n, dim)) return EMB_EINVAL;
+  if (!expert_rows_ok(n, k, dim, dtype) || !in_ld_ok(dxs_ld) || !out_ld_ok(dx_ld, n, dim)) return EMB_EINVAL;
   const int elem = dtype == EMB_BF16 ? 2 : 4;
   if (n > 0 && (!d_dxs || !d_pos || !d_dx)) return EMB_EINVAL;
   if (!aligned_to(d_dxs, elem) || !aligned_to(d_dx, elem)) return EMB_EINVAL;
@@ -1163,7 +1166,7 @@ emb_status emb_expert_dispatch_backward(const void* d_dxs, int64_t dxs_ld, const
 emb_status emb_expert_combine(const void* d_ys, int64_t ys_ld, const int32_t* d_pos,
                               const float* d_w, int64_t n, int32_t k, int32_t dim, int32_t dtype,
                               void* d_out, int64_t out_ld, void* stream) {
-  if (!expert_rows_ok(n, k, dim, dtype) || ys_ld < 0 || !out_ld_ok(out_ld, n, dim)) return EMB_EINVAL;
+  if (!expert_rows_ok(n, k, dim, dtype) || !in_ld_ok(ys_ld) || !out_ld_ok(out_ld, n, dim)) return EMB_EINVAL;
   const int elem = dtype == EMB_BF16 ? 2 : 4;
   if (n > 0 && (!d_ys || !d_pos || !d_w || !d_out)) return EMB_EINVAL;
   if (!aligned_to(d_ys, elem) || !aligned_to(d_out, elem)) return EMB_EINVAL;
@@ -1175,7 +1178,8 @@ emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, cons
                                        int64_t ys_ld, const int32_t* d_pos, const float* d_w,
                                        int64_t n, int32_t k, int32_t dim, int32_t dtype,
                                        void* d_dys, int64_t dys_ld, float* d_dw, void* stream) {
-  if (!expert_rows_ok(n, k, dim, dtype) || dout_ld < 0 || ys_ld < 0 || !out_ld_ok(dys_ld, n * k, dim))
+  if (!expert_rows_ok(n, k, dim, dtype) || !in_ld_ok(dout_ld) || !in_ld_ok(ys_ld) ||
+      !out_ld_ok(dys_ld, n * k, dim))
     return EMB_EINVAL;
   const int elem = dtype == EMB_BF16 ? 2 : 4;
   if (n > 0 && (!d_dout || !d_ys || !d_pos || !d_w || !d_dys || !d_dw)) return EMB_EINVAL;
@@ -1196,7 +1200,7 @@ static bool norm_ok(const emb_norm* p) {
   if (p->n > 0 && p->d_gate && (!p->d_y || (p->gate_cols != 1 && p->gate_cols != p->dim))) return false;
   for (int64_t ld : {p->x_ld, p->y_ld, p->gate_ld, p->x_out_ld, p->h_ld, p->dx_out_ld, p->dh_ld,
                      p->dx_ld, p->dy_ld, p->dgate_ld})
-    if (ld < 0 || ld >= (1 << 30)) return false;
+    if (!in_ld_ok(ld)) return false;
   const int xe = p->x_dtype == EMB_BF16 ? 2 : 4, be = p->dtype == EMB_BF16 ? 2 : 4;
   const void* xs[] = {p->d_x, p->d_x_out, p->d_dx_out, p->d_dx};
   const void* bs[] = {p->d_y, p->d_gate, p->d_h, p->d_dh, p->d_dy, p->d_dgate};

@@ -8,9 +8,9 @@
 //   backward  dx[i] = sum over kept j of dxs[pos],  dys[pos] = w * dout[i] (zero past
 //             offsets[E]),  dw[i][j] = dout[i] . ys[pos] (zero when dropped)
 //
-// Everything is data movement, so every kernel is row-major over the unsorted rows: x and dout
-// are read once, the sorted side is touched one whole row at a time through pos, and no
-// output needs an atomic (fixed order of summation: results repeat bit for bit).
+// Everything is data movement, so every kernel walks the unsorted rows: x and dout are read once,
+// the sorted side is touched one whole row at a time through pos, and no output needs an atomic
+// (fixed order of summation: results repeat bit for bit).
 #include "rows_common.cuh"
 
 namespace emb {
@@ -18,59 +18,94 @@ namespace emb {
 // ---- sort: a stable counting sort, keys 0..E (E: dropped) ----
 // Each CTA takes a contiguous chunk of slots and each of its warps a contiguous part of it, so
 // a slot's place is base(expert) + earlier chunks + earlier warps + earlier slots of the warp.
-// A first launch counts each chunk's keys; the second sums those counts (every CTA reads all
-// of them: a few hundred KB from L2), scans them over the experts and places the slots.  A
-// single chunk needs no first launch.
-constexpr int kSortWarps = 16;
-constexpr int kSortChunk = 4096;  // slots of a chunk, at least
+// A first launch counts each chunk's keys; the second (started early: it waits for the first
+// only where it reads the counts) sums those counts over the chunks (every CTA reads all of
+// them from L2), scans them over the experts and places the slots.  A single chunk needs no
+// first launch.  Bound by latency, not bytes: chunks are as small as the SMs allow, and a
+// warp has the ids of eight groups of 32 slots in flight.
+constexpr int kSortWarps = 16, kSortThreads = kSortWarps * 32;
+constexpr int kSortDepth = 8;      // groups of 32 ids a warp loads at once
+constexpr int kSortSingle = 4096;  // slots of one CTA alone, at most
 
-__device__ __forceinline__ uint32_t expert_key(const int64_t* ids, int64_t q, int64_t end, int E) {
-  if (q >= end) return (uint32_t)E + 1u;  // no slot: matches only its like
-  const uint64_t id = (uint64_t)ids[q];
-  return id < (uint64_t)E ? (uint32_t)id : (uint32_t)E;
+// Calls f(slot, key) for the groups of 32 slots of a warp's part [w0, w0 + 32 * groups), with all
+// lanes; key E + 1 past the end.
+template <typename F>
+__device__ __forceinline__ void each_key(const int64_t* ids, int64_t w0, int64_t groups, int64_t end,
+                                         int E, F f) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t g0 = 0; g0 < groups; g0 += kSortDepth) {
+    uint32_t key[kSortDepth];
+#pragma unroll
+    for (int u = 0; u < kSortDepth; ++u) {
+      const int64_t q = w0 + (g0 + u) * 32 + lane;
+      key[u] = (uint32_t)E + 1u;
+      if (g0 + u < groups && q < end) {
+        const uint64_t id = (uint64_t)ids[q];
+        key[u] = id < (uint64_t)E ? (uint32_t)id : (uint32_t)E;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kSortDepth; ++u)
+      if (g0 + u < groups) f(w0 + (g0 + u) * 32 + lane, key[u]);
+  }
 }
 
-__global__ void __launch_bounds__(kSortWarps * 32) k_expert_count(const int64_t* ids, int64_t S,
-                                                                  int E, int64_t chunk,
-                                                                  uint32_t* hist) {
+__global__ void __launch_bounds__(kSortThreads) k_expert_count(const int64_t* ids, int64_t S, int E,
+                                                               int64_t chunk, uint32_t* hist) {
   extern __shared__ uint32_t sm_count[];
+  asm volatile("griddepcontrol.launch_dependents;");
   for (int e = threadIdx.x; e <= E; e += blockDim.x) sm_count[e] = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const int64_t c0 = (int64_t)blockIdx.x * chunk;
   const int64_t c1 = c0 + chunk < S ? c0 + chunk : S;
-  for (int64_t b = c0 + (threadIdx.x & ~31); b < c1; b += blockDim.x) {
-    const uint32_t key = expert_key(ids, b + lane, c1, E);
+  const int64_t groups = (c1 - c0 + kSortThreads - 1) / kSortThreads;
+  each_key(ids, c0 + (threadIdx.x >> 5) * groups * 32, groups, c1, E, [&](int64_t, uint32_t key) {
     const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
     if (key <= (uint32_t)E && lane == __ffs(peers) - 1) atomicAdd(sm_count + key, __popc(peers));
-  }
+  });
   __syncthreads();
   for (int e = threadIdx.x; e <= E; e += blockDim.x)
     hist[(int64_t)blockIdx.x * (E + 1) + e] = sm_count[e];
 }
 
-__global__ void __launch_bounds__(kSortWarps * 32)
+__global__ void __launch_bounds__(kSortThreads)
     k_expert_place(const int64_t* ids, int64_t S, int E, int64_t chunk, const uint32_t* hist,
                    int32_t* order, int32_t* pos, int32_t* offsets) {
-  extern __shared__ uint32_t sm_place[];  // [warps][E + 1] places within the chunk, [E + 1] bases
+  // [warps][E + 1] places within the chunk; [E + 1] totals, then bases; [E + 1] earlier chunks
+  extern __shared__ uint32_t sm_place[];
   __shared__ uint32_t warp_tot[kSortWarps];
   const int K = E + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t* base = sm_place + kSortWarps * K;
+  uint32_t* total = sm_place + kSortWarps * K;
+  uint32_t* before = total + K;
   uint32_t* mine = sm_place + warp * K;
-  for (int e = threadIdx.x; e < kSortWarps * K; e += blockDim.x) sm_place[e] = 0;
+  for (int e = threadIdx.x; e < (kSortWarps + 2) * K; e += blockDim.x) sm_place[e] = 0;
   __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * chunk;
   const int64_t c1 = c0 + chunk < S ? c0 + chunk : S;
-  const int64_t groups = (c1 - c0 + kSortWarps * 32 - 1) / (kSortWarps * 32);  // of 32, per warp
+  const int64_t groups = (c1 - c0 + kSortThreads - 1) / kSortThreads;
   const int64_t w0 = c0 + warp * groups * 32;
-  for (int64_t g = 0; g < groups; ++g) {
-    const uint32_t key = expert_key(ids, w0 + g * 32 + lane, c1, E);
+  each_key(ids, w0, groups, c1, E, [&](int64_t, uint32_t key) {
     const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
     if (key <= (uint32_t)E && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
     __syncwarp();
+  });
+  if (hist) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int e = lane; e < K; e += 32) {  // warp w: chunks w, w + 16, ...
+      uint32_t t = 0, b = 0;
+#pragma unroll 10
+      for (uint32_t g = warp; g < gridDim.x; g += kSortWarps) {
+        const uint32_t c = __ldcg(hist + (int64_t)g * K + e);
+        t += c;
+        b += g < blockIdx.x ? c : 0u;
+      }
+      if (t) atomicAdd(total + e, t);
+      if (b) atomicAdd(before + e, b);
+    }
   }
   __syncthreads();
-  // per key: earlier warps' counts, the chunk's place among the chunks, the total
+  // per key: earlier warps' counts, and its first place: earlier keys' totals + earlier chunks
   const int per = (K + blockDim.x - 1) / blockDim.x;  // keys of a thread (consecutive)
   uint32_t sum = 0;
   for (int i = 0; i < per; ++i) {
@@ -82,19 +117,8 @@ __global__ void __launch_bounds__(kSortWarps * 32)
       sm_place[w * K + e] = run;
       run += c;
     }
-    uint32_t before = 0, total = run;
-    if (hist) {
-      total = 0;
-#pragma unroll 8
-      for (uint32_t g = 0; g < gridDim.x; ++g) {
-        const uint32_t c = hist[(int64_t)g * K + e];
-        if (g < blockIdx.x) before += c;
-        total += c;
-      }
-    }
-    base[e] = sum + before;  // the keys before this thread's are added below
-    if (blockIdx.x == 0) offsets[e] = (int32_t)sum;
-    sum += total;
+    if (!hist) total[e] = run;
+    sum += total[e];
   }
   uint32_t incl = sum;
 #pragma unroll
@@ -104,36 +128,36 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   }
   if (lane == 31) warp_tot[warp] = incl;
   __syncthreads();
-  uint32_t pre = incl - sum;
-  for (int w = 0; w < warp; ++w) pre += warp_tot[w];
+  uint32_t first = incl - sum;
+  for (int w = 0; w < warp; ++w) first += warp_tot[w];
   for (int i = 0; i < per; ++i) {
     const int e = threadIdx.x * per + i;
     if (e >= K) break;
-    base[e] += pre;
-    if (blockIdx.x == 0) offsets[e] += (int32_t)pre;
+    const uint32_t t = total[e];
+    if (blockIdx.x == 0) offsets[e] = (int32_t)first;
+    total[e] = first + before[e];
+    first += t;
   }
   __syncthreads();
-  for (int64_t g = 0; g < groups; ++g) {
-    const int64_t q = w0 + g * 32 + lane;
-    const uint32_t key = expert_key(ids, q, c1, E);
+  each_key(ids, w0, groups, c1, E, [&](int64_t q, uint32_t key) {
     const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
     const bool in = key <= (uint32_t)E;
-    const uint32_t first = in ? mine[key] : 0u;
+    const uint32_t at = in ? mine[key] : 0u;
     __syncwarp();
-    if (in && lane == __ffs(peers) - 1) mine[key] = first + __popc(peers);
+    if (in && lane == __ffs(peers) - 1) mine[key] = at + __popc(peers);
     __syncwarp();
     if (in) {
-      const uint32_t p = base[key] + first + __popc(peers & ((1u << lane) - 1u));
-      pos[q] = key < (uint32_t)E ? (int32_t)p : -1 - (int32_t)p;
+      const uint32_t p = total[key] + at + __popc(peers & ((1u << lane) - 1u));
+      pos[q] = key < (uint32_t)E ? (int32_t)p : ~(int32_t)p;
       order[p] = (int32_t)q;
     }
-  }
+  });
 }
 
 static int64_t sort_chunk(int64_t S, int sms) {
+  if (S <= kSortSingle) return kSortSingle;
   const int64_t even = (S + sms - 1) / sms;
-  const int64_t c = even > kSortChunk ? even : kSortChunk;
-  return (c + kSortWarps * 32 - 1) / (kSortWarps * 32) * (kSortWarps * 32);
+  return (even + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 
 int64_t expert_sort_workspace(int64_t S, int E) {
@@ -147,19 +171,58 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
   const int64_t chunk = sort_chunk(S, device_sms());
   const int G = S > 0 ? (int)((S + chunk - 1) / chunk) : 1;  // an empty batch still writes offsets
   uint32_t* hist = G > 1 ? static_cast<uint32_t*>(ws) : nullptr;
-  const int smem = (kSortWarps + 1) * (E + 1) * (int)sizeof(uint32_t);
-  cudaError_t e = cudaFuncSetAttribute(k_expert_place, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = (kSortWarps + 2) * (E + 1) * (int)sizeof(uint32_t);
+  cudaError_t e = smem > 48 * 1024 ? cudaFuncSetAttribute(k_expert_place, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
+                                   : cudaSuccess;
   if (e != cudaSuccess) return e;
-  if (hist)
-    k_expert_count<<<G, kSortWarps * 32, (E + 1) * sizeof(uint32_t), s>>>(ids, S, E, chunk, hist);
-  k_expert_place<<<G, kSortWarps * 32, smem, s>>>(ids, S, E, chunk, hist, order, pos, offsets);
-  return cudaGetLastError();
+  if (!hist) {
+    k_expert_place<<<G, kSortThreads, smem, s>>>(ids, S, E, chunk, hist, order, pos, offsets);
+    return cudaGetLastError();
+  }
+  k_expert_count<<<G, kSortThreads, (E + 1) * sizeof(uint32_t), s>>>(ids, S, E, chunk, hist);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_early(k_expert_place, G, kSortThreads, smem, s, ids, S, E, chunk,
+                      (const uint32_t*)hist, order, pos, offsets);
 }
 
-// ---- dispatch: rows copied to their sorted places, in units of UB bytes ----
-// A CTA takes a tile of rows; its threads step through the tile's (row, unit) items, four loads
-// in flight each, and store every unit to the row's k places.
-constexpr int kMoveThreads = 256, kMoveItems = 4;
+// ---- rows to and from their sorted places ----
+// A task is a row, or a part of one: `lanes` neighbouring threads (32, fewer for rows of fewer
+// units), each with UN units of the row `lanes` apart, all loaded before the first is used.  A
+// unit is 16 bytes where every row start and the row length are multiples of 16, else 4 or 2:
+// the row's addresses are worked out once a task, so that narrow units cost little more.
+constexpr int kMoveThreads = 256;
+
+struct MoveShape {
+  uint32_t tasks, n;
+  int U, lanes, shift;  // units of a row; threads of a task, and their log2
+  FastDiv segs;         // tasks of a row
+};
+
+// The largest UN (a power of two, at most `most`) that a row fills, and the shape for it.
+static int move_shape(MoveShape& m, int64_t n, int units, int most) {
+  m.n = (uint32_t)n, m.U = units, m.lanes = 32, m.shift = 5;
+  while (m.lanes > 1 && m.lanes / 2 >= units) m.lanes /= 2, --m.shift;
+  int un = 1;
+  while (un < most && un * m.lanes < units) un *= 2;
+  m.segs = FastDiv((uint32_t)((units + un * m.lanes - 1) / (un * m.lanes)));
+  m.tasks = m.n * m.segs.d;
+  return un;
+}
+
+static unsigned move_grid(const MoveShape& m) {
+  return (unsigned)(((int64_t)m.tasks * m.lanes + kMoveThreads - 1) / kMoveThreads);
+}
+
+// This thread's task: its row and first unit (false: none).
+__device__ __forceinline__ bool move_task(const MoveShape& m, int un, uint32_t& row, int& unit) {
+  const uint32_t task =
+      (uint32_t)(((uint64_t)blockIdx.x * kMoveThreads + threadIdx.x) >> m.shift);
+  if (task >= m.tasks) return false;
+  row = m.segs.div(task);
+  unit = (int)(task - row * m.segs.d) * un * m.lanes + (threadIdx.x & (m.lanes - 1));
+  return true;
+}
 
 template <int UB>
 struct Unit;
@@ -179,147 +242,142 @@ struct Unit<2> {
   static __device__ __forceinline__ T zero() { return 0; }
 };
 
-struct MoveTile {
-  int64_t n, tiles;
-  int R;        // rows of a tile
-  FastDiv U;    // units of a row
-};
-
-static MoveTile move_tile(int64_t n, int64_t units) {
-  MoveTile t;
-  t.n = n;
-  t.U = FastDiv((uint32_t)units);
-  const int64_t per = kMoveThreads * kMoveItems;
-  t.R = (int)(units >= per ? 1 : per / units);
-  t.tiles = (n + t.R - 1) / t.R;
-  return t;
-}
-
-static int move_grid(const MoveTile& t) {
-  const int64_t cap = (int64_t)device_sms() * 64;
-  return (int)(t.tiles < cap ? t.tiles : cap);
+template <int UB, int UN>
+__global__ void __launch_bounds__(kMoveThreads)
+    k_expert_dispatch(const char* x, uint32_t x_st, const int32_t* pos, int k, MoveShape m, char* xs,
+                      uint32_t xs_st) {
+  using V = typename Unit<UB>::T;
+  uint32_t row;
+  int unit;
+  if (!move_task(m, UN, row, unit)) return;
+  const uint32_t S = m.n * (uint32_t)k;
+  const char* src = x + ((uint64_t)row * x_st + (uint32_t)unit * UB);
+  V v[UN];
+#pragma unroll
+  for (int u = 0; u < UN; ++u)
+    if (unit + u * m.lanes < m.U) v[u] = *reinterpret_cast<const V*>(src + u * m.lanes * UB);
+  const int32_t* ps = pos + (uint64_t)row * k;
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int32_t p = ps[j];
+    const uint32_t to = (uint32_t)(p >= 0 ? p : ~p);
+    if (to >= S) continue;
+    char* dst = xs + ((uint64_t)to * xs_st + (uint32_t)unit * UB);
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+      if (unit + u * m.lanes < m.U)
+        *reinterpret_cast<V*>(dst + u * m.lanes * UB) = p >= 0 ? v[u] : Unit<UB>::zero();
+  }
 }
 
 template <int UB>
-__global__ void __launch_bounds__(kMoveThreads) k_expert_dispatch(const char* x, int64_t x_step,
-                                                                  const int32_t* pos, int k,
-                                                                  MoveTile t, char* xs,
-                                                                  int64_t xs_step) {
-  using V = typename Unit<UB>::T;
-  const int64_t S = t.n * k;
-  for (int64_t tile = blockIdx.x; tile < t.tiles; tile += gridDim.x) {
-    const int64_t row0 = tile * t.R;
-    const int rows = (int)(t.n - row0 < t.R ? t.n - row0 : t.R);
-    const uint32_t items = (uint32_t)rows * t.U.d;
-    for (uint32_t i0 = threadIdx.x; i0 < items; i0 += kMoveThreads * kMoveItems) {
-      V v[kMoveItems];
-#pragma unroll
-      for (int u = 0; u < kMoveItems; ++u) {
-        const uint32_t i = i0 + u * kMoveThreads;
-        if (i < items) {
-          const uint32_t r = t.U.div(i), c = i - r * t.U.d;
-          v[u] = *reinterpret_cast<const V*>(x + (row0 + r) * x_step + (int64_t)c * UB);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kMoveItems; ++u) {
-        const uint32_t i = i0 + u * kMoveThreads;
-        if (i < items) {
-          const uint32_t r = t.U.div(i), c = i - r * t.U.d;
-          const int32_t* ps = pos + (row0 + r) * k;
-          for (int j = 0; j < k; ++j) {
-            const int32_t p = ps[j];
-            const int64_t to = p >= 0 ? (int64_t)p : -1 - (int64_t)p;
-            if (to < S)
-              *reinterpret_cast<V*>(xs + to * xs_step + (int64_t)c * UB) = p >= 0 ? v[u] : Unit<UB>::zero();
-          }
-        }
-      }
-    }
-  }
+static void dispatch_units(const void* x, uint32_t x_st, const int32_t* pos, int64_t n, int k,
+                           int row, void* xs, uint32_t xs_st, cudaStream_t s) {
+  MoveShape m;
+  const int un = move_shape(m, n, row / UB, 8);
+  const unsigned grid = move_grid(m);
+  const char* in = static_cast<const char*>(x);
+  char* out = static_cast<char*>(xs);
+  if (un == 1) k_expert_dispatch<UB, 1><<<grid, kMoveThreads, 0, s>>>(in, x_st, pos, k, m, out, xs_st);
+  else if (un == 2) k_expert_dispatch<UB, 2><<<grid, kMoveThreads, 0, s>>>(in, x_st, pos, k, m, out, xs_st);
+  else if (un == 4) k_expert_dispatch<UB, 4><<<grid, kMoveThreads, 0, s>>>(in, x_st, pos, k, m, out, xs_st);
+  else k_expert_dispatch<UB, 8><<<grid, kMoveThreads, 0, s>>>(in, x_st, pos, k, m, out, xs_st);
 }
 
 cudaError_t launch_expert_dispatch(const void* x, int64_t x_ld, const int32_t* pos, int64_t n, int k,
                                    int dim, int elem, void* xs, int64_t xs_ld, cudaStream_t s) {
   if (n == 0) return cudaSuccess;
-  const int64_t xb = x_ld * elem, sb = xs_ld * elem, row = (int64_t)dim * elem;
-  const uint64_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(xs) |
-                       (uint64_t)xb | (uint64_t)sb | (uint64_t)row;
-  const char* xc = static_cast<const char*>(x);
-  char* xsc = static_cast<char*>(xs);
-  // the widest unit that every row start and the row length are multiples of
-  if ((all & 15) == 0) {
-    const MoveTile t = move_tile(n, row / 16);
-    k_expert_dispatch<16><<<move_grid(t), kMoveThreads, 0, s>>>(xc, xb, pos, k, t, xsc, sb);
-  } else if ((all & 3) == 0) {
-    const MoveTile t = move_tile(n, row / 4);
-    k_expert_dispatch<4><<<move_grid(t), kMoveThreads, 0, s>>>(xc, xb, pos, k, t, xsc, sb);
-  } else {
-    const MoveTile t = move_tile(n, row / 2);
-    k_expert_dispatch<2><<<move_grid(t), kMoveThreads, 0, s>>>(xc, xb, pos, k, t, xsc, sb);
-  }
+  const uint32_t x_st = (uint32_t)(x_ld * elem), xs_st = (uint32_t)(xs_ld * elem);
+  const int row = dim * elem;
+  const uint64_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(xs) | x_st | xs_st |
+                       (uint64_t)row;
+  if ((all & 15) == 0) dispatch_units<16>(x, x_st, pos, n, k, row, xs, xs_st, s);
+  else if ((all & 3) == 0) dispatch_units<4>(x, x_st, pos, n, k, row, xs, xs_st, s);
+  else dispatch_units<2>(x, x_st, pos, n, k, row, xs, xs_st, s);
   return cudaGetLastError();
 }
 
-// ---- combine: each row gathers its kept sorted rows, fp32 sum in the order of j ----
-// KU sorted rows are loaded together (min(k, 4)); the products and sums are fp32 whatever the
-// rows' type, rounded once into out.
-template <typename T, int EPU, int KU, bool WEIGHTED>
-__global__ void __launch_bounds__(kMoveThreads) k_expert_combine(const T* ys, int64_t ys_ld,
-                                                                 const int32_t* pos, const float* w,
-                                                                 int k, MoveTile t, T* out,
-                                                                 int64_t out_ld) {
-  const int64_t S = t.n * k;
-  for (int64_t tile = blockIdx.x; tile < t.tiles; tile += gridDim.x) {
-    const int64_t row0 = tile * t.R;
-    const int rows = (int)(t.n - row0 < t.R ? t.n - row0 : t.R);
-    const uint32_t items = (uint32_t)rows * t.U.d;
-    for (uint32_t i = threadIdx.x; i < items; i += kMoveThreads) {
-      const uint32_t r = t.U.div(i), c = i - r * t.U.d;
-      const int64_t q0 = (row0 + r) * k;
-      float acc[EPU];
+// Combine: KU sorted rows are loaded together (min(k, 4)); products and sums are fp32 whatever
+// the rows' type, in the order of j, rounded once into out.
+template <typename T, int EPU, int UN, int KU, bool WEIGHTED>
+__global__ void __launch_bounds__(kMoveThreads)
+    k_expert_combine(const T* ys, uint32_t ys_st, const int32_t* pos, const float* w, int k,
+                     MoveShape m, T* out, uint32_t out_st) {
+  constexpr int UB = EPU * (int)sizeof(T);
+  uint32_t row;
+  int unit;
+  if (!move_task(m, UN, row, unit)) return;
+  const uint32_t S = m.n * (uint32_t)k;
+  const uint64_t q0 = (uint64_t)row * k;
+  float acc[UN][EPU];
 #pragma unroll
-      for (int m = 0; m < EPU; ++m) acc[m] = 0.f;
-      for (int j0 = 0; j0 < k; j0 += KU) {
-        Pack<T, EPU> v[KU];
-        bool in[KU];
+  for (int u = 0; u < UN; ++u)
 #pragma unroll
-        for (int j = 0; j < KU; ++j) {
-          const int64_t p = j0 + j < k ? (int64_t)pos[q0 + j0 + j] : -1;
-          in[j] = p >= 0 && p < S;
-          if (in[j]) v[j].load(ys + p * ys_ld + (int64_t)c * EPU);
-        }
+    for (int e = 0; e < EPU; ++e) acc[u][e] = 0.f;
+  for (int j0 = 0; j0 < k; j0 += KU) {
+    Pack<T, EPU> v[KU][UN];
+    uint32_t p[KU];
 #pragma unroll
-        for (int j = 0; j < KU; ++j)
-          if (in[j]) {
-            float f[EPU];
-            v[j].get(f);
-            const float g = WEIGHTED ? w[q0 + j0 + j] : 1.f;
+    for (int j = 0; j < KU; ++j) p[j] = j0 + j < k ? (uint32_t)pos[q0 + j0 + j] : ~0u;
 #pragma unroll
-            for (int m = 0; m < EPU; ++m) acc[m] = WEIGHTED ? fmaf(g, f[m], acc[m]) : acc[m] + f[m];
-          }
+    for (int j = 0; j < KU; ++j)
+      if (p[j] < S) {  // a dropped slot's place is negative: above S
+        const char* src = reinterpret_cast<const char*>(ys) + ((uint64_t)p[j] * ys_st + (uint32_t)unit * UB);
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+          if (unit + u * m.lanes < m.U) v[j][u].load(reinterpret_cast<const T*>(src + u * m.lanes * UB));
       }
-      Pack<T, EPU> o;
-      o.set(acc);
-      o.store(out + (row0 + r) * out_ld + (int64_t)c * EPU);
-    }
+#pragma unroll
+    for (int j = 0; j < KU; ++j)
+      if (p[j] < S) {
+        const float g = WEIGHTED ? w[q0 + j0 + j] : 1.f;
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          if (unit + u * m.lanes >= m.U) continue;
+          float f[EPU];
+          v[j][u].get(f);
+#pragma unroll
+          for (int e = 0; e < EPU; ++e) acc[u][e] = WEIGHTED ? fmaf(g, f[e], acc[u][e]) : acc[u][e] + f[e];
+        }
+      }
   }
+  char* dst = reinterpret_cast<char*>(out) + ((uint64_t)row * out_st + (uint32_t)unit * UB);
+#pragma unroll
+  for (int u = 0; u < UN; ++u)
+    if (unit + u * m.lanes < m.U) {
+      Pack<T, EPU> o;
+      o.set(acc[u]);
+      o.store(reinterpret_cast<T*>(dst + u * m.lanes * UB));
+    }
+}
+
+template <typename T, int EPU, int UN, bool WEIGHTED>
+static void combine_un(const T* ys, uint32_t ys_st, const int32_t* pos, const float* w, int k,
+                       const MoveShape& m, T* out, uint32_t out_st, cudaStream_t s) {
+  const unsigned grid = move_grid(m);
+  if (k == 1)
+    k_expert_combine<T, EPU, UN, 1, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
+  else if (k == 2)
+    k_expert_combine<T, EPU, UN, 2, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
+  else
+    k_expert_combine<T, EPU, UN, 4, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
 }
 
 template <typename T, int EPU>
-static void combine_k(const void* ys, int64_t ys_ld, const int32_t* pos, const float* w, int64_t n,
-                      int k, int dim, void* out, int64_t out_ld, cudaStream_t s) {
-  const MoveTile t = move_tile(n, dim / EPU);
-  const int grid = move_grid(t);
+static void combine_units(const void* ys, uint32_t ys_st, const int32_t* pos, const float* w,
+                          int64_t n, int k, int dim, void* out, uint32_t out_st, cudaStream_t s) {
+  MoveShape m;
+  const int un = move_shape(m, n, dim / EPU, EPU == 8 ? 2 : 4);
   const T* y = static_cast<const T*>(ys);
   T* o = static_cast<T*>(out);
-#define EMB_COMBINE(KU)                                                                          \
-  (w ? k_expert_combine<T, EPU, KU, true><<<grid, kMoveThreads, 0, s>>>(y, ys_ld, pos, w, k, t, o, out_ld) \
-     : k_expert_combine<T, EPU, KU, false><<<grid, kMoveThreads, 0, s>>>(y, ys_ld, pos, w, k, t, o, out_ld))
-  if (k == 1) EMB_COMBINE(1);
-  else if (k == 2) EMB_COMBINE(2);
-  else EMB_COMBINE(4);
-#undef EMB_COMBINE
+  const auto run = [&](auto unc) {
+    constexpr int UN = decltype(unc)::value;
+    if (w) combine_un<T, EPU, UN, true>(y, ys_st, pos, w, k, m, o, out_st, s);
+    else combine_un<T, EPU, UN, false>(y, ys_st, pos, w, k, m, o, out_st, s);
+  };
+  if (un == 1) run(std::integral_constant<int, 1>{});
+  else if (un == 2) run(std::integral_constant<int, 2>{});
+  else if constexpr (EPU < 8) run(std::integral_constant<int, 4>{});
 }
 
 // w NULL: weights of one (the gradient of dispatch)
@@ -328,122 +386,133 @@ cudaError_t launch_expert_combine(const void* ys, int64_t ys_ld, const int32_t* 
                                   cudaStream_t s) {
   if (n == 0) return cudaSuccess;
   const int elem = bf16 ? 2 : 4;
-  const bool vec = rows16(ys, ys_ld, elem) && rows16(out, out_ld, elem) && dim * elem % 16 == 0;
+  const uint32_t ys_st = (uint32_t)(ys_ld * elem), out_st = (uint32_t)(out_ld * elem);
+  const uint64_t all = reinterpret_cast<uintptr_t>(ys) | reinterpret_cast<uintptr_t>(out) | ys_st |
+                       out_st | (uint64_t)(dim * elem);
+  using H = __nv_bfloat16;
   if (bf16) {
-    if (vec) combine_k<__nv_bfloat16, 8>(ys, ys_ld, pos, w, n, k, dim, out, out_ld, s);
-    else combine_k<__nv_bfloat16, 1>(ys, ys_ld, pos, w, n, k, dim, out, out_ld, s);
+    if ((all & 15) == 0) combine_units<H, 8>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
+    else if ((all & 3) == 0) combine_units<H, 2>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
+    else combine_units<H, 1>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
   } else {
-    if (vec) combine_k<float, 4>(ys, ys_ld, pos, w, n, k, dim, out, out_ld, s);
-    else combine_k<float, 1>(ys, ys_ld, pos, w, n, k, dim, out, out_ld, s);
+    if ((all & 15) == 0) combine_units<float, 4>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
+    else combine_units<float, 1>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
   }
   return cudaGetLastError();
 }
 
 // ---- gradient of combine: dys and dw in one pass over dout and the sorted rows ----
-// `tpr` threads share a row (a power of two, at least 4): each pack of dout is loaded once,
-// multiplied into the row's k sorted places and dotted with their rows; the k dot products
-// are summed over the threads at the end.  Rows of more than 32 threads are summed through
-// shared memory.
+// `tpr` threads share a row (a power of two): each unit of dout is loaded once, multiplied into
+// the row's k sorted places and dotted with their rows; the k dot products are summed over
+// the threads at the end.  A warp takes a row (less where 32 units are more than the row);
+// batches too small to fill the device that way take up to a CTA a row, whose warps add
+// their parts in shared memory.  UN units are in flight a thread, for each of the k rows.
 constexpr int kCombThreads = 256;
 
-template <typename T, int EPU, int KM>
+template <typename T, int EPU, int KM, int UN>
 __global__ void __launch_bounds__(kCombThreads)
-    k_expert_combine_bwd(const T* dout, int64_t dout_ld, const T* ys, int64_t ys_ld,
-                         const int32_t* pos, const float* w, int64_t n, int k, int U, int tpr,
-                         T* dys, int64_t dys_ld, float* dw) {
+    k_expert_combine_bwd(const T* dout, uint32_t dout_st, const T* ys, uint32_t ys_st,
+                         const int32_t* pos, const float* w, uint32_t n, int k, int U, int shift,
+                         T* dys, uint32_t dys_st, float* dw) {
+  constexpr int UB = EPU * (int)sizeof(T);
   __shared__ float part[KM][kCombThreads / 32];
-  const int rpb = kCombThreads / tpr, sub = threadIdx.x % tpr;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t S = n * k;
-  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < n; r0 += (int64_t)gridDim.x * rpb) {
-    const int64_t row = r0 + threadIdx.x / tpr;
-    const bool live = row < n;
-    int64_t to[KM];
-    bool kept[KM];
-    float g[KM], dot[KM];
+  const int tpr = 1 << shift, sub = threadIdx.x & (tpr - 1);
+  const uint32_t row = blockIdx.x * (kCombThreads >> shift) + (threadIdx.x >> shift);
+  const bool live = row < n;
+  const uint32_t S = n * (uint32_t)k;
+  const uint64_t q0 = (uint64_t)row * k;
+  int32_t p[KM];
+  float g[KM], dot[KM];
+#pragma unroll
+  for (int j = 0; j < KM; ++j) {
+    dot[j] = g[j] = 0.f;
+    p[j] = live && j < k ? pos[q0 + j] : (int32_t)0x80000000;  // a place no slot has
+  }
+#pragma unroll
+  for (int j = 0; j < KM; ++j)
+    if (p[j] >= 0) g[j] = w[q0 + j];
+  const char* gr = reinterpret_cast<const char*>(dout) + (uint64_t)row * dout_st;
+  if (live)
+    for (int c0 = sub; c0 < U; c0 += tpr * UN) {
+      Pack<T, EPU> d[UN], y[KM][UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u)
+        if (c0 + u * tpr < U) d[u].load(reinterpret_cast<const T*>(gr + (uint32_t)(c0 + u * tpr) * UB));
+#pragma unroll
+      for (int j = 0; j < KM; ++j)
+        if ((uint32_t)p[j] < S) {
+          const char* src = reinterpret_cast<const char*>(ys) + ((uint64_t)(uint32_t)p[j] * ys_st + (uint32_t)c0 * UB);
+#pragma unroll
+          for (int u = 0; u < UN; ++u)
+            if (c0 + u * tpr < U) y[j][u].load(reinterpret_cast<const T*>(src + u * tpr * UB));
+        }
+#pragma unroll
+      for (int j = 0; j < KM; ++j) {
+        const bool kept = p[j] >= 0;
+        const uint32_t to = (uint32_t)(kept ? p[j] : ~p[j]);
+        if (to >= S) continue;
+        char* dst = reinterpret_cast<char*>(dys) + ((uint64_t)to * dys_st + (uint32_t)c0 * UB);
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          if (c0 + u * tpr >= U) continue;
+          Pack<T, EPU> o;
+          if (kept) {
+            float f[EPU], v[EPU];
+            d[u].get(f);
+            y[j][u].get(v);
+#pragma unroll
+            for (int e = 0; e < EPU; ++e) {
+              dot[j] = fmaf(f[e], v[e], dot[j]);
+              f[e] *= g[j];
+            }
+            o.set(f);
+          } else {
+            o.zero();
+          }
+          o.store(reinterpret_cast<T*>(dst + u * tpr * UB));
+        }
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < KM; ++j) dot[j] = lanes_sum(dot[j], tpr < 32 ? tpr : 32);
+  if (tpr > 32) {
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int j = 0; j < KM; ++j) part[j][threadIdx.x >> 5] = dot[j];
+    __syncthreads();
+    const int w0 = (threadIdx.x >> shift) << (shift - 5);
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
       dot[j] = 0.f;
-      g[j] = 0.f;
-      to[j] = S;
-      kept[j] = false;
-      if (live && j < k) {
-        const int32_t p = pos[row * k + j];
-        kept[j] = p >= 0 && p < S;
-        to[j] = p >= 0 ? (int64_t)p : -1 - (int64_t)p;
-        if (kept[j]) g[j] = w[row * k + j];
-      }
+      for (int i = 0; i < tpr / 32; ++i) dot[j] += part[j][w0 + i];
     }
-    if (live)
-      for (int c = sub; c < U; c += tpr) {
-        Pack<T, EPU> d, y[KM];
-        d.load(dout + row * dout_ld + (int64_t)c * EPU);
-#pragma unroll
-        for (int j = 0; j < KM; ++j)
-          if (kept[j]) y[j].load(ys + to[j] * ys_ld + (int64_t)c * EPU);
-        float f[EPU];
-        d.get(f);
-#pragma unroll
-        for (int j = 0; j < KM; ++j) {
-          if (to[j] >= S) continue;
-          float o[EPU];
-          Pack<T, EPU> out;
-          if (kept[j]) {
-            float v[EPU];
-            y[j].get(v);
-#pragma unroll
-            for (int m = 0; m < EPU; ++m) {
-              dot[j] = fmaf(f[m], v[m], dot[j]);
-              o[m] = g[j] * f[m];
-            }
-            out.set(o);
-          } else {
-            out.zero();
-          }
-          out.store(dys + to[j] * dys_ld + (int64_t)c * EPU);
-        }
-      }
-#pragma unroll
-    for (int j = 0; j < KM; ++j) dot[j] = lanes_sum(dot[j], tpr < 32 ? tpr : 32);
-    if (tpr > 32) {
-      __syncthreads();
-      if (lane == 0)
-#pragma unroll
-        for (int j = 0; j < KM; ++j) part[j][warp] = dot[j];
-      __syncthreads();
-      const int w0 = threadIdx.x / tpr * (tpr / 32);
-#pragma unroll
-      for (int j = 0; j < KM; ++j) {
-        dot[j] = 0.f;
-        for (int i = 0; i < tpr / 32; ++i) dot[j] += part[j][w0 + i];
-      }
-    }
-    if (live && sub == 0)
-#pragma unroll
-      for (int j = 0; j < KM; ++j)
-        if (j < k) dw[row * k + j] = dot[j];
   }
+  if (live && sub == 0)
+#pragma unroll
+    for (int j = 0; j < KM; ++j)
+      if (j < k) dw[q0 + j] = dot[j];
 }
 
 template <typename T, int EPU>
-static void combine_bwd_k(const void* dout, int64_t dout_ld, const void* ys, int64_t ys_ld,
-                          const int32_t* pos, const float* w, int64_t n, int k, int dim, void* dys,
-                          int64_t dys_ld, float* dw, cudaStream_t s) {
+static void combine_bwd_units(const void* dout, uint32_t dout_st, const void* ys, uint32_t ys_st,
+                              const int32_t* pos, const float* w, int64_t n, int k, int dim,
+                              void* dys, uint32_t dys_st, float* dw, cudaStream_t s) {
   const int U = dim / EPU;
-  int tpr = 4;
-  while (tpr < kCombThreads && tpr < U) tpr *= 2;
-  const int rpb = kCombThreads / tpr;
-  const int64_t blocks = (n + rpb - 1) / rpb, cap = (int64_t)device_sms() * 64;
-  const int grid = (int)(blocks < cap ? blocks : cap);
-#define EMB_COMBINE_BWD(KM)                                                                  \
-  k_expert_combine_bwd<T, EPU, KM><<<grid, kCombThreads, 0, s>>>(                            \
-      static_cast<const T*>(dout), dout_ld, static_cast<const T*>(ys), ys_ld, pos, w, n, k, U, \
-      tpr, static_cast<T*>(dys), dys_ld, dw)
-  if (k == 1) EMB_COMBINE_BWD(1);
-  else if (k == 2) EMB_COMBINE_BWD(2);
-  else if (k <= 4) EMB_COMBINE_BWD(4);
-  else if (k <= 8) EMB_COMBINE_BWD(8);
-  else EMB_COMBINE_BWD(16);
+  int shift = 0;
+  while ((1 << shift) < U && shift < 5) ++shift;
+  // more threads a row while that leaves under 16 warps an SM and the row has units for them
+  const int64_t enough = (int64_t)device_sms() * 16 * 32;
+  while (shift >= 5 && shift < 8 && (n << shift) < enough && (1 << shift) < U) ++shift;
+  const unsigned grid = (unsigned)(((n << shift) + kCombThreads - 1) / kCombThreads);
+#define EMB_COMBINE_BWD(KM, UN)                                                                   \
+  k_expert_combine_bwd<T, EPU, KM, UN><<<grid, kCombThreads, 0, s>>>(                             \
+      static_cast<const T*>(dout), dout_st, static_cast<const T*>(ys), ys_st, pos, w, (uint32_t)n, \
+      k, U, shift, static_cast<T*>(dys), dys_st, dw)
+  if (k == 1) EMB_COMBINE_BWD(1, 4);
+  else if (k == 2) EMB_COMBINE_BWD(2, 2);
+  else if (k <= 4) EMB_COMBINE_BWD(4, (EPU > 2 ? 1 : 2));
+  else if (k <= 8) EMB_COMBINE_BWD(8, 1);
+  else EMB_COMBINE_BWD(16, 1);
 #undef EMB_COMBINE_BWD
 }
 
@@ -453,14 +522,18 @@ cudaError_t launch_expert_combine_bwd(const void* dout, int64_t dout_ld, const v
                                       cudaStream_t s) {
   if (n == 0) return cudaSuccess;
   const int elem = bf16 ? 2 : 4;
-  const bool vec = rows16(dout, dout_ld, elem) && rows16(ys, ys_ld, elem) &&
-                   rows16(dys, dys_ld, elem) && dim * elem % 16 == 0;
+  const uint32_t g_st = (uint32_t)(dout_ld * elem), y_st = (uint32_t)(ys_ld * elem),
+                 o_st = (uint32_t)(dys_ld * elem);
+  const uint64_t all = reinterpret_cast<uintptr_t>(dout) | reinterpret_cast<uintptr_t>(ys) |
+                       reinterpret_cast<uintptr_t>(dys) | g_st | y_st | o_st | (uint64_t)(dim * elem);
+  using H = __nv_bfloat16;
   if (bf16) {
-    if (vec) combine_bwd_k<__nv_bfloat16, 8>(dout, dout_ld, ys, ys_ld, pos, w, n, k, dim, dys, dys_ld, dw, s);
-    else combine_bwd_k<__nv_bfloat16, 1>(dout, dout_ld, ys, ys_ld, pos, w, n, k, dim, dys, dys_ld, dw, s);
+    if ((all & 15) == 0) combine_bwd_units<H, 8>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
+    else if ((all & 3) == 0) combine_bwd_units<H, 2>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
+    else combine_bwd_units<H, 1>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
   } else {
-    if (vec) combine_bwd_k<float, 4>(dout, dout_ld, ys, ys_ld, pos, w, n, k, dim, dys, dys_ld, dw, s);
-    else combine_bwd_k<float, 1>(dout, dout_ld, ys, ys_ld, pos, w, n, k, dim, dys, dys_ld, dw, s);
+    if ((all & 15) == 0) combine_bwd_units<float, 4>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
+    else combine_bwd_units<float, 1>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
   }
   return cudaGetLastError();
 }

@@ -3,6 +3,9 @@
 // element), held as loaded and widened to fp32 where they are used.
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "emb_internal.cuh"
 
 namespace emb {
@@ -42,6 +45,24 @@ struct Pack<float, 4> {
     r = make_float4(v[0], v[1], v[2], v[3]);
   }
   __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = r; }
+};
+
+template <>
+struct Pack<__nv_bfloat16, 2> {
+  uint32_t r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ void zero() { r = 0u; }
+  __device__ __forceinline__ void get(float (&v)[2]) const {
+    v[0] = __uint_as_float(r << 16);
+    v[1] = __uint_as_float(r & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ void set(const float (&v)[2]) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
+    r = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint32_t*>(p) = r; }
 };
 
 template <>
@@ -110,6 +131,21 @@ struct FastDiv {
 __device__ __forceinline__ float lanes_sum(float v, int tpr) {
   for (int o = tpr >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
+}
+
+// Launches the second kernel of a call so that it may start while the first still runs: the
+// kernel must pass griddepcontrol.wait, which holds until the first has finished and its
+// writes are visible, before it touches anything the first or earlier work writes or reads.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), int grid, int threads, int smem, cudaStream_t s,
+                         A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem, cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
 }
 
 // Multiprocessors of the current device (context-free calls).
