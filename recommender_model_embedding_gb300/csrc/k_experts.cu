@@ -21,54 +21,67 @@ namespace emb {
 // A first launch counts each chunk's keys; the second (started early: it waits for the first
 // only where it reads the counts) sums those counts over the chunks (every CTA reads all of
 // them from L2), scans them over the experts and places the slots.  A single chunk needs no
-// first launch.  Bound by latency, not bytes: chunks are as small as the SMs allow, and a
-// warp has the ids of eight groups of 32 slots in flight.
-constexpr int kSortWarps = 16, kSortThreads = kSortWarps * 32;
+// first launch.  Bound by latency, not bytes: a chunk is as short as one CTA an SM allows, a
+// warp loads the ids of eight groups of 32 slots at once, and where that is all of its part
+// (KEEP: chunks of up to 8192 slots) keys and ranks stay in registers from counting to placing.
+constexpr int kSortWarps = 32, kSortThreads = kSortWarps * 32;
 constexpr int kSortDepth = 8;      // groups of 32 ids a warp loads at once
 constexpr int kSortSingle = 4096;  // slots of one CTA alone, at most
 
-// Calls f(slot, key) for the groups of 32 slots of a warp's part [w0, w0 + 32 * groups), with all
-// lanes; key E + 1 past the end.
-template <typename F>
-__device__ __forceinline__ void each_key(const int64_t* ids, int64_t w0, int64_t groups, int64_t end,
-                                         int E, F f) {
-  const int lane = threadIdx.x & 31;
-  for (int64_t g0 = 0; g0 < groups; g0 += kSortDepth) {
-    uint32_t key[kSortDepth];
+// Keys of up to eight groups of 32 slots of a warp's part, from group g0 on; E + 1 past its end.
+__device__ __forceinline__ void load_keys(const int64_t* ids, int64_t w0, int64_t g0, int64_t groups,
+                                          int64_t end, int E, uint32_t (&key)[kSortDepth]) {
 #pragma unroll
-    for (int u = 0; u < kSortDepth; ++u) {
-      const int64_t q = w0 + (g0 + u) * 32 + lane;
-      key[u] = (uint32_t)E + 1u;
-      if (g0 + u < groups && q < end) {
-        const uint64_t id = (uint64_t)ids[q];
-        key[u] = id < (uint64_t)E ? (uint32_t)id : (uint32_t)E;
-      }
+  for (int u = 0; u < kSortDepth; ++u) {
+    const int64_t q = w0 + (g0 + u) * 32 + (threadIdx.x & 31);
+    key[u] = (uint32_t)E + 1u;
+    if (g0 + u < groups && q < end) {
+      const uint64_t id = (uint64_t)ids[q];
+      key[u] = id < (uint64_t)E ? (uint32_t)id : (uint32_t)E;
     }
-#pragma unroll
-    for (int u = 0; u < kSortDepth; ++u)
-      if (g0 + u < groups) f(w0 + (g0 + u) * 32 + lane, key[u]);
   }
+}
+
+// A slot's rank among the warp's earlier ones of its key, counted up in `mine` (all lanes call).
+__device__ __forceinline__ uint32_t take_rank(uint32_t* mine, uint32_t key, int E) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
+  const bool in = key <= (uint32_t)E;
+  const uint32_t at = in ? mine[key] : 0u;
+  __syncwarp();
+  if (in && lane == __ffs(peers) - 1) mine[key] = at + __popc(peers);
+  __syncwarp();
+  return at + __popc(peers & ((1u << lane) - 1u));
 }
 
 __global__ void __launch_bounds__(kSortThreads) k_expert_count(const int64_t* ids, int64_t S, int E,
                                                                int64_t chunk, uint32_t* hist) {
   extern __shared__ uint32_t sm_count[];
   asm volatile("griddepcontrol.launch_dependents;");
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) sm_count[e] = 0;
-  __syncthreads();
   const int lane = threadIdx.x & 31;
   const int64_t c0 = (int64_t)blockIdx.x * chunk;
   const int64_t c1 = c0 + chunk < S ? c0 + chunk : S;
   const int64_t groups = (c1 - c0 + kSortThreads - 1) / kSortThreads;
-  each_key(ids, c0 + (threadIdx.x >> 5) * groups * 32, groups, c1, E, [&](int64_t, uint32_t key) {
-    const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
-    if (key <= (uint32_t)E && lane == __ffs(peers) - 1) atomicAdd(sm_count + key, __popc(peers));
-  });
+  const int64_t w0 = c0 + (threadIdx.x >> 5) * groups * 32;
+  uint32_t key[kSortDepth];
+  load_keys(ids, w0, 0, groups, c1, E, key);
+  for (int e = threadIdx.x; e <= E; e += kSortThreads) sm_count[e] = 0;
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += blockDim.x)
+  for (int64_t g0 = 0; g0 < groups; g0 += kSortDepth) {
+    if (g0) load_keys(ids, w0, g0, groups, c1, E, key);
+#pragma unroll
+    for (int u = 0; u < kSortDepth; ++u) {
+      if (g0 + u >= groups) break;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key[u]);
+      if (key[u] <= (uint32_t)E && lane == __ffs(peers) - 1) atomicAdd(sm_count + key[u], __popc(peers));
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += kSortThreads)
     hist[(int64_t)blockIdx.x * (E + 1) + e] = sm_count[e];
 }
 
+template <bool KEEP>
 __global__ void __launch_bounds__(kSortThreads)
     k_expert_place(const int64_t* ids, int64_t S, int E, int64_t chunk, const uint32_t* hist,
                    int32_t* order, int32_t* pos, int32_t* offsets) {
@@ -79,26 +92,36 @@ __global__ void __launch_bounds__(kSortThreads)
   uint32_t* total = sm_place + kSortWarps * K;
   uint32_t* before = total + K;
   uint32_t* mine = sm_place + warp * K;
-  for (int e = threadIdx.x; e < (kSortWarps + 2) * K; e += blockDim.x) sm_place[e] = 0;
-  __syncthreads();
   const int64_t c0 = (int64_t)blockIdx.x * chunk;
   const int64_t c1 = c0 + chunk < S ? c0 + chunk : S;
   const int64_t groups = (c1 - c0 + kSortThreads - 1) / kSortThreads;
   const int64_t w0 = c0 + warp * groups * 32;
-  each_key(ids, w0, groups, c1, E, [&](int64_t, uint32_t key) {
-    const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
-    if (key <= (uint32_t)E && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
-    __syncwarp();
-  });
+  uint32_t key[kSortDepth], rank[kSortDepth];
+  load_keys(ids, w0, 0, groups, c1, E, key);
+  for (int e = threadIdx.x; e < (kSortWarps + 2) * K; e += kSortThreads) sm_place[e] = 0;
+  __syncthreads();
+  for (int64_t g0 = 0; g0 < groups; g0 += kSortDepth) {
+    if (g0) load_keys(ids, w0, g0, groups, c1, E, key);
+#pragma unroll
+    for (int u = 0; u < kSortDepth; ++u)
+      if (g0 + u < groups) rank[u] = take_rank(mine, key[u], E);
+  }
   if (hist) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int e = lane; e < K; e += 32) {  // warp w: chunks w, w + 16, ...
+    for (int e = lane; e < K; e += 32) {  // warp w: chunks w, w + 32, ...
       uint32_t t = 0, b = 0;
-#pragma unroll 10
-      for (uint32_t g = warp; g < gridDim.x; g += kSortWarps) {
-        const uint32_t c = __ldcg(hist + (int64_t)g * K + e);
-        t += c;
-        b += g < blockIdx.x ? c : 0u;
+      for (uint32_t g0 = warp; g0 < gridDim.x; g0 += kSortWarps * 5) {
+        uint32_t c[5];  // loaded together: one trip to L2 for up to 160 chunks
+#pragma unroll
+        for (int u = 0; u < 5; ++u) {
+          const uint32_t g = g0 + u * kSortWarps;
+          c[u] = g < gridDim.x ? __ldcg(hist + (int64_t)g * K + e) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < 5; ++u) {
+          t += c[u];
+          b += g0 + u * kSortWarps < blockIdx.x ? c[u] : 0u;
+        }
       }
       if (t) atomicAdd(total + e, t);
       if (b) atomicAdd(before + e, b);
@@ -106,16 +129,22 @@ __global__ void __launch_bounds__(kSortThreads)
   }
   __syncthreads();
   // per key: earlier warps' counts, and its first place: earlier keys' totals + earlier chunks
-  const int per = (K + blockDim.x - 1) / blockDim.x;  // keys of a thread (consecutive)
+  const int per = (K + kSortThreads - 1) / kSortThreads;  // keys of a thread (consecutive): 1 or 2
   uint32_t sum = 0;
   for (int i = 0; i < per; ++i) {
     const int e = threadIdx.x * per + i;
     if (e >= K) break;
     uint32_t run = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t c = sm_place[w * K + e];
-      sm_place[w * K + e] = run;
-      run += c;
+#pragma unroll
+    for (int w0 = 0; w0 < kSortWarps; w0 += 8) {
+      uint32_t c[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) c[w] = sm_place[(w0 + w) * K + e];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        sm_place[(w0 + w) * K + e] = run;
+        run += c[w];
+      }
     }
     if (!hist) total[e] = run;
     sum += total[e];
@@ -128,8 +157,10 @@ __global__ void __launch_bounds__(kSortThreads)
   }
   if (lane == 31) warp_tot[warp] = incl;
   __syncthreads();
-  uint32_t first = incl - sum;
-  for (int w = 0; w < warp; ++w) first += warp_tot[w];
+  uint32_t first = lane < warp ? warp_tot[lane] : 0u;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) first += __shfl_xor_sync(0xFFFFFFFFu, first, o);
+  first += incl - sum;
   for (int i = 0; i < per; ++i) {
     const int e = threadIdx.x * per + i;
     if (e >= K) break;
@@ -139,19 +170,22 @@ __global__ void __launch_bounds__(kSortThreads)
     first += t;
   }
   __syncthreads();
-  each_key(ids, w0, groups, c1, E, [&](int64_t q, uint32_t key) {
-    const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
-    const bool in = key <= (uint32_t)E;
-    const uint32_t at = in ? mine[key] : 0u;
-    __syncwarp();
-    if (in && lane == __ffs(peers) - 1) mine[key] = at + __popc(peers);
-    __syncwarp();
-    if (in) {
-      const uint32_t p = total[key] + at + __popc(peers & ((1u << lane) - 1u));
-      pos[q] = key < (uint32_t)E ? (int32_t)p : ~(int32_t)p;
-      order[p] = (int32_t)q;
+  for (int64_t g0 = 0; g0 < groups; g0 += kSortDepth) {
+    if (!KEEP) load_keys(ids, w0, g0, groups, c1, E, key);
+#pragma unroll
+    for (int u = 0; u < kSortDepth; ++u) {
+      if (g0 + u >= groups) break;
+      uint32_t p;
+      if (KEEP) p = (key[u] <= (uint32_t)E ? mine[key[u]] : 0u) + rank[u];
+      else p = take_rank(mine, key[u], E);
+      if (key[u] <= (uint32_t)E) {
+        const int64_t q = w0 + (g0 + u) * 32 + lane;
+        p += total[key[u]];
+        pos[q] = key[u] < (uint32_t)E ? (int32_t)p : ~(int32_t)p;
+        order[p] = (int32_t)q;
+      }
     }
-  });
+  }
 }
 
 static int64_t sort_chunk(int64_t S, int sms) {
@@ -171,19 +205,20 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
   const int64_t chunk = sort_chunk(S, device_sms());
   const int G = S > 0 ? (int)((S + chunk - 1) / chunk) : 1;  // an empty batch still writes offsets
   uint32_t* hist = G > 1 ? static_cast<uint32_t*>(ws) : nullptr;
+  const auto place = chunk <= kSortDepth * kSortThreads ? k_expert_place<true> : k_expert_place<false>;
   const int smem = (kSortWarps + 2) * (E + 1) * (int)sizeof(uint32_t);
-  cudaError_t e = smem > 48 * 1024 ? cudaFuncSetAttribute(k_expert_place, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
+  cudaError_t e = smem > 48 * 1024 ? cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
                                    : cudaSuccess;
   if (e != cudaSuccess) return e;
   if (!hist) {
-    k_expert_place<<<G, kSortThreads, smem, s>>>(ids, S, E, chunk, hist, order, pos, offsets);
+    place<<<G, kSortThreads, smem, s>>>(ids, S, E, chunk, hist, order, pos, offsets);
     return cudaGetLastError();
   }
   k_expert_count<<<G, kSortThreads, (E + 1) * sizeof(uint32_t), s>>>(ids, S, E, chunk, hist);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_early(k_expert_place, G, kSortThreads, smem, s, ids, S, E, chunk,
-                      (const uint32_t*)hist, order, pos, offsets);
+  return launch_early(place, G, kSortThreads, smem, s, ids, S, E, chunk, (const uint32_t*)hist, order,
+                      pos, offsets);
 }
 
 // ---- rows to and from their sorted places ----
@@ -300,7 +335,7 @@ cudaError_t launch_expert_dispatch(const void* x, int64_t x_ld, const int32_t* p
 // Combine: KU sorted rows are loaded together (min(k, 4)); products and sums are fp32 whatever
 // the rows' type, in the order of j, rounded once into out.
 template <typename T, int EPU, int UN, int KU, bool WEIGHTED>
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, EPU * UN * KU > 48 ? 3 : 4)
     k_expert_combine(const T* ys, uint32_t ys_st, const int32_t* pos, const float* w, int k,
                      MoveShape m, T* out, uint32_t out_st) {
   constexpr int UB = EPU * (int)sizeof(T);
@@ -317,8 +352,12 @@ __global__ void __launch_bounds__(kMoveThreads)
   for (int j0 = 0; j0 < k; j0 += KU) {
     Pack<T, EPU> v[KU][UN];
     uint32_t p[KU];
+    float g[KU];
 #pragma unroll
-    for (int j = 0; j < KU; ++j) p[j] = j0 + j < k ? (uint32_t)pos[q0 + j0 + j] : ~0u;
+    for (int j = 0; j < KU; ++j) {
+      p[j] = j0 + j < k ? (uint32_t)pos[q0 + j0 + j] : ~0u;
+      g[j] = WEIGHTED && j0 + j < k ? w[q0 + j0 + j] : 1.f;
+    }
 #pragma unroll
     for (int j = 0; j < KU; ++j)
       if (p[j] < S) {  // a dropped slot's place is negative: above S
@@ -330,14 +369,13 @@ __global__ void __launch_bounds__(kMoveThreads)
 #pragma unroll
     for (int j = 0; j < KU; ++j)
       if (p[j] < S) {
-        const float g = WEIGHTED ? w[q0 + j0 + j] : 1.f;
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
           if (unit + u * m.lanes >= m.U) continue;
           float f[EPU];
           v[j][u].get(f);
 #pragma unroll
-          for (int e = 0; e < EPU; ++e) acc[u][e] = WEIGHTED ? fmaf(g, f[e], acc[u][e]) : acc[u][e] + f[e];
+          for (int e = 0; e < EPU; ++e) acc[u][e] = WEIGHTED ? fmaf(g[j], f[e], acc[u][e]) : acc[u][e] + f[e];
         }
       }
   }
@@ -359,6 +397,8 @@ static void combine_un(const T* ys, uint32_t ys_st, const int32_t* pos, const fl
     k_expert_combine<T, EPU, UN, 1, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
   else if (k == 2)
     k_expert_combine<T, EPU, UN, 2, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
+  else if (k == 3)
+    k_expert_combine<T, EPU, UN, 3, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
   else
     k_expert_combine<T, EPU, UN, 4, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
 }
@@ -367,7 +407,7 @@ template <typename T, int EPU>
 static void combine_units(const void* ys, uint32_t ys_st, const int32_t* pos, const float* w,
                           int64_t n, int k, int dim, void* out, uint32_t out_st, cudaStream_t s) {
   MoveShape m;
-  const int un = move_shape(m, n, dim / EPU, EPU == 8 ? 2 : 4);
+  const int un = move_shape(m, n, dim / EPU, EPU > 2 ? 2 : 8 / EPU);
   const T* y = static_cast<const T*>(ys);
   T* o = static_cast<T*>(out);
   const auto run = [&](auto unc) {
@@ -377,7 +417,10 @@ static void combine_units(const void* ys, uint32_t ys_st, const int32_t* pos, co
   };
   if (un == 1) run(std::integral_constant<int, 1>{});
   else if (un == 2) run(std::integral_constant<int, 2>{});
-  else if constexpr (EPU < 8) run(std::integral_constant<int, 4>{});
+  else if constexpr (EPU <= 2) {
+    if (un == 4) run(std::integral_constant<int, 4>{});
+    else if constexpr (EPU == 1) run(std::integral_constant<int, 8>{});
+  }
 }
 
 // w NULL: weights of one (the gradient of dispatch)
