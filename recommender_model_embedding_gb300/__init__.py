@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -99,11 +100,11 @@ _SIGS = {
     "emb_expert_combine": ([_P, _I64, _P, _P, _I64, _I32, _I32, _I32, _P, _I64, _P], ctypes.c_int),
     "emb_expert_combine_backward": ([_P, _I64, _P, _I64, _P, _P, _I64, _I32, _I32, _I32, _P, _I64,
                                      _P, _P], ctypes.c_int),
-    "emb_gated_norm": ([ctypes.POINTER(EmbNorm), _P], ctypes.c_int),
+    "emb_gated_norm": ([_P, _P], ctypes.c_int),
     "emb_gated_norm_backward_workspace": ([_I64, _I32], _I64),
-    "emb_gated_norm_backward": ([ctypes.POINTER(EmbNorm), _P, _I64, _P], ctypes.c_int),
+    "emb_gated_norm_backward": ([_P, _P, _I64, _P], ctypes.c_int),
     "emb_clip_grads_workspace": ([_I64], _I64),
-    "emb_clip_grads": ([ctypes.POINTER(EmbTensor), _I64, ctypes.c_float, _P, _P, _I64, _P], ctypes.c_int),
+    "emb_clip_grads": ([_P, _I64, ctypes.c_float, _P, _P, _I64, _P], ctypes.c_int),
     "emb_unique_keys_noalloc": ([_P, _I64, _P, _P, _P, _P], ctypes.c_int),
 }
 NOALLOC_MAX_KEYS = 524288
@@ -228,51 +229,78 @@ def _stream(stream) -> Optional[int]:
 
 
 # ---- expert tower (context-free) ----
+# These calls are short enough on the device for their own cost on the host to count: tensors are
+# checked by a few attribute reads, structures are packed in one step, and the reason of a
+# refusal is looked for only once there is one.
 EXPERT_MAX, EXPERT_MAX_K, EXPERT_MAX_DIM, NORM_MAX_DIM = 1024, 16, 65536, 8192
+_NORM_PACK = struct.Struct("@q4if4x6Q3q2Q2q5Q3Q5q")  # struct emb_norm
+assert _NORM_PACK.size == ctypes.sizeof(EmbNorm)
 
-_ROW_TYPES = {}  # torch dtype -> (EMB_F32 or EMB_BF16); filled on first use
+_TORCH = {}  # "f32", "bf16", "i32", "i64" -> torch dtype, and "raw_stream"; filled on first use
+_ROW_CODES = {}  # torch dtype of a matrix -> EMB_F32 or EMB_BF16
 
 
-def _row_type(t, name: str) -> int:
-    if not _ROW_TYPES:
-        import torch
-        _ROW_TYPES[torch.float32], _ROW_TYPES[torch.bfloat16] = F32, BF16
-    code = _ROW_TYPES.get(t.dtype)
+def _load_torch():
+    import torch
+    _ROW_CODES[torch.float32], _ROW_CODES[torch.bfloat16] = F32, BF16
+    _TORCH.update(f32=torch.float32, bf16=torch.bfloat16, i32=torch.int32, i64=torch.int64,
+                  raw_stream=getattr(torch._C, "_cuda_getCurrentRawStream", None))
+
+
+def _row_code(t, name: str) -> int:
+    if not _ROW_CODES:
+        _load_torch()
+    code = _ROW_CODES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
     return code
 
 
-def _rows(t, code: int, n: int, dim: int, name: str):
-    """(pointer, row step) of a CUDA matrix [n, dim] of the given element type; its rows may lie
+def _rows(t, dtype, n: int, dim: int, name: str):
+    """(pointer, row step) of a CUDA matrix [n, dim] of the given torch dtype; its rows may lie
     any number of elements apart."""
-    if not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{name}: expected a CUDA matrix")
-    if _row_type(t, name) != code:
-        raise ValueError(f"{name}: expected {'bfloat16' if code == BF16 else 'float32'}, got {t.dtype}")
-    if t.shape[0] != n or t.shape[1] != dim:
-        raise ValueError(f"{name}: {tuple(t.shape)}, expected {(n, dim)}")
-    step, inner = t.stride()
-    if inner != 1 and dim > 1:
+    if t.dtype is dtype and t.shape == (n, dim) and t.is_cuda:
+        step, inner = t.stride()
+        if inner == 1 or dim <= 1:
+            return t.data_ptr(), step if n > 1 else dim
         raise ValueError(f"{name}: the elements of a row must be adjacent")
-    return t.data_ptr(), step if n > 1 else dim
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA matrix")
+    raise ValueError(f"{name}: expected {dtype} {(n, dim)}, got {t.dtype} {tuple(t.shape)}")
 
 
-def _opt_rows(t, code: int, n: int, dim: int, name: str):
-    return (None, 0) if t is None else _rows(t, code, n, dim, name)
+def _flat(t, kind: str, n: int, name: str) -> int:
+    """_dptr of a tensor that has to be there."""
+    if t is not None and t.dtype is _TORCH[kind] and t.numel() >= n and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if t is None:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return _dptr(t, kind, n, name)
 
 
-def _vec(t, dim: int, name: str) -> Optional[int]:
-    if t is not None and t.numel() != dim:
+def _vec(t, dim: int, name: str) -> int:
+    """Address of an optional float32 vector of dim elements (0: none)."""
+    if t is None:
+        return 0
+    if t.numel() != dim:
         raise ValueError(f"{name}: {t.numel()} elements, expected {dim}")
-    return _dptr(t, "f32", dim, name)
+    return _flat(t, "f32", dim, name)
+
+
+def _on(stream, like) -> Optional[int]:
+    """The call's stream: the given one, or the current one of the tensor's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    raw = _TORCH["raw_stream"]
+    return raw(like.get_device()) if raw is not None else _stream(None)
 
 
 def _workspace(need: int, workspace, stream, like):
-    """The caller's workspace (any contiguous CUDA tensor of enough bytes), or one from torch's
-    allocator, taken on the call's stream so that its memory is reused in that stream's order."""
+    """(tensor, address, bytes) of the caller's workspace (any contiguous CUDA tensor of enough
+    bytes), or of one from torch's allocator, taken on the call's stream so that its memory is
+    reused in that stream's order.  The tensor has to live until the call has been made."""
     if need <= 0:
-        return None, 0
+        return None, None, 0
     if workspace is None:
         import torch
         if stream is None:
@@ -280,11 +308,11 @@ def _workspace(need: int, workspace, stream, like):
         else:
             with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return workspace, workspace.data_ptr(), need
     have = workspace.numel() * workspace.element_size()
     if have < need:
         raise ValueError(f"workspace: {have} bytes, at least {need} needed")
-    _dptr(workspace, name="workspace")
-    return workspace, have
+    return workspace, _dptr(workspace, name="workspace"), have
 
 
 def expert_sort_workspace(n: int, k: int, num_experts: int) -> int:
@@ -297,24 +325,26 @@ def expert_sort(ids, num_experts: int, order, pos, offsets, workspace=None, stre
     [0, num_experts): dropped) stably by expert into `order` (int32 [n*k], slot at each place),
     `pos` (int32 [n*k], place of each slot, -1 - place when dropped) and `offsets` (int32
     [num_experts + 1], first place of each expert; the last: kept slots).  Asynchronous."""
+    if not _TORCH:
+        _load_torch()
     if ids.dim() != 2:
         raise ValueError("ids: expected a matrix [n, k]")
     n, k = ids.shape
     S = n * k
-    args = (_dptr(ids, "i64", S, "ids"), n, k, num_experts, _dptr(order, "i32", S, "order"),
-            _dptr(pos, "i32", S, "pos"), _dptr(offsets, "i32", num_experts + 1, "offsets"))
-    ws, have = _workspace(_lib.emb_expert_sort_workspace(n, k, num_experts), workspace, stream, ids)
-    _check("emb_expert_sort", _lib.emb_expert_sort(*args, _dptr(ws), have, _stream(stream)))
+    ip, op, pp = _flat(ids, "i64", S, "ids"), _flat(order, "i32", S, "order"), _flat(pos, "i32", S, "pos")
+    fp = _flat(offsets, "i32", num_experts + 1, "offsets")
+    ws, wp, have = _workspace(_lib.emb_expert_sort_workspace(n, k, num_experts), workspace, stream, ids)
+    st = _lib.emb_expert_sort(ip, n, k, num_experts, op, pp, fp, wp, have, _on(stream, ids))
+    if st:
+        _check("emb_expert_sort", st)
 
 
 def _slots(pos, n: int) -> int:
     """Experts of a row: k of a pos with n * k places."""
     S = pos.numel()
-    if n == 0:
-        if S:
-            raise ValueError(f"pos: {S} elements for no rows")
+    if n == 0 and S == 0:
         return 1
-    if S % n or not S:
+    if n == 0 or S % n or not S:
         raise ValueError(f"pos: {S} elements, expected a multiple of {n} rows")
     return S // n
 
@@ -322,68 +352,65 @@ def _slots(pos, n: int) -> int:
 def expert_dispatch(x, pos, xs, stream=None):
     """xs[pos[i, j]] = x[i] for the kept slots, zero rows at the dropped ones' places.  x [n, d]
     and xs [n*k, d] float32 or bfloat16, rows any step apart; pos of expert_sort."""
-    code, (n, d) = _row_type(x, "x"), x.shape
+    code, t, (n, d) = _row_code(x, "x"), x.dtype, x.shape
     k = _slots(pos, n)
-    xp, xl = _rows(x, code, n, d, "x")
-    op, ol = _rows(xs, code, n * k, d, "xs")
-    _check("emb_expert_dispatch",
-           _lib.emb_expert_dispatch(xp, xl, _dptr(pos, "i32", n * k, "pos"), n, k, d, code, op, ol,
-                                    _stream(stream)))
+    xp, xl = _rows(x, t, n, d, "x")
+    op, ol = _rows(xs, t, n * k, d, "xs")
+    st = _lib.emb_expert_dispatch(xp, xl, _flat(pos, "i32", n * k, "pos"), n, k, d, code, op, ol,
+                                  _on(stream, x))
+    if st:
+        _check("emb_expert_dispatch", st)
 
 
 def expert_dispatch_backward(dxs, pos, dx, stream=None):
     """dx[i] = sum of dxs over row i's kept places (dxs [n*k, d], dx [n, d])."""
-    code, (n, d) = _row_type(dx, "dx"), dx.shape
+    code, t, (n, d) = _row_code(dx, "dx"), dx.dtype, dx.shape
     k = _slots(pos, n)
-    ip, il = _rows(dxs, code, n * k, d, "dxs")
-    op, ol = _rows(dx, code, n, d, "dx")
-    _check("emb_expert_dispatch_backward",
-           _lib.emb_expert_dispatch_backward(ip, il, _dptr(pos, "i32", n * k, "pos"), n, k, d, code,
-                                             op, ol, _stream(stream)))
+    ip, il = _rows(dxs, t, n * k, d, "dxs")
+    op, ol = _rows(dx, t, n, d, "dx")
+    st = _lib.emb_expert_dispatch_backward(ip, il, _flat(pos, "i32", n * k, "pos"), n, k, d, code, op,
+                                           ol, _on(stream, dx))
+    if st:
+        _check("emb_expert_dispatch_backward", st)
 
 
 def expert_combine(ys, pos, w, out, stream=None):
     """out[i] = sum over row i's kept slots of w[i, j] * ys[place] (ys [n*k, d], w float32
     [n, k], out [n, d])."""
-    code, (n, d) = _row_type(out, "out"), out.shape
+    code, t, (n, d) = _row_code(out, "out"), out.dtype, out.shape
     k = _slots(pos, n)
-    ip, il = _rows(ys, code, n * k, d, "ys")
-    op, ol = _rows(out, code, n, d, "out")
-    _check("emb_expert_combine",
-           _lib.emb_expert_combine(ip, il, _dptr(pos, "i32", n * k, "pos"),
-                                   _dptr(w, "f32", n * k, "w"), n, k, d, code, op, ol,
-                                   _stream(stream)))
+    ip, il = _rows(ys, t, n * k, d, "ys")
+    op, ol = _rows(out, t, n, d, "out")
+    st = _lib.emb_expert_combine(ip, il, _flat(pos, "i32", n * k, "pos"), _flat(w, "f32", n * k, "w"), n,
+                                 k, d, code, op, ol, _on(stream, out))
+    if st:
+        _check("emb_expert_combine", st)
 
 
 def expert_combine_backward(dout, ys, pos, w, dys, dw, stream=None):
     """Gradients of expert_combine: dys [n*k, d] (zero rows at dropped places) and dw float32
     [n, k] (0 when dropped)."""
-    code, (n, d) = _row_type(dout, "dout"), dout.shape
+    code, t, (n, d) = _row_code(dout, "dout"), dout.dtype, dout.shape
     k = _slots(pos, n)
-    gp, gl = _rows(dout, code, n, d, "dout")
-    yp, yl = _rows(ys, code, n * k, d, "ys")
-    op, ol = _rows(dys, code, n * k, d, "dys")
-    _check("emb_expert_combine_backward",
-           _lib.emb_expert_combine_backward(gp, gl, yp, yl, _dptr(pos, "i32", n * k, "pos"),
-                                            _dptr(w, "f32", n * k, "w"), n, k, d, code, op, ol,
-                                            _dptr(dw, "f32", n * k, "dw"), _stream(stream)))
+    gp, gl = _rows(dout, t, n, d, "dout")
+    yp, yl = _rows(ys, t, n * k, d, "ys")
+    op, ol = _rows(dys, t, n * k, d, "dys")
+    st = _lib.emb_expert_combine_backward(gp, gl, yp, yl, _flat(pos, "i32", n * k, "pos"),
+                                          _flat(w, "f32", n * k, "w"), n, k, d, code, op, ol,
+                                          _flat(dw, "f32", n * k, "dw"), _on(stream, dout))
+    if st:
+        _check("emb_expert_combine_backward", st)
 
 
-def _norm_args(x, y, gate, h, eps, names):
-    """The sizes and types of a gated-norm call, from the residual stream x and the first of the
-    block's matrices that is there."""
-    code, (n, d) = _row_type(x, names[0]), x.shape
-    block = next((t for t in (y, h) if t is not None), None)
-    bcode = code if block is None else _row_type(block, "y" if y is not None else names[1])
-    a = EmbNorm(n=n, dim=d, x_dtype=code, dtype=bcode, eps=eps)
-    a.d_y, a.y_ld = _opt_rows(y, bcode, n, d, "y")
-    if gate is not None:
-        cols = gate.shape[-1]
-        if cols not in (1, d):
-            raise ValueError(f"gate: {cols} columns, expected 1 or {d}")
-        a.gate_cols = cols
-        a.d_gate, a.gate_ld = _rows(gate, bcode, n, cols, "gate")
-    return a, code, bcode, n, d
+def _gate(gate, dtype, n: int, d: int):
+    """(address, row step, columns) of an optional gate."""
+    if gate is None:
+        return 0, 0, 0
+    cols = gate.shape[-1]
+    if cols != 1 and cols != d:
+        raise ValueError(f"gate: {cols} columns, expected 1 or {d}")
+    p, step = _rows(gate, dtype, n, cols, "gate")
+    return p, step, cols
 
 
 def gated_norm(x, y, x_out, h, gate=None, w_post=None, res_scale=None, w_pre=None,
@@ -393,13 +420,26 @@ def gated_norm(x, y, x_out, h, gate=None, w_post=None, res_scale=None, w_pre=Non
     x, x_out [n, d] float32 or bfloat16; y, h, gate ([n, d], or [n, 1]: one gate a row) of one
     type, bfloat16 or as x; vectors float32 [d], None counts as ones.  y None: h from x alone;
     h None: only x_out.  x_out may be x.  Asynchronous."""
-    a, code, bcode, n, d = _norm_args(x, y, gate, h, eps, ("x", "h"))
-    a.d_x, a.x_ld = _rows(x, code, n, d, "x")
-    a.d_x_out, a.x_out_ld = _opt_rows(x_out, code, n, d, "x_out")
-    a.d_h, a.h_ld = _opt_rows(h, bcode, n, d, "h")
-    a.d_w_post, a.d_res_scale = _vec(w_post, d, "w_post"), _vec(res_scale, d, "res_scale")
-    a.d_w_pre = _vec(w_pre, d, "w_pre")
-    _check("emb_gated_norm", _lib.emb_gated_norm(ctypes.byref(a), _stream(stream)))
+    code, xt, (n, d) = _row_code(x, "x"), x.dtype, x.shape
+    bt, bcode = xt, code
+    yp = yl = op = ol = hp = hl = 0
+    if y is not None:
+        bt, bcode = y.dtype, _row_code(y, "y")
+        yp, yl = _rows(y, bt, n, d, "y")
+    elif h is not None:
+        bt, bcode = h.dtype, _row_code(h, "h")
+    xp, xl = _rows(x, xt, n, d, "x")
+    if x_out is not None:
+        op, ol = _rows(x_out, xt, n, d, "x_out")
+    if h is not None:
+        hp, hl = _rows(h, bt, n, d, "h")
+    gp, gl, cols = _gate(gate, bt, n, d)
+    st = _lib.emb_gated_norm(
+        _NORM_PACK.pack(n, d, code, bcode, cols, eps, yp, gp, _vec(w_post, d, "w_post"),
+                        _vec(res_scale, d, "res_scale"), _vec(w_pre, d, "w_pre"), op, yl, gl, ol, xp,
+                        hp, xl, hl, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0), _on(stream, x))
+    if st:
+        _check("emb_gated_norm", st)
 
 
 def gated_norm_backward_workspace(n: int, d: int) -> int:
@@ -413,20 +453,35 @@ def gated_norm_backward(dx_out, dh, x_out, y, dx, dy, gate=None, w_post=None, re
     """Gradients of gated_norm from dx_out (None: zero) and dh (None: no h), with x_out, y, gate
     and the vectors of the forward: dx, dy, dgate and the vectors' (float32 [d], overwritten).
     Outputs may be None; dx may be dx_out.  Asynchronous."""
-    a, code, bcode, n, d = _norm_args(x_out, y, gate, dh, eps, ("x_out", "dh"))
-    a.d_x_out, a.x_out_ld = _rows(x_out, code, n, d, "x_out")
-    a.d_dx_out, a.dx_out_ld = _opt_rows(dx_out, code, n, d, "dx_out")
-    a.d_dh, a.dh_ld = _opt_rows(dh, bcode, n, d, "dh")
-    a.d_dx, a.dx_ld = _opt_rows(dx, code, n, d, "dx")
-    a.d_dy, a.dy_ld = _opt_rows(dy, bcode, n, d, "dy")
+    code, xt, (n, d) = _row_code(x_out, "x_out"), x_out.dtype, x_out.shape
+    bt, bcode = xt, code
+    yp = yl = tp = tl = hp = hl = dp = dl = ep = el = qp = ql = 0
+    if y is not None:
+        bt, bcode = y.dtype, _row_code(y, "y")
+        yp, yl = _rows(y, bt, n, d, "y")
+    elif dh is not None:
+        bt, bcode = dh.dtype, _row_code(dh, "dh")
+    xp, xl = _rows(x_out, xt, n, d, "x_out")
+    if dx_out is not None:
+        tp, tl = _rows(dx_out, xt, n, d, "dx_out")
+    if dh is not None:
+        hp, hl = _rows(dh, bt, n, d, "dh")
+    if dx is not None:
+        dp, dl = _rows(dx, xt, n, d, "dx")
+    if dy is not None:
+        ep, el = _rows(dy, bt, n, d, "dy")
+    gp, gl, cols = _gate(gate, bt, n, d)
     if dgate is not None:
-        a.d_dgate, a.dgate_ld = _rows(dgate, bcode, n, a.gate_cols if gate is not None else d, "dgate")
-    a.d_w_post, a.d_res_scale = _vec(w_post, d, "w_post"), _vec(res_scale, d, "res_scale")
-    a.d_w_pre, a.d_dw_post = _vec(w_pre, d, "w_pre"), _vec(dw_post, d, "dw_post")
-    a.d_dres_scale, a.d_dw_pre = _vec(dres_scale, d, "dres_scale"), _vec(dw_pre, d, "dw_pre")
-    ws, have = _workspace(_lib.emb_gated_norm_backward_workspace(n, d), workspace, stream, x_out)
-    _check("emb_gated_norm_backward",
-           _lib.emb_gated_norm_backward(ctypes.byref(a), _dptr(ws), have, _stream(stream)))
+        qp, ql = _rows(dgate, bt, n, cols or d, "dgate")
+    ws, wp, have = _workspace(_lib.emb_gated_norm_backward_workspace(n, d), workspace, stream, x_out)
+    st = _lib.emb_gated_norm_backward(
+        _NORM_PACK.pack(n, d, code, bcode, cols, eps, yp, gp, _vec(w_post, d, "w_post"),
+                        _vec(res_scale, d, "res_scale"), _vec(w_pre, d, "w_pre"), xp, yl, gl, xl, 0,
+                        0, 0, 0, tp, hp, dp, ep, qp, _vec(dw_post, d, "dw_post"),
+                        _vec(dres_scale, d, "dres_scale"), _vec(dw_pre, d, "dw_pre"), tl, hl, dl, el,
+                        ql), wp, have, _on(stream, x_out))
+    if st:
+        _check("emb_gated_norm_backward", st)
 
 
 def clip_grads_workspace(count: int) -> int:
@@ -439,26 +494,35 @@ def clip_grads(grads, max_norm: float, norm, out=None, workspace=None, stream=No
     min(1, max_norm / norm), in place or into `out` (contiguous CUDA tensors, float32 or
     bfloat16, of the gradients' types and sizes).  An infinite or NaN norm clips nothing.
     Asynchronous."""
-    grads = list(grads)
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError(f"out: {len(outs)} tensors for {len(grads)} gradients")
-    lst = (EmbTensor * len(grads))()
-    for e, g, o in zip(lst, grads, outs):
-        if not g.is_cuda or not g.is_contiguous():
-            raise ValueError("grads: expected contiguous CUDA tensors")
-        e.dtype = _row_type(g, "grads")
-        e.numel = g.numel()
-        e.d_src = e.d_out = g.data_ptr()
-        if o is not g:
-            if not o.is_cuda or not o.is_contiguous() or o.dtype != g.dtype or o.numel() != e.numel:
+    if not _TORCH:
+        _load_torch()
+    codes, flat = _ROW_CODES, []
+    if out is None:
+        for g in grads:
+            code = codes.get(g.dtype)
+            if code is None or not g.is_cuda or not g.is_contiguous():
+                raise ValueError("grads: expected contiguous CUDA tensors, float32 or bfloat16")
+            p = g.data_ptr()
+            flat += (p, p, g.numel(), code)
+    else:
+        grads, out = list(grads), list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"out: {len(out)} tensors for {len(grads)} gradients")
+        for g, o in zip(grads, out):
+            t, m = g.dtype, g.numel()
+            code = codes.get(t)
+            if code is None or not g.is_cuda or not g.is_contiguous():
+                raise ValueError("grads: expected contiguous CUDA tensors, float32 or bfloat16")
+            if o.dtype is not t or o.numel() != m or not o.is_cuda or not o.is_contiguous():
                 raise ValueError("out: expected contiguous CUDA tensors of the gradients' types and sizes")
-            e.d_out = o.data_ptr()
-    np_ = _dptr(norm, "f32", 1, "norm")
-    ws, have = _workspace(_lib.emb_clip_grads_workspace(len(grads)), workspace, stream, norm)
-    _check("emb_clip_grads",
-           _lib.emb_clip_grads(lst, len(grads), float(max_norm), np_, _dptr(ws), have,
-                               _stream(stream)))
+            flat += (g.data_ptr(), o.data_ptr(), m, code)
+    count = len(flat) // 4
+    np_ = _flat(norm, "f32", 1, "norm")
+    ws, wp, have = _workspace(_lib.emb_clip_grads_workspace(count), workspace, stream, norm)
+    st = _lib.emb_clip_grads(struct.pack("@" + "QQqi4x" * count, *flat), count, max_norm, np_, wp, have,
+                             _on(stream, norm))
+    if st:
+        _check("emb_clip_grads", st)
 
 
 class EmbCtx:

@@ -665,14 +665,18 @@ static int norm_ring(NormArgs& a, int thread_bytes) {
   return a.stages * per;
 }
 
-// CTAs of `kern` on the device at once.
+// CTAs on the device at once: `per` an SM by registers (the kernels' launch bounds), fewer where
+// shared memory (the ring, and up to 3 KB beside it) allows no more.
+static int64_t norm_ctas(int per, int smem) {
+  const int fit = 227 * 1024 / (smem + 3 * 1024);
+  return (int64_t)(fit < 1 ? 1 : fit < per ? fit : per) * device_sms();
+}
+
+// Rings above the default limit have to be asked for.
 template <typename K>
-static int norm_ctas(K kern, int threads, int smem, cudaError_t* e) {
-  int per = 0;
-  *e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (*e == cudaSuccess)
-    *e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, smem);
-  return (per < 1 ? 1 : per) * device_sms();
+static cudaError_t norm_smem(K kern, int smem) {
+  return smem <= 44 * 1024 ? cudaSuccess
+                           : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 static NormArgs norm_args(const emb_norm& p) {
@@ -711,8 +715,8 @@ template <typename XT, typename BT, int EPU, int V, bool GATE>
 static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
   const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>), threads = a.rpb * a.tpr;
   const auto kern = k_gated_norm<XT, BT, EPU, V, GATE>;
-  cudaError_t e;
-  const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = norm_ctas(kern, threads, smem, &e);
+  const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = norm_ctas(V * EPU > 8 ? kNormWide / threads : 4, smem);
+  const cudaError_t e = norm_smem(kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<(int)(blocks < cap ? blocks : cap), threads, smem, s>>>(a);
   return cudaGetLastError();
@@ -725,7 +729,7 @@ static int64_t norm_bwd_grid(int64_t n, int rpb, int64_t cap) {
   return blocks < 1 ? 1 : blocks < cap ? blocks : cap;
 }
 
-constexpr int kNormCtasPerSm = 4;  // CTAs of the backward per SM, at most
+constexpr int kNormCtasPerSm = 3;  // CTAs of the backward per SM, at most (wide rows: 160 threads and more)
 
 int64_t gated_norm_bwd_workspace(int64_t n, int dim) {
   NormArgs a{};
@@ -740,11 +744,9 @@ static cudaError_t norm_bwd_v(NormArgs& a, int* grid, cudaStream_t s) {
   const int threads = a.rpb * a.tpr, cols = a.rpb > 1 ? 2 * a.dim * (int)sizeof(float) : 0;
   if (smem < cols) smem = cols;
   const auto kern = k_gated_norm_bwd<XT, BT, EPU, V, GATE>;
-  cudaError_t e;
-  int64_t cap = norm_ctas(kern, threads, smem, &e);
+  const cudaError_t e = norm_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  if (cap > (int64_t)device_sms() * kNormCtasPerSm) cap = (int64_t)device_sms() * kNormCtasPerSm;
-  *grid = (int)norm_bwd_grid(a.n, a.rpb, cap);
+  *grid = (int)norm_bwd_grid(a.n, a.rpb, norm_ctas(V * EPU > 8 ? kNormWide / threads : kNormCtasPerSm, smem));
   kern<<<*grid, threads, smem, s>>>(a);
   return cudaGetLastError();
 }

@@ -3,6 +3,7 @@
 // element), held as loaded and widened to fp32 where they are used.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 #include <utility>
 
@@ -148,13 +149,20 @@ cudaError_t launch_early(void (*kern)(P...), int grid, int threads, int smem, cu
   return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
 }
 
-// Multiprocessors of the current device (context-free calls).
+// Multiprocessors of the current device (context-free calls; the count is read once a device).
 inline int device_sms() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    cudaGetLastError();
-  return sms < 1 ? 1 : sms;
+  if (cudaGetDevice(&dev) == cudaSuccess) {
+    if (dev < kDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && sms > 0) {
+      if (dev < kDevices) known[dev].store(sms, std::memory_order_relaxed);
+      return sms;
+    }
+  }
+  cudaGetLastError();
+  return 1;
 }
 
 // Whether a matrix of rows allows accesses of `bytes` (a power of two): base and row step on
