@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
 
 template <typename XT, typename BT, int EPU, int V, bool GATE>
 __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EPU > 8 ? 1 : 3) k_gated_norm_bwd(NormArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;");
   using K = Chunks<EPU, V>;
   using LX = Lane<XT, EPU, V>;
   using LB = Lane<BT, EPU, V>;
@@ -619,6 +620,7 @@ __global__ void __launch_bounds__(1024) k_gated_norm_cols(const float* part, int
                                                           float* dw_post, float* dres_scale,
                                                           float* dw_pre) {
   __shared__ float sh[2][32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, k = blockIdx.x * 32 + lane;
   float p = 0.f, t = 0.f;
   if (k < dim) {
@@ -787,10 +789,8 @@ cudaError_t launch_gated_norm_bwd(const emb_norm& p, void* ws, cudaStream_t s) {
   int grid = 0;
   cudaError_t e = p.n > 0 ? norm_call<true>(p, a, &grid, s) : cudaSuccess;
   if (e == cudaSuccess && (p.d_dw_post || p.d_dres_scale || p.d_dw_pre)) {
-    k_gated_norm_cols<<<(p.dim + 31) / 32, 1024, 0, s>>>(a.part, grid, p.dim, p.d_w_post,
-                                                         p.d_res_scale, p.d_dw_post, p.d_dres_scale,
-                                                         p.d_dw_pre);
-    e = cudaGetLastError();
+    e = launch_early(k_gated_norm_cols, (p.dim + 31) / 32, 1024, 0, s, (const float*)a.part, grid, p.dim,
+                     p.d_w_post, p.d_res_scale, p.d_dw_post, p.d_dres_scale, p.d_dw_pre);
   }
   return e;
 }
