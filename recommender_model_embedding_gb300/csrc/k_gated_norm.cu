@@ -239,6 +239,17 @@ __device__ __forceinline__ void load_cols(const float* w, int col, float* v) {
   }
 }
 
+// Which packs of a row a thread has: first, first + step, ... (V of them).  WARP: the row takes
+// whole warps, each V * 32 packs in a row, so that the step is known to the compiler (addresses
+// of a thread's packs differ by constants); else the threads of the row deal its packs in turn.
+template <int V, bool WARP>
+struct Share {
+  int first, tpr;
+  __device__ __forceinline__ Share(int sub, int tpr_)
+      : first(WARP ? (sub & ~31) * V + (sub & 31) : sub), tpr(tpr_) {}
+  __device__ __forceinline__ int step(int i) const { return WARP ? i * 32 : i * tpr; }
+};
+
 // How a thread's V packs of EPU elements are taken: in NC chunks of C elements (PP packs), the
 // unit of arithmetic.
 template <int EPU, int V>
@@ -248,15 +259,15 @@ struct Chunks {
 
 // res_scale * w_post and w_pre of a thread's columns: in registers for all its rows when it has
 // one chunk, else loaded where they are used (from L1).  Zero past the row's end.
-template <int EPU, int V>
+template <int EPU, int V, bool WARP>
 struct ColWeights {
   using K = Chunks<EPU, V>;
   float rw[K::C], wq[K::C];
-  __device__ __forceinline__ void load(const NormArgs& a, int sub, int chunk) {
+  __device__ __forceinline__ void load(const NormArgs& a, const Share<V, WARP>& sh, int chunk) {
     float wp[K::C];
 #pragma unroll
     for (int p = 0; p < K::PP; ++p) {
-      const int c = sub + (chunk * K::PP + p) * a.tpr;
+      const int c = sh.first + sh.step(chunk * K::PP + p);
 #pragma unroll
       for (int m = 0; m < EPU; ++m) rw[p * EPU + m] = wq[p * EPU + m] = wp[p * EPU + m] = 0.f;
       if (c < a.packs) {
@@ -267,11 +278,11 @@ struct ColWeights {
     }
     v_mul(rw, rw, wp);
   }
-  __device__ __forceinline__ void init(const NormArgs& a, int sub) {
-    if constexpr (K::NC == 1) load(a, sub, 0);
+  __device__ __forceinline__ void init(const NormArgs& a, const Share<V, WARP>& sh) {
+    if constexpr (K::NC == 1) load(a, sh, 0);
   }
-  __device__ __forceinline__ void use(const NormArgs& a, int sub, int chunk) {
-    if constexpr (K::NC > 1) load(a, sub, chunk);
+  __device__ __forceinline__ void use(const NormArgs& a, const Share<V, WARP>& sh, int chunk) {
+    if constexpr (K::NC > 1) load(a, sh, chunk);
   }
 };
 
@@ -280,41 +291,42 @@ template <typename XT, typename BT, int EPU, int V, int XS, int BS>
 constexpr int kRingBytes = V * EPU * (XS * (int)sizeof(XT) + BS * (int)sizeof(BT));
 
 // One matrix's part of the ring, and its rows in memory: offsets and strides in bytes.
-template <typename T, int EPU, int V>
+template <typename T, int EPU, int V, bool WARP>
 struct Lane {
   using S = Slot<T, EPU>;
+  using Sh = Share<V, WARP>;
   using K = Chunks<EPU, V>;
   uint32_t at, plane;  // this thread's place of the matrix in stage 0; bytes of a plane
   __device__ __forceinline__ uint32_t pack(uint32_t stage, int i) const {
     return at + stage + i * plane;
   }
   // the thread's packs of a row, into the ring (`left`: packs of the row from this thread's on)
-  __device__ __forceinline__ void fetch(uint32_t stage, const char* row, int left, int tpr) const {
+  __device__ __forceinline__ void fetch(uint32_t stage, const char* row, int left, const Sh& sh) const {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i * tpr < left) S::fetch(pack(stage, i), row + i * tpr * S::kBytes);
+      if (sh.step(i) < left) S::fetch(pack(stage, i), row + sh.step(i) * S::kBytes);
   }
-  __device__ __forceinline__ void zero_tail(uint32_t stage, int left, int tpr) const {
+  __device__ __forceinline__ void zero_tail(uint32_t stage, int left, const Sh& sh) const {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i * tpr >= left) S::zero(pack(stage, i));
+      if (sh.step(i) >= left) S::zero(pack(stage, i));
   }
   __device__ __forceinline__ void read(uint32_t stage, int chunk, float (&v)[K::C]) const {
 #pragma unroll
     for (int p = 0; p < K::PP; ++p) S::read(pack(stage, chunk * K::PP + p), v + p * EPU);
   }
   static __device__ __forceinline__ void store(char* row, int chunk, const float (&v)[K::C], int left,
-                                               int tpr) {
+                                               const Sh& sh) {
 #pragma unroll
     for (int p = 0; p < K::PP; ++p) {
       const int i = chunk * K::PP + p;
-      if (i * tpr < left) {
+      if (sh.step(i) < left) {
         float f[EPU];
 #pragma unroll
         for (int m = 0; m < EPU; ++m) f[m] = v[p * EPU + m];
         Pack<T, EPU> o;
         o.set(f);
-        o.store(reinterpret_cast<T*>(row + i * tpr * S::kBytes));
+        o.store(reinterpret_cast<T*>(row + sh.step(i) * S::kBytes));
       }
     }
   }
@@ -340,38 +352,39 @@ __device__ __forceinline__ void row_gate(const NormArgs& a, uint32_t row, float&
 }
 
 // GATE: a gate for each element.
-template <typename XT, typename BT, int EPU, int V, bool GATE>
+template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EPU > 8 ? 1 : 4) k_gated_norm(NormArgs a) {
   using K = Chunks<EPU, V>;
-  using LX = Lane<XT, EPU, V>;
-  using LB = Lane<BT, EPU, V>;
+  using LX = Lane<XT, EPU, V, WARP>;
+  using LB = Lane<BT, EPU, V, WARP>;
   extern __shared__ __align__(16) char ring[];
   __shared__ __align__(16) float red_all[8 * 2 * 16];
   for (int i = threadIdx.x; i < 8 * 2 * 16; i += blockDim.x) red_all[i] = 0.f;
   const RowGroup grp{a.tpr, (int)threadIdx.x / a.tpr, (int)threadIdx.x % a.tpr};
   float* red = red_all + (a.tpr > 32 ? grp.id : 0) * 2 * 16;
-  const int left = a.packs - grp.sub, tpr = a.tpr;
+  const Share<V, WARP> sh(grp.sub, a.tpr);
+  const int left = a.packs - sh.first, tpr = a.tpr;
   const uint32_t plx = blockDim.x * LX::S::kBytes, plb = blockDim.x * LB::S::kBytes;
   const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>;
   const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::kBytes;
   const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::kBytes + V * plx;
   const LX lx{tx, plx};
   const LB ly{tb, plb}, lg{tb + V * plb, plb};
-  const uint64_t cx = (uint32_t)grp.sub * LX::S::kBytes, cb = (uint32_t)grp.sub * LB::S::kBytes;
-  ColWeights<EPU, V> cw;
-  cw.init(a, grp.sub);
+  const uint64_t cx = (uint32_t)sh.first * LX::S::kBytes, cb = (uint32_t)sh.first * LB::S::kBytes;
+  ColWeights<EPU, V, WARP> cw;
+  cw.init(a, sh);
   for (int s = 0; s < a.stages; ++s) {
-    lx.zero_tail(s * stage_bytes, left, tpr);
-    ly.zero_tail(s * stage_bytes, left, tpr);
-    if (GATE) lg.zero_tail(s * stage_bytes, left, tpr);
+    lx.zero_tail(s * stage_bytes, left, sh);
+    ly.zero_tail(s * stage_bytes, left, sh);
+    if (GATE) lg.zero_tail(s * stage_bytes, left, sh);
   }
   __syncthreads();
 
   auto fetch = [&](uint32_t row, uint32_t stage) {
     if (row < a.n) {
-      lx.fetch(stage, at_row(a.x, row, a.x_st, cx), left, tpr);
-      if (a.y) ly.fetch(stage, at_row(a.y, row, a.y_st, cb), left, tpr);
-      if (GATE) lg.fetch(stage, at_row(a.gate, row, a.gate_st, cb), left, tpr);
+      lx.fetch(stage, at_row(a.x, row, a.x_st, cx), left, sh);
+      if (a.y) ly.fetch(stage, at_row(a.y, row, a.y_st, cb), left, sh);
+      if (GATE) lg.fetch(stage, at_row(a.gate, row, a.gate_st, cb), left, sh);
     }
     ring_commit();
   };
@@ -407,7 +420,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
         lx.read(st, i, x);
         if (a.y) {
           float g[K::C], y[K::C];
-          cw.use(a, grp.sub, i);
+          cw.use(a, sh, i);
           ly.read(st, i, y);
           v_mul(y, y, ry);
           if (GATE) {
@@ -419,7 +432,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
             v_mul(g, cw.rw, g_row);
           }
           v_fma(x, g, y, x);
-          LX::store(at_row(a.x_out, row, a.x_out_st, cx), i, x, left, tpr);
+          LX::store(at_row(a.x_out, row, a.x_out_st, cx), i, x, left, sh);
         }
         v_dot(s2, x, x);
 #pragma unroll
@@ -432,10 +445,10 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
       if (live)
 #pragma unroll
         for (int i = 0; i < K::NC; ++i) {
-          cw.use(a, grp.sub, i);
+          cw.use(a, sh, i);
           v_mul(f[i], f[i], rx);
           v_mul(f[i], f[i], cw.wq);
-          LB::store(at_row(a.h, row, a.h_st, cb), i, f[i], left, tpr);
+          LB::store(at_row(a.h, row, a.h_st, cb), i, f[i], left, sh);
         }
     }
     // a call with one sum a row leaves no second barrier between its uses of `red`
@@ -444,18 +457,19 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
   }
 }
 
-template <typename XT, typename BT, int EPU, int V, bool GATE>
+template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EPU > 8 ? 1 : 3) k_gated_norm_bwd(NormArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
   using K = Chunks<EPU, V>;
-  using LX = Lane<XT, EPU, V>;
-  using LB = Lane<BT, EPU, V>;
+  using LX = Lane<XT, EPU, V, WARP>;
+  using LB = Lane<BT, EPU, V, WARP>;
   extern __shared__ __align__(16) char ring[];
   __shared__ __align__(16) float red_all[8 * 4 * 16];
   for (int i = threadIdx.x; i < 8 * 4 * 16; i += blockDim.x) red_all[i] = 0.f;
   const RowGroup grp{a.tpr, (int)threadIdx.x / a.tpr, (int)threadIdx.x % a.tpr};
   float* red = red_all + (a.tpr > 32 ? grp.id : 0) * 4 * 16;
-  const int left = a.packs - grp.sub, tpr = a.tpr;
+  const Share<V, WARP> sh(grp.sub, a.tpr);
+  const int left = a.packs - sh.first, tpr = a.tpr;
   const uint32_t plx = blockDim.x * LX::S::kBytes, plb = blockDim.x * LB::S::kBytes;
   const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>;
   const uint32_t mx = V * plx, mb = V * plb;  // of a matrix
@@ -463,30 +477,30 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
   const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::kBytes + 2 * mx;
   const LX lx{tx, plx}, lt{tx + mx, plx};
   const LB ld{tb, plb}, ly{tb + mb, plb}, lg{tb + 2 * mb, plb};
-  const uint64_t cx = (uint32_t)grp.sub * LX::S::kBytes, cb = (uint32_t)grp.sub * LB::S::kBytes;
-  ColWeights<EPU, V> cw;
-  cw.init(a, grp.sub);
+  const uint64_t cx = (uint32_t)sh.first * LX::S::kBytes, cb = (uint32_t)sh.first * LB::S::kBytes;
+  ColWeights<EPU, V, WARP> cw;
+  cw.init(a, sh);
   float col_pre[K::NC][K::C], col_t[K::NC][K::C];
 #pragma unroll
   for (int i = 0; i < K::NC; ++i)
 #pragma unroll
     for (int m = 0; m < K::C; ++m) col_pre[i][m] = col_t[i][m] = 0.f;
   for (int s = 0; s < a.stages; ++s) {
-    lx.zero_tail(s * stage_bytes, left, tpr);
-    lt.zero_tail(s * stage_bytes, left, tpr);
-    ld.zero_tail(s * stage_bytes, left, tpr);
-    ly.zero_tail(s * stage_bytes, left, tpr);
-    if (GATE) lg.zero_tail(s * stage_bytes, left, tpr);
+    lx.zero_tail(s * stage_bytes, left, sh);
+    lt.zero_tail(s * stage_bytes, left, sh);
+    ld.zero_tail(s * stage_bytes, left, sh);
+    ly.zero_tail(s * stage_bytes, left, sh);
+    if (GATE) lg.zero_tail(s * stage_bytes, left, sh);
   }
   __syncthreads();
 
   auto fetch = [&](uint32_t row, uint32_t stage) {
     if (row < a.n) {
-      lx.fetch(stage, at_row(a.x_out, row, a.x_out_st, cx), left, tpr);
-      if (a.dx_out) lt.fetch(stage, at_row(a.dx_out, row, a.dx_out_st, cx), left, tpr);
-      if (a.dh) ld.fetch(stage, at_row(a.dh, row, a.dh_st, cb), left, tpr);
-      if (a.y) ly.fetch(stage, at_row(a.y, row, a.y_st, cb), left, tpr);
-      if (GATE) lg.fetch(stage, at_row(a.gate, row, a.gate_st, cb), left, tpr);
+      lx.fetch(stage, at_row(a.x_out, row, a.x_out_st, cx), left, sh);
+      if (a.dx_out) lt.fetch(stage, at_row(a.dx_out, row, a.dx_out_st, cx), left, sh);
+      if (a.dh) ld.fetch(stage, at_row(a.dh, row, a.dh_st, cb), left, sh);
+      if (a.y) ly.fetch(stage, at_row(a.y, row, a.y_st, cb), left, sh);
+      if (GATE) lg.fetch(stage, at_row(a.gate, row, a.gate_st, cb), left, sh);
     }
     ring_commit();
   };
@@ -508,7 +522,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
         lx.read(st, i, x);
         v_dot(sx, x, x);
         if (a.dh) {
-          cw.use(a, grp.sub, i);
+          cw.use(a, sh, i);
           ld.read(st, i, d);
           v_mul(d, d, cw.wq);
           v_dot(sd, d, x);
@@ -528,7 +542,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
 #pragma unroll
       for (int i = 0; i < K::NC; ++i) {
         float t[K::C];
-        cw.use(a, grp.sub, i);
+        cw.use(a, sh, i);
         if (a.dx_out) lt.read(st, i, t);
         else
 #pragma unroll
@@ -542,7 +556,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
           v_fma(t, x, xm, t);
           v_fma(col_pre[i], d, x, col_pre[i]);
         }
-        if (a.dx) LX::store(at_row(a.dx, row, a.dx_st, cx), i, t, left, tpr);
+        if (a.dx) LX::store(at_row(a.dx, row, a.dx_st, cx), i, t, left, sh);
         if (a.y) {
           float y[K::C], rest[K::C];
           ly.read(st, i, y);
@@ -562,7 +576,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
           if (GATE && a.dgate) {
             v_mul(y, u[i], y);
             v_mul(y, y, rest);
-            LB::store(at_row(a.dgate, row, a.dgate_st, cb), i, y, left, tpr);
+            LB::store(at_row(a.dgate, row, a.dgate_st, cb), i, y, left, sh);
           }
         }
       }
@@ -584,7 +598,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
           ly.read(st, i, y);
           v_mul(y, y, um);
           v_fma(y, u[i], ry, y);
-          LB::store(at_row(a.dy, row, a.dy_st, cb), i, y, left, tpr);
+          LB::store(at_row(a.dy, row, a.dy_st, cb), i, y, left, sh);
         }
     } else if (tpr > 32) {  // one sum a row: no second barrier between its uses of `red`
       asm volatile("bar.sync %0, %1;" ::"r"(grp.id + 1), "r"(tpr) : "memory");
@@ -600,10 +614,10 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
     if (grp.id != r) continue;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (i * tpr >= left) continue;
+      if (sh.step(i) >= left) continue;
 #pragma unroll
       for (int m = 0; m < EPU; ++m) {
-        const int k = (grp.sub + i * tpr) * EPU + m, e = i * EPU + m;
+        const int k = (sh.first + sh.step(i)) * EPU + m, e = i * EPU + m;
         float p = col_pre[e / K::C][e % K::C], q = col_t[e / K::C][e % K::C];
         if (r > 0) p += cols[k], q += cols[a.dim + k];
         if (r < a.rpb - 1) cols[k] = p, cols[a.dim + k] = q;
@@ -658,20 +672,24 @@ static void norm_shape(NormArgs& a, int epu) {
   a.rpb = t >= kNormThreads ? 1 : kNormThreads / t;
 }
 
-// Ring stages and their bytes: up to kStages, but no fewer than two CTAs an SM for it while two
-// stages are left, and at least one.
-static int norm_ring(NormArgs& a, int thread_bytes) {
-  const int per = a.rpb * a.tpr * thread_bytes, most = 220 * 1024;
-  a.stages = kStages;
-  while (a.stages > 1 && a.stages * per > (a.stages > 2 ? most / 2 : most)) --a.stages;
-  return a.stages * per;
+// CTAs an SM holds: `per` by registers (the kernels' launch bounds), fewer where shared memory
+// (the ring, and up to 3 KB beside it) allows no more.
+static int norm_fit(int per, int smem) {
+  const int fit = 227 * 1024 / (smem + 3 * 1024);
+  return fit < per ? fit : per;
 }
 
-// CTAs on the device at once: `per` an SM by registers (the kernels' launch bounds), fewer where
-// shared memory (the ring, and up to 3 KB beside it) allows no more.
-static int64_t norm_ctas(int per, int smem) {
-  const int fit = 227 * 1024 / (smem + 3 * 1024);
-  return (int64_t)(fit < 1 ? 1 : fit < per ? fit : per) * device_sms();
+// Ring stages and their bytes: kStages, but two where that puts more CTAs on an SM (as many rows
+// are in flight either way, and more warps hide the arithmetic), and one for the widest rows.
+static int norm_ring(NormArgs& a, int thread_bytes, int per) {
+  const int bytes = a.rpb * a.tpr * thread_bytes;
+  a.stages = kStages;
+  while (a.stages > 1) {
+    const int fit = norm_fit(per, a.stages * bytes);
+    if (fit > 0 && (a.stages == 2 || fit == norm_fit(per, (a.stages - 1) * bytes))) break;
+    --a.stages;
+  }
+  return a.stages * bytes;
 }
 
 // Rings above the default limit have to be asked for.
@@ -713,11 +731,12 @@ static bool norm_vec(const emb_norm& p) {
          rows16(p.d_res_scale, 0, 4) && rows16(p.d_w_pre, 0, 4);
 }
 
-template <typename XT, typename BT, int EPU, int V, bool GATE>
+template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
-  const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>), threads = a.rpb * a.tpr;
-  const auto kern = k_gated_norm<XT, BT, EPU, V, GATE>;
-  const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = norm_ctas(V * EPU > 8 ? kNormWide / threads : 4, smem);
+  const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : 4;
+  const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>, per);
+  const auto kern = k_gated_norm<XT, BT, EPU, V, GATE, WARP>;
+  const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = (int64_t)device_sms() * norm_fit(per, smem);
   const cudaError_t e = norm_smem(kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<(int)(blocks < cap ? blocks : cap), threads, smem, s>>>(a);
@@ -740,30 +759,37 @@ int64_t gated_norm_bwd_workspace(int64_t n, int dim) {
   return norm_bwd_grid(n, a.rpb, (int64_t)device_sms() * kNormCtasPerSm) * 2 * dim * (int64_t)sizeof(float);
 }
 
-template <typename XT, typename BT, int EPU, int V, bool GATE>
+template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_bwd_v(NormArgs& a, int* grid, cudaStream_t s) {
-  int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>);
-  const int threads = a.rpb * a.tpr, cols = a.rpb > 1 ? 2 * a.dim * (int)sizeof(float) : 0;
+  const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : kNormCtasPerSm;
+  int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>, per);
+  const int cols = a.rpb > 1 ? 2 * a.dim * (int)sizeof(float) : 0;
   if (smem < cols) smem = cols;
-  const auto kern = k_gated_norm_bwd<XT, BT, EPU, V, GATE>;
+  const auto kern = k_gated_norm_bwd<XT, BT, EPU, V, GATE, WARP>;
   const cudaError_t e = norm_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  *grid = (int)norm_bwd_grid(a.n, a.rpb, norm_ctas(V * EPU > 8 ? kNormWide / threads : kNormCtasPerSm, smem));
+  *grid = (int)norm_bwd_grid(a.n, a.rpb, (int64_t)device_sms() * norm_fit(per, smem));
   kern<<<*grid, threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-// The kernel of a call by packs per thread (1, 2, 4, 8 or 16: at most 16 elements).
+// The kernel of a call by packs per thread (1, 2, 4, 8 or 16: at most 16 elements), gate and
+// threads per row.  Rows of 16 elements a thread always take whole warps.
 template <typename XT, typename BT, int EPU, bool BWD, int V = 1>
 static cudaError_t norm_t(NormArgs& a, int* grid, cudaStream_t s) {
   if constexpr (V == 1) norm_shape(a, EPU);
   if constexpr (V * EPU < 16)
     if ((a.packs + a.tpr - 1) / a.tpr > V) return norm_t<XT, BT, EPU, BWD, 2 * V>(a, grid, s);
+  const auto run = [&](auto gate, auto warp) {
+    constexpr bool G = decltype(gate)::value, W = decltype(warp)::value;
+    if constexpr (BWD) return norm_bwd_v<XT, BT, EPU, V, G, W>(a, grid, s);
+    else return norm_fwd_v<XT, BT, EPU, V, G, W>(a, s);
+  };
   const bool gate = a.gate && !a.gate_row;
-  if constexpr (BWD)
-    return gate ? norm_bwd_v<XT, BT, EPU, V, true>(a, grid, s) : norm_bwd_v<XT, BT, EPU, V, false>(a, grid, s);
-  else
-    return gate ? norm_fwd_v<XT, BT, EPU, V, true>(a, s) : norm_fwd_v<XT, BT, EPU, V, false>(a, s);
+  if constexpr (V * EPU <= 8)
+    if (a.tpr < 32 || V == 1) return gate ? run(std::true_type{}, std::false_type{}) : run(std::false_type{}, std::false_type{});
+  if constexpr (V > 1) return gate ? run(std::true_type{}, std::true_type{}) : run(std::false_type{}, std::true_type{});
+  return cudaErrorInvalidValue;  // not reached: one pack a thread was taken above
 }
 
 template <bool BWD>
