@@ -385,8 +385,10 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
  * a buffer of the same type that overlaps no other.  numel may be 0, and count too (norm 0).
  * EMB_EINVAL: count < 0 or above EMB_CLIP_MAX_TENSORS, a negative numel, a bad dtype, a NULL or
  * (for its type) misaligned buffer, max_norm negative or NaN (infinity: only the norm and
- * copies), a short or misaligned workspace. */
+ * copies), a short or misaligned workspace.  Lists of up to 256 tensors with
+ * EMB_CLIP_ONE_LAUNCH elements in all need none (NULL, 0 bytes). */
 #define EMB_CLIP_MAX_TENSORS 65536
+#define EMB_CLIP_ONE_LAUNCH 1048576
 typedef struct emb_tensor {
   const void* d_src;
   void* d_out;

@@ -233,6 +233,7 @@ def _stream(stream) -> Optional[int]:
 # checked by a few attribute reads, structures are packed in one step, and the reason of a
 # refusal is looked for only once there is one.
 EXPERT_MAX, EXPERT_MAX_K, EXPERT_MAX_DIM, NORM_MAX_DIM = 1024, 16, 65536, 8192
+CLIP_ONE_LAUNCH = 1048576
 _NORM_PACK = struct.Struct("@q4if4x6Q3q2Q2q5Q3Q5q")  # struct emb_norm
 assert _NORM_PACK.size == ctypes.sizeof(EmbNorm)
 
@@ -496,14 +497,15 @@ def clip_grads(grads, max_norm: float, norm, out=None, workspace=None, stream=No
     Asynchronous."""
     if not _TORCH:
         _load_torch()
-    codes, flat = _ROW_CODES, []
+    codes, flat, total = _ROW_CODES, [], 0
     if out is None:
         for g in grads:
             code = codes.get(g.dtype)
             if code is None or not g.is_cuda or not g.is_contiguous():
                 raise ValueError("grads: expected contiguous CUDA tensors, float32 or bfloat16")
-            p = g.data_ptr()
-            flat += (p, p, g.numel(), code)
+            p, m = g.data_ptr(), g.numel()
+            flat += (p, p, m, code)
+            total += m
     else:
         grads, out = list(grads), list(out)
         if len(out) != len(grads):
@@ -516,9 +518,12 @@ def clip_grads(grads, max_norm: float, norm, out=None, workspace=None, stream=No
             if o.dtype is not t or o.numel() != m or not o.is_cuda or not o.is_contiguous():
                 raise ValueError("out: expected contiguous CUDA tensors of the gradients' types and sizes")
             flat += (g.data_ptr(), o.data_ptr(), m, code)
+            total += m
     count = len(flat) // 4
     np_ = _flat(norm, "f32", 1, "norm")
-    ws, wp, have = _workspace(_lib.emb_clip_grads_workspace(count), workspace, stream, norm)
+    # short lists take one launch and no workspace
+    need = 0 if total <= CLIP_ONE_LAUNCH and count <= 256 else _lib.emb_clip_grads_workspace(count)
+    ws, wp, have = _workspace(need, workspace, stream, norm)
     st = _lib.emb_clip_grads(struct.pack("@" + "QQqi4x" * count, *flat), count, max_norm, np_, wp, have,
                              _on(stream, norm))
     if st:

@@ -1252,14 +1252,17 @@ emb_status emb_clip_grads(const emb_tensor* h_list, int64_t count, float max_nor
                           void* d_ws, int64_t ws_bytes, void* stream) {
   const int64_t need = emb_clip_grads_workspace(count);
   if (need < 0 || (count > 0 && !h_list) || !d_norm || !(max_norm >= 0.f)) return EMB_EINVAL;
+  int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
     const emb_tensor& t = h_list[i];
-    if (t.numel < 0 || (t.dtype != EMB_F32 && t.dtype != EMB_BF16)) return EMB_EINVAL;
+    if (t.numel < 0 || t.numel > INT64_MAX / 16 - total || (t.dtype != EMB_F32 && t.dtype != EMB_BF16)) return EMB_EINVAL;
     const int elem = t.dtype == EMB_BF16 ? 2 : 4;
     if (t.numel > 0 && (!t.d_src || !t.d_out)) return EMB_EINVAL;
     if (!aligned_to(t.d_src, elem) || !aligned_to(t.d_out, elem)) return EMB_EINVAL;
+    total += t.numel;
   }
-  if (!ws_ok(d_ws, ws_bytes, need)) return EMB_EINVAL;
+  const bool none = !d_ws && ws_bytes == 0 && clip_in_one_launch(count, total);
+  if (!none && !ws_ok(d_ws, ws_bytes, need)) return EMB_EINVAL;
   return check_launch(launch_clip_grads(h_list, count, max_norm, d_norm, d_ws,
                                         reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -19,6 +19,7 @@ constexpr int kClipShort = 32, kClipLong = 256;  // tensors of one launch: lists
 constexpr int kClipCtasPerSm = 8;                // CTAs of the norm's launch, at most, per SM
 constexpr int kClipScaleCtasPerSm = 4;           // of the scaling launch (64 registers a thread)
 constexpr int kClipTile = 16384, kClipTileMin = 2048;  // elements
+constexpr int kClusterCtas = 16, kClusterThreads = 1024;
 
 template <int N>
 struct ClipList {
@@ -61,17 +62,17 @@ __device__ __forceinline__ int clip_tensor(const ClipList<N>& l, int64_t tile) {
   return lo;
 }
 
-template <typename T, int EPU>
+template <int THREADS, typename T, int EPU>
 __device__ __forceinline__ double tile_squares(const T* p, int64_t n) {
   constexpr int U = EPU == 8 ? 2 : 4;  // 16 elements a group (4 where they come one by one)
   double acc = 0.0;
   const int64_t packs = n / EPU;
-  for (int64_t c0 = threadIdx.x; c0 < packs; c0 += kClipThreads * U) {
+  for (int64_t c0 = threadIdx.x; c0 < packs; c0 += THREADS * U) {
     Pack<T, EPU> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       v[u].zero();
-      if (c0 + u * kClipThreads < packs) v[u].load(p + (c0 + u * kClipThreads) * EPU);
+      if (c0 + u * THREADS < packs) v[u].load(p + (c0 + u * THREADS) * EPU);
     }
     float f[U * EPU];
 #pragma unroll
@@ -84,7 +85,7 @@ __device__ __forceinline__ double tile_squares(const T* p, int64_t n) {
     acc += square_sum(f);
   }
   if (EPU > 1)
-    for (int64_t i = packs * EPU + threadIdx.x; i < n; i += kClipThreads) {
+    for (int64_t i = packs * EPU + threadIdx.x; i < n; i += THREADS) {
       Pack<T, 1> v;
       v.load(p + i);
       float f[1];
@@ -94,63 +95,73 @@ __device__ __forceinline__ double tile_squares(const T* p, int64_t n) {
   return acc;
 }
 
-// Sum over the CTA, the same in every thread.
+// Sum over the CTA, in thread 0.  fp64 additions are scarce (two lanes a cycle and SM), so one
+// warp adds the others' values up and reduces once: 12 warp additions for 256 threads, where
+// a shuffle tree in every warp would take over 100.
+template <int THREADS>
 __device__ __forceinline__ double cta_sum(double v) {
-  __shared__ double sh[kClipThreads / 32];
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __shared__ double sh[THREADS];
+  sh[threadIdx.x] = v;
   __syncthreads();
-  v = 0.0;
+  if (threadIdx.x < 32) {
+#pragma unroll 8
+    for (int w = 1; w < THREADS / 32; ++w) v += sh[w * 32 + threadIdx.x];
 #pragma unroll
-  for (int w = 0; w < kClipThreads / 32; ++w) v += sh[w];
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_down_sync(0xFFFFFFFFu, v, o);
+  }
   return v;
+}
+
+// Sum of squares of tiles t0, t0 + step, ... over this thread.
+template <int THREADS, int N>
+__device__ __forceinline__ double share_squares(const ClipList<N>& l, int64_t t0, int64_t step) {
+  double acc = 0.0;
+  const int64_t tiles = l.first[l.count];
+  for (int64_t t = t0; t < tiles; t += step) {
+    const int i = clip_tensor(l, t);
+    const int64_t at = (t - l.first[i]) * l.tile;
+    const int64_t n = l.numel[i] - at < l.tile ? l.numel[i] - at : l.tile;
+    if (l.bf16[i]) {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(l.src[i]) + at;
+      acc += l.vec[i] ? tile_squares<THREADS, __nv_bfloat16, 8>(p, n) : tile_squares<THREADS, __nv_bfloat16, 1>(p, n);
+    } else {
+      const float* p = static_cast<const float*>(l.src[i]) + at;
+      acc += l.vec[i] ? tile_squares<THREADS, float, 4>(p, n) : tile_squares<THREADS, float, 1>(p, n);
+    }
+  }
+  return acc;
 }
 
 template <int N>
 __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
     k_clip_norm(const __grid_constant__ ClipList<N> l, double* part) {
   asm volatile("griddepcontrol.launch_dependents;");
-  double acc = 0.0;
-  const int64_t tiles = l.first[l.count];
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int i = clip_tensor(l, t);
-    const int64_t at = (t - l.first[i]) * l.tile;
-    const int64_t n = l.numel[i] - at < l.tile ? l.numel[i] - at : l.tile;
-    if (l.bf16[i]) {
-      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(l.src[i]) + at;
-      acc += l.vec[i] ? tile_squares<__nv_bfloat16, 8>(p, n) : tile_squares<__nv_bfloat16, 1>(p, n);
-    } else {
-      const float* p = static_cast<const float*>(l.src[i]) + at;
-      acc += l.vec[i] ? tile_squares<float, 4>(p, n) : tile_squares<float, 1>(p, n);
-    }
-  }
-  acc = cta_sum(acc);
+  const double acc = cta_sum<kClipThreads>(share_squares<kClipThreads>(l, blockIdx.x, gridDim.x));
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
 
-template <typename T, int EPU>
+template <int THREADS, typename T, int EPU>
 __device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, float c) {
   constexpr int U = 4;
   const int64_t packs = n / EPU;
-  for (int64_t c0 = threadIdx.x; c0 < packs; c0 += kClipThreads * U) {
+  for (int64_t c0 = threadIdx.x; c0 < packs; c0 += THREADS * U) {
     Pack<T, EPU> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (c0 + u * kClipThreads < packs) v[u].load(p + (c0 + u * kClipThreads) * EPU);
+      if (c0 + u * THREADS < packs) v[u].load(p + (c0 + u * THREADS) * EPU);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (c0 + u * kClipThreads < packs) {
+      if (c0 + u * THREADS < packs) {
         float f[EPU];
         v[u].get(f);
 #pragma unroll
         for (int m = 0; m < EPU; ++m) f[m] *= c;
         v[u].set(f);
-        v[u].store(o + (c0 + u * kClipThreads) * EPU);
+        v[u].store(o + (c0 + u * THREADS) * EPU);
       }
   }
   if (EPU > 1)
-    for (int64_t i = packs * EPU + threadIdx.x; i < n; i += kClipThreads) {
+    for (int64_t i = packs * EPU + threadIdx.x; i < n; i += THREADS) {
       Pack<T, 1> v;
       v.load(p + i);
       float f[1];
@@ -161,44 +172,114 @@ __device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, float c)
     }
 }
 
-// Every CTA adds up all `parts` itself (a few KB from L2).  The tiles are taken from the last to
-// the first: the norm's pass left the last ones in L2.
-template <int N>
-__global__ void __launch_bounds__(kClipThreads, kClipScaleCtasPerSm)
-    k_clip_scale(const __grid_constant__ ClipList<N> l, const double* part, int parts, float max_norm,
-                 float* norm_out, int inplace) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  double acc = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kClipThreads) acc += __ldcg(part + i);
-  const double norm = sqrt(cta_sum(acc));
-  const float nf = (float)norm;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = nf;
-  // a norm that is infinite or NaN scales nothing: the caller sees it and drops the step
-  const bool clip = norm > (double)max_norm && isfinite(nf);
-  if (!clip && inplace) return;
-  const float c = clip ? (float)((double)max_norm / norm) : 1.f;
-  const int64_t tiles = l.first[l.count];
-  for (int64_t t = tiles - 1 - blockIdx.x; t >= 0; t -= gridDim.x) {
+// Tiles t0, t0 - step, ... scaled by c.
+template <int THREADS, int N>
+__device__ __forceinline__ void share_scale(const ClipList<N>& l, int64_t t0, int64_t step, float c) {
+  for (int64_t t = t0; t >= 0; t -= step) {
     const int i = clip_tensor(l, t);
     const int64_t at = (t - l.first[i]) * l.tile;
     const int64_t n = l.numel[i] - at < l.tile ? l.numel[i] - at : l.tile;
     if (l.bf16[i]) {
       const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(l.src[i]) + at;
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(l.dst[i]) + at;
-      if (l.vec[i]) tile_scale<__nv_bfloat16, 8>(p, o, n, c);
-      else tile_scale<__nv_bfloat16, 1>(p, o, n, c);
+      if (l.vec[i]) tile_scale<THREADS, __nv_bfloat16, 8>(p, o, n, c);
+      else tile_scale<THREADS, __nv_bfloat16, 1>(p, o, n, c);
     } else {
       const float* p = static_cast<const float*>(l.src[i]) + at;
       float* o = static_cast<float*>(l.dst[i]) + at;
-      if (l.vec[i]) tile_scale<float, 4>(p, o, n, c);
-      else tile_scale<float, 1>(p, o, n, c);
+      if (l.vec[i]) tile_scale<THREADS, float, 4>(p, o, n, c);
+      else tile_scale<THREADS, float, 1>(p, o, n, c);
     }
   }
+}
+
+// The factor of a sum of squares (negative: nothing is to be scaled).  A norm that is infinite
+// or NaN scales nothing: the caller sees it and drops the step.  One thread's work (fp64).
+__device__ __forceinline__ float clip_factor(double squares, float max_norm, float& norm) {
+  const double n = sqrt(squares);
+  norm = (float)n;
+  return n > (double)max_norm && isfinite(norm) ? (float)((double)max_norm / n) : -1.f;
+}
+
+// Every CTA adds up all `parts` itself (a few KB from L2).  The tiles are taken from the last to
+// the first: the norm's pass left the last ones in L2.
+template <int N>
+__global__ void __launch_bounds__(kClipThreads, kClipScaleCtasPerSm)
+    k_clip_scale(const __grid_constant__ ClipList<N> l, const double* part, int parts, float max_norm,
+                 float* norm_out, int inplace) {
+  __shared__ float factor;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  double acc = 0.0;
+#pragma unroll 5
+  for (int i = threadIdx.x; i < parts; i += kClipThreads) acc += __ldcg(part + i);
+  acc = cta_sum<kClipThreads>(acc);
+  if (threadIdx.x == 0) {
+    float norm;
+    factor = clip_factor(acc, max_norm, norm);
+    if (blockIdx.x == 0) *norm_out = norm;
+  }
+  __syncthreads();
+  const float c = factor;
+  if (c < 0.f && inplace) return;
+  share_scale<kClipThreads>(l, l.first[l.count] - 1 - blockIdx.x, gridDim.x, c < 0.f ? 1.f : c);
+}
+
+// Short lists in one launch: a cluster of CTAs exchanges its parts through shared memory (the
+// second read then comes from L1 or L2).  Up to EMB_CLIP_ONE_LAUNCH elements: above, the
+// cluster's 16 SMs are slower than all of them in two launches.
+template <int N>
+__global__ void __launch_bounds__(kClusterThreads)
+    k_clip_cluster(const __grid_constant__ ClipList<N> l, float max_norm, float* norm_out, int inplace) {
+  __shared__ double part;
+  __shared__ float factor;
+  const double mine = cta_sum<kClusterThreads>(share_squares<kClusterThreads>(l, blockIdx.x, gridDim.x));
+  if (threadIdx.x == 0) part = mine;
+  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+  if (threadIdx.x < 32) {  // lane r: the part of CTA r
+    double v = 0.0;
+    if (threadIdx.x < gridDim.x) {
+      uint32_t there;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                   : "=r"(there) : "r"((uint32_t)__cvta_generic_to_shared(&part)), "r"(threadIdx.x));
+      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(there) : "memory");
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_down_sync(0xFFFFFFFFu, v, o);
+    if (threadIdx.x == 0) {
+      float norm;
+      factor = clip_factor(v, max_norm, norm);
+      if (blockIdx.x == 0) *norm_out = norm;
+    }
+  }
+  // every part has been read before any CTA may leave
+  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+  const float c = factor;
+  if (c < 0.f && inplace) return;
+  share_scale<kClusterThreads>(l, l.first[l.count] - 1 - blockIdx.x, gridDim.x, c < 0.f ? 1.f : c);
 }
 
 int64_t clip_grads_workspace(int64_t count) {
   const int64_t launches = count > 0 ? (count + kClipLong - 1) / kClipLong : 1;
   return launches * device_sms() * kClipCtasPerSm * (int64_t)sizeof(double);
+}
+
+bool clip_in_one_launch(int64_t count, int64_t total) {
+  return count <= kClipLong && total <= EMB_CLIP_ONE_LAUNCH;
+}
+
+template <int N>
+static cudaError_t clip_cluster(const ClipList<N>& l, float max_norm, float* norm, int inplace,
+                                cudaStream_t s) {
+  const auto kern = k_clip_cluster<N>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kClusterCtas, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kClusterCtas), cfg.blockDim = dim3(kClusterThreads);
+  cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, l, max_norm, norm, inplace);
 }
 
 template <int N>
@@ -229,6 +310,13 @@ static cudaError_t clip_lists(const emb_tensor* list, int64_t count, float max_n
     const int64_t tiles = l.first[l.count];
     return (int)(tiles < 1 ? 1 : tiles < cap ? tiles : cap);
   };
+  if (clip_in_one_launch(count, total)) {
+    // two tiles a CTA: few enough steps, and tensors of any size share out
+    l.tile = (int)((total / (2 * kClusterCtas) + 2047) / 2048 * 2048);
+    if (l.tile < kClipTileMin) l.tile = kClipTileMin;
+    fill(0);
+    return clip_cluster(l, max_norm, norm, inplace, s);
+  }
   int parts = 0, grid = 1;
   int64_t i0 = 0;
   cudaError_t e = cudaSuccess;
