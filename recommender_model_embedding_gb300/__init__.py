@@ -1,15 +1,15 @@
 """GB300-native sparse embedding layer for DLRM-style recommenders.
 
-A thin ctypes binding over libemb.so, the CUDA library declared in include/emb.h.  Every
-method marshals its arguments (torch tensors -> device pointers, the current CUDA stream)
-and calls the C entry point of the same name; all arithmetic runs in the library's
-kernels.  There is no CPU path: if libemb.so is missing this package fails to import.
+A thin binding over libemb.so, the CUDA library declared in include/emb.h: ctypes, and a small
+compiled module for the expert tower's calls (csrc/py_tower.c).  Every method marshals its
+arguments (torch tensors -> device pointers, the current CUDA stream) and calls the C entry
+point of the same name; all arithmetic runs in the library's kernels.  There is no CPU path:
+if libemb.so is missing this package fails to import.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +22,12 @@ if not os.path.exists(LIB_PATH):
         "python recommender_model_embedding_gb300/build.py)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+try:
+    from . import _tower  # noqa: E402  (loads libemb.so too: the same library)
+except ImportError as _e:
+    raise ImportError(f"{_e}: build the library first (python "
+                      "recommender_model_embedding_gb300/build.py)") from _e
 
 EMB_OK, EMB_EINVAL, EMB_ENOMEM, EMB_ESTATE, EMB_ECUDA = 0, 1, 2, 3, 4
 FLAG_ID_RANGE, FLAG_BAD_KEY, FLAG_TABLE_FULL, FLAG_BAD_OFFSETS = 0x1, 0x2, 0x4, 0x8
@@ -100,11 +106,11 @@ _SIGS = {
     "emb_expert_combine": ([_P, _I64, _P, _P, _I64, _I32, _I32, _I32, _P, _I64, _P], ctypes.c_int),
     "emb_expert_combine_backward": ([_P, _I64, _P, _I64, _P, _P, _I64, _I32, _I32, _I32, _P, _I64,
                                      _P, _P], ctypes.c_int),
-    "emb_gated_norm": ([_P, _P], ctypes.c_int),
+    "emb_gated_norm": ([ctypes.POINTER(EmbNorm), _P], ctypes.c_int),
     "emb_gated_norm_backward_workspace": ([_I64, _I32], _I64),
-    "emb_gated_norm_backward": ([_P, _P, _I64, _P], ctypes.c_int),
+    "emb_gated_norm_backward": ([ctypes.POINTER(EmbNorm), _P, _I64, _P], ctypes.c_int),
     "emb_clip_grads_workspace": ([_I64], _I64),
-    "emb_clip_grads": ([_P, _I64, ctypes.c_float, _P, _P, _I64, _P], ctypes.c_int),
+    "emb_clip_grads": ([ctypes.POINTER(EmbTensor), _I64, ctypes.c_float, _P, _P, _I64, _P], ctypes.c_int),
     "emb_unique_keys_noalloc": ([_P, _I64, _P, _P, _P, _P], ctypes.c_int),
 }
 NOALLOC_MAX_KEYS = 524288
@@ -228,92 +234,24 @@ def _stream(stream) -> Optional[int]:
     return s.cuda_stream
 
 
-# ---- expert tower (context-free) ----
-# These calls are short enough on the device for their own cost on the host to count: tensors are
-# checked by a few attribute reads, structures are packed in one step, and the reason of a
-# refusal is looked for only once there is one.
+# ---- expert tower (context-free; arguments are checked and passed on by the _tower module) ----
 EXPERT_MAX, EXPERT_MAX_K, EXPERT_MAX_DIM, NORM_MAX_DIM = 1024, 16, 65536, 8192
 CLIP_ONE_LAUNCH = 1048576
-_NORM_PACK = struct.Struct("@q4if4x6Q3q2Q2q5Q3Q5q")  # struct emb_norm
-assert _NORM_PACK.size == ctypes.sizeof(EmbNorm)
-
-_TORCH = {}  # "f32", "bf16", "i32", "i64" -> torch dtype, and "raw_stream"; filled on first use
-_ROW_CODES = {}  # torch dtype of a matrix -> EMB_F32 or EMB_BF16
 
 
-def _load_torch():
+def _current_stream(device: int) -> int:
     import torch
-    _ROW_CODES[torch.float32], _ROW_CODES[torch.bfloat16] = F32, BF16
-    _TORCH.update(f32=torch.float32, bf16=torch.bfloat16, i32=torch.int32, i64=torch.int64,
-                  raw_stream=getattr(torch._C, "_cuda_getCurrentRawStream", None))
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-def _row_code(t, name: str) -> int:
-    if not _ROW_CODES:
-        _load_torch()
-    code = _ROW_CODES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
-    return code
-
-
-def _rows(t, dtype, n: int, dim: int, name: str):
-    """(pointer, row step) of a CUDA matrix [n, dim] of the given torch dtype; its rows may lie
-    any number of elements apart."""
-    if t.dtype is dtype and t.shape == (n, dim) and t.is_cuda:
-        step, inner = t.stride()
-        if inner == 1 or dim <= 1:
-            return t.data_ptr(), step if n > 1 else dim
-        raise ValueError(f"{name}: the elements of a row must be adjacent")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA matrix")
-    raise ValueError(f"{name}: expected {dtype} {(n, dim)}, got {t.dtype} {tuple(t.shape)}")
-
-
-def _flat(t, kind: str, n: int, name: str) -> int:
-    """_dptr of a tensor that has to be there."""
-    if t is not None and t.dtype is _TORCH[kind] and t.numel() >= n and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    if t is None:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    return _dptr(t, kind, n, name)
-
-
-def _vec(t, dim: int, name: str) -> int:
-    """Address of an optional float32 vector of dim elements (0: none)."""
-    if t is None:
-        return 0
-    if t.numel() != dim:
-        raise ValueError(f"{name}: {t.numel()} elements, expected {dim}")
-    return _flat(t, "f32", dim, name)
-
-
-def _on(stream, like) -> Optional[int]:
-    """The call's stream: the given one, or the current one of the tensor's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    raw = _TORCH["raw_stream"]
-    return raw(like.get_device()) if raw is not None else _stream(None)
-
-
-def _workspace(need: int, workspace, stream, like):
-    """(tensor, address, bytes) of the caller's workspace (any contiguous CUDA tensor of enough
-    bytes), or of one from torch's allocator, taken on the call's stream so that its memory is
-    reused in that stream's order.  The tensor has to live until the call has been made."""
-    if need <= 0:
-        return None, None, 0
-    if workspace is None:
-        import torch
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-        return workspace, workspace.data_ptr(), need
-    have = workspace.numel() * workspace.element_size()
-    if have < need:
-        raise ValueError(f"workspace: {have} bytes, at least {need} needed")
-    return workspace, _dptr(workspace, name="workspace"), have
+def _new_workspace(need: int, stream, like):
+    """Workspace from torch's allocator, taken on the call's stream so that its memory is reused
+    in that stream's order."""
+    import torch
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
 
 
 def expert_sort_workspace(n: int, k: int, num_experts: int) -> int:
@@ -326,92 +264,30 @@ def expert_sort(ids, num_experts: int, order, pos, offsets, workspace=None, stre
     [0, num_experts): dropped) stably by expert into `order` (int32 [n*k], slot at each place),
     `pos` (int32 [n*k], place of each slot, -1 - place when dropped) and `offsets` (int32
     [num_experts + 1], first place of each expert; the last: kept slots).  Asynchronous."""
-    if not _TORCH:
-        _load_torch()
-    if ids.dim() != 2:
-        raise ValueError("ids: expected a matrix [n, k]")
-    n, k = ids.shape
-    S = n * k
-    ip, op, pp = _flat(ids, "i64", S, "ids"), _flat(order, "i32", S, "order"), _flat(pos, "i32", S, "pos")
-    fp = _flat(offsets, "i32", num_experts + 1, "offsets")
-    ws, wp, have = _workspace(_lib.emb_expert_sort_workspace(n, k, num_experts), workspace, stream, ids)
-    st = _lib.emb_expert_sort(ip, n, k, num_experts, op, pp, fp, wp, have, _on(stream, ids))
-    if st:
-        _check("emb_expert_sort", st)
-
-
-def _slots(pos, n: int) -> int:
-    """Experts of a row: k of a pos with n * k places."""
-    S = pos.numel()
-    if n == 0 and S == 0:
-        return 1
-    if n == 0 or S % n or not S:
-        raise ValueError(f"pos: {S} elements, expected a multiple of {n} rows")
-    return S // n
+    _tower.sort(ids, num_experts, order, pos, offsets, workspace, stream)
 
 
 def expert_dispatch(x, pos, xs, stream=None):
     """xs[pos[i, j]] = x[i] for the kept slots, zero rows at the dropped ones' places.  x [n, d]
     and xs [n*k, d] float32 or bfloat16, rows any step apart; pos of expert_sort."""
-    code, t, (n, d) = _row_code(x, "x"), x.dtype, x.shape
-    k = _slots(pos, n)
-    xp, xl = _rows(x, t, n, d, "x")
-    op, ol = _rows(xs, t, n * k, d, "xs")
-    st = _lib.emb_expert_dispatch(xp, xl, _flat(pos, "i32", n * k, "pos"), n, k, d, code, op, ol,
-                                  _on(stream, x))
-    if st:
-        _check("emb_expert_dispatch", st)
+    _tower.dispatch(x, pos, xs, stream)
 
 
 def expert_dispatch_backward(dxs, pos, dx, stream=None):
     """dx[i] = sum of dxs over row i's kept places (dxs [n*k, d], dx [n, d])."""
-    code, t, (n, d) = _row_code(dx, "dx"), dx.dtype, dx.shape
-    k = _slots(pos, n)
-    ip, il = _rows(dxs, t, n * k, d, "dxs")
-    op, ol = _rows(dx, t, n, d, "dx")
-    st = _lib.emb_expert_dispatch_backward(ip, il, _flat(pos, "i32", n * k, "pos"), n, k, d, code, op,
-                                           ol, _on(stream, dx))
-    if st:
-        _check("emb_expert_dispatch_backward", st)
+    _tower.dispatch_backward(dxs, pos, dx, stream)
 
 
 def expert_combine(ys, pos, w, out, stream=None):
     """out[i] = sum over row i's kept slots of w[i, j] * ys[place] (ys [n*k, d], w float32
     [n, k], out [n, d])."""
-    code, t, (n, d) = _row_code(out, "out"), out.dtype, out.shape
-    k = _slots(pos, n)
-    ip, il = _rows(ys, t, n * k, d, "ys")
-    op, ol = _rows(out, t, n, d, "out")
-    st = _lib.emb_expert_combine(ip, il, _flat(pos, "i32", n * k, "pos"), _flat(w, "f32", n * k, "w"), n,
-                                 k, d, code, op, ol, _on(stream, out))
-    if st:
-        _check("emb_expert_combine", st)
+    _tower.combine(ys, pos, w, out, stream)
 
 
 def expert_combine_backward(dout, ys, pos, w, dys, dw, stream=None):
     """Gradients of expert_combine: dys [n*k, d] (zero rows at dropped places) and dw float32
     [n, k] (0 when dropped)."""
-    code, t, (n, d) = _row_code(dout, "dout"), dout.dtype, dout.shape
-    k = _slots(pos, n)
-    gp, gl = _rows(dout, t, n, d, "dout")
-    yp, yl = _rows(ys, t, n * k, d, "ys")
-    op, ol = _rows(dys, t, n * k, d, "dys")
-    st = _lib.emb_expert_combine_backward(gp, gl, yp, yl, _flat(pos, "i32", n * k, "pos"),
-                                          _flat(w, "f32", n * k, "w"), n, k, d, code, op, ol,
-                                          _flat(dw, "f32", n * k, "dw"), _on(stream, dout))
-    if st:
-        _check("emb_expert_combine_backward", st)
-
-
-def _gate(gate, dtype, n: int, d: int):
-    """(address, row step, columns) of an optional gate."""
-    if gate is None:
-        return 0, 0, 0
-    cols = gate.shape[-1]
-    if cols != 1 and cols != d:
-        raise ValueError(f"gate: {cols} columns, expected 1 or {d}")
-    p, step = _rows(gate, dtype, n, cols, "gate")
-    return p, step, cols
+    _tower.combine_backward(dout, ys, pos, w, dys, dw, stream)
 
 
 def gated_norm(x, y, x_out, h, gate=None, w_post=None, res_scale=None, w_pre=None,
@@ -421,26 +297,7 @@ def gated_norm(x, y, x_out, h, gate=None, w_post=None, res_scale=None, w_pre=Non
     x, x_out [n, d] float32 or bfloat16; y, h, gate ([n, d], or [n, 1]: one gate a row) of one
     type, bfloat16 or as x; vectors float32 [d], None counts as ones.  y None: h from x alone;
     h None: only x_out.  x_out may be x.  Asynchronous."""
-    code, xt, (n, d) = _row_code(x, "x"), x.dtype, x.shape
-    bt, bcode = xt, code
-    yp = yl = op = ol = hp = hl = 0
-    if y is not None:
-        bt, bcode = y.dtype, _row_code(y, "y")
-        yp, yl = _rows(y, bt, n, d, "y")
-    elif h is not None:
-        bt, bcode = h.dtype, _row_code(h, "h")
-    xp, xl = _rows(x, xt, n, d, "x")
-    if x_out is not None:
-        op, ol = _rows(x_out, xt, n, d, "x_out")
-    if h is not None:
-        hp, hl = _rows(h, bt, n, d, "h")
-    gp, gl, cols = _gate(gate, bt, n, d)
-    st = _lib.emb_gated_norm(
-        _NORM_PACK.pack(n, d, code, bcode, cols, eps, yp, gp, _vec(w_post, d, "w_post"),
-                        _vec(res_scale, d, "res_scale"), _vec(w_pre, d, "w_pre"), op, yl, gl, ol, xp,
-                        hp, xl, hl, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0), _on(stream, x))
-    if st:
-        _check("emb_gated_norm", st)
+    _tower.norm(x, y, x_out, h, gate, w_post, res_scale, w_pre, eps, stream)
 
 
 def gated_norm_backward_workspace(n: int, d: int) -> int:
@@ -454,35 +311,8 @@ def gated_norm_backward(dx_out, dh, x_out, y, dx, dy, gate=None, w_post=None, re
     """Gradients of gated_norm from dx_out (None: zero) and dh (None: no h), with x_out, y, gate
     and the vectors of the forward: dx, dy, dgate and the vectors' (float32 [d], overwritten).
     Outputs may be None; dx may be dx_out.  Asynchronous."""
-    code, xt, (n, d) = _row_code(x_out, "x_out"), x_out.dtype, x_out.shape
-    bt, bcode = xt, code
-    yp = yl = tp = tl = hp = hl = dp = dl = ep = el = qp = ql = 0
-    if y is not None:
-        bt, bcode = y.dtype, _row_code(y, "y")
-        yp, yl = _rows(y, bt, n, d, "y")
-    elif dh is not None:
-        bt, bcode = dh.dtype, _row_code(dh, "dh")
-    xp, xl = _rows(x_out, xt, n, d, "x_out")
-    if dx_out is not None:
-        tp, tl = _rows(dx_out, xt, n, d, "dx_out")
-    if dh is not None:
-        hp, hl = _rows(dh, bt, n, d, "dh")
-    if dx is not None:
-        dp, dl = _rows(dx, xt, n, d, "dx")
-    if dy is not None:
-        ep, el = _rows(dy, bt, n, d, "dy")
-    gp, gl, cols = _gate(gate, bt, n, d)
-    if dgate is not None:
-        qp, ql = _rows(dgate, bt, n, cols or d, "dgate")
-    ws, wp, have = _workspace(_lib.emb_gated_norm_backward_workspace(n, d), workspace, stream, x_out)
-    st = _lib.emb_gated_norm_backward(
-        _NORM_PACK.pack(n, d, code, bcode, cols, eps, yp, gp, _vec(w_post, d, "w_post"),
-                        _vec(res_scale, d, "res_scale"), _vec(w_pre, d, "w_pre"), xp, yl, gl, xl, 0,
-                        0, 0, 0, tp, hp, dp, ep, qp, _vec(dw_post, d, "dw_post"),
-                        _vec(dres_scale, d, "dres_scale"), _vec(dw_pre, d, "dw_pre"), tl, hl, dl, el,
-                        ql), wp, have, _on(stream, x_out))
-    if st:
-        _check("emb_gated_norm_backward", st)
+    _tower.norm_backward(dx_out, dh, x_out, y, dx, dy, gate, w_post, res_scale, w_pre, dgate, dw_post,
+                         dres_scale, dw_pre, eps, workspace, stream)
 
 
 def clip_grads_workspace(count: int) -> int:
@@ -495,39 +325,7 @@ def clip_grads(grads, max_norm: float, norm, out=None, workspace=None, stream=No
     min(1, max_norm / norm), in place or into `out` (contiguous CUDA tensors, float32 or
     bfloat16, of the gradients' types and sizes).  An infinite or NaN norm clips nothing.
     Asynchronous."""
-    if not _TORCH:
-        _load_torch()
-    codes, flat, total = _ROW_CODES, [], 0
-    if out is None:
-        for g in grads:
-            code = codes.get(g.dtype)
-            if code is None or not g.is_cuda or not g.is_contiguous():
-                raise ValueError("grads: expected contiguous CUDA tensors, float32 or bfloat16")
-            p, m = g.data_ptr(), g.numel()
-            flat += (p, p, m, code)
-            total += m
-    else:
-        grads, out = list(grads), list(out)
-        if len(out) != len(grads):
-            raise ValueError(f"out: {len(out)} tensors for {len(grads)} gradients")
-        for g, o in zip(grads, out):
-            t, m = g.dtype, g.numel()
-            code = codes.get(t)
-            if code is None or not g.is_cuda or not g.is_contiguous():
-                raise ValueError("grads: expected contiguous CUDA tensors, float32 or bfloat16")
-            if o.dtype is not t or o.numel() != m or not o.is_cuda or not o.is_contiguous():
-                raise ValueError("out: expected contiguous CUDA tensors of the gradients' types and sizes")
-            flat += (g.data_ptr(), o.data_ptr(), m, code)
-            total += m
-    count = len(flat) // 4
-    np_ = _flat(norm, "f32", 1, "norm")
-    # short lists take one launch and no workspace
-    need = 0 if total <= CLIP_ONE_LAUNCH and count <= 256 else _lib.emb_clip_grads_workspace(count)
-    ws, wp, have = _workspace(need, workspace, stream, norm)
-    st = _lib.emb_clip_grads(struct.pack("@" + "QQqi4x" * count, *flat), count, max_norm, np_, wp, have,
-                             _on(stream, norm))
-    if st:
-        _check("emb_clip_grads", st)
+    _tower.clip(grads, max_norm, norm, out, workspace, stream)
 
 
 class EmbCtx:

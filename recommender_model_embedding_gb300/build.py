@@ -2,7 +2,9 @@
 
 Each .cu file under csrc/ is compiled to an object in parallel, then linked into a shared
 library next to this file.  The CUDA runtime is linked statically, so the library loads
-on a machine without a GPU (it only needs the driver when a call reaches the device).
+on a machine without a GPU (it only needs the driver when a call reaches the device).  The
+Python side of the expert tower's calls (csrc/py_tower.c) becomes _tower.so beside it, linked
+to the library.
 """
 from __future__ import annotations
 
@@ -12,12 +14,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libemb.so")
+TOWER_SRC = os.path.join(CSRC, "py_tower.c")
+TOWER = os.path.join(HERE, "_tower.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -72,6 +77,15 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link of libemb.so failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if todo or force or _stale(TOWER, TOWER_SRC):
+        tmp = TOWER + f".tmp{os.getpid()}"
+        cmd = [shutil.which("gcc") or "gcc", "-O2", "-Wall", "-shared", "-fPIC", TOWER_SRC, "-o", tmp,
+               "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"),
+               "-L" + HERE, "-l:libemb.so", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"build of _tower.so failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, TOWER)
     if verbose:
         for l in logs:
             sys.stderr.write(l)
