@@ -48,13 +48,17 @@ __device__ __forceinline__ void load_keys(const int64_t* ids, int64_t w0, int64_
   }
 }
 
-// The lanes of the warp with this lane's key, of `bits` bits (all lanes call).
+// The lanes of the warp with this lane's key, of `bits` bits (all lanes call; four bits a step:
+// those above the key are zero in every lane and match).
 __device__ __forceinline__ uint32_t same_key(uint32_t key, int bits) {
   uint32_t peers = 0xFFFFFFFFu;
-  for (int b = 0; b < bits; ++b) {
-    const bool set = (key >> b) & 1u;
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, set);
-    peers &= set ? m : ~m;
+  for (int b0 = 0; b0 < bits; b0 += 4, key >>= 4) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const bool set = key & (1u << b);
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, set);
+      peers &= set ? m : ~m;
+    }
   }
   return peers;
 }
@@ -75,7 +79,6 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_count(const int64_t* id
                                                                int64_t chunk, uint32_t* hist) {
   extern __shared__ uint32_t sm_count[];
   asm volatile("griddepcontrol.launch_dependents;");
-  const int lane = threadIdx.x & 31, bits = 32 - __clz(E + 1);
   const int64_t c0 = (int64_t)blockIdx.x * chunk;
   const int64_t c1 = c0 + chunk < S ? c0 + chunk : S;
   const int64_t groups = (c1 - c0 + kSortThreads - 1) / kSortThreads;
@@ -89,8 +92,7 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_count(const int64_t* id
 #pragma unroll
     for (int u = 0; u < kSortDepth; ++u) {
       if (g0 + u >= groups) break;
-      const uint32_t peers = same_key(key[u], bits);
-      if (key[u] <= (uint32_t)E && lane == __ffs(peers) - 1) atomicAdd(sm_count + key[u], __popc(peers));
+      if (key[u] <= (uint32_t)E) atomicAdd(sm_count + key[u], 1u);
     }
   }
   __syncthreads();
