@@ -298,31 +298,33 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
   const int G = (int)p.chunks;
   uint32_t* hist = G > 1 ? static_cast<uint32_t*>(ws) : nullptr;
   const uint32_t* sums = hist;
-  const auto run = [&](auto kern, int warps, int staged) -> cudaError_t {
-    const int smem = (warps + 2) * (E + 1) * (int)sizeof(uint32_t) + staged * 6;
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-    }
-    if (hist) return launch_early(kern, G, warps * 32, smem, s, ids, S, E, p.chunk, sums, order, pos, offsets);
-    kern<<<1, warps * 32, smem, s>>>(ids, S, E, p.chunk, sums, order, pos, offsets);
+  const int staged = p.keep && hist ? kSortDepth * kSortThreads * 6 : 0;
+  const auto smem = [&](int warps) { return (warps + 2) * (E + 1) * (int)sizeof(uint32_t) + staged; };
+  if (!hist) {  // an empty batch still writes offsets
+    const bool few = S <= kSortFewWarps * 32 * kSortDepth;
+    constexpr auto small = k_expert_place<kSortFewWarps, true, false, false>;
+    constexpr auto big = k_expert_place<kSortWarps, true, false, false>;
+    const cudaError_t e = few ? allow_smem<small>() : allow_smem<big>();
+    if (e != cudaSuccess) return e;
+    if (few) small<<<1, kSortFewWarps * 32, smem(kSortFewWarps), s>>>(ids, S, E, p.chunk, sums, order, pos, offsets);
+    else big<<<1, kSortThreads, smem(kSortWarps), s>>>(ids, S, E, p.chunk, sums, order, pos, offsets);
     return cudaGetLastError();
-  };
-  if (!hist)  // an empty batch still writes offsets
-    return S <= kSortFewWarps * 32 * kSortDepth
-               ? run(k_expert_place<kSortFewWarps, true, false, false>, kSortFewWarps, 0)
-               : run(k_expert_place<kSortWarps, true, false, false>, kSortWarps, 0);
+  }
   k_expert_count<<<G, kSortThreads, (E + 1) * sizeof(uint32_t), s>>>(ids, S, E, p.chunk, hist);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.scan)
     e = launch_early(k_expert_scan, (E + 1 + 7) / 8, 256, 0, s, hist, G, E + 1);
   if (e != cudaSuccess) return e;
-  const int staged = kSortDepth * kSortThreads;
-  if (p.keep)
-    return p.scan ? run(k_expert_place<kSortWarps, true, true, true>, kSortWarps, staged)
-                  : run(k_expert_place<kSortWarps, true, true, false>, kSortWarps, staged);
-  return p.scan ? run(k_expert_place<kSortWarps, false, false, true>, kSortWarps, 0)
-                : run(k_expert_place<kSortWarps, false, false, false>, kSortWarps, 0);
+  const auto place = [&](auto keep, auto scanned) {
+    constexpr bool K = decltype(keep)::value;
+    constexpr auto kern = k_expert_place<kSortWarps, K, K, decltype(scanned)::value>;
+    const cudaError_t f = allow_smem<kern>();
+    return f != cudaSuccess ? f
+                            : launch_early(kern, G, kSortThreads, smem(kSortWarps), s, ids, S, E, p.chunk, sums,
+                                           order, pos, offsets);
+  };
+  if (p.keep) return p.scan ? place(std::true_type{}, std::true_type{}) : place(std::true_type{}, std::false_type{});
+  return p.scan ? place(std::false_type{}, std::true_type{}) : place(std::false_type{}, std::false_type{});
 }
 
 // ---- rows to and from their sorted places ----

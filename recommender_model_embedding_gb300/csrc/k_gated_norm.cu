@@ -46,6 +46,7 @@ struct NormArgs {
   char *x_out, *h, *dx, *dy, *dgate;
   uint32_t x_st, y_st, gate_st, dx_out_st, dh_st, x_out_st, h_st, dx_st, dy_st, dgate_st;  // bytes
   const float *w_post, *res_scale, *w_pre;
+  float *dw_post, *dres_scale, *dw_pre;
   float* part;  // [CTAs][2][dim] column sums (backward)
 };
 
@@ -342,6 +343,13 @@ __device__ __forceinline__ P at_row(P base, uint32_t row, uint32_t step, uint64_
   return base + ((uint64_t)row * step + ofs);
 }
 
+// The vectors' gradients of column k from its sums of dh q and t g a.
+__device__ __forceinline__ void put_cols(const NormArgs& a, int k, float pre, float t) {
+  if (a.dw_pre) a.dw_pre[k] = pre;
+  if (a.dw_post) a.dw_post[k] = (a.res_scale ? a.res_scale[k] : 1.f) * t;
+  if (a.dres_scale) a.dres_scale[k] = (a.w_post ? a.w_post[k] : 1.f) * t;
+}
+
 template <typename BT>
 __device__ __forceinline__ void row_gate(const NormArgs& a, uint32_t row, float& g, float& rest) {
   Pack<BT, 1> p;
@@ -371,14 +379,6 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
   const LX lx{tx, plx};
   const LB ly{tb, plb}, lg{tb + V * plb, plb};
   const uint64_t cx = (uint32_t)sh.first * LX::S::kBytes, cb = (uint32_t)sh.first * LB::S::kBytes;
-  ColWeights<EPU, V, WARP> cw;
-  cw.init(a, sh);
-  for (int s = 0; s < a.stages; ++s) {
-    lx.zero_tail(s * stage_bytes, left, sh);
-    ly.zero_tail(s * stage_bytes, left, sh);
-    if (GATE) lg.zero_tail(s * stage_bytes, left, sh);
-  }
-  __syncthreads();
 
   auto fetch = [&](uint32_t row, uint32_t stage) {
     if (row < a.n) {
@@ -391,6 +391,14 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
   const uint32_t step = gridDim.x * a.rpb, last = (a.stages - 1) * stage_bytes;
   uint32_t row = blockIdx.x * a.rpb + grp.id;
   for (int s = 0; s < a.stages - 1; ++s) fetch(row + s * step, s * stage_bytes);
+  ColWeights<EPU, V, WARP> cw;
+  cw.init(a, sh);
+  for (int s = 0; s < a.stages; ++s) {
+    lx.zero_tail(s * stage_bytes, left, sh);
+    ly.zero_tail(s * stage_bytes, left, sh);
+    if (GATE) lg.zero_tail(s * stage_bytes, left, sh);
+  }
+  __syncthreads();  // red_all is cleared
   uint32_t st = 0;
   // every group runs as many rounds as the CTA's first: shuffles and barriers stay whole
   for (uint32_t r0 = blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
@@ -478,21 +486,11 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
   const LX lx{tx, plx}, lt{tx + mx, plx};
   const LB ld{tb, plb}, ly{tb + mb, plb}, lg{tb + 2 * mb, plb};
   const uint64_t cx = (uint32_t)sh.first * LX::S::kBytes, cb = (uint32_t)sh.first * LB::S::kBytes;
-  ColWeights<EPU, V, WARP> cw;
-  cw.init(a, sh);
   float col_pre[K::NC][K::C], col_t[K::NC][K::C];
 #pragma unroll
   for (int i = 0; i < K::NC; ++i)
 #pragma unroll
     for (int m = 0; m < K::C; ++m) col_pre[i][m] = col_t[i][m] = 0.f;
-  for (int s = 0; s < a.stages; ++s) {
-    lx.zero_tail(s * stage_bytes, left, sh);
-    lt.zero_tail(s * stage_bytes, left, sh);
-    ld.zero_tail(s * stage_bytes, left, sh);
-    ly.zero_tail(s * stage_bytes, left, sh);
-    if (GATE) lg.zero_tail(s * stage_bytes, left, sh);
-  }
-  __syncthreads();
 
   auto fetch = [&](uint32_t row, uint32_t stage) {
     if (row < a.n) {
@@ -507,6 +505,16 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
   const uint32_t step = gridDim.x * a.rpb, last = (a.stages - 1) * stage_bytes;
   uint32_t row = blockIdx.x * a.rpb + grp.id;
   for (int s = 0; s < a.stages - 1; ++s) fetch(row + s * step, s * stage_bytes);
+  ColWeights<EPU, V, WARP> cw;
+  cw.init(a, sh);
+  for (int s = 0; s < a.stages; ++s) {
+    lx.zero_tail(s * stage_bytes, left, sh);
+    lt.zero_tail(s * stage_bytes, left, sh);
+    ld.zero_tail(s * stage_bytes, left, sh);
+    ly.zero_tail(s * stage_bytes, left, sh);
+    if (GATE) lg.zero_tail(s * stage_bytes, left, sh);
+  }
+  __syncthreads();  // red_all is cleared
   uint32_t st = 0;
   for (uint32_t r0 = blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
     const bool live = row < a.n;
@@ -606,43 +614,63 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
     st = st == last ? 0 : st + stage_bytes;
   }
   ring_wait_n<0>();
-  // the CTA's column sums: its groups are added one after another in shared memory
-  float* cols = reinterpret_cast<float*>(ring);  // [2][dim], when a CTA has more than one group
+  // the CTA's column sums: a warp's groups by shuffles, then the slices (warps, or groups of whole
+  // warps) side by side in shared memory
+  const int slices = tpr < 32 ? (int)blockDim.x / 32 : a.rpb;
+  const int slice = tpr < 32 ? (int)threadIdx.x / 32 : grp.id;
+  const bool writes = tpr >= 32 || (int)(threadIdx.x & 31) < tpr;
+  float* cols = reinterpret_cast<float*>(ring);  // [slices][2][dim], when there are several
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.dim;
-  for (int r = 0; r < a.rpb; ++r) {
-    if (a.rpb > 1) __syncthreads();
-    if (grp.id != r) continue;
+  const bool alone = gridDim.x == 1;  // then there is nothing to add: the results themselves
+  __syncthreads();  // the ring has been read
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (sh.step(i) >= left) continue;
+  for (int i = 0; i < V; ++i) {
 #pragma unroll
-      for (int m = 0; m < EPU; ++m) {
-        const int k = (sh.first + sh.step(i)) * EPU + m, e = i * EPU + m;
-        float p = col_pre[e / K::C][e % K::C], q = col_t[e / K::C][e % K::C];
-        if (r > 0) p += cols[k], q += cols[a.dim + k];
-        if (r < a.rpb - 1) cols[k] = p, cols[a.dim + k] = q;
+    for (int m = 0; m < EPU; ++m) {
+      const int e = i * EPU + m;
+      float p = col_pre[e / K::C][e % K::C], q = col_t[e / K::C][e % K::C];
+      if (!WARP)
+        for (int o = tpr; o < 32; o <<= 1) {
+          p += __shfl_xor_sync(0xFFFFFFFFu, p, o);
+          q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+        }
+      if (writes && sh.step(i) < left) {
+        const int k = (sh.first + sh.step(i)) * EPU + m;
+        if (slices > 1) cols[slice * 2 * a.dim + k] = p, cols[(slice * 2 + 1) * a.dim + k] = q;
+        else if (alone) put_cols(a, k, p, q);
         else out[k] = p, out[a.dim + k] = q;
       }
     }
+  }
+  if (slices == 1) return;
+  __syncthreads();
+  for (int k = threadIdx.x; k < a.dim; k += blockDim.x) {
+    float p = 0.f, q = 0.f;
+    for (int r = 0; r < slices; ++r) p += cols[r * 2 * a.dim + k], q += cols[(r * 2 + 1) * a.dim + k];
+    if (alone) put_cols(a, k, p, q);
+    else out[k] = p, out[a.dim + k] = q;
   }
 }
 
 // Sums the CTAs' parts: 32 columns a CTA, 32 threads a column over interleaved parts, then over
 // the 32 in order.
-__global__ void __launch_bounds__(1024) k_gated_norm_cols(const float* part, int parts, int dim,
-                                                          const float* w_post, const float* res_scale,
-                                                          float* dw_post, float* dres_scale,
-                                                          float* dw_pre) {
+__global__ void __launch_bounds__(1024) k_gated_norm_cols(NormArgs a, int parts) {
   __shared__ float sh[2][32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, k = blockIdx.x * 32 + lane;
+  const float* part = a.part;
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, k = blockIdx.x * 32 + lane, dim = a.dim;
   float p = 0.f, t = 0.f;
-  if (k < dim) {
-#pragma unroll 4
-    for (int g = slice; g < parts; g += 32) {
-      p += part[(int64_t)g * 2 * dim + k];
-      t += part[(int64_t)g * 2 * dim + dim + k];
+  for (int g0 = slice; g0 < parts; g0 += 32 * 8) {  // 8 CTAs' parts loaded together
+    float c[8], d[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool in = g0 + u * 32 < parts && k < dim;
+      const float* q = part + (int64_t)(g0 + u * 32) * 2 * dim + k;
+      c[u] = in ? __ldcg(q) : 0.f;
+      d[u] = in ? __ldcg(q + dim) : 0.f;
     }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) p += c[u], t += d[u];
   }
   sh[0][slice][lane] = p;
   sh[1][slice][lane] = t;
@@ -652,9 +680,7 @@ __global__ void __launch_bounds__(1024) k_gated_norm_cols(const float* part, int
   p = lanes_sum(sh[0][lane][slice], 32);
   t = lanes_sum(sh[1][lane][slice], 32);
   if (lane == 0 && col < dim) {
-    if (dw_pre) dw_pre[col] = p;
-    if (dw_post) dw_post[col] = (res_scale ? res_scale[col] : 1.f) * t;
-    if (dres_scale) dres_scale[col] = (w_post ? w_post[col] : 1.f) * t;
+    put_cols(a, col, p, t);
   }
 }
 
@@ -692,13 +718,6 @@ static int norm_ring(NormArgs& a, int thread_bytes, int per) {
   return a.stages * bytes;
 }
 
-// Rings above the default limit have to be asked for.
-template <typename K>
-static cudaError_t norm_smem(K kern, int smem) {
-  return smem <= 44 * 1024 ? cudaSuccess
-                           : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-}
-
 static NormArgs norm_args(const emb_norm& p) {
   const int xe = p.x_dtype == EMB_BF16 ? 2 : 4, be = p.dtype == EMB_BF16 ? 2 : 4;
   const auto in = [](const void* q) { return static_cast<const char*>(q); };
@@ -715,6 +734,7 @@ static NormArgs norm_args(const emb_norm& p) {
   a.h_st = (uint32_t)(p.h_ld * be), a.dh_st = (uint32_t)(p.dh_ld * be);
   a.dy_st = (uint32_t)(p.dy_ld * be), a.dgate_st = (uint32_t)(p.dgate_ld * be);
   a.w_post = p.d_w_post, a.res_scale = p.d_res_scale, a.w_pre = p.d_w_pre;
+  a.dw_post = p.d_dw_post, a.dres_scale = p.d_dres_scale, a.dw_pre = p.d_dw_pre;
   return a;
 }
 
@@ -735,18 +755,19 @@ template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
   const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : 4;
   const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>, per);
-  const auto kern = k_gated_norm<XT, BT, EPU, V, GATE, WARP>;
+  constexpr auto kern = k_gated_norm<XT, BT, EPU, V, GATE, WARP>;
   const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = (int64_t)device_sms() * norm_fit(per, smem);
-  const cudaError_t e = norm_smem(kern, smem);
+  const cudaError_t e = allow_smem<kern>();
   if (e != cudaSuccess) return e;
   kern<<<(int)(blocks < cap ? blocks : cap), threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-// CTAs of the backward: no more than `cap`, and at least four rows a group where that is fewer,
-// so that the column parts stay small beside the rows.
+// CTAs of the backward: a row a group up to one CTA an SM, then at least four rows a group up to
+// `cap`, so that the column parts stay small beside the rows.
 static int64_t norm_bwd_grid(int64_t n, int rpb, int64_t cap) {
-  const int64_t blocks = (n + 4 * rpb - 1) / (4 * rpb);
+  const int64_t sms = device_sms(), all = (n + rpb - 1) / rpb, four = (n + 4 * rpb - 1) / (4 * rpb);
+  const int64_t blocks = all <= sms ? all : four > sms ? four : sms;
   return blocks < 1 ? 1 : blocks < cap ? blocks : cap;
 }
 
@@ -763,10 +784,11 @@ template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_bwd_v(NormArgs& a, int* grid, cudaStream_t s) {
   const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : kNormCtasPerSm;
   int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>, per);
-  const int cols = a.rpb > 1 ? 2 * a.dim * (int)sizeof(float) : 0;
+  const int slices = a.tpr < 32 ? threads / 32 : a.rpb;
+  const int cols = slices > 1 ? slices * 2 * a.dim * (int)sizeof(float) : 0;
   if (smem < cols) smem = cols;
-  const auto kern = k_gated_norm_bwd<XT, BT, EPU, V, GATE, WARP>;
-  const cudaError_t e = norm_smem(kern, smem);
+  constexpr auto kern = k_gated_norm_bwd<XT, BT, EPU, V, GATE, WARP>;
+  const cudaError_t e = allow_smem<kern>();
   if (e != cudaSuccess) return e;
   *grid = (int)norm_bwd_grid(a.n, a.rpb, (int64_t)device_sms() * norm_fit(per, smem));
   kern<<<*grid, threads, smem, s>>>(a);
@@ -814,11 +836,8 @@ cudaError_t launch_gated_norm_bwd(const emb_norm& p, void* ws, cudaStream_t s) {
   a.part = static_cast<float*>(ws);
   int grid = 0;
   cudaError_t e = p.n > 0 ? norm_call<true>(p, a, &grid, s) : cudaSuccess;
-  if (e == cudaSuccess && (p.d_dw_post || p.d_dres_scale || p.d_dw_pre)) {
-    e = launch_early(k_gated_norm_cols, (p.dim + 31) / 32, 1024, 0, s, (const float*)a.part, grid, p.dim,
-                     p.d_w_post, p.d_res_scale, p.d_dw_post, p.d_dres_scale, p.d_dw_pre);
-  }
-  return e;
+  if (e != cudaSuccess || grid == 1 || !(p.d_dw_post || p.d_dres_scale || p.d_dw_pre)) return e;
+  return launch_early(k_gated_norm_cols, (p.dim + 31) / 32, 1024, 0, s, a, grid);
 }
 
 }  // namespace emb

@@ -165,6 +165,25 @@ inline int device_sms() {
   return 1;
 }
 
+// Lets a kernel take as much dynamic shared memory as a CTA can have (asked for once per kernel and
+// device: the request costs a call's host time).
+template <auto KERN>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0, most = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes fa{};
+  e = cudaFuncGetAttributes(&fa, KERN);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // Whether a matrix of rows allows accesses of `bytes` (a power of two): base and row step on
 // such boundaries.
 inline bool rows_on(const void* p, int64_t ld, int elem, int bytes) {
