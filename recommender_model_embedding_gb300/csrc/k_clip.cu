@@ -135,7 +135,8 @@ __device__ __forceinline__ double share_squares(const ClipList<N>& l, int64_t t0
 template <int N>
 __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
     k_clip_norm(const __grid_constant__ ClipList<N> l, double* part) {
-  asm volatile("griddepcontrol.launch_dependents;");
+  let_next_start();
+  wait_for_earlier();
   const double acc = cta_sum<kClipThreads>(share_squares<kClipThreads>(l, blockIdx.x, gridDim.x));
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(kClipThreads, kClipScaleCtasPerSm)
     k_clip_scale(const __grid_constant__ ClipList<N> l, const double* part, int parts, float max_norm,
                  float* norm_out, int inplace) {
   __shared__ float factor;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
+  wait_for_earlier();
   double acc = 0.0;
 #pragma unroll 5
   for (int i = threadIdx.x; i < parts; i += kClipThreads) acc += __ldcg(part + i);
@@ -232,6 +234,8 @@ __global__ void __launch_bounds__(kClusterThreads)
     k_clip_cluster(const __grid_constant__ ClipList<N> l, float max_norm, float* norm_out, int inplace) {
   __shared__ double part;
   __shared__ float factor;
+  let_next_start();
+  wait_for_earlier();
   const double mine = cta_sum<kClusterThreads>(share_squares<kClusterThreads>(l, blockIdx.x, gridDim.x));
   if (threadIdx.x == 0) part = mine;
   asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
@@ -273,12 +277,14 @@ static cudaError_t clip_cluster(const ClipList<N>& l, float max_norm, float* nor
   const auto kern = k_clip_cluster<N>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kClusterCtas, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kClusterCtas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(kClusterCtas), cfg.blockDim = dim3(kClusterThreads);
-  cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
+  cfg.stream = s, cfg.attrs = attr, cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, l, max_norm, norm, inplace);
 }
 
@@ -322,8 +328,7 @@ static cudaError_t clip_lists(const emb_tensor* list, int64_t count, float max_n
   cudaError_t e = cudaSuccess;
   do {  // an empty list still gives its norm of zero
     grid = fill(i0);
-    k_clip_norm<N><<<grid, kClipThreads, 0, s>>>(l, part + parts);
-    e = cudaGetLastError();
+    e = launch_early(k_clip_norm<N>, (unsigned)grid, kClipThreads, 0, s, l, part + parts);
     parts += grid;
     i0 += N;
   } while (i0 < count && e == cudaSuccess);
@@ -331,7 +336,7 @@ static cudaError_t clip_lists(const emb_tensor* list, int64_t count, float max_n
   for (i0 = 0; e == cudaSuccess && (i0 < count || i0 == 0); i0 += N) {
     if (!one) grid = fill(i0);
     const int64_t most = sms * kClipScaleCtasPerSm;
-    e = launch_early(k_clip_scale<N>, (int)(grid < most ? grid : most), kClipThreads, 0, s, l,
+    e = launch_early(k_clip_scale<N>, (unsigned)(grid < most ? grid : most), kClipThreads, 0, s, l,
                      (const double*)part, parts, max_norm, norm, inplace);
   }
   return e;

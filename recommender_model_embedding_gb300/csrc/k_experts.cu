@@ -78,7 +78,8 @@ __device__ __forceinline__ uint32_t take_rank(uint32_t* mine, uint32_t key, int 
 __global__ void __launch_bounds__(kSortThreads) k_expert_count(const int64_t* ids, int64_t S, int E,
                                                                int64_t chunk, uint32_t* hist) {
   extern __shared__ uint32_t sm_count[];
-  asm volatile("griddepcontrol.launch_dependents;");
+  wait_for_earlier();
+  let_next_start();  // not before: the placing kernel reads the ids before it waits for this one
   const int64_t c0 = (int64_t)blockIdx.x * chunk;
   const int64_t c1 = c0 + chunk < S ? c0 + chunk : S;
   const int64_t groups = (c1 - c0 + kSortThreads - 1) / kSortThreads;
@@ -103,8 +104,8 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_count(const int64_t* id
 // The counts of all chunks, summed over the chunks before each (in place), and their totals after
 // the last chunk's: one warp a key.
 __global__ void __launch_bounds__(256) k_expert_scan(uint32_t* hist, int chunks, int K) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
+  wait_for_earlier();
   const int lane = threadIdx.x & 31, e = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (e >= K) return;
   uint32_t run = 0;
@@ -142,6 +143,8 @@ __global__ void __launch_bounds__(WARPS * 32)
   // [warps][E + 1] places within the chunk; [E + 1] totals, then bases; [E + 1] earlier chunks, then
   // how far the places are from the chunk's own order; KEEP: [8192] slots and keys in that order
   extern __shared__ uint32_t sm_place[];
+  let_next_start();
+  if (!hist) wait_for_earlier();
   __shared__ uint32_t warp_tot[2][WARPS];
   const int K = E + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bits = 32 - __clz(E + 1);
   uint32_t* total = sm_place + WARPS * K;
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(WARPS * 32)
       if (g0 + u < groups) rank[u] = take_rank(mine, key[u], E, bits);
   }
   if (hist) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_earlier();
     if (SCANNED)
       for (int e = threadIdx.x; e < K; e += THREADS) {
         before[e] = __ldcg(hist + (int64_t)blockIdx.x * K + e);
@@ -306,12 +309,12 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
     constexpr auto big = k_expert_place<kSortWarps, true, false, false>;
     const cudaError_t e = few ? allow_smem<small>() : allow_smem<big>();
     if (e != cudaSuccess) return e;
-    if (few) small<<<1, kSortFewWarps * 32, smem(kSortFewWarps), s>>>(ids, S, E, p.chunk, sums, order, pos, offsets);
-    else big<<<1, kSortThreads, smem(kSortWarps), s>>>(ids, S, E, p.chunk, sums, order, pos, offsets);
-    return cudaGetLastError();
+    const int warps = few ? kSortFewWarps : kSortWarps;
+    return launch_early(few ? small : big, 1, warps * 32, smem(warps), s, ids, S, E, p.chunk, sums, order,
+                        pos, offsets);
   }
-  k_expert_count<<<G, kSortThreads, (E + 1) * sizeof(uint32_t), s>>>(ids, S, E, p.chunk, hist);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_early(k_expert_count, G, kSortThreads, (E + 1) * (int)sizeof(uint32_t), s, ids, S, E,
+                               p.chunk, hist);
   if (e == cudaSuccess && p.scan)
     e = launch_early(k_expert_scan, (E + 1 + 7) / 8, 256, 0, s, hist, G, E + 1);
   if (e != cudaSuccess) return e;
@@ -388,6 +391,8 @@ __global__ void __launch_bounds__(kMoveThreads)
     k_expert_dispatch(const char* x, uint32_t x_st, const int32_t* pos, int k, MoveShape m, char* xs,
                       uint32_t xs_st) {
   using V = typename Unit<UB>::T;
+  let_next_start();
+  wait_for_earlier();
   uint32_t row;
   int unit;
   if (!move_task(m, UN, row, unit)) return;
@@ -412,17 +417,20 @@ __global__ void __launch_bounds__(kMoveThreads)
 }
 
 template <int UB>
-static void dispatch_units(const void* x, uint32_t x_st, const int32_t* pos, int64_t n, int k,
+static cudaError_t dispatch_units(const void* x, uint32_t x_st, const int32_t* pos, int64_t n, int k,
                            int row, void* xs, uint32_t xs_st, cudaStream_t s) {
   MoveShape m;
   const int un = move_shape(m, n, row / UB, 8);
   const unsigned grid = move_grid(m);
   const char* in = static_cast<const char*>(x);
   char* out = static_cast<char*>(xs);
-  if (un == 1) k_expert_dispatch<UB, 1><<<grid, kMoveThreads, 0, s>>>(in, x_st, pos, k, m, out, xs_st);
-  else if (un == 2) k_expert_dispatch<UB, 2><<<grid, kMoveThreads, 0, s>>>(in, x_st, pos, k, m, out, xs_st);
-  else if (un == 4) k_expert_dispatch<UB, 4><<<grid, kMoveThreads, 0, s>>>(in, x_st, pos, k, m, out, xs_st);
-  else k_expert_dispatch<UB, 8><<<grid, kMoveThreads, 0, s>>>(in, x_st, pos, k, m, out, xs_st);
+  const auto run = [&](auto kern) {
+    return launch_early(kern, grid, kMoveThreads, 0, s, in, x_st, pos, k, m, out, xs_st);
+  };
+  return un == 1   ? run(k_expert_dispatch<UB, 1>)
+         : un == 2 ? run(k_expert_dispatch<UB, 2>)
+         : un == 4 ? run(k_expert_dispatch<UB, 4>)
+                   : run(k_expert_dispatch<UB, 8>);
 }
 
 cudaError_t launch_expert_dispatch(const void* x, int64_t x_ld, const int32_t* pos, int64_t n, int k,
@@ -432,10 +440,9 @@ cudaError_t launch_expert_dispatch(const void* x, int64_t x_ld, const int32_t* p
   const int row = dim * elem;
   const uint64_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(xs) | x_st | xs_st |
                        (uint64_t)row;
-  if ((all & 15) == 0) dispatch_units<16>(x, x_st, pos, n, k, row, xs, xs_st, s);
-  else if ((all & 3) == 0) dispatch_units<4>(x, x_st, pos, n, k, row, xs, xs_st, s);
-  else dispatch_units<2>(x, x_st, pos, n, k, row, xs, xs_st, s);
-  return cudaGetLastError();
+  if ((all & 15) == 0) return dispatch_units<16>(x, x_st, pos, n, k, row, xs, xs_st, s);
+  if ((all & 3) == 0) return dispatch_units<4>(x, x_st, pos, n, k, row, xs, xs_st, s);
+  return dispatch_units<2>(x, x_st, pos, n, k, row, xs, xs_st, s);
 }
 
 // Combine: KU sorted rows are loaded together (min(k, 4)); products and sums are fp32 whatever
@@ -445,6 +452,8 @@ __global__ void __launch_bounds__(kMoveThreads, EPU * UN * KU > 48 ? 3 : 4)
     k_expert_combine(const T* ys, uint32_t ys_st, const int32_t* pos, const float* w, int k,
                      MoveShape m, T* out, uint32_t out_st) {
   constexpr int UB = EPU * (int)sizeof(T);
+  let_next_start();
+  wait_for_earlier();
   uint32_t row;
   int unit;
   if (!move_task(m, UN, row, unit)) return;
@@ -496,37 +505,37 @@ __global__ void __launch_bounds__(kMoveThreads, EPU * UN * KU > 48 ? 3 : 4)
 }
 
 template <typename T, int EPU, int UN, bool WEIGHTED>
-static void combine_un(const T* ys, uint32_t ys_st, const int32_t* pos, const float* w, int k,
-                       const MoveShape& m, T* out, uint32_t out_st, cudaStream_t s) {
-  const unsigned grid = move_grid(m);
-  if (k == 1)
-    k_expert_combine<T, EPU, UN, 1, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
-  else if (k == 2)
-    k_expert_combine<T, EPU, UN, 2, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
-  else if (k == 3)
-    k_expert_combine<T, EPU, UN, 3, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
-  else
-    k_expert_combine<T, EPU, UN, 4, WEIGHTED><<<grid, kMoveThreads, 0, s>>>(ys, ys_st, pos, w, k, m, out, out_st);
+static cudaError_t combine_un(const T* ys, uint32_t ys_st, const int32_t* pos, const float* w, int k,
+                              const MoveShape& m, T* out, uint32_t out_st, cudaStream_t s) {
+  const auto run = [&](auto kern) {
+    return launch_early(kern, move_grid(m), kMoveThreads, 0, s, ys, ys_st, pos, w, k, m, out, out_st);
+  };
+  return k == 1   ? run(k_expert_combine<T, EPU, UN, 1, WEIGHTED>)
+         : k == 2 ? run(k_expert_combine<T, EPU, UN, 2, WEIGHTED>)
+         : k == 3 ? run(k_expert_combine<T, EPU, UN, 3, WEIGHTED>)
+                  : run(k_expert_combine<T, EPU, UN, 4, WEIGHTED>);
 }
 
 template <typename T, int EPU>
-static void combine_units(const void* ys, uint32_t ys_st, const int32_t* pos, const float* w,
-                          int64_t n, int k, int dim, void* out, uint32_t out_st, cudaStream_t s) {
+static cudaError_t combine_units(const void* ys, uint32_t ys_st, const int32_t* pos, const float* w,
+                                 int64_t n, int k, int dim, void* out, uint32_t out_st, cudaStream_t s) {
   MoveShape m;
   const int un = move_shape(m, n, dim / EPU, EPU > 2 ? 2 : 8 / EPU);
   const T* y = static_cast<const T*>(ys);
   T* o = static_cast<T*>(out);
   const auto run = [&](auto unc) {
     constexpr int UN = decltype(unc)::value;
-    if (w) combine_un<T, EPU, UN, true>(y, ys_st, pos, w, k, m, o, out_st, s);
-    else combine_un<T, EPU, UN, false>(y, ys_st, pos, w, k, m, o, out_st, s);
+    return w ? combine_un<T, EPU, UN, true>(y, ys_st, pos, w, k, m, o, out_st, s)
+             : combine_un<T, EPU, UN, false>(y, ys_st, pos, w, k, m, o, out_st, s);
   };
-  if (un == 1) run(std::integral_constant<int, 1>{});
-  else if (un == 2) run(std::integral_constant<int, 2>{});
-  else if constexpr (EPU <= 2) {
-    if (un == 4) run(std::integral_constant<int, 4>{});
-    else if constexpr (EPU == 1) run(std::integral_constant<int, 8>{});
-  }
+  if (un == 1) return run(std::integral_constant<int, 1>{});
+  if constexpr (EPU <= 2)
+    if (un >= 4) {
+      if constexpr (EPU == 1)
+        if (un == 8) return run(std::integral_constant<int, 8>{});
+      return run(std::integral_constant<int, 4>{});
+    }
+  return run(std::integral_constant<int, 2>{});
 }
 
 // w NULL: weights of one (the gradient of dispatch)
@@ -540,14 +549,12 @@ cudaError_t launch_expert_combine(const void* ys, int64_t ys_ld, const int32_t* 
                        out_st | (uint64_t)(dim * elem);
   using H = __nv_bfloat16;
   if (bf16) {
-    if ((all & 15) == 0) combine_units<H, 8>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
-    else if ((all & 3) == 0) combine_units<H, 2>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
-    else combine_units<H, 1>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
-  } else {
-    if ((all & 15) == 0) combine_units<float, 4>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
-    else combine_units<float, 1>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
+    if ((all & 15) == 0) return combine_units<H, 8>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
+    if ((all & 3) == 0) return combine_units<H, 2>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
+    return combine_units<H, 1>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
   }
-  return cudaGetLastError();
+  if ((all & 15) == 0) return combine_units<float, 4>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
+  return combine_units<float, 1>(ys, ys_st, pos, w, n, k, dim, out, out_st, s);
 }
 
 // ---- gradient of combine: dys and dw in one pass over dout and the sorted rows ----
@@ -564,6 +571,8 @@ __global__ void __launch_bounds__(kCombThreads)
                          const int32_t* pos, const float* w, uint32_t n, int k, int U, int shift,
                          T* dys, uint32_t dys_st, float* dw) {
   constexpr int UB = EPU * (int)sizeof(T);
+  let_next_start();
+  wait_for_earlier();
   __shared__ float part[KM][kCombThreads / 32];
   const int tpr = 1 << shift, sub = threadIdx.x & (tpr - 1);
   const uint32_t row = blockIdx.x * (kCombThreads >> shift) + (threadIdx.x >> shift);
@@ -643,7 +652,7 @@ __global__ void __launch_bounds__(kCombThreads)
 }
 
 template <typename T, int EPU>
-static void combine_bwd_units(const void* dout, uint32_t dout_st, const void* ys, uint32_t ys_st,
+static cudaError_t combine_bwd_units(const void* dout, uint32_t dout_st, const void* ys, uint32_t ys_st,
                               const int32_t* pos, const float* w, int64_t n, int k, int dim,
                               void* dys, uint32_t dys_st, float* dw, cudaStream_t s) {
   const int U = dim / EPU;
@@ -653,16 +662,16 @@ static void combine_bwd_units(const void* dout, uint32_t dout_st, const void* ys
   const int64_t enough = (int64_t)device_sms() * 16 * 32;
   while (shift >= 5 && shift < 8 && (n << shift) < enough && (1 << shift) < U) ++shift;
   const unsigned grid = (unsigned)(((n << shift) + kCombThreads - 1) / kCombThreads);
-#define EMB_COMBINE_BWD(KM, UN)                                                                   \
-  k_expert_combine_bwd<T, EPU, KM, UN><<<grid, kCombThreads, 0, s>>>(                             \
-      static_cast<const T*>(dout), dout_st, static_cast<const T*>(ys), ys_st, pos, w, (uint32_t)n, \
-      k, U, shift, static_cast<T*>(dys), dys_st, dw)
-  if (k == 1) EMB_COMBINE_BWD(1, 4);
-  else if (k == 2) EMB_COMBINE_BWD(2, 2);
-  else if (k <= 4) EMB_COMBINE_BWD(4, (EPU > 2 ? 1 : 2));
-  else if (k <= 8) EMB_COMBINE_BWD(8, 1);
-  else EMB_COMBINE_BWD(16, 1);
-#undef EMB_COMBINE_BWD
+  const auto run = [&](auto kern) {
+    return launch_early(kern, grid, kCombThreads, 0, s, static_cast<const T*>(dout), dout_st,
+                        static_cast<const T*>(ys), ys_st, pos, w, (uint32_t)n, k, U, shift,
+                        static_cast<T*>(dys), dys_st, dw);
+  };
+  return k == 1   ? run(k_expert_combine_bwd<T, EPU, 1, 4>)
+         : k == 2 ? run(k_expert_combine_bwd<T, EPU, 2, 2>)
+         : k <= 4 ? run(k_expert_combine_bwd<T, EPU, 4, (EPU > 2 ? 1 : 2)>)
+         : k <= 8 ? run(k_expert_combine_bwd<T, EPU, 8, 1>)
+                  : run(k_expert_combine_bwd<T, EPU, 16, 1>);
 }
 
 cudaError_t launch_expert_combine_bwd(const void* dout, int64_t dout_ld, const void* ys,
@@ -677,14 +686,12 @@ cudaError_t launch_expert_combine_bwd(const void* dout, int64_t dout_ld, const v
                        reinterpret_cast<uintptr_t>(dys) | g_st | y_st | o_st | (uint64_t)(dim * elem);
   using H = __nv_bfloat16;
   if (bf16) {
-    if ((all & 15) == 0) combine_bwd_units<H, 8>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
-    else if ((all & 3) == 0) combine_bwd_units<H, 2>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
-    else combine_bwd_units<H, 1>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
-  } else {
-    if ((all & 15) == 0) combine_bwd_units<float, 4>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
-    else combine_bwd_units<float, 1>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
+    if ((all & 15) == 0) return combine_bwd_units<H, 8>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
+    if ((all & 3) == 0) return combine_bwd_units<H, 2>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
+    return combine_bwd_units<H, 1>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
   }
-  return cudaGetLastError();
+  if ((all & 15) == 0) return combine_bwd_units<float, 4>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
+  return combine_bwd_units<float, 1>(dout, g_st, ys, y_st, pos, w, n, k, dim, dys, o_st, dw, s);
 }
 
 }  // namespace emb

@@ -362,6 +362,8 @@ __device__ __forceinline__ void row_gate(const NormArgs& a, uint32_t row, float&
 // GATE: a gate for each element.
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EPU > 8 ? 1 : 4) k_gated_norm(NormArgs a) {
+  let_next_start();
+  wait_for_earlier();
   using K = Chunks<EPU, V>;
   using LX = Lane<XT, EPU, V, WARP>;
   using LB = Lane<BT, EPU, V, WARP>;
@@ -467,7 +469,8 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EPU > 8 ? 1 : 3) k_gated_norm_bwd(NormArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;");
+  let_next_start();
+  wait_for_earlier();
   using K = Chunks<EPU, V>;
   using LX = Lane<XT, EPU, V, WARP>;
   using LB = Lane<BT, EPU, V, WARP>;
@@ -656,7 +659,8 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
 // the 32 in order.
 __global__ void __launch_bounds__(1024) k_gated_norm_cols(NormArgs a, int parts) {
   __shared__ float sh[2][32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early
+  let_next_start();
+  wait_for_earlier();
   const float* part = a.part;
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, k = blockIdx.x * 32 + lane, dim = a.dim;
   float p = 0.f, t = 0.f;
@@ -759,8 +763,7 @@ static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
   const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = (int64_t)device_sms() * norm_fit(per, smem);
   const cudaError_t e = allow_smem<kern>();
   if (e != cudaSuccess) return e;
-  kern<<<(int)(blocks < cap ? blocks : cap), threads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(kern, (unsigned)(blocks < cap ? blocks : cap), threads, smem, s, a);
 }
 
 // CTAs of the backward: a row a group up to one CTA an SM, then at least four rows a group up to
@@ -791,8 +794,7 @@ static cudaError_t norm_bwd_v(NormArgs& a, int* grid, cudaStream_t s) {
   const cudaError_t e = allow_smem<kern>();
   if (e != cudaSuccess) return e;
   *grid = (int)norm_bwd_grid(a.n, a.rpb, (int64_t)device_sms() * norm_fit(per, smem));
-  kern<<<*grid, threads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(kern, (unsigned)*grid, threads, smem, s, a);
 }
 
 // The kernel of a call by packs per thread (1, 2, 4, 8 or 16: at most 16 elements), gate and

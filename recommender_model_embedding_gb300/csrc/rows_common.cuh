@@ -134,17 +134,26 @@ __device__ __forceinline__ float lanes_sum(float v, int tpr) {
   return v;
 }
 
-// Launches the second kernel of a call so that it may start while the first still runs: the
-// kernel must pass griddepcontrol.wait, which holds until the first has finished and its
-// writes are visible, before it touches anything the first or earlier work writes or reads.
+// The tower's kernels run for microseconds, so they are launched early: the next kernel of the
+// stream may be set up and its CTAs placed while the last one still runs.  Every kernel
+// therefore passes wait_for_earlier() before it touches anything that earlier work writes or
+// reads (it holds until that work has finished and its writes are visible; since every kernel
+// passes it, that covers all earlier work, not the last kernel's alone), and says
+// let_next_start() once its own CTAs may be joined.  Work of other kinds before or after such a
+// kernel (copies, kernels launched in the ordinary way) is ordered as always.
+__device__ __forceinline__ void wait_for_earlier() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 template <typename... P, typename... A>
-cudaError_t launch_early(void (*kern)(P...), int grid, int threads, int smem, cudaStream_t s,
+cudaError_t launch_early(void (*kern)(P...), unsigned grid, int threads, int smem, cudaStream_t s,
                          A&&... args) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid), cfg.blockDim = dim3((unsigned)threads);
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem, cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
 }
