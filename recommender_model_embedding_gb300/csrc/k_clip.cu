@@ -274,8 +274,8 @@ bool clip_in_one_launch(int64_t count, int64_t total) {
 template <int N>
 static cudaError_t clip_cluster(const ClipList<N>& l, float max_norm, float* norm, int inplace,
                                 cudaStream_t s) {
-  const auto kern = k_clip_cluster<N>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  constexpr auto kern = k_clip_cluster<N>;
+  const cudaError_t e = prepare_kernel<kern, true>();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2]{};
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -307,7 +307,7 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
     const bool few = S <= kSortFewWarps * 32 * kSortDepth;
     constexpr auto small = k_expert_place<kSortFewWarps, true, false, false>;
     constexpr auto big = k_expert_place<kSortWarps, true, false, false>;
-    const cudaError_t e = few ? allow_smem<small>() : allow_smem<big>();
+    const cudaError_t e = few ? prepare_kernel<small>() : prepare_kernel<big>();
     if (e != cudaSuccess) return e;
     const int warps = few ? kSortFewWarps : kSortWarps;
     return launch_early(few ? small : big, 1, warps * 32, smem(warps), s, ids, S, E, p.chunk, sums, order,
@@ -321,7 +321,7 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
   const auto place = [&](auto keep, auto scanned) {
     constexpr bool K = decltype(keep)::value;
     constexpr auto kern = k_expert_place<kSortWarps, K, K, decltype(scanned)::value>;
-    const cudaError_t f = allow_smem<kern>();
+    const cudaError_t f = prepare_kernel<kern>();
     return f != cudaSuccess ? f
                             : launch_early(kern, G, kSortThreads, smem(kSortWarps), s, ids, S, E, p.chunk, sums,
                                            order, pos, offsets);

@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
     float g_row = 1.f, rest;
     if (!GATE && a.gate_row && live) row_gate<BT>(a, row, g_row, rest);
     ring_wait(a.stages);
-    float f[K::NC][K::C];  // x_out
+    float f[K::NC][K::C];  // y, then x_out
     float s[1], s2[2] = {0.f, 0.f}, ry = 0.f;
     if (a.y) {
       if (live)
@@ -429,10 +429,9 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
         float x[K::C];
         lx.read(st, i, x);
         if (a.y) {
-          float g[K::C], y[K::C];
+          float g[K::C];
           cw.use(a, sh, i);
-          ly.read(st, i, y);
-          v_mul(y, y, ry);
+          v_mul(f[i], f[i], ry);
           if (GATE) {
             lg.read(st, i, g);
 #pragma unroll
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
           } else {
             v_mul(g, cw.rw, g_row);
           }
-          v_fma(x, g, y, x);
+          v_fma(x, g, f[i], x);
           LX::store(at_row(a.x_out, row, a.x_out_st, cx), i, x, left, sh);
         }
         v_dot(s2, x, x);
@@ -761,7 +760,7 @@ static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
   const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>, per);
   constexpr auto kern = k_gated_norm<XT, BT, EPU, V, GATE, WARP>;
   const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = (int64_t)device_sms() * norm_fit(per, smem);
-  const cudaError_t e = allow_smem<kern>();
+  const cudaError_t e = prepare_kernel<kern>();
   if (e != cudaSuccess) return e;
   return launch_early(kern, (unsigned)(blocks < cap ? blocks : cap), threads, smem, s, a);
 }
@@ -791,7 +790,7 @@ static cudaError_t norm_bwd_v(NormArgs& a, int* grid, cudaStream_t s) {
   const int cols = slices > 1 ? slices * 2 * a.dim * (int)sizeof(float) : 0;
   if (smem < cols) smem = cols;
   constexpr auto kern = k_gated_norm_bwd<XT, BT, EPU, V, GATE, WARP>;
-  const cudaError_t e = allow_smem<kern>();
+  const cudaError_t e = prepare_kernel<kern>();
   if (e != cudaSuccess) return e;
   *grid = (int)norm_bwd_grid(a.n, a.rpb, (int64_t)device_sms() * norm_fit(per, smem));
   return launch_early(kern, (unsigned)*grid, threads, smem, s, a);

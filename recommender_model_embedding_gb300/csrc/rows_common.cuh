@@ -174,10 +174,11 @@ inline int device_sms() {
   return 1;
 }
 
-// Lets a kernel take as much dynamic shared memory as a CTA can have (asked for once per kernel and
-// device: the request costs a call's host time).
-template <auto KERN>
-cudaError_t allow_smem() {
+// Settings of a kernel that its default launch does not have, asked for once per kernel and device
+// (the request costs a call's host time): as much dynamic shared memory as a CTA can have, and
+// clusters of 16 CTAs.
+template <auto KERN, bool CLUSTER = false>
+cudaError_t prepare_kernel() {
   static std::atomic<uint64_t> done{0};
   int dev = 0, most = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -189,6 +190,7 @@ cudaError_t allow_smem() {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
+  if (e == cudaSuccess && CLUSTER) e = cudaFuncSetAttribute(KERN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }

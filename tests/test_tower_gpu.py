@@ -636,3 +636,81 @@ def test_workspace_contents_do_not_matter(E):
         assert torch.equal(a, b)
     a, b = norm_grad(E, s, 1e-6, workspace=ws), norm_grad(E, s, 1e-6)
     assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+def test_calls_between_other_work(E):
+    """Calls queued back to back with torch's kernels and copies before, between and after them, on
+    buffers that are written again every round, give what the same work gives with a wait after
+    every step."""
+    n, k, e, d = 700, 3, 9, 96
+    g = gen(21)
+    ids0 = torch.randint(-1, e, (n, k), generator=g, device="cuda")
+    base = rows(g, n, d, torch.float32)
+    host = torch.randn(n, d).pin_memory()
+
+    def run(wait):
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        x, h, xs = torch.empty_like(base), torch.empty_like(base), torch.empty((n * k, d), device="cuda")
+        ids, y, out = torch.empty_like(ids0), torch.empty_like(base), []
+        w = torch.full((n, k), 1.0 / k, device="cuda")
+        order, pos = (torch.empty(n * k, dtype=torch.int32, device="cuda") for _ in range(2))
+        off, norm = torch.empty(e + 1, dtype=torch.int32, device="cuda"), torch.empty(1, device="cuda")
+        dw = torch.empty(d, device="cuda")
+        for r in range(12):
+            steps = [
+                lambda: x.copy_(host, non_blocking=True),
+                lambda: x.add_(base * r),
+                lambda: E.gated_norm(x, None, None, h),
+                lambda: ids.copy_((ids0 + r) % (e + 1) - 1),
+                lambda: E.expert_sort(ids, e, order, pos, off),
+                lambda: E.expert_dispatch(h, pos, xs),
+                lambda: xs.mul_(1.5),
+                lambda: E.expert_combine(xs, pos, w, y),
+                lambda: E.gated_norm(x, y, x, h),
+                lambda: E.gated_norm_backward(x, h, x, y, x, y, dw_post=dw),
+                lambda: E.clip_grads([x, y, dw], 3.0, norm),
+                lambda: out.append(torch.cat([x.flatten(), y.flatten(), h.flatten(), dw, norm])),
+                lambda: x.zero_(),
+            ]
+            for s in steps:
+                s()
+                pause()
+        torch.cuda.synchronize()
+        return out
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
+
+
+def test_graph_with_other_work_and_streams(E):
+    """A captured step with copies, fills, torch kernels and a forked stream between the calls."""
+    g = gen(22)
+    n, d = 513, 120
+    src, x, h = rows(g, n, d, torch.bfloat16), torch.empty((n, d), dtype=torch.bfloat16, device="cuda"), torch.empty((n, d), dtype=torch.bfloat16, device="cuda")
+    z, dw, norm = torch.empty_like(h), torch.empty(d, device="cuda"), torch.empty(1, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        x.copy_(src)
+        E.gated_norm(x, None, None, h)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            z.copy_(h)
+            E.gated_norm(z, src, z, None)
+        dw.zero_()
+        E.gated_norm_backward(x, h, x, None, x, None, dw_pre=dw)
+        torch.cuda.current_stream().wait_stream(side)
+        E.clip_grads([x, z, dw], 0.5, norm)
+        x.add_(z)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    src.copy_(rows(g, n, d, torch.bfloat16))
+    graph.replay()
+    got = [v.clone() for v in (x, z, h, dw, norm)]
+    step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (x, z, h, dw, norm)))
