@@ -331,10 +331,12 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
 }
 
 // ---- rows to and from their sorted places ----
-// A task is a row, or a part of one: `lanes` neighbouring threads (32, fewer for rows of fewer
-// units), each with UN units of the row `lanes` apart, all loaded before the first is used.  A
-// unit is 16 bytes where every row start and the row length are multiples of 16, else 4 or 2:
-// the row's addresses are worked out once a task, so that narrow units cost little more.
+// A task is a row, or a part of one: `lanes` neighbouring threads (a power of two, up to 32), each
+// with UN units of the row `lanes` apart, all loaded before the first is used.  A unit is 16
+// bytes where every row start and the row length are multiples of 16, else 4 or 2: the row's
+// addresses are worked out once a task, so that narrow units cost little more.  Narrow rows
+// take few threads (but a 32-byte sector's worth) with several units each, so that a warp has
+// several rows in flight; with too few rows to fill the device that way, more threads.
 constexpr int kMoveThreads = 256;
 
 struct MoveShape {
@@ -343,10 +345,13 @@ struct MoveShape {
   FastDiv segs;         // tasks of a row
 };
 
-// The largest UN (a power of two, at most `most`) that a row fills, and the shape for it.
-static int move_shape(MoveShape& m, int64_t n, int units, int most) {
-  m.n = (uint32_t)n, m.U = units, m.lanes = 32, m.shift = 5;
-  while (m.lanes > 1 && m.lanes / 2 >= units) m.lanes /= 2, --m.shift;
+// UN (a power of two, at most `most`) and the shape for it.
+static int move_shape(MoveShape& m, int64_t n, int units, int unit_bytes, int most) {
+  const int64_t enough = (int64_t)device_sms() * 1024;
+  m.n = (uint32_t)n, m.U = units, m.lanes = unit_bytes < 32 ? 32 / unit_bytes : 1, m.shift = 0;
+  while (m.lanes > 1 && m.lanes / 2 >= units) m.lanes /= 2;
+  while (m.lanes < 32 && m.lanes < units && (m.lanes * most < units || n * m.lanes < enough)) m.lanes *= 2;
+  while ((1 << m.shift) < m.lanes) ++m.shift;
   int un = 1;
   while (un < most && un * m.lanes < units) un *= 2;
   m.segs = FastDiv((uint32_t)((units + un * m.lanes - 1) / (un * m.lanes)));
@@ -420,17 +425,17 @@ template <int UB>
 static cudaError_t dispatch_units(const void* x, uint32_t x_st, const int32_t* pos, int64_t n, int k,
                            int row, void* xs, uint32_t xs_st, cudaStream_t s) {
   MoveShape m;
-  const int un = move_shape(m, n, row / UB, 8);
+  const int un = move_shape(m, n, row / UB, UB, UB == 16 ? 2 : 8);
   const unsigned grid = move_grid(m);
   const char* in = static_cast<const char*>(x);
   char* out = static_cast<char*>(xs);
   const auto run = [&](auto kern) {
     return launch_early(kern, grid, kMoveThreads, 0, s, in, x_st, pos, k, m, out, xs_st);
   };
-  return un == 1   ? run(k_expert_dispatch<UB, 1>)
-         : un == 2 ? run(k_expert_dispatch<UB, 2>)
-         : un == 4 ? run(k_expert_dispatch<UB, 4>)
-                   : run(k_expert_dispatch<UB, 8>);
+  if (un == 1) return run(k_expert_dispatch<UB, 1>);
+  if constexpr (UB < 16)
+    if (un >= 4) return un == 4 ? run(k_expert_dispatch<UB, 4>) : run(k_expert_dispatch<UB, 8>);
+  return run(k_expert_dispatch<UB, 2>);
 }
 
 cudaError_t launch_expert_dispatch(const void* x, int64_t x_ld, const int32_t* pos, int64_t n, int k,
@@ -520,7 +525,7 @@ template <typename T, int EPU>
 static cudaError_t combine_units(const void* ys, uint32_t ys_st, const int32_t* pos, const float* w,
                                  int64_t n, int k, int dim, void* out, uint32_t out_st, cudaStream_t s) {
   MoveShape m;
-  const int un = move_shape(m, n, dim / EPU, EPU > 2 ? 2 : 8 / EPU);
+  const int un = move_shape(m, n, dim / EPU, EPU * (int)sizeof(T), EPU > 2 ? 2 : 8 / EPU);
   const T* y = static_cast<const T*>(ys);
   T* o = static_cast<T*>(out);
   const auto run = [&](auto unc) {
@@ -656,11 +661,12 @@ static cudaError_t combine_bwd_units(const void* dout, uint32_t dout_st, const v
                               const int32_t* pos, const float* w, int64_t n, int k, int dim,
                               void* dys, uint32_t dys_st, float* dw, cudaStream_t s) {
   const int U = dim / EPU;
+  // threads of a row: so many that UN units each cover it, up to a warp, and more while that leaves
+  // under 32 warps an SM (up to a CTA) and the row has units for them
+  const int64_t enough = (int64_t)device_sms() * 32 * 32;
+  const int un = k == 1 ? 4 : k == 2 || (k <= 4 && EPU <= 2) ? 2 : 1;
   int shift = 0;
-  while ((1 << shift) < U && shift < 5) ++shift;
-  // more threads a row while that leaves under 16 warps an SM and the row has units for them
-  const int64_t enough = (int64_t)device_sms() * 16 * 32;
-  while (shift >= 5 && shift < 8 && (n << shift) < enough && (1 << shift) < U) ++shift;
+  while ((1 << shift) < U && ((shift < 5 && (un << shift) < U) || (shift < 8 && (n << shift) < enough))) ++shift;
   const unsigned grid = (unsigned)(((n << shift) + kCombThreads - 1) / kCombThreads);
   const auto run = [&](auto kern) {
     return launch_early(kern, grid, kCombThreads, 0, s, static_cast<const T*>(dout), dout_st,

@@ -35,6 +35,13 @@ struct Pack<__nv_bfloat16, 1> {
 };
 
 template <>
+struct Pack<float, 2> {
+  float2 r;
+  __device__ __forceinline__ void set(const float (&v)[2]) { r = make_float2(v[0], v[1]); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float2*>(p) = r; }
+};
+
+template <>
 struct Pack<float, 4> {
   float4 r;
   __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
