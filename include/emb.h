@@ -374,6 +374,7 @@ typedef struct emb_norm {
 } emb_norm;
 emb_status emb_gated_norm(const emb_norm* args, void* stream);
 int64_t emb_gated_norm_backward_workspace(int64_t n, int32_t dim);
+int32_t emb_gated_norm_backward_one_launch(int64_t n, int32_t dim);
 emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_bytes,
                                    void* stream);
 

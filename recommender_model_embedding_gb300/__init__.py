@@ -108,6 +108,7 @@ _SIGS = {
                                      _P, _P], ctypes.c_int),
     "emb_gated_norm": ([ctypes.POINTER(EmbNorm), _P], ctypes.c_int),
     "emb_gated_norm_backward_workspace": ([_I64, _I32], _I64),
+    "emb_gated_norm_backward_one_launch": ([_I64, _I32], _I32),
     "emb_gated_norm_backward": ([ctypes.POINTER(EmbNorm), _P, _I64, _P], ctypes.c_int),
     "emb_clip_grads_workspace": ([_I64], _I64),
     "emb_clip_grads": ([ctypes.POINTER(EmbTensor), _I64, ctypes.c_float, _P, _P, _I64, _P], ctypes.c_int),

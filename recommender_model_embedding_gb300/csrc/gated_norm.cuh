@@ -26,7 +26,7 @@
 // over the row, since only dy needs the second row sum: it keeps u in registers and y in the
 // ring.  A thread has the same columns for all its rows, so the column sums stay in its
 // registers until the end, when they go to the workspace and a second launch adds the CTAs'
-// parts in a fixed order.
+// parts in a fixed order (few rows: a cluster's CTAs add them in shared memory, in one launch).
 #pragma once
 
 #include "rows_common.cuh"
@@ -49,7 +49,10 @@ struct NormArgs {
   uint32_t x_st, y_st, gate_st, dx_out_st, dh_st, x_out_st, h_st, dx_st, dy_st, dgate_st;  // bytes
   const float *w_post, *res_scale, *w_pre;
   float *dw_post, *dres_scale, *dw_pre;
-  float* part;  // [CTAs][2][dim] column sums (backward)
+  // backward: [CTAs][2][dim] column sums; whether any vector's gradient is asked for; CTAs of the
+  // cluster that adds them up itself (0: none)
+  float* part;
+  int cols, cluster;
 };
 
 // ---- arithmetic on N elements a thread: two at a time (fp32 pairs) where N is even ----

@@ -277,15 +277,7 @@ static cudaError_t clip_cluster(const ClipList<N>& l, float max_norm, float* nor
   constexpr auto kern = k_clip_cluster<N>;
   const cudaError_t e = prepare_kernel<kern, true>();
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kClusterCtas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kClusterCtas), cfg.blockDim = dim3(kClusterThreads);
-  cfg.stream = s, cfg.attrs = attr, cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, l, max_norm, norm, inplace);
+  return launch_early_cluster(kern, kClusterCtas, kClusterThreads, 0, s, l, max_norm, norm, inplace);
 }
 
 template <int N>

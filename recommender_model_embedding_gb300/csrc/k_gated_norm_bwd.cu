@@ -157,15 +157,15 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
     st = st == last ? 0 : st + stage_bytes;
   }
   ring_wait_n<0>();
+  if (!a.cols) return;
   // the CTA's column sums: a warp's groups by shuffles, then the slices (warps, or groups of whole
   // warps) side by side in shared memory
   const int slices = tpr < 32 ? (int)blockDim.x / 32 : a.rpb;
   const int slice = tpr < 32 ? (int)threadIdx.x / 32 : grp.id;
   const bool writes = tpr >= 32 || (int)(threadIdx.x & 31) < tpr;
-  float* cols = reinterpret_cast<float*>(ring);  // [slices][2][dim], when there are several
-  float* out = a.part + (int64_t)blockIdx.x * 2 * a.dim;
-  const bool alone = gridDim.x == 1;  // then there is nothing to add: the results themselves
-  __syncthreads();  // the ring has been read
+  float* cols = reinterpret_cast<float*>(ring);  // [slices][2][dim]; a single slice is the CTA's sums
+  float* sums = slices > 1 ? cols + slices * 2 * a.dim : cols;  // [2][dim]
+  __syncthreads();                                              // the ring has been read
 #pragma unroll
   for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -179,23 +179,42 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
         }
       if (writes && sh.step(i) < left) {
         const int k = (sh.first + sh.step(i)) * EPU + m;
-        if (slices > 1) cols[slice * 2 * a.dim + k] = p, cols[(slice * 2 + 1) * a.dim + k] = q;
-        else if (alone) put_cols(a, k, p, q);
-        else out[k] = p, out[a.dim + k] = q;
+        cols[slice * 2 * a.dim + k] = p, cols[(slice * 2 + 1) * a.dim + k] = q;
       }
     }
   }
-  if (slices == 1) return;
   __syncthreads();
-  for (int k = threadIdx.x; k < a.dim; k += blockDim.x) {
+  // where they go: the workspace; the results, if there is one CTA; or, in a cluster, shared memory,
+  // from which each of its CTAs adds up some of the columns
+  float* out = a.part + (int64_t)blockIdx.x * 2 * a.dim;
+  if (slices > 1 || !a.cluster || gridDim.x == 1)
+    for (int k = threadIdx.x; k < a.dim; k += blockDim.x) {
+      float p = cols[k], q = cols[a.dim + k];
+      for (int r = 1; r < slices; ++r) p += cols[r * 2 * a.dim + k], q += cols[(r * 2 + 1) * a.dim + k];
+      if (gridDim.x == 1) put_cols(a, k, p, q);
+      else if (a.cluster) sums[k] = p, sums[a.dim + k] = q;
+      else out[k] = p, out[a.dim + k] = q;
+    }
+  if (!a.cluster || gridDim.x == 1) return;
+  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+  const uint32_t here = smem_at(sums);
+  for (int k = blockIdx.x * blockDim.x + threadIdx.x; k < a.dim; k += gridDim.x * blockDim.x) {
     float p = 0.f, q = 0.f;
-    for (int r = 0; r < slices; ++r) p += cols[r * 2 * a.dim + k], q += cols[(r * 2 + 1) * a.dim + k];
-    if (alone) put_cols(a, k, p, q);
-    else out[k] = p, out[a.dim + k] = q;
+    for (uint32_t r = 0; r < gridDim.x; ++r) {
+      uint32_t there;
+      float c, d;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(r));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(c) : "r"(there + k * 4) : "memory");
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(d) : "r"(there + (a.dim + k) * 4) : "memory");
+      p += c, q += d;
+    }
+    put_cols(a, k, p, q);
   }
+  // every CTA's sums have been read before it may leave
+  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Sums the CTAs' parts: 32 columns a CTA, 32 threads a column over interleaved parts, then over
+// Sums the CTAs' parts (none: zeros): 32 columns a CTA, 32 threads a column over interleaved parts, then over
 // the 32 in order.
 __global__ void __launch_bounds__(1024) k_gated_norm_cols(NormArgs a, int parts) {
   __shared__ float sh[2][32][33];
@@ -228,15 +247,27 @@ __global__ void __launch_bounds__(1024) k_gated_norm_cols(NormArgs a, int parts)
   }
 }
 
-// CTAs of the backward: a row a group up to one CTA an SM, then at least four rows a group up to
-// `cap`, so that the column parts stay small beside the rows.
+// Few rows take one launch: a cluster of up to 16 CTAs, whose column sums meet in shared memory,
+// with up to kNormRounds rows a group.  Otherwise a row a group up to one CTA an SM, then at least
+// four rows a group up to `cap`, so that the column parts stay small beside the rows.
+constexpr int kNormCluster = 16, kNormRounds = 6;
+constexpr int kNormCtasPerSm = 3;  // CTAs per SM, at most (wide rows: 160 threads and more)
+
+static int64_t norm_blocks(int64_t n, int rpb) { return (n + rpb - 1) / rpb; }
+
+static int norm_cluster(int64_t n, int rpb) {  // CTAs of the cluster; 0: too many rows
+  const int64_t blocks = norm_blocks(n, rpb);
+  if (blocks > kNormCluster * kNormRounds) return 0;
+  int c = 1;
+  while (c < kNormCluster && c < blocks) c *= 2;
+  return c;
+}
+
 static int64_t norm_bwd_grid(int64_t n, int rpb, int64_t cap) {
-  const int64_t sms = device_sms(), all = (n + rpb - 1) / rpb, four = (n + 4 * rpb - 1) / (4 * rpb);
+  const int64_t sms = device_sms(), all = norm_blocks(n, rpb), four = (n + 4 * rpb - 1) / (4 * rpb);
   const int64_t blocks = all <= sms ? all : four > sms ? four : sms;
   return blocks < 1 ? 1 : blocks < cap ? blocks : cap;
 }
-
-constexpr int kNormCtasPerSm = 3;  // CTAs of the backward per SM, at most (wide rows: 160 threads and more)
 
 int64_t gated_norm_bwd_workspace(int64_t n, int dim) {
   NormArgs a{};
@@ -245,34 +276,50 @@ int64_t gated_norm_bwd_workspace(int64_t n, int dim) {
   return norm_bwd_grid(n, a.rpb, (int64_t)device_sms() * kNormCtasPerSm) * 2 * dim * (int64_t)sizeof(float);
 }
 
+bool gated_norm_bwd_one_launch(int64_t n, int dim) {
+  NormArgs a{};
+  a.dim = dim;
+  norm_shape(a, 1);
+  return norm_cluster(n, a.rpb) > 0;
+}
+
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
-static cudaError_t norm_bwd_v(NormArgs& a, int* grid, cudaStream_t s) {
+static cudaError_t norm_bwd_v(NormArgs& a, int* parts, cudaStream_t s) {
   const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : kNormCtasPerSm;
   int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>, per, V * EPU > 8 ? a.tpr * 128 : 0);
   const int slices = a.tpr < 32 ? threads / 32 : a.rpb;
-  const int cols = slices > 1 ? slices * 2 * a.dim * (int)sizeof(float) : 0;
+  const int cols = (slices > 1 ? slices + 1 : 1) * 2 * a.dim * (int)sizeof(float);
   if (smem < cols) smem = cols;
   constexpr auto kern = k_gated_norm_bwd<XT, BT, EPU, V, GATE, WARP>;
-  const cudaError_t e = prepare_kernel<kern>();
+  const cudaError_t e = prepare_kernel<kern, true>();
   if (e != cudaSuccess) return e;
-  *grid = (int)norm_bwd_grid(a.n, a.rpb, (int64_t)device_sms() * norm_fit(per, smem));
-  return launch_early(kern, (unsigned)*grid, threads, smem, s, a);
+  a.cluster = a.cols ? norm_cluster(a.n, a.rpb) : 0;
+  if (a.cluster > 1) return launch_early_cluster(kern, (unsigned)a.cluster, threads, smem, s, a);
+  const unsigned grid =
+      a.cluster ? 1u : (unsigned)norm_bwd_grid(a.n, a.rpb, (int64_t)device_sms() * norm_fit(per, smem));
+  if (a.cols && grid > 1) *parts = (int)grid;
+  return launch_early(kern, grid, threads, smem, s, a);
 }
 
 struct NormBackward {
   cudaStream_t s;
-  int* grid;
+  int* parts;  // CTAs whose column sums are in the workspace (0: none to add)
   template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
-  cudaError_t run(NormArgs& a) const { return norm_bwd_v<XT, BT, EPU, V, GATE, WARP>(a, grid, s); }
+  cudaError_t run(NormArgs& a) const { return norm_bwd_v<XT, BT, EPU, V, GATE, WARP>(a, parts, s); }
 };
 
 cudaError_t launch_gated_norm_bwd(const emb_norm& p, void* ws, cudaStream_t s) {
   NormArgs a = norm_args(p);
   a.part = static_cast<float*>(ws);
-  int grid = 0;
-  cudaError_t e = p.n > 0 ? norm_call(p, a, NormBackward{s, &grid}) : cudaSuccess;
-  if (e != cudaSuccess || grid == 1 || !(p.d_dw_post || p.d_dres_scale || p.d_dw_pre)) return e;
-  return launch_early(k_gated_norm_cols, (p.dim + 31) / 32, 1024, 0, s, a, grid);
+  a.cols = p.d_dw_post || p.d_dres_scale || p.d_dw_pre;
+  int parts = 0;
+  if (p.n > 0) {
+    const cudaError_t e = norm_call(p, a, NormBackward{s, &parts});
+    if (e != cudaSuccess || parts == 0) return e;
+  } else if (!a.cols) {
+    return cudaSuccess;
+  }
+  return launch_early(k_gated_norm_cols, (p.dim + 31) / 32, 1024, 0, s, a, parts);
 }
 
 }  // namespace emb

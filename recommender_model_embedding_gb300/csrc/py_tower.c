@@ -428,7 +428,10 @@ static PyObject* py_norm_backward(PyObject* self, PyObject* const* a, Py_ssize_t
   p.d_dw_post = u, p.d_dres_scale = v, p.d_dw_pre = w;
   p.eps = (float)PyFloat_AsDouble(a[14]);
   if (PyErr_Occurred() ||
-      !workspace(emb_gated_norm_backward_workspace(p.n, p.dim), a[15], a[16], a[2], &keep, &ws, &have))
+      !workspace(a[15] == Py_None && emb_gated_norm_backward_one_launch(p.n, p.dim)
+                     ? 0
+                     : emb_gated_norm_backward_workspace(p.n, p.dim),
+                 a[15], a[16], a[2], &keep, &ws, &have))
     return NULL;
   if (!on(a[16], a[2], &s)) {
     Py_XDECREF(keep);

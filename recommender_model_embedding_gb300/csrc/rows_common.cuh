@@ -165,6 +165,21 @@ cudaError_t launch_early(void (*kern)(P...), unsigned grid, int threads, int sme
   return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
 }
 
+// The same for a grid that is one cluster of `grid` CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_early_cluster(void (*kern)(P...), unsigned grid, int threads, int smem,
+                                 cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = grid, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem, cfg.stream = s, cfg.attrs = attr, cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+}
+
 // Multiprocessors of the current device (context-free calls; the count is read once a device).
 inline int device_sms() {
   constexpr int kDevices = 64;
