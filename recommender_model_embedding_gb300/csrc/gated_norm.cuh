@@ -274,11 +274,24 @@ struct ColWeights {
   uint32_t at;  // kShared: the shared copy
   __device__ __forceinline__ void init(const NormArgs& a, const Share<V, WARP>& sh, float* shared) {
     if constexpr (kShared) {
-      const int n = a.tpr * K::EPT;
-      for (int k = threadIdx.x; k < n; k += blockDim.x) {
-        const bool in = k < a.dim;
-        shared[k] = in ? (a.w_post ? a.w_post[k] : 1.f) * (a.res_scale ? a.res_scale[k] : 1.f) : 0.f;
-        shared[n + k] = in ? (a.w_pre ? a.w_pre[k] : 1.f) : 0.f;
+      const int n = a.tpr * K::EPT;  // a row a CTA: EPT columns a thread
+#pragma unroll
+      for (int j0 = 0; j0 < K::EPT; j0 += 8) {
+        float wp[8], rs[8], wn[8];  // loaded together
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int k = threadIdx.x + (j0 + j) * a.tpr;
+          const bool in = k < a.dim;
+          wp[j] = in ? a.w_post ? __ldg(a.w_post + k) : 1.f : 0.f;
+          rs[j] = in ? a.res_scale ? __ldg(a.res_scale + k) : 1.f : 0.f;
+          wn[j] = in ? a.w_pre ? __ldg(a.w_pre + k) : 1.f : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int k = threadIdx.x + (j0 + j) * a.tpr;
+          shared[k] = wp[j] * rs[j];
+          shared[n + k] = wn[j];
+        }
       }
       at = (uint32_t)__cvta_generic_to_shared(shared + sh.first * EPU);
     } else {

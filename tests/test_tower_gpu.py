@@ -714,3 +714,47 @@ def test_graph_with_other_work_and_streams(E):
     step()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, (x, z, h, dw, norm)))
+
+
+@pytest.mark.parametrize("n,k,e", [
+    (2048, 1, 9), (2049, 1, 9), (4096, 1, 1024), (4097, 1, 1024), (1025, 16, 300), (32768, 2, 64),
+    (32769, 2, 64), (20000, 16, 128), (155648, 8, 255), (155649, 8, 256), (1_100_000, 8, 40),
+    (1_100_000, 8, 900)])
+def test_sort_where_its_launches_change(E, n, k, e):
+    """Sizes on either side of one CTA of few warps, one CTA, a cluster, two launches and three, and
+    chunks too large for registers."""
+    g = gen(n + e)
+    ids = torch.randint(0, e, (n, k), generator=g, device="cuda")
+    ids = ids.masked_fill(torch.rand((n, k), generator=g, device="cuda") < 0.1, -1)
+    ids[: n // 3] = ids[: n // 3] % 3  # a few crowded experts
+    check_sort(E, ids, e)
+
+
+@pytest.mark.parametrize("n,d", [(1, 64), (95 * 32, 64), (97 * 32, 64), (16 * 6 * 2, 1024), (16 * 6 * 2 + 1, 1024),
+                                 (96, 8192), (97, 8192)])
+def test_gated_norm_backward_where_its_launches_change(E, n, d):
+    """Rows on either side of what one cluster takes, with and without the vectors' gradients."""
+    s = norm_case(n, d, "full", torch.float32, torch.bfloat16, 0, 0, n)
+    ref, got = norm_grad_ref(s, 1e-6), norm_grad(E, s, 1e-6)
+    for k, v in got.items():
+        within(v, *ref[k], k)
+    for k, v in norm_grad(E, s, 1e-6, names=("dx", "dy")).items():
+        assert v is None or torch.equal(v, got[k]), k
+    ws = torch.empty(max(16, E.gated_norm_backward_workspace(n, d)), dtype=torch.uint8, device="cuda")
+    for k, v in norm_grad(E, s, 1e-6, workspace=ws).items():
+        assert torch.equal(v, got[k]), k
+
+
+@pytest.mark.parametrize("total,count", [(1048576, 3), (1048577, 3), (5000, 256), (5000, 257)])
+def test_clip_where_its_launches_change(E, total, count):
+    """Lists on either side of what one launch takes, by elements and by tensors."""
+    g = gen(count)
+    cut = sorted(torch.randint(0, total + 1, (count - 1,), generator=g, device="cuda").tolist())
+    sizes = [b - a for a, b in zip([0] + cut, cut + [total])]
+    grads = [torch.randn(m, generator=g, device="cuda") for m in sizes]
+    norm, out = torch.empty(1, device="cuda"), [torch.empty_like(x) for x in grads]
+    E.clip_grads(grads, 2.0, norm, out=out)
+    ref, c = clip_ref(grads, 2.0)
+    assert abs(norm.item() - ref) <= 20 * U32 * ref
+    for x, o in zip(grads, out):
+        within(o, x.double() * c, 24 * U32 * c * x.double().abs(), "out")
