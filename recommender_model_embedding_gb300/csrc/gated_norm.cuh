@@ -15,27 +15,39 @@
 //   dw_pre = sum over rows of dh * q;   with T = sum over rows of t * g * a:
 //   dw_post = res_scale * T, dres_scale = w_post * T
 //
-// Both are bound by HBM bandwidth.  A group of `tpr` threads takes a row, about eight elements a
-// thread (V packs of EPU: 16 bytes a pack where everything is aligned, else 4 or an element;
-// with an fp32 stream beside bf16 blocks 4 elements, 16 and 8 bytes, so that neighbouring
-// threads' accesses of either type are neighbours in memory), so a row costs each thread few shuffles per element.  CTAs are persistent; every thread
-// copies its own packs of the next rows to shared memory asynchronously, kStages rows ahead,
-// and reads back only what it copied itself, so the ring needs no barrier; the groups of
-// a CTA run independently of each other (named barriers for the row sums, and only for rows
-// of more than 32 threads).  The backward computes everything but dy in one sweep
-// over the row, since only dy needs the second row sum: it keeps u in registers and y in the
-// ring.  A thread has the same columns for all its rows, so the column sums stay in its
-// registers until the end, when they go to the workspace and a second launch adds the CTAs'
-// parts in a fixed order (few rows: a cluster's CTAs add them in shared memory, in one launch).
+// Both are bound by HBM bandwidth while the elements are wide enough, and then by instruction
+// issue: the forward takes about 300 warp instructions a warp's share of a row (8 elements a
+// thread), the backward 530.  Measured with a gate for each element, 262144 x 1024: forward with
+// an fp32 stream and bf16 blocks 3.76 GB in 0.552 ms (6.80 TB/s, the measured copy rate), backward
+// all in bf16 4.29 GB in 0.67 ms (6.40 TB/s, 94%); without the gate's bytes the bf16 backward
+// stays issue-bound (59% at 65536 x 2048, one gate a row; fp32 there 93%).
+//
+// A group of `tpr` threads takes a row, about eight elements a thread (V packs of EPU: 16 bytes
+// a pack where everything is aligned, else 4 or one element; with an fp32 stream beside bf16
+// blocks 4 elements, 16 and 8 bytes, so that neighbouring threads' accesses of either type are
+// neighbours in memory: with 8, half-filled sectors took 0.72 ms, not 0.57), so a row costs each
+// thread few shuffles per element.  CTAs are persistent; every thread copies its own packs of
+// the next rows to shared memory asynchronously, up to two rows ahead, and reads back only what
+// it copied itself, so the ring needs no barrier (rows loaded straight to registers: 2.88 ms
+// backward, 1.17 ms forward); the groups of a CTA run independently of each other (named
+// barriers for the row sums, and only for rows of more than 32 threads).  Packs past the row's
+// end are zero in the ring, which takes the place of masks.  The backward computes everything
+// but dy in one sweep over the row, since only dy needs the second row sum: it keeps u in
+// registers and y in the ring.  A thread has the same columns for all its rows, so the column
+// sums stay in its registers until the end, when they go to the workspace and a second launch
+// adds the CTAs' parts in a fixed order (few rows: a cluster's CTAs add them in shared
+// memory, in one launch; 16 rows of 1024: 6.3 us, 8.2 in two).
 #pragma once
 
 #include "rows_common.cuh"
 
 namespace emb {
 
-constexpr int kNormThreads = 256;  // of a CTA (8 elements a thread)
-constexpr int kNormWide = 512;     // of a CTA whose rows take 16 elements a thread, at most
-constexpr int kStages = 3;            // rows of the ring
+// Threads: a CTA of narrow rows has 256.  A row has 8 elements a thread while that takes up to
+// kNormForward or kNormBackward threads (two such CTAs fill an SM's registers, 64 and 80 a
+// thread), 16 above.
+constexpr int kNormThreads = 256, kNormForward = 512, kNormBackward = 384, kNormWide = 512;
+constexpr int kStages = 3;  // rows of the ring
 
 struct NormArgs {
   uint32_t n;
@@ -109,9 +121,11 @@ __device__ __forceinline__ void v_dot(float (&s)[2], const float (&a)[N], const 
 }
 
 // g = sigmoid(z) = 1 / (1 + e) and rest = 1 - g, with e = exp(-z), both to a few units in the
-// last place: rest is taken as e g where that difference would cancel (z >= 0).
+// last place for moderate z: rest is taken as e g where that difference would cancel (z >= 0).
+// The fast exponential and reciprocal stand in for the exact ones, whose instructions bounded the
+// backward; the rounding of the exponent's product moves e by up to about |z| 2^-24 of itself.
 __device__ __forceinline__ void sigmoid2(float z, float& g, float& rest) {
-  float e;  // the product's rounding moves e by less than |z| units, where e is at most that small
+  float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(1.f + e));
   rest = z < 0.f ? 1.f - g : e * g;
@@ -416,11 +430,11 @@ struct RowGate {
 
 // ---- host ----
 
-// Threads of a row: for 8 elements each (16 in rows of more than 2048), a power of two up to a
-// warp, whole warps above.
-inline void norm_shape(NormArgs& a, int epu) {
+// Threads of a row: for 8 elements each while that is at most `most` threads, else 16; a power of
+// two up to a warp, whole warps above.
+inline void norm_shape(NormArgs& a, int epu, int most) {
   a.packs = a.dim / epu;
-  const int each = a.dim > 8 * kNormThreads ? 16 : 8, want = (a.dim + each - 1) / each;
+  const int each = a.dim > 8 * most ? 16 : 8, want = (a.dim + each - 1) / each;
   int t = 4;
   while (t < want && t < 32) t *= 2;
   if (want > 32) t = (want + 31) / 32 * 32;
@@ -486,7 +500,7 @@ inline bool norm_allows(const emb_norm& p, int epu) {
 // threads per row.  Rows of 16 elements a thread always take whole warps.
 template <typename Call, typename XT, typename BT, int EPU, int V = 1>
 cudaError_t norm_t(NormArgs& a, Call call) {
-  if constexpr (V == 1) norm_shape(a, EPU);
+  if constexpr (V == 1) norm_shape(a, EPU, Call::kMost);
   if constexpr (V * EPU < 16)
     if ((a.packs + a.tpr - 1) / a.tpr > V) return norm_t<Call, XT, BT, EPU, 2 * V>(a, call);
   const auto run = [&](auto gate, auto warp) {

@@ -10,7 +10,10 @@
 //
 // Everything is data movement, so every kernel walks the unsorted rows: x and dout are read once,
 // the sorted side is touched one whole row at a time through pos, and no output needs an atomic
-// (fixed order of summation: results repeat bit for bit).
+// (fixed order of summation: results repeat bit for bit).  Dispatch, combine and the gradients
+// are bound by HBM bandwidth.  Measured in bf16: dispatch 262144 x 4 rows of 512, 1.34 GB in
+// 193 us (6.95 TB/s), combine the same 1.34 GB in 206 us (6.5), its gradient 262144 x 2, 1.34 GB in
+// 208 us (6.4), dispatch's gradient 0.81 GB in 128 us (6.3).
 #include "rows_common.cuh"
 
 namespace emb {
@@ -24,12 +27,14 @@ namespace emb {
 // and places the slots.  A single chunk needs no first launch, and up to 16 chunks of 2048 slots
 // exchange their counts through the shared memory of a cluster (8192 slots: 5.8 us where two
 // launches take 8.3, and no workspace; 49,000 slots in chunks of 4096: 7.9 against 8.3, but the
-// kernels around it overlap less and sort, dispatch and combine together took 56 us, not 53).  Bound by latency, not bytes: a chunk is as short as one CTA an SM allows, a
-// warp loads the ids of eight groups of 32 slots at once, and where that is all of its part
-// (KEEP: chunks of up to 8192 slots) keys and ranks stay in registers from counting to placing
-// and the chunk is put in order in shared memory first, so that its places are written in runs.
-// Lanes with equal keys find each other by ballots over the key's bits: __match_any_sync, which
-// works through the distinct keys, took 29 us where this takes 23 (1M slots, 128 experts).
+// kernels around it overlap less: sort, dispatch and combine together took 56 us, not 53).
+// Bound by latency, not bytes (1M slots of 128 experts: 15 us, 2M of 64: 27): a chunk is as short
+// as one CTA an SM allows, a warp loads the ids of eight groups of 32 slots at once, and where
+// that is all of its part (KEEP: chunks of up to 8192 slots) keys and ranks stay in registers
+// from counting to placing and the chunk is put in order in shared memory first, so that its
+// places are written in runs.  Lanes with equal keys find each other by ballots over the key's
+// bits: __match_any_sync, which works through the distinct keys, took 29 us where this took 23
+// (1M slots of 128 experts, at that point).
 constexpr int kSortWarps = 32, kSortThreads = kSortWarps * 32;
 constexpr int kSortDepth = 8;       // groups of 32 ids a warp loads at once
 constexpr int kSortSingle = 4096;   // slots of one CTA alone, at most
@@ -375,8 +380,9 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
 // A task is a row, or a part of one: `lanes` neighbouring threads (a power of two, up to 32), each
 // with UN units of the row `lanes` apart, all loaded before the first is used.  A unit is 16
 // bytes where every row start and the row length are multiples of 16, else 4 or 2: the row's
-// addresses are worked out once a task, so that narrow units cost little more.  Narrow rows
-// take few threads (but a 32-byte sector's worth) with several units each, so that a warp has
+// addresses are worked out once a task, so that narrow units cost little more (rows of 479 fp32:
+// dispatch 34 -> 19 us, combine 54 -> 24 us for 16411 x 3 of them, against a division an
+// element).  Narrow rows take few threads (but a 32-byte sector's worth) with several units each, so that a warp has
 // several rows in flight; with too few rows to fill the device that way, more threads.
 constexpr int kMoveThreads = 256;
 

@@ -5,7 +5,7 @@ namespace emb {
 
 // GATE: a gate for each element.
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
-__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EPU > 8 ? 1 : 4) k_gated_norm(NormArgs a) {
+__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EPU > 8 ? 1 : 2) k_gated_norm(NormArgs a) {
   let_next_start();
   wait_for_earlier();
   using K = Chunks<EPU, V>;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EP
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
-  const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : 4;
+  const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : 2 * kNormForward / threads;
   const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>, per, V * EPU > 8 ? a.tpr * 128 : 0);
   constexpr auto kern = k_gated_norm<XT, BT, EPU, V, GATE, WARP>;
   const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = (int64_t)device_sms() * norm_fit(per, smem);
@@ -124,6 +124,7 @@ static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
 }
 
 struct NormForward {
+  static constexpr int kMost = kNormForward;
   cudaStream_t s;
   template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
   cudaError_t run(NormArgs& a) const { return norm_fwd_v<XT, BT, EPU, V, GATE, WARP>(a, s); }

@@ -5,7 +5,7 @@
 namespace emb {
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
-__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormThreads, V * EPU > 8 ? 1 : 3) k_gated_norm_bwd(NormArgs a) {
+__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormBackward, V * EPU > 8 ? 1 : 2) k_gated_norm_bwd(NormArgs a) {
   let_next_start();
   wait_for_earlier();
   using K = Chunks<EPU, V>;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(1024) k_gated_norm_cols(NormArgs a, int parts)
 // with up to kNormRounds rows a group.  Otherwise a row a group up to one CTA an SM, then at least
 // four rows a group up to `cap`, so that the column parts stay small beside the rows.
 constexpr int kNormCluster = 16, kNormRounds = 6;
-constexpr int kNormCtasPerSm = 3;  // CTAs per SM, at most (wide rows: 160 threads and more)
+constexpr int kNormCtasPerSm = 2 * kNormBackward / 160;  // at most (a CTA has at least 160 threads)
 
 static int64_t norm_blocks(int64_t n, int rpb) { return (n + rpb - 1) / rpb; }
 
@@ -272,20 +272,20 @@ static int64_t norm_bwd_grid(int64_t n, int rpb, int64_t cap) {
 int64_t gated_norm_bwd_workspace(int64_t n, int dim) {
   NormArgs a{};
   a.dim = dim;
-  norm_shape(a, 1);
+  norm_shape(a, 1, kNormBackward);
   return norm_bwd_grid(n, a.rpb, (int64_t)device_sms() * kNormCtasPerSm) * 2 * dim * (int64_t)sizeof(float);
 }
 
 bool gated_norm_bwd_one_launch(int64_t n, int dim) {
   NormArgs a{};
   a.dim = dim;
-  norm_shape(a, 1);
+  norm_shape(a, 1, kNormBackward);
   return norm_cluster(n, a.rpb) > 0;
 }
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_bwd_v(NormArgs& a, int* parts, cudaStream_t s) {
-  const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : kNormCtasPerSm;
+  const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : 2 * kNormBackward / threads;
   int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>, per, V * EPU > 8 ? a.tpr * 128 : 0);
   const int slices = a.tpr < 32 ? threads / 32 : a.rpb;
   const int cols = (slices > 1 ? slices + 1 : 1) * 2 * a.dim * (int)sizeof(float);
@@ -302,6 +302,7 @@ static cudaError_t norm_bwd_v(NormArgs& a, int* parts, cudaStream_t s) {
 }
 
 struct NormBackward {
+  static constexpr int kMost = kNormBackward;
   cudaStream_t s;
   int* parts;  // CTAs whose column sums are in the workspace (0: none to add)
   template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
