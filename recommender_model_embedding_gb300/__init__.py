@@ -1,7 +1,7 @@
 """GB300-native sparse embedding layer for DLRM-style recommenders.
 
 A thin binding over libemb.so, the CUDA library declared in include/emb.h: ctypes, and a small
-compiled module for the expert tower's calls (csrc/py_tower.c).  Every method marshals its
+compiled module for the expert tower's calls (csrc/py_tower.cpp).  Every method marshals its
 arguments (torch tensors -> device pointers, the current CUDA stream) and calls the C entry
 point of the same name; all arithmetic runs in the library's kernels.  There is no CPU path:
 if libemb.so is missing this package fails to import.
@@ -23,11 +23,25 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-try:
-    from . import _tower  # noqa: E402  (loads libemb.so too: the same library)
-except ImportError as _e:
-    raise ImportError(f"{_e}: build the library first (python "
-                      "recommender_model_embedding_gb300/build.py)") from _e
+TOWER_PATH = os.path.join(_HERE, "_tower.so")
+if not os.path.exists(TOWER_PATH):
+    raise ImportError(f"{TOWER_PATH} is missing: build the library first "
+                      "(python recommender_model_embedding_gb300/build.py)")
+
+
+class _LoadTower:
+    """Stands in for the compiled module of the tower's calls until the first of them: the module
+    needs torch, and the rest of the package imports without it."""
+
+    def __getattr__(self, name):
+        import importlib
+
+        import torch  # noqa: F401  (its libraries have to be there first)
+        # importing a submodule also puts it in this stand-in's place
+        return getattr(importlib.import_module(__name__ + "._tower"), name)
+
+
+_tower = _LoadTower()
 
 EMB_OK, EMB_EINVAL, EMB_ENOMEM, EMB_ESTATE, EMB_ECUDA = 0, 1, 2, 3, 4
 FLAG_ID_RANGE, FLAG_BAD_KEY, FLAG_TABLE_FULL, FLAG_BAD_OFFSETS = 0x1, 0x2, 0x4, 0x8
@@ -238,21 +252,6 @@ def _stream(stream) -> Optional[int]:
 # ---- expert tower (context-free; arguments are checked and passed on by the _tower module) ----
 EXPERT_MAX, EXPERT_MAX_K, EXPERT_MAX_DIM, NORM_MAX_DIM = 1024, 16, 65536, 8192
 CLIP_ONE_LAUNCH = 1048576
-
-
-def _current_stream(device: int) -> int:
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _new_workspace(need: int, stream, like):
-    """Workspace from torch's allocator, taken on the call's stream so that its memory is reused
-    in that stream's order."""
-    import torch
-    if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
 
 
 def expert_sort_workspace(n: int, k: int, num_experts: int) -> int:

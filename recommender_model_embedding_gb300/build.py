@@ -3,8 +3,8 @@
 Each .cu file under csrc/ is compiled to an object in parallel, then linked into a shared
 library next to this file.  The CUDA runtime is linked statically, so the library loads
 on a machine without a GPU (it only needs the driver when a call reaches the device).  The
-Python side of the expert tower's calls (csrc/py_tower.c) becomes _tower.so beside it, linked
-to the library.
+Python side of the expert tower's calls (csrc/py_tower.cpp, against torch's headers) becomes
+_tower.so beside it, linked to the library.
 """
 from __future__ import annotations
 
@@ -21,7 +21,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libemb.so")
-TOWER_SRC = os.path.join(CSRC, "py_tower.c")
+TOWER_SRC = os.path.join(CSRC, "py_tower.cpp")
+TOWER_OBJ = os.path.join(BUILD, "py_tower.o")
 TOWER = os.path.join(HERE, "_tower.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -41,6 +42,26 @@ def _flags(verbose: bool):
     return f
 
 
+def gxx() -> str:
+    return shutil.which("g++") or "g++"
+
+
+def torch_dirs(what: str):
+    """torch's include or lib directories (found without importing it)."""
+    import importlib.util
+    root = os.path.dirname(importlib.util.find_spec("torch").origin)
+    if what == "lib":
+        return [os.path.join(root, "lib")]
+    inc = os.path.join(root, "include")
+    return [inc, os.path.join(inc, "torch", "csrc", "api", "include")]
+
+
+def _tower_flags():
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    dirs = torch_dirs("include") + [cuda, sysconfig.get_paths()["include"]]
+    return ["-O2", "-std=c++17", "-fPIC", "-I" + os.path.join(ROOT, "include")] + [f"-isystem{d}" for d in dirs]
+
+
 def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
@@ -54,15 +75,17 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     todo = [(s, o) for s, o in zip(srcs, objs) if force or _stale(o, s)]
+    if force or _stale(TOWER_OBJ, TOWER_SRC):
+        todo.insert(0, (TOWER_SRC, TOWER_OBJ))
     nv = nvcc()
 
     def compile_one(so):
         s, o = so
         tmp = o + f".tmp{os.getpid()}"
-        cmd = [nv] + _flags(verbose) + ["-c", s, "-o", tmp]
+        cmd = ([nv] + _flags(verbose) if s != TOWER_SRC else [gxx()] + _tower_flags()) + ["-c", s, "-o", tmp]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(s)}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compiler failed on {os.path.basename(s)}:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, o)
         return r.stderr
 
@@ -77,14 +100,15 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link of libemb.so failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    if todo or force or _stale(TOWER, TOWER_SRC):
+    if todo or force or not os.path.exists(TOWER):  # relinked to the new library
         tmp = TOWER + f".tmp{os.getpid()}"
-        cmd = [shutil.which("gcc") or "gcc", "-O2", "-Wall", "-shared", "-fPIC", TOWER_SRC, "-o", tmp,
-               "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"),
-               "-L" + HERE, "-l:libemb.so", "-Wl,-rpath,$ORIGIN"]
+        cmd = [gxx(), "-shared", TOWER_OBJ, "-o", tmp, "-L" + HERE, "-l:libemb.so", "-Wl,-rpath,$ORIGIN"]
+        for d in torch_dirs("lib"):
+            cmd += ["-L" + d, "-Wl,-rpath," + d]
+        cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"build of _tower.so failed:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"link of _tower.so failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, TOWER)
     if verbose:
         for l in logs:

@@ -1,0 +1,463 @@
+// Python side of the expert-tower calls: tensors are checked and their addresses handed to the C
+// entry points of libemb.so.
+//
+// The kernels behind a small call run for a few microseconds, so the host's share of the call is
+// what a caller waits for.  Read from Python with ctypes, the arguments of one call cost about
+// as much as its launch; read from the tensor object itself they cost next to nothing.  Objects
+// that are not torch's own tensors are read through the same public attributes (dtype, shape,
+// stride(), data_ptr(), ...).  Every check comes before the library is called: a mismatch raises
+// ValueError, a status of the library the package's EmbError.
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include <exception>
+#include <vector>
+
+#include "emb.h"
+
+namespace {
+
+enum Kind { F32, BF16, I32, I64, OTHER };
+const char* const kKindNames[] = {"float32", "bfloat16", "int32", "int64", "another type (float16, say)"};
+constexpr const char* kPackage = "recommender_model_embedding_gb300";
+
+// A Python exception is set; unwinds to the call's guard.
+struct Raised : std::exception {};
+
+template <typename... A>
+[[noreturn]] void refuse(const char* format, A... a) {
+  PyErr_Format(PyExc_ValueError, format, a...);
+  throw Raised();
+}
+
+struct Ref {  // an owned reference
+  PyObject* o;
+  explicit Ref(PyObject* p) : o(p) {
+    if (!o) throw Raised();
+  }
+  Ref(const Ref&) = delete;
+  Ref& operator=(const Ref&) = delete;
+  ~Ref() { Py_DECREF(o); }
+};
+
+int64_t number(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised();
+  return v;
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised();
+  return v;
+}
+
+// What the checks read of a tensor.
+struct Seen {
+  Kind kind = OTHER;
+  int64_t dims = 0, numel = 0, size[2] = {0, 0}, step[2] = {0, 0};
+  bool cuda = false, dense = false;
+  int device = -1;
+  void* p = nullptr;
+};
+
+Seen see_object(PyObject* o) {  // through attributes
+  Seen s;
+  const Ref dtype(PyObject_GetAttrString(o, "dtype"));
+  const Ref name(PyObject_Str(dtype.o));
+  const char* text = PyUnicode_AsUTF8(name.o);
+  if (!text) throw Raised();
+  for (int k = F32; k < OTHER; ++k)
+    if (std::string("torch.") + kKindNames[k] == text) s.kind = (Kind)k;
+  const Ref cuda(PyObject_GetAttrString(o, "is_cuda"));
+  s.cuda = truth(cuda.o);
+  const Ref shape(PyObject_GetAttrString(o, "shape"));
+  const Ref step(PyObject_CallMethod(o, "stride", nullptr));
+  s.dims = PySequence_Size(shape.o);
+  if (s.dims < 0) throw Raised();
+  if (s.dims == 2)
+    for (int i = 0; i < 2; ++i) {
+      const Ref a(PySequence_GetItem(shape.o, i)), b(PySequence_GetItem(step.o, i));
+      s.size[i] = number(a.o), s.step[i] = number(b.o);
+    }
+  const Ref numel(PyObject_CallMethod(o, "numel", nullptr)), dense(PyObject_CallMethod(o, "is_contiguous", nullptr));
+  s.numel = number(numel.o), s.dense = truth(dense.o);
+  const Ref p(PyObject_CallMethod(o, "data_ptr", nullptr));
+  s.p = PyLong_AsVoidPtr(p.o);
+  if (!s.p && PyErr_Occurred()) throw Raised();
+  return s;
+}
+
+Seen see(PyObject* o, const char* name) {
+  if (o == Py_None) refuse("%s: expected a CUDA tensor", name);
+  if (!THPVariable_CheckExact(o)) return see_object(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  Seen s;
+  if (t.layout() != c10::kStrided) refuse("%s: expected a dense tensor", name);
+  switch (t.scalar_type()) {
+    case at::kFloat: s.kind = F32; break;
+    case at::kBFloat16: s.kind = BF16; break;
+    case at::kInt: s.kind = I32; break;
+    case at::kLong: s.kind = I64; break;
+    default: break;
+  }
+  s.dims = t.dim(), s.numel = t.numel();
+  s.cuda = t.is_cuda(), s.dense = t.is_contiguous();
+  if (s.dims == 2)
+    for (int i = 0; i < 2; ++i) s.size[i] = t.size(i), s.step[i] = t.stride(i);
+  if (s.cuda) s.device = t.get_device(), s.p = t.data_ptr();
+  return s;
+}
+
+// EMB_F32 or EMB_BF16 of a matrix
+int32_t code_of(const Seen& s, const char* name) {
+  if (s.kind != F32 && s.kind != BF16) refuse("%s: expected float32 or bfloat16, got %s", name, kKindNames[s.kind]);
+  if (s.dims != 2) refuse("%s: expected a matrix", name);
+  return s.kind == BF16 ? EMB_BF16 : EMB_F32;
+}
+
+struct Rows {
+  void* p = nullptr;
+  int64_t ld = 0;
+};
+
+// a CUDA matrix [n, d] of the kind whose rows may lie any number of elements apart
+Rows rows(const Seen& s, Kind kind, int64_t n, int64_t d, const char* name) {
+  if (s.kind != kind) refuse("%s: expected dtype %s, got %s", name, kKindNames[kind], kKindNames[s.kind]);
+  if (!s.cuda) refuse("%s: expected a CUDA tensor", name);
+  if (s.dims != 2) refuse("%s: expected a matrix", name);
+  if (s.size[0] != n || s.size[1] != d)
+    refuse("%s: (%lld, %lld), expected (%lld, %lld)", name, (long long)s.size[0], (long long)s.size[1],
+           (long long)n, (long long)d);
+  if (s.step[1] != 1 && d > 1) refuse("%s: the elements of a row must be adjacent", name);
+  return {s.p, n > 1 ? s.step[0] : d};
+}
+
+Rows rows(PyObject* o, Kind kind, int64_t n, int64_t d, const char* name) {
+  return rows(see(o, name), kind, n, d, name);
+}
+
+Rows opt_rows(PyObject* o, Kind kind, int64_t n, int64_t d, const char* name) {
+  return o == Py_None ? Rows{} : rows(o, kind, n, d, name);
+}
+
+// a contiguous CUDA tensor of the kind and at least n elements (`exact`: of n)
+void* flat(const Seen& s, Kind kind, int64_t n, bool exact, const char* name) {
+  if (s.kind != kind) refuse("%s: expected dtype %s, got %s", name, kKindNames[kind], kKindNames[s.kind]);
+  if (!s.cuda || !s.dense) refuse("%s: expected a contiguous CUDA tensor", name);
+  if (s.numel < n || (exact && s.numel != n))
+    refuse("%s: %lld elements, %s%lld needed", name, (long long)s.numel, exact ? "" : "at least ", (long long)n);
+  return s.p;
+}
+
+void* flat(PyObject* o, Kind kind, int64_t n, const char* name) { return flat(see(o, name), kind, n, false, name); }
+
+void* vec(PyObject* o, int64_t d, const char* name) {  // optional float32 [d]
+  return o == Py_None ? nullptr : flat(see(o, name), F32, d, true, name);
+}
+
+int32_t fits_int(int64_t v, const char* name) {
+  if (v < 0 || v > INT32_MAX) refuse("%s: %lld is out of range", name, (long long)v);
+  return (int32_t)v;
+}
+
+// the call's stream: the given one, or the current one of the tensor's device
+void* stream_of(PyObject* stream, const Seen& like) {
+  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)like.device).stream();
+  const Ref o(PyObject_GetAttrString(stream, "cuda_stream"));
+  void* s = PyLong_AsVoidPtr(o.o);
+  if (!s && PyErr_Occurred()) throw Raised();
+  return s;
+}
+
+// The workspace of a call: the caller's (any contiguous CUDA tensor of enough bytes, checked at
+// once), or one that take() gets from torch's allocator for the call's stream, given back after
+// the call and reused in that stream's order.
+struct Workspace {
+  void* p = nullptr;
+  int64_t bytes = 0;
+  bool mine = false;
+  Workspace(int64_t need, PyObject* ws) {
+    if (need <= 0) return;
+    bytes = need;
+    mine = ws == Py_None;
+    if (mine) return;
+    const Seen s = see(ws, "workspace");
+    if (!s.cuda || !s.dense) refuse("workspace: expected a contiguous CUDA tensor");
+    const Ref size(PyObject_CallMethod(ws, "element_size", nullptr));
+    p = s.p, bytes = s.numel * number(size.o);
+    if (bytes < need) refuse("workspace: %lld bytes, at least %lld needed", (long long)bytes, (long long)need);
+  }
+  void take(void* stream) {
+    if (mine) p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream((size_t)bytes, (cudaStream_t)stream);
+  }
+  Workspace(const Workspace&) = delete;
+  Workspace& operator=(const Workspace&) = delete;
+  ~Workspace() {
+    if (mine && p) c10::cuda::CUDACachingAllocator::raw_delete(p);
+  }
+};
+
+// the library's call without the interpreter's lock; its status as an exception
+template <typename F>
+PyObject* call(const char* name, F f) {
+  emb_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = f();
+  Py_END_ALLOW_THREADS;
+  if (st != EMB_OK) {
+    const Ref pkg(PyImport_ImportModule(kPackage));
+    const Ref raised(PyObject_CallMethod(pkg.o, "_check", "si", name, (int)st));  // raises
+  }
+  Py_RETURN_NONE;
+}
+
+template <typename F>
+PyObject* guard(Py_ssize_t got, Py_ssize_t want, F f) {
+  try {
+    if (got != want) {
+      PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, got);
+      return nullptr;
+    }
+    return f();
+  } catch (const Raised&) {
+  } catch (const std::exception& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+// experts of a row: k of a pos with n * k places
+struct Places {
+  int32_t k;
+  const int32_t* p;
+};
+Places places(PyObject* pos, int64_t n) {
+  const Seen s = see(pos, "pos");
+  if (n == 0 ? s.numel != 0 : (s.numel == 0 || s.numel % n))
+    refuse("pos: %lld elements, expected a multiple of %lld rows", (long long)s.numel, (long long)n);
+  const int64_t k = n ? s.numel / n : 1;
+  return {fits_int(k, "pos"), static_cast<const int32_t*>(flat(s, I32, s.numel, false, "pos"))};
+}
+
+// (ids, num_experts, order, pos, offsets, workspace, stream)
+PyObject* py_sort(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 7, [&]() -> PyObject* {
+    const Seen ids = see(a[0], "ids");
+    if (ids.dims != 2) refuse("ids: expected a matrix [n, k]");
+    const int64_t n = ids.size[0], S = ids.numel;
+    const int32_t k = fits_int(ids.size[1], "ids"), E = fits_int(number(a[1]), "num_experts");
+    const auto* p = static_cast<const int64_t*>(flat(ids, I64, S, false, "ids"));
+    auto* order = static_cast<int32_t*>(flat(a[2], I32, S, "order"));
+    auto* pos = static_cast<int32_t*>(flat(a[3], I32, S, "pos"));
+    auto* offsets = static_cast<int32_t*>(flat(a[4], I32, (int64_t)E + 1, "offsets"));
+    Workspace ws(emb_expert_sort_workspace(n, k, E), a[5]);
+    void* s = stream_of(a[6], ids);
+    ws.take(s);
+    return call("emb_expert_sort", [&] { return emb_expert_sort(p, n, k, E, order, pos, offsets, ws.p, ws.bytes, s); });
+  });
+}
+
+// (x, pos, xs, stream)
+PyObject* py_dispatch(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 4, [&]() -> PyObject* {
+    const Seen m = see(a[0], "x");
+    const int32_t code = code_of(m, "x"), d = fits_int(m.size[1], "x");
+    const int64_t n = m.size[0];
+    const Places pos = places(a[1], n);
+    const Rows x = rows(m, m.kind, n, d, "x"), xs = rows(a[2], m.kind, n * pos.k, d, "xs");
+    void* s = stream_of(a[3], m);
+    return call("emb_expert_dispatch",
+                [&] { return emb_expert_dispatch(x.p, x.ld, pos.p, n, pos.k, d, code, xs.p, xs.ld, s); });
+  });
+}
+
+// (dxs, pos, dx, stream)
+PyObject* py_dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 4, [&]() -> PyObject* {
+    const Seen m = see(a[2], "dx");
+    const int32_t code = code_of(m, "dx"), d = fits_int(m.size[1], "dx");
+    const int64_t n = m.size[0];
+    const Places pos = places(a[1], n);
+    const Rows in = rows(a[0], m.kind, n * pos.k, d, "dxs"), out = rows(m, m.kind, n, d, "dx");
+    void* s = stream_of(a[3], m);
+    return call("emb_expert_dispatch_backward", [&] {
+      return emb_expert_dispatch_backward(in.p, in.ld, pos.p, n, pos.k, d, code, out.p, out.ld, s);
+    });
+  });
+}
+
+// (ys, pos, w, out, stream)
+PyObject* py_combine(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 5, [&]() -> PyObject* {
+    const Seen m = see(a[3], "out");
+    const int32_t code = code_of(m, "out"), d = fits_int(m.size[1], "out");
+    const int64_t n = m.size[0];
+    const Places pos = places(a[1], n);
+    const Rows in = rows(a[0], m.kind, n * pos.k, d, "ys"), out = rows(m, m.kind, n, d, "out");
+    const auto* w = static_cast<const float*>(flat(a[2], F32, n * pos.k, "w"));
+    void* s = stream_of(a[4], m);
+    return call("emb_expert_combine", [&] {
+      return emb_expert_combine(in.p, in.ld, pos.p, w, n, pos.k, d, code, out.p, out.ld, s);
+    });
+  });
+}
+
+// (dout, ys, pos, w, dys, dw, stream)
+PyObject* py_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 7, [&]() -> PyObject* {
+    const Seen m = see(a[0], "dout");
+    const int32_t code = code_of(m, "dout"), d = fits_int(m.size[1], "dout");
+    const int64_t n = m.size[0];
+    const Places pos = places(a[2], n);
+    const int64_t S = n * pos.k;
+    const Rows g = rows(m, m.kind, n, d, "dout"), y = rows(a[1], m.kind, S, d, "ys"),
+               dys = rows(a[4], m.kind, S, d, "dys");
+    const auto* w = static_cast<const float*>(flat(a[3], F32, S, "w"));
+    auto* dw = static_cast<float*>(flat(a[5], F32, S, "dw"));
+    void* s = stream_of(a[6], m);
+    return call("emb_expert_combine_backward", [&] {
+      return emb_expert_combine_backward(g.p, g.ld, y.p, y.ld, pos.p, w, n, pos.k, d, code, dys.p, dys.ld, dw, s);
+    });
+  });
+}
+
+// Sizes and types of a gated-norm call: from the stream's matrix, and the block's matrices y or,
+// without them, `other` (h or its gradient).
+struct NormCall {
+  emb_norm p{};
+  Seen x;
+  Kind xt, bt;
+  int64_t n, d;
+  NormCall(PyObject* xo, const char* xname, PyObject* y, PyObject* other, const char* oname, PyObject* gate)
+      : x(see(xo, xname)) {
+    p.x_dtype = p.dtype = code_of(x, xname);
+    p.n = n = x.size[0];
+    p.dim = fits_int(d = x.size[1], xname);
+    xt = bt = x.kind;
+    if (y != Py_None || other != Py_None) {
+      const char* name = y != Py_None ? "y" : oname;
+      const Seen b = see(y != Py_None ? y : other, name);
+      p.dtype = code_of(b, name), bt = b.kind;
+    }
+    const Rows r = opt_rows(y, bt, n, d, "y");
+    p.d_y = r.p, p.y_ld = r.ld;
+    if (gate == Py_None) return;
+    const Seen g = see(gate, "gate");
+    if (g.dims != 2 || (g.size[1] != 1 && g.size[1] != d))
+      refuse("gate: expected (%lld, 1) or (%lld, %lld)", (long long)n, (long long)n, (long long)d);
+    p.gate_cols = (int32_t)g.size[1];
+    const Rows q = rows(g, bt, n, p.gate_cols, "gate");
+    p.d_gate = q.p, p.gate_ld = q.ld;
+  }
+  void vectors(PyObject* w_post, PyObject* res_scale, PyObject* w_pre, PyObject* eps) {
+    p.d_w_post = static_cast<const float*>(vec(w_post, d, "w_post"));
+    p.d_res_scale = static_cast<const float*>(vec(res_scale, d, "res_scale"));
+    p.d_w_pre = static_cast<const float*>(vec(w_pre, d, "w_pre"));
+    p.eps = (float)PyFloat_AsDouble(eps);
+    if (PyErr_Occurred()) throw Raised();
+  }
+};
+
+// (x, y, x_out, h, gate, w_post, res_scale, w_pre, eps, stream)
+PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 10, [&]() -> PyObject* {
+    NormCall c(a[0], "x", a[1], a[3], "h", a[4]);
+    emb_norm& p = c.p;
+    const Rows x = rows(c.x, c.xt, c.n, c.d, "x"), o = opt_rows(a[2], c.xt, c.n, c.d, "x_out"),
+               h = opt_rows(a[3], c.bt, c.n, c.d, "h");
+    p.d_x = x.p, p.x_ld = x.ld, p.d_x_out = o.p, p.x_out_ld = o.ld, p.d_h = h.p, p.h_ld = h.ld;
+    c.vectors(a[5], a[6], a[7], a[8]);
+    void* s = stream_of(a[9], c.x);
+    return call("emb_gated_norm", [&] { return emb_gated_norm(&p, s); });
+  });
+}
+
+// (dx_out, dh, x_out, y, dx, dy, gate, w_post, res_scale, w_pre, dgate, dw_post, dres_scale, dw_pre,
+//  eps, workspace, stream)
+PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 17, [&]() -> PyObject* {
+    NormCall c(a[2], "x_out", a[3], a[1], "dh", a[6]);
+    emb_norm& p = c.p;
+    const int64_t n = c.n, d = c.d;
+    const Rows x = rows(c.x, c.xt, n, d, "x_out"), t = opt_rows(a[0], c.xt, n, d, "dx_out"),
+               h = opt_rows(a[1], c.bt, n, d, "dh"), dx = opt_rows(a[4], c.xt, n, d, "dx"),
+               dy = opt_rows(a[5], c.bt, n, d, "dy"),
+               dg = opt_rows(a[10], c.bt, n, p.gate_cols ? p.gate_cols : d, "dgate");
+    p.d_x_out = x.p, p.x_out_ld = x.ld, p.d_dx_out = t.p, p.dx_out_ld = t.ld, p.d_dh = h.p, p.dh_ld = h.ld;
+    p.d_dx = dx.p, p.dx_ld = dx.ld, p.d_dy = dy.p, p.dy_ld = dy.ld, p.d_dgate = dg.p, p.dgate_ld = dg.ld;
+    c.vectors(a[7], a[8], a[9], a[14]);
+    p.d_dw_post = static_cast<float*>(vec(a[11], d, "dw_post"));
+    p.d_dres_scale = static_cast<float*>(vec(a[12], d, "dres_scale"));
+    p.d_dw_pre = static_cast<float*>(vec(a[13], d, "dw_pre"));
+    const bool none = a[15] == Py_None && emb_gated_norm_backward_one_launch(p.n, p.dim);
+    Workspace ws(none ? 0 : emb_gated_norm_backward_workspace(p.n, p.dim), a[15]);
+    void* s = stream_of(a[16], c.x);
+    ws.take(s);
+    return call("emb_gated_norm_backward", [&] { return emb_gated_norm_backward(&p, ws.p, ws.bytes, s); });
+  });
+}
+
+// (grads, max_norm, norm, out, workspace, stream)
+PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 6, [&]() -> PyObject* {
+    const Ref grads(PySequence_Fast(a[0], "grads: expected a list of tensors"));
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(grads.o);
+    const bool apart = a[3] != Py_None;
+    const Ref out(apart ? PySequence_Fast(a[3], "out: expected a list of tensors") : Py_NewRef(Py_None));
+    if (apart && PySequence_Fast_GET_SIZE(out.o) != count)
+      refuse("out: %zd tensors for %zd gradients", PySequence_Fast_GET_SIZE(out.o), count);
+    const double max_norm = PyFloat_AsDouble(a[1]);
+    if (max_norm == -1.0 && PyErr_Occurred()) throw Raised();
+    std::vector<emb_tensor> list((size_t)count);
+    int64_t total = 0;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      const Seen g = see(PySequence_Fast_GET_ITEM(grads.o, i), "grads");
+      if ((g.kind != F32 && g.kind != BF16) || !g.cuda || !g.dense)
+        refuse("grads: expected contiguous CUDA tensors, float32 or bfloat16");
+      emb_tensor& t = list[(size_t)i];
+      t.dtype = g.kind == BF16 ? EMB_BF16 : EMB_F32;
+      t.d_src = t.d_out = g.p;
+      t.numel = g.numel;
+      total += g.numel;
+      if (!apart) continue;
+      const Seen o = see(PySequence_Fast_GET_ITEM(out.o, i), "out");
+      if (o.kind != g.kind || o.numel != g.numel || !o.cuda || !o.dense)
+        refuse("out: expected a contiguous CUDA tensor of each gradient's type and size");
+      t.d_out = o.p;
+    }
+    const Seen norm = see(a[2], "norm");
+    auto* np = static_cast<float*>(flat(norm, F32, 1, false, "norm"));
+    // short lists take one launch and no workspace
+    const bool none = total <= EMB_CLIP_ONE_LAUNCH && count <= 256;
+    Workspace ws(none ? 0 : emb_clip_grads_workspace(count), a[4]);
+    void* s = stream_of(a[5], norm);
+    ws.take(s);
+    return call("emb_clip_grads", [&] {
+      return emb_clip_grads(list.data(), count, (float)max_norm, np, ws.p, ws.bytes, s);
+    });
+  });
+}
+
+template <typename F>
+PyCFunction fast(F f) {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
+}
+
+PyMethodDef methods[] = {{"sort", fast(py_sort), METH_FASTCALL, nullptr},
+                         {"dispatch", fast(py_dispatch), METH_FASTCALL, nullptr},
+                         {"dispatch_backward", fast(py_dispatch_backward), METH_FASTCALL, nullptr},
+                         {"combine", fast(py_combine), METH_FASTCALL, nullptr},
+                         {"combine_backward", fast(py_combine_backward), METH_FASTCALL, nullptr},
+                         {"norm", fast(py_norm), METH_FASTCALL, nullptr},
+                         {"norm_backward", fast(py_norm_backward), METH_FASTCALL, nullptr},
+                         {"clip", fast(py_clip), METH_FASTCALL, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tower", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tower(void) { return PyModule_Create(&module); }
