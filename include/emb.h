@@ -290,7 +290,8 @@ emb_status emb_dequantize_rows(const int8_t* d_q, const float* d_scale, int64_t 
  * give the same bits.  Outputs must not overlap inputs or each other except where a call says
  * so.  Workspaces are 16-byte aligned device buffers of at least the size the call's
  * *_workspace function gives (0: may be NULL; -1: bad sizes); their contents need not be kept
- * between calls, and calls that may overlap on the GPU need one each. */
+ * between calls, and calls that may overlap on the GPU need one each.  The calls can be captured
+ * into graphs; the first of each kind on a device sets its kernels up and comes before that. */
 #define EMB_EXPERT_MAX 1024       /* experts */
 #define EMB_EXPERT_MAX_K 16       /* experts of one row */
 #define EMB_EXPERT_MAX_DIM 65536  /* elements of a row */
@@ -374,7 +375,6 @@ typedef struct emb_norm {
 } emb_norm;
 emb_status emb_gated_norm(const emb_norm* args, void* stream);
 int64_t emb_gated_norm_backward_workspace(int64_t n, int32_t dim);
-int32_t emb_gated_norm_backward_one_launch(int64_t n, int32_t dim);
 emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_bytes,
                                    void* stream);
 
@@ -386,10 +386,8 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
  * a buffer of the same type that overlaps no other.  numel may be 0, and count too (norm 0).
  * EMB_EINVAL: count < 0 or above EMB_CLIP_MAX_TENSORS, a negative numel, a bad dtype, a NULL or
  * (for its type) misaligned buffer, max_norm negative or NaN (infinity: only the norm and
- * copies), a short or misaligned workspace.  Lists of up to 256 tensors with
- * EMB_CLIP_ONE_LAUNCH elements in all need none (NULL, 0 bytes). */
+ * copies), a short or misaligned workspace. */
 #define EMB_CLIP_MAX_TENSORS 65536
-#define EMB_CLIP_ONE_LAUNCH 1048576
 typedef struct emb_tensor {
   const void* d_src;
   void* d_out;

@@ -122,7 +122,6 @@ _SIGS = {
                                      _P, _P], ctypes.c_int),
     "emb_gated_norm": ([ctypes.POINTER(EmbNorm), _P], ctypes.c_int),
     "emb_gated_norm_backward_workspace": ([_I64, _I32], _I64),
-    "emb_gated_norm_backward_one_launch": ([_I64, _I32], _I32),
     "emb_gated_norm_backward": ([ctypes.POINTER(EmbNorm), _P, _I64, _P], ctypes.c_int),
     "emb_clip_grads_workspace": ([_I64], _I64),
     "emb_clip_grads": ([ctypes.POINTER(EmbTensor), _I64, ctypes.c_float, _P, _P, _I64, _P], ctypes.c_int),
@@ -251,7 +250,6 @@ def _stream(stream) -> Optional[int]:
 
 # ---- expert tower (context-free; arguments are checked and passed on by the _tower module) ----
 EXPERT_MAX, EXPERT_MAX_K, EXPERT_MAX_DIM, NORM_MAX_DIM = 1024, 16, 65536, 8192
-CLIP_ONE_LAUNCH = 1048576
 
 
 def expert_sort_workspace(n: int, k: int, num_experts: int) -> int:

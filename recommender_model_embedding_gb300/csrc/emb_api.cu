@@ -1225,10 +1225,6 @@ int64_t emb_gated_norm_backward_workspace(int64_t n, int32_t dim) {
   return gated_norm_bwd_workspace(n, dim);
 }
 
-int32_t emb_gated_norm_backward_one_launch(int64_t n, int32_t dim) {
-  return n >= 0 && dim >= 1 && dim <= EMB_NORM_MAX_DIM && gated_norm_bwd_one_launch(n, dim);
-}
-
 emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_bytes,
                                    void* stream) {
   if (!norm_ok(args)) return EMB_EINVAL;
@@ -1243,8 +1239,7 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
   if ((p.d_dx && !out_ld_ok(p.dx_ld, p.n, p.dim)) || (p.d_dy && !out_ld_ok(p.dy_ld, p.n, p.dim)) ||
       (p.d_dgate && !out_ld_ok(p.dgate_ld, p.n, p.gate_cols)))
     return EMB_EINVAL;
-  const bool none = !d_ws && ws_bytes == 0 && gated_norm_bwd_one_launch(p.n, p.dim);
-  if (!none && !ws_ok(d_ws, ws_bytes, gated_norm_bwd_workspace(p.n, p.dim))) return EMB_EINVAL;
+  if (!ws_ok(d_ws, ws_bytes, gated_norm_bwd_workspace(p.n, p.dim))) return EMB_EINVAL;
   return check_launch(launch_gated_norm_bwd(p, d_ws, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1266,8 +1261,7 @@ emb_status emb_clip_grads(const emb_tensor* h_list, int64_t count, float max_nor
     if (!aligned_to(t.d_src, elem) || !aligned_to(t.d_out, elem)) return EMB_EINVAL;
     total += t.numel;
   }
-  const bool none = !d_ws && ws_bytes == 0 && clip_in_one_launch(count, total);
-  if (!none && !ws_ok(d_ws, ws_bytes, need)) return EMB_EINVAL;
+  if (!ws_ok(d_ws, ws_bytes, need)) return EMB_EINVAL;
   return check_launch(launch_clip_grads(h_list, count, max_norm, d_norm, d_ws,
                                         reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -317,10 +317,8 @@ cudaError_t launch_expert_combine_bwd(const void* dout, int64_t dout_ld, const v
                                       cudaStream_t s);
 cudaError_t launch_gated_norm(const emb_norm& p, cudaStream_t s);
 int64_t gated_norm_bwd_workspace(int64_t n, int dim);
-bool gated_norm_bwd_one_launch(int64_t n, int dim);  // no workspace used
 cudaError_t launch_gated_norm_bwd(const emb_norm& p, void* ws, cudaStream_t s);
 int64_t clip_grads_workspace(int64_t count);
-bool clip_in_one_launch(int64_t count, int64_t total);  // no workspace used
 cudaError_t launch_clip_grads(const emb_tensor* list, int64_t count, float max_norm, float* norm,
                               void* ws, cudaStream_t s);
 cudaError_t launch_key_stats(Ctx* c, const uint32_t* rows, int64_t n, uint32_t* freq,

@@ -35,8 +35,7 @@
 // but dy in one sweep over the row, since only dy needs the second row sum: it keeps u in
 // registers and y in the ring.  A thread has the same columns for all its rows, so the column
 // sums stay in its registers until the end, when they go to the workspace and a second launch
-// adds the CTAs' parts in a fixed order (few rows: a cluster's CTAs add them in shared
-// memory, in one launch; 16 rows of 1024: 6.3 us, 8.2 in two).
+// adds the CTAs' parts in a fixed order (6 us; a single CTA writes the results itself).
 #pragma once
 
 #include "rows_common.cuh"
@@ -61,10 +60,9 @@ struct NormArgs {
   uint32_t x_st, y_st, gate_st, dx_out_st, dh_st, x_out_st, h_st, dx_st, dy_st, dgate_st;  // bytes
   const float *w_post, *res_scale, *w_pre;
   float *dw_post, *dres_scale, *dw_pre;
-  // backward: [CTAs][2][dim] column sums; whether any vector's gradient is asked for; CTAs of the
-  // cluster that adds them up itself (0: none)
+  // backward: [CTAs][2][dim] column sums, and whether any vector's gradient is asked for
   float* part;
-  int cols, cluster;
+  int cols;
 };
 
 // ---- arithmetic on N elements a thread: two at a time (fp32 pairs) where N is even ----

@@ -6,7 +6,9 @@
 // (6.6 TB/s), 477 us a call back to back.  The list is cut into tiles of equal size, dealt to the
 // CTAs in turn whatever the tensors' sizes (neighbouring CTAs read neighbouring tiles: one
 // contiguous share for each CTA took 505 us); the tensors' addresses travel as kernel
-// parameters, so nothing is staged or kept.  Squares are summed in fp32 over at most 16
+// parameters, so nothing is staged or kept.  Two launches serve short lists too: a cluster of
+// 16 CTAs that did both passes in one took 6.3 us for 1024 elements and 10.7 for 524,288 where
+// two launches take 5.6 and 8.0.  Squares are summed in fp32 over at most 16
 // elements, those sums in fp64: a thread's, the CTA's and the list's, all in a fixed order, so
 // the norm repeats bit for bit.  A group of elements whose fp32 sum overflows, or is so
 // small that squares may have been lost, is summed again in fp64, so the norm is right for
@@ -20,7 +22,6 @@ constexpr int kClipShort = 32, kClipLong = 256;  // tensors of one launch: lists
 constexpr int kClipCtasPerSm = 8;                // CTAs of the norm's launch, at most, per SM
 constexpr int kClipScaleCtasPerSm = 4;           // of the scaling launch (64 registers a thread)
 constexpr int kClipTile = 16384, kClipTileMin = 2048;  // elements
-constexpr int kClusterCtas = 16, kClusterThreads = 1024;
 
 template <int N>
 struct ClipList {
@@ -227,59 +228,9 @@ __global__ void __launch_bounds__(kClipThreads, kClipScaleCtasPerSm)
   share_scale<kClipThreads>(l, l.first[l.count] - 1 - blockIdx.x, gridDim.x, c < 0.f ? 1.f : c);
 }
 
-// Short lists in one launch: a cluster of CTAs exchanges its parts through shared memory (the
-// second read then comes from L1 or L2).  Up to EMB_CLIP_ONE_LAUNCH elements: there the cluster's
-// 16 SMs take about 4 us more than all of them in two launches, and the host 8 us less; above,
-// the difference grows.  516,064 elements in 16 tensors: 13 us a call, 27 in two launches.
-template <int N>
-__global__ void __launch_bounds__(kClusterThreads)
-    k_clip_cluster(const __grid_constant__ ClipList<N> l, float max_norm, float* norm_out, int inplace) {
-  __shared__ double part;
-  __shared__ float factor;
-  let_next_start();
-  wait_for_earlier();
-  const double mine = cta_sum<kClusterThreads>(share_squares<kClusterThreads>(l, blockIdx.x, gridDim.x));
-  if (threadIdx.x == 0) part = mine;
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-  if (threadIdx.x < 32) {  // lane r: the part of CTA r
-    double v = 0.0;
-    if (threadIdx.x < gridDim.x) {
-      uint32_t there;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                   : "=r"(there) : "r"((uint32_t)__cvta_generic_to_shared(&part)), "r"(threadIdx.x));
-      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(there) : "memory");
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_down_sync(0xFFFFFFFFu, v, o);
-    if (threadIdx.x == 0) {
-      float norm;
-      factor = clip_factor(v, max_norm, norm);
-      if (blockIdx.x == 0) *norm_out = norm;
-    }
-  }
-  // every part has been read before any CTA may leave
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-  const float c = factor;
-  if (c < 0.f && inplace) return;
-  share_scale<kClusterThreads>(l, l.first[l.count] - 1 - blockIdx.x, gridDim.x, c < 0.f ? 1.f : c);
-}
-
 int64_t clip_grads_workspace(int64_t count) {
   const int64_t launches = count > 0 ? (count + kClipLong - 1) / kClipLong : 1;
   return launches * device_sms() * kClipCtasPerSm * (int64_t)sizeof(double);
-}
-
-bool clip_in_one_launch(int64_t count, int64_t total) {
-  return count <= kClipLong && total <= EMB_CLIP_ONE_LAUNCH;
-}
-
-template <int N>
-static cudaError_t clip_cluster(const ClipList<N>& l, float max_norm, float* norm, int inplace,
-                                cudaStream_t s) {
-  constexpr auto kern = k_clip_cluster<N>;
-  const cudaError_t e = prepare_kernel<kern, true>();
-  if (e != cudaSuccess) return e;
-  return launch_early_cluster(kern, kClusterCtas, kClusterThreads, 0, s, l, max_norm, norm, inplace);
 }
 
 template <int N>
@@ -310,13 +261,6 @@ static cudaError_t clip_lists(const emb_tensor* list, int64_t count, float max_n
     const int64_t tiles = l.first[l.count];
     return (int)(tiles < 1 ? 1 : tiles < cap ? tiles : cap);
   };
-  if (clip_in_one_launch(count, total)) {
-    // two tiles a CTA: few enough steps, and tensors of any size share out
-    l.tile = (int)((total / (2 * kClusterCtas) + 2047) / 2048 * 2048);
-    if (l.tile < kClipTileMin) l.tile = kClipTileMin;
-    fill(0);
-    return clip_cluster(l, max_norm, norm, inplace, s);
-  }
   int parts = 0, grid = 1;
   int64_t i0 = 0;
   cudaError_t e = cudaSuccess;

@@ -24,11 +24,9 @@ namespace emb {
 // A first launch counts each chunk's keys; the last (started early: it waits for the first only
 // where it reads the counts) sums those counts over the chunks (every CTA reads all of them
 // from L2; a launch between the two does it where they are many), scans them over the experts
-// and places the slots.  A single chunk needs no first launch, and up to 16 chunks of 2048 slots
-// exchange their counts through the shared memory of a cluster (8192 slots: 5.8 us where two
-// launches take 8.3, and no workspace; 49,000 slots in chunks of 4096: 7.9 against 8.3, but the
-// kernels around it overlap less: sort, dispatch and combine together took 56 us, not 53).
-// Bound by latency, not bytes (1M slots of 128 experts: 15 us, 2M of 64: 27): a chunk is as short
+// and places the slots.  A single chunk needs no first launch.  (Up to 16 chunks exchanging
+// their counts through the shared memory of a cluster, in one launch, took 6.1 us for 16384 slots
+// of 64 experts where two launches take 6.3, and 15.4 against 9.9 for 32768 of 1024.)  Bound by latency, not bytes (1M slots of 128 experts: 15 us, 2M of 64: 27): a chunk is as short
 // as one CTA an SM allows, a warp loads the ids of eight groups of 32 slots at once, and where
 // that is all of its part (KEEP: chunks of up to 8192 slots) keys and ranks stay in registers
 // from counting to placing and the chunk is put in order in shared memory first, so that its
@@ -39,7 +37,6 @@ constexpr int kSortWarps = 32, kSortThreads = kSortWarps * 32;
 constexpr int kSortDepth = 8;       // groups of 32 ids a warp loads at once
 constexpr int kSortSingle = 4096;   // slots of one CTA alone, at most
 constexpr int kSortFewWarps = 8;    // of that CTA, for up to 2048 slots
-constexpr int kSortCluster = 16, kSortClusterChunk = 2048;  // CTAs of a cluster, slots of each at most
 constexpr int kSortScan = 32768;    // counts (chunks x keys) above which a launch sums them
 constexpr int kSortMaxKeep = 1024;  // chunks, at most, of the size that stays in registers
 
@@ -143,9 +140,8 @@ __global__ void __launch_bounds__(256) k_expert_scan(uint32_t* hist, int chunks,
 
 // KEEP: keys and ranks stay in registers (chunks of WARPS * 256 slots); STAGE: the chunk is put in
 // order in shared memory.  The other chunks' counts come from hist (SCANNED: k_expert_scan's
-// sums), or, with CLUSTER, from the shared memory of the CTAs of one cluster; hist NULL without
-// CLUSTER: one chunk.
-template <int WARPS, bool KEEP, bool STAGE, bool SCANNED, bool CLUSTER>
+// sums); NULL: one chunk.
+template <int WARPS, bool KEEP, bool STAGE, bool SCANNED>
 __global__ void __launch_bounds__(WARPS * 32)
     k_expert_place(const int64_t* ids, int64_t S, int E, int64_t chunk, const uint32_t* hist,
                    int32_t* order, int32_t* pos, int32_t* offsets) {
@@ -161,8 +157,7 @@ __global__ void __launch_bounds__(WARPS * 32)
   uint32_t* total = sm_place + WARPS * K;
   uint32_t* before = total + K;
   uint32_t* mine = sm_place + warp * K;
-  uint32_t* mine_all = before + K;  // CLUSTER: the chunk's counts, for the other CTAs
-  uint32_t* by_slot = mine_all + (CLUSTER ? K : 0);
+  uint32_t* by_slot = before + K;
   uint16_t* by_key = reinterpret_cast<uint16_t*>(by_slot + kSortDepth * THREADS);
   const int64_t c0 = (int64_t)blockIdx.x * chunk;
   const int64_t c1 = c0 + chunk < S ? c0 + chunk : S;
@@ -226,28 +221,9 @@ __global__ void __launch_bounds__(WARPS * 32)
         run += c[w];
       }
     }
-    own += mine_of[i] = run;
-    if (CLUSTER) mine_all[e] = run;
-    else if (!hist) total[e] = run;
-  }
-  if (CLUSTER) asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = threadIdx.x * per + i;
-    if (i >= per || e >= K) break;
-    if (CLUSTER) {
-      const uint32_t here = (uint32_t)__cvta_generic_to_shared(mine_all + e);
-      uint32_t t = 0, b = 0;
-      for (uint32_t r = 0; r < gridDim.x; ++r) {
-        uint32_t there, c;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(r));
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c) : "r"(there) : "memory");
-        t += c;
-        b += r < blockIdx.x ? c : 0u;
-      }
-      total[e] = t, before[e] = b;
-    }
+    if (!hist) total[e] = run;
     sum += total[e];
+    own += mine_of[i] = run;
   }
   uint32_t incl = sum, incl_own = own;
 #pragma unroll
@@ -302,25 +278,17 @@ __global__ void __launch_bounds__(WARPS * 32)
     for (int l = threadIdx.x; l < (int)(c1 - c0); l += THREADS)
       order[l + before[by_key[l]]] = (int32_t)by_slot[l];
   }
-  // every CTA's counts have been read before it may leave
-  if (CLUSTER) asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 struct SortPlan {
   int64_t chunk, chunks;
-  bool keep, scan, cluster;
+  bool keep, scan;
 };
 
 // One chunk an SM, or as many of the size that stays in registers as it takes.
 static SortPlan sort_plan(int64_t S, int E, int sms) {
-  SortPlan p{kSortSingle, 1, true, false, false};
+  SortPlan p{kSortSingle, 1, true, false};
   if (S <= kSortSingle) return p;
-  if (S <= kSortCluster * kSortClusterChunk) {
-    p.cluster = true;
-    p.chunks = kSortCluster;
-    p.chunk = (S + kSortCluster * kSortThreads - 1) / (kSortCluster * kSortThreads) * kSortThreads;
-    return p;
-  }
   const int64_t most = kSortDepth * kSortThreads, even = (S + sms - 1) / sms;
   p.keep = (S + most - 1) / most <= kSortMaxKeep;
   p.chunk = p.keep && even > most ? most : (even + kSortThreads - 1) / kSortThreads * kSortThreads;
@@ -331,28 +299,21 @@ static SortPlan sort_plan(int64_t S, int E, int sms) {
 
 int64_t expert_sort_workspace(int64_t S, int E) {
   const SortPlan p = sort_plan(S, E, device_sms());
-  return p.chunks <= 1 || p.cluster ? 0 : (p.chunks + 1) * (E + 1) * (int64_t)sizeof(uint32_t);
+  return p.chunks <= 1 ? 0 : (p.chunks + 1) * (E + 1) * (int64_t)sizeof(uint32_t);
 }
 
 cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* order, int32_t* pos,
                                int32_t* offsets, void* ws, cudaStream_t s) {
   const SortPlan p = sort_plan(S, E, device_sms());
   const int G = (int)p.chunks;
-  uint32_t* hist = G > 1 && !p.cluster ? static_cast<uint32_t*>(ws) : nullptr;
+  uint32_t* hist = G > 1 ? static_cast<uint32_t*>(ws) : nullptr;
   const uint32_t* sums = hist;
-  const int staged = p.keep && G > 1 ? kSortDepth * kSortThreads * 6 : 0;
+  const int staged = p.keep && hist ? kSortDepth * kSortThreads * 6 : 0;
   const auto smem = [&](int warps) { return (warps + 2) * (E + 1) * (int)sizeof(uint32_t) + staged; };
-  if (p.cluster) {
-    constexpr auto kern = k_expert_place<kSortWarps, true, true, false, true>;
-    const cudaError_t e = prepare_kernel<kern, true>();
-    if (e != cudaSuccess) return e;
-    return launch_early_cluster(kern, kSortCluster, kSortThreads, smem(kSortWarps + 1), s, ids, S, E, p.chunk,
-                                sums, order, pos, offsets);
-  }
   if (!hist) {  // an empty batch still writes offsets
     const bool few = S <= kSortFewWarps * 32 * kSortDepth;
-    constexpr auto small = k_expert_place<kSortFewWarps, true, false, false, false>;
-    constexpr auto big = k_expert_place<kSortWarps, true, false, false, false>;
+    constexpr auto small = k_expert_place<kSortFewWarps, true, false, false>;
+    constexpr auto big = k_expert_place<kSortWarps, true, false, false>;
     const cudaError_t e = few ? prepare_kernel<small>() : prepare_kernel<big>();
     if (e != cudaSuccess) return e;
     const int warps = few ? kSortFewWarps : kSortWarps;
@@ -366,7 +327,7 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
   if (e != cudaSuccess) return e;
   const auto place = [&](auto keep, auto scanned) {
     constexpr bool K = decltype(keep)::value;
-    constexpr auto kern = k_expert_place<kSortWarps, K, K, decltype(scanned)::value, false>;
+    constexpr auto kern = k_expert_place<kSortWarps, K, K, decltype(scanned)::value>;
     const cudaError_t f = prepare_kernel<kern>();
     return f != cudaSuccess ? f
                             : launch_early(kern, G, kSortThreads, smem(kSortWarps), s, ids, S, E, p.chunk, sums,

@@ -163,9 +163,8 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormBackward, V * E
   const int slices = tpr < 32 ? (int)blockDim.x / 32 : a.rpb;
   const int slice = tpr < 32 ? (int)threadIdx.x / 32 : grp.id;
   const bool writes = tpr >= 32 || (int)(threadIdx.x & 31) < tpr;
-  float* cols = reinterpret_cast<float*>(ring);  // [slices][2][dim]; a single slice is the CTA's sums
-  float* sums = slices > 1 ? cols + slices * 2 * a.dim : cols;  // [2][dim]
-  __syncthreads();                                              // the ring has been read
+  float* cols = reinterpret_cast<float*>(ring);  // [slices][2][dim]
+  __syncthreads();                               // the ring has been read
 #pragma unroll
   for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -184,34 +183,14 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormBackward, V * E
     }
   }
   __syncthreads();
-  // where they go: the workspace; the results, if there is one CTA; or, in a cluster, shared memory,
-  // from which each of its CTAs adds up some of the columns
+  // where they go: the workspace, or the results, if there is one CTA
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.dim;
-  if (slices > 1 || !a.cluster || gridDim.x == 1)
-    for (int k = threadIdx.x; k < a.dim; k += blockDim.x) {
-      float p = cols[k], q = cols[a.dim + k];
-      for (int r = 1; r < slices; ++r) p += cols[r * 2 * a.dim + k], q += cols[(r * 2 + 1) * a.dim + k];
-      if (gridDim.x == 1) put_cols(a, k, p, q);
-      else if (a.cluster) sums[k] = p, sums[a.dim + k] = q;
-      else out[k] = p, out[a.dim + k] = q;
-    }
-  if (!a.cluster || gridDim.x == 1) return;
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-  const uint32_t here = smem_at(sums);
-  for (int k = blockIdx.x * blockDim.x + threadIdx.x; k < a.dim; k += gridDim.x * blockDim.x) {
-    float p = 0.f, q = 0.f;
-    for (uint32_t r = 0; r < gridDim.x; ++r) {
-      uint32_t there;
-      float c, d;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(r));
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(c) : "r"(there + k * 4) : "memory");
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(d) : "r"(there + (a.dim + k) * 4) : "memory");
-      p += c, q += d;
-    }
-    put_cols(a, k, p, q);
+  for (int k = threadIdx.x; k < a.dim; k += blockDim.x) {
+    float p = cols[k], q = cols[a.dim + k];
+    for (int r = 1; r < slices; ++r) p += cols[r * 2 * a.dim + k], q += cols[(r * 2 + 1) * a.dim + k];
+    if (gridDim.x == 1) put_cols(a, k, p, q);
+    else out[k] = p, out[a.dim + k] = q;
   }
-  // every CTA's sums have been read before it may leave
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // Sums the CTAs' parts (none: zeros): 32 columns a CTA, 32 threads a column over interleaved parts, then over
@@ -247,24 +226,13 @@ __global__ void __launch_bounds__(1024) k_gated_norm_cols(NormArgs a, int parts)
   }
 }
 
-// Few rows take one launch: a cluster of up to 16 CTAs, whose column sums meet in shared memory,
-// with up to kNormRounds rows a group.  Otherwise a row a group up to one CTA an SM, then at least
-// four rows a group up to `cap`, so that the column parts stay small beside the rows.
-constexpr int kNormCluster = 16, kNormRounds = 6;
+// CTAs: a row a group up to one CTA an SM, then at least four rows a group up to `cap`, so that the
+// column parts stay small beside the rows.  (A cluster of 16 CTAs that added its parts itself, in
+// one launch, was no faster: 16 x 1024 rows 6.3 us against 6.7, 96 x 1024 9.7 against 7.3.)
 constexpr int kNormCtasPerSm = 2 * kNormBackward / 160;  // at most (a CTA has at least 160 threads)
 
-static int64_t norm_blocks(int64_t n, int rpb) { return (n + rpb - 1) / rpb; }
-
-static int norm_cluster(int64_t n, int rpb) {  // CTAs of the cluster; 0: too many rows
-  const int64_t blocks = norm_blocks(n, rpb);
-  if (blocks > kNormCluster * kNormRounds) return 0;
-  int c = 1;
-  while (c < kNormCluster && c < blocks) c *= 2;
-  return c;
-}
-
 static int64_t norm_bwd_grid(int64_t n, int rpb, int64_t cap) {
-  const int64_t sms = device_sms(), all = norm_blocks(n, rpb), four = (n + 4 * rpb - 1) / (4 * rpb);
+  const int64_t sms = device_sms(), all = (n + rpb - 1) / rpb, four = (n + 4 * rpb - 1) / (4 * rpb);
   const int64_t blocks = all <= sms ? all : four > sms ? four : sms;
   return blocks < 1 ? 1 : blocks < cap ? blocks : cap;
 }
@@ -276,27 +244,17 @@ int64_t gated_norm_bwd_workspace(int64_t n, int dim) {
   return norm_bwd_grid(n, a.rpb, (int64_t)device_sms() * kNormCtasPerSm) * 2 * dim * (int64_t)sizeof(float);
 }
 
-bool gated_norm_bwd_one_launch(int64_t n, int dim) {
-  NormArgs a{};
-  a.dim = dim;
-  norm_shape(a, 1, kNormBackward);
-  return norm_cluster(n, a.rpb) > 0;
-}
-
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_bwd_v(NormArgs& a, int* parts, cudaStream_t s) {
   const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : 2 * kNormBackward / threads;
   int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>, per, V * EPU > 8 ? a.tpr * 128 : 0);
   const int slices = a.tpr < 32 ? threads / 32 : a.rpb;
-  const int cols = (slices > 1 ? slices + 1 : 1) * 2 * a.dim * (int)sizeof(float);
+  const int cols = slices * 2 * a.dim * (int)sizeof(float);
   if (smem < cols) smem = cols;
   constexpr auto kern = k_gated_norm_bwd<XT, BT, EPU, V, GATE, WARP>;
-  const cudaError_t e = prepare_kernel<kern, true>();
+  const cudaError_t e = prepare_kernel<kern>();
   if (e != cudaSuccess) return e;
-  a.cluster = a.cols ? norm_cluster(a.n, a.rpb) : 0;
-  if (a.cluster > 1) return launch_early_cluster(kern, (unsigned)a.cluster, threads, smem, s, a);
-  const unsigned grid =
-      a.cluster ? 1u : (unsigned)norm_bwd_grid(a.n, a.rpb, (int64_t)device_sms() * norm_fit(per, smem));
+  const unsigned grid = (unsigned)norm_bwd_grid(a.n, a.rpb, (int64_t)device_sms() * norm_fit(per, smem));
   if (a.cols && grid > 1) *parts = (int)grid;
   return launch_early(kern, grid, threads, smem, s, a);
 }

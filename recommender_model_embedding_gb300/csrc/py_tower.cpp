@@ -392,8 +392,7 @@ PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     p.d_dw_post = static_cast<float*>(vec(a[11], d, "dw_post"));
     p.d_dres_scale = static_cast<float*>(vec(a[12], d, "dres_scale"));
     p.d_dw_pre = static_cast<float*>(vec(a[13], d, "dw_pre"));
-    const bool none = a[15] == Py_None && emb_gated_norm_backward_one_launch(p.n, p.dim);
-    Workspace ws(none ? 0 : emb_gated_norm_backward_workspace(p.n, p.dim), a[15]);
+    Workspace ws(emb_gated_norm_backward_workspace(p.n, p.dim), a[15]);
     void* s = stream_of(a[16], c.x);
     ws.take(s);
     return call("emb_gated_norm_backward", [&] { return emb_gated_norm_backward(&p, ws.p, ws.bytes, s); });
@@ -412,7 +411,6 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const double max_norm = PyFloat_AsDouble(a[1]);
     if (max_norm == -1.0 && PyErr_Occurred()) throw Raised();
     std::vector<emb_tensor> list((size_t)count);
-    int64_t total = 0;
     for (Py_ssize_t i = 0; i < count; ++i) {
       const Seen g = see(PySequence_Fast_GET_ITEM(grads.o, i), "grads");
       if ((g.kind != F32 && g.kind != BF16) || !g.cuda || !g.dense)
@@ -421,7 +419,6 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t na) {
       t.dtype = g.kind == BF16 ? EMB_BF16 : EMB_F32;
       t.d_src = t.d_out = g.p;
       t.numel = g.numel;
-      total += g.numel;
       if (!apart) continue;
       const Seen o = see(PySequence_Fast_GET_ITEM(out.o, i), "out");
       if (o.kind != g.kind || o.numel != g.numel || !o.cuda || !o.dense)
@@ -430,9 +427,7 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t na) {
     }
     const Seen norm = see(a[2], "norm");
     auto* np = static_cast<float*>(flat(norm, F32, 1, false, "norm"));
-    // short lists take one launch and no workspace
-    const bool none = total <= EMB_CLIP_ONE_LAUNCH && count <= 256;
-    Workspace ws(none ? 0 : emb_clip_grads_workspace(count), a[4]);
+    Workspace ws(emb_clip_grads_workspace(count), a[4]);
     void* s = stream_of(a[5], norm);
     ws.take(s);
     return call("emb_clip_grads", [&] {

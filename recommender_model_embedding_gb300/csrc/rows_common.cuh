@@ -165,21 +165,6 @@ cudaError_t launch_early(void (*kern)(P...), unsigned grid, int threads, int sme
   return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
 }
 
-// The same for a grid that is one cluster of `grid` CTAs.
-template <typename... P, typename... A>
-cudaError_t launch_early_cluster(void (*kern)(P...), unsigned grid, int threads, int smem,
-                                 cudaStream_t s, A&&... args) {
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = grid, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid), cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem, cfg.stream = s, cfg.attrs = attr, cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
-}
-
 // Multiprocessors of the current device (context-free calls; the count is read once a device).
 inline int device_sms() {
   constexpr int kDevices = 64;
@@ -196,10 +181,9 @@ inline int device_sms() {
   return 1;
 }
 
-// Settings of a kernel that its default launch does not have, asked for once per kernel and device
-// (the request costs a call's host time): as much dynamic shared memory as a CTA can have, and
-// clusters of 16 CTAs.
-template <auto KERN, bool CLUSTER = false>
+// Lets a kernel take as much dynamic shared memory as a CTA can have (asked for once per kernel and
+// device: the request costs a call's host time).
+template <auto KERN>
 cudaError_t prepare_kernel() {
   static std::atomic<uint64_t> done{0};
   int dev = 0, most = 0;
@@ -212,7 +196,6 @@ cudaError_t prepare_kernel() {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
-  if (e == cudaSuccess && CLUSTER) e = cudaFuncSetAttribute(KERN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }

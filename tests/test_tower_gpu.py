@@ -721,8 +721,8 @@ def test_graph_with_other_work_and_streams(E):
     (32769, 2, 64), (20000, 16, 128), (155648, 8, 255), (155649, 8, 256), (1_100_000, 8, 40),
     (1_100_000, 8, 900)])
 def test_sort_where_its_launches_change(E, n, k, e):
-    """Sizes on either side of one CTA of few warps, one CTA, a cluster, two launches and three, and
-    chunks too large for registers."""
+    """Sizes on either side of one CTA of few warps, one CTA, two launches and three, and chunks too
+    large for registers."""
     g = gen(n + e)
     ids = torch.randint(0, e, (n, k), generator=g, device="cuda")
     ids = ids.masked_fill(torch.rand((n, k), generator=g, device="cuda") < 0.1, -1)
@@ -733,7 +733,7 @@ def test_sort_where_its_launches_change(E, n, k, e):
 @pytest.mark.parametrize("n,d", [(1, 64), (95 * 32, 64), (97 * 32, 64), (16 * 6 * 2, 1024), (16 * 6 * 2 + 1, 1024),
                                  (96, 8192), (97, 8192)])
 def test_gated_norm_backward_where_its_launches_change(E, n, d):
-    """Rows on either side of what one cluster takes, with and without the vectors' gradients."""
+    """Rows that take one CTA, one CTA an SM and more, with and without the vectors' gradients."""
     s = norm_case(n, d, "full", torch.float32, torch.bfloat16, 0, 0, n)
     ref, got = norm_grad_ref(s, 1e-6), norm_grad(E, s, 1e-6)
     for k, v in got.items():
@@ -747,7 +747,7 @@ def test_gated_norm_backward_where_its_launches_change(E, n, d):
 
 @pytest.mark.parametrize("total,count", [(1048576, 3), (1048577, 3), (5000, 256), (5000, 257)])
 def test_clip_where_its_launches_change(E, total, count):
-    """Lists on either side of what one launch takes, by elements and by tensors."""
+    """Lists that cut a tensor range at random places, on either side of what one launch takes."""
     g = gen(count)
     cut = sorted(torch.randint(0, total + 1, (count - 1,), generator=g, device="cuda").tolist())
     sizes = [b - a for a, b in zip([0] + cut, cut + [total])]
