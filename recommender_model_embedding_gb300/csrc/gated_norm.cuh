@@ -28,7 +28,7 @@
 // neighbours in memory: with 8, half-filled sectors took 0.72 ms, not 0.57), so a row costs each
 // thread few shuffles per element.  CTAs are persistent; every thread copies its own packs of
 // the next rows to shared memory asynchronously, up to two rows ahead, and reads back only what
-// it copied itself, so the ring needs no barrier (rows loaded straight to registers: 2.88 ms
+// it copied itself, so the ring needs no barrier (a row loaded only when its turn came: 2.88 ms
 // backward, 1.17 ms forward); the groups of a CTA run independently of each other (named
 // barriers for the row sums, and only for rows of more than 32 threads).  Packs past the row's
 // end are zero in the ring, which takes the place of masks.  The backward computes everything
@@ -345,9 +345,16 @@ struct ColWeights {
   }
 };
 
+// Whether a thread's packs of the next row wait in registers instead of the ring: packs of one
+// element, up to 8 of them.  There a ring would take two more instructions of the same pipe for
+// every 4 bytes, and bf16 elements have no asynchronous copy at all (forward of 16411 x 479 fp32:
+// 33 us through the ring, 27 so; of 83781 x 801 bf16 225 and 169, backward 466 and 339).
+template <int EPU, int V>
+constexpr bool kAhead = EPU == 1 && V <= 8;
+
 // Bytes of one ring stage for one thread: XS matrices of XT and BS of BT.
 template <typename XT, typename BT, int EPU, int V, int XS, int BS>
-constexpr int kRingBytes = V * EPU * (XS * (int)sizeof(XT) + BS * (int)sizeof(BT));
+constexpr int kRingBytes = kAhead<EPU, V> ? 0 : V * EPU * (XS * (int)sizeof(XT) + BS * (int)sizeof(BT));
 
 // One matrix's part of the ring, and its rows in memory: offsets and strides in bytes.
 template <typename T, int EPU, int V, bool WARP>
@@ -356,23 +363,44 @@ struct Lane {
   using Sh = Share<V, WARP>;
   using K = Chunks<EPU, V>;
   uint32_t at, plane;  // this thread's place of the matrix in stage 0; bytes of a plane
+  uint32_t now[kAhead<EPU, V> ? V : 1], next[kAhead<EPU, V> ? V : 1];  // kAhead: the elements' bits
+  __device__ __forceinline__ Lane(uint32_t at_, uint32_t plane_) : at(at_), plane(plane_) {}
   __device__ __forceinline__ uint32_t pack(uint32_t stage, int i) const {
     return at + stage + i * plane;
   }
   // the thread's packs of a row, into the ring (`left`: packs of the row from this thread's on)
-  __device__ __forceinline__ void fetch(uint32_t stage, const char* row, int left, const Sh& sh) const {
+  __device__ __forceinline__ void fetch(uint32_t stage, const char* row, int left, const Sh& sh) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (sh.step(i) < left) S::fetch(pack(stage, i), row + sh.step(i) * S::kBytes);
+    for (int i = 0; i < V; ++i) {
+      if constexpr (kAhead<EPU, V>) {
+        next[i] = 0;
+        if (sh.step(i) < left) {
+          if constexpr (sizeof(T) == 4) next[i] = *reinterpret_cast<const uint32_t*>(row + sh.step(i) * 4);
+          else next[i] = *reinterpret_cast<const uint16_t*>(row + sh.step(i) * 2);
+        }
+      } else if (sh.step(i) < left) {
+        S::fetch(pack(stage, i), row + sh.step(i) * S::kBytes);
+      }
+    }
+  }
+  __device__ __forceinline__ void advance() {  // kAhead: the row fetched last becomes the current one
+#pragma unroll
+    for (int i = 0; i < (kAhead<EPU, V> ? V : 0); ++i) now[i] = next[i];
   }
   __device__ __forceinline__ void zero_tail(uint32_t stage, int left, const Sh& sh) const {
+    if constexpr (!kAhead<EPU, V>)
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (sh.step(i) >= left) S::zero(pack(stage, i));
+      for (int i = 0; i < V; ++i)
+        if (sh.step(i) >= left) S::zero(pack(stage, i));
   }
   __device__ __forceinline__ void read(uint32_t stage, int chunk, float (&v)[K::C]) const {
 #pragma unroll
-    for (int p = 0; p < K::PP; ++p) S::read(pack(stage, chunk * K::PP + p), v + p * EPU);
+    for (int p = 0; p < K::PP; ++p) {
+      if constexpr (kAhead<EPU, V>)
+        v[p] = __uint_as_float(sizeof(T) == 4 ? now[chunk * K::PP + p] : now[chunk * K::PP + p] << 16);
+      else
+        S::read(pack(stage, chunk * K::PP + p), v + p * EPU);
+    }
   }
   static __device__ __forceinline__ void store(char* row, int chunk, const float (&v)[K::C], int left,
                                                const Sh& sh) {
@@ -452,7 +480,7 @@ inline int norm_fit(int per, int smem) {
 // and one for the widest rows.  `extra`: bytes beside the ring.
 inline int norm_ring(NormArgs& a, int thread_bytes, int per, int extra) {
   const int bytes = a.rpb * a.tpr * thread_bytes;
-  a.stages = kStages;
+  a.stages = bytes ? kStages : 2;  // (in registers: the next row)
   while (a.stages > 1) {
     const int fit = norm_fit(per, a.stages * bytes + extra);
     if (fit > 0 && (a.stages == 2 || fit == norm_fit(per, (a.stages - 1) * bytes + extra))) break;
@@ -498,7 +526,7 @@ inline bool norm_allows(const emb_norm& p, int epu) {
 // threads per row.  Rows of 16 elements a thread always take whole warps.
 template <typename Call, typename XT, typename BT, int EPU, int V = 1>
 cudaError_t norm_t(NormArgs& a, Call call) {
-  if constexpr (V == 1) norm_shape(a, EPU, Call::kMost);
+  if constexpr (V == 1) norm_shape(a, EPU, Call::most(EPU));
   if constexpr (V * EPU < 16)
     if ((a.packs + a.tpr - 1) / a.tpr > V) return norm_t<Call, XT, BT, EPU, 2 * V>(a, call);
   const auto run = [&](auto gate, auto warp) {

@@ -24,15 +24,17 @@ namespace emb {
 // A first launch counts each chunk's keys; the last (started early: it waits for the first only
 // where it reads the counts) sums those counts over the chunks (every CTA reads all of them
 // from L2; a launch between the two does it where they are many), scans them over the experts
-// and places the slots.  A single chunk needs no first launch.  (Up to 16 chunks exchanging
-// their counts through the shared memory of a cluster, in one launch, took 6.1 us for 16384 slots
-// of 64 experts where two launches take 6.3, and 15.4 against 9.9 for 32768 of 1024.)  Bound by latency, not bytes (1M slots of 128 experts: 15 us, 2M of 64: 27): a chunk is as short
+// and places the slots.  A single chunk needs no first launch (3000 slots: 4.5 us in one launch,
+// 4.8 in two).  Up to 16 chunks exchanging their counts through the shared memory of a cluster,
+// in one launch, were no faster: 6.1 us for 16384 slots of 64 experts where two launches take
+// 6.3, 15.4 against 9.9 for 32768 of 1024.
+// Bound by latency, not bytes (1M slots of 128 experts: 15 us, 2M of 64: 27): a chunk is as short
 // as one CTA an SM allows, a warp loads the ids of eight groups of 32 slots at once, and where
 // that is all of its part (KEEP: chunks of up to 8192 slots) keys and ranks stay in registers
 // from counting to placing and the chunk is put in order in shared memory first, so that its
-// places are written in runs.  Lanes with equal keys find each other by ballots over the key's
-// bits: __match_any_sync, which works through the distinct keys, took 29 us where this took 23
-// (1M slots of 128 experts, at that point).
+// places are written in runs (1M slots: 23 -> 21 us).  Lanes with equal keys find each other by
+// ballots over the key's bits: __match_any_sync, which works through the distinct keys, took
+// 29 us where this took 23 (1M slots of 128 experts, before the staged writes).
 constexpr int kSortWarps = 32, kSortThreads = kSortWarps * 32;
 constexpr int kSortDepth = 8;       // groups of 32 ids a warp loads at once
 constexpr int kSortSingle = 4096;   // slots of one CTA alone, at most
@@ -341,10 +343,12 @@ cudaError_t launch_expert_sort(const int64_t* ids, int64_t S, int E, int32_t* or
 // A task is a row, or a part of one: `lanes` neighbouring threads (a power of two, up to 32), each
 // with UN units of the row `lanes` apart, all loaded before the first is used.  A unit is 16
 // bytes where every row start and the row length are multiples of 16, else 4 or 2: the row's
-// addresses are worked out once a task, so that narrow units cost little more (rows of 479 fp32:
-// dispatch 34 -> 19 us, combine 54 -> 24 us for 16411 x 3 of them, against a division an
-// element).  Narrow rows take few threads (but a 32-byte sector's worth) with several units each, so that a warp has
-// several rows in flight; with too few rows to fill the device that way, more threads.
+// addresses are worked out once a task, so that narrow units cost little more (16411 x 3 rows of
+// 479 fp32: dispatch 34 -> 19 us, combine 54 -> 24 us, against a division an element).  Narrow
+// rows take few threads (but a 32-byte sector's worth) with several units each, so that a warp
+// has several rows in flight (177877 x 1 rows of 40 fp32, both gradients: 68 -> 31 us); with too
+// few rows to fill the device that way, more threads.  Units of 16 bytes go at most two a
+// thread: with eight, dispatch of 262144 x 4 rows of 512 bf16 took 8 us more.
 constexpr int kMoveThreads = 256;
 
 struct MoveShape {

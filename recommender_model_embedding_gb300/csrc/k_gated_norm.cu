@@ -5,7 +5,7 @@ namespace emb {
 
 // GATE: a gate for each element.
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
-__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EPU > 8 ? 1 : 2) k_gated_norm(NormArgs a) {
+__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EPU > 8 || kAhead<EPU, V> ? 1 : 2) k_gated_norm(NormArgs a) {
   let_next_start();
   wait_for_earlier();
   using K = Chunks<EPU, V>;
@@ -22,8 +22,8 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EP
   const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>;
   const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::kBytes;
   const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::kBytes + V * plx;
-  const LX lx{tx, plx};
-  const LB ly{tb, plb}, lg{tb + V * plb, plb};
+  LX lx(tx, plx);
+  LB ly(tb, plb), lg(tb + V * plb, plb);
   const uint64_t cx = (uint32_t)sh.first * LX::S::kBytes, cb = (uint32_t)sh.first * LB::S::kBytes;
 
   auto fetch = [&](uint32_t row, uint32_t stage) {
@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EP
   // every group runs as many rounds as the CTA's first: shuffles and barriers stay whole
   for (uint32_t r0 = blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
     const bool live = row < a.n;
+    if constexpr (kAhead<EPU, V>) lx.advance(), ly.advance(), lg.advance();
     fetch(row + (a.stages - 1) * step, st == 0 ? last : st - stage_bytes);
     float g_row = 1.f, rest;
     if (!GATE) row_gate.take(a, row + step, g_row, rest);
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EP
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
-  const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : 2 * kNormForward / threads;
+  const int threads = a.rpb * a.tpr, per = (V * EPU > 8 || kAhead<EPU, V> ? 1 : 2) * kNormForward / threads;
   const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>, per, V * EPU > 8 ? a.tpr * 128 : 0);
   constexpr auto kern = k_gated_norm<XT, BT, EPU, V, GATE, WARP>;
   const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = (int64_t)device_sms() * norm_fit(per, smem);
@@ -124,7 +125,7 @@ static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
 }
 
 struct NormForward {
-  static constexpr int kMost = kNormForward;
+  static constexpr int most(int) { return kNormForward; }
   cudaStream_t s;
   template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
   cudaError_t run(NormArgs& a) const { return norm_fwd_v<XT, BT, EPU, V, GATE, WARP>(a, s); }

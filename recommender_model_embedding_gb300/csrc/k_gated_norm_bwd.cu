@@ -5,7 +5,7 @@
 namespace emb {
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
-__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormBackward, V * EPU > 8 ? 1 : 2) k_gated_norm_bwd(NormArgs a) {
+__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kAhead<EPU, V> ? kNormThreads : kNormBackward, V * EPU > 8 ? 1 : 2) k_gated_norm_bwd(NormArgs a) {
   let_next_start();
   wait_for_earlier();
   using K = Chunks<EPU, V>;
@@ -23,8 +23,8 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormBackward, V * E
   const uint32_t mx = V * plx, mb = V * plb;  // of a matrix
   const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::kBytes;
   const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::kBytes + 2 * mx;
-  const LX lx{tx, plx}, lt{tx + mx, plx};
-  const LB ld{tb, plb}, ly{tb + mb, plb}, lg{tb + 2 * mb, plb};
+  LX lx(tx, plx), lt(tx + mx, plx);
+  LB ld(tb, plb), ly(tb + mb, plb), lg(tb + 2 * mb, plb);
   const uint64_t cx = (uint32_t)sh.first * LX::S::kBytes, cb = (uint32_t)sh.first * LB::S::kBytes;
   float col_pre[K::NC][K::C], col_t[K::NC][K::C];
 #pragma unroll
@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormBackward, V * E
   uint32_t st = 0;
   for (uint32_t r0 = blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
     const bool live = row < a.n;
+    if constexpr (kAhead<EPU, V>) lx.advance(), lt.advance(), ld.advance(), ly.advance(), lg.advance();
     fetch(row + (a.stages - 1) * step, st == 0 ? last : st - stage_bytes);
     float g_row = 1.f, rest_row = 0.f;
     if (!GATE) row_gate.take(a, row + step, g_row, rest_row);
@@ -246,7 +247,7 @@ int64_t gated_norm_bwd_workspace(int64_t n, int dim) {
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_bwd_v(NormArgs& a, int* parts, cudaStream_t s) {
-  const int threads = a.rpb * a.tpr, per = V * EPU > 8 ? kNormWide / threads : 2 * kNormBackward / threads;
+  const int threads = a.rpb * a.tpr, per = (V * EPU > 8 ? kNormWide : kAhead<EPU, V> ? 2 * kNormThreads : 2 * kNormBackward) / threads;
   int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>, per, V * EPU > 8 ? a.tpr * 128 : 0);
   const int slices = a.tpr < 32 ? threads / 32 : a.rpb;
   const int cols = slices * 2 * a.dim * (int)sizeof(float);
@@ -260,7 +261,7 @@ static cudaError_t norm_bwd_v(NormArgs& a, int* parts, cudaStream_t s) {
 }
 
 struct NormBackward {
-  static constexpr int kMost = kNormBackward;
+  static constexpr int most(int epu) { return epu == 1 ? kNormThreads : kNormBackward; }
   cudaStream_t s;
   int* parts;  // CTAs whose column sums are in the workspace (0: none to add)
   template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
