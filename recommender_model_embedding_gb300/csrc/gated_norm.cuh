@@ -345,25 +345,31 @@ struct ColWeights {
   }
 };
 
-// Whether a thread's packs of the next row wait in registers instead of the ring: packs of one
-// element, up to 8 of them.  There a ring would take two more instructions of the same pipe for
-// every 4 bytes, and bf16 elements have no asynchronous copy at all (forward of 16411 x 479 fp32:
-// 33 us through the ring, 27 so; of 83781 x 801 bf16 225 and 169, backward 466 and 339).
+// Whether a thread's packs of the next row wait in registers instead of the ring, for small packs,
+// up to 8 elements: there a ring would take two more instructions of the same pipe for every few
+// bytes, and single bf16 elements have no asynchronous copy at all.  Packs of one element:
+// forward of 16411 x 479 fp32 33 us through the ring, 27 so; of 83781 x 801 bf16 225 and 169,
+// backward 466 and 339.  Packs of two, 83676 x 802 bf16: backward 275 and 236, but the forward,
+// with more rows in flight through the ring, 140 and 148; wider packs lose in the backward too
+// (262144 x 1024 bf16: 0.67 ms and 0.71).
 template <int EPU, int V>
-constexpr bool kAhead = EPU == 1 && V <= 8;
+constexpr bool kAheadForward = EPU == 1 && V <= 8;
+template <int EPU, int V>
+constexpr bool kAheadBackward = EPU <= 2 && V * EPU <= 8;
 
 // Bytes of one ring stage for one thread: XS matrices of XT and BS of BT.
 template <typename XT, typename BT, int EPU, int V, int XS, int BS>
-constexpr int kRingBytes = kAhead<EPU, V> ? 0 : V * EPU * (XS * (int)sizeof(XT) + BS * (int)sizeof(BT));
+constexpr int kRingBytes = V * EPU * (XS * (int)sizeof(XT) + BS * (int)sizeof(BT));
 
 // One matrix's part of the ring, and its rows in memory: offsets and strides in bytes.
-template <typename T, int EPU, int V, bool WARP>
+template <typename T, int EPU, int V, bool WARP, bool AHEAD>
 struct Lane {
   using S = Slot<T, EPU>;
   using Sh = Share<V, WARP>;
   using K = Chunks<EPU, V>;
   uint32_t at, plane;  // this thread's place of the matrix in stage 0; bytes of a plane
-  uint32_t now[kAhead<EPU, V> ? V : 1], next[kAhead<EPU, V> ? V : 1];  // kAhead: the elements' bits
+  static constexpr int W = S::kBytes < 4 ? 1 : S::kBytes / 4;  // words of a pack
+  uint32_t now[AHEAD ? V * W : 1], next[AHEAD ? V * W : 1];  // AHEAD: the packs
   __device__ __forceinline__ Lane(uint32_t at_, uint32_t plane_) : at(at_), plane(plane_) {}
   __device__ __forceinline__ uint32_t pack(uint32_t stage, int i) const {
     return at + stage + i * plane;
@@ -372,23 +378,32 @@ struct Lane {
   __device__ __forceinline__ void fetch(uint32_t stage, const char* row, int left, const Sh& sh) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if constexpr (kAhead<EPU, V>) {
-        next[i] = 0;
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) next[i * W + w] = 0;
         if (sh.step(i) < left) {
-          if constexpr (sizeof(T) == 4) next[i] = *reinterpret_cast<const uint32_t*>(row + sh.step(i) * 4);
-          else next[i] = *reinterpret_cast<const uint16_t*>(row + sh.step(i) * 2);
+          const char* p = row + sh.step(i) * S::kBytes;
+          if constexpr (S::kBytes == 2) {
+            next[i] = *reinterpret_cast<const uint16_t*>(p);
+          } else if constexpr (S::kBytes == 4) {
+            next[i] = *reinterpret_cast<const uint32_t*>(p);
+          } else {
+            static_assert(S::kBytes == 8, "packs of up to two elements");
+            const uint2 q = *reinterpret_cast<const uint2*>(p);
+            next[i * 2] = q.x, next[i * 2 + 1] = q.y;
+          }
         }
       } else if (sh.step(i) < left) {
         S::fetch(pack(stage, i), row + sh.step(i) * S::kBytes);
       }
     }
   }
-  __device__ __forceinline__ void advance() {  // kAhead: the row fetched last becomes the current one
+  __device__ __forceinline__ void advance() {  // AHEAD: the row fetched last becomes the current one
 #pragma unroll
-    for (int i = 0; i < (kAhead<EPU, V> ? V : 0); ++i) now[i] = next[i];
+    for (int i = 0; i < (AHEAD ? V * W : 0); ++i) now[i] = next[i];
   }
   __device__ __forceinline__ void zero_tail(uint32_t stage, int left, const Sh& sh) const {
-    if constexpr (!kAhead<EPU, V>)
+    if constexpr (!AHEAD)
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (sh.step(i) >= left) S::zero(pack(stage, i));
@@ -396,10 +411,16 @@ struct Lane {
   __device__ __forceinline__ void read(uint32_t stage, int chunk, float (&v)[K::C]) const {
 #pragma unroll
     for (int p = 0; p < K::PP; ++p) {
-      if constexpr (kAhead<EPU, V>)
-        v[p] = __uint_as_float(sizeof(T) == 4 ? now[chunk * K::PP + p] : now[chunk * K::PP + p] << 16);
-      else
+      if constexpr (AHEAD) {
+        const int i = (chunk * K::PP + p) * W;
+#pragma unroll
+        for (int m = 0; m < EPU; ++m) {
+          if constexpr (sizeof(T) == 4) v[p * EPU + m] = __uint_as_float(now[i + m]);
+          else v[p * EPU + m] = __uint_as_float(m % 2 ? now[i + m / 2] & 0xFFFF0000u : now[i + m / 2] << 16);
+        }
+      } else {
         S::read(pack(stage, chunk * K::PP + p), v + p * EPU);
+      }
     }
   }
   static __device__ __forceinline__ void store(char* row, int chunk, const float (&v)[K::C], int left,

@@ -5,12 +5,12 @@ namespace emb {
 
 // GATE: a gate for each element.
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
-__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EPU > 8 || kAhead<EPU, V> ? 1 : 2) k_gated_norm(NormArgs a) {
+__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EPU > 8 || kAheadForward<EPU, V> ? 1 : 2) k_gated_norm(NormArgs a) {
   let_next_start();
   wait_for_earlier();
   using K = Chunks<EPU, V>;
-  using LX = Lane<XT, EPU, V, WARP>;
-  using LB = Lane<BT, EPU, V, WARP>;
+  using LX = Lane<XT, EPU, V, WARP, kAheadForward<EPU, V>>;
+  using LB = Lane<BT, EPU, V, WARP, kAheadForward<EPU, V>>;
   extern __shared__ __align__(16) char ring[];
   __shared__ __align__(16) float red_all[8 * 2 * 16];
   for (int i = threadIdx.x; i < 8 * 2 * 16; i += blockDim.x) red_all[i] = 0.f;
@@ -19,7 +19,8 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EP
   const Share<V, WARP> sh(grp.sub, a.tpr);
   const int left = a.packs - sh.first, tpr = a.tpr;
   const uint32_t plx = blockDim.x * LX::S::kBytes, plb = blockDim.x * LB::S::kBytes;
-  const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>;
+  const uint32_t stage_bytes =
+      kAheadForward<EPU, V> ? 0 : blockDim.x * kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>;
   const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::kBytes;
   const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::kBytes + V * plx;
   LX lx(tx, plx);
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EP
   // every group runs as many rounds as the CTA's first: shuffles and barriers stay whole
   for (uint32_t r0 = blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
     const bool live = row < a.n;
-    if constexpr (kAhead<EPU, V>) lx.advance(), ly.advance(), lg.advance();
+    if constexpr (kAheadForward<EPU, V>) lx.advance(), ly.advance(), lg.advance();
     fetch(row + (a.stages - 1) * step, st == 0 ? last : st - stage_bytes);
     float g_row = 1.f, rest;
     if (!GATE) row_gate.take(a, row + step, g_row, rest);
@@ -115,8 +116,8 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EP
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_fwd_v(NormArgs& a, cudaStream_t s) {
-  const int threads = a.rpb * a.tpr, per = (V * EPU > 8 || kAhead<EPU, V> ? 1 : 2) * kNormForward / threads;
-  const int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>, per, V * EPU > 8 ? a.tpr * 128 : 0);
+  const int threads = a.rpb * a.tpr, per = (V * EPU > 8 || kAheadForward<EPU, V> ? 1 : 2) * kNormForward / threads;
+  const int smem = norm_ring(a, kAheadForward<EPU, V> ? 0 : kRingBytes<XT, BT, EPU, V, 1, GATE ? 2 : 1>, per, V * EPU > 8 ? a.tpr * 128 : 0);
   constexpr auto kern = k_gated_norm<XT, BT, EPU, V, GATE, WARP>;
   const int64_t blocks = ((int64_t)a.n + a.rpb - 1) / a.rpb, cap = (int64_t)device_sms() * norm_fit(per, smem);
   const cudaError_t e = prepare_kernel<kern>();

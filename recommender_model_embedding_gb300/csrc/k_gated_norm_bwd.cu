@@ -5,12 +5,12 @@
 namespace emb {
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
-__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kAhead<EPU, V> ? kNormThreads : kNormBackward, V * EPU > 8 ? 1 : 2) k_gated_norm_bwd(NormArgs a) {
+__global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kAheadBackward<EPU, V> ? kNormThreads : kNormBackward, V * EPU > 8 ? 1 : 2) k_gated_norm_bwd(NormArgs a) {
   let_next_start();
   wait_for_earlier();
   using K = Chunks<EPU, V>;
-  using LX = Lane<XT, EPU, V, WARP>;
-  using LB = Lane<BT, EPU, V, WARP>;
+  using LX = Lane<XT, EPU, V, WARP, kAheadBackward<EPU, V>>;
+  using LB = Lane<BT, EPU, V, WARP, kAheadBackward<EPU, V>>;
   extern __shared__ __align__(16) char ring[];
   __shared__ __align__(16) float red_all[8 * 4 * 16];
   for (int i = threadIdx.x; i < 8 * 4 * 16; i += blockDim.x) red_all[i] = 0.f;
@@ -19,7 +19,8 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kAhead<EPU, V> ? kNo
   const Share<V, WARP> sh(grp.sub, a.tpr);
   const int left = a.packs - sh.first, tpr = a.tpr;
   const uint32_t plx = blockDim.x * LX::S::kBytes, plb = blockDim.x * LB::S::kBytes;
-  const uint32_t stage_bytes = blockDim.x * kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>;
+  const uint32_t stage_bytes =
+      kAheadBackward<EPU, V> ? 0 : blockDim.x * kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>;
   const uint32_t mx = V * plx, mb = V * plb;  // of a matrix
   const uint32_t tx = smem_at(ring) + threadIdx.x * LX::S::kBytes;
   const uint32_t tb = smem_at(ring) + threadIdx.x * LB::S::kBytes + 2 * mx;
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kAhead<EPU, V> ? kNo
   uint32_t st = 0;
   for (uint32_t r0 = blockIdx.x * a.rpb; r0 < a.n; r0 += step, row += step) {
     const bool live = row < a.n;
-    if constexpr (kAhead<EPU, V>) lx.advance(), lt.advance(), ld.advance(), ly.advance(), lg.advance();
+    if constexpr (kAheadBackward<EPU, V>) lx.advance(), lt.advance(), ld.advance(), ly.advance(), lg.advance();
     fetch(row + (a.stages - 1) * step, st == 0 ? last : st - stage_bytes);
     float g_row = 1.f, rest_row = 0.f;
     if (!GATE) row_gate.take(a, row + step, g_row, rest_row);
@@ -247,8 +248,8 @@ int64_t gated_norm_bwd_workspace(int64_t n, int dim) {
 
 template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
 static cudaError_t norm_bwd_v(NormArgs& a, int* parts, cudaStream_t s) {
-  const int threads = a.rpb * a.tpr, per = (V * EPU > 8 ? kNormWide : kAhead<EPU, V> ? 2 * kNormThreads : 2 * kNormBackward) / threads;
-  int smem = norm_ring(a, kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>, per, V * EPU > 8 ? a.tpr * 128 : 0);
+  const int threads = a.rpb * a.tpr, per = (V * EPU > 8 ? kNormWide : kAheadBackward<EPU, V> ? 2 * kNormThreads : 2 * kNormBackward) / threads;
+  int smem = norm_ring(a, kAheadBackward<EPU, V> ? 0 : kRingBytes<XT, BT, EPU, V, 2, GATE ? 3 : 2>, per, V * EPU > 8 ? a.tpr * 128 : 0);
   const int slices = a.tpr < 32 ? threads / 32 : a.rpb;
   const int cols = slices * 2 * a.dim * (int)sizeof(float);
   if (smem < cols) smem = cols;
@@ -261,7 +262,7 @@ static cudaError_t norm_bwd_v(NormArgs& a, int* parts, cudaStream_t s) {
 }
 
 struct NormBackward {
-  static constexpr int most(int epu) { return epu == 1 ? kNormThreads : kNormBackward; }
+  static constexpr int most(int epu) { return epu <= 2 ? kNormThreads : kNormBackward; }
   cudaStream_t s;
   int* parts;  // CTAs whose column sums are in the workspace (0: none to add)
   template <typename XT, typename BT, int EPU, int V, bool GATE, bool WARP>
