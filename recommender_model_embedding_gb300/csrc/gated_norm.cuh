@@ -18,8 +18,8 @@
 // Both are bound by HBM bandwidth while the elements are wide enough, and then by instruction
 // issue: the forward takes about 300 warp instructions a warp's share of a row (8 elements a
 // thread), the backward 530.  Measured with a gate for each element, 262144 x 1024: forward with
-// an fp32 stream and bf16 blocks 3.76 GB in 0.552 ms (6.80 TB/s, the measured copy rate), backward
-// all in bf16 4.29 GB in 0.67 ms (6.40 TB/s, 94%); without the gate's bytes the bf16 backward
+// an fp32 stream and bf16 blocks 3.76 GB in 0.555 ms (6.77 TB/s, the measured copy rate), backward
+// all in bf16 4.29 GB in 0.677 ms (6.34 TB/s, 93%); without the gate's bytes the bf16 backward
 // stays issue-bound (59% at 65536 x 2048, one gate a row; fp32 there 93%).
 //
 // A group of `tpr` threads takes a row, about eight elements a thread (V packs of EPU: 16 bytes
@@ -118,15 +118,40 @@ __device__ __forceinline__ void v_dot(float (&s)[2], const float (&a)[N], const 
     for (int m = 0; m < N; m += 2) fma2(s[0], s[1], a[m], a[m + 1], b[m], b[m + 1], s[0], s[1]);
 }
 
-// g = sigmoid(z) = 1 / (1 + e) and rest = 1 - g, with e = exp(-z), both to a few units in the
-// last place for moderate z: rest is taken as e g where that difference would cancel (z >= 0).
-// The fast exponential and reciprocal stand in for the exact ones, whose instructions bounded the
-// backward; the rounding of the exponent's product moves e by up to about |z| 2^-24 of itself.
-__device__ __forceinline__ void sigmoid2(float z, float& g, float& rest) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(1.f + e));
-  rest = z < 0.f ? 1.f - g : e * g;
+// g = sigmoid(z) = 1 / (1 + e) and rest = 1 - g = e g, with e = exp(-z), to a few units in the last
+// place at every z.  The fast exponential 2^t of t = -z / ln 2 alone would be off by the rounding
+// of t, about z 2^-24 of itself (58 units of 2^-24 in g at z = -80); with d = -z - t ln 2, which
+// is that rounding's size, e = 2^t exp(d) = 2^t (1 + d) to within d^2 < 2^-34.  z is held to where
+// e neither overflows nor leaves infinities to subtract in d: from 104 on e is zero in fp32 anyway,
+// and from -87.4 down g is zero, and rest too, which is only ever multiplied by g.  NaN stays.
+// In pairs, and with no choice between 1 - g and e g by the sign of z, this costs the backward little
+// (262144 x 1024 bf16 with a gate for each element: 666 us with 2^t alone, 677 so, 709 with expf).
+template <int N>
+__device__ __forceinline__ void v_sigmoid(const float (&gate)[N], float (&g)[N], float (&rest)[N]) {
+  constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f, kLn2Rest = -1.90465421e-9f;
+  constexpr int P = N < 2 ? 1 : 2;
+#pragma unroll
+  for (int m = 0; m < N; m += P) {
+    float z[P], t[P], d[P], e[P], q[P], one[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(z[i]) : "f"(-gate[m + i]), "f"(-104.f));
+      asm("min.NaN.f32 %0, %1, %2;" : "=f"(z[i]) : "f"(z[i]), "f"(88.f));
+      one[i] = 1.f;
+    }
+    v_mul(t, z, kLog2e);
+#pragma unroll
+    for (int i = 0; i < P; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(t[i]));
+    v_fma(d, t, -kLn2, z);
+    v_fma(d, t, -kLn2Rest, d);
+    v_fma(e, e, d, e);
+    v_fma(t, e, 1.f, one);
+#pragma unroll
+    for (int i = 0; i < P; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q[i]) : "f"(t[i]));
+    v_mul(e, e, q);
+#pragma unroll
+    for (int i = 0; i < P; ++i) g[m + i] = q[i], rest[m + i] = e[i];
+  }
 }
 
 // The ring: for each matrix and pack a plane of one place per thread.
@@ -467,11 +492,13 @@ struct RowGate {
   }
   // the gate fetched last, and 1 - gate; fetches the one of row `then`
   __device__ __forceinline__ void take(const NormArgs& a, uint32_t then, float& g, float& rest) {
-    float z[1];
+    float z[1], gs[1], rs[1];
     next.get(z);
     fetch(a, then);
     g = 1.f, rest = 0.f;
-    if (a.gate_row) sigmoid2(z[0], g, rest);
+    if (!a.gate_row) return;
+    v_sigmoid(z, gs, rs);
+    g = gs[0], rest = rs[0];
   }
 };
 

@@ -81,9 +81,9 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kNormForward, V * EP
           cw.use_rw(a, sh, i);
           v_mul(f[i], f[i], ry);
           if (GATE) {
-            lg.read(st, i, g);
-#pragma unroll
-            for (int m = 0; m < K::C; ++m) sigmoid2(g[m], g[m], rest);
+            float z[K::C], others[K::C];
+            lg.read(st, i, z);
+            v_sigmoid(z, g, others);
             v_mul(g, g, cw.rw);
           } else {
             v_mul(g, cw.rw, g_row);

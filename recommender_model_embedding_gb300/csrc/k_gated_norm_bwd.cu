@@ -114,10 +114,9 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kAheadBackward<EPU, 
           ly.read(st, i, y);
           v_mul(y, y, ry);
           if (GATE) {
-            float g[K::C];
-            lg.read(st, i, g);
-#pragma unroll
-            for (int m = 0; m < K::C; ++m) sigmoid2(g[m], g[m], rest[m]);
+            float z[K::C], g[K::C];
+            lg.read(st, i, z);
+            v_sigmoid(z, g, rest);
             v_mul(t, t, g);
           } else {
             v_mul(t, t, g_row);
