@@ -282,7 +282,8 @@ emb_status emb_dequantize_rows(const int8_t* d_q, const float* d_scale, int64_t 
  * its training step: rows sorted by expert and brought back, the norms, gate and scale around
  * a residual block, and the clipping of the dense gradients.  The source pages name none of
  * them; the formulas are stated at each call.  They need no context; every buffer is a device
- * buffer owned by the caller.  Matrices are rows of `dim` elements, fp32 (EMB_F32) or bf16
+ * buffer owned by the caller.  A call runs on the calling thread's current device, which has to be
+ * the one of its buffers and its stream (workspace sizes too are the current device's).  Matrices are rows of `dim` elements, fp32 (EMB_F32) or bf16
  * (EMB_BF16), with a row step (*_ld, in elements, below 2^30): an input may have any step >= 0
  * (0: one row for all), an output one of at least dim (any, for a single row).  Any alignment of the
  * element type serves; bases and steps on 16-byte boundaries are faster.  Sums are fp32 or

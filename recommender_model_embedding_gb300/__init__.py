@@ -249,6 +249,8 @@ def _stream(stream) -> Optional[int]:
 
 
 # ---- expert tower (context-free; arguments are checked and passed on by the _tower module) ----
+# A call's tensors, workspace and stream are on one device (else ValueError), and the call runs there
+# whichever device is current; the *_workspace sizes are the current device's.
 EXPERT_MAX, EXPERT_MAX_K, EXPERT_MAX_DIM, NORM_MAX_DIM = 1024, 16, 65536, 8192
 
 

@@ -6,13 +6,18 @@
 // as much as its launch; read from the tensor object itself they cost next to nothing.  Objects
 // that are not torch's own tensors are read through the same public attributes (dtype, shape,
 // stride(), data_ptr(), ...).  Every check comes before the library is called: a mismatch raises
-// ValueError, a status of the library the package's EmbError.
+// ValueError, a status of the library the package's EmbError.  A call's tensors, its workspace and
+// its stream are on one device, and that device is the current one while the library is called.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <cstdlib>
+#include <cstring>
 #include <exception>
+#include <string>
 #include <vector>
 
 #include "emb.h"
@@ -63,6 +68,21 @@ struct Seen {
   void* p = nullptr;
 };
 
+// The one device of a call: that of the first tensor seen.
+struct Device {
+  int index = -1;
+  c10::cuda::OptionalCUDAGuard guard;
+  void same(int other, const char* name) {
+    if (other < 0) return;  // an object that does not say
+    if (index < 0) index = other;
+    if (other != index) refuse("%s: on cuda:%d, the call's first tensor is on cuda:%d", name, other, index);
+  }
+  // makes it current until the call returns (where there is none, the library's call says so)
+  void enter() {
+    if (index >= 0 && c10::cuda::device_count() > 0) guard.set_index((c10::DeviceIndex)index);
+  }
+};
+
 Seen see_object(PyObject* o) {  // through attributes
   Seen s;
   const Ref dtype(PyObject_GetAttrString(o, "dtype"));
@@ -73,6 +93,13 @@ Seen see_object(PyObject* o) {  // through attributes
     if (std::string("torch.") + kKindNames[k] == text) s.kind = (Kind)k;
   const Ref cuda(PyObject_GetAttrString(o, "is_cuda"));
   s.cuda = truth(cuda.o);
+  if (s.cuda && PyObject_HasAttrString(o, "device")) {
+    const Ref device(PyObject_GetAttrString(o, "device"));
+    const Ref name(PyObject_Str(device.o));  // cuda:N
+    const char* text = PyUnicode_AsUTF8(name.o);
+    if (!text) throw Raised();
+    if (const char* colon = std::strchr(text, ':')) s.device = std::atoi(colon + 1);
+  }
   const Ref shape(PyObject_GetAttrString(o, "shape"));
   const Ref step(PyObject_CallMethod(o, "stride", nullptr));
   s.dims = PySequence_Size(shape.o);
@@ -90,9 +117,13 @@ Seen see_object(PyObject* o) {  // through attributes
   return s;
 }
 
-Seen see(PyObject* o, const char* name) {
+Seen see(PyObject* o, const char* name, Device& dev) {
   if (o == Py_None) refuse("%s: expected a CUDA tensor", name);
-  if (!THPVariable_CheckExact(o)) return see_object(o);
+  if (!THPVariable_CheckExact(o)) {
+    const Seen s = see_object(o);
+    if (s.cuda) dev.same(s.device, name);
+    return s;
+  }
   const at::Tensor& t = THPVariable_Unpack(o);
   Seen s;
   if (t.layout() != c10::kStrided) refuse("%s: expected a dense tensor", name);
@@ -107,7 +138,7 @@ Seen see(PyObject* o, const char* name) {
   s.cuda = t.is_cuda(), s.dense = t.is_contiguous();
   if (s.dims == 2)
     for (int i = 0; i < 2; ++i) s.size[i] = t.size(i), s.step[i] = t.stride(i);
-  if (s.cuda) s.device = t.get_device(), s.p = t.data_ptr();
+  if (s.cuda) s.device = t.get_device(), s.p = t.data_ptr(), dev.same(s.device, name);
   return s;
 }
 
@@ -135,12 +166,12 @@ Rows rows(const Seen& s, Kind kind, int64_t n, int64_t d, const char* name) {
   return {s.p, n > 1 ? s.step[0] : d};
 }
 
-Rows rows(PyObject* o, Kind kind, int64_t n, int64_t d, const char* name) {
-  return rows(see(o, name), kind, n, d, name);
+Rows rows(PyObject* o, Kind kind, int64_t n, int64_t d, const char* name, Device& dev) {
+  return rows(see(o, name, dev), kind, n, d, name);
 }
 
-Rows opt_rows(PyObject* o, Kind kind, int64_t n, int64_t d, const char* name) {
-  return o == Py_None ? Rows{} : rows(o, kind, n, d, name);
+Rows opt_rows(PyObject* o, Kind kind, int64_t n, int64_t d, const char* name, Device& dev) {
+  return o == Py_None ? Rows{} : rows(o, kind, n, d, name, dev);
 }
 
 // a contiguous CUDA tensor of the kind and at least n elements (`exact`: of n)
@@ -152,10 +183,12 @@ void* flat(const Seen& s, Kind kind, int64_t n, bool exact, const char* name) {
   return s.p;
 }
 
-void* flat(PyObject* o, Kind kind, int64_t n, const char* name) { return flat(see(o, name), kind, n, false, name); }
+void* flat(PyObject* o, Kind kind, int64_t n, const char* name, Device& dev) {
+  return flat(see(o, name, dev), kind, n, false, name);
+}
 
-void* vec(PyObject* o, int64_t d, const char* name) {  // optional float32 [d]
-  return o == Py_None ? nullptr : flat(see(o, name), F32, d, true, name);
+void* vec(PyObject* o, int64_t d, const char* name, Device& dev) {  // optional float32 [d]
+  return o == Py_None ? nullptr : flat(see(o, name, dev), F32, d, true, name);
 }
 
 int32_t fits_int(int64_t v, const char* name) {
@@ -163,9 +196,13 @@ int32_t fits_int(int64_t v, const char* name) {
   return (int32_t)v;
 }
 
-// the call's stream: the given one, or the current one of the tensor's device
-void* stream_of(PyObject* stream, const Seen& like) {
-  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)like.device).stream();
+// the call's stream: the given one, or the current one of the call's device
+void* stream_of(PyObject* stream, Device& dev) {
+  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
+  if (PyObject_HasAttrString(stream, "device_index")) {
+    const Ref index(PyObject_GetAttrString(stream, "device_index"));
+    dev.same((int)number(index.o), "stream");
+  }
   const Ref o(PyObject_GetAttrString(stream, "cuda_stream"));
   void* s = PyLong_AsVoidPtr(o.o);
   if (!s && PyErr_Occurred()) throw Raised();
@@ -179,12 +216,12 @@ struct Workspace {
   void* p = nullptr;
   int64_t bytes = 0;
   bool mine = false;
-  Workspace(int64_t need, PyObject* ws) {
+  Workspace(int64_t need, PyObject* ws, Device& dev) {
     if (need <= 0) return;
     bytes = need;
     mine = ws == Py_None;
     if (mine) return;
-    const Seen s = see(ws, "workspace");
+    const Seen s = see(ws, "workspace", dev);
     if (!s.cuda || !s.dense) refuse("workspace: expected a contiguous CUDA tensor");
     const Ref size(PyObject_CallMethod(ws, "element_size", nullptr));
     p = s.p, bytes = s.numel * number(size.o);
@@ -234,8 +271,8 @@ struct Places {
   int32_t k;
   const int32_t* p;
 };
-Places places(PyObject* pos, int64_t n) {
-  const Seen s = see(pos, "pos");
+Places places(PyObject* pos, int64_t n, Device& dev) {
+  const Seen s = see(pos, "pos", dev);
   if (n == 0 ? s.numel != 0 : (s.numel == 0 || s.numel % n))
     refuse("pos: %lld elements, expected a multiple of %lld rows", (long long)s.numel, (long long)n);
   const int64_t k = n ? s.numel / n : 1;
@@ -245,16 +282,18 @@ Places places(PyObject* pos, int64_t n) {
 // (ids, num_experts, order, pos, offsets, workspace, stream)
 PyObject* py_sort(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 7, [&]() -> PyObject* {
-    const Seen ids = see(a[0], "ids");
+    Device dev;
+    const Seen ids = see(a[0], "ids", dev);
     if (ids.dims != 2) refuse("ids: expected a matrix [n, k]");
     const int64_t n = ids.size[0], S = ids.numel;
     const int32_t k = fits_int(ids.size[1], "ids"), E = fits_int(number(a[1]), "num_experts");
     const auto* p = static_cast<const int64_t*>(flat(ids, I64, S, false, "ids"));
-    auto* order = static_cast<int32_t*>(flat(a[2], I32, S, "order"));
-    auto* pos = static_cast<int32_t*>(flat(a[3], I32, S, "pos"));
-    auto* offsets = static_cast<int32_t*>(flat(a[4], I32, (int64_t)E + 1, "offsets"));
-    Workspace ws(emb_expert_sort_workspace(n, k, E), a[5]);
-    void* s = stream_of(a[6], ids);
+    auto* order = static_cast<int32_t*>(flat(a[2], I32, S, "order", dev));
+    auto* pos = static_cast<int32_t*>(flat(a[3], I32, S, "pos", dev));
+    auto* offsets = static_cast<int32_t*>(flat(a[4], I32, (int64_t)E + 1, "offsets", dev));
+    dev.enter();
+    Workspace ws(emb_expert_sort_workspace(n, k, E), a[5], dev);
+    void* s = stream_of(a[6], dev);
     ws.take(s);
     return call("emb_expert_sort", [&] { return emb_expert_sort(p, n, k, E, order, pos, offsets, ws.p, ws.bytes, s); });
   });
@@ -263,12 +302,14 @@ PyObject* py_sort(PyObject*, PyObject* const* a, Py_ssize_t na) {
 // (x, pos, xs, stream)
 PyObject* py_dispatch(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 4, [&]() -> PyObject* {
-    const Seen m = see(a[0], "x");
+    Device dev;
+    const Seen m = see(a[0], "x", dev);
     const int32_t code = code_of(m, "x"), d = fits_int(m.size[1], "x");
     const int64_t n = m.size[0];
-    const Places pos = places(a[1], n);
-    const Rows x = rows(m, m.kind, n, d, "x"), xs = rows(a[2], m.kind, n * pos.k, d, "xs");
-    void* s = stream_of(a[3], m);
+    const Places pos = places(a[1], n, dev);
+    const Rows x = rows(m, m.kind, n, d, "x"), xs = rows(a[2], m.kind, n * pos.k, d, "xs", dev);
+    dev.enter();
+    void* s = stream_of(a[3], dev);
     return call("emb_expert_dispatch",
                 [&] { return emb_expert_dispatch(x.p, x.ld, pos.p, n, pos.k, d, code, xs.p, xs.ld, s); });
   });
@@ -277,12 +318,14 @@ PyObject* py_dispatch(PyObject*, PyObject* const* a, Py_ssize_t na) {
 // (dxs, pos, dx, stream)
 PyObject* py_dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 4, [&]() -> PyObject* {
-    const Seen m = see(a[2], "dx");
+    Device dev;
+    const Seen m = see(a[2], "dx", dev);
     const int32_t code = code_of(m, "dx"), d = fits_int(m.size[1], "dx");
     const int64_t n = m.size[0];
-    const Places pos = places(a[1], n);
-    const Rows in = rows(a[0], m.kind, n * pos.k, d, "dxs"), out = rows(m, m.kind, n, d, "dx");
-    void* s = stream_of(a[3], m);
+    const Places pos = places(a[1], n, dev);
+    const Rows in = rows(a[0], m.kind, n * pos.k, d, "dxs", dev), out = rows(m, m.kind, n, d, "dx");
+    dev.enter();
+    void* s = stream_of(a[3], dev);
     return call("emb_expert_dispatch_backward", [&] {
       return emb_expert_dispatch_backward(in.p, in.ld, pos.p, n, pos.k, d, code, out.p, out.ld, s);
     });
@@ -292,13 +335,15 @@ PyObject* py_dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
 // (ys, pos, w, out, stream)
 PyObject* py_combine(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 5, [&]() -> PyObject* {
-    const Seen m = see(a[3], "out");
+    Device dev;
+    const Seen m = see(a[3], "out", dev);
     const int32_t code = code_of(m, "out"), d = fits_int(m.size[1], "out");
     const int64_t n = m.size[0];
-    const Places pos = places(a[1], n);
-    const Rows in = rows(a[0], m.kind, n * pos.k, d, "ys"), out = rows(m, m.kind, n, d, "out");
-    const auto* w = static_cast<const float*>(flat(a[2], F32, n * pos.k, "w"));
-    void* s = stream_of(a[4], m);
+    const Places pos = places(a[1], n, dev);
+    const Rows in = rows(a[0], m.kind, n * pos.k, d, "ys", dev), out = rows(m, m.kind, n, d, "out");
+    const auto* w = static_cast<const float*>(flat(a[2], F32, n * pos.k, "w", dev));
+    dev.enter();
+    void* s = stream_of(a[4], dev);
     return call("emb_expert_combine", [&] {
       return emb_expert_combine(in.p, in.ld, pos.p, w, n, pos.k, d, code, out.p, out.ld, s);
     });
@@ -308,16 +353,18 @@ PyObject* py_combine(PyObject*, PyObject* const* a, Py_ssize_t na) {
 // (dout, ys, pos, w, dys, dw, stream)
 PyObject* py_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 7, [&]() -> PyObject* {
-    const Seen m = see(a[0], "dout");
+    Device dev;
+    const Seen m = see(a[0], "dout", dev);
     const int32_t code = code_of(m, "dout"), d = fits_int(m.size[1], "dout");
     const int64_t n = m.size[0];
-    const Places pos = places(a[2], n);
+    const Places pos = places(a[2], n, dev);
     const int64_t S = n * pos.k;
-    const Rows g = rows(m, m.kind, n, d, "dout"), y = rows(a[1], m.kind, S, d, "ys"),
-               dys = rows(a[4], m.kind, S, d, "dys");
-    const auto* w = static_cast<const float*>(flat(a[3], F32, S, "w"));
-    auto* dw = static_cast<float*>(flat(a[5], F32, S, "dw"));
-    void* s = stream_of(a[6], m);
+    const Rows g = rows(m, m.kind, n, d, "dout"), y = rows(a[1], m.kind, S, d, "ys", dev),
+               dys = rows(a[4], m.kind, S, d, "dys", dev);
+    const auto* w = static_cast<const float*>(flat(a[3], F32, S, "w", dev));
+    auto* dw = static_cast<float*>(flat(a[5], F32, S, "dw", dev));
+    dev.enter();
+    void* s = stream_of(a[6], dev);
     return call("emb_expert_combine_backward", [&] {
       return emb_expert_combine_backward(g.p, g.ld, y.p, y.ld, pos.p, w, n, pos.k, d, code, dys.p, dys.ld, dw, s);
     });
@@ -327,25 +374,26 @@ PyObject* py_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
 // Sizes and types of a gated-norm call: from the stream's matrix, and the block's matrices y or,
 // without them, `other` (h or its gradient).
 struct NormCall {
+  Device dev;
   emb_norm p{};
   Seen x;
   Kind xt, bt;
   int64_t n, d;
   NormCall(PyObject* xo, const char* xname, PyObject* y, PyObject* other, const char* oname, PyObject* gate)
-      : x(see(xo, xname)) {
+      : x(see(xo, xname, dev)) {
     p.x_dtype = p.dtype = code_of(x, xname);
     p.n = n = x.size[0];
     p.dim = fits_int(d = x.size[1], xname);
     xt = bt = x.kind;
     if (y != Py_None || other != Py_None) {
       const char* name = y != Py_None ? "y" : oname;
-      const Seen b = see(y != Py_None ? y : other, name);
+      const Seen b = see(y != Py_None ? y : other, name, dev);
       p.dtype = code_of(b, name), bt = b.kind;
     }
-    const Rows r = opt_rows(y, bt, n, d, "y");
+    const Rows r = opt_rows(y, bt, n, d, "y", dev);
     p.d_y = r.p, p.y_ld = r.ld;
     if (gate == Py_None) return;
-    const Seen g = see(gate, "gate");
+    const Seen g = see(gate, "gate", dev);
     if (g.dims != 2 || (g.size[1] != 1 && g.size[1] != d))
       refuse("gate: expected (%lld, 1) or (%lld, %lld)", (long long)n, (long long)n, (long long)d);
     p.gate_cols = (int32_t)g.size[1];
@@ -353,9 +401,9 @@ struct NormCall {
     p.d_gate = q.p, p.gate_ld = q.ld;
   }
   void vectors(PyObject* w_post, PyObject* res_scale, PyObject* w_pre, PyObject* eps) {
-    p.d_w_post = static_cast<const float*>(vec(w_post, d, "w_post"));
-    p.d_res_scale = static_cast<const float*>(vec(res_scale, d, "res_scale"));
-    p.d_w_pre = static_cast<const float*>(vec(w_pre, d, "w_pre"));
+    p.d_w_post = static_cast<const float*>(vec(w_post, d, "w_post", dev));
+    p.d_res_scale = static_cast<const float*>(vec(res_scale, d, "res_scale", dev));
+    p.d_w_pre = static_cast<const float*>(vec(w_pre, d, "w_pre", dev));
     p.eps = (float)PyFloat_AsDouble(eps);
     if (PyErr_Occurred()) throw Raised();
   }
@@ -366,11 +414,13 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 10, [&]() -> PyObject* {
     NormCall c(a[0], "x", a[1], a[3], "h", a[4]);
     emb_norm& p = c.p;
-    const Rows x = rows(c.x, c.xt, c.n, c.d, "x"), o = opt_rows(a[2], c.xt, c.n, c.d, "x_out"),
-               h = opt_rows(a[3], c.bt, c.n, c.d, "h");
+    Device& dev = c.dev;
+    const Rows x = rows(c.x, c.xt, c.n, c.d, "x"), o = opt_rows(a[2], c.xt, c.n, c.d, "x_out", dev),
+               h = opt_rows(a[3], c.bt, c.n, c.d, "h", dev);
     p.d_x = x.p, p.x_ld = x.ld, p.d_x_out = o.p, p.x_out_ld = o.ld, p.d_h = h.p, p.h_ld = h.ld;
     c.vectors(a[5], a[6], a[7], a[8]);
-    void* s = stream_of(a[9], c.x);
+    dev.enter();
+    void* s = stream_of(a[9], dev);
     return call("emb_gated_norm", [&] { return emb_gated_norm(&p, s); });
   });
 }
@@ -381,19 +431,21 @@ PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 17, [&]() -> PyObject* {
     NormCall c(a[2], "x_out", a[3], a[1], "dh", a[6]);
     emb_norm& p = c.p;
+    Device& dev = c.dev;
     const int64_t n = c.n, d = c.d;
-    const Rows x = rows(c.x, c.xt, n, d, "x_out"), t = opt_rows(a[0], c.xt, n, d, "dx_out"),
-               h = opt_rows(a[1], c.bt, n, d, "dh"), dx = opt_rows(a[4], c.xt, n, d, "dx"),
-               dy = opt_rows(a[5], c.bt, n, d, "dy"),
-               dg = opt_rows(a[10], c.bt, n, p.gate_cols ? p.gate_cols : d, "dgate");
+    const Rows x = rows(c.x, c.xt, n, d, "x_out"), t = opt_rows(a[0], c.xt, n, d, "dx_out", dev),
+               h = opt_rows(a[1], c.bt, n, d, "dh", dev), dx = opt_rows(a[4], c.xt, n, d, "dx", dev),
+               dy = opt_rows(a[5], c.bt, n, d, "dy", dev),
+               dg = opt_rows(a[10], c.bt, n, p.gate_cols ? p.gate_cols : d, "dgate", dev);
     p.d_x_out = x.p, p.x_out_ld = x.ld, p.d_dx_out = t.p, p.dx_out_ld = t.ld, p.d_dh = h.p, p.dh_ld = h.ld;
     p.d_dx = dx.p, p.dx_ld = dx.ld, p.d_dy = dy.p, p.dy_ld = dy.ld, p.d_dgate = dg.p, p.dgate_ld = dg.ld;
     c.vectors(a[7], a[8], a[9], a[14]);
-    p.d_dw_post = static_cast<float*>(vec(a[11], d, "dw_post"));
-    p.d_dres_scale = static_cast<float*>(vec(a[12], d, "dres_scale"));
-    p.d_dw_pre = static_cast<float*>(vec(a[13], d, "dw_pre"));
-    Workspace ws(emb_gated_norm_backward_workspace(p.n, p.dim), a[15]);
-    void* s = stream_of(a[16], c.x);
+    p.d_dw_post = static_cast<float*>(vec(a[11], d, "dw_post", dev));
+    p.d_dres_scale = static_cast<float*>(vec(a[12], d, "dres_scale", dev));
+    p.d_dw_pre = static_cast<float*>(vec(a[13], d, "dw_pre", dev));
+    dev.enter();
+    Workspace ws(emb_gated_norm_backward_workspace(p.n, p.dim), a[15], dev);
+    void* s = stream_of(a[16], dev);
     ws.take(s);
     return call("emb_gated_norm_backward", [&] { return emb_gated_norm_backward(&p, ws.p, ws.bytes, s); });
   });
@@ -402,6 +454,7 @@ PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
 // (grads, max_norm, norm, out, workspace, stream)
 PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 6, [&]() -> PyObject* {
+    Device dev;
     const Ref grads(PySequence_Fast(a[0], "grads: expected a list of tensors"));
     const Py_ssize_t count = PySequence_Fast_GET_SIZE(grads.o);
     const bool apart = a[3] != Py_None;
@@ -412,7 +465,7 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t na) {
     if (max_norm == -1.0 && PyErr_Occurred()) throw Raised();
     std::vector<emb_tensor> list((size_t)count);
     for (Py_ssize_t i = 0; i < count; ++i) {
-      const Seen g = see(PySequence_Fast_GET_ITEM(grads.o, i), "grads");
+      const Seen g = see(PySequence_Fast_GET_ITEM(grads.o, i), "grads", dev);
       if ((g.kind != F32 && g.kind != BF16) || !g.cuda || !g.dense)
         refuse("grads: expected contiguous CUDA tensors, float32 or bfloat16");
       emb_tensor& t = list[(size_t)i];
@@ -420,15 +473,16 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t na) {
       t.d_src = t.d_out = g.p;
       t.numel = g.numel;
       if (!apart) continue;
-      const Seen o = see(PySequence_Fast_GET_ITEM(out.o, i), "out");
+      const Seen o = see(PySequence_Fast_GET_ITEM(out.o, i), "out", dev);
       if (o.kind != g.kind || o.numel != g.numel || !o.cuda || !o.dense)
         refuse("out: expected a contiguous CUDA tensor of each gradient's type and size");
       t.d_out = o.p;
     }
-    const Seen norm = see(a[2], "norm");
+    const Seen norm = see(a[2], "norm", dev);
     auto* np = static_cast<float*>(flat(norm, F32, 1, false, "norm"));
-    Workspace ws(emb_clip_grads_workspace(count), a[4]);
-    void* s = stream_of(a[5], norm);
+    dev.enter();
+    Workspace ws(emb_clip_grads_workspace(count), a[4], dev);
+    void* s = stream_of(a[5], dev);
     ws.take(s);
     return call("emb_clip_grads", [&] {
       return emb_clip_grads(list.data(), count, (float)max_norm, np, ws.p, ws.bytes, s);

@@ -1,0 +1,57 @@
+"""What the binding of the expert-tower calls refuses about tensors that fit in type and size.  No GPU
+is needed."""
+import pytest
+
+from test_tower_checks import E, FakeCuda  # noqa: F401  (E: fixture)
+
+
+class On(FakeCuda):
+    """A tensor of the given device."""
+
+    def __init__(self, device, dtype, *shape, **kw):
+        super().__init__(dtype, *shape, **kw)
+        self.device = device
+
+
+class Stream:
+    cuda_stream, device_index = 0, 1
+
+
+def _calls(E):
+    """Every call with its tensors' types and shapes, in the call's order (None: left out)."""
+    n, k, d, e = 4, 2, 8, 8
+    f, i, x = "float32", "int32", ("float32", n, d)
+    xs, pos, w, v = ("float32", n * k, d), (i, n * k), (f, n, k), (f, d)
+    ws, m = ("uint8", 1 << 24), 40000  # (m rows: so many that the sort takes a workspace)
+    return [
+        (lambda t, **kw: E.expert_sort(t[0], e, *t[1:4], workspace=t[4], **kw),
+         [("int64", m, k), (i, m * k), (i, m * k), (i, e + 1), ws]),
+        (lambda t, **kw: E.expert_dispatch(*t, **kw), [x, pos, xs]),
+        (lambda t, **kw: E.expert_dispatch_backward(*t, **kw), [xs, pos, x]),
+        (lambda t, **kw: E.expert_combine(*t, **kw), [xs, pos, w, x]),
+        (lambda t, **kw: E.expert_combine_backward(*t, **kw), [x, xs, pos, w, xs, w]),
+        (lambda t, **kw: E.gated_norm(*t[:4], gate=t[4], w_post=t[5], res_scale=t[6], w_pre=t[7], **kw),
+         [x, x, x, x, x, v, v, v]),
+        (lambda t, **kw: E.gated_norm_backward(*t[:6], gate=t[6], w_post=t[7], res_scale=t[8], w_pre=t[9],
+                                               dgate=t[10], dw_post=t[11], dres_scale=t[12], dw_pre=t[13],
+                                               workspace=t[14], **kw),
+         [x] * 7 + [v, v, v] + [x] + [v, v, v] + [ws]),
+        (lambda t, **kw: E.clip_grads(t[:2], 1.0, t[4], out=t[2:4], workspace=t[5], **kw),
+         [(f, 9), (f, 5), (f, 9), (f, 5), (f, 1), ws]),
+    ]
+
+
+@pytest.mark.parametrize("call", range(8))
+def test_tensors_of_two_devices_are_refused(E, call):
+    run, specs = _calls(E)[call]
+    for i in range(len(specs)):
+        t = [On("cuda:1" if j == i else "cuda:0", *s) for j, s in enumerate(specs)]
+        with pytest.raises(ValueError, match="cuda:[01], the call's first tensor is on cuda:[01]"):
+            run(t)
+
+
+@pytest.mark.parametrize("call", range(8))
+def test_stream_of_another_device_is_refused(E, call):
+    run, specs = _calls(E)[call]
+    with pytest.raises(ValueError, match="stream: on cuda:1"):
+        run([On("cuda:0", *s) for s in specs], stream=Stream())
