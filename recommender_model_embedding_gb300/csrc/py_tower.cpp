@@ -187,6 +187,19 @@ void* flat(PyObject* o, Kind kind, int64_t n, const char* name, Device& dev) {
   return flat(see(o, name, dev), kind, n, false, name);
 }
 
+// a value for each slot of n rows of k: as flat(), and a matrix has to be k wide (one of another width
+// would be read and written as if its rows were k long)
+void* by_slot(const Seen& s, Kind kind, int64_t n, int64_t k, const char* name) {
+  if (s.dims == 2 && s.size[0] > 1 && s.size[1] > 1 && s.size[1] != k)
+    refuse("%s: (%lld, %lld), expected (%lld, %lld)", name, (long long)s.size[0], (long long)s.size[1],
+           (long long)n, (long long)k);
+  return flat(s, kind, n * k, false, name);
+}
+
+void* by_slot(PyObject* o, Kind kind, int64_t n, int64_t k, const char* name, Device& dev) {
+  return by_slot(see(o, name, dev), kind, n, k, name);
+}
+
 void* vec(PyObject* o, int64_t d, const char* name, Device& dev) {  // optional float32 [d]
   return o == Py_None ? nullptr : flat(see(o, name, dev), F32, d, true, name);
 }
@@ -276,7 +289,7 @@ Places places(PyObject* pos, int64_t n, Device& dev) {
   if (n == 0 ? s.numel != 0 : (s.numel == 0 || s.numel % n))
     refuse("pos: %lld elements, expected a multiple of %lld rows", (long long)s.numel, (long long)n);
   const int64_t k = n ? s.numel / n : 1;
-  return {fits_int(k, "pos"), static_cast<const int32_t*>(flat(s, I32, s.numel, false, "pos"))};
+  return {fits_int(k, "pos"), static_cast<const int32_t*>(by_slot(s, I32, n, k, "pos"))};
 }
 
 // (ids, num_experts, order, pos, offsets, workspace, stream)
@@ -289,7 +302,7 @@ PyObject* py_sort(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const int32_t k = fits_int(ids.size[1], "ids"), E = fits_int(number(a[1]), "num_experts");
     const auto* p = static_cast<const int64_t*>(flat(ids, I64, S, false, "ids"));
     auto* order = static_cast<int32_t*>(flat(a[2], I32, S, "order", dev));
-    auto* pos = static_cast<int32_t*>(flat(a[3], I32, S, "pos", dev));
+    auto* pos = static_cast<int32_t*>(by_slot(a[3], I32, n, k, "pos", dev));
     auto* offsets = static_cast<int32_t*>(flat(a[4], I32, (int64_t)E + 1, "offsets", dev));
     dev.enter();
     Workspace ws(emb_expert_sort_workspace(n, k, E), a[5], dev);
@@ -341,7 +354,7 @@ PyObject* py_combine(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const int64_t n = m.size[0];
     const Places pos = places(a[1], n, dev);
     const Rows in = rows(a[0], m.kind, n * pos.k, d, "ys", dev), out = rows(m, m.kind, n, d, "out");
-    const auto* w = static_cast<const float*>(flat(a[2], F32, n * pos.k, "w", dev));
+    const auto* w = static_cast<const float*>(by_slot(a[2], F32, n, pos.k, "w", dev));
     dev.enter();
     void* s = stream_of(a[4], dev);
     return call("emb_expert_combine", [&] {
@@ -361,8 +374,8 @@ PyObject* py_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const int64_t S = n * pos.k;
     const Rows g = rows(m, m.kind, n, d, "dout"), y = rows(a[1], m.kind, S, d, "ys", dev),
                dys = rows(a[4], m.kind, S, d, "dys", dev);
-    const auto* w = static_cast<const float*>(flat(a[3], F32, S, "w", dev));
-    auto* dw = static_cast<float*>(flat(a[5], F32, S, "dw", dev));
+    const auto* w = static_cast<const float*>(by_slot(a[3], F32, n, pos.k, "w", dev));
+    auto* dw = static_cast<float*>(by_slot(a[5], F32, n, pos.k, "dw", dev));
     dev.enter();
     void* s = stream_of(a[6], dev);
     return call("emb_expert_combine_backward", [&] {

@@ -55,3 +55,25 @@ def test_stream_of_another_device_is_refused(E, call):
     run, specs = _calls(E)[call]
     with pytest.raises(ValueError, match="stream: on cuda:1"):
         run([On("cuda:0", *s) for s in specs], stream=Stream())
+
+
+def test_slot_matrices_of_another_width_are_refused(E):
+    """A pos, w or dw whose rows are not k long would be taken apart at the wrong places."""
+    F = FakeCuda
+    x, xs, pos, w = F("float32", 4, 8), F("float32", 8, 8), F("int32", 8), F("float32", 4, 2)
+    wide, flipped = F("float32", 4, 3), F("float32", 2, 4)
+    for bad in (wide, flipped):
+        with pytest.raises(ValueError, match="w: .*expected .4, 2."):
+            E.expert_combine(xs, pos, bad, x)
+        with pytest.raises(ValueError, match="w: .*expected .4, 2."):
+            E.expert_combine_backward(x, xs, pos, bad, xs, w)
+        with pytest.raises(ValueError, match="dw: .*expected .4, 2."):
+            E.expert_combine_backward(x, xs, pos, w, xs, bad)
+    # the places of eight rows with the first four of them: not four rows of twice as many
+    many, room = F("int32", 8, 2), F("float32", 16, 8)
+    for call in (lambda: E.expert_dispatch(x, many, room), lambda: E.expert_dispatch_backward(room, many, x),
+                 lambda: E.expert_combine(room, many, F("float32", 16), x)):
+        with pytest.raises(ValueError, match="pos: .8, 2., expected .4, 4."):
+            call()
+    with pytest.raises(ValueError, match="pos: .4, 3., expected .4, 2."):
+        E.expert_sort(F("int64", 4, 2), 8, pos, F("int32", 4, 3), F("int32", 9))
