@@ -303,7 +303,7 @@ emb_status emb_dequantize_rows(const int8_t* d_q, const float* d_scale, int64_t 
  *   d_pos     [n*k] int32: pos[slot] = its place p, or -1 - p for a dropped slot
  *   d_offsets [E+1] int32: offsets[e] = first place of expert e; offsets[E] = kept slots
  * EMB_EINVAL: n < 0, k outside [1, EMB_EXPERT_MAX_K], E outside [1, EMB_EXPERT_MAX],
- * n*k >= 2^31, a NULL buffer, a short or misaligned workspace. */
+ * n*k >= 2^31, a NULL buffer or one misaligned for its type, a short or misaligned workspace. */
 int64_t emb_expert_sort_workspace(int64_t n, int32_t k, int32_t num_experts);
 emb_status emb_expert_sort(const int64_t* d_ids, int64_t n, int32_t k, int32_t num_experts,
                            int32_t* d_order, int32_t* d_pos, int32_t* d_offsets, void* d_ws,
@@ -314,7 +314,7 @@ emb_status emb_expert_sort(const int64_t* d_ids, int64_t n, int32_t k, int32_t n
  * each row's kept places: dx[i] = sum over kept j of dxs[pos[i*k + j]] (what a dropped slot's
  * place holds is not read).  A place outside [0, n*k) is neither read nor written.
  * EMB_EINVAL: sizes as above, dim outside [1, EMB_EXPERT_MAX_DIM], a bad dtype or row step, a
- * NULL buffer. */
+ * NULL buffer or one misaligned for its type. */
 emb_status emb_expert_dispatch(const void* d_x, int64_t x_ld, const int32_t* d_pos, int64_t n,
                                int32_t k, int32_t dim, int32_t dtype, void* d_xs, int64_t xs_ld,
                                void* stream);
@@ -351,8 +351,8 @@ emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, cons
  * Any of its outputs may be NULL; dx may be dx_out itself (same row step).  With d_y NULL, dy,
  * dgate, dw_post and dres_scale are NULL; with d_dh NULL, dw_pre is.
  * EMB_EINVAL: n outside [0, 2^31), dim outside [1, EMB_NORM_MAX_DIM], bad types, gate_cols or row
- * steps, eps not a positive finite number, a missing buffer, nothing to compute; the backward also for a
- * short or misaligned workspace. */
+ * steps, eps not a positive finite number, a missing buffer or one misaligned for its type, nothing to
+ * compute; the backward also for a short or misaligned workspace. */
 #define EMB_NORM_MAX_DIM 8192
 typedef struct emb_norm {
   int64_t n;

@@ -1135,6 +1135,8 @@ emb_status emb_expert_sort(const int64_t* d_ids, int64_t n, int32_t k, int32_t n
                            int64_t ws_bytes, void* stream) {
   const int64_t need = emb_expert_sort_workspace(n, k, num_experts);
   if (need < 0 || !d_offsets || (n > 0 && (!d_ids || !d_order || !d_pos))) return EMB_EINVAL;
+  if (!aligned_to(d_ids, 8) || !aligned_to(d_order, 4) || !aligned_to(d_pos, 4) || !aligned_to(d_offsets, 4))
+    return EMB_EINVAL;
   if (!ws_ok(d_ws, ws_bytes, need)) return EMB_EINVAL;
   return check_launch(launch_expert_sort(d_ids, n * k, num_experts, d_order, d_pos, d_offsets, d_ws,
                                          reinterpret_cast<cudaStream_t>(stream)));
@@ -1146,7 +1148,7 @@ emb_status emb_expert_dispatch(const void* d_x, int64_t x_ld, const int32_t* d_p
   if (!expert_rows_ok(n, k, dim, dtype) || !in_ld_ok(x_ld) || !out_ld_ok(xs_ld, n * k, dim)) return EMB_EINVAL;
   const int elem = dtype == EMB_BF16 ? 2 : 4;
   if (n > 0 && (!d_x || !d_pos || !d_xs)) return EMB_EINVAL;
-  if (!aligned_to(d_x, elem) || !aligned_to(d_xs, elem)) return EMB_EINVAL;
+  if (!aligned_to(d_x, elem) || !aligned_to(d_xs, elem) || !aligned_to(d_pos, 4)) return EMB_EINVAL;
   return check_launch(launch_expert_dispatch(d_x, x_ld, d_pos, n, k, dim, elem, d_xs, xs_ld,
                                              reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -1157,7 +1159,7 @@ emb_status emb_expert_dispatch_backward(const void* d_dxs, int64_t dxs_ld, const
   if (!expert_rows_ok(n, k, dim, dtype) || !in_ld_ok(dxs_ld) || !out_ld_ok(dx_ld, n, dim)) return EMB_EINVAL;
   const int elem = dtype == EMB_BF16 ? 2 : 4;
   if (n > 0 && (!d_dxs || !d_pos || !d_dx)) return EMB_EINVAL;
-  if (!aligned_to(d_dxs, elem) || !aligned_to(d_dx, elem)) return EMB_EINVAL;
+  if (!aligned_to(d_dxs, elem) || !aligned_to(d_dx, elem) || !aligned_to(d_pos, 4)) return EMB_EINVAL;
   return check_launch(launch_expert_combine(d_dxs, dxs_ld, d_pos, nullptr, n, k, dim,
                                             dtype == EMB_BF16, d_dx, dx_ld,
                                             reinterpret_cast<cudaStream_t>(stream)));
@@ -1169,7 +1171,8 @@ emb_status emb_expert_combine(const void* d_ys, int64_t ys_ld, const int32_t* d_
   if (!expert_rows_ok(n, k, dim, dtype) || !in_ld_ok(ys_ld) || !out_ld_ok(out_ld, n, dim)) return EMB_EINVAL;
   const int elem = dtype == EMB_BF16 ? 2 : 4;
   if (n > 0 && (!d_ys || !d_pos || !d_w || !d_out)) return EMB_EINVAL;
-  if (!aligned_to(d_ys, elem) || !aligned_to(d_out, elem)) return EMB_EINVAL;
+  if (!aligned_to(d_ys, elem) || !aligned_to(d_out, elem) || !aligned_to(d_pos, 4) || !aligned_to(d_w, 4))
+    return EMB_EINVAL;
   return check_launch(launch_expert_combine(d_ys, ys_ld, d_pos, d_w, n, k, dim, dtype == EMB_BF16,
                                             d_out, out_ld, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -1184,6 +1187,7 @@ emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, cons
   const int elem = dtype == EMB_BF16 ? 2 : 4;
   if (n > 0 && (!d_dout || !d_ys || !d_pos || !d_w || !d_dys || !d_dw)) return EMB_EINVAL;
   if (!aligned_to(d_dout, elem) || !aligned_to(d_ys, elem) || !aligned_to(d_dys, elem)) return EMB_EINVAL;
+  if (!aligned_to(d_pos, 4) || !aligned_to(d_w, 4) || !aligned_to(d_dw, 4)) return EMB_EINVAL;
   return check_launch(launch_expert_combine_bwd(d_dout, dout_ld, d_ys, ys_ld, d_pos, d_w, n, k, dim,
                                                 dtype == EMB_BF16, d_dys, dys_ld, d_dw,
                                                 reinterpret_cast<cudaStream_t>(stream)));
@@ -1204,6 +1208,9 @@ static bool norm_ok(const emb_norm* p) {
   const int xe = p->x_dtype == EMB_BF16 ? 2 : 4, be = p->dtype == EMB_BF16 ? 2 : 4;
   const void* xs[] = {p->d_x, p->d_x_out, p->d_dx_out, p->d_dx};
   const void* bs[] = {p->d_y, p->d_gate, p->d_h, p->d_dh, p->d_dy, p->d_dgate};
+  const void* vs[] = {p->d_w_post, p->d_res_scale, p->d_w_pre, p->d_dw_post, p->d_dres_scale, p->d_dw_pre};
+  for (const void* q : vs)
+    if (!aligned_to(q, 4)) return false;
   for (const void* q : xs)
     if (!aligned_to(q, xe)) return false;
   for (const void* q : bs)
@@ -1251,7 +1258,8 @@ int64_t emb_clip_grads_workspace(int64_t count) {
 emb_status emb_clip_grads(const emb_tensor* h_list, int64_t count, float max_norm, float* d_norm,
                           void* d_ws, int64_t ws_bytes, void* stream) {
   const int64_t need = emb_clip_grads_workspace(count);
-  if (need < 0 || (count > 0 && !h_list) || !d_norm || !(max_norm >= 0.f)) return EMB_EINVAL;
+  if (need < 0 || (count > 0 && !h_list) || !aligned_to(d_norm, 4) || !d_norm || !(max_norm >= 0.f))
+    return EMB_EINVAL;
   int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
     const emb_tensor& t = h_list[i];

@@ -1,8 +1,9 @@
-"""What the binding of the expert-tower calls refuses about tensors that fit in type and size.  No GPU
-is needed."""
+"""What the expert-tower calls refuse about buffers that fit in type and size.  No GPU is needed."""
+import ctypes
+
 import pytest
 
-from test_tower_checks import E, FakeCuda  # noqa: F401  (E: fixture)
+from test_tower_checks import E, FakeCuda, P, _norm  # noqa: F401  (E: fixture)
 
 
 class On(FakeCuda):
@@ -77,3 +78,29 @@ def test_slot_matrices_of_another_width_are_refused(E):
             call()
     with pytest.raises(ValueError, match="pos: .4, 3., expected .4, 2."):
         E.expert_sort(F("int64", 4, 2), 8, pos, F("int32", 4, 3), F("int32", 9))
+
+
+def test_c_calls_refuse_misaligned_buffers(E):
+    """Every index, weight and vector buffer is on a boundary of its type: a kernel's access to one that
+    is not would fault."""
+    L, q, bad = E._lib, P + 2, E.EMB_EINVAL
+    for i in range(4):
+        b = [P] * 4
+        b[i] = P + 4 if i == 0 else q
+        assert L.emb_expert_sort(b[0], 4, 2, 8, b[1], b[2], b[3], P, 1 << 20, None) == bad
+    assert L.emb_expert_dispatch(P, 8, q, 4, 2, 8, 1, P, 8, None) == bad
+    assert L.emb_expert_dispatch_backward(P, 8, q, 4, 2, 8, 1, P, 8, None) == bad
+    assert L.emb_expert_combine(P, 8, q, P, 4, 2, 8, 1, P, 8, None) == bad
+    assert L.emb_expert_combine(P, 8, P, q, 4, 2, 8, 1, P, 8, None) == bad
+    for i in range(3):
+        b = [P] * 3
+        b[i] = q
+        assert L.emb_expert_combine_backward(P, 8, P, 8, b[0], b[1], 4, 2, 8, 1, P, 8, b[2], None) == bad
+    for name in ("d_w_post", "d_res_scale", "d_w_pre"):
+        assert L.emb_gated_norm(ctypes.byref(_norm(E, **{name: q})), None) == bad
+    grad = dict(d_x=None, d_h=None, d_dx_out=P, d_dh=P, d_dx=P, d_dy=P, dx_out_ld=8, dh_ld=8, dx_ld=8, dy_ld=8)
+    for name in ("d_w_post", "d_res_scale", "d_w_pre", "d_dw_post", "d_dres_scale", "d_dw_pre"):
+        a = _norm(E, **grad, **{name: q})
+        assert L.emb_gated_norm_backward(ctypes.byref(a), P, 1 << 40, None) == bad
+    one = (E.EmbTensor * 1)(E.EmbTensor(d_src=P, d_out=P, numel=4, dtype=0))
+    assert L.emb_clip_grads(one, 1, 1.0, q, P, 1 << 20, None) == bad
