@@ -79,7 +79,8 @@ struct Device {
   }
   // makes it current until the call returns (where there is none, the library's call says so)
   void enter() {
-    if (index >= 0 && c10::cuda::device_count() > 0) guard.set_index((c10::DeviceIndex)index);
+    if (index < 0 || c10::cuda::device_count() == 0 || c10::cuda::current_device() == index) return;
+    guard.set_index((c10::DeviceIndex)index);
   }
 };
 
