@@ -381,7 +381,8 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
 
 /* Global gradient norm and clipping over `count` tensors: *d_norm = sqrt(sum of g^2 over all
  * of them), out = g * min(1, max_norm / norm).  The squares' sums are fp64 beyond groups of a
- * few elements, so neither huge nor tiny finite gradients lose the norm.  A norm that is
+ * few elements, so neither huge nor tiny finite gradients lose the norm, and a factor below fp32's
+ * normal numbers keeps its bits.  A norm that is
  * infinite or NaN in fp32 clips nothing: the outputs equal the gradients, and the caller sees
  * the norm.  h_list: host array, read before the call returns; d_out may be d_src (in place) or
  * a buffer of the same type that overlaps no other.  numel may be 0, and count too (norm 0).

@@ -143,8 +143,15 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
 
+// The factor as c * back, back a power of two: one so small that fp32 would hold it with few bits
+// or as zero is carried by c near one, and the product's exponent by back, applied last.
+struct Factor {
+  float c, back;
+  __device__ __forceinline__ float operator()(float v) const { return v * c * back; }
+};
+
 template <int THREADS, typename T, int EPU>
-__device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, float c) {
+__device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, Factor c) {
   constexpr int U = 4;
   const int64_t packs = n / EPU;
   for (int64_t c0 = threadIdx.x; c0 < packs; c0 += THREADS * U) {
@@ -158,7 +165,7 @@ __device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, float c)
         float f[EPU];
         v[u].get(f);
 #pragma unroll
-        for (int m = 0; m < EPU; ++m) f[m] *= c;
+        for (int m = 0; m < EPU; ++m) f[m] = c(f[m]);
         v[u].set(f);
         v[u].store(o + (c0 + u * THREADS) * EPU);
       }
@@ -169,7 +176,7 @@ __device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, float c)
       v.load(p + i);
       float f[1];
       v.get(f);
-      f[0] *= c;
+      f[0] = c(f[0]);
       v.set(f);
       v.store(o + i);
     }
@@ -177,7 +184,7 @@ __device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, float c)
 
 // Tiles t0, t0 - step, ... scaled by c.
 template <int THREADS, int N>
-__device__ __forceinline__ void share_scale(const ClipList<N>& l, int64_t t0, int64_t step, float c) {
+__device__ __forceinline__ void share_scale(const ClipList<N>& l, int64_t t0, int64_t step, Factor c) {
   for (int64_t t = t0; t >= 0; t -= step) {
     const int i = clip_tensor(l, t);
     const int64_t at = (t - l.first[i]) * l.tile;
@@ -198,10 +205,16 @@ __device__ __forceinline__ void share_scale(const ClipList<N>& l, int64_t t0, in
 
 // The factor of a sum of squares (negative: nothing is to be scaled).  A norm that is infinite
 // or NaN scales nothing: the caller sees it and drops the step.  One thread's work (fp64).
-__device__ __forceinline__ float clip_factor(double squares, float max_norm, float& norm) {
+__device__ __forceinline__ Factor clip_factor(double squares, float max_norm, float& norm) {
   const double n = sqrt(squares);
   norm = (float)n;
-  return n > (double)max_norm && isfinite(norm) ? (float)((double)max_norm / n) : -1.f;
+  if (!(n > (double)max_norm && isfinite(norm))) return {-1.f, 1.f};
+  const double f = (double)max_norm / n;
+  if (f >= 0x1p-64 || f == 0.0) return {(float)f, 1.f};
+  int x;
+  frexp(f, &x);  // f < 2^x, and 2^x is in fp32 from 2^-149 on
+  if (x < -149) x = -149;
+  return {(float)ldexp(f, -x), (float)ldexp(1.0, x)};
 }
 
 // Every CTA adds up all `parts` itself (a few KB from L2).  The tiles are taken from the last to
@@ -210,7 +223,7 @@ template <int N>
 __global__ void __launch_bounds__(kClipThreads, kClipScaleCtasPerSm)
     k_clip_scale(const __grid_constant__ ClipList<N> l, const double* part, int parts, float max_norm,
                  float* norm_out, int inplace) {
-  __shared__ float factor;
+  __shared__ Factor factor;
   let_next_start();
   wait_for_earlier();
   double acc = 0.0;
@@ -223,9 +236,12 @@ __global__ void __launch_bounds__(kClipThreads, kClipScaleCtasPerSm)
     if (blockIdx.x == 0) *norm_out = norm;
   }
   __syncthreads();
-  const float c = factor;
-  if (c < 0.f && inplace) return;
-  share_scale<kClipThreads>(l, l.first[l.count] - 1 - blockIdx.x, gridDim.x, c < 0.f ? 1.f : c);
+  Factor c = factor;
+  if (c.c < 0.f) {
+    if (inplace) return;
+    c.c = 1.f;
+  }
+  share_scale<kClipThreads>(l, l.first[l.count] - 1 - blockIdx.x, gridDim.x, c);
 }
 
 int64_t clip_grads_workspace(int64_t count) {

@@ -41,3 +41,25 @@ def test_gate_is_as_exact_far_from_zero(E, cols):
     # one gate a row: d equal terms are added, of 8 a thread and then in pairs (at most 16 u more)
     off = ((dgate.double() - ref) / ref).abs().max().item()
     assert off <= (32 if cols == "full" else 48) * U32, off / U32
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("limit", [1.0, 1e-3, 1e-6, 1e-20, 1e-36])
+def test_clip_factors_below_normal_numbers(E, limit, dtype):
+    """A factor that fp32 alone would hold with few bits, or as zero.  The norm is within 20 u (16
+    squares a sum in fp32, fp64 beyond, one rounding), the factor and its two products round
+    three times, then the output rounds once; a result below the normal numbers keeps what its type
+    has there."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    grads = [(torch.randn(m, generator=g, device="cuda").clamp(-3, 3) * 1e37).to(dtype) for m in (64, 7)]
+    grads.append((torch.randn(900, generator=g, device="cuda") * 1e20).to(dtype))
+    full = torch.cat([x.double() for x in grads]).norm().item()
+    norm, out = torch.empty(1, device="cuda"), [torch.empty_like(x) for x in grads]
+    E.clip_grads(grads, limit, norm, out=out)
+    assert abs(norm.item() - full) <= 20 * U32 * full
+    c = torch.tensor(limit, device="cuda").double() / full
+    r, least = (U32, 2.0 ** -149) if dtype == torch.float32 else (2.0 ** -8, 2.0 ** -133)
+    for x, o in zip(grads, out):
+        ref = x.double() * c
+        assert bool(((o.double() - ref).abs() <= (24 * U32 + r) * ref.abs() + least).all())
