@@ -250,7 +250,8 @@ def _stream(stream) -> Optional[int]:
 
 # ---- expert tower (context-free; arguments are checked and passed on by the _tower module) ----
 # A call's tensors, workspace and stream are on one device (else ValueError), and the call runs there
-# whichever device is current; the *_workspace sizes are the current device's.
+# whichever device is current; the *_workspace sizes are the current device's.  The calls are no
+# autograd functions; what one writes counts as changed in place, so a backward that saved it says so.
 EXPERT_MAX, EXPERT_MAX_K, EXPERT_MAX_DIM, NORM_MAX_DIM = 1024, 16, 65536, 8192
 
 

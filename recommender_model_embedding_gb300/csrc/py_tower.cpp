@@ -17,6 +17,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <exception>
+#include <initializer_list>
 #include <string>
 #include <vector>
 
@@ -251,9 +252,18 @@ struct Workspace {
   }
 };
 
-// the library's call without the interpreter's lock; its status as an exception
+// A tensor that a call has written is new to autograd, as after torch's own operations in place: a
+// backward that saved what it held before says so.
+void wrote(PyObject* o) {
+  if (o == Py_None || !THPVariable_Check(o)) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();  // (those have no versions)
+}
+
+// the library's call without the interpreter's lock; its status as an exception.  `outs`: what it
+// writes
 template <typename F>
-PyObject* call(const char* name, F f) {
+PyObject* call(const char* name, std::initializer_list<PyObject*> outs, F f) {
   emb_status st;
   Py_BEGIN_ALLOW_THREADS;
   st = f();
@@ -262,6 +272,7 @@ PyObject* call(const char* name, F f) {
     const Ref pkg(PyImport_ImportModule(kPackage));
     const Ref raised(PyObject_CallMethod(pkg.o, "_check", "si", name, (int)st));  // raises
   }
+  for (PyObject* o : outs) wrote(o);
   Py_RETURN_NONE;
 }
 
@@ -309,7 +320,9 @@ PyObject* py_sort(PyObject*, PyObject* const* a, Py_ssize_t na) {
     Workspace ws(emb_expert_sort_workspace(n, k, E), a[5], dev);
     void* s = stream_of(a[6], dev);
     ws.take(s);
-    return call("emb_expert_sort", [&] { return emb_expert_sort(p, n, k, E, order, pos, offsets, ws.p, ws.bytes, s); });
+    return call("emb_expert_sort", {a[2], a[3], a[4]}, [&] {
+      return emb_expert_sort(p, n, k, E, order, pos, offsets, ws.p, ws.bytes, s);
+    });
   });
 }
 
@@ -324,7 +337,7 @@ PyObject* py_dispatch(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const Rows x = rows(m, m.kind, n, d, "x"), xs = rows(a[2], m.kind, n * pos.k, d, "xs", dev);
     dev.enter();
     void* s = stream_of(a[3], dev);
-    return call("emb_expert_dispatch",
+    return call("emb_expert_dispatch", {a[2]},
                 [&] { return emb_expert_dispatch(x.p, x.ld, pos.p, n, pos.k, d, code, xs.p, xs.ld, s); });
   });
 }
@@ -340,7 +353,7 @@ PyObject* py_dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const Rows in = rows(a[0], m.kind, n * pos.k, d, "dxs", dev), out = rows(m, m.kind, n, d, "dx");
     dev.enter();
     void* s = stream_of(a[3], dev);
-    return call("emb_expert_dispatch_backward", [&] {
+    return call("emb_expert_dispatch_backward", {a[2]}, [&] {
       return emb_expert_dispatch_backward(in.p, in.ld, pos.p, n, pos.k, d, code, out.p, out.ld, s);
     });
   });
@@ -358,7 +371,7 @@ PyObject* py_combine(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const auto* w = static_cast<const float*>(by_slot(a[2], F32, n, pos.k, "w", dev));
     dev.enter();
     void* s = stream_of(a[4], dev);
-    return call("emb_expert_combine", [&] {
+    return call("emb_expert_combine", {a[3]}, [&] {
       return emb_expert_combine(in.p, in.ld, pos.p, w, n, pos.k, d, code, out.p, out.ld, s);
     });
   });
@@ -379,7 +392,7 @@ PyObject* py_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     auto* dw = static_cast<float*>(by_slot(a[5], F32, n, pos.k, "dw", dev));
     dev.enter();
     void* s = stream_of(a[6], dev);
-    return call("emb_expert_combine_backward", [&] {
+    return call("emb_expert_combine_backward", {a[4], a[5]}, [&] {
       return emb_expert_combine_backward(g.p, g.ld, y.p, y.ld, pos.p, w, n, pos.k, d, code, dys.p, dys.ld, dw, s);
     });
   });
@@ -435,7 +448,7 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t na) {
     c.vectors(a[5], a[6], a[7], a[8]);
     dev.enter();
     void* s = stream_of(a[9], dev);
-    return call("emb_gated_norm", [&] { return emb_gated_norm(&p, s); });
+    return call("emb_gated_norm", {a[1] != Py_None ? a[2] : Py_None, a[3]}, [&] { return emb_gated_norm(&p, s); });
   });
 }
 
@@ -461,7 +474,8 @@ PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     Workspace ws(emb_gated_norm_backward_workspace(p.n, p.dim), a[15], dev);
     void* s = stream_of(a[16], dev);
     ws.take(s);
-    return call("emb_gated_norm_backward", [&] { return emb_gated_norm_backward(&p, ws.p, ws.bytes, s); });
+    return call("emb_gated_norm_backward", {a[4], a[5], a[10], a[11], a[12], a[13]},
+                [&] { return emb_gated_norm_backward(&p, ws.p, ws.bytes, s); });
   });
 }
 
@@ -498,9 +512,11 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t na) {
     Workspace ws(emb_clip_grads_workspace(count), a[4], dev);
     void* s = stream_of(a[5], dev);
     ws.take(s);
-    return call("emb_clip_grads", [&] {
+    PyObject* done = call("emb_clip_grads", {a[2]}, [&] {
       return emb_clip_grads(list.data(), count, (float)max_norm, np, ws.p, ws.bytes, s);
     });
+    for (Py_ssize_t i = 0; i < count; ++i) wrote(PySequence_Fast_GET_ITEM(apart ? out.o : grads.o, i));
+    return done;
   });
 }
 

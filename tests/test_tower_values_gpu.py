@@ -63,3 +63,70 @@ def test_clip_factors_below_normal_numbers(E, limit, dtype):
     for x, o in zip(grads, out):
         ref = x.double() * c
         assert bool(((o.double() - ref).abs() <= (24 * U32 + r) * ref.abs() + least).all())
+
+
+def _each_call(E, make):
+    """(call, inputs, outputs) of every tower call, on tensors from make(shape, dtype)."""
+    n, k, d, e = 6, 2, 16, 4
+    f, i = torch.float32, torch.int32
+    x, w, xs = lambda: make((n, d), f), lambda: make((n, k), f), lambda: make((n * k, d), f)
+    ids, pos = make((n, k), torch.int64), make((n * k,), i)
+    o3 = make((n * k,), i), make((n * k,), i), make((e + 1,), i)
+    yield lambda: E.expert_sort(ids, e, *o3), [ids], o3
+    E.expert_sort(ids, e, make((n * k,), i), pos, make((e + 1,), i))
+    a, b = x(), xs()
+    yield lambda: E.expert_dispatch(a, pos, b), [a, pos], [b]
+    c, dd = xs(), x()
+    yield lambda: E.expert_dispatch_backward(c, pos, dd), [c, pos], [dd]
+    y, ww, o = xs(), w(), x()
+    yield lambda: E.expert_combine(y, pos, ww, o), [y, pos, ww], [o]
+    do, dy, dw = x(), xs(), w()
+    yield lambda: E.expert_combine_backward(do, y, pos, ww, dy, dw), [do, y, pos, ww], [dy, dw]
+    g, h, v = x(), x(), [make((d,), f) for _ in range(6)]
+    yield lambda: E.gated_norm(a, do, o, h, gate=g, w_post=v[0]), [a, do, g, v[0]], [o, h]
+    dx, dy2, dg = x(), x(), x()
+    yield (lambda: E.gated_norm_backward(a, h, o, do, dx, dy2, gate=g, w_post=v[0], dgate=dg, dw_post=v[3],
+                                         dres_scale=v[4], dw_pre=v[5]), [a, h, o, do, g, v[0]], [dx, dy2, dg] + v[3:])
+    norm, into = make((1,), f), [x(), xs()]
+    yield lambda: E.clip_grads([dx, dy], 1.0, norm, out=into), [dx, dy], into + [norm]
+    yield lambda: E.clip_grads(into, 1.0, norm), [], into + [norm]
+
+
+def _make(shape, dtype):
+    if dtype.is_floating_point:
+        return torch.randn(shape, device="cuda").to(dtype)
+    return torch.randint(0, 4, shape, dtype=dtype, device="cuda")
+
+
+def test_written_tensors_are_new_to_autograd(E):
+    for call, ins, outs in _each_call(E, _make):
+        before = [t._version for t in ins], [t._version for t in outs]
+        call()
+        assert [t._version for t in ins] == before[0]
+        assert all(t._version > b for t, b in zip(outs, before[1]))
+    x = torch.randn((5, 16), device="cuda", requires_grad=True)
+    kept = x.exp()  # its backward needs the values it has now
+    E.gated_norm(x.detach(), None, None, kept)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        kept.sum().backward()
+    # an x_out beside no block is not written
+    unwritten = torch.zeros((5, 16), device="cuda")
+    E.gated_norm(x.detach(), None, unwritten, kept)
+    assert unwritten._version == 0 and not bool(unwritten.any())
+
+
+def test_inference_tensors_and_subclasses(E):
+    """Tensors without versions, and tensors of a subclass of torch's, are taken like any other."""
+    class Named(torch.Tensor):
+        pass
+
+    with torch.inference_mode():
+        for call, _, _ in _each_call(E, _make):
+            call()
+    for call, _, _ in _each_call(E, lambda s, t: _make(s, t).as_subclass(Named)):
+        call()
+    x, y = _make((9, 33), torch.float32), _make((9, 33), torch.float32)
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    E.gated_norm(x, y, a, None)
+    E.gated_norm(x.as_subclass(Named), y.as_subclass(Named), b.as_subclass(Named), None)
+    assert torch.equal(a, b)
