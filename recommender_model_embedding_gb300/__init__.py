@@ -24,17 +24,18 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 TOWER_PATH = os.path.join(_HERE, "_tower.so")
-if not os.path.exists(TOWER_PATH):
-    raise ImportError(f"{TOWER_PATH} is missing: build the library first "
-                      "(python recommender_model_embedding_gb300/build.py)")
 
 
 class _LoadTower:
     """Stands in for the compiled module of the tower's calls until the first of them: the module
-    needs torch, and the rest of the package imports without it."""
+    needs torch, and the rest of the package imports and runs without either."""
 
     def __getattr__(self, name):
         import importlib
+
+        if not os.path.exists(TOWER_PATH):
+            raise ImportError(f"{TOWER_PATH} is missing: the tower's calls need it, built with torch "
+                              "installed (python recommender_model_embedding_gb300/build.py)")
 
         import torch  # noqa: F401  (its libraries have to be there first)
         # importing a submodule also puts it in this stand-in's place

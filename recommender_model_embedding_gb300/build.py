@@ -4,7 +4,8 @@ Each .cu file under csrc/ is compiled to an object in parallel, then linked into
 library next to this file.  The CUDA runtime is linked statically, so the library loads
 on a machine without a GPU (it only needs the driver when a call reaches the device).  The
 Python side of the expert tower's calls (csrc/py_tower.cpp, against torch's headers) becomes
-_tower.so beside it, linked to the library.
+_tower.so beside it, linked to the library; the library itself needs no torch, and where there is
+none it is all that is built.
 """
 from __future__ import annotations
 
@@ -46,10 +47,16 @@ def gxx() -> str:
     return shutil.which("g++") or "g++"
 
 
-def torch_dirs(what: str):
-    """torch's include or lib directories (found without importing it)."""
+def torch_root():
+    """Where torch is installed (found without importing it); None: nowhere."""
     import importlib.util
-    root = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def torch_dirs(what: str):
+    """torch's include or lib directories."""
+    root = torch_root()
     if what == "lib":
         return [os.path.join(root, "lib")]
     inc = os.path.join(root, "include")
@@ -75,12 +82,11 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     todo = [(s, o) for s, o in zip(srcs, objs) if force or _stale(o, s)]
-    if force or _stale(TOWER_OBJ, TOWER_SRC):
-        todo.insert(0, (TOWER_SRC, TOWER_OBJ))
+    tower = torch_root() is not None
+    tower_todo = tower and (force or _stale(TOWER_OBJ, TOWER_SRC))
     nv = nvcc()
 
-    def compile_one(so):
-        s, o = so
+    def compile_one(s, o):
         tmp = o + f".tmp{os.getpid()}"
         cmd = ([nv] + _flags(verbose) if s != TOWER_SRC else [gxx()] + _tower_flags()) + ["-c", s, "-o", tmp]
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -89,10 +95,9 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
         os.replace(tmp, o)
         return r.stderr
 
-    logs = []
-    if todo:
-        with cf.ThreadPoolExecutor(max_workers=jobs or min(len(todo), os.cpu_count() or 4)) as ex:
-            logs = list(ex.map(compile_one, todo))
+    with cf.ThreadPoolExecutor(max_workers=jobs or max(1, min(len(todo) + 1, os.cpu_count() or 4))) as ex:
+        tower_job = ex.submit(compile_one, TOWER_SRC, TOWER_OBJ) if tower_todo else None
+        logs = list(ex.map(compile_one, *zip(*todo))) if todo else []
     if todo or force or not os.path.exists(LIB):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nv] + ARCH + ["-shared", "-o", tmp] + objs
@@ -100,7 +105,11 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link of libemb.so failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    if todo or force or not os.path.exists(TOWER):  # relinked to the new library
+    if not tower:
+        sys.stderr.write("torch is not installed: _tower.so (the Python side of the tower's calls) is not built\n")
+    elif todo or tower_todo or not os.path.exists(TOWER):  # relinked to the new library
+        if tower_job:
+            logs.append(tower_job.result())
         tmp = TOWER + f".tmp{os.getpid()}"
         cmd = [gxx(), "-shared", TOWER_OBJ, "-o", tmp, "-L" + HERE, "-l:libemb.so", "-Wl,-rpath,$ORIGIN"]
         for d in torch_dirs("lib"):
