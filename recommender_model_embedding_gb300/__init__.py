@@ -37,9 +37,15 @@ class _LoadTower:
             raise ImportError(f"{TOWER_PATH} is missing: the tower's calls need it, built with torch "
                               "installed (python recommender_model_embedding_gb300/build.py)")
 
-        import torch  # noqa: F401  (its libraries have to be there first)
-        # importing a submodule also puts it in this stand-in's place
-        return getattr(importlib.import_module(__name__ + "._tower"), name)
+        import torch  # (its libraries have to be there first)
+
+        global _tower
+        tower = importlib.import_module(__name__ + "._tower")
+        if tower.torch_version != torch.__version__:
+            _tower = self  # (importing a submodule puts it in this stand-in's place)
+            raise ImportError(f"{TOWER_PATH} was built for torch {tower.torch_version}, this is "
+                              f"{torch.__version__}: build it again")
+        return getattr(tower, name)
 
 
 _tower = _LoadTower()

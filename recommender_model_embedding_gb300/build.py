@@ -24,7 +24,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libemb.so")
 TOWER_SRC = os.path.join(CSRC, "py_tower.cpp")
 TOWER_OBJ = os.path.join(BUILD, "py_tower.o")
-TOWER = os.path.join(HERE, "_tower.so")
+TOWER = os.path.join(HERE, "_tower.so")  # (TOWER_OBJ's stamp: what it was compiled for)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -63,10 +63,36 @@ def torch_dirs(what: str):
     return [inc, os.path.join(inc, "torch", "csrc", "api", "include")]
 
 
+def torch_version() -> str:
+    """torch's version as it says it itself (read without importing it)."""
+    import re
+    path = os.path.join(torch_root(), "version.py")
+    with open(path) as f:
+        found = re.search(r"^__version__\s*=\s*['\"]([^'\"]*)['\"]", f.read(), re.M)
+    if not found:
+        raise RuntimeError(f"{path} gives no version")
+    return found.group(1)
+
+
 def _tower_flags():
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     dirs = torch_dirs("include") + [cuda, sysconfig.get_paths()["include"]]
-    return ["-O2", "-std=c++17", "-fPIC", "-I" + os.path.join(ROOT, "include")] + [f"-isystem{d}" for d in dirs]
+    return ["-O2", "-std=c++17", "-fPIC", f'-DEMB_TORCH_VERSION="{torch_version()}"',
+            "-I" + os.path.join(ROOT, "include")] + [f"-isystem{d}" for d in dirs]
+
+
+def _tower_stamp() -> str:
+    """What _tower.so depends on beside the sources: it reads torch's and Python's objects in place,
+    so it serves the versions that it was compiled for and no other."""
+    return "\n".join([str(sysconfig.get_config_var("SOABI")), gxx()] + _tower_flags() + torch_dirs("lib")) + "\n"
+
+
+def _stamped(stamp: str) -> bool:
+    try:
+        with open(TOWER_OBJ + ".stamp") as f:
+            return f.read() == stamp
+    except OSError:
+        return False
 
 
 def _stale(obj: str, src: str) -> bool:
@@ -83,7 +109,8 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     todo = [(s, o) for s, o in zip(srcs, objs) if force or _stale(o, s)]
     tower = torch_root() is not None
-    tower_todo = tower and (force or _stale(TOWER_OBJ, TOWER_SRC))
+    stamp = _tower_stamp() if tower else ""
+    tower_todo = tower and (force or _stale(TOWER_OBJ, TOWER_SRC) or not _stamped(stamp))
     nv = nvcc()
 
     def compile_one(s, o):
@@ -119,6 +146,8 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link of _tower.so failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, TOWER)
+        with open(TOWER_OBJ + ".stamp", "w") as f:
+            f.write(stamp)
     if verbose:
         for l in logs:
             sys.stderr.write(l)

@@ -539,4 +539,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tower", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tower(void) { return PyModule_Create(&module); }
+// `torch_version`: the torch whose tensors this module reads in place
+PyMODINIT_FUNC PyInit__tower(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", EMB_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

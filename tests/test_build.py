@@ -63,6 +63,68 @@ def test_second_build_has_nothing_to_do(build):
     assert not build.ran
 
 
+def test_tower_module_is_built_again_for_another_torch(build, tmp_path, monkeypatch):
+    """A new torch version, a torch elsewhere or another Python rebuild the module and nothing else."""
+    def torch_at(name, version):
+        root = tmp_path / name / "torch"
+        root.mkdir(parents=True, exist_ok=True)
+        (root / "__init__.py").touch()
+        (root / "version.py").write_text(f"__all__ = ['__version__']\n__version__ = '{version}'\n")
+        spec = types.SimpleNamespace(origin=str(root / "__init__.py"))
+        find = importlib.util.find_spec
+        monkeypatch.setattr(importlib.util, "find_spec", lambda n, *a: spec if n == "torch" else find(n, *a))
+
+    def again():
+        build.ran.clear()
+        build.build()
+        done = [sum(text in c for cmd in build.ran for c in cmd) for text in ("py_tower.cpp", "-ltorch_python")]
+        assert len(build.ran) == sum(done)
+        build_once_more = len(build.ran)
+        build.build()
+        assert len(build.ran) == build_once_more
+        return done
+
+    torch_at("a", "2.9.1")
+    build.build()
+    assert again() == [0, 0]
+    torch_at("a", "2.11.0+cu130")
+    assert again() == [1, 1]
+    torch_at("b", "2.11.0+cu130")
+    assert again() == [1, 1]
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-399-x")
+    assert again() == [1, 1]
+    # a module whose link failed is not taken for the new one
+    torch_at("b", "2.12.0")
+    build.fails = "-ltorch_python"
+    with pytest.raises(RuntimeError):
+        build.build()
+    build.fails = None
+    assert again() == [1, 1]
+
+
+def test_tower_module_of_another_torch_is_refused():
+    from helpers import build_lib
+    build_lib()
+    code = """
+import torch
+import recommender_model_embedding_gb300 as E
+real, torch.__version__ = torch.__version__, "0.1"
+for _ in range(2):
+    try:
+        E.expert_dispatch(None, None, None)
+    except ImportError as e:
+        assert "this is 0.1" in str(e), e
+    else:
+        raise AssertionError("no ImportError")
+torch.__version__ = real
+try:
+    E.expert_dispatch(None, None, None)
+except ValueError:
+    pass
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
+
+
 def test_package_imports_without_the_tower_module():
     """Everything but the tower's calls works without _tower.so, and those say what is missing."""
     from helpers import build_lib
