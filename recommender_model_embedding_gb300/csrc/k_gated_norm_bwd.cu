@@ -87,7 +87,9 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kAheadBackward<EPU, 
     float s[3] = {sx[0] + sx[1], sd[0] + sd[1], sy[0] + sy[1]};
     grp.sum(s, red);
     const float rx = rsqrtf(s[0] * a.inv_dim + a.eps), ry = rsqrtf(s[2] * a.inv_dim + a.eps);
-    const float xm = -rx * rx * (rx * s[1] * a.inv_dim);  // x_out * xm = -q mean(dh w_pre q) / rms
+    // x_out * xm = -q mean(dh w_pre q) / rms; the sum comes first: for a row of zeros it is zero, where
+    // 1 / rms^2 may be past fp32 (eps below 2^-127)
+    const float xm = -(rx * s[1] * a.inv_dim) * rx * rx;
     float su2[2] = {0.f, 0.f}, su[1];
     float u[K::NC][K::C];
     if (live)
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(V * EPU > 8 ? kNormWide : kAheadBackward<EPU, 
         p.set(z);
         p.store(reinterpret_cast<BT*>(at_row(a.dgate, row, a.dgate_st)));
       }
-      const float um = -ry * ry * su[0] * a.inv_dim;
+      const float um = -(su[0] * a.inv_dim) * ry * ry;
       if (a.dy && live)
 #pragma unroll
         for (int i = 0; i < K::NC; ++i) {

@@ -130,3 +130,28 @@ def test_inference_tensors_and_subclasses(E):
     E.gated_norm(x, y, a, None)
     E.gated_norm(x.as_subclass(Named), y.as_subclass(Named), b.as_subclass(Named), None)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("eps", [1e-6, 1e-30, 1e-42])
+def test_rows_of_zeros(E, eps):
+    """A row that no expert took is zero.  Its norm's gradient is w / sqrt(eps) times what comes in, also
+    for an eps whose reciprocal is past fp32 (1e-42).  The root is within 2 units (4 u); three to five
+    products round once each."""
+    n, d = 5, 192
+    x = _make((n, d), torch.float32)
+    x[1:4] = 0
+    dh, w = _make((n, d), torch.float32), _make((d,), torch.float32)
+    r = torch.tensor(eps, device="cuda").double().rsqrt()  # eps as the call takes it
+    h, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+    E.gated_norm(x, None, None, h, w_pre=w, eps=eps)
+    assert not bool(h[1:4].any()) and bool(h.isfinite().all())
+    E.gated_norm_backward(None, dh, x, None, dx, None, w_pre=w, dw_pre=dw, eps=eps)
+    ref = dh.double() * w.double() * r
+    assert bool(((dx.double() - ref).abs() <= 10 * U32 * ref.abs())[1:4].all())
+    assert bool(dx.isfinite().all()) and bool(dw.isfinite().all())
+    gate, dy, dg = _make((n, 1), torch.float32), torch.empty_like(x), torch.empty((n, 1), device="cuda")
+    out = torch.ones_like(x)
+    E.gated_norm_backward(dh, None, out, x, None, dy, gate=gate, w_post=w, dgate=dg, dw_post=dw, eps=eps)
+    ref = dh.double() * w.double() * torch.sigmoid(gate.double()) * r
+    assert bool(((dy.double() - ref).abs() <= 20 * U32 * ref.abs())[1:4].all())
+    assert bool(dy.isfinite().all()) and not bool(dg[1:4].any()) and bool(dw.isfinite().all())
