@@ -348,7 +348,8 @@ emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, cons
  * and y as stored, and the same gate and vectors:
  *   dx = dx_out + the gradient of h through the norm;  dy and dgate from dx;
  *   dw_post, dres_scale, dw_pre: summed over the rows (fp32 [dim], overwritten).
- * Any of its outputs may be NULL; dx may be dx_out itself (same row step).  With d_y NULL, dy,
+ * Any of its outputs may be NULL; dx may be dx_out or x_out itself, and dy y itself (same row
+ * steps).  With d_y NULL, dy,
  * dgate, dw_post and dres_scale are NULL; with d_dh NULL, dw_pre is.
  * EMB_EINVAL: n outside [0, 2^31), dim outside [1, EMB_NORM_MAX_DIM], bad types, gate_cols or row
  * steps, eps not a positive finite number, a missing buffer or one misaligned for its type, nothing to

@@ -318,7 +318,7 @@ def gated_norm_backward(dx_out, dh, x_out, y, dx, dy, gate=None, w_post=None, re
                         eps: float = 1e-6, workspace=None, stream=None):
     """Gradients of gated_norm from dx_out (None: zero) and dh (None: no h), with x_out, y, gate
     and the vectors of the forward: dx, dy, dgate and the vectors' (float32 [d], overwritten).
-    Outputs may be None; dx may be dx_out.  Asynchronous."""
+    Outputs may be None; dx may be dx_out or x_out, and dy y.  Asynchronous."""
     _tower.norm_backward(dx_out, dh, x_out, y, dx, dy, gate, w_post, res_scale, w_pre, dgate, dw_post,
                          dres_scale, dw_pre, eps, workspace, stream)
 
