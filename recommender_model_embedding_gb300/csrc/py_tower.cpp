@@ -8,6 +8,7 @@
 // stride(), data_ptr(), ...).  Every check comes before the library is called: a mismatch raises
 // ValueError, a status of the library the package's EmbError.  A call's tensors, its workspace and
 // its stream are on one device, and that device is the current one while the library is called.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <c10/cuda/CUDACachingAllocator.h>
@@ -285,8 +286,8 @@ PyObject* guard(Py_ssize_t got, Py_ssize_t want, F f) {
     }
     return f();
   } catch (const Raised&) {
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own exceptions keep their types (OutOfMemoryError)
+    if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

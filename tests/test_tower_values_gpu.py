@@ -155,3 +155,24 @@ def test_rows_of_zeros(E, eps):
     ref = dh.double() * w.double() * torch.sigmoid(gate.double()) * r
     assert bool(((dy.double() - ref).abs() <= 20 * U32 * ref.abs())[1:4].all())
     assert bool(dy.isfinite().all()) and not bool(dg[1:4].any()) and bool(dw.isfinite().all())
+
+
+def test_workspace_out_of_memory(E):
+    """A workspace that torch's allocator has no room for is torch's out-of-memory error, and the next
+    call works."""
+    n, d = 3000, 8192
+    x, dh, dx = _make((n, d), torch.float32), _make((n, d), torch.float32), torch.empty((n, d), device="cuda")
+    dw = torch.empty(d, device="cuda")
+    assert E.gated_norm_backward_workspace(n, d) > 1 << 22
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 20)) / total)
+    try:
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            E.gated_norm_backward(None, dh, x, None, dx, None, dw_pre=dw)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    E.gated_norm_backward(None, dh, x, None, dx, None, dw_pre=dw)
+    torch.cuda.synchronize()
+    assert bool(dx.isfinite().all()) and bool(dw.isfinite().all())
