@@ -343,14 +343,15 @@ emb_status emb_expert_combine_backward(const void* d_dout, int64_t dout_ld, cons
  * when dtype is BF16, either); the vectors w_post, res_scale, w_pre and their gradients are
  * fp32 [dim], and a NULL one counts as ones.  d_gate: gate_cols columns, 1 (one gate for a row)
  * or dim; NULL: no gate.  d_y NULL: no block, x_out = x (not written), only h.  d_h NULL: only
- * x_out (h is taken from x_out before its rounding).  x_out may be x itself (same row step).
+ * x_out (h is taken from x_out before its rounding).  x_out may be x itself (same row step).  The
+ * sums of squares are fp32: a row whose sum leaves that range (values beyond about 1e18) counts as
+ * one of infinite norm, and its term or h is zero.
  * Backward, from the residual stream's gradient dx_out (NULL: zero) and dh (NULL: no h), x_out
  * and y as stored, and the same gate and vectors:
  *   dx = dx_out + the gradient of h through the norm;  dy and dgate from dx;
  *   dw_post, dres_scale, dw_pre: summed over the rows (fp32 [dim], overwritten).
  * Any of its outputs may be NULL; dx may be dx_out or x_out itself, and dy y itself (same row
- * steps).  With d_y NULL, dy,
- * dgate, dw_post and dres_scale are NULL; with d_dh NULL, dw_pre is.
+ * steps).  With d_y NULL, dy, dgate, dw_post and dres_scale are NULL; with d_dh NULL, dw_pre is.
  * EMB_EINVAL: n outside [0, 2^31), dim outside [1, EMB_NORM_MAX_DIM], bad types, gate_cols or row
  * steps, eps not a positive finite number, a missing buffer or one misaligned for its type, nothing to
  * compute; the backward also for a short or misaligned workspace. */
@@ -382,10 +383,11 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
 
 /* Global gradient norm and clipping over `count` tensors: *d_norm = sqrt(sum of g^2 over all
  * of them), out = g * min(1, max_norm / norm).  The squares' sums are fp64 beyond groups of a
- * few elements, so neither huge nor tiny finite gradients lose the norm, and a factor below fp32's
- * normal numbers keeps its bits.  A norm that is
- * infinite or NaN in fp32 clips nothing: the outputs equal the gradients, and the caller sees
- * the norm.  h_list: host array, read before the call returns; d_out may be d_src (in place) or
+ * few elements, so neither huge nor tiny finite gradients lose the norm, and a factor below
+ * fp32's normal numbers keeps its bits.  A norm that is infinite or NaN in fp32 clips nothing: the
+ * outputs equal the gradients, and the caller sees the norm.  The norm is that of the tensors
+ * listed: the embedding rows' gradients, which the backward calls of a context apply as they
+ * form them, are in no list, so the dense part of a model is clipped by its own norm.  h_list: host array, read before the call returns; d_out may be d_src (in place) or
  * a buffer of the same type that overlaps no other.  numel may be 0, and count too (norm 0).
  * EMB_EINVAL: count < 0 or above EMB_CLIP_MAX_TENSORS, a negative numel, a bad dtype, a NULL or
  * (for its type) misaligned buffer, max_norm negative or NaN (infinity: only the norm and

@@ -4,7 +4,8 @@ A thin binding over libemb.so, the CUDA library declared in include/emb.h: ctype
 compiled module for the expert tower's calls (csrc/py_tower.cpp).  Every method marshals its
 arguments (torch tensors -> device pointers, the current CUDA stream) and calls the C entry
 point of the same name; all arithmetic runs in the library's kernels.  There is no CPU path:
-if libemb.so is missing this package fails to import.
+if libemb.so is missing this package fails to import, and if the compiled module is missing the
+tower's calls fail.
 """
 from __future__ import annotations
 
@@ -69,6 +70,8 @@ class EmbConfig(ctypes.Structure):
                 ("max_batch", ctypes.c_int64), ("max_lookups", ctypes.c_int64)]
 
 
+# The tower's structures and signatures, for calls of the C entry points themselves (the package's own
+# go through the compiled module).
 class EmbNorm(ctypes.Structure):
     _P, _I64 = ctypes.c_void_p, ctypes.c_int64
     _fields_ = [("n", _I64), ("dim", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
@@ -303,8 +306,8 @@ def gated_norm(x, y, x_out, h, gate=None, w_post=None, res_scale=None, w_pre=Non
     """The end of a residual block and the start of the next in one pass:
     x_out = x + res_scale * sigmoid(gate) * (y / rms(y) * w_post), h = x_out / rms(x_out) * w_pre.
     x, x_out [n, d] float32 or bfloat16; y, h, gate ([n, d], or [n, 1]: one gate a row) of one
-    type, bfloat16 or as x; vectors float32 [d], None counts as ones.  y None: h from x alone;
-    h None: only x_out.  x_out may be x.  Asynchronous."""
+    type, bfloat16 or as x; vectors float32 [d], None counts as ones.  y None: h from x alone
+    (x_out is then not written); h None: only x_out.  x_out may be x.  Asynchronous."""
     _tower.norm(x, y, x_out, h, gate, w_post, res_scale, w_pre, eps, stream)
 
 
@@ -331,8 +334,9 @@ def clip_grads_workspace(count: int) -> int:
 def clip_grads(grads, max_norm: float, norm, out=None, workspace=None, stream=None):
     """norm (float32 [1]) = sqrt(sum of squares over all of `grads`), and every gradient times
     min(1, max_norm / norm), in place or into `out` (contiguous CUDA tensors, float32 or
-    bfloat16, of the gradients' types and sizes).  An infinite or NaN norm clips nothing.
-    Asynchronous."""
+    bfloat16, of the gradients' types and sizes; none may overlap another, so a shared gradient
+    is listed once).  An infinite or NaN norm clips nothing.  The embedding layer's own gradients,
+    applied by its backward, are not part of the norm.  Asynchronous."""
     _tower.clip(grads, max_norm, norm, out, workspace, stream)
 
 

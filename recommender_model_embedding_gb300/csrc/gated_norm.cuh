@@ -15,12 +15,14 @@
 //   dw_pre = sum over rows of dh * q;   with T = sum over rows of t * g * a:
 //   dw_post = res_scale * T, dres_scale = w_post * T
 //
-// Both are bound by HBM bandwidth while the elements are wide enough, and then by instruction
-// issue: the forward takes about 300 warp instructions a warp's share of a row (8 elements a
-// thread), the backward 530.  Measured with a gate for each element, 262144 x 1024: forward with
+// Both are bound by HBM bandwidth while there are bytes enough for each row's chain of work (loads,
+// two row sums one after the other, arithmetic), and by that chain where there are not: the forward
+// takes about 300 warp instructions a warp's share of a row (8 elements a thread), the backward
+// 530, with 24 warps an SM to hide one another's waits.  Measured with a gate for each element, 262144 x 1024: forward with
 // an fp32 stream and bf16 blocks 3.76 GB in 0.555 ms (6.77 TB/s, the measured copy rate), backward
-// all in bf16 4.29 GB in 0.677 ms (6.34 TB/s, 93%); without the gate's bytes the bf16 backward
-// stays issue-bound (59% at 65536 x 2048, one gate a row; fp32 there 93%).
+// all in bf16 4.29 GB in 0.679 ms (6.32 TB/s, 93%); with one gate a row the bf16 backward reaches
+// 75% there and 59% at 65536 x 2048, where it issues in 64% of the cycles and has DRAM busy for
+// 46%; fp32 reaches 90% at 262144 x 1024.
 //
 // A group of `tpr` threads takes a row, about eight elements a thread (V packs of EPU: 16 bytes
 // a pack where everything is aligned, else 4 or one element; with an fp32 stream beside bf16
@@ -43,8 +45,9 @@
 namespace emb {
 
 // Threads: a CTA of narrow rows has 256.  A row has 8 elements a thread while that takes up to
-// kNormForward or kNormBackward threads (two such CTAs fill an SM's registers, 64 and 80 a
-// thread), 16 above.
+// kNormForward threads forward, and backward kNormBackward for packs of four elements and more (two
+// such CTAs fill an SM's registers, 64 and 80 a thread), kNormThreads for narrower ones (128
+// registers); 16 above.
 constexpr int kNormThreads = 256, kNormForward = 512, kNormBackward = 384, kNormWide = 512;
 constexpr int kStages = 3;  // rows of the ring
 
@@ -125,7 +128,7 @@ __device__ __forceinline__ void v_dot(float (&s)[2], const float (&a)[N], const 
 // e neither overflows nor leaves infinities to subtract in d: from 104 on e is zero in fp32 anyway,
 // and from -87.4 down g is zero, and rest too, which is only ever multiplied by g.  NaN stays.
 // In pairs, and with no choice between 1 - g and e g by the sign of z, this costs the backward little
-// (262144 x 1024 bf16 with a gate for each element: 666 us with 2^t alone, 677 so, 709 with expf).
+// (262144 x 1024 bf16 with a gate for each element: 666 us with 2^t alone, 678 so, 709 with expf).
 template <int N>
 __device__ __forceinline__ void v_sigmoid(const float (&gate)[N], float (&g)[N], float (&rest)[N]) {
   constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f, kLn2Rest = -1.90465421e-9f;
@@ -374,9 +377,9 @@ struct ColWeights {
 // up to 8 elements: there a ring would take two more instructions of the same pipe for every few
 // bytes, and single bf16 elements have no asynchronous copy at all.  Packs of one element:
 // forward of 16411 x 479 fp32 33 us through the ring, 27 so; of 83781 x 801 bf16 225 and 169,
-// backward 466 and 339.  Packs of two, 83676 x 802 bf16: backward 275 and 236, but the forward,
+// backward 466 and 339.  Packs of two, 83676 x 802 bf16: backward 275 and 240, but the forward,
 // with more rows in flight through the ring, 140 and 148; wider packs lose in the backward too
-// (262144 x 1024 bf16: 0.67 ms and 0.71).
+// (262144 x 1024 bf16: 0.67 ms and 0.71, before the gate's error was carried along).
 template <int EPU, int V>
 constexpr bool kAheadForward = EPU == 1 && V <= 8;
 template <int EPU, int V>

@@ -99,7 +99,7 @@ __device__ __forceinline__ double tile_squares(const T* p, int64_t n) {
 
 // Sum over the CTA, in thread 0.  fp64 additions are scarce (two lanes a cycle and SM), so one
 // warp adds the others' values up and reduces once: 12 warp additions for 256 threads, where
-// a shuffle tree in every warp would take over 100.
+// a shuffle tree in each of the 8 warps would take 40, and a few more to join them.
 template <int THREADS>
 __device__ __forceinline__ double cta_sum(double v) {
   __shared__ double sh[THREADS];

@@ -26,9 +26,10 @@ namespace emb {
 // from L2; a launch between the two does it where they are many), scans them over the experts
 // and places the slots.  A single chunk needs no first launch (3000 slots: 4.5 us in one launch,
 // 4.8 in two).  Up to 16 chunks exchanging their counts through the shared memory of a cluster,
-// in one launch, were no faster: 6.1 us for 16384 slots of 64 experts where two launches take
-// 6.3, 15.4 against 9.9 for 32768 of 1024.
-// Bound by latency, not bytes (1M slots of 128 experts: 15 us, 2M of 64: 27): a chunk is as short
+// in one launch, gained little with few experts (6.1 us for 16384 slots of 64, two launches 6.3)
+// and lost with many (15.4 us for 32768 slots of 1024, two launches 9.9).
+// Bound by instructions and latency, not bytes (1M slots of 128 experts: 15 us, 2M of 64: 27; the
+// placing kernel issues in 56% of the cycles with half the warps there are): a chunk is as short
 // as one CTA an SM allows, a warp loads the ids of eight groups of 32 slots at once, and where
 // that is all of its part (KEEP: chunks of up to 8192 slots) keys and ranks stay in registers
 // from counting to placing and the chunk is put in order in shared memory first, so that its

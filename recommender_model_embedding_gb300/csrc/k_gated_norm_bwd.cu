@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(1024) k_gated_norm_cols(NormArgs a, int parts)
 
 // CTAs: a row a group up to one CTA an SM, then at least four rows a group up to `cap`, so that the
 // column parts stay small beside the rows.  (A cluster of 16 CTAs that added its parts itself, in
-// one launch, was no faster: 16 x 1024 rows 6.3 us against 6.7, 96 x 1024 9.7 against 7.3.)
+// one launch, gained little on few rows, 16 x 1024 6.3 us against 6.7, and lost on more, 96 x 1024
+// 9.7 against 7.3.)
 constexpr int kNormCtasPerSm = 2 * kNormBackward / 160;  // at most (a CTA has at least 160 threads)
 
 static int64_t norm_bwd_grid(int64_t n, int rpb, int64_t cap) {
