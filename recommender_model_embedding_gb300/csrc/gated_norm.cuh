@@ -270,18 +270,20 @@ struct RowGroup {
   }
 };
 
+// (Ordinary loads: an early-launched kernel is there before the work ahead of it has written its last,
+// so nothing that it reads is read-only for as long as it runs.)
 template <int EPU>
 __device__ __forceinline__ void load_cols(const float* w, int col, float* v) {
   if constexpr (EPU >= 4) {
 #pragma unroll
     for (int m = 0; m < EPU; m += 4) {
-      const float4 f = w ? __ldg(reinterpret_cast<const float4*>(w + col + m))
+      const float4 f = w ? *reinterpret_cast<const float4*>(w + col + m)
                          : make_float4(1.f, 1.f, 1.f, 1.f);
       v[m] = f.x, v[m + 1] = f.y, v[m + 2] = f.z, v[m + 3] = f.w;
     }
   } else {
 #pragma unroll
-    for (int m = 0; m < EPU; ++m) v[m] = w ? __ldg(w + col + m) : 1.f;
+    for (int m = 0; m < EPU; ++m) v[m] = w ? w[col + m] : 1.f;
   }
 }
 
@@ -322,9 +324,9 @@ struct ColWeights {
         for (int j = 0; j < 8; ++j) {
           const int k = threadIdx.x + (j0 + j) * a.tpr;
           const bool in = k < a.dim;
-          wp[j] = in ? a.w_post ? __ldg(a.w_post + k) : 1.f : 0.f;
-          rs[j] = in ? a.res_scale ? __ldg(a.res_scale + k) : 1.f : 0.f;
-          wn[j] = in ? a.w_pre ? __ldg(a.w_pre + k) : 1.f : 0.f;
+          wp[j] = in ? a.w_post ? a.w_post[k] : 1.f : 0.f;
+          rs[j] = in ? a.res_scale ? a.res_scale[k] : 1.f : 0.f;
+          wn[j] = in ? a.w_pre ? a.w_pre[k] : 1.f : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

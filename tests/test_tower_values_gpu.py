@@ -183,3 +183,33 @@ def test_workspace_out_of_memory(E):
     E.gated_norm_backward(None, dh, x, None, dx, None, dw_pre=dw)
     torch.cuda.synchronize()
     assert bool(dx.isfinite().all()) and bool(dw.isfinite().all())
+
+
+@pytest.mark.parametrize("d", [96, 479, 1024, 4100])
+def test_vectors_written_by_the_call_before(E, d):
+    """A vector that the call just ahead writes in place, off any wide boundary, over and over: each call
+    sees what the one before it left, as with a wait after every call."""
+    n, rounds = 700, 20
+    x, y, base = _make((n, d), torch.float32), _make((n, d), torch.float32), _make((3 * d + 7,), torch.float32)
+
+    def run(wait):
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        flat = base.clone()
+        v = [flat[1 + i * d:1 + (i + 1) * d] for i in range(3)]
+        xo, dw, norm = torch.empty_like(x), torch.empty(d, device="cuda"), torch.empty(1, device="cuda")
+        hs, ds = ([torch.empty_like(x) for _ in range(rounds)] for _ in range(2))
+        for r in range(rounds):
+            E.gated_norm(x, y, xo, hs[r], w_post=v[0], res_scale=v[1], w_pre=v[2])
+            pause()
+            E.clip_grads(v, 20.0 / (r + 1), norm)
+            pause()
+            E.gated_norm_backward(x, hs[r], xo, y, ds[r], None, w_post=v[0], res_scale=v[1], w_pre=v[2], dw_pre=dw)
+            pause()
+            E.clip_grads([v[2], v[0]], 10.0 / (r + 1), norm)
+            pause()
+        torch.cuda.synchronize()
+        return hs + ds + [flat, dw]
+
+    ref = run(True)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(ref, run(False)))
