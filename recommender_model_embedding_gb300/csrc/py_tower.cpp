@@ -81,8 +81,9 @@ struct Device {
   }
   // makes it current until the call returns (where there is none, the library's call says so)
   void enter() {
-    if (index < 0 || c10::cuda::device_count() == 0 || c10::cuda::current_device() == index) return;
-    guard.set_index((c10::DeviceIndex)index);
+    const int devices = c10::cuda::device_count();
+    if (index < 0 || devices == 0 || (devices == 1 && index == 0)) return;
+    if (c10::cuda::current_device() != index) guard.set_index((c10::DeviceIndex)index);
   }
 };
 
