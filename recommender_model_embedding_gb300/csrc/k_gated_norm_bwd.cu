@@ -283,6 +283,8 @@ cudaError_t launch_gated_norm_bwd(const emb_norm& p, void* ws, cudaStream_t s) {
     if (e != cudaSuccess || parts == 0) return e;
   } else if (!a.cols) {
     return cudaSuccess;
+  } else {
+    a.w_post = a.res_scale = nullptr;  // a sum over no rows is zero, whatever the vectors hold
   }
   return launch_early(k_gated_norm_cols, (p.dim + 31) / 32, 1024, 0, s, a, parts);
 }

@@ -213,3 +213,12 @@ def test_vectors_written_by_the_call_before(E, d):
     ref = run(True)
     for _ in range(5):
         assert all(torch.equal(a, b) for a, b in zip(ref, run(False)))
+
+
+def test_empty_batch_beside_infinite_vectors(E):
+    """A sum over no rows is zero whatever factors it would have had."""
+    z, v = torch.empty((0, 40), device="cuda"), torch.full((40,), float("inf"), device="cuda")
+    dw = [torch.full((40,), 3.0, device="cuda") for _ in range(3)]
+    E.gated_norm_backward(z, z, z, z, z, z, w_post=v, res_scale=v * 0, w_pre=v, dw_post=dw[0], dres_scale=dw[1],
+                          dw_pre=dw[2])
+    assert all(bool((x == 0).all()) for x in dw)
