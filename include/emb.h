@@ -381,6 +381,106 @@ int64_t emb_gated_norm_backward_workspace(int64_t n, int32_t dim);
 emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_bytes,
                                    void* stream);
 
+/* Experts' products: rows sorted by expert (emb_expert_sort, emb_expert_dispatch) through each
+ * expert's own weights, without the host learning how many rows an expert has.  Expert e's rows are
+ * [offsets[e], offsets[e+1]) of x; d_offsets is int32 [experts + 1] as emb_expert_sort writes it, or
+ * NULL for one dense layer (experts = 1, all rows).  Rows of no expert are neither read nor
+ * written.  Offsets have to ascend within [0, rows]: others lead to unspecified results, but never outside
+ * the buffers.
+ *
+ *   linear  out[r] = W_e x[r]                              W_e [out][in]
+ *           dx[r] = W_e^T dout[r];  dW_e = sum over e's rows of dout[r] x[r]^T
+ *   gated   g = Wg x[r], u = Wu x[r], h[r] = act(g) u      W_e [2 out][in]: Wg above Wu
+ *           backward from dh and gu = [g, u] as the forward left it (rows of 2 out):
+ *           dg = dh u act'(g), du = dh act(g), then as the linear layer's with dout = [dg, du]
+ *
+ * An expert without rows has dW_e = 0; dw is overwritten.  act: silu g s(g), gelu g P(g) (P the normal
+ * distribution), relu, or sigmoid s(g) = 1 / (1 + exp(-g)).  Everything is of `dtype`; dw is of dw_dtype
+ * (F32, or as dtype).  bf16: exact products, fp32 sums, and the gated backward's dg, du rounded to bf16 once
+ * as they enter its products.  F32: operands are split into three bf16 parts and the products of the
+ * larger six pairs summed in fp32, about as exact as an fp32 product; an infinite element makes what it
+ * enters non-finite (infinite or NaN).
+ * A weight matrix lies in rows of `in` elements (row step w_ld), or with w_turned in rows of `out` (2 out)
+ * elements, one for each input; experts w_step elements apart (0: the same matrix).  dw likewise by dw_ld,
+ * dw_turned, dw_step, its matrices apart.
+ * Workspace: what has to be copied for the tensor cores (fp32 operands, and rows or weights not on 16-byte
+ * boundaries), the gated backward's [dg, du], and parts of dw; from the same arguments, pointers among
+ * them (only their alignment is looked at).
+ * EMB_EINVAL: rows outside [0, 2^31), experts outside [1, EMB_EXPERT_MAX] or not 1 without offsets, in or
+ * out outside [1, EMB_EXPERT_MAX_DIM], bad types, act or steps, a missing buffer (d_dx or d_dw may be
+ * NULL, not both; d_gu of the forward too) or one misaligned for its type, a short or misaligned
+ * workspace. */
+enum { EMB_ACT_SILU = 0, EMB_ACT_GELU = 1, EMB_ACT_RELU = 2, EMB_ACT_SIGMOID = 3 };
+typedef struct emb_product {
+  int64_t rows;
+  int32_t experts, in, out; /* gated: out is the width of h */
+  int32_t dtype, act, w_turned, dw_turned, dw_dtype;
+  const int32_t* d_offsets;
+  const void *d_x, *d_w;
+  int64_t x_ld, w_ld, w_step;
+  void *d_out, *d_gu; /* linear: out; gated: h and (forward: or NULL) gu */
+  int64_t out_ld, gu_ld;
+  const void* d_dout; /* backward: of out, or of h */
+  void *d_dx, *d_dw;
+  int64_t dout_ld, dx_ld, dw_ld, dw_step;
+} emb_product;
+int64_t emb_expert_linear_workspace(const emb_product* args);
+emb_status emb_expert_linear(const emb_product* args, void* d_ws, int64_t ws_bytes, void* stream);
+int64_t emb_expert_linear_backward_workspace(const emb_product* args);
+emb_status emb_expert_linear_backward(const emb_product* args, void* d_ws, int64_t ws_bytes, void* stream);
+int64_t emb_expert_gated_workspace(const emb_product* args);
+emb_status emb_expert_gated(const emb_product* args, void* d_ws, int64_t ws_bytes, void* stream);
+int64_t emb_expert_gated_backward_workspace(const emb_product* args);
+emb_status emb_expert_gated_backward(const emb_product* args, void* d_ws, int64_t ws_bytes, void* stream);
+
+/* 4-bit weights.  Packing: per group of `group` columns of a row (the last may be shorter),
+ * scale = max|w| / 7 and code = w / scale rounded to nearest, ties to even, within [-7, 7] (a zero group:
+ * scale 0, codes 0), stored as code + 8: d_q [n][(d + 1) / 2] bytes, column 2i in the low half of byte i, and
+ * d_scale fp32 [n][ceil(d / group)].  Each step is one IEEE fp32 operation.  Inputs must be finite.
+ * Product, rows by expert as above: out[r] = W_e x[r] with W = scale * (code - 8), any of the 16 codes;
+ * d_q [experts][out][(in + 1) / 2], d_scale [experts][out][ceil(in / group)].  For few rows an expert (serving):
+ * the codes are read again for every 32 of them.
+ * EMB_EINVAL: sizes and types as above, group not a positive multiple of 32 up to
+ * EMB_EXPERT_MAX_DIM, a NULL buffer or one misaligned for its type. */
+typedef struct emb_product4 {
+  int64_t rows;
+  int32_t experts, in, out, dtype, group;
+  const int32_t* d_offsets;
+  const void* d_x;
+  int64_t x_ld;
+  const uint8_t* d_q;
+  const float* d_scale;
+  void* d_out;
+  int64_t out_ld;
+} emb_product4;
+emb_status emb_quantize_rows4(const void* d_w, int64_t w_ld, int64_t n, int32_t d, int32_t dtype, int32_t group,
+                              uint8_t* d_q, float* d_scale, void* stream);
+emb_status emb_expert_linear4(const emb_product4* args, void* stream);
+
+/* Dropout, with a residual's addition where d_residual is given:
+ *   out[i][j] = residual[i][j] + (kept ? x[i][j] / (1 - p') : 0),  p' = round(p 2^16) / 2^16
+ * The 16 bits of element (i, j) are half j % 2 (0: low) of word j / 2 % 4 of Philox4x32-10 (Salmon,
+ * Moraes, Dror and Shaw, 2011) of the counter (j / 8, i, step, site) under the key `seed`; it is kept where
+ * they are at least p' 2^16.  They depend on nothing else, so the backward, dx = kept ? dout / (1 - p') : 0, is
+ * the same call on dout without a residual, and no mask is stored.  d_rng: int64 [2] on the device, the seed and
+ * the step (its low 32 bits count), read when the call runs: a replayed graph draws anew after they are
+ * changed.  site: tells apart the places of one step that share d_rng.  A dropped element may hold
+ * anything.  x of dtype; residual and out of out_dtype (F32 or as dtype; without a residual as dtype).
+ * out may be x or the residual itself (same row step, same type).
+ * EMB_EINVAL: n outside [0, 2^31), dim outside [1, EMB_EXPERT_MAX_DIM], p outside [0, 1], bad types or row
+ * steps, a NULL or (for its type) misaligned buffer. */
+typedef struct emb_dropout_rows {
+  int64_t n;
+  int32_t dim, dtype, out_dtype;
+  uint32_t site;
+  double p;
+  const int64_t* d_rng;
+  const void *d_x, *d_residual;
+  void* d_out;
+  int64_t x_ld, residual_ld, out_ld;
+} emb_dropout_rows;
+emb_status emb_dropout(const emb_dropout_rows* args, void* stream);
+
 /* Global gradient norm and clipping over `count` tensors: *d_norm = sqrt(sum of g^2 over all
  * of them), out = g * min(1, max_norm / norm).  The squares' sums are fp64 beyond groups of a
  * few elements, so neither huge nor tiny finite gradients lose the norm, and a factor below

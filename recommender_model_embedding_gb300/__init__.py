@@ -84,6 +84,31 @@ class EmbNorm(ctypes.Structure):
                 ("dh_ld", _I64), ("dx_ld", _I64), ("dy_ld", _I64), ("dgate_ld", _I64)]
 
 
+class EmbProduct(ctypes.Structure):
+    _P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    _fields_ = [("rows", _I64), ("experts", _I32), ("in_", _I32), ("out", _I32), ("dtype", _I32),
+                ("act", _I32), ("w_turned", _I32), ("dw_turned", _I32), ("dw_dtype", _I32),
+                ("d_offsets", _P), ("d_x", _P), ("d_w", _P), ("x_ld", _I64), ("w_ld", _I64),
+                ("w_step", _I64), ("d_out", _P), ("d_gu", _P), ("out_ld", _I64), ("gu_ld", _I64),
+                ("d_dout", _P), ("d_dx", _P), ("d_dw", _P), ("dout_ld", _I64), ("dx_ld", _I64),
+                ("dw_ld", _I64), ("dw_step", _I64)]
+
+
+class EmbProduct4(ctypes.Structure):
+    _P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    _fields_ = [("rows", _I64), ("experts", _I32), ("in_", _I32), ("out", _I32), ("dtype", _I32),
+                ("group", _I32), ("d_offsets", _P), ("d_x", _P), ("x_ld", _I64), ("d_q", _P),
+                ("d_scale", _P), ("d_out", _P), ("out_ld", _I64)]
+
+
+class EmbDropoutRows(ctypes.Structure):
+    _P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    _fields_ = [("n", _I64), ("dim", _I32), ("dtype", _I32), ("out_dtype", _I32),
+                ("site", ctypes.c_uint32), ("p", ctypes.c_double), ("d_rng", _P), ("d_x", _P),
+                ("d_residual", _P), ("d_out", _P), ("x_ld", _I64), ("residual_ld", _I64),
+                ("out_ld", _I64)]
+
+
 class EmbTensor(ctypes.Structure):
     _fields_ = [("d_src", ctypes.c_void_p), ("d_out", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("dtype", ctypes.c_int32)]
@@ -135,6 +160,17 @@ _SIGS = {
     "emb_gated_norm_backward": ([ctypes.POINTER(EmbNorm), _P, _I64, _P], ctypes.c_int),
     "emb_clip_grads_workspace": ([_I64], _I64),
     "emb_clip_grads": ([ctypes.POINTER(EmbTensor), _I64, ctypes.c_float, _P, _P, _I64, _P], ctypes.c_int),
+    "emb_expert_linear_workspace": ([ctypes.POINTER(EmbProduct)], _I64),
+    "emb_expert_linear": ([ctypes.POINTER(EmbProduct), _P, _I64, _P], ctypes.c_int),
+    "emb_expert_linear_backward_workspace": ([ctypes.POINTER(EmbProduct)], _I64),
+    "emb_expert_linear_backward": ([ctypes.POINTER(EmbProduct), _P, _I64, _P], ctypes.c_int),
+    "emb_expert_gated_workspace": ([ctypes.POINTER(EmbProduct)], _I64),
+    "emb_expert_gated": ([ctypes.POINTER(EmbProduct), _P, _I64, _P], ctypes.c_int),
+    "emb_expert_gated_backward_workspace": ([ctypes.POINTER(EmbProduct)], _I64),
+    "emb_expert_gated_backward": ([ctypes.POINTER(EmbProduct), _P, _I64, _P], ctypes.c_int),
+    "emb_quantize_rows4": ([_P, _I64, _I64, _I32, _I32, _I32, _P, _P, _P], ctypes.c_int),
+    "emb_expert_linear4": ([ctypes.POINTER(EmbProduct4), _P], ctypes.c_int),
+    "emb_dropout": ([ctypes.POINTER(EmbDropoutRows), _P], ctypes.c_int),
     "emb_unique_keys_noalloc": ([_P, _I64, _P, _P, _P, _P], ctypes.c_int),
 }
 NOALLOC_MAX_KEYS = 524288
@@ -324,6 +360,67 @@ def gated_norm_backward(dx_out, dh, x_out, y, dx, dy, gate=None, w_post=None, re
     Outputs may be None; dx may be dx_out or x_out, and dy y.  Asynchronous."""
     _tower.norm_backward(dx_out, dh, x_out, y, dx, dy, gate, w_post, res_scale, w_pre, dgate, dw_post,
                          dres_scale, dw_pre, eps, workspace, stream)
+
+
+def expert_linear(x, w, out, offsets=None, workspace=None, stream=None):
+    """out[r] = W[e] x[r] for the rows r in [offsets[e], offsets[e + 1]) of each expert e (offsets of
+    expert_sort, int32 [experts + 1]; None: one dense layer).  x [S, in] and out [S, out] float32 or
+    bfloat16, rows any step apart; w [experts, out, in] (or [out, in]) of the same type, either its
+    rows or its columns adjacent (so a transposed [experts, in, out] serves).  Rows of no expert
+    are left as they were.  The host does not wait for the offsets.  Asynchronous."""
+    _tower.linear(x, w, out, offsets, workspace, stream)
+
+
+def expert_linear_backward(dout, x, w, dx, dw, offsets=None, workspace=None, stream=None):
+    """Gradients of expert_linear: dx [S, in], and dw [experts, out, in] float32 or of w's type
+    (overwritten; zero for an expert without rows).  Either may be None."""
+    _tower.linear_backward(dout, x, w, dx, dw, offsets, workspace, stream)
+
+
+def expert_gated(x, w, h, gu=None, offsets=None, act: str = "silu", workspace=None, stream=None):
+    """A gated feed-forward block's first half for rows by expert, as expert_linear: with the gate's
+    weights w[e, :f] and the others w[e, f:] (w [experts, 2f, in] or [2f, in]),
+    h[r] = act(g) * u, g = w[e, :f] x[r], u = w[e, f:] x[r].  act: "silu", "gelu", "relu" or
+    "sigmoid".  gu [S, 2f] (may be None): g and u side by side, for the backward."""
+    _tower.gated(x, w, h, gu, offsets, act, workspace, stream)
+
+
+def expert_gated_backward(dh, gu, x, w, dx, dw, offsets=None, act: str = "silu", workspace=None,
+                          stream=None):
+    """Gradients of expert_gated from dh [S, f], and gu as the forward left it: dx [S, in], and dw
+    [experts, 2f, in] float32 or of w's type (overwritten).  Either may be None."""
+    _tower.gated_backward(dh, gu, x, w, dx, dw, offsets, act, workspace, stream)
+
+
+def quantize_rows4(w, q, scale, group: int = 64, stream=None):
+    """4-bit codes of the rows of `w` (float32 or bfloat16 [n, d], rows any step apart, or contiguous
+    [experts, n, d]): `q` uint8 [..., n, ceil(d / 2)], two columns a byte (the even one low, stored
+    as code + 8), and `scale` float32 [..., n, ceil(d / group)], max / 7 of each group of columns.
+    group: a multiple of 32.  Asynchronous."""
+    _tower.quantize4(w, q, scale, group, stream)
+
+
+def expert_linear4(x, q, scale, out, group: int = 64, offsets=None, stream=None):
+    """expert_linear from 4-bit weights, for few rows an expert: out[r] = W[e] x[r] with
+    W = scale * (code - 8); q [experts, out, ceil(in / 2)] (or [out, ...]) and scale as
+    quantize_rows4 writes them, both contiguous."""
+    _tower.linear4(x, q, scale, out, group, offsets, stream)
+
+
+def dropout(x, out, p: float, rng, site: int = 0, residual=None, stream=None):
+    """out = residual + (kept ? x / (1 - p) : 0), or without the residual.  Which elements of x
+    [n, d] are kept depends on (rng, site, row, column) alone; rng: int64 [2] on the device, a seed
+    and a step (read when the call runs: add one to rng[1] between steps, also between replays of
+    a graph); site: one number for each place of a step that uses the same rng.  p counts in steps
+    of 2^-16.  x float32 or bfloat16, residual and out of one type, float32 or as x (without a
+    residual as x); out may be x or residual.  Asynchronous."""
+    _tower.dropout(x, out, p, rng, site, residual, stream)
+
+
+def dropout_backward(dout, dx, p: float, rng, site: int = 0, stream=None):
+    """The gradient of dropout to x, with rng and site as the forward had them (the residual's is
+    dout itself): dx = kept ? dout / (1 - p) : 0."""
+    _tower.dropout(dout, dx, p, rng, site, None, stream)
 
 
 def clip_grads_workspace(count: int) -> int:

@@ -19,6 +19,7 @@
 #include <sys/mman.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -1272,6 +1273,109 @@ emb_status emb_clip_grads(const emb_tensor* h_list, int64_t count, float max_nor
   if (!ws_ok(d_ws, ws_bytes, need)) return EMB_EINVAL;
   return check_launch(launch_clip_grads(h_list, count, max_norm, d_norm, d_ws,
                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Matrices of an expert's weights: rows of `inner` elements, `experts` of them `step` apart; an output's may
+// not overlap (one after the other, or row by row among each other).
+static bool weights_ok(int64_t ld, int64_t step, int64_t rows, int64_t inner, int64_t experts, bool out) {
+  if (!in_ld_ok(ld) || step < 0 || step >= ((int64_t)1 << 40)) return false;
+  if (!out) return true;
+  if (rows > 1 && ld < inner) return false;
+  const int64_t one = (rows - 1) * ld + inner;
+  return experts <= 1 || step >= one || (step >= inner && (rows <= 1 || ld >= (experts - 1) * step + inner));
+}
+
+static bool product_ok(const emb_product* p, ProductKind kind) {
+  if (!p || p->rows < 0 || p->rows > INT32_MAX || p->experts < 1 || p->experts > EMB_EXPERT_MAX) return false;
+  if (!p->d_offsets && p->experts != 1) return false;
+  if (p->in < 1 || p->in > EMB_EXPERT_MAX_DIM || p->out < 1 || p->out > EMB_EXPERT_MAX_DIM) return false;
+  if (p->dtype != EMB_F32 && p->dtype != EMB_BF16) return false;
+  const bool gated = kind == kGated || kind == kGatedBackward, back = kind == kLinearBackward || kind == kGatedBackward;
+  if (gated && (p->act < EMB_ACT_SILU || p->act > EMB_ACT_SIGMOID)) return false;
+  const int elem = p->dtype == EMB_BF16 ? 2 : 4;
+  const int64_t O = gated ? 2 * (int64_t)p->out : p->out;
+  if (!in_ld_ok(p->x_ld) || !aligned_to(p->d_x, elem) || !aligned_to(p->d_w, elem) || !aligned_to(p->d_offsets, 4)) return false;
+  if (!weights_ok(p->w_ld, p->w_step, p->w_turned ? p->in : O, p->w_turned ? O : p->in, p->experts, false)) return false;
+  const bool any = p->rows > 0;
+  if (!back) {
+    if (any && (!p->d_x || !p->d_w || !p->d_out)) return false;
+    if (!out_ld_ok(p->out_ld, p->rows, p->out) || !aligned_to(p->d_out, elem)) return false;
+    return !gated || !p->d_gu || (out_ld_ok(p->gu_ld, p->rows, O) && aligned_to(p->d_gu, elem));
+  }
+  if (!p->d_dx && !p->d_dw) return false;
+  if (any && (!p->d_dout || (p->d_dx && !p->d_w) || (p->d_dw && !p->d_x) || (gated && !p->d_gu))) return false;
+  if (!in_ld_ok(p->dout_ld) || !aligned_to(p->d_dout, elem)) return false;
+  if (gated && (!in_ld_ok(p->gu_ld) || !aligned_to(p->d_gu, elem))) return false;
+  if (p->d_dx && (!out_ld_ok(p->dx_ld, p->rows, p->in) || !aligned_to(p->d_dx, elem))) return false;
+  if (!p->d_dw) return true;
+  if (p->dw_dtype != EMB_F32 && p->dw_dtype != p->dtype) return false;
+  return aligned_to(p->d_dw, p->dw_dtype == EMB_BF16 ? 2 : 4) &&
+         weights_ok(p->dw_ld, p->dw_step, p->dw_turned ? p->in : O, p->dw_turned ? O : p->in, p->experts, true);
+}
+
+static int64_t product_workspace(const emb_product* p, ProductKind kind) {
+  return product_ok(p, kind) ? expert_product_workspace(*p, kind) : -1;
+}
+
+static emb_status product(const emb_product* p, ProductKind kind, void* ws, int64_t bytes, void* stream) {
+  const int64_t need = product_workspace(p, kind);
+  if (need < 0 || !ws_ok(ws, bytes, need)) return EMB_EINVAL;
+  return check_launch(launch_expert_product(*p, kind, ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t emb_expert_linear_workspace(const emb_product* p) { return product_workspace(p, kLinear); }
+int64_t emb_expert_linear_backward_workspace(const emb_product* p) { return product_workspace(p, kLinearBackward); }
+int64_t emb_expert_gated_workspace(const emb_product* p) { return product_workspace(p, kGated); }
+int64_t emb_expert_gated_backward_workspace(const emb_product* p) { return product_workspace(p, kGatedBackward); }
+emb_status emb_expert_linear(const emb_product* p, void* ws, int64_t bytes, void* stream) {
+  return product(p, kLinear, ws, bytes, stream);
+}
+emb_status emb_expert_linear_backward(const emb_product* p, void* ws, int64_t bytes, void* stream) {
+  return product(p, kLinearBackward, ws, bytes, stream);
+}
+emb_status emb_expert_gated(const emb_product* p, void* ws, int64_t bytes, void* stream) {
+  return product(p, kGated, ws, bytes, stream);
+}
+emb_status emb_expert_gated_backward(const emb_product* p, void* ws, int64_t bytes, void* stream) {
+  return product(p, kGatedBackward, ws, bytes, stream);
+}
+
+static bool group4_ok(int32_t group) { return group >= 32 && group <= EMB_EXPERT_MAX_DIM && group % 32 == 0; }
+
+emb_status emb_quantize_rows4(const void* d_w, int64_t w_ld, int64_t n, int32_t d, int32_t dtype, int32_t group,
+                              uint8_t* d_q, float* d_scale, void* stream) {
+  if (n < 0 || n > INT32_MAX || d < 1 || d > EMB_EXPERT_MAX_DIM || !group4_ok(group) || !in_ld_ok(w_ld) ||
+      (dtype != EMB_F32 && dtype != EMB_BF16) || (n > 0 && (!d_w || !d_q || !d_scale)))
+    return EMB_EINVAL;
+  if (!aligned_to(d_w, dtype == EMB_BF16 ? 2 : 4) || !aligned_to(d_scale, 4)) return EMB_EINVAL;
+  return check_launch(launch_quantize_rows4(d_w, w_ld, n, d, dtype == EMB_BF16, group, d_q, d_scale,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+emb_status emb_expert_linear4(const emb_product4* p, void* stream) {
+  if (!p || p->rows < 0 || p->rows > INT32_MAX || p->experts < 1 || p->experts > EMB_EXPERT_MAX ||
+      (!p->d_offsets && p->experts != 1) || p->in < 1 || p->in > EMB_EXPERT_MAX_DIM || p->out < 1 ||
+      p->out > EMB_EXPERT_MAX_DIM || !group4_ok(p->group) || (p->dtype != EMB_F32 && p->dtype != EMB_BF16))
+    return EMB_EINVAL;
+  if (p->rows > 0 && (!p->d_x || !p->d_q || !p->d_scale || !p->d_out)) return EMB_EINVAL;
+  const int elem = p->dtype == EMB_BF16 ? 2 : 4;
+  if (!in_ld_ok(p->x_ld) || !out_ld_ok(p->out_ld, p->rows, p->out) || !aligned_to(p->d_x, elem) ||
+      !aligned_to(p->d_out, elem) || !aligned_to(p->d_scale, 4) || !aligned_to(p->d_offsets, 4))
+    return EMB_EINVAL;
+  return check_launch(launch_linear4(*p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+emb_status emb_dropout(const emb_dropout_rows* p, void* stream) {
+  if (!p || p->n < 0 || p->n > INT32_MAX || p->dim < 1 || p->dim > EMB_EXPERT_MAX_DIM || !(p->p >= 0.0 && p->p <= 1.0))
+    return EMB_EINVAL;
+  if ((p->dtype != EMB_F32 && p->dtype != EMB_BF16) || (p->out_dtype != p->dtype && (p->out_dtype != EMB_F32 || !p->d_residual)))
+    return EMB_EINVAL;
+  if (p->n > 0 && (!p->d_x || !p->d_out || !p->d_rng)) return EMB_EINVAL;
+  const int elem = p->dtype == EMB_BF16 ? 2 : 4, oe = p->out_dtype == EMB_BF16 ? 2 : 4;
+  if (!in_ld_ok(p->x_ld) || !in_ld_ok(p->residual_ld) || !out_ld_ok(p->out_ld, p->n, p->dim) || !aligned_to(p->d_x, elem) ||
+      !aligned_to(p->d_residual, oe) || !aligned_to(p->d_out, oe) || !aligned_to(p->d_rng, 8))
+    return EMB_EINVAL;
+  return check_launch(launch_dropout(*p, (uint32_t)std::nearbyint(p->p * 65536.0), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int32_t emb_step_tracks_once(const emb_ctx* ctx) {

@@ -321,6 +321,13 @@ cudaError_t launch_gated_norm_bwd(const emb_norm& p, void* ws, cudaStream_t s);
 int64_t clip_grads_workspace(int64_t count);
 cudaError_t launch_clip_grads(const emb_tensor* list, int64_t count, float max_norm, float* norm,
                               void* ws, cudaStream_t s);
+enum ProductKind { kLinear, kLinearBackward, kGated, kGatedBackward };
+int64_t expert_product_workspace(const emb_product& p, ProductKind kind);
+cudaError_t launch_expert_product(const emb_product& p, ProductKind kind, void* ws, cudaStream_t s);
+cudaError_t launch_linear4(const emb_product4& p, cudaStream_t s);
+cudaError_t launch_quantize_rows4(const void* w, int64_t w_ld, int64_t n, int d, int bf16, int group, uint8_t* q,
+                                  float* scale, cudaStream_t s);
+cudaError_t launch_dropout(const emb_dropout_rows& p, uint32_t cut, cudaStream_t s);
 cudaError_t launch_key_stats(Ctx* c, const uint32_t* rows, int64_t n, uint32_t* freq,
                              uint32_t* last, cudaStream_t s);
 

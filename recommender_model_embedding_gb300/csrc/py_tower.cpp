@@ -26,8 +26,8 @@
 
 namespace {
 
-enum Kind { F32, BF16, I32, I64, OTHER };
-const char* const kKindNames[] = {"float32", "bfloat16", "int32", "int64", "another type (float16, say)"};
+enum Kind { F32, BF16, I32, I64, U8, OTHER };
+const char* const kKindNames[] = {"float32", "bfloat16", "int32", "int64", "uint8", "another type (float16, say)"};
 constexpr const char* kPackage = "recommender_model_embedding_gb300";
 
 // A Python exception is set; unwinds to the call's guard.
@@ -64,7 +64,7 @@ bool truth(PyObject* o) {
 // What the checks read of a tensor.
 struct Seen {
   Kind kind = OTHER;
-  int64_t dims = 0, numel = 0, size[2] = {0, 0}, step[2] = {0, 0};
+  int64_t dims = 0, numel = 0, size[3] = {0, 0, 0}, step[3] = {0, 0, 0};  // (of 2 and 3 dims)
   bool cuda = false, dense = false;
   int device = -1;
   void* p = nullptr;
@@ -108,8 +108,8 @@ Seen see_object(PyObject* o) {  // through attributes
   const Ref step(PyObject_CallMethod(o, "stride", nullptr));
   s.dims = PySequence_Size(shape.o);
   if (s.dims < 0) throw Raised();
-  if (s.dims == 2)
-    for (int i = 0; i < 2; ++i) {
+  if (s.dims == 2 || s.dims == 3)
+    for (int i = 0; i < (int)s.dims; ++i) {
       const Ref a(PySequence_GetItem(shape.o, i)), b(PySequence_GetItem(step.o, i));
       s.size[i] = number(a.o), s.step[i] = number(b.o);
     }
@@ -136,12 +136,13 @@ Seen see(PyObject* o, const char* name, Device& dev) {
     case at::kBFloat16: s.kind = BF16; break;
     case at::kInt: s.kind = I32; break;
     case at::kLong: s.kind = I64; break;
+    case at::kByte: s.kind = U8; break;
     default: break;
   }
   s.dims = t.dim(), s.numel = t.numel();
   s.cuda = t.is_cuda(), s.dense = t.is_contiguous();
-  if (s.dims == 2)
-    for (int i = 0; i < 2; ++i) s.size[i] = t.size(i), s.step[i] = t.stride(i);
+  if (s.dims == 2 || s.dims == 3)
+    for (int i = 0; i < (int)s.dims; ++i) s.size[i] = t.size(i), s.step[i] = t.stride(i);
   if (s.cuda) s.device = t.get_device(), s.p = t.data_ptr(), dev.same(s.device, name);
   return s;
 }
@@ -522,6 +523,223 @@ PyObject* py_clip(PyObject*, PyObject* const* a, Py_ssize_t na) {
   });
 }
 
+// ---- experts' products ----
+
+// Weights: [experts, out, in], or [out, in] for one, rows of either axis adjacent.
+struct Weights {
+  void* p = nullptr;
+  int64_t experts = 1, out = 0, in = 0, ld = 0, step = 0;
+  int32_t turned = 0;
+};
+
+Weights weights(const Seen& s, const char* name) {
+  if (!s.cuda) refuse("%s: expected a CUDA tensor", name);
+  if (s.dims != 2 && s.dims != 3) refuse("%s: expected [experts, out, in] or [out, in]", name);
+  const int i = (int)s.dims - 2;
+  Weights w;
+  w.p = s.p;
+  if (i) w.experts = s.size[0], w.step = s.size[0] > 1 ? s.step[0] : 0;
+  w.out = s.size[i], w.in = s.size[i + 1];
+  if (s.step[i + 1] == 1 || w.in == 1) {
+    w.ld = w.out > 1 ? s.step[i] : w.in;
+  } else if (s.step[i] == 1 || w.out == 1) {
+    w.turned = 1, w.ld = w.in > 1 ? s.step[i + 1] : w.out;
+  } else {
+    refuse("%s: the elements of its rows or of its columns must be adjacent", name);
+  }
+  return w;
+}
+
+int32_t act_of(PyObject* o) {
+  const char* name = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
+  const char* const names[] = {"silu", "gelu", "relu", "sigmoid"};  // EMB_ACT_*
+  for (int i = 0; name && i < 4; ++i)
+    if (std::strcmp(names[i], name) == 0) return i;
+  refuse("act: expected 'silu', 'gelu', 'relu' or 'sigmoid'");
+}
+
+const int32_t* offsets_of(PyObject* o, int64_t experts, Device& dev) {
+  if (o == Py_None) {
+    if (experts != 1) refuse("offsets: needed for weights of %lld experts", (long long)experts);
+    return nullptr;
+  }
+  return static_cast<const int32_t*>(flat(o, I32, experts + 1, "offsets", dev));
+}
+
+// Rows x, weights and offsets of a product; `halves` 2: a gated block's weights.
+struct ProductCall {
+  Device dev;
+  emb_product p{};
+  Kind kind;
+  int64_t n, d, f;
+  ProductCall(PyObject* xo, PyObject* wo, PyObject* offsets, int64_t halves) {
+    const Seen x = see(xo, "x", dev);
+    p.dtype = code_of(x, "x"), kind = x.kind;
+    p.rows = n = x.size[0];
+    p.in = fits_int(d = x.size[1], "x");
+    const Seen ws = see(wo, "w", dev);
+    if (ws.kind != kind) refuse("w: expected dtype %s, got %s", kKindNames[kind], kKindNames[ws.kind]);
+    const Weights w = weights(ws, "w");
+    if (w.in != d) refuse("w: %lld inputs, x has %lld columns", (long long)w.in, (long long)d);
+    if (w.out % halves) refuse("w: %lld outputs, expected a gate's and as many more", (long long)w.out);
+    p.experts = fits_int(w.experts, "w");
+    p.out = fits_int(f = w.out / halves, "w");
+    p.d_w = w.p, p.w_ld = w.ld, p.w_step = w.step, p.w_turned = w.turned;
+    const Rows r = rows(x, kind, n, d, "x");
+    p.d_x = r.p, p.x_ld = r.ld;
+    p.d_offsets = offsets_of(offsets, w.experts, dev);
+  }
+  void gradients(PyObject* dout, PyObject* dx, PyObject* dw, const char* name, int64_t halves) {
+    const Rows g = rows(dout, kind, n, f, name, dev), x = opt_rows(dx, kind, n, d, "dx", dev);
+    p.d_dout = g.p, p.dout_ld = g.ld, p.d_dx = x.p, p.dx_ld = x.ld;
+    if (dw == Py_None) return;
+    const Seen s = see(dw, "dw", dev);
+    if (s.kind != F32 && s.kind != kind) refuse("dw: expected float32 or the type of w, got %s", kKindNames[s.kind]);
+    const Weights w = weights(s, "dw");
+    if (w.experts != p.experts || w.out != halves * f || w.in != d)
+      refuse("dw: (%lld, %lld, %lld), expected (%lld, %lld, %lld)", (long long)w.experts, (long long)w.out, (long long)w.in,
+             (long long)p.experts, (long long)(halves * f), (long long)d);
+    p.dw_dtype = s.kind == BF16 ? EMB_BF16 : EMB_F32;
+    p.d_dw = w.p, p.dw_ld = w.ld, p.dw_step = w.step, p.dw_turned = w.turned;
+  }
+  using Need = int64_t (*)(const emb_product*);
+  using Run = emb_status (*)(const emb_product*, void*, int64_t, void*);
+  PyObject* run(const char* name, Need need, Run f, PyObject* workspace, PyObject* stream, std::initializer_list<PyObject*> outs) {
+    dev.enter();
+    Workspace ws(need(&p), workspace, dev);
+    void* s = stream_of(stream, dev);
+    ws.take(s);
+    return call(name, outs, [&] { return f(&p, ws.p, ws.bytes, s); });
+  }
+};
+
+// (x, w, out, offsets, workspace, stream)
+PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 6, [&]() -> PyObject* {
+    ProductCall c(a[0], a[1], a[3], 1);
+    const Rows o = rows(a[2], c.kind, c.n, c.f, "out", c.dev);
+    c.p.d_out = o.p, c.p.out_ld = o.ld;
+    return c.run("emb_expert_linear", emb_expert_linear_workspace, emb_expert_linear, a[4], a[5], {a[2]});
+  });
+}
+
+// (dout, x, w, dx, dw, offsets, workspace, stream)
+PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 8, [&]() -> PyObject* {
+    ProductCall c(a[1], a[2], a[5], 1);
+    c.gradients(a[0], a[3], a[4], "dout", 1);
+    return c.run("emb_expert_linear_backward", emb_expert_linear_backward_workspace, emb_expert_linear_backward, a[6], a[7], {a[3], a[4]});
+  });
+}
+
+// (x, w, h, gu, offsets, act, workspace, stream)
+PyObject* py_gated(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 8, [&]() -> PyObject* {
+    ProductCall c(a[0], a[1], a[4], 2);
+    const Rows h = rows(a[2], c.kind, c.n, c.f, "h", c.dev), gu = opt_rows(a[3], c.kind, c.n, 2 * c.f, "gu", c.dev);
+    c.p.d_out = h.p, c.p.out_ld = h.ld, c.p.d_gu = gu.p, c.p.gu_ld = gu.ld;
+    c.p.act = act_of(a[5]);
+    return c.run("emb_expert_gated", emb_expert_gated_workspace, emb_expert_gated, a[6], a[7], {a[2], a[3]});
+  });
+}
+
+// (dh, gu, x, w, dx, dw, offsets, act, workspace, stream)
+PyObject* py_gated_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 10, [&]() -> PyObject* {
+    ProductCall c(a[2], a[3], a[6], 2);
+    c.gradients(a[0], a[4], a[5], "dh", 2);
+    const Rows gu = rows(a[1], c.kind, c.n, 2 * c.f, "gu", c.dev);
+    c.p.d_gu = gu.p, c.p.gu_ld = gu.ld;
+    c.p.act = act_of(a[7]);
+    return c.run("emb_expert_gated_backward", emb_expert_gated_backward_workspace, emb_expert_gated_backward, a[8], a[9], {a[4], a[5]});
+  });
+}
+
+// Codes [experts, out, bytes] or [out, bytes], and their scales.
+void* codes_of(const Seen& s, int64_t bytes, const char* name) {
+  if (s.dims != 2 && s.dims != 3) refuse("%s: expected [experts, rows, bytes] or [rows, bytes]", name);
+  if (s.size[s.dims - 1] != bytes) refuse("%s: rows of %lld bytes, expected %lld", name, (long long)s.size[s.dims - 1], (long long)bytes);
+  return flat(s, U8, s.numel, true, name);
+}
+
+int32_t group_of(PyObject* o) {
+  const int64_t v = number(o);
+  if (v < 32 || v % 32 || v > EMB_EXPERT_MAX_DIM) refuse("group: %lld, expected a multiple of 32 up to %d", (long long)v, EMB_EXPERT_MAX_DIM);
+  return (int32_t)v;
+}
+
+// (x, q, scale, out, group, offsets, stream)
+PyObject* py_linear4(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 7, [&]() -> PyObject* {
+    Device dev;
+    emb_product4 p{};
+    const Seen x = see(a[0], "x", dev), q = see(a[1], "q", dev);
+    p.dtype = code_of(x, "x"), p.in = fits_int(x.size[1], "x"), p.group = group_of(a[4]);
+    p.rows = x.size[0];
+    p.d_q = static_cast<const uint8_t*>(codes_of(q, ((int64_t)p.in + 1) / 2, "q"));
+    const int64_t experts = q.dims == 3 ? q.size[0] : 1;
+    p.experts = fits_int(experts, "q"), p.out = fits_int(q.size[q.dims - 2], "q");
+    const int64_t groups = ((int64_t)p.in + p.group - 1) / p.group;
+    p.d_scale = static_cast<const float*>(flat(see(a[2], "scale", dev), F32, experts * p.out * groups, true, "scale"));
+    const Rows r = rows(x, x.kind, p.rows, p.in, "x"), o = rows(a[3], x.kind, p.rows, p.out, "out", dev);
+    p.d_x = r.p, p.x_ld = r.ld, p.d_out = o.p, p.out_ld = o.ld;
+    p.d_offsets = offsets_of(a[5], experts, dev);
+    dev.enter();
+    void* s = stream_of(a[6], dev);
+    return call("emb_expert_linear4", {a[3]}, [&] { return emb_expert_linear4(&p, s); });
+  });
+}
+
+// (w, q, scale, group, stream)
+PyObject* py_quantize4(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 5, [&]() -> PyObject* {
+    Device dev;
+    const Seen w = see(a[0], "w", dev), q = see(a[1], "q", dev);
+    const int32_t group = group_of(a[3]);
+    if (w.kind != F32 && w.kind != BF16) refuse("w: expected float32 or bfloat16, got %s", kKindNames[w.kind]);
+    if (!w.cuda) refuse("w: expected a CUDA tensor");
+    if (w.dims != 2 && !(w.dims == 3 && w.dense)) refuse("w: expected a matrix, or contiguous matrices [experts, rows, columns]");
+    const int32_t d = fits_int(w.size[w.dims - 1], "w");
+    const int64_t n = w.dims == 3 ? w.size[0] * w.size[1] : w.size[0], groups = ((int64_t)d + group - 1) / group;
+    if (w.dims == 2 && w.step[1] != 1 && d > 1) refuse("w: the elements of a row must be adjacent");
+    const int64_t ld = w.dims == 2 && n > 1 ? w.step[0] : d;
+    auto* codes = static_cast<uint8_t*>(flat(q, U8, n * (((int64_t)d + 1) / 2), true, "q"));
+    auto* scale = static_cast<float*>(flat(see(a[2], "scale", dev), F32, n * groups, true, "scale"));
+    dev.enter();
+    void* s = stream_of(a[4], dev);
+    return call("emb_quantize_rows4", {a[1], a[2]}, [&] {
+      return emb_quantize_rows4(w.p, ld, n, d, w.kind == BF16 ? EMB_BF16 : EMB_F32, group, codes, scale, s);
+    });
+  });
+}
+
+// (x, out, p, rng, site, residual, stream)
+PyObject* py_dropout(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guard(na, 7, [&]() -> PyObject* {
+    Device dev;
+    emb_dropout_rows p{};
+    const Seen x = see(a[0], "x", dev), out = see(a[1], "out", dev);
+    p.dtype = code_of(x, "x"), p.out_dtype = code_of(out, "out");
+    p.n = x.size[0], p.dim = fits_int(x.size[1], "x");
+    if (a[5] == Py_None && out.kind != x.kind) refuse("out: expected dtype %s, got %s", kKindNames[x.kind], kKindNames[out.kind]);
+    if (out.kind != x.kind && out.kind != F32) refuse("out: expected float32 or the type of x, got %s", kKindNames[out.kind]);
+    const Rows r = rows(x, x.kind, p.n, p.dim, "x"), o = rows(out, out.kind, p.n, p.dim, "out"),
+               res = opt_rows(a[5], out.kind, p.n, p.dim, "residual", dev);
+    p.d_x = r.p, p.x_ld = r.ld, p.d_out = o.p, p.out_ld = o.ld, p.d_residual = res.p, p.residual_ld = res.ld;
+    if (a[5] != Py_None && !res.p && p.n > 0) refuse("residual: no storage");
+    p.p = PyFloat_AsDouble(a[2]);
+    if (PyErr_Occurred()) throw Raised();
+    if (!(p.p >= 0.0 && p.p <= 1.0)) refuse("p: expected a probability");
+    p.d_rng = static_cast<const int64_t*>(flat(see(a[3], "rng", dev), I64, 2, true, "rng"));
+    const int64_t site = number(a[4]);
+    if (site < 0 || site > UINT32_MAX) refuse("site: %lld is out of range", (long long)site);
+    p.site = (uint32_t)site;
+    dev.enter();
+    void* s = stream_of(a[6], dev);
+    return call("emb_dropout", {a[1]}, [&] { return emb_dropout(&p, s); });
+  });
+}
+
 template <typename F>
 PyCFunction fast(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -535,6 +753,13 @@ PyMethodDef methods[] = {{"sort", fast(py_sort), METH_FASTCALL, nullptr},
                          {"norm", fast(py_norm), METH_FASTCALL, nullptr},
                          {"norm_backward", fast(py_norm_backward), METH_FASTCALL, nullptr},
                          {"clip", fast(py_clip), METH_FASTCALL, nullptr},
+                         {"linear", fast(py_linear), METH_FASTCALL, nullptr},
+                         {"linear_backward", fast(py_linear_backward), METH_FASTCALL, nullptr},
+                         {"gated", fast(py_gated), METH_FASTCALL, nullptr},
+                         {"gated_backward", fast(py_gated_backward), METH_FASTCALL, nullptr},
+                         {"linear4", fast(py_linear4), METH_FASTCALL, nullptr},
+                         {"quantize4", fast(py_quantize4), METH_FASTCALL, nullptr},
+                         {"dropout", fast(py_dropout), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tower", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
