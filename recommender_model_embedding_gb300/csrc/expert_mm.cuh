@@ -67,16 +67,21 @@ __device__ __forceinline__ void split3(float v, float& a, float& b, float& c) {
 
 // ---- activations ----
 
-// Exponential and quotient: CUDA's full ones for fp32 results, the fast ones for bf16 (their error,
-// below 2^-17 where the result is not lost anyway, is far inside bf16's 2^-9).
+// s(v) = 1 / (1 + exp(-v)): for fp32 results with CUDA's full exponential and quotient, for bf16 with the
+// hardware's approximate power of two and reciprocal (their error, 2^-22 and |v| 2^-24 of the value, is far inside
+// bf16's 2^-9 wherever the value is not zero to bf16 anyway).  Where exp(-v) overflows s is zero.
 template <bool FULL>
 __device__ __forceinline__ float sigmoid_of(float v) {
-  return FULL ? 1.f / (1.f + expf(-v)) : __fdividef(1.f, 1.f + fminf(__expf(-v), 1e37f));
+  if (FULL) return 1.f / (1.f + expf(-v));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * v));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
 }
 
 // act(v), and in `slope` its derivative where wanted.  silu v s(v); gelu v P(v) with the normal
-// distribution P(v) = erfc(-v / sqrt 2) / 2; relu; sigmoid s(v) = 1 / (1 + exp(-v)).  Far out, where
-// v times zero or a lost sum would be NaN, the limits hold (NaN stays NaN).
+// distribution P(v) = erfc(-v / sqrt 2) / 2; relu; sigmoid s(v).  Finite v gives finite results; an infinite one
+// NaN where the formula has infinity times zero.
 template <int ACT, bool FULL, bool SLOPE>
 __device__ __forceinline__ float activate(float v, float& slope) {
   if (ACT == EMB_ACT_RELU) {
@@ -85,21 +90,18 @@ __device__ __forceinline__ float activate(float v, float& slope) {
   }
   if (ACT == EMB_ACT_GELU) {
     const float p = 0.5f * erfcf(-0.70710678f * v);
-    // (exp(-v v / 2) is zero beyond 14; there v may be infinite)
-    if (SLOPE) slope = p + (fabsf(v) < 14.5f ? 0.39894228f * v * (FULL ? expf(-0.5f * v * v) : __expf(-0.5f * v * v)) : 0.f);
-    return v < -14.5f ? 0.f : v * p;
+    if (SLOPE) slope = fmaf(0.39894228f * v, FULL ? expf(-0.5f * v * v) : __expf(-0.5f * v * v), p);
+    return v * p;
   }
   const float s = sigmoid_of<FULL>(v);
+  // 1 - s(v) = s(-v), which is not lost where s is near one
+  const float rest = SLOPE ? sigmoid_of<FULL>(-v) : 0.f;
   if (ACT == EMB_ACT_SIGMOID) {
-    // 1 - s(v) = s(-v), which is not lost where s is near one
-    if (SLOPE) slope = s * sigmoid_of<FULL>(-v);
+    if (SLOPE) slope = s * rest;
     return s;
   }
-  if (SLOPE) {
-    const float rest = sigmoid_of<FULL>(-v);
-    slope = fabsf(v) < 104.f || v != v ? s + v * s * rest : (v > 0.f ? 1.f : 0.f);
-  }
-  return v < -104.f ? 0.f : v * s;
+  if (SLOPE) slope = fmaf(v * s, rest, s);
+  return v * s;
 }
 
 // ---- operands and launchers ----
@@ -122,7 +124,7 @@ struct PackArgs {
 };
 cudaError_t launch_expert_pack(const PackArgs& a, cudaStream_t s);
 // [dg, du] of a gated block's backward, to rows of 2 * p.out
-cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, cudaStream_t s);
+cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, cudaStream_t s);  // (planes: to's)
 
 struct MmArgs {
   MmOperand a, b;
@@ -132,15 +134,28 @@ struct MmArgs {
   int S = 0;
   int M = 0, N = 0, K = 0;       // rows product: N columns, K; weight gradient: M x N
   int act = -1;                  // rows product: gated (N: columns of a half), or -1
-  bool f32 = false;              // operands split in three planes
+  bool f32 = false;
   void* out = nullptr;
   int64_t out_ld = 0, out_step = 0;
   bool out_bf16 = false;
   void* gu = nullptr;
   int64_t gu_ld = 0;
+  int tile_n = 256;              // weight gradient: columns of a tile, 256 or 128
   int split = 0;                 // weight gradient: rows of a part (a multiple of 64), 0: no parts
   float* parts = nullptr;        // [parts][M][N]
 };
+// A rows product where experts have few rows, from the matrices as they lie.
+struct FewArgs {
+  const int32_t* offsets = nullptr;
+  int E = 1, S = 0, in = 0, out = 0, act = -1;  // out: of a half where gated
+  bool f32 = false, turned = false;             // turned: w's rows run along the outputs
+  const void *x = nullptr, *w = nullptr;
+  int64_t x_ld = 0, w_ld = 0, w_step = 0, half = 0;
+  void *y = nullptr, *gu = nullptr;
+  int64_t y_ld = 0, gu_ld = 0;
+};
+cudaError_t launch_expert_few(const FewArgs& a, cudaStream_t s);
+int64_t mm_pairs();
 cudaError_t launch_expert_mm_rows(const MmArgs& a, cudaStream_t s);
 cudaError_t launch_expert_mm_wgrad(const MmArgs& a, cudaStream_t s);
 

@@ -2,7 +2,7 @@
 // are copied first, and the launches in order.
 #include <algorithm>
 
-#include "expert_mm.cuh"
+#include "expert_few.cuh"
 
 namespace emb {
 
@@ -28,9 +28,9 @@ struct Source {
 };
 
 // Room for an operand of the tensor cores: row steps on 16 bytes, three planes for fp32.
-MmOperand packed(Room& room, int64_t inner, int64_t rows, int halves, int experts, bool f32) {
+MmOperand packed(Room& room, int64_t inner, int64_t rows, int halves, int experts, int planes) {
   MmOperand o;
-  o.inner = inner, o.rows = rows, o.halves = halves, o.experts = experts, o.planes = f32 ? 3 : 1;
+  o.inner = inner, o.rows = rows, o.halves = halves, o.experts = experts, o.planes = planes;
   o.ld = (inner + 7) / 8 * 8;
   o.half_step = rows * o.ld, o.expert_step = halves * o.half_step, o.plane_step = experts * o.expert_step;
   o.p = room.take<__nv_bfloat16>(o.planes * o.plane_step);
@@ -47,7 +47,7 @@ cudaError_t operand(const Source& m, bool f32, Room& room, bool launch, cudaStre
     o.halves = m.halves, o.experts = m.experts;
     return cudaSuccess;
   }
-  o = packed(room, m.inner, m.rows, m.halves, m.experts, f32);
+  o = packed(room, m.inner, m.rows, m.halves, m.experts, f32 ? 3 : 1);
   if (!launch) return cudaSuccess;
   PackArgs a;
   a.src = m.p, a.ld = m.ld, a.half_step = m.half_step, a.expert_step = m.expert_step;
@@ -55,14 +55,22 @@ cudaError_t operand(const Source& m, bool f32, Room& room, bool launch, cudaStre
   return launch_expert_pack(a, s);
 }
 
-// Rows of a part of a weight gradient with M x N outputs, 0: no parts.  With fewer than two tiles for each
-// pair of SMs, the rows are cut so that there are about three.
-int split_rows(int64_t rows, int experts, int64_t M, int64_t N) {
-  const int64_t each = ((M + 255) / 256) * ((N + 255) / 256), pairs = std::max(1, device_sms() / 2);
-  if (experts * each >= 2 * pairs) return 0;
-  const int64_t cut = std::max<int64_t>(512, (rows * each / (3 * pairs) + 63) / 64 * 64);
-  return cut * experts < rows ? (int)cut : 0;
+// Tiles of a weight gradient with M x N outputs: narrower ones, and then rows cut into parts, where the
+// experts' tiles alone leave pairs of SMs without work.  A part's rows are such that one dense layer's tiles
+// fill the pairs once, and several experts' (which have unlike numbers of rows) about twice.
+void cut_wgrad(MmArgs& a, int64_t rows) {
+  const int64_t pairs = mm_pairs();
+  const auto tiles = [&](int n) { return (int64_t)((a.M + 255) / 256) * ((a.N + n - 1) / n); };
+  a.tile_n = a.E * tiles(256) >= pairs ? 256 : 128, a.split = 0;
+  const int64_t each = tiles(a.tile_n);
+  if (a.E * each >= pairs) return;
+  const int64_t parts = a.E == 1 ? pairs / each : 2 * pairs / each;
+  const int64_t cut = std::max<int64_t>(256, (rows / parts + 63) / 64 * 64);
+  if (cut * a.E < rows) a.split = (int)cut;
 }
+
+// Whether experts have so few rows that the kernel for them is the faster.
+bool few(int64_t rows, int experts, bool f32) { return rows <= 32 * (int64_t)experts && few_tiles(rows, experts, 8) <= 65535; }
 
 cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool launch, cudaStream_t s) {
   const bool f32 = p.dtype == EMB_F32, gated = kind == kGated || kind == kGatedBackward;
@@ -75,6 +83,16 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
   const Source x{p.d_x, in, S, p.x_ld, 0, 0, 1, 1, last};
   if (!back) {
     if (S == 0) return cudaSuccess;
+    if (few(S, p.experts, f32)) {
+      FewArgs w;
+      w.offsets = p.d_offsets, w.E = p.experts, w.S = (int)S, w.in = (int)in, w.out = (int)f, w.act = gated ? p.act : -1;
+      w.f32 = f32, w.turned = p.w_turned != 0;
+      w.x = p.d_x, w.x_ld = p.x_ld, w.w = p.d_w, w.w_ld = p.w_ld, w.w_step = p.w_step;
+      w.half = gated ? (p.w_turned ? f : f * p.w_ld) : 0;
+      w.y = p.d_out, w.y_ld = p.out_ld;
+      if (gated) w.gu = p.d_gu, w.gu_ld = p.gu_ld;
+      return launch ? launch_expert_few(w, s) : cudaSuccess;
+    }
     Source w{p.d_w, p.w_turned ? f : in, p.w_turned ? in : f, p.w_ld, p.w_turned ? f : f * p.w_ld, p.w_step, gated ? 2 : 1, p.experts};
     if ((e = operand(x, f32, room, launch, s, a.a)) != cudaSuccess) return e;
     if ((e = operand(w, f32, room, launch, s, a.b)) != cudaSuccess || !launch) return e;
@@ -87,7 +105,8 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
   MmOperand d;  // [dg, du], or dout
   if (S > 0) {
     if (gated) {
-      d = packed(room, O, S, 1, 1, f32);
+      // (an fp32 gradient of bf16 weights takes all of dg and du, dx their first plane)
+      d = packed(room, O, S, 1, 1, f32 || (p.d_dw && p.dw_dtype == EMB_F32) ? 3 : 1);
       if (launch) e = launch_expert_gated_bwd(p, d, s);
     } else {
       e = operand({p.d_dout, f, S, p.dout_ld, 0, 0, 1, 1, last}, f32, room, launch, s, d);
@@ -96,6 +115,7 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
   }
   if (p.d_dx && S > 0) {
     a.a = d;
+    if (!f32) a.a.planes = 1;
     const Source w{p.d_w, p.w_turned ? O : in, p.w_turned ? in : O, p.w_ld, 0, p.w_step, 1, p.experts};
     if ((e = operand(w, f32, room, launch, s, a.b)) != cudaSuccess) return e;
     a.b_mn = p.w_turned == 0;
@@ -109,7 +129,7 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
     a.a = p.dw_turned ? xo : d, a.b = p.dw_turned ? d : xo;
     a.M = (int)(p.dw_turned ? in : O), a.N = (int)(p.dw_turned ? O : in), a.K = 0;
     a.out = p.d_dw, a.out_ld = p.dw_ld, a.out_step = p.dw_step, a.out_bf16 = p.dw_dtype == EMB_BF16;
-    a.split = split_rows(S, p.experts, a.M, a.N);
+    cut_wgrad(a, S);
     if (a.split) a.parts = room.take<float>((S / a.split + std::min<int64_t>(p.experts, S)) * a.M * a.N);
     if (launch) return launch_expert_mm_wgrad(a, s);
   }

@@ -7,7 +7,7 @@
 // Both are one kernel: a pair of CTAs (a cluster on two SMs) computes tiles of 256 x 256, each CTA
 // holding 128 rows of the accumulator in its tensor memory, with tcgen05.mma.cta_group::2 (M = 256,
 // N = 256, K = 16) issued by one thread of the pair's first CTA.  Per 64 of K each CTA brings 128 x
-// 64 of A and of B by TMA (16 KB each, 128-byte swizzle) into a ring of five stages; the pair reads
+// 64 of A and of B by TMA (16 KB each, 128-byte swizzle) into a ring of four stages; the pair reads
 // B from both.  A tile alone in one CTA (128 x 256) would write 48 KB and read 48 KB of shared memory
 // for the same arithmetic as 32 KB and 32 KB here, over what an SM's shared memory moves in
 // that time.  Operands may run along either axis (the descriptors take K-major and
@@ -36,13 +36,14 @@
 
 namespace emb {
 
-constexpr int kMmEpi = 8;                          // warps that write tiles out
+constexpr int kMmEpi = 16;                         // warps that write tiles out
 constexpr int kMmWarpTma = kMmEpi, kMmWarpMma = kMmEpi + 1, kMmWarpRelay = kMmEpi + 2;
 constexpr int kMmThreads = 32 * (kMmEpi + 3);
-constexpr int kMmStages = 5;
+constexpr int kMmStages = 4;
 constexpr int kMmOperand = 128 * 128;              // bytes of an operand's stage: 128 x 64 bf16
 constexpr int kMmStage = 2 * kMmOperand;
-constexpr int kMmStaging = 32 * 128;               // bytes of a writing warp: 32 rows of 128
+constexpr int kMmPart = 32 * 64;                   // bytes that a warp writes at once: 32 rows of 64
+constexpr int kMmStaging = 2 * kMmPart;            // of a writing warp
 constexpr int kMmOffStaging = kMmStages * kMmStage;
 constexpr int kMmOffBars = kMmOffStaging + kMmEpi * kMmStaging;
 constexpr int kMmNumBars = 3 * kMmStages + 4;
@@ -53,27 +54,39 @@ constexpr int kMmCols = 512;
 struct MmParams {
   const int32_t* offsets;
   int E, S, N, K, nt, mt;
-  int planes_terms;     // 1 or 6
+  int terms;            // products of planes: 1, 3 or 6
+  uint32_t planes_a, planes_b;  // of each, four bits
+  int tile_n;           // columns of a tile: 256 or 128
   int chunk;            // blocks of 64 along K between sums in registers
   int split;
   uint32_t idesc;
   int b_mn;
   void* out;
   int64_t out_ld, out_step;
-  int out_vec;
   void* gu;
   int64_t gu_ld;
-  int gu_vec;
+  int out_map, gu_map;  // whether the kernel has maps of them
   int M;
   float* parts;
 };
 
 // ---- cluster-wide barriers, TMA, MMA of a pair ----
+//
+// Every wait has a limit.  A role whose wait runs out does no more work, so the others' run out too, each once, and
+// all meet at the kernel's end; the tiles concerned are written as NaN.
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
+}
+// One lane of the warp.  The warps that issue copies and products run their loops whole, and this lane the
+// instruction: so their operands stay in the warp's uniform registers, which the instructions take (with a
+// single lane in the loop they were moved there one by one, 587 cycles for a stage's products instead of 512).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
 }
 __device__ __forceinline__ uint32_t addr_in(uint32_t local, uint32_t rank) {
   uint32_t a;
@@ -82,6 +95,11 @@ __device__ __forceinline__ uint32_t addr_in(uint32_t local, uint32_t rank) {
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// The same without release: for accumulators read (their loads have returned), where a release would hold the warp
+// until its stores of the last tile have reached memory.
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
   for (int n = 0; n < kWaitLimit; ++n) {
@@ -111,17 +129,17 @@ __device__ __forceinline__ void tma_box(const CUtensorMap* map, uint32_t dst, ui
       : "memory");
 }
 
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                         uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"((uint16_t)3)
       : "memory");
 }
@@ -146,53 +164,91 @@ struct Walk {
 
 // ---- writing out ----
 
-// 32 rows of 32 values, one row a lane, through the warp's staging to `rows` rows of `cols` valid
-// columns: 16 bytes a lane where the output allows it.
-template <typename T>
-__device__ __forceinline__ void write32(const float (&v)[32], unsigned char* staging, int lane, T* out, int64_t ld,
-                                        int rows, int cols, bool vec) {
-  constexpr int kChunks = 32 * sizeof(T) / 16;  // of a row: 8 or 4
-  constexpr int kEach = 16 / sizeof(T);
-  // chunk c of row r at a place where neither writes (lanes: rows) nor reads (lanes: chunks) collide
-  const auto place = [](int r, int c) {
-    return kChunks == 8 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  };
+// A warp's output: parts of 32 rows of 64 bytes (one row a lane: 32 bf16 or 16 fp32 values), staged in turn in
+// its two buffers.  Full parts of an output on 16-byte boundaries leave as one TMA copy each, which takes the
+// store out of the warp's hands (and out of the load-store pipe, which the tensor core's operands
+// share); parts at an expert's end or the last columns go row by row.  Chunk c of row r lies at c ^ (r / 2 % 4), the
+// 64-byte swizzle, so that neither the lanes' writes nor reads collide.
+struct Writer {
+  unsigned char* staging;
+  int lane, turn = 0;
+  __device__ __forceinline__ static int place(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
+
+  // map: of `out`'s matrices, or NULL; x, y, z: the part's place in it
+  template <typename T>
+  __device__ __forceinline__ void part(const float* v, T* out, int64_t ld, int rows, int cols, const CUtensorMap* map, int x,
+                                       int y, int z) {
+    constexpr int kEach = 16 / sizeof(T), kCols = 4 * kEach;
+    unsigned char* at = staging + turn * kMmPart;
+    turn ^= 1;
+    // the copy before the last has read this buffer
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    float part[kEach];
+    for (int c = 0; c < 4; ++c) {
+      float e[kEach];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) part[i] = v[c * kEach + i];
-    Pack<T, kEach> p;
-    p.set(part);
-    p.store(reinterpret_cast<T*>(staging + place(lane, c)));
-  }
-  __syncwarp();
-  if (vec && cols >= 32) {
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int r = (i * 32 + lane) / kChunks, c = lane % kChunks;
+      for (int i = 0; i < kEach; ++i) e[i] = v[c * kEach + i];
       Pack<T, kEach> p;
-      p.load(reinterpret_cast<const T*>(staging + place(r, c)));
-      if (r < rows) p.store(out + (int64_t)r * ld + c * kEach);
+      p.set(e);
+      p.store(reinterpret_cast<T*>(at + place(lane, c)));
     }
-  } else if (lane < cols) {
-    const int c = lane / kEach, i = lane % kEach;
-    for (int r = 0; r < min(rows, 32); ++r)
-      out[(int64_t)r * ld + lane] = *reinterpret_cast<const T*>(staging + place(r, c) + i * sizeof(T));
+    const bool whole = map != nullptr && rows >= 32 && cols >= kCols;
+    if (whole) fence_proxy_async();
+    __syncwarp();
+    if (whole) {
+      if (lane == 0)
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n"
+                     "cp.async.bulk.commit_group;" ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(at))
+                     : "memory");
+      return;
+    }
+    const int col = lane % kCols, c = col / kEach, i = col % kEach;
+    if (col < cols)
+      for (int r = lane / kCols; r < min(rows, 32); r += 32 / kCols)
+        out[(int64_t)r * ld + col] = *reinterpret_cast<const T*>(at + place(r, c) + i * sizeof(T));
+    if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // (an empty one: the count stays)
   }
-  __syncwarp();
+
+  // 32 values a row
+  template <typename T>
+  __device__ __forceinline__ void write(const float (&v)[32], T* out, int64_t ld, int rows, int cols, const CUtensorMap* map,
+                                        int x, int y, int z) {
+    part<T>(v, out, ld, rows, cols, map, x, y, z);
+    if constexpr (sizeof(T) == 4)
+      if (cols > 16) part<T>(v + 16, out + 16, ld, rows, cols - 16, map, x + 16, y, z);
+  }
+
+  __device__ __forceinline__ void finish() {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+  }
+};
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // WGRAD: the contraction runs over rows.  ACT: gated, or -1.  SUM: parts of K are summed in registers.
 template <bool WGRAD, int ACT, bool SUM, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
-    k_expert_mm(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, MmParams p) {
+    k_expert_mm(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap gmap, MmParams p) {
   constexpr bool GATED = ACT >= 0;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // (the same in both CTAs)
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kMmOffBars);
@@ -202,7 +258,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   uint64_t* dfull = landed + kMmStages;      // [2] accumulator written (commit, to both)
   uint64_t* dempty = dfull + 2;              // [2] first CTA: accumulator read by both
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMmOffTmem);
-  volatile uint32_t* abort_flag = tmem_slot + 1;
   int32_t* cuts = reinterpret_cast<int32_t*>(smem + kMmOffTables);
   int32_t* prefix = cuts + p.E + 1;
 
@@ -216,7 +271,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       mbar_init(dfull + i, 1);
       mbar_init(dempty + i, 2 * kMmEpi);
     }
-    *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kMmWarpMma) {
@@ -245,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   let_next_start();
   const uint32_t tmem = *tmem_slot;
   const int tiles = prefix[p.E];
-  const int terms = p.planes_terms;
+  const int terms = p.terms, tile_n = p.tile_n;
   Walk walk{cuts, prefix};
 
   // blocks of 64 along a tile's contraction; WGRAD: and its rows [r0, r1)
@@ -260,7 +314,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   };
 
   if (warp == kMmWarpTma) {
-    if (lane == 0) {
+    {
+      const bool one = elect_one();
+      const uint32_t full0 = addr_in(smem_u32(full), 0);  // of the pair's first CTA
+      const uint32_t bytes = kMmOperand + tile_n / 2 * 128;  // that a CTA brings for a stage
       int stage = 0;
       uint32_t phase = 1;
       bool ok = true;
@@ -270,30 +327,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         int r0 = 0, r1 = 0;
         const int blocks = k_blocks(local, r0, r1);
         const int m0 = (WGRAD ? 0 : cuts[e]) + m * 256 + (int)rank * 128;
-        const int n0 = GATED ? n * 128 : n * 256 + (int)rank * 128;
+        const int n0 = GATED ? n * (tile_n / 2) : n * tile_n + (int)rank * (tile_n / 2);
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
           for (int t = 0; ok && t < terms; ++t) {
-            // planes of the six products, small ones first: (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
-            const int pa = terms == 1 ? 0 : (0x001012 >> (4 * t)) & 15, pb = terms == 1 ? 0 : (0x010210 >> (4 * t)) & 15;
+            const int pa = (p.planes_a >> (4 * t)) & 15, pb = (p.planes_b >> (4 * t)) & 15;
             for (int kb = c0; kb < c1; ++kb) {
-              if (!(ok = mbar_wait_bounded(empty + stage, phase) && !*abort_flag)) break;
-              uint64_t* mine = (WGRAD ? landed : full) + stage;
-              const uint32_t bar = WGRAD ? smem_u32(mine) : addr_in(smem_u32(mine), 0);
-              if (WGRAD || rank == 0) mbar_arrive_expect_tx(mine, WGRAD ? kMmStage : 2 * kMmStage);
+              if (!(ok = mbar_wait_bounded(empty + stage, phase))) break;
+              uint32_t bar;
+              if (WGRAD && r1 - r0 - kb * 64 < 64) {  // by way of the warp that clears rows
+                bar = smem_u32(landed + stage);
+                if (one) mbar_arrive_expect_tx(landed + stage, bytes);
+              } else {
+                bar = full0 + stage * 8;
+                if (rank == 0 && one) {
+                  mbar_arrive_expect_tx(full + stage, 2 * bytes);
+                  if (WGRAD) mbar_arrive(full + stage);
+                }
+              }
               const uint32_t a = sbase + stage * kMmStage, b = a + kMmOperand;
-              if (WGRAD) {
+              if (!one) {
+              } else if (WGRAD) {
                 const int k = r0 + kb * 64;
                 tma_box(&amap, a, bar, m0, k, 0, 0, pa);
                 tma_box(&amap, a + 8192, bar, m0 + 64, k, 0, 0, pa);
                 tma_box(&bmap, b, bar, n0, k, 0, 0, pb);
-                tma_box(&bmap, b + 8192, bar, n0 + 64, k, 0, 0, pb);
+                if (tile_n > 128) tma_box(&bmap, b + 8192, bar, n0 + 64, k, 0, 0, pb);
               } else {
                 const int half = GATED ? (int)rank : 0;
                 tma_box(&amap, a, bar, kb * 64, m0, 0, 0, pa);
                 if (p.b_mn) {
                   tma_box(&bmap, b, bar, n0, kb * 64, half, e, pb);
-                  tma_box(&bmap, b + 8192, bar, n0 + 64, kb * 64, half, e, pb);
+                  if (tile_n > 128) tma_box(&bmap, b + 8192, bar, n0 + 64, kb * 64, half, e, pb);
                 } else {
                   tma_box(&bmap, b, bar, kb * 64, n0, half, e, pb);
                 }
@@ -303,7 +368,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           }
         }
       }
-      if (!ok) *abort_flag = 1;
       // the last copies are read before the CTA leaves: every stage handed back
       for (int i = 0; ok && i < kMmStages; ++i) {
         ok = mbar_wait_bounded(empty + stage, phase);
@@ -311,84 +375,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       }
     }
   } else if (warp == kMmWarpMma) {
-    if (rank == 0 && lane == 0) {
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, dphase = 1;
+    if (rank == 0) {
+      // One lane feeds the tensor core, which takes 512 cycles for a stage: the loop keeps to what has to be in it
+      // (addresses of descriptors and barriers are steps from the first stage's).
+      const uint64_t desc_a = mm_desc(sbase, WGRAD), desc_b = mm_desc(sbase + kMmOperand, WGRAD || p.b_mn);
+      const uint32_t step_a = WGRAD ? 2048 >> 4 : 32 >> 4, step_b = WGRAD || p.b_mn ? 2048 >> 4 : 32 >> 4;
+      const uint32_t hi_a = (uint32_t)(desc_a >> 32), hi_b = (uint32_t)(desc_b >> 32), idesc = p.idesc;
+      const uint32_t empty0 = smem_u32(empty);
+      const bool one = elect_one();
+      const int chunk = p.chunk, K = p.K;
+      int buf = 0;
+      uint32_t stage = 0, phase = 0, dphase = 1;
       bool ok = true;
       for (int tile = pair; ok && tile < tiles; tile += pairs) {
-        const int local = walk.local(tile);
-        int r0 = 0, r1 = p.K;
-        const int blocks = k_blocks(local, r0, r1);
-        for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
-          const int c1 = min(blocks, c0 + p.chunk);
-          if (!(ok = wait_cluster(dempty + buf, dphase))) break;
+        int length = K;  // of the contraction
+        if (WGRAD) {
+          int r0 = 0, r1 = 0;
+          k_blocks(walk.local(tile), r0, r1);
+          length = r1 - r0;
+        }
+        for (int done = 0; ok && done < length; done += chunk * 64) {
+          const int part = min(length - done, chunk * 64);
+          if (!(ok = mbar_wait_bounded(dempty + buf, dphase))) break;
           tc_fence_after();
+          const uint32_t d = tmem + buf * 256;
           uint32_t accumulate = 0;
           for (int t = 0; ok && t < terms; ++t)
-            for (int kb = c0; kb < c1; ++kb) {
-              if (!(ok = wait_cluster(full + stage, phase) && !*abort_flag)) break;
+            for (int left = part; left > 0; left -= 64) {
+              // (rows cleared by the other CTA's threads want an acquire of the cluster's scope; copies do not)
+              ok = WGRAD && left < 64 ? wait_cluster(full + stage, phase) : mbar_wait_bounded(full + stage, phase);
+              if (!ok) break;
               tc_fence_after();
-              const uint32_t a = sbase + stage * kMmStage;
-              uint64_t da = mm_desc(a, WGRAD), db = mm_desc(a + kMmOperand, WGRAD || p.b_mn);
-              const int left = r1 - r0 - kb * 64;
+              const uint32_t lo_a = (uint32_t)desc_a + stage * (kMmStage >> 4), lo_b = (uint32_t)desc_b + stage * (kMmStage >> 4);
+              if (one) {
+                mma_pair(d, lo_a, hi_a, lo_b, hi_b, idesc, accumulate);
+                if (left > 48) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (k * 16 < left) {
-                  mma_pair(tmem + buf * 256, da, db, p.idesc, accumulate);
-                  accumulate = 1;
+                  for (int k = 1; k < 4; ++k) mma_pair(d, lo_a + k * step_a, hi_a, lo_b + k * step_b, hi_b, idesc, 1);
+                } else {
+                  for (int k = 1; k * 16 < left; ++k) mma_pair(d, lo_a + k * step_a, hi_a, lo_b + k * step_b, hi_b, idesc, 1);
                 }
-                da += WGRAD ? 2048 >> 4 : 32 >> 4;
-                db += WGRAD || p.b_mn ? 2048 >> 4 : 32 >> 4;
+                commit_pair(empty0 + stage * 8);
               }
-              commit_pair(empty + stage);
+              accumulate = 1;
               if (++stage == kMmStages) stage = 0, phase ^= 1;
             }
-          if (ok) commit_pair(dfull + buf);
-          if (++buf == 2) buf = 0, dphase ^= 1;
+          if (ok && one) commit_pair(smem_u32(dfull + buf));
+          buf ^= 1;
+          dphase ^= buf ^ 1;
         }
       }
-      if (!ok) *abort_flag = 1;
     }
   } else if (warp == kMmWarpRelay) {
     if (WGRAD) {
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phases = 0;  // of `landed`, a bit a stage
       bool ok = true;
       for (int tile = pair; ok && tile < tiles; tile += pairs) {
         const int local = walk.local(tile);
         int r0 = 0, r1 = 0;
         const int blocks = k_blocks(local, r0, r1);
+        const int left = r1 - r0 - (blocks - 1) * 64;  // rows of the last block
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
-          for (int t = 0; ok && t < terms; ++t)
-            for (int kb = c0; kb < c1; ++kb) {
-              if (!(ok = mbar_wait_bounded(landed + stage, phase) && !*abort_flag)) break;
-              const int left = r1 - r0 - kb * 64;
-              if (left < 64) {  // rows of 128 bytes, one for each K, in four boxes of 64
-                unsigned char* at = smem + stage * kMmStage;
-                for (int i = lane; i < (64 - left) * 32; i += 32)
+          for (int t = 0; ok && t < terms; ++t) {
+            stage = (stage + c1 - c0 - 1) % kMmStages;  // the part's last block
+            if (c1 == blocks && left < 64) {
+              if (!(ok = mbar_wait_bounded(landed + stage, phases >> stage & 1))) break;
+              phases ^= 1u << stage;
+              // rows of 128 bytes, one for each K, in boxes of 64: two of A, one or two of B
+              unsigned char* at = smem + stage * kMmStage;
+              const int boxes = tile_n > 128 ? 4 : 3;
+              for (int i = lane; i < (64 - left) * 32; i += 32)
+                if ((i >> 3 & 3) < boxes)
                   *reinterpret_cast<uint4*>(at + (i >> 3 & 3) * 8192 + (left + (i >> 5)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async();
-              }
+              fence_proxy_async();
               __syncwarp();
               if (lane == 0) arrive_cluster(addr_in(smem_u32(full + stage), 0));
-              if (++stage == kMmStages) stage = 0, phase ^= 1;
             }
+            stage = stage + 1 == kMmStages ? 0 : stage + 1;
+          }
         }
       }
-      if (!ok && lane == 0) *abort_flag = 1;
     }
   } else {
-    const int quarter = warp & 3, side = warp >> 2;  // lanes 32 * quarter.., half of the columns
-    unsigned char* staging = smem + kMmOffStaging + warp * kMmStaging;
+    const int quarter = warp & 3, side = warp >> 2;  // lanes 32 * quarter.., parts `side` and `side` + 4 of 32 columns
+    Writer to{smem + kMmOffStaging + warp * kMmStaging, lane};
+    const CUtensorMap *om = p.out_map ? &omap : nullptr, *gm = p.gu_map ? &gmap : nullptr;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    // accumulator columns of the two parts: gated, the gate's and the up half's of the same outputs
+    const uint32_t at0 = side * 32, at1 = GATED ? tile_n / 2 + side * 32 : 128 + side * 32;
+    const bool has0 = !GATED || side * 32 < tile_n / 2, has1 = GATED ? has0 : tile_n > 128;
     int buf = 0;
     uint32_t dphase = 0;
     bool ok = true;
     const auto release = [&](int b) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(addr_in(smem_u32(dempty + b), 0));
+      if (lane == 0) arrive_cluster_relaxed(addr_in(smem_u32(dempty + b), 0));
     };
     for (int tile = pair; tile < tiles; tile += pairs) {
       const int local = walk.local(tile), e = walk.e;
@@ -398,88 +482,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       // this warp's rows, and how many of them are there
       const int row = (WGRAD ? 0 : cuts[e]) + m * 256 + (int)rank * 128 + quarter * 32;
       const int rows = (WGRAD ? p.M : cuts[e + 1]) - row;
-      constexpr int kCols = GATED ? 64 : 128;  // of the output
-      const int col = n * (2 * kCols) + side * kCols;
-      // accumulator columns of part i of 32: gated, the gate's first and then the up half's
-      const auto column = [&](int i) { return GATED ? (i >> 1) * 128 + side * 64 + (i & 1) * 32 : side * 128 + i * 32; };
-      float acc[4][32];
+      const int col = n * (GATED ? tile_n / 2 : tile_n) + side * 32, cols = p.N - col;
+      float v0[32], v1[32];
       if (SUM) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 32; ++j) v0[j] = v1[j] = 0.f;
         for (int c0 = 0; c0 < blocks; c0 += p.chunk) {
-          ok = ok && mbar_wait_bounded(dfull + buf, dphase) && !*abort_flag;
+          ok = ok && mbar_wait_bounded(dfull + buf, dphase);
           tc_fence_after();
+          __syncwarp();
+          const uint32_t from = lanes + buf * 256;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float v[32];
-            __syncwarp();
-            tmem_ld32(lanes + buf * 256 + column(i), v);
+            if (!(i < 2 ? has0 : has1)) continue;
+            float v[16];
+            tmem_ld16(from + (i < 2 ? at0 : at1) + (i & 1) * 16, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[i][j] += ok ? v[j] : __int_as_float(0x7FC00000);
+            for (int j = 0; j < 16; ++j) (i < 2 ? v0 : v1)[(i & 1) * 16 + j] += v[j];
           }
           release(buf);
           if (++buf == 2) buf = 0, dphase ^= 1;
         }
       } else {
-        ok = ok && mbar_wait_bounded(dfull + buf, dphase) && !*abort_flag;
+        ok = ok && mbar_wait_bounded(dfull + buf, dphase);
         tc_fence_after();
+        __syncwarp();
+        if (has0) tmem_ld32(lanes + buf * 256 + at0, v0);
+        if (has1) tmem_ld32(lanes + buf * 256 + at1, v1);
+        release(buf);
+        if (++buf == 2) buf = 0, dphase ^= 1;
       }
-      // a wait that ran out shows as NaN
-      const auto get = [&](int i, float (&v)[32]) {
-        if (SUM) {
+      if (!ok)  // a wait that ran out shows as NaN
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = acc[i][j];
-        } else {
-          __syncwarp();
-          tmem_ld32(lanes + buf * 256 + column(i), v);
-          if (!ok)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __int_as_float(0x7FC00000);
-        }
-      };
+        for (int j = 0; j < 32; ++j) v0[j] = v1[j] = __int_as_float(0x7FC00000);
+      if (rows <= 0 || cols <= 0) continue;
       if (GATED) {
-        T* out = static_cast<T*>(p.out) + (int64_t)row * p.out_ld + col;
-        T* gu = static_cast<T*>(p.gu) + (int64_t)row * p.gu_ld + col;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float g[32], u[32];
-          const int cols = p.N - col - i * 32;
-          get(i, g);
-          get(2 + i, u);
-          if (!SUM && i == 1) release(buf);
-          if (rows <= 0 || cols <= 0) continue;
-          if (p.gu != nullptr) {
-            write32<T>(g, staging, lane, gu + i * 32, p.gu_ld, rows, cols, p.gu_vec);
-            write32<T>(u, staging, lane, gu + p.N + i * 32, p.gu_ld, rows, cols, p.gu_vec);
-          }
-          float none;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) u[j] *= activate<ACT, SUM, false>(g[j], none);
-          write32<T>(u, staging, lane, out + i * 32, p.out_ld, rows, cols, p.out_vec);
+        if (!has0) continue;
+        if (p.gu != nullptr) {
+          T* gu = static_cast<T*>(p.gu) + (int64_t)row * p.gu_ld + col;
+          to.write<T>(v0, gu, p.gu_ld, rows, cols, gm, col, row, 0);
+          to.write<T>(v1, gu + p.N, p.gu_ld, rows, cols, gm, p.N + col, row, 0);
         }
+        float none;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v1[j] *= activate<ACT, SUM, false>(v0[j], none);
+        to.write<T>(v1, static_cast<T*>(p.out) + (int64_t)row * p.out_ld + col, p.out_ld, rows, cols, om, col, row, 0);
+      } else if (WGRAD && p.split) {
+        const int z = tile / (p.mt * p.nt);
+        float* part = p.parts + ((int64_t)z * p.M + row) * p.N + col;
+        to.write<float>(v0, part, p.N, rows, cols, om, col, row, z);
+        if (has1 && cols > 128) to.write<float>(v1, part + 128, p.N, rows, cols - 128, om, col + 128, row, z);
       } else {
-        T* out = static_cast<T*>(p.out) + (int64_t)row * p.out_ld + col;
-        if (WGRAD) out += e * p.out_step;
-        float* part = nullptr;
-        if (WGRAD && p.split) part = p.parts + (int64_t)(tile / (p.mt * p.nt)) * p.M * p.N + (int64_t)row * p.N + col;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v[32];
-          get(i, v);
-          if (!SUM && i == 3) release(buf);
-          const int cols = p.N - col - i * 32;
-          if (rows <= 0 || cols <= 0) continue;
-          if (WGRAD && p.split)
-            write32<float>(v, staging, lane, part + i * 32, p.N, rows, cols, p.N % 4 == 0);
-          else
-            write32<T>(v, staging, lane, out + i * 32, p.out_ld, rows, cols, p.out_vec);
-        }
+        T* out = static_cast<T*>(p.out) + (WGRAD ? e * p.out_step : 0) + (int64_t)row * p.out_ld + col;
+        const int z = WGRAD ? e : 0;
+        to.write<T>(v0, out, p.out_ld, rows, cols, om, col, row, z);
+        if (has1 && cols > 128) to.write<T>(v1, out + 128, p.out_ld, rows, cols - 128, om, col + 128, row, z);
       }
-      if (!SUM && ++buf == 2) buf = 0, dphase ^= 1;
     }
-    if (!ok && lane == 0) *abort_flag = 1;
+    to.finish();
   }
   __syncwarp();
   tc_fence_before();
@@ -519,6 +579,9 @@ __global__ void __launch_bounds__(256)
 
 // ---- host ----
 
+// Pairs of CTAs that run at once.
+int64_t mm_pairs() { return std::max(1, device_sms() / 2); }
+
 namespace {
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -555,9 +618,24 @@ bool make_map(CUtensorMap* map, const MmOperand& o, int box_rows) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr uint32_t mm_idesc(bool a_mn, bool b_mn) {
+uint32_t mm_idesc(bool a_mn, bool b_mn, int tile_n) {
   return (1u << 4) | (1u << 7) | (1u << 10)  // D fp32, A and B bf16
-         | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
+         | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) | ((uint32_t)(tile_n >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+// Parts (32 rows of 64 bytes) of `count` output matrices, where they lie on 16-byte boundaries.
+bool make_out_map(CUtensorMap* map, void* p, int64_t rows, int64_t cols, int64_t ld, int64_t count, int64_t step, bool bf16) {
+  const EncodeTiled encode = encode_tiled();
+  const int elem = bf16 ? 2 : 4;
+  if (encode == nullptr || p == nullptr || reinterpret_cast<uintptr_t>(p) % 16 || (rows > 1 && ld * elem % 16) ||
+      (count > 1 && step * elem % 16))
+    return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
+  const cuuint64_t steps[2] = {(cuuint64_t)(rows > 1 ? ld * elem : 16), (cuuint64_t)(count > 1 ? step * elem : 16)};
+  const cuuint32_t box[3] = {64u / (cuuint32_t)elem, 32, 1}, ones[3] = {1, 1, 1};
+  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, steps, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool WGRAD, int ACT, bool SUM, typename T>
@@ -565,23 +643,36 @@ cudaError_t launch_mm(const MmArgs& a, MmParams p, int64_t tiles_most, cudaStrea
   constexpr auto kern = k_expert_mm<WGRAD, ACT, SUM, T>;
   cudaError_t e = prepare_kernel<kern>();
   if (e != cudaSuccess) return e;
-  CUtensorMap amap, bmap;
-  if (!make_map(&amap, a.a, WGRAD ? 64 : 128) || !make_map(&bmap, a.b, WGRAD || a.b_mn ? 64 : 128))
+  CUtensorMap amap, bmap, omap, gmap;
+  if (!make_map(&amap, a.a, WGRAD ? 64 : 128) || !make_map(&bmap, a.b, WGRAD || a.b_mn ? 64 : p.tile_n / 2))
     return cudaErrorInvalidValue;
-  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(device_sms() / 2, tiles_most));
+  if (WGRAD && a.split)
+    p.out_map = make_out_map(&omap, a.parts, a.M, a.N, a.N, tiles_most / (p.mt * p.nt), (int64_t)a.M * a.N, false);
+  else
+    p.out_map = make_out_map(&omap, a.out, WGRAD ? a.M : a.S, a.N, a.out_ld, WGRAD ? a.E : 1, a.out_step, a.out_bf16);
+  // (the up half's parts start at column N)
+  p.gu_map = ACT >= 0 && a.N * (a.out_bf16 ? 2 : 4) % 16 == 0 && make_out_map(&gmap, a.gu, a.S, 2 * (int64_t)a.N, a.gu_ld, 1, 0, a.out_bf16);
+  if (!p.out_map) omap = amap;
+  if (!p.gu_map) gmap = amap;
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(mm_pairs(), tiles_most));
   const int smem = kMmOffTables + 2 * (p.E + 1) * 4 + 1024;
-  return launch_early(kern, (unsigned)(2 * pairs), kMmThreads, smem, s, amap, bmap, p);
+  return launch_early(kern, (unsigned)(2 * pairs), kMmThreads, smem, s, amap, bmap, omap, gmap, p);
 }
 
 MmParams params_of(const MmArgs& a) {
   MmParams p{};
-  const int elem = a.out_bf16 ? 2 : 4;
   p.offsets = a.offsets, p.E = a.E, p.S = a.S, p.N = a.N, p.K = a.K, p.M = a.M;
-  p.planes_terms = a.f32 ? 6 : 1;
+  p.terms = 1;
+  // products of the operands' planes (a, b), small ones first
+  if (a.a.planes > 1 && a.b.planes > 1) {  // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
+    p.terms = 6, p.planes_a = 0x001012, p.planes_b = 0x010210;
+  } else if (a.a.planes > 1) {             // (2,0) (1,0) (0,0)
+    p.terms = 3, p.planes_a = 0x012;
+  } else if (a.b.planes > 1) {
+    p.terms = 3, p.planes_b = 0x012;
+  }
   p.out = a.out, p.out_ld = a.out_ld, p.out_step = a.out_step;
-  p.out_vec = rows_on(a.out, a.out_ld, elem, 16) && a.out_step * elem % 16 == 0;
   p.gu = a.gu, p.gu_ld = a.gu_ld;
-  p.gu_vec = rows_on(a.gu, a.gu_ld, elem, 16) && (int64_t)a.N * elem % 16 == 0;
   p.split = a.split, p.parts = a.parts;
   return p;
 }
@@ -592,11 +683,14 @@ cudaError_t launch_expert_mm_rows(const MmArgs& a, cudaStream_t s) {
   if (a.S == 0) return cudaSuccess;
   MmParams p = params_of(a);
   const bool gated = a.act >= 0;
-  p.nt = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256), p.mt = 1;
+  const int64_t N = gated ? 2 * (int64_t)a.N : a.N, down = (int64_t)a.S / 256 + std::min(a.E, a.S);
+  p.tile_n = down * ((N + 255) / 256) > mm_pairs() ? 256 : 128;
+  p.nt = (int)((N + p.tile_n - 1) / p.tile_n), p.mt = 1;
+  if (gated) p.nt = (a.N + p.tile_n / 2 - 1) / (p.tile_n / 2);
   p.b_mn = a.b_mn;
-  p.idesc = mm_idesc(false, a.b_mn);
+  p.idesc = mm_idesc(false, a.b_mn, p.tile_n);
   p.chunk = a.f32 ? 4 : 1 << 20;
-  const int64_t most = ((int64_t)a.S / 256 + std::min(a.E, a.S)) * p.nt;
+  const int64_t most = down * p.nt;
   using H = __nv_bfloat16;
   if (a.f32) switch (a.act) {
       case EMB_ACT_SILU: return launch_mm<false, EMB_ACT_SILU, true, float>(a, p, most, s);
@@ -616,9 +710,10 @@ cudaError_t launch_expert_mm_rows(const MmArgs& a, cudaStream_t s) {
 
 cudaError_t launch_expert_mm_wgrad(const MmArgs& a, cudaStream_t s) {
   MmParams p = params_of(a);
-  p.nt = (a.N + 255) / 256, p.mt = (a.M + 255) / 256;
-  p.idesc = mm_idesc(true, true);
-  p.chunk = a.f32 ? 4 : 8;
+  p.tile_n = a.tile_n;
+  p.nt = (a.N + p.tile_n - 1) / p.tile_n, p.mt = (a.M + 255) / 256;
+  p.idesc = mm_idesc(true, true, p.tile_n);
+  p.chunk = p.terms == 1 ? 8 : 4;
   if (a.S > 0) {
     const int64_t parts = a.split ? (int64_t)a.S / a.split + std::min(a.E, a.S) : a.E;
     const cudaError_t e = a.out_bf16 ? launch_mm<true, -1, true, __nv_bfloat16>(a, p, parts * p.mt * p.nt, s)

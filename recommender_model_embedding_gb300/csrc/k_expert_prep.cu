@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(kPrepThreads)
   }
 }
 
-template <typename T, int ACT, int EPU>
+template <typename T, int PLANES, int ACT, int EPU>
 __global__ void __launch_bounds__(kPrepThreads)
     k_expert_gated_bwd(const T* dh, int64_t dh_ld, const T* gu, int64_t gu_ld, const int32_t* last, uint32_t S, int f,
                        int shift, __nv_bfloat16* to, int64_t to_ld, int64_t to_plane) {
-  constexpr bool F32 = sizeof(T) == 4;
+  constexpr bool F32 = PLANES == 3;  // what is to be of fp32's exactness
   wait_for_earlier();
   let_next_start();
   const uint32_t per = kPrepThreads >> shift;
@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kPrepThreads)
         gv[i] = dv[i] * uv[i] * slope;
         uv[i] = dv[i] * a;
       }
-      store_piece<F32 ? 3 : 1, EPU>(out + c * EPU, to_plane, gv);
-      store_piece<F32 ? 3 : 1, EPU>(out + f + c * EPU, to_plane, uv);
+      store_piece<PLANES, EPU>(out + c * EPU, to_plane, gv);
+      store_piece<PLANES, EPU>(out + f + c * EPU, to_plane, uv);
     }
   }
 }
@@ -170,8 +170,11 @@ cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, c
   const auto by_act = [&](auto act) {
     constexpr int A = decltype(act)::value;
     using H = __nv_bfloat16;
-    if (p.dtype == EMB_BF16) return vec ? run(k_expert_gated_bwd<H, A, 8>, (H*)nullptr) : run(k_expert_gated_bwd<H, A, 1>, (H*)nullptr);
-    return vec ? run(k_expert_gated_bwd<float, A, 8>, (float*)nullptr) : run(k_expert_gated_bwd<float, A, 1>, (float*)nullptr);
+    H* h = nullptr;
+    float* f = nullptr;
+    if (p.dtype == EMB_F32) return vec ? run(k_expert_gated_bwd<float, 3, A, 8>, f) : run(k_expert_gated_bwd<float, 3, A, 1>, f);
+    if (to.planes == 3) return vec ? run(k_expert_gated_bwd<H, 3, A, 8>, h) : run(k_expert_gated_bwd<H, 3, A, 1>, h);
+    return vec ? run(k_expert_gated_bwd<H, 1, A, 8>, h) : run(k_expert_gated_bwd<H, 1, A, 1>, h);
   };
   switch (p.act) {
     case EMB_ACT_SILU: return by_act(std::integral_constant<int, EMB_ACT_SILU>());

@@ -15,20 +15,11 @@
 // contraction and add up through shared memory in a fixed order.
 #include <algorithm>
 
-#include "expert_mm.cuh"
+#include "expert_few.cuh"
 
 namespace emb {
 
 namespace {
-
-constexpr int kL4Warps = 8, kL4Threads = 32 * kL4Warps;
-
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 // Codes k and k + 4 of a word of eight, less eight, as bf16: 128 + code is exact, and so is the difference.
 __device__ __forceinline__ uint32_t codes_at(uint32_t word, int k) {
@@ -37,42 +28,15 @@ __device__ __forceinline__ uint32_t codes_at(uint32_t word, int k) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-__device__ __forceinline__ uint32_t pair_bf16(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Eight elements of a row of x from k on (zero from `valid` on) as the fragments of two products: pairs
-// (k, k + 4) of each plane.
+// Eight elements of a row of x as the fragments of two products: pairs (k, k + 4) of each plane.
 template <typename T, int PLANES>
-__device__ __forceinline__ void x_pairs(const T* x, int valid, bool vec, uint32_t (&f)[PLANES][4]) {
+__device__ __forceinline__ void x_pairs(const Raw<T, 8>& x, uint32_t (&f)[PLANES][4]) {
   if constexpr (PLANES == 1) {
-    uint32_t w[4];
-    if (vec && valid >= 8) {
-      const uint4 q = *reinterpret_cast<const uint4*>(x);
-      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = 2 * i < valid ? reinterpret_cast<const uint16_t*>(x)[2 * i] : 0u;
-        const uint32_t hi = 2 * i + 1 < valid ? reinterpret_cast<const uint16_t*>(x)[2 * i + 1] : 0u;
-        w[i] = lo | hi << 16;
-      }
-    }
-    f[0][0] = __byte_perm(w[0], w[2], 0x5410), f[0][1] = __byte_perm(w[0], w[2], 0x7632);
-    f[0][2] = __byte_perm(w[1], w[3], 0x5410), f[0][3] = __byte_perm(w[1], w[3], 0x7632);
+    f[0][0] = __byte_perm(x.w[0], x.w[2], 0x5410), f[0][1] = __byte_perm(x.w[0], x.w[2], 0x7632);
+    f[0][2] = __byte_perm(x.w[1], x.w[3], 0x5410), f[0][3] = __byte_perm(x.w[1], x.w[3], 0x7632);
   } else {
-    float v[8];
-    if (vec && valid >= 8) {
-      const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < valid ? x[i] : 0.f;
-    }
     float p[3][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) split3(v[i], p[0][i], p[1][i], p[2][i]);
+    planes_of(x.w, p);
 #pragma unroll
     for (int q = 0; q < 3; ++q)
 #pragma unroll
@@ -80,111 +44,112 @@ __device__ __forceinline__ void x_pairs(const T* x, int valid, bool vec, uint32_
   }
 }
 
-// W: words (of eight codes) that a lane takes of a group's four lanes' share: 1 for groups of 32, 2 of
-// 64, 4 of 128 and more.  NT: eights of rows.
+// W words of eight codes, zero from byte `valid` on.
+template <int W, bool VEC>
+__device__ __forceinline__ void load_codes(const uint8_t* q, int valid, uint32_t (&w)[W]) {
+  if (VEC && valid >= 4 * W) {
+    if constexpr (W == 1) w[0] = *reinterpret_cast<const uint32_t*>(q);
+    if constexpr (W == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(q);
+      w[0] = v.x, w[1] = v.y;
+    }
+    if constexpr (W == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) w[j] = 0;
+  if (valid <= 0) return;
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * j + i < valid) w[j] |= (uint32_t)q[4 * j + i] << (8 * i);
+  }
+}
+
+// W: words (of eight codes) that a lane takes of a step: 1 for groups of 32, 2 of 64, 4 of 128 and more, so
+// that the four lanes of an output stay inside a group.  NT: eights of rows.
 template <typename T, int W, int NT, bool VEC_Q>
-__global__ void __launch_bounds__(kL4Threads)
+__global__ void __launch_bounds__(kFewThreads)
     k_linear4(const T* x, int64_t x_ld, int x_vec, const int32_t* offsets, int E, int S, const uint8_t* q, const float* scale,
-              int in, int out_dim, int group, int col_tiles, T* out, int64_t out_ld) {
+              int in, int out_dim, int per_group, int groups, T* out, int64_t out_ld, int tile0) {
   constexpr int PLANES = sizeof(T) == 4 ? 3 : 1, RT = 8 * NT, SPAN = 32 * W;  // SPAN: k of a step
-  __shared__ float sums[kL4Warps][RT][17];
-  extern __shared__ int32_t tables[];
-  int32_t *cuts = tables, *prefix = tables + E + 1;
+  constexpr int U = W * NT * PLANES <= 2 ? 4 : W * NT * PLANES <= 4 ? 2 : 1;   // steps loaded ahead
+  __shared__ float sums[kFewWarps][RT][17];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   wait_for_earlier();
   let_next_start();
-  if (warp == 0) {
-    expert_cuts(offsets, E, S, cuts, lane);
-    expert_prefix(cuts, E, prefix, lane, [=](int rows) { return (rows + RT - 1) / RT; });
-  }
-  __syncthreads();
-  const int row_bytes = (in + 1) / 2, groups = (in + group - 1) / group, steps = (in + SPAN - 1) / SPAN;
-  const int per_group = group / SPAN;
-  const int64_t tiles = (int64_t)prefix[E] * col_tiles;
-  int e = 0;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int rt = (int)(tile / col_tiles), o0 = (int)(tile - (int64_t)rt * col_tiles) * 16;
-    while (rt >= prefix[e + 1]) ++e;
-    const int r0 = cuts[e] + (rt - prefix[e]) * RT, rows = min(RT, cuts[e + 1] - r0);
-    float acc[NT][4] = {};
-    // this lane's two outputs (held inside the matrix: what lies past its end is not stored)
-    const int oa = min(o0 + g, out_dim - 1), ob = min(o0 + g + 8, out_dim - 1);
-    const int64_t base = (int64_t)e * out_dim;
-    const uint8_t *qa = q + (base + oa) * row_bytes, *qb = q + (base + ob) * row_bytes;
-    const float *sa = scale + (base + oa) * groups, *sb = scale + (base + ob) * groups;
-    // warps take whole groups in turn
-    for (int gi = warp; gi < groups; gi += kL4Warps) {
-      float part[NT][4] = {};
-      for (int st = gi * per_group; st < min(steps, (gi + 1) * per_group); ++st) {
-        const int k0 = st * SPAN + t * (8 * W);
-        uint32_t wa[W], wb[W];
-        const int b0 = k0 / 2;
-        if (VEC_Q && b0 + 4 * W <= row_bytes) {
-          if constexpr (W == 1) wa[0] = *reinterpret_cast<const uint32_t*>(qa + b0), wb[0] = *reinterpret_cast<const uint32_t*>(qb + b0);
-          if constexpr (W == 2) {
-            const uint2 u = *reinterpret_cast<const uint2*>(qa + b0), v = *reinterpret_cast<const uint2*>(qb + b0);
-            wa[0] = u.x, wa[1] = u.y, wb[0] = v.x, wb[1] = v.y;
-          }
-          if constexpr (W == 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(qa + b0), v = *reinterpret_cast<const uint4*>(qb + b0);
-            wa[0] = u.x, wa[1] = u.y, wa[2] = u.z, wa[3] = u.w, wb[0] = v.x, wb[1] = v.y, wb[2] = v.z, wb[3] = v.w;
-          }
-        } else {
+  int e, r0, rows;
+  if (!few_tile(offsets, E, S, RT, tile0 + (int)blockIdx.y, lane, e, r0, rows)) return;
+  const int row_bytes = (in + 1) / 2, steps = (in + SPAN - 1) / SPAN, o0 = blockIdx.x * 16;
+  float acc[NT][4] = {};
+  // this lane's two outputs (held inside the matrix: what lies past its end is not stored)
+  const int64_t oa = (int64_t)e * out_dim + min(o0 + g, out_dim - 1), ob = (int64_t)e * out_dim + min(o0 + g + 8, out_dim - 1);
+  const uint8_t *qa = q + oa * row_bytes, *qb = q + ob * row_bytes;
+  const float *sa = scale + oa * groups, *sb = scale + ob * groups;
+  x += (int64_t)r0 * x_ld;
+  for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
+    uint32_t wa[U][W], wb[U][W];
+    float fa[U], fb[U];
+    Raw<T, 8> rx[U][W][NT];
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            wa[j] = wb[j] = 0;
+    for (int u = 0; u < U; ++u) {
+      const int st = s0 + u * kFewWarps, k0 = st * SPAN + t * (8 * W), b0 = k0 / 2;
+      const bool there = k0 < in;
+      load_codes<W, VEC_Q>(qa + (there ? b0 : 0), there ? row_bytes - b0 : 0, wa[u]);
+      load_codes<W, VEC_Q>(qb + (there ? b0 : 0), there ? row_bytes - b0 : 0, wb[u]);
+      fa[u] = st < steps ? sa[st / per_group] : 0.f, fb[u] = st < steps ? sb[st / per_group] : 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (b0 + 4 * j + i < row_bytes) {
-                wa[j] |= (uint32_t)qa[b0 + 4 * j + i] << (8 * i);
-                wb[j] |= (uint32_t)qb[b0 + 4 * j + i] << (8 * i);
-              }
-          }
+      for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          const int r = g + 8 * m, k = k0 + 8 * j;
+          rx[u][j][m].load(x + (int64_t)(r < rows ? r : 0) * x_ld + (k < in ? k : 0), r < rows ? in - k : 0, x_vec);
         }
+    }
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const int k = k0 + 8 * j;
-          uint32_t f[NT][PLANES][4];
+    for (int u = 0; u < U; ++u) {
+      float part[NT][4] = {};
 #pragma unroll
-          for (int m = 0; m < NT; ++m) {
-            const int r = g + 8 * m;
-            x_pairs<T, PLANES>(x + (int64_t)(r0 + (r < rows ? r : 0)) * x_ld + (k < in ? k : 0), r < rows ? in - k : 0, x_vec, f[m]);
-          }
+      for (int j = 0; j < W; ++j) {
+        uint32_t f[NT][PLANES][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a[4] = {codes_at(wa[j], 2 * h), codes_at(wb[j], 2 * h), codes_at(wa[j], 2 * h + 1), codes_at(wb[j], 2 * h + 1)};
+        for (int m = 0; m < NT; ++m) x_pairs<T, PLANES>(rx[u][j][m], f[m]);
 #pragma unroll
-            for (int m = 0; m < NT; ++m)
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a[4] = {codes_at(wa[u][j], 2 * h), codes_at(wb[u][j], 2 * h), codes_at(wa[u][j], 2 * h + 1),
+                                 codes_at(wb[u][j], 2 * h + 1)};
 #pragma unroll
-              for (int pl = PLANES - 1; pl >= 0; --pl) mma16816(part[m], a, f[m][pl][2 * h], f[m][pl][2 * h + 1]);
-          }
+          for (int m = 0; m < NT; ++m)
+#pragma unroll
+            for (int pl = PLANES - 1; pl >= 0; --pl) mma16816(part[m], a, f[m][pl][2 * h], f[m][pl][2 * h + 1]);
         }
       }
-      const float fa = sa[gi], fb = sb[gi];
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
-        acc[m][0] = fmaf(fa, part[m][0], acc[m][0]), acc[m][1] = fmaf(fa, part[m][1], acc[m][1]);
-        acc[m][2] = fmaf(fb, part[m][2], acc[m][2]), acc[m][3] = fmaf(fb, part[m][3], acc[m][3]);
+        acc[m][0] = fmaf(fa[u], part[m][0], acc[m][0]), acc[m][1] = fmaf(fa[u], part[m][1], acc[m][1]);
+        acc[m][2] = fmaf(fb[u], part[m][2], acc[m][2]), acc[m][3] = fmaf(fb[u], part[m][3], acc[m][3]);
       }
     }
+  }
 #pragma unroll
-    for (int m = 0; m < NT; ++m) {  // outputs g and g + 8, rows 2 t and 2 t + 1
-      sums[warp][m * 8 + 2 * t][g] = acc[m][0], sums[warp][m * 8 + 2 * t + 1][g] = acc[m][1];
-      sums[warp][m * 8 + 2 * t][g + 8] = acc[m][2], sums[warp][m * 8 + 2 * t + 1][g + 8] = acc[m][3];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < RT * 16; i += kL4Threads) {
-      const int r = i >> 4, o = i & 15;
-      float v[1] = {0.f};
+  for (int m = 0; m < NT; ++m)
 #pragma unroll
-      for (int w = 0; w < kL4Warps; ++w) v[0] += sums[w][r][o];
-      if (r < rows && o0 + o < out_dim) {
-        Pack<T, 1> p;
-        p.set(v);
-        p.store(out + (int64_t)(r0 + r) * out_ld + o0 + o);
-      }
+    for (int i = 0; i < 4; ++i) sums[warp][m * 8 + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[m][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < RT * 16; i += kFewThreads) {
+    const int r = i >> 4, o = i & 15;
+    float v[1] = {0.f};
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) v[0] += sums[w][r][o];
+    if (r < rows && o0 + o < out_dim) {
+      Pack<T, 1> p;
+      p.set(v);
+      p.store(out + (int64_t)(r0 + r) * out_ld + o0 + o);
     }
-    __syncthreads();
   }
 }
 
@@ -225,18 +190,28 @@ __global__ void __launch_bounds__(256)
 
 template <typename T, int W, int NT>
 cudaError_t run_linear4(const emb_product4& a, cudaStream_t s) {
-  const int row_bytes = (a.in + 1) / 2, col_tiles = (a.out + 15) / 16;
+  const int row_bytes = (a.in + 1) / 2, groups = (a.in + a.group - 1) / a.group;
   const bool vec_q = row_bytes % (4 * W) == 0 && reinterpret_cast<uintptr_t>(a.d_q) % (4 * W) == 0;
   const int x_vec = rows16(a.d_x, a.x_ld, sizeof(T));
-  const int64_t most = ((int64_t)a.rows / (8 * NT) + std::min<int64_t>(a.experts, a.rows)) * col_tiles;
-  const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)device_sms() * 16);
-  const int smem = 2 * (a.experts + 1) * 4;
-  const auto run = [&](auto kern) {
-    return launch_early(kern, grid, kL4Threads, smem, s, static_cast<const T*>(a.d_x), a.x_ld, x_vec, a.d_offsets, (int)a.experts,
-                        (int)a.rows, a.d_q, a.d_scale, (int)a.in, (int)a.out, (int)a.group, col_tiles, static_cast<T*>(a.d_out),
-                        a.out_ld);
+  const auto run = [&](auto kern, int64_t tile0, int64_t tiles) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((a.out + 15) / 16), (unsigned)tiles);
+    cfg.blockDim = dim3(kFewThreads), cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(a.d_x), a.x_ld, x_vec, a.d_offsets, (int)a.experts, (int)a.rows,
+                              (const uint8_t*)a.d_q, (const float*)a.d_scale, (int)a.in, (int)a.out, (int)a.group / (32 * W), groups,
+                              static_cast<T*>(a.d_out), a.out_ld, (int)tile0);
   };
-  return vec_q ? run(k_linear4<T, W, NT, true>) : run(k_linear4<T, W, NT, false>);
+  // (a grid has 65535 rows at most)
+  const int64_t all = few_tiles(a.rows, a.experts, 8 * NT);
+  for (int64_t at = 0; at < all; at += 65535) {
+    const int64_t n = std::min<int64_t>(65535, all - at);
+    const cudaError_t e = vec_q ? run(k_linear4<T, W, NT, true>, at, n) : run(k_linear4<T, W, NT, false>, at, n);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 template <typename T, int W>

@@ -108,6 +108,12 @@ SHAPES = [
     ([511], 0, 1030, 17, "oi", 0, 0),
     ([40] * 30, 9, 72, 520, "among", 0, 0),
     ([2049, 30], 1, 320, 384, "oi", 0, 0),
+    ([20, 30, 0, 14], 2, 72, 40, "oi", 0, 0),
+    ([20, 30, 0, 14], 2, 72, 40, "io", 0, 0),
+    ([0, 60, 0, 3], 1, 479, 33, "io", 5, 1),
+    ([31], 0, 1030, 130, "io", 0, 0),
+    ([31], 0, 1030, 130, "oi", 0, 0),
+    ([1, 0, 2] * 15, 4, 256, 72, "oi", 0, 0),
 ]
 IDS = [f"{len(s[0])}x{sum(s[0])}+{s[1]}-{s[2]}-{s[3]}-{s[4]}" for s in SHAPES]
 
