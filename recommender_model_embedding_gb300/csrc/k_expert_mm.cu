@@ -7,7 +7,8 @@
 // Both are one kernel: a pair of CTAs (a cluster on two SMs) computes tiles of 256 x 256, each CTA
 // holding 128 rows of the accumulator in its tensor memory, with tcgen05.mma.cta_group::2 (M = 256,
 // N = 256, K = 16) issued by one thread of the pair's first CTA.  Per 64 of K each CTA brings 128 x
-// 64 of A and of B by TMA (16 KB each, 128-byte swizzle) into a ring of four stages; the pair reads
+// 64 of A and of B by TMA (16 KB each, 128-byte swizzle) into a ring of six stages (five
+// beyond some 100 experts; the pair reads
 // B from both.  A tile alone in one CTA (128 x 256) would write 48 KB and read 48 KB of shared memory
 // for the same arithmetic as 32 KB and 32 KB here, over what an SM's shared memory moves in
 // that time.  Operands may run along either axis (the descriptors take K-major and
@@ -39,16 +40,18 @@ namespace emb {
 constexpr int kMmEpi = 16;                         // warps that write tiles out
 constexpr int kMmWarpTma = kMmEpi, kMmWarpMma = kMmEpi + 1, kMmWarpRelay = kMmEpi + 2;
 constexpr int kMmThreads = 32 * (kMmEpi + 3);
-constexpr int kMmStages = 4;
+constexpr int kMmMaxStages = 6;
 constexpr int kMmOperand = 128 * 128;              // bytes of an operand's stage: 128 x 64 bf16
 constexpr int kMmStage = 2 * kMmOperand;
 constexpr int kMmPart = 32 * 64;                   // bytes that a warp writes at once: 32 rows of 64
-constexpr int kMmStaging = 2 * kMmPart;            // of a writing warp
-constexpr int kMmOffStaging = kMmStages * kMmStage;
-constexpr int kMmOffBars = kMmOffStaging + kMmEpi * kMmStaging;
-constexpr int kMmNumBars = 3 * kMmStages + 4;
+// shared memory: the warps' parts, barriers, the tensor memory's address, tables of E + 1 rows and tiles, stages
+constexpr int kMmNumBars = 3 * kMmMaxStages + 4;
+constexpr int kMmOffBars = kMmEpi * kMmPart;
 constexpr int kMmOffTmem = kMmOffBars + 8 * kMmNumBars;
 constexpr int kMmOffTables = kMmOffTmem + 16;
+constexpr int kMmMost = 232448;                    // bytes that a CTA can have
+__host__ __device__ constexpr int mm_off_stages(int E) { return (kMmOffTables + 8 * (E + 1) + 1023) / 1024 * 1024; }
+constexpr int mm_smem(int E, int stages) { return mm_off_stages(E) + stages * kMmStage + 1024; }  // (+ to align it)
 constexpr int kMmCols = 512;
 
 struct MmParams {
@@ -57,6 +60,7 @@ struct MmParams {
   int terms;            // products of planes: 1, 3 or 6
   uint32_t planes_a, planes_b;  // of each, four bits
   int tile_n;           // columns of a tile: 256 or 128
+  int stages;
   int chunk;            // blocks of 64 along K between sums in registers
   int split;
   uint32_t idesc;
@@ -164,14 +168,14 @@ struct Walk {
 
 // ---- writing out ----
 
-// A warp's output: parts of 32 rows of 64 bytes (one row a lane: 32 bf16 or 16 fp32 values), staged in turn in
-// its two buffers.  Full parts of an output on 16-byte boundaries leave as one TMA copy each, which takes the
+// A warp's output: parts of 32 rows of 64 bytes (one row a lane: 32 bf16 or 16 fp32 values), staged in
+// its buffer.  Full parts of an output on 16-byte boundaries leave as one TMA copy each, which takes the
 // store out of the warp's hands (and out of the load-store pipe, which the tensor core's operands
 // share); parts at an expert's end or the last columns go row by row.  Chunk c of row r lies at c ^ (r / 2 % 4), the
 // 64-byte swizzle, so that neither the lanes' writes nor reads collide.
 struct Writer {
   unsigned char* staging;
-  int lane, turn = 0;
+  int lane;
   __device__ __forceinline__ static int place(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
 
   // map: of `out`'s matrices, or NULL; x, y, z: the part's place in it
@@ -179,10 +183,9 @@ struct Writer {
   __device__ __forceinline__ void part(const float* v, T* out, int64_t ld, int rows, int cols, const CUtensorMap* map, int x,
                                        int y, int z) {
     constexpr int kEach = 16 / sizeof(T), kCols = 4 * kEach;
-    unsigned char* at = staging + turn * kMmPart;
-    turn ^= 1;
-    // the copy before the last has read this buffer
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    unsigned char* at = staging;
+    // the last copy has read the buffer
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -207,7 +210,6 @@ struct Writer {
     if (col < cols)
       for (int r = lane / kCols; r < min(rows, 32); r += 32 / kCols)
         out[(int64_t)r * ld + col] = *reinterpret_cast<const T*>(at + place(r, c) + i * sizeof(T));
-    if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // (an empty one: the count stays)
   }
 
   // 32 values a row
@@ -247,22 +249,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // (the same in both CTAs)
-  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sbase = smem_u32(smem) + mm_off_stages(p.E);  // the stages'
+  const int stages = p.stages;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kMmOffBars);
   uint64_t* full = bars;                     // first CTA: stage filled in both
-  uint64_t* empty = full + kMmStages;        // stage read (commit, to both)
-  uint64_t* landed = empty + kMmStages;      // weight gradient: this CTA's copies have landed
-  uint64_t* dfull = landed + kMmStages;      // [2] accumulator written (commit, to both)
+  uint64_t* empty = full + kMmMaxStages;        // stage read (commit, to both)
+  uint64_t* landed = empty + kMmMaxStages;      // weight gradient: this CTA's copies have landed
+  uint64_t* dfull = landed + kMmMaxStages;      // [2] accumulator written (commit, to both)
   uint64_t* dempty = dfull + 2;              // [2] first CTA: accumulator read by both
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMmOffTmem);
   int32_t* cuts = reinterpret_cast<int32_t*>(smem + kMmOffTables);
   int32_t* prefix = cuts + p.E + 1;
 
   if (tid == 0) {
-    for (int i = 0; i < kMmStages; ++i) {
+    for (int i = 0; i < kMmMaxStages; ++i) {
       mbar_init(full + i, WGRAD ? 2 : 1);
       mbar_init(empty + i, 1);
       mbar_init(landed + i, 1);
@@ -363,15 +366,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                   tma_box(&bmap, b, bar, kb * 64, n0, half, e, pb);
                 }
               }
-              if (++stage == kMmStages) stage = 0, phase ^= 1;
+              if (++stage == stages) stage = 0, phase ^= 1;
             }
           }
         }
       }
       // the last copies are read before the CTA leaves: every stage handed back
-      for (int i = 0; ok && i < kMmStages; ++i) {
+      for (int i = 0; ok && i < stages; ++i) {
         ok = mbar_wait_bounded(empty + stage, phase);
-        if (++stage == kMmStages) stage = 0, phase ^= 1;
+        if (++stage == stages) stage = 0, phase ^= 1;
       }
     }
   } else if (warp == kMmWarpMma) {
@@ -418,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                 commit_pair(empty0 + stage * 8);
               }
               accumulate = 1;
-              if (++stage == kMmStages) stage = 0, phase ^= 1;
+              if (++stage == stages) stage = 0, phase ^= 1;
             }
           if (ok && one) commit_pair(smem_u32(dfull + buf));
           buf ^= 1;
@@ -439,12 +442,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
           for (int t = 0; ok && t < terms; ++t) {
-            stage = (stage + c1 - c0 - 1) % kMmStages;  // the part's last block
+            stage = (stage + c1 - c0 - 1) % stages;  // the part's last block
             if (c1 == blocks && left < 64) {
               if (!(ok = mbar_wait_bounded(landed + stage, phases >> stage & 1))) break;
               phases ^= 1u << stage;
               // rows of 128 bytes, one for each K, in boxes of 64: two of A, one or two of B
-              unsigned char* at = smem + stage * kMmStage;
+              unsigned char* at = smem + mm_off_stages(p.E) + stage * kMmStage;
               const int boxes = tile_n > 128 ? 4 : 3;
               for (int i = lane; i < (64 - left) * 32; i += 32)
                 if ((i >> 3 & 3) < boxes)
@@ -453,14 +456,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
               __syncwarp();
               if (lane == 0) arrive_cluster(addr_in(smem_u32(full + stage), 0));
             }
-            stage = stage + 1 == kMmStages ? 0 : stage + 1;
+            stage = stage + 1 == stages ? 0 : stage + 1;
           }
         }
       }
     }
   } else {
     const int quarter = warp & 3, side = warp >> 2;  // lanes 32 * quarter.., parts `side` and `side` + 4 of 32 columns
-    Writer to{smem + kMmOffStaging + warp * kMmStaging, lane};
+    Writer to{smem + warp * kMmPart, lane};
     const CUtensorMap *om = p.out_map ? &omap : nullptr, *gm = p.gu_map ? &gmap : nullptr;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     // accumulator columns of the two parts: gated, the gate's and the up half's of the same outputs
@@ -655,7 +658,9 @@ cudaError_t launch_mm(const MmArgs& a, MmParams p, int64_t tiles_most, cudaStrea
   if (!p.out_map) omap = amap;
   if (!p.gu_map) gmap = amap;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(mm_pairs(), tiles_most));
-  const int smem = kMmOffTables + 2 * (p.E + 1) * 4 + 1024;
+  p.stages = kMmMaxStages;
+  while (mm_smem(p.E, p.stages) > kMmMost) --p.stages;
+  const int smem = mm_smem(p.E, p.stages);
   return launch_early(kern, (unsigned)(2 * pairs), kMmThreads, smem, s, amap, bmap, omap, gmap, p);
 }
 
@@ -678,6 +683,8 @@ MmParams params_of(const MmArgs& a) {
 }
 
 }  // namespace
+
+static_assert(mm_smem(kMaxExperts, 5) <= kMmMost && mm_smem(128, kMmMaxStages) <= kMmMost, "shared memory of the products");
 
 cudaError_t launch_expert_mm_rows(const MmArgs& a, cudaStream_t s) {
   if (a.S == 0) return cudaSuccess;
