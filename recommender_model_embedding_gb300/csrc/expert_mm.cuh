@@ -122,7 +122,8 @@ struct PackArgs {
   const int32_t* last = nullptr;  // rows from *last on need no copy (NULL: all)
   MmOperand to;
 };
-cudaError_t launch_expert_pack(const PackArgs& a, cudaStream_t s);
+constexpr int kMaxPacks = 3;
+cudaError_t launch_expert_packs(const PackArgs* args, int count, cudaStream_t s);  // all fp32, or all bf16
 // [dg, du] of a gated block's backward, to rows of 2 * p.out
 cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, cudaStream_t s);  // (planes: to's)
 

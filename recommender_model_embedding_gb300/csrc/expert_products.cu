@@ -37,22 +37,28 @@ MmOperand packed(Room& room, int64_t inner, int64_t rows, int halves, int expert
   return o;
 }
 
-// A matrix as the tensor cores take it: in place, or copied (the launches of a call follow it).
-cudaError_t operand(const Source& m, bool f32, Room& room, bool launch, cudaStream_t s, MmOperand& o) {
+// The copies that a call begins with.
+struct Packs {
+  PackArgs list[kMaxPacks];
+  int count = 0;
+};
+
+// A matrix as the tensor cores take it: in place, or as a copy.
+MmOperand operand(const Source& m, bool f32, Room& room, Packs& packs) {
+  MmOperand o;
   if (!f32 && reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && (m.rows <= 1 || (m.ld % 8 == 0 && m.ld >= m.inner)) &&
       (m.halves == 1 || (m.half_step % 8 == 0 && m.half_step > 0)) &&
       (m.experts == 1 || (m.expert_step % 8 == 0 && m.expert_step > 0))) {
     o.p = static_cast<const __nv_bfloat16*>(m.p);
     o.inner = m.inner, o.rows = m.rows, o.ld = m.ld, o.half_step = m.half_step, o.expert_step = m.expert_step;
     o.halves = m.halves, o.experts = m.experts;
-    return cudaSuccess;
+    return o;
   }
   o = packed(room, m.inner, m.rows, m.halves, m.experts, f32 ? 3 : 1);
-  if (!launch) return cudaSuccess;
-  PackArgs a;
+  PackArgs& a = packs.list[packs.count++];
   a.src = m.p, a.ld = m.ld, a.half_step = m.half_step, a.expert_step = m.expert_step;
   a.f32 = f32, a.last = m.last, a.to = o;
-  return launch_expert_pack(a, s);
+  return o;
 }
 
 // Tiles of a weight gradient with M x N outputs: narrower ones, and then rows cut into parts, where the
@@ -64,6 +70,9 @@ void cut_wgrad(MmArgs& a, int64_t rows) {
   a.tile_n = a.E * tiles(256) >= pairs ? 256 : 128, a.split = 0;
   const int64_t each = tiles(a.tile_n);
   if (a.E * each >= pairs) return;
+  // a tile takes about 0.15 us for 64 rows and product of planes; parts cost a launch and their sum, some 6 us
+  const int terms = a.f32 ? 6 : std::max(a.a.planes, a.b.planes);
+  if (rows * terms < (int64_t)a.E * 64 * 80) return;
   const int64_t parts = a.E == 1 ? pairs / each : 2 * pairs / each;
   const int64_t cut = std::max<int64_t>(256, (rows / parts + 63) / 64 * 64);
   if (cut * a.E < rows) a.split = (int)cut;
@@ -78,6 +87,7 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
   const int64_t S = p.rows, in = p.in, f = p.out, O = gated ? 2 * f : f;
   const int32_t* last = p.d_offsets ? p.d_offsets + p.experts : nullptr;
   cudaError_t e = cudaSuccess;
+  Packs packs;
   MmArgs a;
   a.offsets = p.d_offsets, a.E = p.experts, a.S = (int)S, a.f32 = f32;
   const Source x{p.d_x, in, S, p.x_ld, 0, 0, 1, 1, last};
@@ -94,38 +104,35 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
       return launch ? launch_expert_few(w, s) : cudaSuccess;
     }
     Source w{p.d_w, p.w_turned ? f : in, p.w_turned ? in : f, p.w_ld, p.w_turned ? f : f * p.w_ld, p.w_step, gated ? 2 : 1, p.experts};
-    if ((e = operand(x, f32, room, launch, s, a.a)) != cudaSuccess) return e;
-    if ((e = operand(w, f32, room, launch, s, a.b)) != cudaSuccess || !launch) return e;
+    a.a = operand(x, f32, room, packs), a.b = operand(w, f32, room, packs);
+    if (!launch) return cudaSuccess;
+    if ((e = launch_expert_packs(packs.list, packs.count, s)) != cudaSuccess) return e;
     a.b_mn = p.w_turned != 0;
     a.N = (int)f, a.K = (int)in, a.act = gated ? p.act : -1;
     a.out = p.d_out, a.out_ld = p.out_ld, a.out_bf16 = !f32;
     if (gated) a.gu = p.d_gu, a.gu_ld = p.gu_ld;
     return launch_expert_mm_rows(a, s);
   }
-  MmOperand d;  // [dg, du], or dout
+  // [dg, du], or dout; an fp32 gradient of bf16 weights takes all of dg and du, dx their first plane
+  MmOperand d, xo, wo;
+  const bool dx = p.d_dx && S > 0;
   if (S > 0) {
-    if (gated) {
-      // (an fp32 gradient of bf16 weights takes all of dg and du, dx their first plane)
-      d = packed(room, O, S, 1, 1, f32 || (p.d_dw && p.dw_dtype == EMB_F32) ? 3 : 1);
-      if (launch) e = launch_expert_gated_bwd(p, d, s);
-    } else {
-      e = operand({p.d_dout, f, S, p.dout_ld, 0, 0, 1, 1, last}, f32, room, launch, s, d);
-    }
-    if (e != cudaSuccess) return e;
+    if (gated) d = packed(room, O, S, 1, 1, f32 || (p.d_dw && p.dw_dtype == EMB_F32) ? 3 : 1);
+    else d = operand({p.d_dout, f, S, p.dout_ld, 0, 0, 1, 1, last}, f32, room, packs);
+    if (dx) wo = operand({p.d_w, p.w_turned ? O : in, p.w_turned ? in : O, p.w_ld, 0, p.w_step, 1, p.experts}, f32, room, packs);
+    if (p.d_dw) xo = operand(x, f32, room, packs);
+    if (launch && packs.count && (e = launch_expert_packs(packs.list, packs.count, s)) != cudaSuccess) return e;
+    if (launch && gated && (e = launch_expert_gated_bwd(p, d, s)) != cudaSuccess) return e;
   }
-  if (p.d_dx && S > 0) {
-    a.a = d;
+  if (dx) {
+    a.a = d, a.b = wo;
     if (!f32) a.a.planes = 1;
-    const Source w{p.d_w, p.w_turned ? O : in, p.w_turned ? in : O, p.w_ld, 0, p.w_step, 1, p.experts};
-    if ((e = operand(w, f32, room, launch, s, a.b)) != cudaSuccess) return e;
     a.b_mn = p.w_turned == 0;
     a.N = (int)in, a.K = (int)O;
     a.out = p.d_dx, a.out_ld = p.dx_ld, a.out_bf16 = !f32;
     if (launch && (e = launch_expert_mm_rows(a, s)) != cudaSuccess) return e;
   }
   if (p.d_dw) {
-    MmOperand xo;
-    if (S > 0 && (e = operand(x, f32, room, launch, s, xo)) != cudaSuccess) return e;
     a.a = p.dw_turned ? xo : d, a.b = p.dw_turned ? d : xo;
     a.M = (int)(p.dw_turned ? in : O), a.N = (int)(p.dw_turned ? O : in), a.K = 0;
     a.out = p.d_dw, a.out_ld = p.dw_ld, a.out_step = p.dw_step, a.out_bf16 = p.dw_dtype == EMB_BF16;

@@ -552,32 +552,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kMmCols) : "memory");
 }
 
-// Sums the parts of each expert's weight gradient, in order.
-template <typename T>
+// Sums the parts of each expert's weight gradient, in order: 1 << shift threads of a row, EPU columns each.
+template <typename T, int EPU>
 __global__ void __launch_bounds__(256)
-    k_expert_parts(const float* parts, const int32_t* offsets, int E, int S, int split, int M, int N, T* out, int64_t ld,
-                   int64_t step) {
+    k_expert_parts(const float* parts, const int32_t* offsets, int E, int S, int split, int M, int N, int shift, T* out,
+                   int64_t ld, int64_t step) {
   __shared__ int32_t cuts[kMaxExperts + 1], prefix[kMaxExperts + 1];
   wait_for_earlier();
+  let_next_start();
   if (threadIdx.x < 32) {
     expert_cuts(offsets, E, S, cuts, threadIdx.x);
     expert_prefix(cuts, E, prefix, threadIdx.x, [=](int rows) { return (rows + split - 1) / split; });
   }
   __syncthreads();
-  let_next_start();
   const int64_t each = (int64_t)M * N;
-  for (int e = blockIdx.y; e < E; e += gridDim.y) {
-    const int a = prefix[e], b = prefix[e + 1];
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < each; i += (int64_t)gridDim.x * 256) {
-      float v = 0.f;
-      for (int k = a; k < b; ++k) v += parts[k * each + i];
-      const int64_t r = i / N;
-      Pack<T, 1> o;
-      const float one[1] = {v};
-      o.set(one);
-      o.store(out + e * step + r * ld + (i - r * N));
+  const int e = blockIdx.y, a = prefix[e], b = prefix[e + 1], per = 256 >> shift;
+  for (int r = blockIdx.x * per + (threadIdx.x >> shift); r < M; r += gridDim.x * per)
+    for (int c = (threadIdx.x & ((1 << shift) - 1)) * EPU; c < N; c += EPU << shift) {
+      const float* from = parts + a * each + (int64_t)r * N + c;
+      float v[EPU] = {};
+#pragma unroll 4
+      for (int k = a; k < b; ++k, from += each) {
+        Pack<float, EPU> q;
+        float x[EPU];
+        q.load(from);
+        q.get(x);
+#pragma unroll
+        for (int i = 0; i < EPU; ++i) v[i] += x[i];
+      }
+      Pack<T, EPU> o;
+      o.set(v);
+      o.store(out + e * step + r * ld + c);
     }
-  }
 }
 
 // ---- host ----
@@ -729,19 +735,26 @@ cudaError_t launch_expert_mm_wgrad(const MmArgs& a, cudaStream_t s) {
   }
   // (no rows: no parts, and zeros)
   const int split = a.split ? a.split : 64;
-  const int64_t each = (int64_t)a.M * a.N;
-  const unsigned gx = (unsigned)std::min<int64_t>((each + 255) / 256, std::max(1, device_sms() * 8 / a.E));
-  const auto sum = [&](auto* out) {
+  const int oe = a.out_bf16 ? 2 : 4;
+  const bool vec = a.N % 4 == 0 && rows_on(a.out, a.out_ld, oe, 4 * oe) && a.out_step % 4 == 0;
+  int shift = 0;
+  while (shift < 8 && (1 << shift) < (vec ? a.N / 4 : a.N)) ++shift;
+  const int64_t per = 256 >> shift;
+  const auto sum = [&](auto kern, auto* out) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(gx, (unsigned)a.E), cfg.blockDim = dim3(256), cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
-    using T = std::remove_pointer_t<decltype(out)>;
-    return cudaLaunchKernelEx(&cfg, k_expert_parts<T>, (const float*)a.parts, a.offsets, a.E, a.S, split, a.M, a.N, out,
-                              a.out_ld, a.out_step);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>((a.M + per - 1) / per, std::max(1, device_sms() * 16 / a.E)), (unsigned)a.E);
+    cfg.blockDim = dim3(256), cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, (const float*)a.parts, a.offsets, a.E, a.S, split, a.M, a.N, shift, out, a.out_ld, a.out_step);
   };
-  return a.out_bf16 ? sum(static_cast<__nv_bfloat16*>(a.out)) : sum(static_cast<float*>(a.out));
+  if (a.out_bf16) {
+    auto* out = static_cast<__nv_bfloat16*>(a.out);
+    return vec ? sum(k_expert_parts<__nv_bfloat16, 4>, out) : sum(k_expert_parts<__nv_bfloat16, 1>, out);
+  }
+  auto* out = static_cast<float*>(a.out);
+  return vec ? sum(k_expert_parts<float, 4>, out) : sum(k_expert_parts<float, 1>, out);
 }
 
 }  // namespace emb

@@ -19,38 +19,62 @@ namespace {
 
 constexpr int kPrepThreads = 256;
 
-// elements [0, EPU) of a row's piece; places from `valid` on are zero
-template <typename T, int EPU>
-__device__ __forceinline__ void load_piece(const T* p, int valid, bool vec, float (&v)[EPU]) {
-  if constexpr (EPU == 8) {
-    if (vec && valid >= 8) {
-      if constexpr (sizeof(T) == 2) {
-        Pack<T, 8> a;
-        a.load(p);
-        a.get(v);
-      } else {
-        Pack<T, 4> a, b;
-        a.load(p);
-        b.load(p + 4);
-        float x[4], y[4];
-        a.get(x);
-        b.get(y);
+// Eight elements of a row, zero from `valid` on, of a matrix that lies in [lo, hi): in whole 16-byte words where the
+// row is not on their boundary too (those that hold the elements, shifted into place), one by one at the matrix's
+// ends.
+template <typename T>
+__device__ __forceinline__ void load_any8(const T* p, int valid, uintptr_t lo, uintptr_t hi, float (&v)[8]) {
+  constexpr int N = 8 * sizeof(T) / 4, C = N / 4 + 1;  // words of the elements, 16-byte words that hold them
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p), from = at & ~(uintptr_t)15;
+  const uint32_t s = (uint32_t)(at - from);
+  uint32_t w[N];
+  if (valid >= 8 && from >= lo && from + 16 * (s ? C : C - 1) <= hi) {
+    uint32_t q[4 * C];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = x[i], v[4 + i] = y[i];
+    for (int c = 0; c < C; ++c) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (c < C - 1 || s) u = reinterpret_cast<const uint4*>(from)[c];
+      q[4 * c] = u.x, q[4 * c + 1] = u.y, q[4 * c + 2] = u.z, q[4 * c + 3] = u.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * C - 1; ++i) q[i] = s & 4 ? q[i + 1] : q[i];
+#pragma unroll
+    for (int i = 0; i < 4 * C - 3; ++i) q[i] = s & 8 ? q[i + 2] : q[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = sizeof(T) == 2 ? __funnelshift_r(q[i], q[i + 1], (s & 2) * 8) : q[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = i < valid ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+      } else {
+        const uint32_t a = 2 * i < valid ? reinterpret_cast<const uint16_t*>(p)[2 * i] : 0u;
+        const uint32_t b = 2 * i + 1 < valid ? reinterpret_cast<const uint16_t*>(p)[2 * i + 1] : 0u;
+        w[i] = a | b << 16;
       }
-      return;
     }
   }
 #pragma unroll
-  for (int i = 0; i < EPU; ++i) {
-    v[i] = 0.f;
-    if (i < valid) {
-      Pack<T, 1> a;
-      a.load(p + i);
-      float x[1];
-      a.get(x);
-      v[i] = x[0];
-    }
+  for (int i = 0; i < 8; ++i)
+    v[i] = sizeof(T) == 4 ? __uint_as_float(w[i]) : __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+}
+
+// EPU elements on their boundary
+template <typename T, int EPU>
+__device__ __forceinline__ void load_piece(const T* p, float (&v)[EPU]) {
+  if constexpr (EPU == 8 && sizeof(T) == 4) {
+    Pack<T, 4> a, b;
+    a.load(p);
+    b.load(p + 4);
+    float x[4], y[4];
+    a.get(x);
+    b.get(y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = x[i], v[4 + i] = y[i];
+  } else {
+    Pack<T, EPU> a;
+    a.load(p);
+    a.get(v);
   }
 }
 
@@ -74,24 +98,44 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* to, int64_t plane, co
   }
 }
 
+// The matrices to copy, in one launch: blocks [first, next one's first) are a job's.
+struct PackJob {
+  const void* src;
+  int64_t ld, half_step, expert_step;
+  const int32_t* last;
+  FastDiv rows, halves;
+  uint32_t all, first, blocks;
+  int inner, shift;
+  __nv_bfloat16* to;
+  int64_t to_ld, to_half, to_expert, to_plane;
+};
+struct PackJobs {
+  PackJob job[kMaxPacks];
+  int count;
+};
+
 template <typename T, int PLANES>
-__global__ void __launch_bounds__(kPrepThreads)
-    k_expert_pack(const T* src, int64_t ld, int64_t half_step, int64_t expert_step, int vec, const int32_t* last,
-                  FastDiv rows, FastDiv halves, uint32_t all, int inner, int shift, __nv_bfloat16* to, int64_t to_ld,
-                  int64_t to_half, int64_t to_expert, int64_t to_plane) {
+__global__ void __launch_bounds__(kPrepThreads) k_expert_pack(const __grid_constant__ PackJobs jobs) {
   wait_for_earlier();
   let_next_start();
+  int j = 0;
+  while (j + 1 < jobs.count && blockIdx.x >= jobs.job[j + 1].first) ++j;
+  const PackJob& a = jobs.job[j];
+  const int shift = a.shift;
   const uint32_t per = kPrepThreads >> shift;
-  const uint32_t most = last ? (uint32_t)min(max(*last, 0), (int)all) : all;
-  const int units = (inner + 7) / 8, sub = threadIdx.x & ((1 << shift) - 1);
-  for (uint32_t i = blockIdx.x * per + (threadIdx.x >> shift); i < most; i += gridDim.x * per) {
-    const uint32_t m = rows.div(i), r = i - m * rows.d, e = halves.div(m), h = m - e * halves.d;
-    const T* from = src + (int64_t)r * ld + (int64_t)h * half_step + (int64_t)e * expert_step;
-    __nv_bfloat16* out = to + (int64_t)r * to_ld + (int64_t)h * to_half + (int64_t)e * to_expert;
+  const uint32_t most = a.last ? (uint32_t)min(max(*a.last, 0), (int)a.all) : a.all;
+  const int units = (a.inner + 7) / 8, sub = threadIdx.x & ((1 << shift) - 1);
+  const int64_t bytes = ((int64_t)(a.rows.d - 1) * a.ld + a.inner) * (int64_t)sizeof(T);
+  for (uint32_t i = (blockIdx.x - a.first) * per + (threadIdx.x >> shift); i < most; i += a.blocks * per) {
+    const uint32_t m = a.rows.div(i), r = i - m * a.rows.d, e = a.halves.div(m), h = m - e * a.halves.d;
+    const T* from = static_cast<const T*>(a.src) + (int64_t)h * a.half_step + (int64_t)e * a.expert_step;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(from), hi = lo + bytes;
+    from += (int64_t)r * a.ld;
+    __nv_bfloat16* out = a.to + (int64_t)r * a.to_ld + (int64_t)h * a.to_half + (int64_t)e * a.to_expert;
     for (int u = sub; u < units; u += 1 << shift) {
       float v[8];
-      load_piece<T, 8>(from + u * 8, inner - u * 8, vec, v);
-      store_piece<PLANES, 8>(out + u * 8, to_plane, v);
+      load_any8<T>(from + u * 8, a.inner - u * 8, lo, hi, v);
+      store_piece<PLANES, 8>(out + u * 8, a.to_plane, v);
     }
   }
 }
@@ -111,9 +155,9 @@ __global__ void __launch_bounds__(kPrepThreads)
     __nv_bfloat16* out = to + (int64_t)r * to_ld;
     for (int c = sub; c < units; c += 1 << shift) {
       float dv[EPU], gv[EPU], uv[EPU];
-      load_piece<T, EPU>(d + c * EPU, EPU, true, dv);
-      load_piece<T, EPU>(g + c * EPU, EPU, true, gv);
-      load_piece<T, EPU>(g + f + c * EPU, EPU, true, uv);
+      load_piece<T, EPU>(d + c * EPU, dv);
+      load_piece<T, EPU>(g + c * EPU, gv);
+      load_piece<T, EPU>(g + f + c * EPU, uv);
 #pragma unroll
       for (int i = 0; i < EPU; ++i) {
         float slope;
@@ -141,18 +185,23 @@ unsigned row_grid(int64_t rows, int shift) {
 
 }  // namespace
 
-cudaError_t launch_expert_pack(const PackArgs& a, cudaStream_t s) {
-  const int64_t all = a.to.rows * a.to.halves * a.to.experts;
-  if (all == 0) return cudaSuccess;
-  const int shift = row_shift((a.to.inner + 7) / 8), elem = a.f32 ? 4 : 2;
-  const int vec = rows_on(a.src, a.ld, elem, 16) && a.half_step * elem % 16 == 0 && a.expert_step * elem % 16 == 0;
-  const auto run = [&](auto kern, auto* src) {
-    return launch_early(kern, row_grid(all, shift), kPrepThreads, 0, s, src, a.ld, a.half_step, a.expert_step, vec, a.last,
-                        FastDiv((uint32_t)a.to.rows), FastDiv((uint32_t)a.to.halves), (uint32_t)all, (int)a.to.inner, shift,
-                        const_cast<__nv_bfloat16*>(a.to.p), a.to.ld, a.to.half_step, a.to.expert_step, a.to.plane_step);
-  };
-  return a.f32 ? run(k_expert_pack<float, 3>, static_cast<const float*>(a.src))
-               : run(k_expert_pack<__nv_bfloat16, 1>, static_cast<const __nv_bfloat16*>(a.src));
+cudaError_t launch_expert_packs(const PackArgs* args, int count, cudaStream_t s) {
+  PackJobs jobs{};
+  unsigned blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    const PackArgs& a = args[i];
+    const int64_t all = a.to.rows * a.to.halves * a.to.experts;
+    if (all == 0) continue;
+    const int shift = row_shift((a.to.inner + 7) / 8);
+    const unsigned mine = row_grid(all, shift);
+    jobs.job[jobs.count++] = {a.src, a.ld, a.half_step, a.expert_step, a.last, FastDiv((uint32_t)a.to.rows), FastDiv((uint32_t)a.to.halves),
+                              (uint32_t)all, blocks, mine, (int)a.to.inner, shift, const_cast<__nv_bfloat16*>(a.to.p), a.to.ld,
+                              a.to.half_step, a.to.expert_step, a.to.plane_step};
+    blocks += mine;
+  }
+  if (blocks == 0) return cudaSuccess;
+  return args[0].f32 ? launch_early(k_expert_pack<float, 3>, blocks, kPrepThreads, 0, s, jobs)
+                     : launch_early(k_expert_pack<__nv_bfloat16, 1>, blocks, kPrepThreads, 0, s, jobs);
 }
 
 cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, cudaStream_t s) {

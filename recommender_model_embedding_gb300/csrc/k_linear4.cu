@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kFewThreads)
     k_linear4(const T* x, int64_t x_ld, int x_vec, const int32_t* offsets, int E, int S, const uint8_t* q, const float* scale,
               int in, int out_dim, int per_group, int groups, T* out, int64_t out_ld, int tile0) {
   constexpr int PLANES = sizeof(T) == 4 ? 3 : 1, RT = 8 * NT, SPAN = 32 * W;  // SPAN: k of a step
-  constexpr int U = W * NT * PLANES <= 2 ? 4 : W * NT * PLANES <= 4 ? 2 : 1;   // steps loaded ahead
+  constexpr int U = W * NT <= 1 && PLANES == 1 ? 4 : W * NT * (PLANES == 3 ? 2 : 1) <= 4 ? 2 : 1;  // steps loaded ahead
   __shared__ float sums[kFewWarps][RT][17];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   wait_for_earlier();
@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(kFewThreads)
       const bool there = k0 < in;
       load_codes<W, VEC_Q>(qa + (there ? b0 : 0), there ? row_bytes - b0 : 0, wa[u]);
       load_codes<W, VEC_Q>(qb + (there ? b0 : 0), there ? row_bytes - b0 : 0, wb[u]);
-      fa[u] = st < steps ? sa[st / per_group] : 0.f, fb[u] = st < steps ? sb[st / per_group] : 0.f;
+      const int gi = per_group == 1 ? st : st / per_group;
+      fa[u] = st < steps ? sa[gi] : 0.f, fb[u] = st < steps ? sb[gi] : 0.f;
 #pragma unroll
       for (int j = 0; j < W; ++j)
 #pragma unroll
