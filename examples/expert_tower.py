@@ -5,9 +5,9 @@
 The embedding layer (26 one-hot tables of width 128 and their dot interaction) hands a row of
 128 + 351 features per sample to the tower: a norm and a projection to the residual stream, one
 residual block of experts (each sample goes to the two that its router likes best) with a norm on
-either side and a gate, and a linear head.  Matrix products are torch's; everything else of the
-tower runs in the library: gated_norm, expert_sort, expert_dispatch, expert_combine, their
-gradients, and clip_grads over all of the tower's gradients before its Adagrad step.  The
+either side and a gate, and a linear head.  Dense matrix products are torch's; everything else of the
+tower runs in the library: gated_norm, expert_sort, expert_dispatch, the experts' products
+(expert_linear), expert_combine, their gradients, and clip_grads over all of the tower's gradients before its Adagrad step.  The
 gradient of the tower's input goes back into the embedding layer, which updates its rows itself.
 """
 import argparse
@@ -51,16 +51,15 @@ class ExpertTower:
         top = (h @ p["w_router"]).topk(k, dim=1)
         s["ids"], s["w"] = top.indices, top.values.softmax(1)
         i32 = lambda n: torch.empty(n, dtype=torch.int32, device=x.device)
-        order, s["pos"], offsets = i32(B * k), i32(B * k), i32(self.experts + 1)
-        E.expert_sort(s["ids"], self.experts, order, s["pos"], offsets)
+        order, s["pos"], s["offsets"] = i32(B * k), i32(B * k), i32(self.experts + 1)
+        E.expert_sort(s["ids"], self.experts, order, s["pos"], s["offsets"])
         s["xs"] = torch.empty((B * k, x.shape[1]), device=x.device)
         E.expert_dispatch(h, s["pos"], s["xs"])
-        s["cuts"] = offsets.tolist()  # the products' sizes: the one wait for the device
         s["a"] = torch.empty((B * k, p["w1"].shape[2]), device=x.device)
         s["ys"] = torch.empty_like(s["xs"])
-        for e, (lo, hi) in enumerate(zip(s["cuts"], s["cuts"][1:])):
-            s["a"][lo:hi] = (s["xs"][lo:hi] @ p["w1"][e]).relu()
-            s["ys"][lo:hi] = s["a"][lo:hi] @ p["w2"][e]
+        E.expert_linear(s["xs"], p["w1"].transpose(1, 2), s["a"], offsets=s["offsets"])
+        s["a"].relu_()
+        E.expert_linear(s["a"], p["w2"].transpose(1, 2), s["ys"], offsets=s["offsets"])
         y = s["y"] = torch.empty_like(x)
         E.expert_combine(s["ys"], s["pos"], s["w"], y)
         s["gate"] = h @ p["w_gate"]
@@ -82,13 +81,10 @@ class ExpertTower:
                               dw_pre=g["norm_out"])
         dys, dw = torch.empty_like(s["ys"]), torch.empty_like(s["w"])
         E.expert_combine_backward(dy, s["ys"], s["pos"], s["w"], dys, dw)
-        dxs = torch.empty_like(s["xs"])
-        for e, (lo, hi) in enumerate(zip(s["cuts"], s["cuts"][1:])):
-            a, dyse = s["a"][lo:hi], dys[lo:hi]
-            torch.mm(a.t(), dyse, out=g["w2"][e])
-            da = (dyse @ p["w2"][e].t()) * (a > 0)
-            torch.mm(s["xs"][lo:hi].t(), da, out=g["w1"][e])
-            dxs[lo:hi] = da @ p["w1"][e].t()
+        dxs, da = torch.empty_like(s["xs"]), torch.empty_like(s["a"])
+        E.expert_linear_backward(dys, s["a"], p["w2"].transpose(1, 2), da, g["w2"].transpose(1, 2), offsets=s["offsets"])
+        da *= s["a"] > 0
+        E.expert_linear_backward(da, s["xs"], p["w1"].transpose(1, 2), dxs, g["w1"].transpose(1, 2), offsets=s["offsets"])
         dh = torch.empty_like(x)
         E.expert_dispatch_backward(dxs, s["pos"], dh)
         # the router's softmax over the chosen experts, and the gate

@@ -406,7 +406,7 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
  * Workspace: what has to be copied for the tensor cores (fp32 operands, and rows or weights not on 16-byte
  * boundaries), the gated backward's [dg, du], and parts of dw; from the same arguments, pointers among
  * them (only their alignment is looked at).
- * EMB_EINVAL: rows outside [0, 2^31), experts outside [1, EMB_EXPERT_MAX] or not 1 without offsets, in or
+ * EMB_EINVAL: rows outside [0, 2^31 - 1024], experts outside [1, EMB_EXPERT_MAX] or not 1 without offsets, in or
  * out outside [1, EMB_EXPERT_MAX_DIM], bad types, act or steps, a missing buffer (d_dx or d_dw may be
  * NULL, not both; d_gu of the forward too) or one misaligned for its type, a short or misaligned
  * workspace. */

@@ -1285,8 +1285,11 @@ static bool weights_ok(int64_t ld, int64_t step, int64_t rows, int64_t inner, in
   return experts <= 1 || step >= one || (step >= inner && (rows <= 1 || ld >= (experts - 1) * step + inner));
 }
 
+// (a tile's rows past the last are still numbers of 32 bits)
+constexpr int64_t kProductRows = INT32_MAX - 1023;
+
 static bool product_ok(const emb_product* p, ProductKind kind) {
-  if (!p || p->rows < 0 || p->rows > INT32_MAX || p->experts < 1 || p->experts > EMB_EXPERT_MAX) return false;
+  if (!p || p->rows < 0 || p->rows > kProductRows || p->experts < 1 || p->experts > EMB_EXPERT_MAX) return false;
   if (!p->d_offsets && p->experts != 1) return false;
   if (p->in < 1 || p->in > EMB_EXPERT_MAX_DIM || p->out < 1 || p->out > EMB_EXPERT_MAX_DIM) return false;
   if (p->dtype != EMB_F32 && p->dtype != EMB_BF16) return false;
@@ -1353,7 +1356,7 @@ emb_status emb_quantize_rows4(const void* d_w, int64_t w_ld, int64_t n, int32_t 
 }
 
 emb_status emb_expert_linear4(const emb_product4* p, void* stream) {
-  if (!p || p->rows < 0 || p->rows > INT32_MAX || p->experts < 1 || p->experts > EMB_EXPERT_MAX ||
+  if (!p || p->rows < 0 || p->rows > kProductRows || p->experts < 1 || p->experts > EMB_EXPERT_MAX ||
       (!p->d_offsets && p->experts != 1) || p->in < 1 || p->in > EMB_EXPERT_MAX_DIM || p->out < 1 ||
       p->out > EMB_EXPERT_MAX_DIM || !group4_ok(p->group) || (p->dtype != EMB_F32 && p->dtype != EMB_BF16))
     return EMB_EINVAL;

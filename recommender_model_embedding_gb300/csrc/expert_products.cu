@@ -78,8 +78,18 @@ void cut_wgrad(MmArgs& a, int64_t rows) {
   if (cut * a.E < rows) a.split = (int)cut;
 }
 
-// Whether experts have so few rows that the kernel for them is the faster.
-bool few(int64_t rows, int experts, bool f32) { return rows <= 32 * (int64_t)experts && few_tiles(rows, experts, 8) <= 65535; }
+// Whether the kernel for few rows is the faster, by what both take (microseconds, weights in MB; measured over 1 to
+// 128 experts, widths 128 to 2048, 1 to 256 rows an expert, both layouts): that kernel reads the weights once for
+// every 32 rows of an expert, at a rate that falls with the rows it multiplies them by (64 experts of 1024 x
+// 512 in bf16: 15 us with 8 rows, 22 with 16, 32 with 32); the tiles' kernel takes longer to get going, and
+// reads them once for 256 rows (16 us for all three), for fp32 after copying them as bf16 planes.
+bool few(int64_t rows, int experts, int64_t outs, int64_t in, bool f32) {
+  const int64_t each = (rows + experts - 1) / experts, passes = (each + 31) / 32;
+  if (each > 128 || few_tiles(rows, experts, 8) > 65535) return false;
+  const double mb = 1e-6 * (double)(experts * outs * in) * (f32 ? 4 : 2);
+  const double rate = f32 ? (each <= 8 ? 0.75 : each <= 16 ? 1.0 : 1.4) : (each <= 8 ? 0.19 : each <= 16 ? 0.30 : 0.43);
+  return 2.5 + (double)passes * mb * rate < (f32 ? 10.5 + 0.9 * mb : 6.0 + 0.15 * mb);
+}
 
 cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool launch, cudaStream_t s) {
   const bool f32 = p.dtype == EMB_F32, gated = kind == kGated || kind == kGatedBackward;
@@ -93,7 +103,7 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
   const Source x{p.d_x, in, S, p.x_ld, 0, 0, 1, 1, last};
   if (!back) {
     if (S == 0) return cudaSuccess;
-    if (few(S, p.experts, f32)) {
+    if (few(S, p.experts, O, in, f32)) {
       FewArgs w;
       w.offsets = p.d_offsets, w.E = p.experts, w.S = (int)S, w.in = (int)in, w.out = (int)f, w.act = gated ? p.act : -1;
       w.f32 = f32, w.turned = p.w_turned != 0;

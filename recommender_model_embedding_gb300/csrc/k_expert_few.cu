@@ -55,11 +55,11 @@ __device__ __forceinline__ void store_one(T* p, float v) {
 
 // ACT: gated, or -1.  NT: eights of rows.
 template <typename T, int ACT, int NT, bool TURNED>
-__global__ void __launch_bounds__(kFewThreads) k_expert_few(FewParams p) {
+__global__ void __launch_bounds__(kFewThreads, 2) k_expert_few(FewParams p) {
   constexpr bool GATED = ACT >= 0;
   constexpr int H = GATED ? 2 : 1, PL = kPlanes<T>, RT = 8 * NT;
   constexpr int OUTS = TURNED ? 32 : 16, MT = OUTS / 16;  // outputs of a CTA (of each half), in tiles of 16
-  constexpr int STEP = TURNED ? 16 : 32, U = NT == 1 && H * PL <= 3 ? (TURNED ? 4 : 2) : NT <= 2 ? 2 : 1;
+  constexpr int STEP = TURNED ? 16 : 32, U = PL == 3 ? (NT * H == 1 ? 2 : 1) : NT == 1 ? (TURNED ? 4 : 2) : NT == 2 ? 2 : 1;
   __shared__ float sums[kFewWarps][RT][H * OUTS + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   wait_for_earlier();
@@ -244,11 +244,12 @@ cudaError_t run_few(const FewParams& p, bool turned, cudaStream_t s) {
     cfg.blockDim = dim3(kFewThreads), cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
   };
-  // (a gated block's two halves of 32 outputs for 32 rows would be more sums than shared memory without opting in)
-  constexpr int NTT = ACT >= 0 && NT == 4 ? 2 : NT;
-  if constexpr (NTT != NT) {
-    if (turned) return run_few<T, ACT, NTT>(p, true, s);
-    return run(k_expert_few<T, ACT, NT, false>);
+  // (a gated block's two halves are the sums and registers of twice the outputs: 32 rows of them in bf16 as the
+  // weights usually lie, else 16)
+  if constexpr (ACT >= 0 && NT == 4) {
+    if (turned || sizeof(T) == 4) return run_few<T, ACT, 2>(p, turned, s);
+    if constexpr (sizeof(T) == 2) return run(k_expert_few<T, ACT, NT, false>);
+    return cudaErrorInvalidValue;
   } else {
     return turned ? run(k_expert_few<T, ACT, NT, true>) : run(k_expert_few<T, ACT, NT, false>);
   }

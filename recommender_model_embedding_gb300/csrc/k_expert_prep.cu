@@ -180,7 +180,7 @@ int row_shift(int64_t units) {
 
 unsigned row_grid(int64_t rows, int shift) {
   const int64_t per = kPrepThreads >> shift;
-  return (unsigned)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, (int64_t)device_sms() * 16));
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, (int64_t)device_sms() * 128));
 }
 
 }  // namespace
