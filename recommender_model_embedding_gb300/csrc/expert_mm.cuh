@@ -125,7 +125,7 @@ struct PackArgs {
 constexpr int kMaxPacks = 3;
 cudaError_t launch_expert_packs(const PackArgs* args, int count, cudaStream_t s);  // all fp32, or all bf16
 // [dg, du] of a gated block's backward, to rows of 2 * p.out
-cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, cudaStream_t s);  // (planes: to's)
+cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, bool beside, cudaStream_t s);  // (planes: to's)
 
 struct MmArgs {
   MmOperand a, b;
@@ -144,6 +144,9 @@ struct MmArgs {
   int tile_n = 256;              // weight gradient: columns of a tile, 256 or 128
   int split = 0;                 // weight gradient: rows of a part (a multiple of 64), 0: no parts
   float* parts = nullptr;        // [parts][M][N]
+  // launched right after a kernel of the same call, one that lets the next start only when it has passed its own
+  // wait, and needs nothing of it: the two run side by side
+  bool beside = false;
 };
 // A rows product where experts have few rows, from the matrices as they lie.
 struct FewArgs {

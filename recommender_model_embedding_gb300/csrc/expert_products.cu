@@ -61,18 +61,23 @@ MmOperand operand(const Source& m, bool f32, Room& room, Packs& packs) {
   return o;
 }
 
-// Tiles of a weight gradient with M x N outputs: narrower ones, and then rows cut into parts, where the
+// Tiles of a weight gradient with M x N outputs: narrower ones, or rows cut into parts, where the
 // experts' tiles alone leave pairs of SMs without work.  A part's rows are such that one dense layer's tiles
 // fill the pairs once, and several experts' (which have unlike numbers of rows) about twice.
 void cut_wgrad(MmArgs& a, int64_t rows) {
   const int64_t pairs = mm_pairs();
   const auto tiles = [&](int n) { return (int64_t)((a.M + 255) / 256) * ((a.N + n - 1) / n); };
-  a.tile_n = a.E * tiles(256) >= pairs ? 256 : 128, a.split = 0;
-  const int64_t each = tiles(a.tile_n);
+  const int64_t each = tiles(256);
+  a.tile_n = 256, a.split = 0;
   if (a.E * each >= pairs) return;
-  // a tile takes about 0.15 us for 64 rows and product of planes; parts cost a launch and their sum, some 6 us
+  // A tile takes 0.15 to 0.27 us for 64 rows and product of planes, parts a launch and their sum, some 6 us: where
+  // rows are so few that parts would not save that, tiles of half the columns (all SMs busy, those are bound by their
+  // loads and no faster: 16411 x 1000 x 479 in bf16 30 us with them and 4 parts).
   const int terms = a.f32 ? 6 : std::max(a.a.planes, a.b.planes);
-  if (rows * terms < (int64_t)a.E * 64 * 80) return;
+  if (rows * terms < (int64_t)a.E * 64 * 80) {
+    a.tile_n = 128;
+    return;
+  }
   const int64_t parts = a.E == 1 ? pairs / each : 2 * pairs / each;
   const int64_t cut = std::max<int64_t>(256, (rows / parts + 63) / 64 * 64);
   if (cut * a.E < rows) a.split = (int)cut;
@@ -132,7 +137,7 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
     if (dx) wo = operand({p.d_w, p.w_turned ? O : in, p.w_turned ? in : O, p.w_ld, 0, p.w_step, 1, p.experts}, f32, room, packs);
     if (p.d_dw) xo = operand(x, f32, room, packs);
     if (launch && packs.count && (e = launch_expert_packs(packs.list, packs.count, s)) != cudaSuccess) return e;
-    if (launch && gated && (e = launch_expert_gated_bwd(p, d, s)) != cudaSuccess) return e;
+    if (launch && gated && (e = launch_expert_gated_bwd(p, d, packs.count > 0, s)) != cudaSuccess) return e;
   }
   if (dx) {
     a.a = d, a.b = wo;
@@ -147,6 +152,7 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
     a.M = (int)(p.dw_turned ? in : O), a.N = (int)(p.dw_turned ? O : in), a.K = 0;
     a.out = p.d_dw, a.out_ld = p.dw_ld, a.out_step = p.dw_step, a.out_bf16 = p.dw_dtype == EMB_BF16;
     cut_wgrad(a, S);
+    a.beside = dx;
     if (a.split) a.parts = room.take<float>((S / a.split + std::min<int64_t>(p.experts, S)) * a.M * a.N);
     if (launch) return launch_expert_mm_wgrad(a, s);
   }

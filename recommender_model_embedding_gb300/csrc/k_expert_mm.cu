@@ -63,6 +63,7 @@ struct MmParams {
   int stages;
   int chunk;            // blocks of 64 along K between sums in registers
   int split;
+  int beside;           // starts beside the launch before it, and waits for that at its own end
   uint32_t idesc;
   int b_mn;
   void* out;
@@ -286,7 +287,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&amap) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&bmap) : "memory");
   }
-  wait_for_earlier();
+  // (every CTA of the launch before it has passed its own wait: what came before that is done)
+  if (!p.beside) wait_for_earlier();
   if (warp == 0) {
     expert_cuts(p.offsets, p.E, p.S, cuts, lane);
     const int nt = p.nt, mt = p.mt, split = p.split;
@@ -550,6 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   cluster_sync();
   if (warp == kMmWarpMma)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kMmCols) : "memory");
+  if (p.beside) wait_for_earlier();
 }
 
 // Sums the parts of each expert's weight gradient, in order: 1 << shift threads of a row, EPU columns each.
@@ -684,7 +687,7 @@ MmParams params_of(const MmArgs& a) {
   }
   p.out = a.out, p.out_ld = a.out_ld, p.out_step = a.out_step;
   p.gu = a.gu, p.gu_ld = a.gu_ld;
-  p.split = a.split, p.parts = a.parts;
+  p.split = a.split, p.parts = a.parts, p.beside = a.beside;
   return p;
 }
 

@@ -143,9 +143,9 @@ __global__ void __launch_bounds__(kPrepThreads) k_expert_pack(const __grid_const
 template <typename T, int PLANES, int ACT, int EPU>
 __global__ void __launch_bounds__(kPrepThreads)
     k_expert_gated_bwd(const T* dh, int64_t dh_ld, const T* gu, int64_t gu_ld, const int32_t* last, uint32_t S, int f,
-                       int shift, __nv_bfloat16* to, int64_t to_ld, int64_t to_plane) {
+                       int shift, __nv_bfloat16* to, int64_t to_ld, int64_t to_plane, int beside) {
   constexpr bool F32 = PLANES == 3;  // what is to be of fp32's exactness
-  wait_for_earlier();
+  if (!beside) wait_for_earlier();
   let_next_start();
   const uint32_t per = kPrepThreads >> shift;
   const uint32_t most = last ? (uint32_t)min(max(*last, 0), (int)S) : S;
@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       store_piece<PLANES, EPU>(out + f + c * EPU, to_plane, uv);
     }
   }
+  if (beside) wait_for_earlier();
 }
 
 // threads of a row: a power of two, as many as it has pieces, up to a CTA's
@@ -204,7 +205,7 @@ cudaError_t launch_expert_packs(const PackArgs* args, int count, cudaStream_t s)
                      : launch_early(k_expert_pack<__nv_bfloat16, 1>, blocks, kPrepThreads, 0, s, jobs);
 }
 
-cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, cudaStream_t s) {
+cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, bool beside, cudaStream_t s) {
   if (p.rows == 0) return cudaSuccess;
   const int elem = p.dtype == EMB_BF16 ? 2 : 4;
   const bool vec = p.out % 8 == 0 && rows16(p.d_dout, p.dout_ld, elem) && rows16(p.d_gu, p.gu_ld, elem);
@@ -214,7 +215,7 @@ cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, c
     using T = std::remove_pointer_t<decltype(type)>;
     return launch_early(kern, row_grid(p.rows, shift), kPrepThreads, 0, s, static_cast<const T*>(p.d_dout), p.dout_ld,
                         static_cast<const T*>(p.d_gu), p.gu_ld, last, (uint32_t)p.rows, (int)p.out, shift,
-                        const_cast<__nv_bfloat16*>(to.p), to.ld, to.plane_step);
+                        const_cast<__nv_bfloat16*>(to.p), to.ld, to.plane_step, (int)beside);
   };
   const auto by_act = [&](auto act) {
     constexpr int A = decltype(act)::value;
