@@ -42,6 +42,12 @@ __device__ __forceinline__ bool few_tile(const int32_t* offsets, int E, int S, i
 // Tiles of S rows in E experts, at most.
 inline int64_t few_tiles(int64_t S, int E, int most) { return S / most + (E < S ? E : S); }
 
+// Warps that share a tile's contraction: all of a CTA's, or one alone where the tiles are so many that their warps fill
+// the SMs (a CTA of eight warps for each of 8313 tiles with 352 inputs took 83 us, most of it in starting CTAs;
+// two warps a tile 66, one 51).
+constexpr int kFewAlone = 1;
+inline int few_share(int64_t tiles) { return tiles >= (int64_t)device_sms() * 16 ? kFewAlone : kFewWarps; }
+
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"

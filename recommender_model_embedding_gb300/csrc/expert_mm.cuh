@@ -134,6 +134,7 @@ struct MmArgs {
   int E = 1;
   int S = 0;
   int M = 0, N = 0, K = 0;       // rows product: N columns, K; weight gradient: M x N
+  bool turned = false;           // weight gradient: out is N x M
   int act = -1;                  // rows product: gated (N: columns of a half), or -1
   bool f32 = false;
   void* out = nullptr;
@@ -143,7 +144,7 @@ struct MmArgs {
   int64_t gu_ld = 0;
   int tile_n = 256;              // weight gradient: columns of a tile, 256 or 128
   int split = 0;                 // weight gradient: rows of a part (a multiple of 64), 0: no parts
-  float* parts = nullptr;        // [parts][M][N]
+  float* parts = nullptr;        // as out, one after the other
   // launched right after a kernel of the same call, one that lets the next start only when it has passed its own
   // wait, and needs nothing of it: the two run side by side
   bool beside = false;

@@ -61,14 +61,20 @@ MmOperand operand(const Source& m, bool f32, Room& room, Packs& packs) {
   return o;
 }
 
+// What the tiles of an M x N weight gradient take, in fifths of one of 256 x 256 (one of 128 columns: three).
+int64_t tile_cost(int64_t M, int64_t N) {
+  return (M + 255) / 256 * std::min(5 * ((N + 255) / 256), 3 * ((N + 127) / 128));
+}
+
 // Tiles of a weight gradient with M x N outputs: narrower ones, or rows cut into parts, where the
 // experts' tiles alone leave pairs of SMs without work.  A part's rows are such that one dense layer's tiles
 // fill the pairs once, and several experts' (which have unlike numbers of rows) about twice.
 void cut_wgrad(MmArgs& a, int64_t rows) {
   const int64_t pairs = mm_pairs();
   const auto tiles = [&](int n) { return (int64_t)((a.M + 255) / 256) * ((a.N + n - 1) / n); };
-  const int64_t each = tiles(256);
-  a.tile_n = 256, a.split = 0;
+  // (a tile of 128 columns takes about 0.6 of the time of one of 256)
+  a.tile_n = 5 * tiles(256) > 3 * tiles(128) ? 128 : 256, a.split = 0;
+  const int64_t each = tiles(a.tile_n);
   if (a.E * each >= pairs) return;
   // A tile takes 0.15 to 0.27 us for 64 rows and product of planes, parts a launch and their sum, some 6 us: where
   // rows are so few that parts would not save that, tiles of half the columns (all SMs busy, those are bound by their
@@ -86,14 +92,17 @@ void cut_wgrad(MmArgs& a, int64_t rows) {
 // Whether the kernel for few rows is the faster, by what both take (microseconds, weights in MB; measured over 1 to
 // 128 experts, widths 128 to 2048, 1 to 256 rows an expert, both layouts): that kernel reads the weights once for
 // every 32 rows of an expert, at a rate that falls with the rows it multiplies them by (64 experts of 1024 x
-// 512 in bf16: 15 us with 8 rows, 22 with 16, 32 with 32); the tiles' kernel takes longer to get going, and
-// reads them once for 256 rows (16 us for all three), for fp32 after copying them as bf16 planes.
+// 512 in bf16: 15 us with 8 rows, 22 with 16, 32 with 32); the tiles' kernel takes longer to get going and
+// some 3 us for a tile, and reads them once for 256 rows (16 us for all three), for fp32 after copying them as
+// bf16 planes.
 bool few(int64_t rows, int experts, int64_t outs, int64_t in, bool f32) {
   const int64_t each = (rows + experts - 1) / experts, passes = (each + 31) / 32;
   if (each > 128 || few_tiles(rows, experts, 8) > 65535) return false;
-  const double mb = 1e-6 * (double)(experts * outs * in) * (f32 ? 4 : 2);
+  const double mb = 1e-6 * (double)(std::min<int64_t>(experts, rows) * outs * in) * (f32 ? 4 : 2);
   const double rate = f32 ? (each <= 8 ? 0.75 : each <= 16 ? 1.0 : 1.4) : (each <= 8 ? 0.19 : each <= 16 ? 0.30 : 0.43);
-  return 2.5 + (double)passes * mb * rate < (f32 ? 10.5 + 0.9 * mb : 6.0 + 0.15 * mb);
+  const double all = 1e-6 * (double)(experts * outs * in) * (f32 ? 4 : 2);  // (copies go over all experts' weights)
+  const double tiles = (double)((outs + 255) / 256 * std::min<int64_t>(experts, rows)) / (double)mm_pairs();
+  return 2.5 + (double)passes * mb * rate < (f32 ? 10.5 + 0.9 * all : 6.0 + std::max(0.15 * mb, 3.0 * (tiles - 1)));
 }
 
 cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool launch, cudaStream_t s) {
@@ -148,8 +157,11 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
     if (launch && (e = launch_expert_mm_rows(a, s)) != cudaSuccess) return e;
   }
   if (p.d_dw) {
-    a.a = p.dw_turned ? xo : d, a.b = p.dw_turned ? d : xo;
-    a.M = (int)(p.dw_turned ? in : O), a.N = (int)(p.dw_turned ? O : in), a.K = 0;
+    // dw as it lies, or the other way round where that takes less of tiles of 256 x 256 (or 0.6 for 128)
+    const bool first = p.dw_turned ? tile_cost(O, in) < tile_cost(in, O) : tile_cost(O, in) <= tile_cost(in, O);  // O x in
+    a.a = first ? d : xo, a.b = first ? xo : d;
+    a.M = (int)(first ? O : in), a.N = (int)(first ? in : O), a.K = 0;
+    a.turned = first == (p.dw_turned != 0);
     a.out = p.d_dw, a.out_ld = p.dw_ld, a.out_step = p.dw_step, a.out_bf16 = p.dw_dtype == EMB_BF16;
     cut_wgrad(a, S);
     a.beside = dx;

@@ -4,7 +4,7 @@
 // Bound by reading the weights once, and for a single request by the chain of launch, offsets, loads, sum
 // and store.  A tile of the large kernel takes 256 rows through a pipeline that is filled by a few CTAs;
 // here a CTA takes 16 outputs (32 where the weights lie turned) of one expert and up to 8, 16 or 32 of its rows, so that a small call still spreads
-// over the SMs.  Its eight warps share the contraction, 32 (16) of K a step with the loads of several
+// over the SMs.  Its eight warps share the contraction (where tiles are many, each warp takes one of its own), 32 (16) of K a step with the loads of several
 // steps ahead of their use, and add up through shared memory in a fixed order.  The warp's matrix instruction (m16n8k16)
 // takes the weights as A and the rows as B; the order of the contraction is free, so a lane's fragments are
 // the eight elements along K that one load brings, of an output's weights and of a row alike.  Turned
@@ -24,6 +24,7 @@ struct FewParams {
   const void *x, *w;
   int64_t x_ld, w_ld, w_step, half;
   int x_vec, w_vec;
+  int act;
   void *y, *gu;
   int64_t y_ld, gu_ld;
 };
@@ -53,10 +54,20 @@ __device__ __forceinline__ void store_one(T* p, float v) {
   o.store(p);
 }
 
-// ACT: gated, or -1.  NT: eights of rows.
-template <typename T, int ACT, int NT, bool TURNED>
+template <bool FULL>
+__device__ __forceinline__ float act_by(int act, float v) {
+  float none;
+  switch (act) {
+    case EMB_ACT_SILU: return activate<EMB_ACT_SILU, FULL, false>(v, none);
+    case EMB_ACT_GELU: return activate<EMB_ACT_GELU, FULL, false>(v, none);
+    case EMB_ACT_RELU: return activate<EMB_ACT_RELU, FULL, false>(v, none);
+    default: return activate<EMB_ACT_SIGMOID, FULL, false>(v, none);
+  }
+}
+
+// NT: eights of rows.  share: warps that share a tile's contraction.
+template <typename T, bool GATED, int NT, bool TURNED, int share>
 __global__ void __launch_bounds__(kFewThreads, 2) k_expert_few(FewParams p) {
-  constexpr bool GATED = ACT >= 0;
   constexpr int H = GATED ? 2 : 1, PL = kPlanes<T>, RT = 8 * NT;
   constexpr int OUTS = TURNED ? 32 : 16, MT = OUTS / 16;  // outputs of a CTA (of each half), in tiles of 16
   constexpr int STEP = TURNED ? 16 : 32, U = PL == 3 ? (NT * H == 1 ? 2 : 1) : NT == 1 ? (TURNED ? 4 : 2) : NT == 2 ? 2 : 1;
@@ -66,18 +77,19 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_expert_few(FewParams p) {
   let_next_start();
   int e, r0, rows;
   if (!few_tile(p.offsets, p.E, p.S, RT, blockIdx.y, lane, e, r0, rows)) return;
-  const int o0 = blockIdx.x * OUTS, steps = (p.in + STEP - 1) / STEP;
+  constexpr int tiles = kFewWarps / share;  // tiles of outputs of the CTA
+  const int o0 = (blockIdx.x * tiles + warp / share) * OUTS, steps = (p.in + STEP - 1) / STEP, first = warp % share;
   const T* w = static_cast<const T*>(p.w) + e * p.w_step;
   const T* x = static_cast<const T*>(p.x) + (int64_t)r0 * p.x_ld;
   float acc[H][MT][NT][4] = {};
   if constexpr (!TURNED) {
     // the lane's two outputs (held inside the matrix: what lies past its end is not stored)
     const T *wa = w + (int64_t)min(o0 + g, p.out - 1) * p.w_ld, *wb = w + (int64_t)min(o0 + g + 8, p.out - 1) * p.w_ld;
-    for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
+    for (int s0 = first; s0 < steps; s0 += share * U) {
       Raw<T, 8> ra[U][H][2], rx[U][NT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = (s0 + u * kFewWarps) * STEP + t * 8, at = k < p.in ? k : 0;
+        const int k = (s0 + u * share) * STEP + t * 8, at = k < p.in ? k : 0;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           ra[u][h][0].load(wa + h * p.half + at, p.in - k, p.w_vec);
@@ -133,11 +145,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_expert_few(FewParams p) {
   } else {
     // rows of the matrix run along the outputs: the lane's four, o0 + 4 g.., become rows g and g + 8 of two tiles
     const int o = o0 + 4 * g, ov = p.out - o;
-    for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
+    for (int s0 = first; s0 < steps; s0 += share * U) {
       Raw<T, 4> ra[U][H][4], rx[U][NT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = (s0 + u * kFewWarps) * STEP + t * 4;
+        const int k = (s0 + u * share) * STEP + t * 4;
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -209,67 +221,56 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_expert_few(FewParams p) {
         for (int q = 0; q < 4; ++q)
           sums[warp][8 * m + 2 * t + (q & 1)][h * OUTS + (TURNED ? 4 * g + 2 * j + (q >> 1) : g + 8 * (q >> 1))] = acc[h][j][m][q];
   __syncthreads();
-  for (int i = threadIdx.x; i < RT * OUTS; i += kFewThreads) {
-    const int r = i / OUTS, o = i % OUTS;
-    if (r >= rows || o0 + o >= p.out) continue;
+  for (int i = threadIdx.x; i < rows * tiles * OUTS; i += kFewThreads) {
+    const int o = i % OUTS, q = i / OUTS % tiles, r = i / (OUTS * tiles), col = (blockIdx.x * tiles + q) * OUTS + o;
+    if (col >= p.out) continue;
     float v[H] = {};
 #pragma unroll
-    for (int k = 0; k < kFewWarps; ++k)
+    for (int k = 0; k < share; ++k)
 #pragma unroll
-      for (int h = 0; h < H; ++h) v[h] += sums[k][r][h * OUTS + o];
-    T* y = static_cast<T*>(p.y) + (int64_t)(r0 + r) * p.y_ld + o0 + o;
+      for (int h = 0; h < H; ++h) v[h] += sums[q * share + k][r][h * OUTS + o];
+    T* y = static_cast<T*>(p.y) + (int64_t)(r0 + r) * p.y_ld + col;
     if constexpr (GATED) {
       if (p.gu != nullptr) {
-        T* gu = static_cast<T*>(p.gu) + (int64_t)(r0 + r) * p.gu_ld + o0 + o;
+        T* gu = static_cast<T*>(p.gu) + (int64_t)(r0 + r) * p.gu_ld + col;
         store_one(gu, v[0]);
         store_one(gu + p.out, v[1]);
       }
-      float none;
-      store_one(y, activate<ACT, PL == 3, false>(v[0], none) * v[1]);
+      store_one(y, act_by<PL == 3>(p.act, v[0]) * v[1]);
     } else {
       store_one(y, v[0]);
     }
   }
 }
 
-template <typename T, int ACT, int NT>
+template <typename T, bool GATED, int NT>
 cudaError_t run_few(const FewParams& p, bool turned, cudaStream_t s) {
-  const int outs = turned ? 32 : 16;
+  // (a gated block's two halves are the sums and registers of twice the outputs: 32 rows of them in bf16 as the
+  // weights usually lie, else 16)
+  if constexpr (GATED && NT == 4)
+    if (turned || sizeof(T) == 4) return run_few<T, GATED, 2>(p, turned, s);
+  const int outs = turned ? 32 : 16, down = (int)few_tiles(p.S, p.E, 8 * NT), across = (p.out + outs - 1) / outs;
+  const int share = few_share((int64_t)down * across), tiles = kFewWarps / share;
   const auto run = [&](auto kern) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((p.out + outs - 1) / outs), (unsigned)few_tiles(p.S, p.E, 8 * NT));
+    cfg.gridDim = dim3((unsigned)((across + tiles - 1) / tiles), (unsigned)down);
     cfg.blockDim = dim3(kFewThreads), cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
   };
-  // (a gated block's two halves are the sums and registers of twice the outputs: 32 rows of them in bf16 as the
-  // weights usually lie, else 16)
-  if constexpr (ACT >= 0 && NT == 4) {
-    if (turned || sizeof(T) == 4) return run_few<T, ACT, 2>(p, turned, s);
-    if constexpr (sizeof(T) == 2) return run(k_expert_few<T, ACT, NT, false>);
-    return cudaErrorInvalidValue;
-  } else {
-    return turned ? run(k_expert_few<T, ACT, NT, true>) : run(k_expert_few<T, ACT, NT, false>);
-  }
+  if constexpr (!(GATED && NT == 4))
+    if (turned) return share == kFewWarps ? run(k_expert_few<T, GATED, NT, true, kFewWarps>) : run(k_expert_few<T, GATED, NT, true, kFewAlone>);
+  if constexpr (!(GATED && NT == 4 && sizeof(T) == 4))
+    return share == kFewWarps ? run(k_expert_few<T, GATED, NT, false, kFewWarps>) : run(k_expert_few<T, GATED, NT, false, kFewAlone>);
+  return cudaErrorInvalidValue;
 }
 
-template <typename T, int ACT>
+template <typename T, bool GATED>
 cudaError_t few_rows(const FewParams& p, bool turned, cudaStream_t s) {
   const int each = (p.S + p.E - 1) / p.E;  // rows of an expert, on average
-  return each <= 8 ? run_few<T, ACT, 1>(p, turned, s) : each <= 16 ? run_few<T, ACT, 2>(p, turned, s) : run_few<T, ACT, 4>(p, turned, s);
-}
-
-template <typename T>
-cudaError_t few_of(const FewParams& p, int act, bool turned, cudaStream_t s) {
-  switch (act) {
-    case EMB_ACT_SILU: return few_rows<T, EMB_ACT_SILU>(p, turned, s);
-    case EMB_ACT_GELU: return few_rows<T, EMB_ACT_GELU>(p, turned, s);
-    case EMB_ACT_RELU: return few_rows<T, EMB_ACT_RELU>(p, turned, s);
-    case EMB_ACT_SIGMOID: return few_rows<T, EMB_ACT_SIGMOID>(p, turned, s);
-    default: return few_rows<T, -1>(p, turned, s);
-  }
+  return each <= 8 ? run_few<T, GATED, 1>(p, turned, s) : each <= 16 ? run_few<T, GATED, 2>(p, turned, s) : run_few<T, GATED, 4>(p, turned, s);
 }
 
 }  // namespace
@@ -277,11 +278,13 @@ cudaError_t few_of(const FewParams& p, int act, bool turned, cudaStream_t s) {
 cudaError_t launch_expert_few(const FewArgs& a, cudaStream_t s) {
   if (a.S == 0) return cudaSuccess;
   const int elem = a.f32 ? 4 : 2, each = a.turned ? 4 : 8;
-  FewParams p{a.offsets, a.E, a.S, a.in, a.out, a.x, a.w, a.x_ld, a.w_ld, a.w_step, a.half, 0, 0, a.y, a.gu, a.y_ld, a.gu_ld};
+  FewParams p{a.offsets, a.E, a.S, a.in, a.out, a.x, a.w, a.x_ld, a.w_ld, a.w_step, a.half, 0, 0, a.act, a.y, a.gu, a.y_ld, a.gu_ld};
   const int bytes = std::min(16, elem * each);
   p.x_vec = rows_on(a.x, a.x_ld, elem, bytes);
   p.w_vec = rows_on(a.w, a.w_ld, elem, bytes) && a.w_step * elem % bytes == 0 && a.half * elem % bytes == 0;
-  return a.f32 ? few_of<float>(p, a.act, a.turned, s) : few_of<__nv_bfloat16>(p, a.act, a.turned, s);
+  using H = __nv_bfloat16;
+  if (a.act >= 0) return a.f32 ? few_rows<float, true>(p, a.turned, s) : few_rows<H, true>(p, a.turned, s);
+  return a.f32 ? few_rows<float, false>(p, a.turned, s) : few_rows<H, false>(p, a.turned, s);
 }
 
 }  // namespace emb

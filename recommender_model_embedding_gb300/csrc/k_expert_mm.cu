@@ -23,8 +23,10 @@
 // zero in both operands before the tensor core reads them (they may hold anything, NaN too).
 //
 // fp32: each operand is split into three bf16 planes, v = v0 + v1 + v2 (eight significant bits each),
-// and the six products a_i b_j with i + j <= 2 are added, small ones first; what is left
-// out is below 2^-24 of the product.  The tensor core adds in fp32 but does not round to nearest, so an
+// and the six products a_i b_j with i + j <= 2 are added; what is left out is below 2^-24 of the product.
+// The three planes of 64 K lie in the ring side by side, so each is brought once for its six products (with three
+// products, for an fp32 gradient of bf16 weights, such threes hold the copies up: 2.2 ms for 524288 x 2048 x 512 instead of
+// 1.9, so there each product has a stage).  The tensor core adds in fp32 but does not round to nearest, so an
 // error would grow with the length of the sum: fp32 results are therefore summed over parts of K in
 // registers.  bf16 results take the accumulator as it is (its error, below 2^-12 at K = 65536, is inside
 // bf16's rounding).
@@ -40,9 +42,10 @@ namespace emb {
 constexpr int kMmEpi = 16;                         // warps that write tiles out
 constexpr int kMmWarpTma = kMmEpi, kMmWarpMma = kMmEpi + 1, kMmWarpRelay = kMmEpi + 2;
 constexpr int kMmThreads = 32 * (kMmEpi + 3);
-constexpr int kMmMaxStages = 6;
+constexpr int kMmMaxStages = 8;
 constexpr int kMmOperand = 128 * 128;              // bytes of an operand's stage: 128 x 64 bf16
-constexpr int kMmStage = 2 * kMmOperand;
+// bytes of a stage: both operands', B's as wide as the tile
+__host__ __device__ constexpr int mm_stage(int tile_n) { return kMmOperand + tile_n * 64; }
 constexpr int kMmPart = 32 * 64;                   // bytes that a warp writes at once: 32 rows of 64
 // shared memory: the warps' parts, barriers, the tensor memory's address, tables of E + 1 rows and tiles, stages
 constexpr int kMmNumBars = 3 * kMmMaxStages + 4;
@@ -51,18 +54,19 @@ constexpr int kMmOffTmem = kMmOffBars + 8 * kMmNumBars;
 constexpr int kMmOffTables = kMmOffTmem + 16;
 constexpr int kMmMost = 232448;                    // bytes that a CTA can have
 __host__ __device__ constexpr int mm_off_stages(int E) { return (kMmOffTables + 8 * (E + 1) + 1023) / 1024 * 1024; }
-constexpr int mm_smem(int E, int stages) { return mm_off_stages(E) + stages * kMmStage + 1024; }  // (+ to align it)
+constexpr int mm_smem(int E, int stages, int tile_n) { return mm_off_stages(E) + stages * mm_stage(tile_n) + 1024; }  // (+ to align it)
 constexpr int kMmCols = 512;
 
 struct MmParams {
   const int32_t* offsets;
   int E, S, N, K, nt, mt;
   int terms;            // products of planes: 1, 3 or 6
-  uint32_t planes_a, planes_b;  // of each, four bits
+  uint32_t terms_a, terms_b;  // planes of each, four bits
   int tile_n;           // columns of a tile: 256 or 128
   int stages;
   int chunk;            // blocks of 64 along K between sums in registers
   int split;
+  int turned;           // weight gradient: out (and parts) hold rows of M, one for each column
   int beside;           // starts beside the launch before it, and waits for that at its own end
   uint32_t idesc;
   int b_mn;
@@ -172,7 +176,7 @@ struct Walk {
 // A warp's output: parts of 32 rows of 64 bytes (one row a lane: 32 bf16 or 16 fp32 values), staged in
 // its buffer.  Full parts of an output on 16-byte boundaries leave as one TMA copy each, which takes the
 // store out of the warp's hands (and out of the load-store pipe, which the tensor core's operands
-// share); parts at an expert's end or the last columns go row by row.  Chunk c of row r lies at c ^ (r / 2 % 4), the
+// share); parts at an expert's end go row by row, those at the last columns element by element.  Chunk c of row r lies at c ^ (r / 2 % 4), the
 // 64-byte swizzle, so that neither the lanes' writes nor reads collide.
 struct Writer {
   unsigned char* staging;
@@ -205,6 +209,17 @@ struct Writer {
         asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n"
                      "cp.async.bulk.commit_group;" ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(at))
                      : "memory");
+      return;
+    }
+    if (map != nullptr && cols >= kCols) {
+      const int c = lane & 3;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        Pack<T, kEach> p;
+        p.load(reinterpret_cast<const T*>(at + place(r, c)));
+        if (r < rows) p.store(out + (int64_t)r * ld + c * kEach);
+      }
       return;
     }
     const int col = lane % kCols, c = col / kEach, i = col % kEach;
@@ -304,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   let_next_start();
   const uint32_t tmem = *tmem_slot;
   const int tiles = prefix[p.E];
-  const int terms = p.terms, tile_n = p.tile_n;
+  const int terms = p.terms, tile_n = p.tile_n, slots = terms == 1 ? 1 : 3, stage_bytes = mm_stage(tile_n);  // slots: stages of 64 K
   Walk walk{cuts, prefix};
 
   // blocks of 64 along a tile's contraction; WGRAD: and its rows [r0, r1)
@@ -322,7 +337,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     {
       const bool one = elect_one();
       const uint32_t full0 = addr_in(smem_u32(full), 0);  // of the pair's first CTA
-      const uint32_t bytes = kMmOperand + tile_n / 2 * 128;  // that a CTA brings for a stage
       int stage = 0;
       uint32_t phase = 1;
       bool ok = true;
@@ -335,22 +349,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const int n0 = GATED ? n * (tile_n / 2) : n * tile_n + (int)rank * (tile_n / 2);
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
-          for (int t = 0; ok && t < terms; ++t) {
-            const int pa = (p.planes_a >> (4 * t)) & 15, pb = (p.planes_b >> (4 * t)) & 15;
-            for (int kb = c0; kb < c1; ++kb) {
+          for (int kb = c0; ok && kb < c1; ++kb)
+            for (int i = 0; i < slots; ++i) {
               if (!(ok = mbar_wait_bounded(empty + stage, phase))) break;
+              const int pa = terms == 6 ? i : p.terms_a >> (4 * i) & 15, pb = terms == 6 ? i : p.terms_b >> (4 * i) & 15;
               uint32_t bar;
               if (WGRAD && r1 - r0 - kb * 64 < 64) {  // by way of the warp that clears rows
                 bar = smem_u32(landed + stage);
-                if (one) mbar_arrive_expect_tx(landed + stage, bytes);
+                if (one) mbar_arrive_expect_tx(landed + stage, stage_bytes);
               } else {
                 bar = full0 + stage * 8;
                 if (rank == 0 && one) {
-                  mbar_arrive_expect_tx(full + stage, 2 * bytes);
+                  mbar_arrive_expect_tx(full + stage, 2 * stage_bytes);
                   if (WGRAD) mbar_arrive(full + stage);
                 }
               }
-              const uint32_t a = sbase + stage * kMmStage, b = a + kMmOperand;
+              const uint32_t a = sbase + stage * stage_bytes, b = a + kMmOperand;
               if (!one) {
               } else if (WGRAD) {
                 const int k = r0 + kb * 64;
@@ -370,7 +384,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
               }
               if (++stage == stages) stage = 0, phase ^= 1;
             }
-          }
         }
       }
       // the last copies are read before the CTA leaves: every stage handed back
@@ -386,6 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
       const uint64_t desc_a = mm_desc(sbase, WGRAD), desc_b = mm_desc(sbase + kMmOperand, WGRAD || p.b_mn);
       const uint32_t step_a = WGRAD ? 2048 >> 4 : 32 >> 4, step_b = WGRAD || p.b_mn ? 2048 >> 4 : 32 >> 4;
       const uint32_t hi_a = (uint32_t)(desc_a >> 32), hi_b = (uint32_t)(desc_b >> 32), idesc = p.idesc;
+      const uint32_t stages = p.stages, stage_step = stage_bytes >> 4, terms_a = p.terms_a, terms_b = p.terms_b;
       const uint32_t empty0 = smem_u32(empty);
       const bool one = elect_one();
       const int chunk = p.chunk, K = p.K;
@@ -405,26 +419,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           tc_fence_after();
           const uint32_t d = tmem + buf * 256;
           uint32_t accumulate = 0;
-          for (int t = 0; ok && t < terms; ++t)
+          const auto products = [&](int left, uint32_t sa, uint32_t sb) {
+            const uint32_t lo_a = (uint32_t)desc_a + sa * stage_step, lo_b = (uint32_t)desc_b + sb * stage_step;
+            if (one) {
+              mma_pair(d, lo_a, hi_a, lo_b, hi_b, idesc, accumulate);
+              if (left > 48) {
+#pragma unroll
+                for (int k = 1; k < 4; ++k) mma_pair(d, lo_a + k * step_a, hi_a, lo_b + k * step_b, hi_b, idesc, 1);
+              } else {
+                for (int k = 1; k * 16 < left; ++k) mma_pair(d, lo_a + k * step_a, hi_a, lo_b + k * step_b, hi_b, idesc, 1);
+              }
+            }
+            accumulate = 1;
+          };
+          // (rows cleared by the other CTA's threads want an acquire of the cluster's scope; copies do not)
+          const auto come = [&](int left, uint32_t at, uint32_t parity) {
+            return WGRAD && left < 64 ? wait_cluster(full + at, parity) : mbar_wait_bounded(full + at, parity);
+          };
+          const auto done_with_stage = [&] {
+            if (one) commit_pair(empty0 + stage * 8);
+            if (++stage == stages) stage = 0, phase ^= 1;
+          };
+          if (terms != 6) {  // a stage for each product
+            for (int left = part; ok && left > 0; left -= 64)
+              for (int i = 0; i < slots; ++i) {
+                if (!(ok = come(left, stage, phase))) break;
+                tc_fence_after();
+                products(left, stage, stage);
+                done_with_stage();
+              }
+          } else {
             for (int left = part; left > 0; left -= 64) {
-              // (rows cleared by the other CTA's threads want an acquire of the cluster's scope; copies do not)
-              ok = WGRAD && left < 64 ? wait_cluster(full + stage, phase) : mbar_wait_bounded(full + stage, phase);
+              // a stage for each of both operands' planes, and six products of them
+              uint32_t at = stage, parity = phase;
+              for (int i = 0; ok && i < 3; ++i) {
+                ok = come(left, at, parity);
+                if (++at == stages) at = 0, parity ^= 1;
+              }
               if (!ok) break;
               tc_fence_after();
-              const uint32_t lo_a = (uint32_t)desc_a + stage * (kMmStage >> 4), lo_b = (uint32_t)desc_b + stage * (kMmStage >> 4);
-              if (one) {
-                mma_pair(d, lo_a, hi_a, lo_b, hi_b, idesc, accumulate);
-                if (left > 48) {
-#pragma unroll
-                  for (int k = 1; k < 4; ++k) mma_pair(d, lo_a + k * step_a, hi_a, lo_b + k * step_b, hi_b, idesc, 1);
-                } else {
-                  for (int k = 1; k * 16 < left; ++k) mma_pair(d, lo_a + k * step_a, hi_a, lo_b + k * step_b, hi_b, idesc, 1);
-                }
-                commit_pair(empty0 + stage * 8);
+              for (int t = 0; t < terms; ++t) {
+                uint32_t sa = stage + (terms_a >> (4 * t) & 15), sb = stage + (terms_b >> (4 * t) & 15);
+                if (sa >= stages) sa -= stages;
+                if (sb >= stages) sb -= stages;
+                products(left, sa, sb);
               }
-              accumulate = 1;
-              if (++stage == stages) stage = 0, phase ^= 1;
+              for (int i = 0; i < 3; ++i) done_with_stage();
             }
+          }
           if (ok && one) commit_pair(smem_u32(dfull + buf));
           buf ^= 1;
           dphase ^= buf ^ 1;
@@ -443,21 +485,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const int left = r1 - r0 - (blocks - 1) * 64;  // rows of the last block
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
-          for (int t = 0; ok && t < terms; ++t) {
-            stage = (stage + c1 - c0 - 1) % stages;  // the part's last block
-            if (c1 == blocks && left < 64) {
-              if (!(ok = mbar_wait_bounded(landed + stage, phases >> stage & 1))) break;
-              phases ^= 1u << stage;
-              // rows of 128 bytes, one for each K, in boxes of 64: two of A, one or two of B
-              unsigned char* at = smem + mm_off_stages(p.E) + stage * kMmStage;
-              const int boxes = tile_n > 128 ? 4 : 3;
-              for (int i = lane; i < (64 - left) * 32; i += 32)
-                if ((i >> 3 & 3) < boxes)
-                  *reinterpret_cast<uint4*>(at + (i >> 3 & 3) * 8192 + (left + (i >> 5)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async();
-              __syncwarp();
-              if (lane == 0) arrive_cluster(addr_in(smem_u32(full + stage), 0));
-            }
+          const bool clear = c1 == blocks && left < 64;
+          stage = (stage + (c1 - c0 - (clear ? 1 : 0)) * slots) % stages;
+          for (int i = 0; clear && i < slots; ++i) {
+            if (!(ok = mbar_wait_bounded(landed + stage, phases >> stage & 1))) break;
+            phases ^= 1u << stage;
+            // rows of 128 bytes, one for each K, in boxes of 64: two of A, one or two of B
+            unsigned char* at = smem + mm_off_stages(p.E) + stage * stage_bytes;
+            const int boxes = tile_n > 128 ? 4 : 3;
+            for (int q = lane; q < (64 - left) * 32; q += 32)
+              if ((q >> 3 & 3) < boxes)
+                *reinterpret_cast<uint4*>(at + (q >> 3 & 3) * 8192 + (left + (q >> 5)) * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(addr_in(smem_u32(full + stage), 0));
             stage = stage + 1 == stages ? 0 : stage + 1;
           }
         }
@@ -532,6 +573,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) v1[j] *= activate<ACT, SUM, false>(v0[j], none);
         to.write<T>(v1, static_cast<T*>(p.out) + (int64_t)row * p.out_ld + col, p.out_ld, rows, cols, om, col, row, 0);
+      } else if (WGRAD && p.turned) {
+        // lanes are rows, so a column's 32 values are adjacent: stored as they are
+        float* part = p.split ? p.parts + ((int64_t)(tile / (p.mt * p.nt)) * p.N + col) * p.M + row + lane : nullptr;
+        T* out = static_cast<T*>(p.out) + e * p.out_step + (int64_t)col * p.out_ld + row + lane;
+        if (lane < rows)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (i == 0 || has1)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const int c = i * 128 + j;
+                if (c >= cols) continue;
+                const float v[1] = {(i ? v1 : v0)[j]};
+                if (p.split) {
+                  part[(int64_t)c * p.M] = v[0];
+                } else {
+                  Pack<T, 1> o;
+                  o.set(v);
+                  o.store(out + (int64_t)c * p.out_ld);
+                }
+              }
       } else if (WGRAD && p.split) {
         const int z = tile / (p.mt * p.nt);
         float* part = p.parts + ((int64_t)z * p.M + row) * p.N + col;
@@ -555,12 +617,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   if (p.beside) wait_for_earlier();
 }
 
-// Sums the parts of each expert's weight gradient, in order: 1 << shift threads of a row, EPU columns each.
-template <typename T, int EPU>
+// Sums the parts of each expert's weight gradient, in a fixed order: a thread for EPU elements, or where parts are many
+// eight, of which each takes an eighth of them, added up in shared memory.
+template <typename T, int EPU, int SHARES>
 __global__ void __launch_bounds__(256)
-    k_expert_parts(const float* parts, const int32_t* offsets, int E, int S, int split, int M, int N, int shift, T* out,
+    k_expert_parts(const float* parts, const int32_t* offsets, int E, int S, int split, int64_t each, FastDiv pieces, T* out,
                    int64_t ld, int64_t step) {
   __shared__ int32_t cuts[kMaxExperts + 1], prefix[kMaxExperts + 1];
+  constexpr int SLOTS = 256 / SHARES;
+  __shared__ float sums[SHARES][SHARES > 1 ? SLOTS : 1][EPU + 1];
   wait_for_earlier();
   let_next_start();
   if (threadIdx.x < 32) {
@@ -568,25 +633,39 @@ __global__ void __launch_bounds__(256)
     expert_prefix(cuts, E, prefix, threadIdx.x, [=](int rows) { return (rows + split - 1) / split; });
   }
   __syncthreads();
-  const int64_t each = (int64_t)M * N;
-  const int e = blockIdx.y, a = prefix[e], b = prefix[e + 1], per = 256 >> shift;
-  for (int r = blockIdx.x * per + (threadIdx.x >> shift); r < M; r += gridDim.x * per)
-    for (int c = (threadIdx.x & ((1 << shift) - 1)) * EPU; c < N; c += EPU << shift) {
-      const float* from = parts + a * each + (int64_t)r * N + c;
-      float v[EPU] = {};
+  const int e = blockIdx.y, a = prefix[e], n = prefix[e + 1] - a, slot = threadIdx.x % SLOTS, share = threadIdx.x / SLOTS;
+  const int k0 = (int)((int64_t)n * share / SHARES), k1 = (int)((int64_t)n * (share + 1) / SHARES);
+  const uint32_t i = blockIdx.x * SLOTS + slot;  // of the matrix's pieces of EPU elements
+  const bool there = (int64_t)i * EPU < each;
+  float v[EPU] = {};
+  if (there) {
+    const float* from = parts + (a + k0) * each + (int64_t)i * EPU;
 #pragma unroll 4
-      for (int k = a; k < b; ++k, from += each) {
-        Pack<float, EPU> q;
-        float x[EPU];
-        q.load(from);
-        q.get(x);
+    for (int k = k0; k < k1; ++k, from += each) {
+      Pack<float, EPU> q;
+      float x[EPU];
+      q.load(from);
+      q.get(x);
 #pragma unroll
-        for (int i = 0; i < EPU; ++i) v[i] += x[i];
-      }
-      Pack<T, EPU> o;
-      o.set(v);
-      o.store(out + e * step + r * ld + c);
+      for (int j = 0; j < EPU; ++j) v[j] += x[j];
     }
+  }
+  if constexpr (SHARES > 1) {
+#pragma unroll
+    for (int j = 0; j < EPU; ++j) sums[share][slot][j] = v[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < EPU; ++j) {
+      v[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < SHARES; ++k) v[j] += sums[k][slot][j];
+    }
+  }
+  if (share || !there) return;
+  const uint32_t r = pieces.div(i), c = i - r * pieces.d;
+  Pack<T, EPU> o;
+  o.set(v);
+  o.store(out + e * step + (int64_t)r * ld + c * EPU);
 }
 
 // ---- host ----
@@ -658,7 +737,9 @@ cudaError_t launch_mm(const MmArgs& a, MmParams p, int64_t tiles_most, cudaStrea
   CUtensorMap amap, bmap, omap, gmap;
   if (!make_map(&amap, a.a, WGRAD ? 64 : 128) || !make_map(&bmap, a.b, WGRAD || a.b_mn ? 64 : p.tile_n / 2))
     return cudaErrorInvalidValue;
-  if (WGRAD && a.split)
+  if (WGRAD && a.turned)
+    p.out_map = 0;
+  else if (WGRAD && a.split)
     p.out_map = make_out_map(&omap, a.parts, a.M, a.N, a.N, tiles_most / (p.mt * p.nt), (int64_t)a.M * a.N, false);
   else
     p.out_map = make_out_map(&omap, a.out, WGRAD ? a.M : a.S, a.N, a.out_ld, WGRAD ? a.E : 1, a.out_step, a.out_bf16);
@@ -668,8 +749,8 @@ cudaError_t launch_mm(const MmArgs& a, MmParams p, int64_t tiles_most, cudaStrea
   if (!p.gu_map) gmap = amap;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(mm_pairs(), tiles_most));
   p.stages = kMmMaxStages;
-  while (mm_smem(p.E, p.stages) > kMmMost) --p.stages;
-  const int smem = mm_smem(p.E, p.stages);
+  while (mm_smem(p.E, p.stages, p.tile_n) > kMmMost) --p.stages;
+  const int smem = mm_smem(p.E, p.stages, p.tile_n);
   return launch_early(kern, (unsigned)(2 * pairs), kMmThreads, smem, s, amap, bmap, omap, gmap, p);
 }
 
@@ -679,33 +760,38 @@ MmParams params_of(const MmArgs& a) {
   p.terms = 1;
   // products of the operands' planes (a, b), small ones first
   if (a.a.planes > 1 && a.b.planes > 1) {  // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
-    p.terms = 6, p.planes_a = 0x001012, p.planes_b = 0x010210;
+    p.terms = 6, p.terms_a = 0x001012, p.terms_b = 0x010210;
   } else if (a.a.planes > 1) {             // (2,0) (1,0) (0,0)
-    p.terms = 3, p.planes_a = 0x012;
+    p.terms = 3, p.terms_a = 0x012;
   } else if (a.b.planes > 1) {
-    p.terms = 3, p.planes_b = 0x012;
+    p.terms = 3, p.terms_b = 0x012;
   }
   p.out = a.out, p.out_ld = a.out_ld, p.out_step = a.out_step;
   p.gu = a.gu, p.gu_ld = a.gu_ld;
-  p.split = a.split, p.parts = a.parts, p.beside = a.beside;
+  p.split = a.split, p.parts = a.parts, p.beside = a.beside, p.turned = a.turned;
   return p;
 }
 
 }  // namespace
 
-static_assert(mm_smem(kMaxExperts, 5) <= kMmMost && mm_smem(128, kMmMaxStages) <= kMmMost, "shared memory of the products");
+static_assert(mm_smem(kMaxExperts, 5, 256) <= kMmMost && mm_smem(128, 6, 256) <= kMmMost && mm_smem(128, 8, 128) <= kMmMost, "shared memory of the products");
 
 cudaError_t launch_expert_mm_rows(const MmArgs& a, cudaStream_t s) {
   if (a.S == 0) return cudaSuccess;
   MmParams p = params_of(a);
   const bool gated = a.act >= 0;
   const int64_t N = gated ? 2 * (int64_t)a.N : a.N, down = (int64_t)a.S / 256 + std::min(a.E, a.S);
-  p.tile_n = down * ((N + 255) / 256) > mm_pairs() ? 256 : 128;
+  // rows of tiles: at most `down`, and about as many as there are experts, or half a one for each beyond their rows
+  const int64_t about = std::max<int64_t>(std::min(a.E, a.S), (a.S + 255) / 256 + (a.E > 1 ? a.E / 2 : 0));
+  // columns of a tile by the rounds of tiles that the pairs of SMs go through; one of 128 columns takes about 0.6 of
+  // the time of one of 256
+  const auto rounds = [&](int n) { return (about * ((N + n - 1) / n) + mm_pairs() - 1) / mm_pairs(); };
+  p.tile_n = 5 * rounds(256) > 3 * rounds(128) ? 128 : 256;
   p.nt = (int)((N + p.tile_n - 1) / p.tile_n), p.mt = 1;
   if (gated) p.nt = (a.N + p.tile_n / 2 - 1) / (p.tile_n / 2);
   p.b_mn = a.b_mn;
   p.idesc = mm_idesc(false, a.b_mn, p.tile_n);
-  p.chunk = a.f32 ? 4 : 1 << 20;
+  p.chunk = a.f32 ? 2 : 1 << 20;
   const int64_t most = down * p.nt;
   using H = __nv_bfloat16;
   if (a.f32) switch (a.act) {
@@ -729,7 +815,7 @@ cudaError_t launch_expert_mm_wgrad(const MmArgs& a, cudaStream_t s) {
   p.tile_n = a.tile_n;
   p.nt = (a.N + p.tile_n - 1) / p.tile_n, p.mt = (a.M + 255) / 256;
   p.idesc = mm_idesc(true, true, p.tile_n);
-  p.chunk = p.terms == 1 ? 8 : 4;
+  p.chunk = p.terms == 1 ? 8 : p.terms == 3 ? 4 : 2;
   if (a.S > 0) {
     const int64_t parts = a.split ? (int64_t)a.S / a.split + std::min(a.E, a.S) : a.E;
     const cudaError_t e = a.out_bf16 ? launch_mm<true, -1, true, __nv_bfloat16>(a, p, parts * p.mt * p.nt, s)
@@ -738,26 +824,34 @@ cudaError_t launch_expert_mm_wgrad(const MmArgs& a, cudaStream_t s) {
   }
   // (no rows: no parts, and zeros)
   const int split = a.split ? a.split : 64;
-  const int oe = a.out_bf16 ? 2 : 4;
-  const bool vec = a.N % 4 == 0 && rows_on(a.out, a.out_ld, oe, 4 * oe) && a.out_step % 4 == 0;
-  int shift = 0;
-  while (shift < 8 && (1 << shift) < (vec ? a.N / 4 : a.N)) ++shift;
-  const int64_t per = 256 >> shift;
+  const int oe = a.out_bf16 ? 2 : 4, rows = a.turned ? a.N : a.M, cols = a.turned ? a.M : a.N;  // of out
+  const bool vec = cols % 4 == 0 && rows_on(a.out, a.out_ld, oe, 4 * oe) && a.out_step % 4 == 0;
+  // (parts come of matrices of a few dozen tiles, and zeros alone where there are no rows)
+  const bool many = a.split && a.S / a.split >= 16 * a.E;
   const auto sum = [&](auto kern, auto* out) {
+    const int epu = vec ? 4 : 1, slots = many ? 32 : 256;
+    cudaError_t e = cudaSuccess;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>((a.M + per - 1) / per, std::max(1, device_sms() * 16 / a.E)), (unsigned)a.E);
-    cfg.blockDim = dim3(256), cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, (const float*)a.parts, a.offsets, a.E, a.S, split, a.M, a.N, shift, out, a.out_ld, a.out_step);
+    // a launch takes rows with below 2^31 pieces
+    const int64_t most = std::max<int64_t>(1, INT32_MAX / (cols / epu) - 64);
+    for (int64_t r = 0; r < rows && e == cudaSuccess; r += most) {
+      const int64_t here = std::min<int64_t>(most, rows - r);
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)((here * cols / epu + slots - 1) / slots), (unsigned)a.E);
+      cfg.blockDim = dim3(256), cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
+      e = cudaLaunchKernelEx(&cfg, kern, (const float*)a.parts, a.offsets, a.E, a.S, split, here * cols, FastDiv((uint32_t)(cols / epu)),
+                             out + r * a.out_ld, a.out_ld, a.out_step);
+    }
+    return e;
   };
-  if (a.out_bf16) {
-    auto* out = static_cast<__nv_bfloat16*>(a.out);
-    return vec ? sum(k_expert_parts<__nv_bfloat16, 4>, out) : sum(k_expert_parts<__nv_bfloat16, 1>, out);
-  }
-  auto* out = static_cast<float*>(a.out);
-  return vec ? sum(k_expert_parts<float, 4>, out) : sum(k_expert_parts<float, 1>, out);
+  const auto of = [&](auto* out) {
+    using T = std::remove_pointer_t<decltype(out)>;
+    if (many) return vec ? sum(k_expert_parts<T, 4, 8>, out) : sum(k_expert_parts<T, 1, 8>, out);
+    return vec ? sum(k_expert_parts<T, 4, 1>, out) : sum(k_expert_parts<T, 1, 1>, out);
+  };
+  return a.out_bf16 ? of(static_cast<__nv_bfloat16*>(a.out)) : of(static_cast<float*>(a.out));
 }
 
 }  // namespace emb

@@ -103,7 +103,7 @@ struct PackJob {
   const void* src;
   int64_t ld, half_step, expert_step;
   const int32_t* last;
-  FastDiv rows, halves;
+  FastDiv rows{1}, halves{1};
   uint32_t all, first, blocks;
   int inner, shift;
   __nv_bfloat16* to;
@@ -140,6 +140,9 @@ __global__ void __launch_bounds__(kPrepThreads) k_expert_pack(const __grid_const
   }
 }
 
+// EPU columns of each half at a time: eight, or where rows or halves are not on 16-byte boundaries one (neighbouring
+// lanes, neighbouring columns: pieces of eight of the shifted result cost more, 773 against some 390 us for 175347 x 471
+// gelu in bf16, for each column's activation comes twice).
 template <typename T, int PLANES, int ACT, int EPU>
 __global__ void __launch_bounds__(kPrepThreads)
     k_expert_gated_bwd(const T* dh, int64_t dh_ld, const T* gu, int64_t gu_ld, const int32_t* last, uint32_t S, int f,

@@ -45,9 +45,9 @@ __device__ __forceinline__ void x_pairs(const Raw<T, 8>& x, uint32_t (&f)[PLANES
 }
 
 // W words of eight codes, zero from byte `valid` on.
-template <int W, bool VEC>
-__device__ __forceinline__ void load_codes(const uint8_t* q, int valid, uint32_t (&w)[W]) {
-  if (VEC && valid >= 4 * W) {
+template <int W>
+__device__ __forceinline__ void load_codes(const uint8_t* q, int valid, bool vec, uint32_t (&w)[W]) {
+  if (vec && valid >= 4 * W) {
     if constexpr (W == 1) w[0] = *reinterpret_cast<const uint32_t*>(q);
     if constexpr (W == 2) {
       const uint2 v = *reinterpret_cast<const uint2*>(q);
@@ -71,36 +71,38 @@ __device__ __forceinline__ void load_codes(const uint8_t* q, int valid, uint32_t
 }
 
 // W: words (of eight codes) that a lane takes of a step: 1 for groups of 32, 2 of 64, 4 of 128 and more, so
-// that the four lanes of an output stay inside a group.  NT: eights of rows.
-template <typename T, int W, int NT, bool VEC_Q>
+// that the four lanes of an output stay inside a group.  NT: eights of rows.  U: steps loaded ahead.  share: warps
+// that share a tile's contraction.
+template <typename T, int W, int NT, int U, int share>
 __global__ void __launch_bounds__(kFewThreads)
     k_linear4(const T* x, int64_t x_ld, int x_vec, const int32_t* offsets, int E, int S, const uint8_t* q, const float* scale,
-              int in, int out_dim, int per_group, int groups, T* out, int64_t out_ld, int tile0) {
+              int in, int out_dim, int q_vec, int per_group, int groups, T* out, int64_t out_ld, int tile0) {
   constexpr int PLANES = sizeof(T) == 4 ? 3 : 1, RT = 8 * NT, SPAN = 32 * W;  // SPAN: k of a step
-  constexpr int U = W * NT <= 1 && PLANES == 1 ? 4 : W * NT * (PLANES == 3 ? 2 : 1) <= 4 ? 2 : 1;  // steps loaded ahead
   __shared__ float sums[kFewWarps][RT][17];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   wait_for_earlier();
   let_next_start();
   int e, r0, rows;
   if (!few_tile(offsets, E, S, RT, tile0 + (int)blockIdx.y, lane, e, r0, rows)) return;
-  const int row_bytes = (in + 1) / 2, steps = (in + SPAN - 1) / SPAN, o0 = blockIdx.x * 16;
+  const int row_bytes = (in + 1) / 2, steps = (in + SPAN - 1) / SPAN;
+  constexpr int tiles = kFewWarps / share;
+  const int o0 = (blockIdx.x * tiles + warp / share) * 16;
   float acc[NT][4] = {};
   // this lane's two outputs (held inside the matrix: what lies past its end is not stored)
   const int64_t oa = (int64_t)e * out_dim + min(o0 + g, out_dim - 1), ob = (int64_t)e * out_dim + min(o0 + g + 8, out_dim - 1);
   const uint8_t *qa = q + oa * row_bytes, *qb = q + ob * row_bytes;
   const float *sa = scale + oa * groups, *sb = scale + ob * groups;
   x += (int64_t)r0 * x_ld;
-  for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
+  for (int s0 = warp % share; s0 < steps; s0 += share * U) {
     uint32_t wa[U][W], wb[U][W];
     float fa[U], fb[U];
     Raw<T, 8> rx[U][W][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int st = s0 + u * kFewWarps, k0 = st * SPAN + t * (8 * W), b0 = k0 / 2;
+      const int st = s0 + u * share, k0 = st * SPAN + t * (8 * W), b0 = k0 / 2;
       const bool there = k0 < in;
-      load_codes<W, VEC_Q>(qa + (there ? b0 : 0), there ? row_bytes - b0 : 0, wa[u]);
-      load_codes<W, VEC_Q>(qb + (there ? b0 : 0), there ? row_bytes - b0 : 0, wb[u]);
+      load_codes<W>(qa + (there ? b0 : 0), there ? row_bytes - b0 : 0, q_vec, wa[u]);
+      load_codes<W>(qb + (there ? b0 : 0), there ? row_bytes - b0 : 0, q_vec, wb[u]);
       const int gi = per_group == 1 ? st : st / per_group;
       fa[u] = st < steps ? sa[gi] : 0.f, fb[u] = st < steps ? sb[gi] : 0.f;
 #pragma unroll
@@ -141,15 +143,15 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[warp][m * 8 + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[m][i];
   __syncthreads();
-  for (int i = threadIdx.x; i < RT * 16; i += kFewThreads) {
-    const int r = i >> 4, o = i & 15;
+  for (int i = threadIdx.x; i < rows * tiles * 16; i += kFewThreads) {
+    const int o = i & 15, j = (i >> 4) % tiles, r = (i >> 4) / tiles, col = (blockIdx.x * tiles + j) * 16 + o;
     float v[1] = {0.f};
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) v[0] += sums[w][r][o];
-    if (r < rows && o0 + o < out_dim) {
+    for (int w = 0; w < share; ++w) v[0] += sums[j * share + w][r][o];
+    if (col < out_dim) {
       Pack<T, 1> p;
       p.set(v);
-      p.store(out + (int64_t)(r0 + r) * out_ld + o0 + o);
+      p.store(out + (int64_t)(r0 + r) * out_ld + col);
     }
   }
 }
@@ -194,22 +196,29 @@ cudaError_t run_linear4(const emb_product4& a, cudaStream_t s) {
   const int row_bytes = (a.in + 1) / 2, groups = (a.in + a.group - 1) / a.group;
   const bool vec_q = row_bytes % (4 * W) == 0 && reinterpret_cast<uintptr_t>(a.d_q) % (4 * W) == 0;
   const int x_vec = rows16(a.d_x, a.x_ld, sizeof(T));
+  const int64_t across = (a.out + 15) / 16, all = few_tiles(a.rows, a.experts, 8 * NT);
+  const int share = few_share(all * across), wide = kFewWarps / share;
   const auto run = [&](auto kern, int64_t tile0, int64_t tiles) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((a.out + 15) / 16), (unsigned)tiles);
+    cfg.gridDim = dim3((unsigned)((across + wide - 1) / wide), (unsigned)tiles);
     cfg.blockDim = dim3(kFewThreads), cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(a.d_x), a.x_ld, x_vec, a.d_offsets, (int)a.experts, (int)a.rows,
-                              (const uint8_t*)a.d_q, (const float*)a.d_scale, (int)a.in, (int)a.out, (int)a.group / (32 * W), groups,
+                              (const uint8_t*)a.d_q, (const float*)a.d_scale, (int)a.in, (int)a.out, (int)vec_q, (int)a.group / (32 * W), groups,
                               static_cast<T*>(a.d_out), a.out_ld, (int)tile0);
   };
   // (a grid has 65535 rows at most)
-  const int64_t all = few_tiles(a.rows, a.experts, 8 * NT);
+  // steps loaded ahead: two, and where a warp has more of them four in bf16 (with two steps a warp, four take longer for
+  // the masks: 3.6 -> 4.3 us for a single request; in fp32 four leave room for one CTA an SM: 1 x 7616 x 3664 29 -> 46 us)
+  constexpr int PLANES = sizeof(T) == 4 ? 3 : 1, U = W * NT * (PLANES == 3 ? 2 : 1) <= 4 ? 2 : 1, MORE = W * NT <= 2 && PLANES == 1 ? 4 : U;
+  const bool more = (a.in + 32 * W - 1) / (32 * W) > 2 * share;
   for (int64_t at = 0; at < all; at += 65535) {
     const int64_t n = std::min<int64_t>(65535, all - at);
-    const cudaError_t e = vec_q ? run(k_linear4<T, W, NT, true>, at, n) : run(k_linear4<T, W, NT, false>, at, n);
+    const cudaError_t e = share != kFewWarps ? run(k_linear4<T, W, NT, MORE, kFewAlone>, at, n)
+                          : more             ? run(k_linear4<T, W, NT, MORE, kFewWarps>, at, n)
+                                             : run(k_linear4<T, W, NT, U, kFewWarps>, at, n);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
