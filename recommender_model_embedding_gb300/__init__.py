@@ -362,6 +362,24 @@ def gated_norm_backward(dx_out, dh, x_out, y, dx, dy, gate=None, w_post=None, re
                          dres_scale, dw_pre, eps, workspace, stream)
 
 
+def expert_linear_workspace(x, w, out, offsets=None) -> int:
+    """Bytes of workspace of expert_linear on these tensors (or others of their types, shapes, steps
+    and alignment); so the three below, of their calls."""
+    return _tower.linear_workspace(x, w, out, offsets, None, None)
+
+
+def expert_linear_backward_workspace(dout, x, w, dx, dw, offsets=None) -> int:
+    return _tower.linear_backward_workspace(dout, x, w, dx, dw, offsets, None, None)
+
+
+def expert_gated_workspace(x, w, h, gu=None, offsets=None, act: str = "silu") -> int:
+    return _tower.gated_workspace(x, w, h, gu, offsets, act, None, None)
+
+
+def expert_gated_backward_workspace(dh, gu, x, w, dx, dw, offsets=None, act: str = "silu") -> int:
+    return _tower.gated_backward_workspace(dh, gu, x, w, dx, dw, offsets, act, None, None)
+
+
 def expert_linear(x, w, out, offsets=None, workspace=None, stream=None):
     """out[r] = W[e] x[r] for the rows r in [offsets[e], offsets[e + 1]) of each expert e (offsets of
     expert_sort, int32 [experts + 1]; None: one dense layer).  x [S, in] and out [S, out] float32 or

@@ -48,7 +48,7 @@ MmOperand operand(const Source& m, bool f32, Room& room, Packs& packs) {
   MmOperand o;
   if (!f32 && reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && (m.rows <= 1 || (m.ld % 8 == 0 && m.ld >= m.inner)) &&
       (m.halves == 1 || (m.half_step % 8 == 0 && m.half_step > 0)) &&
-      (m.experts == 1 || (m.expert_step % 8 == 0 && m.expert_step > 0))) {
+      (m.experts == 1 || (m.expert_step % 8 == 0 && m.expert_step > 0 && m.expert_step < (int64_t)1 << 38))) {
     o.p = static_cast<const __nv_bfloat16*>(m.p);
     o.inner = m.inner, o.rows = m.rows, o.ld = m.ld, o.half_step = m.half_step, o.expert_step = m.expert_step;
     o.halves = m.halves, o.experts = m.experts;

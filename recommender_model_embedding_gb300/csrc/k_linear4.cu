@@ -12,7 +12,8 @@
 // each with its product, so nothing is lost of them.
 //
 // A CTA takes 16 outputs of one expert and its (up to 8, 16 or 32) rows; its eight warps share the
-// contraction and add up through shared memory in a fixed order.
+// contraction and add up through shared memory in a fixed order.  Where outputs are many, each warp takes 64, 32 or
+// 16 of its own, for which the rows are brought, and in fp32 split, once.
 #include <algorithm>
 
 #include "expert_few.cuh"
@@ -44,67 +45,78 @@ __device__ __forceinline__ void x_pairs(const Raw<T, 8>& x, uint32_t (&f)[PLANES
   }
 }
 
-// W words of eight codes, zero from byte `valid` on.
+// W words of eight codes, zero from byte `valid` on.  From any byte: the two aligned words that hold one, shifted, or
+// byte by byte at the ends of the codes, [lo, hi).
 template <int W>
-__device__ __forceinline__ void load_codes(const uint8_t* q, int valid, bool vec, uint32_t (&w)[W]) {
+__device__ __forceinline__ void load_codes(const uint8_t* q, int valid, bool vec, uintptr_t lo, uintptr_t hi, uint32_t (&w)[W]) {
   if (vec && valid >= 4 * W) {
     if constexpr (W == 1) w[0] = *reinterpret_cast<const uint32_t*>(q);
     if constexpr (W == 2) {
       const uint2 v = *reinterpret_cast<const uint2*>(q);
       w[0] = v.x, w[1] = v.y;
     }
-    if constexpr (W == 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(q);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    }
     return;
   }
 #pragma unroll
-  for (int j = 0; j < W; ++j) w[j] = 0;
-  if (valid <= 0) return;
-#pragma unroll
   for (int j = 0; j < W; ++j) {
+    w[j] = 0;
+    const int left = valid - 4 * j;
+    if (left <= 0) continue;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(q + 4 * j), from = at & ~(uintptr_t)3;
+    const uint32_t s = (uint32_t)(at - from) * 8;
+    if (from >= lo && from + 8 <= hi) {
+      const uint32_t a = *reinterpret_cast<const uint32_t*>(from), b = reinterpret_cast<const uint32_t*>(from)[1];
+      w[j] = __funnelshift_r(a, b, s);
+      if (left < 4) w[j] &= (1u << (8 * left)) - 1;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (4 * j + i < valid) w[j] |= (uint32_t)q[4 * j + i] << (8 * i);
+      for (int i = 0; i < 4; ++i)
+        if (i < left) w[j] |= (uint32_t)q[4 * j + i] << (8 * i);
+    }
   }
 }
 
-// W: words (of eight codes) that a lane takes of a step: 1 for groups of 32, 2 of 64, 4 of 128 and more, so
-// that the four lanes of an output stay inside a group.  NT: eights of rows.  U: steps loaded ahead.  share: warps
-// that share a tile's contraction.
-template <typename T, int W, int NT, int U, int share>
-__global__ void __launch_bounds__(kFewThreads)
+// W: words (of eight codes) that a lane takes of a step: 1, or 2 where groups of 64 and codes on
+// eight-byte boundaries allow it: the four lanes of an output stay inside a group.  NT: eights of rows.  U: steps loaded ahead.  share: warps
+// that share a tile's contraction; MT: tiles of 16 outputs of a warp, for which x is brought and split once.
+template <typename T, int W, int NT, int U, int share, int MT>
+__global__ void __launch_bounds__(kFewThreads, 2)
     k_linear4(const T* x, int64_t x_ld, int x_vec, const int32_t* offsets, int E, int S, const uint8_t* q, const float* scale,
               int in, int out_dim, int q_vec, int per_group, int groups, T* out, int64_t out_ld, int tile0) {
   constexpr int PLANES = sizeof(T) == 4 ? 3 : 1, RT = 8 * NT, SPAN = 32 * W;  // SPAN: k of a step
-  __shared__ float sums[kFewWarps][RT][17];
+  __shared__ float sums[kFewWarps][RT][16 * MT + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   wait_for_earlier();
   let_next_start();
   int e, r0, rows;
   if (!few_tile(offsets, E, S, RT, tile0 + (int)blockIdx.y, lane, e, r0, rows)) return;
   const int row_bytes = (in + 1) / 2, steps = (in + SPAN - 1) / SPAN;
-  constexpr int tiles = kFewWarps / share;
-  const int o0 = (blockIdx.x * tiles + warp / share) * 16;
-  float acc[NT][4] = {};
-  // this lane's two outputs (held inside the matrix: what lies past its end is not stored)
-  const int64_t oa = (int64_t)e * out_dim + min(o0 + g, out_dim - 1), ob = (int64_t)e * out_dim + min(o0 + g + 8, out_dim - 1);
-  const uint8_t *qa = q + oa * row_bytes, *qb = q + ob * row_bytes;
-  const float *sa = scale + oa * groups, *sb = scale + ob * groups;
+  constexpr int tiles = kFewWarps / share, OUTS = 16 * MT;
+  const int o0 = (blockIdx.x * tiles + warp / share) * OUTS;
+  float acc[MT][NT][4] = {};
+  // this lane's two outputs of each tile (held inside the matrix: what lies past its end is not stored)
+  uint32_t oa[MT], ob[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) oa[i] = min(o0 + 16 * i + g, out_dim - 1), ob[i] = min(o0 + 16 * i + g + 8, out_dim - 1);
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(q), hi = lo + (int64_t)E * out_dim * row_bytes;
+  q += (int64_t)e * out_dim * row_bytes, scale += (int64_t)e * out_dim * groups;
   x += (int64_t)r0 * x_ld;
   for (int s0 = warp % share; s0 < steps; s0 += share * U) {
-    uint32_t wa[U][W], wb[U][W];
-    float fa[U], fb[U];
+    uint32_t wa[U][MT][W], wb[U][MT][W];
+    float fa[U][MT], fb[U][MT];
     Raw<T, 8> rx[U][W][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int st = s0 + u * share, k0 = st * SPAN + t * (8 * W), b0 = k0 / 2;
       const bool there = k0 < in;
-      load_codes<W>(qa + (there ? b0 : 0), there ? row_bytes - b0 : 0, q_vec, wa[u]);
-      load_codes<W>(qb + (there ? b0 : 0), there ? row_bytes - b0 : 0, q_vec, wb[u]);
       const int gi = per_group == 1 ? st : st / per_group;
-      fa[u] = st < steps ? sa[gi] : 0.f, fb[u] = st < steps ? sb[gi] : 0.f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        load_codes<W>(q + (int64_t)oa[i] * row_bytes + (there ? b0 : 0), there ? row_bytes - b0 : 0, q_vec, lo, hi, wa[u][i]);
+        load_codes<W>(q + (int64_t)ob[i] * row_bytes + (there ? b0 : 0), there ? row_bytes - b0 : 0, q_vec, lo, hi, wb[u][i]);
+        fa[u][i] = st < steps ? scale[(int64_t)oa[i] * groups + gi] : 0.f;
+        fb[u][i] = st < steps ? scale[(int64_t)ob[i] * groups + gi] : 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < W; ++j)
 #pragma unroll
@@ -115,36 +127,42 @@ __global__ void __launch_bounds__(kFewThreads)
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float part[NT][4] = {};
+      uint32_t f[W][NT][PLANES][4];
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        uint32_t f[NT][PLANES][4];
+      for (int j = 0; j < W; ++j)
 #pragma unroll
-        for (int m = 0; m < NT; ++m) x_pairs<T, PLANES>(rx[u][j][m], f[m]);
+        for (int m = 0; m < NT; ++m) x_pairs<T, PLANES>(rx[u][j][m], f[j][m]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a[4] = {codes_at(wa[u][j], 2 * h), codes_at(wb[u][j], 2 * h), codes_at(wa[u][j], 2 * h + 1),
-                                 codes_at(wb[u][j], 2 * h + 1)};
+      for (int i = 0; i < MT; ++i) {
+        float part[NT][4] = {};
 #pragma unroll
-          for (int m = 0; m < NT; ++m)
+        for (int j = 0; j < W; ++j)
 #pragma unroll
-            for (int pl = PLANES - 1; pl >= 0; --pl) mma16816(part[m], a, f[m][pl][2 * h], f[m][pl][2 * h + 1]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {codes_at(wa[u][i][j], 2 * h), codes_at(wb[u][i][j], 2 * h), codes_at(wa[u][i][j], 2 * h + 1),
+                                   codes_at(wb[u][i][j], 2 * h + 1)};
+#pragma unroll
+            for (int m = 0; m < NT; ++m)
+#pragma unroll
+              for (int pl = PLANES - 1; pl >= 0; --pl) mma16816(part[m], a, f[j][m][pl][2 * h], f[j][m][pl][2 * h + 1]);
+          }
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          acc[i][m][0] = fmaf(fa[u][i], part[m][0], acc[i][m][0]), acc[i][m][1] = fmaf(fa[u][i], part[m][1], acc[i][m][1]);
+          acc[i][m][2] = fmaf(fb[u][i], part[m][2], acc[i][m][2]), acc[i][m][3] = fmaf(fb[u][i], part[m][3], acc[i][m][3]);
         }
-      }
-#pragma unroll
-      for (int m = 0; m < NT; ++m) {
-        acc[m][0] = fmaf(fa[u], part[m][0], acc[m][0]), acc[m][1] = fmaf(fa[u], part[m][1], acc[m][1]);
-        acc[m][2] = fmaf(fb[u], part[m][2], acc[m][2]), acc[m][3] = fmaf(fb[u], part[m][3], acc[m][3]);
       }
     }
   }
 #pragma unroll
-  for (int m = 0; m < NT; ++m)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sums[warp][m * 8 + 2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[m][i];
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sums[warp][m * 8 + 2 * t + (k & 1)][16 * i + g + 8 * (k >> 1)] = acc[i][m][k];
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * tiles * 16; i += kFewThreads) {
-    const int o = i & 15, j = (i >> 4) % tiles, r = (i >> 4) / tiles, col = (blockIdx.x * tiles + j) * 16 + o;
+  for (int i = threadIdx.x; i < rows * tiles * OUTS; i += kFewThreads) {
+    const int o = i % OUTS, j = i / OUTS % tiles, r = i / (OUTS * tiles), col = (blockIdx.x * tiles + j) * OUTS + o;
     float v[1] = {0.f};
 #pragma unroll
     for (int w = 0; w < share; ++w) v[0] += sums[j * share + w][r][o];
@@ -192,12 +210,18 @@ __global__ void __launch_bounds__(256)
 }
 
 template <typename T, int W, int NT>
-cudaError_t run_linear4(const emb_product4& a, cudaStream_t s) {
-  const int row_bytes = (a.in + 1) / 2, groups = (a.in + a.group - 1) / a.group;
-  const bool vec_q = row_bytes % (4 * W) == 0 && reinterpret_cast<uintptr_t>(a.d_q) % (4 * W) == 0;
-  const int x_vec = rows16(a.d_x, a.x_ld, sizeof(T));
+cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
+  constexpr bool F32 = sizeof(T) == 4;
+  // Warps of their own for 64 outputs (fp32 with 32 rows: 32) where these fill the SMs, else eight warps for 16.
+  constexpr int MT = F32 && NT == 4 ? 2 : 4;
+  // Steps loaded ahead.  Shared tiles: two, and where a warp has more of them four in bf16 (with two steps a warp, four
+  // take longer for the masks: 3.6 -> 4.3 us for a single request; in fp32 they leave room for one CTA an SM: 1 x
+  // 7616 x 3664 29 -> 46 us).  Alone: what registers for two CTAs an SM hold.
+  constexpr int U = NT == 4 ? 1 : 2, MORE = F32 || NT > 1 ? U : 4, ALONE = !F32 && W == 1 && NT <= 2 ? 2 : 1;
+  const int groups = (a.in + a.group - 1) / a.group, x_vec = rows16(a.d_x, a.x_ld, sizeof(T));
   const int64_t across = (a.out + 15) / 16, all = few_tiles(a.rows, a.experts, 8 * NT);
-  const int share = few_share(all * across), wide = kFewWarps / share;
+  const bool alone = all * across >= (int64_t)device_sms() * 8 * MT, more = (a.in + 32 * W - 1) / (32 * W) > 2 * kFewWarps;
+  const int wide = alone ? kFewWarps * MT : 1;  // tiles of a CTA
   const auto run = [&](auto kern, int64_t tile0, int64_t tiles) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -206,33 +230,28 @@ cudaError_t run_linear4(const emb_product4& a, cudaStream_t s) {
     cfg.gridDim = dim3((unsigned)((across + wide - 1) / wide), (unsigned)tiles);
     cfg.blockDim = dim3(kFewThreads), cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(a.d_x), a.x_ld, x_vec, a.d_offsets, (int)a.experts, (int)a.rows,
-                              (const uint8_t*)a.d_q, (const float*)a.d_scale, (int)a.in, (int)a.out, (int)vec_q, (int)a.group / (32 * W), groups,
+                              (const uint8_t*)a.d_q, (const float*)a.d_scale, (int)a.in, (int)a.out, (int)q_vec, (int)a.group / (32 * W), groups,
                               static_cast<T*>(a.d_out), a.out_ld, (int)tile0);
   };
   // (a grid has 65535 rows at most)
-  // steps loaded ahead: two, and where a warp has more of them four in bf16 (with two steps a warp, four take longer for
-  // the masks: 3.6 -> 4.3 us for a single request; in fp32 four leave room for one CTA an SM: 1 x 7616 x 3664 29 -> 46 us)
-  constexpr int PLANES = sizeof(T) == 4 ? 3 : 1, U = W * NT * (PLANES == 3 ? 2 : 1) <= 4 ? 2 : 1, MORE = W * NT <= 2 && PLANES == 1 ? 4 : U;
-  const bool more = (a.in + 32 * W - 1) / (32 * W) > 2 * share;
   for (int64_t at = 0; at < all; at += 65535) {
     const int64_t n = std::min<int64_t>(65535, all - at);
-    const cudaError_t e = share != kFewWarps ? run(k_linear4<T, W, NT, MORE, kFewAlone>, at, n)
-                          : more             ? run(k_linear4<T, W, NT, MORE, kFewWarps>, at, n)
-                                             : run(k_linear4<T, W, NT, U, kFewWarps>, at, n);
+    const cudaError_t e = alone  ? run(k_linear4<T, W, NT, ALONE, 1, MT>, at, n)
+                          : more ? run(k_linear4<T, W, NT, MORE, kFewWarps, 1>, at, n)
+                                 : run(k_linear4<T, W, NT, U, kFewWarps, 1>, at, n);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-template <typename T, int W>
-cudaError_t linear4_rows(const emb_product4& a, cudaStream_t s) {
-  const int64_t each = (a.rows + a.experts - 1) / a.experts;  // rows of an expert, on average
-  return each <= 8 ? run_linear4<T, W, 1>(a, s) : each <= 16 ? run_linear4<T, W, 2>(a, s) : run_linear4<T, W, 4>(a, s);
-}
-
 template <typename T>
 cudaError_t linear4_of(const emb_product4& a, cudaStream_t s) {
-  return a.group % 128 == 0 ? linear4_rows<T, 4>(a, s) : a.group % 64 == 0 ? linear4_rows<T, 2>(a, s) : linear4_rows<T, 1>(a, s);
+  const int64_t each = (a.rows + a.experts - 1) / a.experts;  // rows of an expert, on average
+  const uint64_t on = reinterpret_cast<uintptr_t>(a.d_q) | (uint64_t)((a.in + 1) / 2);
+  if (each > 8) return each <= 16 ? run_linear4<T, 1, 2>(a, on % 4 == 0, s) : run_linear4<T, 1, 4>(a, on % 4 == 0, s);
+  if constexpr (sizeof(T) == 2)
+    if (a.group % 64 == 0 && on % 8 == 0) return run_linear4<T, 2, 1>(a, true, s);
+  return run_linear4<T, 1, 1>(a, on % 4 == 0, s);
 }
 
 }  // namespace

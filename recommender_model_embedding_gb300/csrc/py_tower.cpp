@@ -604,8 +604,11 @@ struct ProductCall {
   }
   using Need = int64_t (*)(const emb_product*);
   using Run = emb_status (*)(const emb_product*, void*, int64_t, void*);
+  // the call, or how many bytes of workspace it takes
+  template <bool SIZE>
   PyObject* run(const char* name, Need need, Run f, PyObject* workspace, PyObject* stream, std::initializer_list<PyObject*> outs) {
     dev.enter();
+    if (SIZE) return PyLong_FromLongLong(need(&p));
     Workspace ws(need(&p), workspace, dev);
     void* s = stream_of(stream, dev);
     ws.take(s);
@@ -614,36 +617,40 @@ struct ProductCall {
 };
 
 // (x, w, out, offsets, workspace, stream)
+template <bool SIZE>
 PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 6, [&]() -> PyObject* {
     ProductCall c(a[0], a[1], a[3], 1);
     const Rows o = rows(a[2], c.kind, c.n, c.f, "out", c.dev);
     c.p.d_out = o.p, c.p.out_ld = o.ld;
-    return c.run("emb_expert_linear", emb_expert_linear_workspace, emb_expert_linear, a[4], a[5], {a[2]});
+    return c.run<SIZE>("emb_expert_linear", emb_expert_linear_workspace, emb_expert_linear, a[4], a[5], {a[2]});
   });
 }
 
 // (dout, x, w, dx, dw, offsets, workspace, stream)
+template <bool SIZE>
 PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 8, [&]() -> PyObject* {
     ProductCall c(a[1], a[2], a[5], 1);
     c.gradients(a[0], a[3], a[4], "dout", 1);
-    return c.run("emb_expert_linear_backward", emb_expert_linear_backward_workspace, emb_expert_linear_backward, a[6], a[7], {a[3], a[4]});
+    return c.run<SIZE>("emb_expert_linear_backward", emb_expert_linear_backward_workspace, emb_expert_linear_backward, a[6], a[7], {a[3], a[4]});
   });
 }
 
 // (x, w, h, gu, offsets, act, workspace, stream)
+template <bool SIZE>
 PyObject* py_gated(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 8, [&]() -> PyObject* {
     ProductCall c(a[0], a[1], a[4], 2);
     const Rows h = rows(a[2], c.kind, c.n, c.f, "h", c.dev), gu = opt_rows(a[3], c.kind, c.n, 2 * c.f, "gu", c.dev);
     c.p.d_out = h.p, c.p.out_ld = h.ld, c.p.d_gu = gu.p, c.p.gu_ld = gu.ld;
     c.p.act = act_of(a[5]);
-    return c.run("emb_expert_gated", emb_expert_gated_workspace, emb_expert_gated, a[6], a[7], {a[2], a[3]});
+    return c.run<SIZE>("emb_expert_gated", emb_expert_gated_workspace, emb_expert_gated, a[6], a[7], {a[2], a[3]});
   });
 }
 
 // (dh, gu, x, w, dx, dw, offsets, act, workspace, stream)
+template <bool SIZE>
 PyObject* py_gated_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guard(na, 10, [&]() -> PyObject* {
     ProductCall c(a[2], a[3], a[6], 2);
@@ -651,7 +658,7 @@ PyObject* py_gated_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const Rows gu = rows(a[1], c.kind, c.n, 2 * c.f, "gu", c.dev);
     c.p.d_gu = gu.p, c.p.gu_ld = gu.ld;
     c.p.act = act_of(a[7]);
-    return c.run("emb_expert_gated_backward", emb_expert_gated_backward_workspace, emb_expert_gated_backward, a[8], a[9], {a[4], a[5]});
+    return c.run<SIZE>("emb_expert_gated_backward", emb_expert_gated_backward_workspace, emb_expert_gated_backward, a[8], a[9], {a[4], a[5]});
   });
 }
 
@@ -753,10 +760,14 @@ PyMethodDef methods[] = {{"sort", fast(py_sort), METH_FASTCALL, nullptr},
                          {"norm", fast(py_norm), METH_FASTCALL, nullptr},
                          {"norm_backward", fast(py_norm_backward), METH_FASTCALL, nullptr},
                          {"clip", fast(py_clip), METH_FASTCALL, nullptr},
-                         {"linear", fast(py_linear), METH_FASTCALL, nullptr},
-                         {"linear_backward", fast(py_linear_backward), METH_FASTCALL, nullptr},
-                         {"gated", fast(py_gated), METH_FASTCALL, nullptr},
-                         {"gated_backward", fast(py_gated_backward), METH_FASTCALL, nullptr},
+                         {"linear", fast(py_linear<false>), METH_FASTCALL, nullptr},
+                         {"linear_workspace", fast(py_linear<true>), METH_FASTCALL, nullptr},
+                         {"linear_backward", fast(py_linear_backward<false>), METH_FASTCALL, nullptr},
+                         {"linear_backward_workspace", fast(py_linear_backward<true>), METH_FASTCALL, nullptr},
+                         {"gated", fast(py_gated<false>), METH_FASTCALL, nullptr},
+                         {"gated_workspace", fast(py_gated<true>), METH_FASTCALL, nullptr},
+                         {"gated_backward", fast(py_gated_backward<false>), METH_FASTCALL, nullptr},
+                         {"gated_backward_workspace", fast(py_gated_backward<true>), METH_FASTCALL, nullptr},
                          {"linear4", fast(py_linear4), METH_FASTCALL, nullptr},
                          {"quantize4", fast(py_quantize4), METH_FASTCALL, nullptr},
                          {"dropout", fast(py_dropout), METH_FASTCALL, nullptr},

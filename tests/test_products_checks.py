@@ -68,6 +68,20 @@ def test_products_refuse_workspaces(E):
     assert getattr(L, "emb_expert_linear")(None, None, 0, None) == E.EMB_EINVAL
 
 
+def test_workspace_sizes_from_tensors(E):
+    """The package's sizes are the library's for the same call."""
+    x, w, o, off = FakeCuda(F, 600, 16), FakeCuda(F, 2, 8, 16), FakeCuda(F, 600, 8), FakeCuda("int32", 3)
+    p = _product(E, rows=600, w_step=128, dw_step=128)
+    L = E._lib
+    assert E.expert_linear_workspace(x, w, o, offsets=off) == L.emb_expert_linear_workspace(ctypes.byref(p)) > 0
+    assert (E.expert_linear_backward_workspace(o, x, w, x, FakeCuda(F, 2, 8, 16), offsets=off)
+            == L.emb_expert_linear_backward_workspace(ctypes.byref(p)) > 0)
+    h, p.out, p.out_ld, p.dout_ld, p.gu_ld = FakeCuda(F, 600, 4), 4, 4, 4, 8
+    assert E.expert_gated_workspace(x, w, h, gu=o, offsets=off) == L.emb_expert_gated_workspace(ctypes.byref(p)) > 0
+    assert (E.expert_gated_backward_workspace(h, o, x, w, x, FakeCuda(F, 2, 8, 16), offsets=off)
+            == L.emb_expert_gated_backward_workspace(ctypes.byref(p)) > 0)
+
+
 def test_linear4_and_packing_refuse(E):
     L = E._lib
     ok = dict(rows=4, experts=2, in_=64, out=8, dtype=0, group=32, d_offsets=P, d_x=P, x_ld=64, d_q=P, d_scale=P, d_out=P, out_ld=8)

@@ -114,6 +114,8 @@ SHAPES = [
     ([31], 0, 1030, 130, "io", 0, 0),
     ([31], 0, 1030, 130, "oi", 0, 0),
     ([1, 0, 2] * 15, 4, 256, 72, "oi", 0, 0),
+    ([9000, 11003], 5, 136, 640, "oi", 0, 0),
+    ([7000, 13003], 5, 640, 136, "io", 8, 0),
 ]
 IDS = [f"{len(s[0])}x{sum(s[0])}+{s[1]}-{s[2]}-{s[3]}-{s[4]}" for s in SHAPES]
 
@@ -232,6 +234,90 @@ def test_gated_backward(E, shape, dtype, act):
     y, m = by_rows(dgu, x, counts)
     mr = by_rows(rough, x, counts)[1]
     assert ((dw.double() - y).abs() <= bound(y, m, mr, max(counts), F32)).all()
+
+
+@pytest.mark.parametrize("order", ["oi", "io"])
+def test_gated_backward_in_parts(E, order):
+    """Gradients in the weights' own type, rounded once more (of [dg, du] rounded to bf16: 2^-8 of each
+    product), and dx and dw each alone."""
+    g, counts = gen(12), [40, 0, 130]
+    off, f, i = offsets_of(counts), 36, 50
+    x, dh, gu = rows(170, i, BF16, g), rows(170, f, BF16, g), rows(170, 2 * f, BF16, g)
+    w = weights(3, 2 * f, i, BF16, g, order)
+    a, slope = act64("silu", gu[:, :f].double())
+    dgu = torch.cat([dh.double() * gu[:, f:].double() * slope, dh.double() * a], 1)
+    y, m = by_rows(dgu, x, counts)
+    dw = torch.empty_like(w).fill_(float("nan"))
+    dx = torch.empty_like(x)
+    E.expert_gated_backward(dh, gu, x, w, dx, dw, offsets=off)
+    assert ((dw.double() - y).abs() <= 2.0 ** -8 * y.abs() + (2.0 ** -8 + 2.0 ** -15) * m + 1e-30).all()
+    dx2, dw2 = torch.empty_like(dx), torch.empty_like(dw)
+    E.expert_gated_backward(dh, gu, x, w, dx2, None, offsets=off)
+    E.expert_gated_backward(dh, gu, x, w, None, dw2, offsets=off)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=NAMES.get)
+def test_most_experts(E, dtype):
+    """1024 experts of no, one and a few rows, in both directions."""
+    g = gen(13)
+    counts = [(7 * i) % 5 for i in range(1024)]
+    n, off = sum(counts), offsets_of(counts)
+    x, dout, w = rows(n, 40, dtype, g), rows(n, 24, dtype, g), weights(1024, 24, 40, dtype, g)
+    out, dx, dw = torch.empty_like(dout), torch.empty_like(x), torch.empty((1024, 24, 40), device="cuda")
+    E.expert_linear(x, w, out, offsets=off)
+    E.expert_linear_backward(dout, x, w, dx, dw, offsets=off)
+    y, m = by_expert(x, w, counts)
+    close(out, y, m, 40, split=dtype == F32)
+    y, m = by_expert(dout, w.transpose(1, 2), counts)
+    close(dx, y, m, 24, split=dtype == F32)
+    y, m = by_rows(dout, x, counts)
+    close(dw, y, m, 4, split=dtype == F32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=NAMES.get)
+def test_calls_in_a_row_and_on_two_streams(E, dtype):
+    """Calls that follow one another on one workspace, each kernel started early, and calls on two streams
+    at once: the bits of calls by themselves."""
+    g, counts = gen(14), [300, 0, 211, 77]
+    off, f, i = offsets_of(counts), 48, 72
+    sets = []
+    for _ in range(3):
+        x, dh, w = rows(588, i, dtype, g), rows(588, f, dtype, g), weights(4, 2 * f, i, dtype, g)
+        room = [torch.zeros(s, device="cuda", dtype=t) for s, t in (((588, f), dtype), ((588, 2 * f), dtype), ((588, i), dtype), ((4, 2 * f, i), F32))]
+        sets.append((x, dh, w, *room))
+
+    def run(s, ws):
+        x, dh, w, h, gu, dx, dw = s
+        E.expert_gated(x, w, h, gu=gu, offsets=off, workspace=ws)
+        E.expert_gated_backward(dh, gu, x, w, dx, dw, offsets=off, workspace=ws)
+
+    alone = []
+    for s in sets:
+        run(s, None)
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in s[3:]])
+        for t in s[3:]:
+            t.zero_()
+    need = E.expert_gated_backward_workspace(sets[0][1], sets[0][4], sets[0][0], sets[0][2], sets[0][5], sets[0][6], offsets=off)
+    spaces = [torch.empty(max(need, 1 << 20), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s in sets:
+            run(s, spaces[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for s, w in zip(sets, alone) for a, b in zip(s[3:], w))
+    for s in sets:
+        for t in s[3:]:
+            t.zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for k, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                run(sets[k], spaces[k])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for k in range(2) for a, b in zip(sets[k][3:], alone[k]))
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=NAMES.get)
