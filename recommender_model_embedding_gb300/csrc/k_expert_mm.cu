@@ -28,7 +28,7 @@
 // products, for an fp32 gradient of bf16 weights, such threes hold the copies up: 2.2 ms for 524288 x 2048 x 512 instead of
 // 1.9, so there each product has a stage).  The tensor core adds in fp32 but does not round to nearest, so an
 // error would grow with the length of the sum: fp32 results are therefore summed over parts of K in
-// registers (8192 rows of bf16: 9.1e-6 off in the 2-norm in one sum, 4.8e-7 in parts of 512).  bf16 results take the accumulator as it is (its error, below 2^-12 at K = 65536, is inside
+// registers, and in a part the small products come first (8192 rows of bf16: 9.1e-6 off in the 2-norm in one sum, 4.8e-7 in parts of 512).  bf16 results take the accumulator as it is (its error, below 2^-12 at K = 65536, is inside
 // bf16's rounding).
 //
 // Measured on bf16 rows of 64 experts: 524288 x 512 through 512 -> 2048 outputs gated, h alone 0.60 ms (1.8 PFLOP/s,
@@ -354,8 +354,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const int n0 = GATED ? n * (tile_n / 2) : n * tile_n + (int)rank * (tile_n / 2);
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
-          for (int kb = c0; ok && kb < c1; ++kb)
-            for (int i = 0; i < slots; ++i) {
+          for (int i = 0; ok && i < slots; ++i)
+            for (int kb = c0; kb < c1; ++kb) {
               if (!(ok = mbar_wait_bounded(empty + stage, phase))) break;
               const int pa = terms == 6 ? i : p.terms_a >> (4 * i) & 15, pb = terms == 6 ? i : p.terms_b >> (4 * i) & 15;
               uint32_t bar;
@@ -418,9 +418,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           k_blocks(walk.local(tile), r0, r1);
           length = r1 - r0;
         }
+        bool ready = false;  // what the next part waits for has been seen
         for (int done = 0; ok && done < length; done += chunk * 64) {
           const int part = min(length - done, chunk * 64);
-          if (!(ok = mbar_wait_bounded(dempty + buf, dphase))) break;
+          if (!ready && !(ok = mbar_wait_bounded(dempty + buf, dphase))) break;
           tc_fence_after();
           const uint32_t d = tmem + buf * 256;
           uint32_t accumulate = 0;
@@ -446,31 +447,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
             if (++stage == stages) stage = 0, phase ^= 1;
           };
           if (terms != 6) {  // a stage for each product
-            for (int left = part; ok && left > 0; left -= 64)
-              for (int i = 0; i < slots; ++i) {
+            for (int i = 0; ok && i < slots; ++i)
+              for (int left = part; left > 0; left -= 64) {
                 if (!(ok = come(left, stage, phase))) break;
                 tc_fence_after();
                 products(left, stage, stage);
                 done_with_stage();
               }
           } else {
-            for (int left = part; left > 0; left -= 64) {
-              // a stage for each of both operands' planes, and six products of them
-              uint32_t at = stage, parity = phase;
-              for (int i = 0; ok && i < 3; ++i) {
-                ok = come(left, at, parity);
+            // parts of 64 K: a stage for each of both operands' planes, and six products of them
+            const auto three = [&](int left, uint32_t at, uint32_t parity) {
+              bool all = true;
+              for (int i = 0; all && i < 3; ++i) {
+                all = come(left, at, parity);
                 if (++at == stages) at = 0, parity ^= 1;
               }
-              if (!ok) break;
-              tc_fence_after();
-              for (int t = 0; t < terms; ++t) {
-                uint32_t sa = stage + (terms_a >> (4 * t) & 15), sb = stage + (terms_b >> (4 * t) & 15);
-                if (sa >= stages) sa -= stages;
-                if (sb >= stages) sb -= stages;
-                products(left, sa, sb);
+              return all;
+            };
+            if (!ready && !(ok = three(part, stage, phase))) break;
+            tc_fence_after();
+            ready = false;
+            for (int t = 0; ok && t < terms; ++t) {
+              uint32_t sa = stage + (terms_a >> (4 * t) & 15), sb = stage + (terms_b >> (4 * t) & 15);
+              if (sa >= stages) sa -= stages;
+              if (sb >= stages) sb -= stages;
+              if (t == terms - 1 && done + 64 < length && stages >= 6) {
+                // the next part's copies and accumulator, waited for while the tensor core still has work (its stages
+                // are others than this part's)
+                uint32_t next = stage + 3, parity = phase;
+                if (next >= stages) next -= stages, parity ^= 1;
+                ok = ready = mbar_wait_bounded(dempty + (buf ^ 1), dphase ^ (buf == 1)) && three(length - done - 64, next, parity);
               }
-              for (int i = 0; i < 3; ++i) done_with_stage();
+              products(part, sa, sb);
             }
+            for (int i = 0; i < 3; ++i) done_with_stage();
           }
           if (ok && one) commit_pair(smem_u32(dfull + buf));
           buf ^= 1;
@@ -491,8 +501,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
           const bool clear = c1 == blocks && left < 64;
-          stage = (stage + (c1 - c0 - (clear ? 1 : 0)) * slots) % stages;
-          for (int i = 0; clear && i < slots; ++i) {
+          for (int i = 0; ok && i < slots; ++i) {
+            stage = (stage + c1 - c0 - (clear ? 1 : 0)) % stages;
+            if (!clear) continue;
             if (!(ok = mbar_wait_bounded(landed + stage, phases >> stage & 1))) break;
             phases ^= 1u << stage;
             // rows of 128 bytes, one for each K, in boxes of 64: two of A, one or two of B
@@ -796,7 +807,7 @@ cudaError_t launch_expert_mm_rows(const MmArgs& a, cudaStream_t s) {
   if (gated) p.nt = (a.N + p.tile_n / 2 - 1) / (p.tile_n / 2);
   p.b_mn = a.b_mn;
   p.idesc = mm_idesc(false, a.b_mn, p.tile_n);
-  p.chunk = a.f32 ? 2 : 1 << 20;
+  p.chunk = a.f32 ? 1 : 1 << 20;
   const int64_t most = down * p.nt;
   using H = __nv_bfloat16;
   if (a.f32) switch (a.act) {
@@ -820,7 +831,7 @@ cudaError_t launch_expert_mm_wgrad(const MmArgs& a, cudaStream_t s) {
   p.tile_n = a.tile_n;
   p.nt = (a.N + p.tile_n - 1) / p.tile_n, p.mt = (a.M + 255) / 256;
   p.idesc = mm_idesc(true, true, p.tile_n);
-  p.chunk = p.terms == 1 ? 8 : p.terms == 3 ? 4 : 2;
+  p.chunk = p.terms == 1 ? 8 : p.terms == 3 ? 4 : 1;
   if (a.S > 0) {
     const int64_t parts = a.split ? (int64_t)a.S / a.split + std::min(a.E, a.S) : a.E;
     const cudaError_t e = a.out_bf16 ? launch_mm<true, -1, true, __nv_bfloat16>(a, p, parts * p.mt * p.nt, s)
