@@ -28,7 +28,7 @@
 // products, for an fp32 gradient of bf16 weights, such threes hold the copies up: 2.2 ms for 524288 x 2048 x 512 instead of
 // 1.9, so there each product has a stage).  The tensor core adds in fp32 but does not round to nearest, so an
 // error would grow with the length of the sum: fp32 results are therefore summed over parts of K in
-// registers, and in a part the small products come first (8192 rows of bf16: 9.1e-6 off in the 2-norm in one sum, 4.8e-7 in parts of 512).  bf16 results take the accumulator as it is (its error, below 2^-12 at K = 65536, is inside
+// registers, the small products' apart from the large one's (8192 rows of bf16: 9.1e-6 off in the 2-norm in one sum, 4.8e-7 in parts of 512).  bf16 results take the accumulator as it is (its error, below 2^-12 at K = 65536, is inside
 // bf16's rounding).
 //
 // Measured on bf16 rows of 64 experts: 524288 x 512 through 512 -> 2048 outputs gated, h alone 0.60 ms (1.8 PFLOP/s,
@@ -261,8 +261,9 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// WGRAD: the contraction runs over rows.  ACT: gated, or -1.  SUM: parts of K are summed in registers.
-template <bool WGRAD, int ACT, bool SUM, typename T>
+// WGRAD: the contraction runs over rows.  ACT: gated, or -1.  SUM: parts of K are summed in registers.  SIX: fp32
+// operands, six products of their planes.
+template <bool WGRAD, int ACT, bool SUM, bool SIX, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     k_expert_mm(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                 const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap gmap, MmParams p) {
@@ -324,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   let_next_start();
   const uint32_t tmem = *tmem_slot;
   const int tiles = prefix[p.E];
-  const int terms = p.terms, tile_n = p.tile_n, slots = terms == 1 ? 1 : 3, stage_bytes = mm_stage(tile_n);  // slots: stages of 64 K
+  const int terms = SIX ? 6 : p.terms, tile_n = p.tile_n, slots = terms == 1 ? 1 : 3, stage_bytes = mm_stage(tile_n);  // slots: stages of 64 K
   Walk walk{cuts, prefix};
 
   // blocks of 64 along a tile's contraction; WGRAD: and its rows [r0, r1)
@@ -354,10 +355,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const int n0 = GATED ? n * (tile_n / 2) : n * tile_n + (int)rank * (tile_n / 2);
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
-          for (int i = 0; ok && i < slots; ++i)
-            for (int kb = c0; kb < c1; ++kb) {
+          // six products: the planes of each 64 K side by side; three: a part's first products, then its second ..
+          const int outer = terms == 6 ? c1 - c0 : slots, inner = terms == 6 ? slots : c1 - c0;
+          for (int u = 0; ok && u < outer; ++u)
+            for (int v = 0; v < inner; ++v) {
+              const int i = terms == 6 ? v : u, kb = c0 + (terms == 6 ? u : v);
               if (!(ok = mbar_wait_bounded(empty + stage, phase))) break;
-              const int pa = terms == 6 ? i : p.terms_a >> (4 * i) & 15, pb = terms == 6 ? i : p.terms_b >> (4 * i) & 15;
+              const int pa = terms == 6 ? 2 - i : p.terms_a >> (4 * i) & 15, pb = terms == 6 ? 2 - i : p.terms_b >> (4 * i) & 15;
               uint32_t bar;
               if (WGRAD && r1 - r0 - kb * 64 < 64) {  // by way of the warp that clears rows
                 bar = smem_u32(landed + stage);
@@ -418,14 +422,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           k_blocks(walk.local(tile), r0, r1);
           length = r1 - r0;
         }
-        bool ready = false;  // what the next part waits for has been seen
         for (int done = 0; ok && done < length; done += chunk * 64) {
           const int part = min(length - done, chunk * 64);
-          if (!ready && !(ok = mbar_wait_bounded(dempty + buf, dphase))) break;
+          if (!(ok = mbar_wait_bounded(dempty + buf, dphase))) break;
           tc_fence_after();
-          const uint32_t d = tmem + buf * 256;
-          uint32_t accumulate = 0;
-          const auto products = [&](int left, uint32_t sa, uint32_t sb) {
+          const auto products = [&](int left, uint32_t sa, uint32_t sb, uint32_t d, uint32_t accumulate) {
             const uint32_t lo_a = (uint32_t)desc_a + sa * stage_step, lo_b = (uint32_t)desc_b + sb * stage_step;
             if (one) {
               mma_pair(d, lo_a, hi_a, lo_b, hi_b, idesc, accumulate);
@@ -436,7 +437,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                 for (int k = 1; k * 16 < left; ++k) mma_pair(d, lo_a + k * step_a, hi_a, lo_b + k * step_b, hi_b, idesc, 1);
               }
             }
-            accumulate = 1;
           };
           // (rows cleared by the other CTA's threads want an acquire of the cluster's scope; copies do not)
           const auto come = [&](int left, uint32_t at, uint32_t parity) {
@@ -446,16 +446,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
             if (one) commit_pair(empty0 + stage * 8);
             if (++stage == stages) stage = 0, phase ^= 1;
           };
-          if (terms != 6) {  // a stage for each product
+          if constexpr (!SIX) {  // a stage for each product
+            uint32_t accumulate = 0;
             for (int i = 0; ok && i < slots; ++i)
               for (int left = part; left > 0; left -= 64) {
                 if (!(ok = come(left, stage, phase))) break;
                 tc_fence_after();
-                products(left, stage, stage);
+                products(left, stage, stage, tmem + buf * 256, accumulate);
+                accumulate = 1;
                 done_with_stage();
               }
+            if (ok && one) commit_pair(smem_u32(dfull + buf));
+            buf ^= 1;
+            dphase ^= buf ^ 1;
           } else {
-            // parts of 64 K: a stage for each of both operands' planes, and six products of them
+            // A stage for each of both operands' planes, 2, 1, 0 in turn, and six products of them: the five small ones
+            // into one half of the tensor memory, the large one into the other.
             const auto three = [&](int left, uint32_t at, uint32_t parity) {
               bool all = true;
               for (int i = 0; all && i < 3; ++i) {
@@ -464,27 +470,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
               }
               return all;
             };
-            if (!ready && !(ok = three(part, stage, phase))) break;
-            tc_fence_after();
-            ready = false;
-            for (int t = 0; ok && t < terms; ++t) {
-              uint32_t sa = stage + (terms_a >> (4 * t) & 15), sb = stage + (terms_b >> (4 * t) & 15);
-              if (sa >= stages) sa -= stages;
-              if (sb >= stages) sb -= stages;
-              if (t == terms - 1 && done + 64 < length && stages >= 6) {
-                // the next part's copies and accumulator, waited for while the tensor core still has work (its stages
-                // are others than this part's)
-                uint32_t next = stage + 3, parity = phase;
-                if (next >= stages) next -= stages, parity ^= 1;
-                ok = ready = mbar_wait_bounded(dempty + (buf ^ 1), dphase ^ (buf == 1)) && three(length - done - 64, next, parity);
+            bool ready = false;
+            for (int left = part; ok && left > 0; left -= 64) {
+              if (!ready && !(ok = three(left, stage, phase))) break;
+              tc_fence_after();
+              ready = false;
+              const uint32_t first = stage;
+              for (int t = 0; ok && t < 6; ++t) {
+                uint32_t sa = first + 2 - (terms_a >> (4 * t) & 15), sb = first + 2 - (terms_b >> (4 * t) & 15);
+                if (sa >= stages) sa -= stages;
+                if (sb >= stages) sb -= stages;
+                if (t == 5) {
+                  // the large sum's half is read last of a part
+                  if (left == part && !(ok = mbar_wait_bounded(dempty + 1, dphase))) break;
+                  if (left > 64 && stages >= 6) {
+                    // the next copies, waited for while the tensor core still has work (their stages are others)
+                    uint32_t next = stage + 1, parity = phase;
+                    if (next >= stages) next -= stages, parity ^= 1;
+                    if (!(ok = ready = three(left - 64, next, parity))) break;
+                  }
+                  tc_fence_after();
+                }
+                products(left, sa, sb, t < 5 ? tmem + 256 : tmem, left < part || (t > 0 && t < 5));
+                if (t == 2 || t >= 4) done_with_stage();  // (planes 2 are done with first, then 1)
               }
-              products(part, sa, sb);
             }
-            for (int i = 0; i < 3; ++i) done_with_stage();
+            if (ok && one) commit_pair(smem_u32(dfull));
+            dphase ^= 1;
           }
-          if (ok && one) commit_pair(smem_u32(dfull + buf));
-          buf ^= 1;
-          dphase ^= buf ^ 1;
         }
       }
     }
@@ -501,9 +514,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
           const bool clear = c1 == blocks && left < 64;
+          if (terms == 6) stage = (stage + (c1 - c0 - 1) * slots) % stages;
           for (int i = 0; ok && i < slots; ++i) {
-            stage = (stage + c1 - c0 - (clear ? 1 : 0)) % stages;
-            if (!clear) continue;
+            if (terms != 6) stage = (stage + c1 - c0 - 1) % stages;  // the part's last block
+            if (!clear) {
+              stage = stage + 1 == stages ? 0 : stage + 1;
+              continue;
+            }
             if (!(ok = mbar_wait_bounded(landed + stage, phases >> stage & 1))) break;
             phases ^= 1u << stage;
             // rows of 128 bytes, one for each K, in boxes of 64: two of A, one or two of B
@@ -553,17 +570,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           ok = ok && mbar_wait_bounded(dfull + buf, dphase);
           tc_fence_after();
           __syncwarp();
-          const uint32_t from = lanes + buf * 256;
+          // six products: the small ones' sum from the upper half, which is given back at once, then the large one's
+          for (int half = SIX; half >= 0; --half) {
+            const uint32_t from = lanes + (SIX ? half : buf) * 256;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (!(i < 2 ? has0 : has1)) continue;
-            float v[16];
-            tmem_ld16(from + (i < 2 ? at0 : at1) + (i & 1) * 16, v);
+            for (int i = 0; i < 4; ++i) {
+              if (!(i < 2 ? has0 : has1)) continue;
+              float v[16];
+              tmem_ld16(from + (i < 2 ? at0 : at1) + (i & 1) * 16, v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) (i < 2 ? v0 : v1)[(i & 1) * 16 + j] += v[j];
+              for (int j = 0; j < 16; ++j) (i < 2 ? v0 : v1)[(i & 1) * 16 + j] += v[j];
+            }
+            release(SIX ? 1 - half : buf);
           }
-          release(buf);
-          if (++buf == 2) buf = 0, dphase ^= 1;
+          if (SIX) dphase ^= 1;
+          else if (++buf == 2) buf = 0, dphase ^= 1;
         }
       } else {
         ok = ok && mbar_wait_bounded(dfull + buf, dphase);
@@ -745,9 +766,9 @@ bool make_out_map(CUtensorMap* map, void* p, int64_t rows, int64_t cols, int64_t
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool WGRAD, int ACT, bool SUM, typename T>
+template <bool WGRAD, int ACT, bool SUM, bool SIX, typename T>
 cudaError_t launch_mm(const MmArgs& a, MmParams p, int64_t tiles_most, cudaStream_t s) {
-  constexpr auto kern = k_expert_mm<WGRAD, ACT, SUM, T>;
+  constexpr auto kern = k_expert_mm<WGRAD, ACT, SUM, SIX, T>;
   cudaError_t e = prepare_kernel<kern>();
   if (e != cudaSuccess) return e;
   CUtensorMap amap, bmap, omap, gmap;
@@ -807,22 +828,22 @@ cudaError_t launch_expert_mm_rows(const MmArgs& a, cudaStream_t s) {
   if (gated) p.nt = (a.N + p.tile_n / 2 - 1) / (p.tile_n / 2);
   p.b_mn = a.b_mn;
   p.idesc = mm_idesc(false, a.b_mn, p.tile_n);
-  p.chunk = a.f32 ? 1 : 1 << 20;
+  p.chunk = a.f32 ? 8 : 1 << 20;
   const int64_t most = down * p.nt;
   using H = __nv_bfloat16;
   if (a.f32) switch (a.act) {
-      case EMB_ACT_SILU: return launch_mm<false, EMB_ACT_SILU, true, float>(a, p, most, s);
-      case EMB_ACT_GELU: return launch_mm<false, EMB_ACT_GELU, true, float>(a, p, most, s);
-      case EMB_ACT_RELU: return launch_mm<false, EMB_ACT_RELU, true, float>(a, p, most, s);
-      case EMB_ACT_SIGMOID: return launch_mm<false, EMB_ACT_SIGMOID, true, float>(a, p, most, s);
-      default: return launch_mm<false, -1, true, float>(a, p, most, s);
+      case EMB_ACT_SILU: return launch_mm<false, EMB_ACT_SILU, true, true, float>(a, p, most, s);
+      case EMB_ACT_GELU: return launch_mm<false, EMB_ACT_GELU, true, true, float>(a, p, most, s);
+      case EMB_ACT_RELU: return launch_mm<false, EMB_ACT_RELU, true, true, float>(a, p, most, s);
+      case EMB_ACT_SIGMOID: return launch_mm<false, EMB_ACT_SIGMOID, true, true, float>(a, p, most, s);
+      default: return launch_mm<false, -1, true, true, float>(a, p, most, s);
     }
   switch (a.act) {
-    case EMB_ACT_SILU: return launch_mm<false, EMB_ACT_SILU, false, H>(a, p, most, s);
-    case EMB_ACT_GELU: return launch_mm<false, EMB_ACT_GELU, false, H>(a, p, most, s);
-    case EMB_ACT_RELU: return launch_mm<false, EMB_ACT_RELU, false, H>(a, p, most, s);
-    case EMB_ACT_SIGMOID: return launch_mm<false, EMB_ACT_SIGMOID, false, H>(a, p, most, s);
-    default: return launch_mm<false, -1, false, H>(a, p, most, s);
+    case EMB_ACT_SILU: return launch_mm<false, EMB_ACT_SILU, false, false, H>(a, p, most, s);
+    case EMB_ACT_GELU: return launch_mm<false, EMB_ACT_GELU, false, false, H>(a, p, most, s);
+    case EMB_ACT_RELU: return launch_mm<false, EMB_ACT_RELU, false, false, H>(a, p, most, s);
+    case EMB_ACT_SIGMOID: return launch_mm<false, EMB_ACT_SIGMOID, false, false, H>(a, p, most, s);
+    default: return launch_mm<false, -1, false, false, H>(a, p, most, s);
   }
 }
 
@@ -831,11 +852,12 @@ cudaError_t launch_expert_mm_wgrad(const MmArgs& a, cudaStream_t s) {
   p.tile_n = a.tile_n;
   p.nt = (a.N + p.tile_n - 1) / p.tile_n, p.mt = (a.M + 255) / 256;
   p.idesc = mm_idesc(true, true, p.tile_n);
-  p.chunk = p.terms == 1 ? 8 : p.terms == 3 ? 4 : 1;
+  p.chunk = p.terms == 3 ? 4 : 8;
   if (a.S > 0) {
     const int64_t parts = a.split ? (int64_t)a.S / a.split + std::min(a.E, a.S) : a.E;
-    const cudaError_t e = a.out_bf16 ? launch_mm<true, -1, true, __nv_bfloat16>(a, p, parts * p.mt * p.nt, s)
-                                     : launch_mm<true, -1, true, float>(a, p, parts * p.mt * p.nt, s);
+    const cudaError_t e = a.f32        ? launch_mm<true, -1, true, true, float>(a, p, parts * p.mt * p.nt, s)
+                          : a.out_bf16 ? launch_mm<true, -1, true, false, __nv_bfloat16>(a, p, parts * p.mt * p.nt, s)
+                                       : launch_mm<true, -1, true, false, float>(a, p, parts * p.mt * p.nt, s);
     if (e != cudaSuccess || !a.split) return e;
   }
   // (no rows: no parts, and zeros)
