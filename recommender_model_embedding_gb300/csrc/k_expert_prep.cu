@@ -7,8 +7,10 @@
 // instead, and infinities and NaN stand in v0 alone.
 //
 // Gated block: from h = act(g) u, dg = dh u act'(g) and du = dh act(g), side by side as the product's
-// operand, rounded to bf16 as the tensor cores take them (fp32: three planes).  Both kernels are bound by
-// HBM bandwidth.
+// operand, rounded to bf16 as the tensor cores take them (for fp32 results, dw among them: three planes, for a
+// gradient in fp32 of [dg, du] rounded to bf16 is 2.6e-3 off in the 2-norm).  Both kernels are bound by HBM bandwidth:
+// 524288 x 1024 in bf16 to three planes 9.7 GB in 1.50 ms (6.4 TB/s, 95% of the measured copy rate); the planes of
+// 8198 x 479 rows and 12 x 1280 x 479 weights in fp32 113 MB in 24 us (4.7 TB/s, in L2 for the most part).
 #include <algorithm>
 
 #include "expert_mm.cuh"

@@ -12,8 +12,14 @@
 // each with its product, so nothing is lost of them.
 //
 // A CTA takes 16 outputs of one expert and its (up to 8, 16 or 32) rows; its eight warps share the
-// contraction and add up through shared memory in a fixed order.  Where outputs are many, each warp takes 64, 32 or
-// 16 of its own, for which the rows are brought, and in fp32 split, once.
+// contraction and add up through shared memory in a fixed order.  Where outputs are many, each warp takes 64 (fp32 with
+// 32 rows: 32) of its own, for which the rows are brought, and in fp32 split, once.
+//
+// Measured, groups of 64: one row for each of two of eight experts of 2048 x 1024 3.3 us a call; 64 experts of that
+// with a row each 34 us in bf16 (33% of the copy rate), 65 in fp32; 25 experts of 4200 x 5064, whose rows lie on
+// 4-byte boundaries only, 245 and 340.
+// With 64 experts neither memory (DRAM busy 24% in bf16, 13% in fp32) nor issue (40% of the cycles) is full: the 13 warps
+// an SM that 128 registers leave wait for loads of 4 and 8 bytes a lane.
 #include <algorithm>
 
 #include "expert_few.cuh"
