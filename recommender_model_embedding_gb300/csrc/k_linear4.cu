@@ -12,17 +12,17 @@
 // each with its product, so nothing is lost of them.
 //
 // A CTA takes 16 outputs of one expert and its (up to 8, 16 or 32) rows; its eight warps share the
-// contraction and add up through shared memory in a fixed order.  Where outputs are many, each warp takes 64 (fp32 with
-// 32 rows: 32) of its own, for which the rows are brought, and in fp32 split, once.
+// contraction and add up through shared memory in a fixed order.  Where outputs are many, each warp takes tiles of its
+// own and streams their codes through shared memory (k_linear4_stream), or, where codes do not start on the boundaries that
+// its copies need, loads them for 64 (fp32 with 32 rows: 32) outputs at a time.
 //
 // Measured, groups of 64: one row for each of two of eight experts of 2048 x 1024 3.3 us a call; 64 experts of that
-// with a row each 34 us in bf16 (33% of the copy rate), 65 in fp32; 25 experts of 4200 x 5064, whose rows lie on
-// 4-byte boundaries only, 245 and 340.
-// With 64 experts neither memory (DRAM busy 24% in bf16, 13% in fp32) nor issue (40% of the cycles) is full: the 13 warps
-// an SM that 128 registers leave wait for loads of 4 and 8 bytes a lane.
+// with a row each 30 us in bf16 (37% of the copy rate) and 38 in fp32 (34 and 65 with loads in place of the ring); 25
+// experts of 4200 x 5064, whose rows lie on 4-byte boundaries only, 130 and 173 (245 and 340).
 #include <algorithm>
 
 #include "expert_few.cuh"
+#include "interact_common.cuh"
 
 namespace emb {
 
@@ -180,6 +180,195 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   }
 }
 
+// The same where outputs are many, codes start on a 16-byte boundary and their rows on 4-byte boundaries.  Each warp
+// has tiles of 16 outputs of its own, up to MT at a time, and streams their codes and scales through a ring in shared memory, four stages (of
+// 128 codes of 16 outputs) ahead of the one it multiplies; the CTA's rows of x lie beside them as the fragments they
+// are taken as, up to KC columns at a time, so that they are brought, and in fp32 split, once for all warps.  Codes come
+// in whole pieces of 16 bytes: four for an output's 64 bytes where rows start on such boundaries (WHOLE), else five.
+constexpr int kRing4 = 5, kCodes4 = 128, kBytes4 = kCodes4 / 2;
+constexpr int kPitch4 = kBytes4 + 16;                     // from one output's codes to the next: eight rows meet no bank twice
+constexpr int kScales4 = 16 * kPitch4;                    // behind the codes, [step of 32 codes][output]
+constexpr int kStage4 = kScales4 + kCodes4 / 32 * 16 * 4;
+template <typename T, int NT>
+struct Stream4 {
+  static constexpr int PLANES = sizeof(T) == 4 ? 3 : 1, MT = PLANES == 3 && NT == 4 ? 2 : 4;
+  static constexpr int KC = (PLANES == 3 ? 1024 : 2048) / NT, kX = KC / 32 * NT * PLANES * 512;
+  static constexpr int kSmem = kX + kFewWarps * kRing4 * kStage4;
+};
+
+// `bytes` of N, zero behind them.
+template <int N>
+__device__ __forceinline__ void copy_ahead(uint32_t to, const void* from, int bytes) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+
+template <typename T, int NT, bool WHOLE>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    k_linear4_stream(const T* x, int64_t x_ld, int x_vec, const int32_t* offsets, int E, int S, const uint8_t* q, const float* scale,
+                     int in, int out_dim, FastDiv per_group, int groups, T* out, int64_t out_ld, int tile0, int each) {
+  using C = Stream4<T, NT>;
+  constexpr int PLANES = C::PLANES, MT = C::MT, KC = C::KC, RT = 8 * NT;
+  extern __shared__ __align__(16) unsigned char room4[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  wait_for_earlier();
+  let_next_start();
+  int e, r0, rows;
+  if (!few_tile(offsets, E, S, RT, tile0 + (int)blockIdx.y, lane, e, r0, rows)) return;
+  const int row_bytes = (in + 1) / 2, chunks = (in + KC - 1) / KC;
+  const int o0 = (blockIdx.x * kFewWarps + warp) * 16 * each;
+  const int mine = min(max((out_dim - o0 + 15) / 16, 0), each);  // tiles of this warp
+  const uint8_t* const end = q + (int64_t)E * out_dim * row_bytes;
+  q += (int64_t)e * out_dim * row_bytes, scale += (int64_t)e * out_dim * groups;
+  x += (int64_t)r0 * x_ld;
+  uint4* const xs = reinterpret_cast<uint4*>(room4);
+  unsigned char* const ring = room4 + C::kX + warp * (kRing4 * kStage4);
+  const auto stages_of = [&](int c) { return (min(KC, in - c * KC) + kCodes4 - 1) / kCodes4; };
+  // codes of output o of this warp's tile i (the last one's behind the matrix: what they give is not stored)
+  const auto codes = [&](int i, int o) { return q + (int64_t)min(o0 + 16 * i + o, out_dim - 1) * row_bytes; };
+
+  // The next stage to bring: its chunk, tile (nf + ni) and place; this lane's pieces of it, and its scales.
+  constexpr int PIECES = WHOLE ? 4 : 5, COPIES = (16 * PIECES + 31) / 32;
+  const uint8_t* from[COPIES];
+  const float* from_scale = scale;
+  int nf = 0, nc = 0, ni = 0, nq = 0, k0 = 0, nstages = stages_of(0);
+  const auto place = [&] {
+#pragma unroll
+    for (int j = 0; j < COPIES; ++j) {
+      const int i = j * 32 + lane;
+      from[j] = codes(nf + ni, i / PIECES) + k0 / 2;
+      from[j] -= reinterpret_cast<uintptr_t>(from[j]) & 15;
+      from[j] += i % PIECES * 16;
+    }
+    from_scale = scale + (int64_t)min(o0 + 16 * (nf + ni) + (lane & 15), out_dim - 1) * groups;
+  };
+  if (mine) place();
+  const auto bring = [&](int slot) {
+    if (nf < mine) {
+      const uint32_t at = smem_u32(ring + slot * kStage4);
+      // whole stages, five pieces of which end inside the row
+      const bool inside = k0 + (WHOLE ? 1 : 2) * kCodes4 <= in;
+#pragma unroll
+      for (int j = 0; j < COPIES; ++j) {
+        const int i = j * 32 + lane, r = i / PIECES, piece = i % PIECES;
+        if (16 * PIECES % 32 != 0 && i >= 16 * PIECES) break;
+        int bytes = 16;
+        if (!inside) {  // none from behind the row's end, nor the matrices'
+          if (WHOLE) {
+            bytes = k0 / 2 + 16 * piece < row_bytes ? 16 : 0;
+          } else {
+            const int64_t left = codes(nf + ni, r) + row_bytes - from[j], all = end - from[j];
+            bytes = left > 0 ? (int)(all < 16 ? all : 16) : 0;
+          }
+        }
+        copy_ahead<16>(at + r * kPitch4 + piece * 16, bytes ? from[j] : q, bytes);
+        from[j] += kBytes4;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int u = j * 2 + (lane >> 4), k = k0 + 32 * u;
+        const bool there = inside || k < in;
+        copy_ahead<4>(at + kScales4 + (j * 32 + lane) * 4, from_scale + (there ? per_group.div((uint32_t)k / 32) : 0), there ? 4 : 0);
+      }
+      k0 += kCodes4;
+      if (++nq == nstages) {
+        nq = 0, k0 = nc * KC;
+        if (++ni == min(MT, mine - nf)) {
+          ni = 0;
+          if (++nc == chunks) nc = 0, nf += MT;
+          nstages = stages_of(nc), k0 = nc * KC;
+          if (nf < mine) place();
+        } else if (o0 + 16 * (nf + ni) + 16 <= out_dim) {  // 16 rows on, as far from a boundary
+#pragma unroll
+          for (int j = 0; j < COPIES; ++j) from[j] += 16 * (int64_t)row_bytes - nstages * kBytes4;
+          from_scale += 16 * groups;
+        } else {
+          place();
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < kRing4 - 1; ++s) bring(s);
+
+  // where this lane's two outputs' codes start in a stage (in every tile as in the first)
+  const uint32_t ga = g * kPitch4 + t * 4 + (WHOLE ? 0 : reinterpret_cast<uintptr_t>(codes(0, g)) & 15);
+  const uint32_t gb = (g + 8) * kPitch4 + t * 4 + (WHOLE ? 0 : reinterpret_cast<uintptr_t>(codes(0, g + 8)) & 15);
+  int slot = 0;
+  for (int first = 0; first < each; first += MT) {
+    float acc[MT][NT][4] = {};
+    for (int c = 0; c < chunks; ++c) {
+      const int stages = stages_of(c);
+      if (first == 0) {  // (more than MT tiles are a warp's only where one piece holds all columns)
+        if (c) __syncthreads();
+        for (int i = warp; i < stages * (kCodes4 / 32) * NT; i += kFewWarps) {
+          const int r = g + 8 * (i % NT), k = c * KC + i / NT * 32 + t * 8;
+          Raw<T, 8> v;
+          v.load(x + (int64_t)(r < rows ? r : 0) * x_ld + (k < in ? k : 0), r < rows ? in - k : 0, x_vec);
+          uint32_t f[PLANES][4];
+          x_pairs<T, PLANES>(v, f);
+#pragma unroll
+          for (int pl = 0; pl < PLANES; ++pl) xs[(i * PLANES + pl) * 32 + lane] = make_uint4(f[pl][0], f[pl][1], f[pl][2], f[pl][3]);
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (first + i >= mine) break;
+        for (int st = 0; st < stages; ++st) {
+          // this stage has come, and all lanes are done with the one whose place is filled again
+          asm volatile("cp.async.wait_group %0;" ::"n"(kRing4 - 2) : "memory");
+          __syncwarp();
+          bring(slot == 0 ? kRing4 - 1 : slot - 1);
+          const unsigned char* at = ring + slot * kStage4;
+          slot = slot + 1 == kRing4 ? 0 : slot + 1;
+#pragma unroll
+          for (int u = 0; u < kCodes4 / 32; ++u) {
+            const uint32_t wa = *reinterpret_cast<const uint32_t*>(at + ga + u * 16);
+            const uint32_t wb = *reinterpret_cast<const uint32_t*>(at + gb + u * 16);
+            const float* s = reinterpret_cast<const float*>(at + kScales4) + u * 16 + g;
+            const float fa = s[0], fb = s[8];
+            uint32_t a[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              a[h][0] = codes_at(wa, 2 * h), a[h][1] = codes_at(wb, 2 * h), a[h][2] = codes_at(wa, 2 * h + 1), a[h][3] = codes_at(wb, 2 * h + 1);
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+              float part[4] = {};
+#pragma unroll
+              for (int pl = PLANES - 1; pl >= 0; --pl) {
+                const uint4 f = xs[(((st * (kCodes4 / 32) + u) * NT + m) * PLANES + pl) * 32 + lane];
+                mma16816(part, a[0], f.x, f.y), mma16816(part, a[1], f.z, f.w);
+              }
+              acc[i][m][0] = fmaf(fa, part[0], acc[i][m][0]), acc[i][m][1] = fmaf(fa, part[1], acc[i][m][1]);
+              acc[i][m][2] = fmaf(fb, part[2], acc[i][m][2]), acc[i][m][3] = fmaf(fb, part[3], acc[i][m][3]);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      if (first + i >= mine) break;  // (what follows is the next warp's)
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = m * 8 + 2 * t + (k & 1), o = o0 + 16 * (first + i) + g + 8 * (k >> 1);
+          if (r < rows && o < out_dim) {
+            const float v[1] = {acc[i][m][k]};
+            Pack<T, 1> p;
+            p.set(v);
+            p.store(out + (int64_t)(r0 + r) * out_ld + o);
+          }
+        }
+    }
+  }
+}
+
 // One group of a row a warp pass: scale = max|w| / 7, code = w / scale rounded to the nearest integer
 // (ties to even) + 8.
 template <typename T>
@@ -218,7 +407,7 @@ __global__ void __launch_bounds__(256)
 template <typename T, int W, int NT>
 cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
   constexpr bool F32 = sizeof(T) == 4;
-  // Warps of their own for 64 outputs (fp32 with 32 rows: 32) where these fill the SMs, else eight warps for 16.
+  // Tiles of a warp at a time where these fill the SMs, else eight warps share one.
   constexpr int MT = F32 && NT == 4 ? 2 : 4;
   // Steps loaded ahead.  Shared tiles: two, and where a warp has more of them four in bf16 (with two steps a warp, four
   // take longer for the masks: 3.6 -> 4.3 us for a single request; in fp32 they leave room for one CTA an SM: 1 x
@@ -239,9 +428,42 @@ cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
                               (const uint8_t*)a.d_q, (const float*)a.d_scale, (int)a.in, (int)a.out, (int)q_vec, (int)a.group / (32 * W), groups,
                               static_cast<T*>(a.d_out), a.out_ld, (int)tile0);
   };
+  using C = Stream4<T, NT>;
+  // Tiles of a warp: such that the SM with most CTAs has least to do where rows spread evenly, a CTA's start taking
+  // about the time of six stages, and fewer than two CTAs an SM as long as two.  Where one piece holds all columns, a
+  // warp's tiles can be more than MT (242 experts of 7824 x 352 in bf16: 141 us, with at most four 180).
+  const int64_t full = std::min<int64_t>(a.experts, a.rows), likely = full * (((a.rows + full - 1) / full + 8 * NT - 1) / (8 * NT));
+  const int64_t stages = (a.in + kCodes4 - 1) / kCodes4;
+  const auto cost = [&](int n) {
+    const int64_t ctas = likely * ((across + kFewWarps * n - 1) / (kFewWarps * n));
+    return std::max<int64_t>((ctas + device_sms() - 1) / device_sms(), 2) * (n * stages + 6);
+  };
+  int each = C::MT;
+  for (const int n : {2, 3, 6, 8, 12, 16})
+    if ((n <= C::MT || a.in <= C::KC) && cost(n) < cost(each)) each = n;
+  const auto stream = [&](auto kern, int64_t tile0, int64_t tiles) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((across + kFewWarps * each - 1) / (kFewWarps * each)), (unsigned)tiles);
+    cfg.blockDim = dim3(kFewThreads), cfg.dynamicSmemBytes = C::kSmem, cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(a.d_x), a.x_ld, x_vec, a.d_offsets, (int)a.experts, (int)a.rows,
+                              (const uint8_t*)a.d_q, (const float*)a.d_scale, (int)a.in, (int)a.out, FastDiv(a.group / 32), groups,
+                              static_cast<T*>(a.d_out), a.out_ld, (int)tile0, each);
+  };
+  const int row_bytes = (a.in + 1) / 2;
+  const bool streams = alone && reinterpret_cast<uintptr_t>(a.d_q) % 16 == 0 && row_bytes % 4 == 0;
   // (a grid has 65535 rows at most)
   for (int64_t at = 0; at < all; at += 65535) {
     const int64_t n = std::min<int64_t>(65535, all - at);
+    if (streams) {
+      const cudaError_t e = row_bytes % 16 == 0 ? stream(k_linear4_stream<T, NT, true>, at, n) : stream(k_linear4_stream<T, NT, false>, at, n);
+      if (e != cudaSuccess) return e;
+      continue;
+    }
     const cudaError_t e = alone  ? run(k_linear4<T, W, NT, ALONE, 1, MT>, at, n)
                           : more ? run(k_linear4<T, W, NT, MORE, kFewWarps, 1>, at, n)
                                  : run(k_linear4<T, W, NT, U, kFewWarps, 1>, at, n);

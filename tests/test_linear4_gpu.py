@@ -84,6 +84,55 @@ def test_product(E, shape, group, dtype, pad):
         assert torch.equal(alone, out)
 
 
+# outputs so many that each warp has its own: rows of codes on 16 bytes, 4 bytes, and any; one, two and more pieces of
+# the columns; a last tile, and a last warp's tiles, that are not whole
+MANY = [([1] * 6, 0, 32, 14000), ([1, 0, 3] * 4, 2, 1024, 9999), ([8] * 5, 1, 479, 16001), ([2, 1, 0, 5], 0, 2056, 20488),
+        ([1] * 30, 1, 2600, 2890), ([1] * 8, 3, 515, 11000), ([16, 9, 12], 1, 1096, 26000), ([9] * 9, 0, 4160, 9001),
+        ([33, 0, 17, 20], 3, 1160, 15003), ([64, 40], 0, 264, 30000), ([1, 2] * 60, 1, 96, 9000), ([17] * 60, 0, 200, 8005),
+        ([10, 16] * 40, 2, 352, 7010)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 96])
+@pytest.mark.parametrize("shape", MANY, ids=[f"{len(s[0])}x{sum(s[0])}-{s[2]}-{s[3]}" for s in MANY])
+def test_many_outputs(E, shape, group, dtype):
+    test_product(E, shape, group, dtype, 3 if group == 96 else 0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_many_outputs_again(E, dtype):
+    """Calls in a row, on two streams, and replayed give the same bits; a scale behind an infinite one is not read
+    for columns that are not there."""
+    e, d, o = 6, 2104, 14008
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.randn((e, d), generator=g, device="cuda").to(dtype)
+    q = torch.randint(0, 256, (e, o, d // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scale = torch.rand((e, o, -(-d // 64)), generator=g, device="cuda")
+    scale[1, 7, -1] = float("inf")
+    off = torch.arange(e + 1, device="cuda").int()
+    outs = [torch.full((e, o), 7.0, device="cuda", dtype=dtype) for _ in range(4)]
+    E.expert_linear4(x, q, scale, outs[0], offsets=off)
+    E.expert_linear4(x, q, scale, outs[1], offsets=off)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        E.expert_linear4(x, q, scale, outs[2], offsets=off)
+    torch.cuda.current_stream().wait_stream(other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        E.expert_linear4(x, q, scale, outs[3], offsets=off)
+    outs[3].fill_(7)
+    graph.replay()
+    last = unpack(q[1, 7], torch.ones_like(scale[1, 7]), d, 64)[d // 64 * 64:] @ x[1, d // 64 * 64:].double()
+    assert outs[0][1, 7].double() == math.copysign(math.inf, last)
+    ok = torch.ones_like(outs[0], dtype=torch.bool)
+    ok[1, 7] = False
+    assert outs[0][ok].isfinite().all()
+    for other in outs[1:]:
+        assert torch.equal(outs[0], other)
+
+
 def test_codes_anywhere(E):
     """Codes that start at any byte."""
     x = torch.randn((3, 64), device="cuda")
