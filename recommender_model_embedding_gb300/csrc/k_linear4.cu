@@ -439,7 +439,7 @@ cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
     return std::max<int64_t>((ctas + device_sms() - 1) / device_sms(), 2) * (n * stages + 6);
   };
   int each = C::MT;
-  for (const int n : {2, 3, 6, 8, 12, 16})
+  for (const int n : {1, 2, 3, 6, 8, 12, 16})
     if ((n <= C::MT || a.in <= C::KC) && cost(n) < cost(each)) each = n;
   const auto stream = [&](auto kern, int64_t tile0, int64_t tiles) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -455,7 +455,10 @@ cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
                               static_cast<T*>(a.d_out), a.out_ld, (int)tile0, each);
   };
   const int row_bytes = (a.in + 1) / 2;
-  const bool streams = alone && reinterpret_cast<uintptr_t>(a.d_q) % 16 == 0 && row_bytes % 4 == 0;
+  // From six tiles an SM on.  At 3.4 (one expert of 8192 x 4096, groups of 32) the shared sum takes 17 us and the ring 21; at
+  // 6.7 (eight of 2048 x 1024) 11.3 and 8.7, with groups of 64 and eight rows each 9.3 and 10.4; at 13 (16 of 2048 x 512)
+  // 14.5 and 6.2.  In fp32 34 and 33, 20 and 12, 21 and 8.
+  const bool streams = likely * across >= (int64_t)device_sms() * 6 && reinterpret_cast<uintptr_t>(a.d_q) % 16 == 0 && row_bytes % 4 == 0;
   // (a grid has 65535 rows at most)
   for (int64_t at = 0; at < all; at += 65535) {
     const int64_t n = std::min<int64_t>(65535, all - at);
