@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const int i = j * 32 + lane, r = i / PIECES, piece = i % PIECES;
         if (16 * PIECES % 32 != 0 && i >= 16 * PIECES) break;
         int bytes = 16;
+        const uint8_t* source = from[j];
         if (!inside) {  // none from behind the row's end, nor the matrices'
           if (WHOLE) {
             bytes = k0 / 2 + 16 * piece < row_bytes ? 16 : 0;
@@ -264,8 +265,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             const int64_t left = codes(nf + ni, r) + row_bytes - from[j], all = end - from[j];
             bytes = left > 0 ? (int)(all < 16 ? all : 16) : 0;
           }
+          if (bytes == 0) source = q - (reinterpret_cast<uintptr_t>(q) & 15);  // (a place to copy nothing from, on its boundary too)
         }
-        copy_ahead<16>(at + r * kPitch4 + piece * 16, bytes ? from[j] : q, bytes);
+        copy_ahead<16>(at + r * kPitch4 + piece * 16, source, bytes);
         from[j] += kBytes4;
       }
 #pragma unroll

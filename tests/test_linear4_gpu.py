@@ -146,6 +146,24 @@ def test_codes_anywhere(E):
         assert torch.allclose(out.double(), want, rtol=1e-5, atol=1e-4)
 
 
+@pytest.mark.parametrize("at", [0, 1, 4, 8, 16])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_many_codes_anywhere(E, at, dtype):
+    """Where codes start says which way they are brought, not what comes out; the last one's bytes end the buffer."""
+    e, d, o = 8, 192, 12008
+    g = torch.Generator(device="cuda")
+    g.manual_seed(at)
+    x = torch.randn((e, d), generator=g, device="cuda").to(dtype)
+    store = torch.randint(0, 256, (at + e * o * d // 2,), generator=g, device="cuda", dtype=torch.uint8)
+    q, scale = store[at:].view(e, o, d // 2), torch.rand((e, o, 3), generator=g, device="cuda")
+    out, off = torch.empty((e, o), device="cuda", dtype=dtype), torch.arange(e + 1, device="cuda").int()
+    E.expert_linear4(x, q, scale, out, offsets=off)
+    w = unpack(q, scale, d, 64)
+    want = torch.einsum("ed,eod->eo", x.double(), w)
+    mag = torch.einsum("ed,eod->eo", x.double().abs(), w.abs())
+    assert ((out.double() - want).abs() <= torch.finfo(dtype).eps / 2 * want.abs() + (d + 2) * 2.0 ** -23 * mag).all()
+
+
 def test_rows_do_not_leak(E):
     """NaN and infinities in one row stay there."""
     x = torch.randn((6, 128), device="cuda").to(BF16)
