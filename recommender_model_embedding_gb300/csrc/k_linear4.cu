@@ -13,7 +13,7 @@
 //
 // A CTA takes 16 outputs of one expert and its (up to 8, 16 or 32) rows; its eight warps share the
 // contraction and add up through shared memory in a fixed order.  Where outputs are many, each warp takes tiles of its
-// own and streams their codes through shared memory (k_linear4_stream), or, where codes do not start on the boundaries that
+// own and streams their codes through shared memory (k_linear4_stream; with fewer, in fp32, a CTA two tiles), or, where codes do not start on the boundaries that
 // its copies need, loads them for 64 (fp32 with 32 rows: 32) outputs at a time.
 //
 // Measured, groups of 64: one row for each of two of eight experts of 2048 x 1024 3.3 us a call; 64 experts of that
@@ -207,7 +207,8 @@ __device__ __forceinline__ void copy_ahead(uint32_t to, const void* from, int by
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 
-template <typename T, int NT, bool WHOLE>
+// SHARED: the CTA's tiles are all its warps', each of which takes every eighth stage of the columns; they add up at the end.
+template <typename T, int NT, bool WHOLE, bool SHARED>
 __global__ void __launch_bounds__(kFewThreads, 2)
     k_linear4_stream(const T* x, int64_t x_ld, int x_vec, const int32_t* offsets, int E, int S, const uint8_t* q, const float* scale,
                      int in, int out_dim, FastDiv per_group, int groups, T* out, int64_t out_ld, int tile0, int each) {
@@ -220,7 +221,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   int e, r0, rows;
   if (!few_tile(offsets, E, S, RT, tile0 + (int)blockIdx.y, lane, e, r0, rows)) return;
   const int row_bytes = (in + 1) / 2, chunks = (in + KC - 1) / KC;
-  const int o0 = (blockIdx.x * kFewWarps + warp) * 16 * each;
+  constexpr int STEP = SHARED ? kFewWarps : 1;
+  const int start = SHARED ? warp : 0;  // this warp's first stage of a chunk
+  const int o0 = (SHARED ? blockIdx.x : blockIdx.x * kFewWarps + warp) * 16 * each;
   const int mine = min(max((out_dim - o0 + 15) / 16, 0), each);  // tiles of this warp
   const uint8_t* const end = q + (int64_t)E * out_dim * row_bytes;
   q += (int64_t)e * out_dim * row_bytes, scale += (int64_t)e * out_dim * groups;
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   constexpr int PIECES = WHOLE ? 4 : 5, COPIES = (16 * PIECES + 31) / 32;
   const uint8_t* from[COPIES];
   const float* from_scale = scale;
-  int nf = 0, nc = 0, ni = 0, nq = 0, k0 = 0, nstages = stages_of(0);
+  int nf = 0, nc = 0, ni = 0, nq = start, k0 = start * kCodes4, nstages = stages_of(0);
   const auto place = [&] {
 #pragma unroll
     for (int j = 0; j < COPIES; ++j) {
@@ -246,7 +249,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
     from_scale = scale + (int64_t)min(o0 + 16 * (nf + ni) + (lane & 15), out_dim - 1) * groups;
   };
-  if (mine) place();
+  if (start >= nstages) nf = mine;  // (a warp without a stage of the first chunk has none of the others)
+  if (nf < mine) place();
   const auto bring = [&](int slot) {
     if (nf < mine) {
       const uint32_t at = smem_u32(ring + slot * kStage4);
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           if (bytes == 0) source = q - (reinterpret_cast<uintptr_t>(q) & 15);  // (a place to copy nothing from, on its boundary too)
         }
         copy_ahead<16>(at + r * kPitch4 + piece * 16, source, bytes);
-        from[j] += kBytes4;
+        from[j] += STEP * kBytes4;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -276,15 +280,16 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const bool there = inside || k < in;
         copy_ahead<4>(at + kScales4 + (j * 32 + lane) * 4, from_scale + (there ? per_group.div((uint32_t)k / 32) : 0), there ? 4 : 0);
       }
-      k0 += kCodes4;
-      if (++nq == nstages) {
-        nq = 0, k0 = nc * KC;
+      k0 += STEP * kCodes4, nq += STEP;
+      if (nq >= nstages) {
+        nq = start, k0 = nc * KC + start * kCodes4;
         if (++ni == min(MT, mine - nf)) {
           ni = 0;
           if (++nc == chunks) nc = 0, nf += MT;
-          nstages = stages_of(nc), k0 = nc * KC;
+          nstages = stages_of(nc), k0 = nc * KC + start * kCodes4;
+          if (SHARED && start >= nstages) nf = mine;  // (the last chunk is shorter, and its tiles are the last)
           if (nf < mine) place();
-        } else if (o0 + 16 * (nf + ni) + 16 <= out_dim) {  // 16 rows on, as far from a boundary
+        } else if (!SHARED && o0 + 16 * (nf + ni) + 16 <= out_dim) {  // 16 rows on, as far from a boundary
 #pragma unroll
           for (int j = 0; j < COPIES; ++j) from[j] += 16 * (int64_t)row_bytes - nstages * kBytes4;
           from_scale += 16 * groups;
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         if (first + i >= mine) break;
-        for (int st = 0; st < stages; ++st) {
+        for (int st = start; st < stages; st += STEP) {
           // this stage has come, and all lanes are done with the one whose place is filled again
           asm volatile("cp.async.wait_group %0;" ::"n"(kRing4 - 2) : "memory");
           __syncwarp();
@@ -354,21 +359,47 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
       }
     }
+    if constexpr (SHARED) {
+      float* const sums = reinterpret_cast<float*>(room4);  // [warp][row][output]
+      const int wide = 16 * each;
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (first + i >= mine) break;  // (what follows is the next warp's)
+      for (int i = 0; i < MT; ++i)
+        if (i < each)
 #pragma unroll
-      for (int m = 0; m < NT; ++m)
+          for (int m = 0; m < NT; ++m)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = m * 8 + 2 * t + (k & 1), o = o0 + 16 * (first + i) + g + 8 * (k >> 1);
-          if (r < rows && o < out_dim) {
-            const float v[1] = {acc[i][m][k]};
-            Pack<T, 1> p;
-            p.set(v);
-            p.store(out + (int64_t)(r0 + r) * out_ld + o);
-          }
+            for (int k = 0; k < 4; ++k)
+              sums[(warp * RT + m * 8 + 2 * t + (k & 1)) * wide + 16 * i + g + 8 * (k >> 1)] = acc[i][m][k];
+      __syncthreads();
+      for (int i = threadIdx.x; i < rows * wide; i += kFewThreads) {
+        const int r = i / wide, o = i - r * wide;
+        float v[1] = {0.f};
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) v[0] += sums[(w * RT + r) * wide + o];
+        if (o0 + o < out_dim) {
+          Pack<T, 1> p;
+          p.set(v);
+          p.store(out + (int64_t)(r0 + r) * out_ld + o0 + o);
         }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (first + i >= mine) break;  // (what follows is the next warp's)
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = m * 8 + 2 * t + (k & 1), o = o0 + 16 * (first + i) + g + 8 * (k >> 1);
+            if (r < rows && o < out_dim) {
+              const float v[1] = {acc[i][m][k]};
+              Pack<T, 1> p;
+              p.set(v);
+              p.store(out + (int64_t)(r0 + r) * out_ld + o);
+            }
+          }
+      }
     }
   }
 }
@@ -445,6 +476,19 @@ cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
   int each = C::MT;
   for (const int n : {1, 2, 3, 6, 8, 12, 16})
     if ((n <= C::MT || a.in <= C::KC) && cost(n) < cost(each)) each = n;
+  const int row_bytes = (a.in + 1) / 2;
+  const bool ring = reinterpret_cast<uintptr_t>(a.d_q) % 16 == 0 && row_bytes % 4 == 0;
+  // From six tiles an SM on.  At 3.4 (one expert of 8192 x 4096, groups of 32) the shared sum takes 17 us and the ring 21; at
+  // 6.7 (eight of 2048 x 1024) 11.3 and 8.7, with groups of 64 and eight rows each 9.3 and 10.4; at 13 (16 of 2048 x 512)
+  // 14.5 and 6.2.  In fp32 34 and 33, 20 and 12, 21 and 8.
+  const bool streams = ring && likely * across >= (int64_t)device_sms() * 6;
+  // Below that the ring's CTAs share their tiles, two at a time, where splitting rows of fp32 anew for each costs most: from two
+  // tiles an SM on (one expert of 8192 x 4096 37 us with the shared sum of single tiles and 26 with this, two of 2600 x 2600 25
+  // and 18; at 1.7, 4096 x 479, 4.1 and 4.5).  With 32 rows, and in bf16, it gains nothing (101 and 116, 12.7 and 14.6).
+  constexpr bool kPairs = F32 && NT <= 2;
+  const bool shared = kPairs && ring && !streams && likely * across >= (int64_t)device_sms() * 2;
+  if (shared) each = 2;
+  const int wide4 = shared ? each : kFewWarps * each;
   const auto stream = [&](auto kern, int64_t tile0, int64_t tiles) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
@@ -452,22 +496,24 @@ cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((across + kFewWarps * each - 1) / (kFewWarps * each)), (unsigned)tiles);
+    cfg.gridDim = dim3((unsigned)((across + wide4 - 1) / wide4), (unsigned)tiles);
     cfg.blockDim = dim3(kFewThreads), cfg.dynamicSmemBytes = C::kSmem, cfg.stream = s, cfg.attrs = &attr, cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(a.d_x), a.x_ld, x_vec, a.d_offsets, (int)a.experts, (int)a.rows,
                               (const uint8_t*)a.d_q, (const float*)a.d_scale, (int)a.in, (int)a.out, FastDiv(a.group / 32), groups,
                               static_cast<T*>(a.d_out), a.out_ld, (int)tile0, each);
   };
-  const int row_bytes = (a.in + 1) / 2;
-  // From six tiles an SM on.  At 3.4 (one expert of 8192 x 4096, groups of 32) the shared sum takes 17 us and the ring 21; at
-  // 6.7 (eight of 2048 x 1024) 11.3 and 8.7, with groups of 64 and eight rows each 9.3 and 10.4; at 13 (16 of 2048 x 512)
-  // 14.5 and 6.2.  In fp32 34 and 33, 20 and 12, 21 and 8.
-  const bool streams = likely * across >= (int64_t)device_sms() * 6 && reinterpret_cast<uintptr_t>(a.d_q) % 16 == 0 && row_bytes % 4 == 0;
   // (a grid has 65535 rows at most)
   for (int64_t at = 0; at < all; at += 65535) {
     const int64_t n = std::min<int64_t>(65535, all - at);
+    if constexpr (kPairs)
+      if (shared) {
+        const cudaError_t e = row_bytes % 16 == 0 ? stream(k_linear4_stream<T, NT, true, true>, at, n)
+                                                  : stream(k_linear4_stream<T, NT, false, true>, at, n);
+        if (e != cudaSuccess) return e;
+        continue;
+      }
     if (streams) {
-      const cudaError_t e = row_bytes % 16 == 0 ? stream(k_linear4_stream<T, NT, true>, at, n) : stream(k_linear4_stream<T, NT, false>, at, n);
+      const cudaError_t e = row_bytes % 16 == 0 ? stream(k_linear4_stream<T, NT, true, false>, at, n) : stream(k_linear4_stream<T, NT, false, false>, at, n);
       if (e != cudaSuccess) return e;
       continue;
     }

@@ -89,7 +89,9 @@ def test_product(E, shape, group, dtype, pad):
 MANY = [([1] * 6, 0, 32, 14000), ([1, 0, 3] * 4, 2, 1024, 9999), ([8] * 5, 1, 479, 16001), ([2, 1, 0, 5], 0, 2056, 20488),
         ([1] * 30, 1, 2600, 2890), ([1] * 8, 3, 515, 11000), ([16, 9, 12], 1, 1096, 26000), ([9] * 9, 0, 4160, 9001),
         ([33, 0, 17, 20], 3, 1160, 15003), ([64, 40], 0, 264, 30000), ([1, 2] * 60, 1, 96, 9000), ([17] * 60, 0, 200, 8005),
-        ([10, 16] * 40, 2, 352, 7010)]
+        ([10, 16] * 40, 2, 352, 7010),
+        # fewer: pairs of tiles of a CTA in fp32
+        ([1], 0, 4104, 8000), ([5, 1], 1, 1024, 3999), ([1, 1, 3], 0, 2600, 2009), ([9, 0, 16], 2, 1160, 3600), ([3] * 8, 0, 200, 1000)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
