@@ -396,8 +396,8 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
  *
  * An expert without rows has dW_e = 0; dw is overwritten.  act: silu g s(g), gelu g P(g) (P the normal
  * distribution), relu, or sigmoid s(g) = 1 / (1 + exp(-g)).  Everything is of `dtype`; dw is of dw_dtype
- * (F32, or as dtype).  bf16: exact products, fp32 sums, and the gated backward's dg, du rounded to bf16 once
- * as they enter its products.  F32: operands are split into three bf16 parts and the products of the
+ * (F32, or as dtype).  bf16: exact products, fp32 sums; the gated backward's dg, du enter an fp32 dw as they are (in
+ * fp32), dx and a bf16 dw less 2^-14 of each at most.  F32: operands are split into three bf16 parts and the products of the
  * larger six pairs summed in fp32, about as exact as an fp32 product; an infinite element makes what it
  * enters non-finite (infinite or NaN).
  * A weight matrix lies in rows of `in` elements (row step w_ld), or with w_turned in rows of `out` (2 out)

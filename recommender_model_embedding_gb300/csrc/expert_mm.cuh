@@ -65,6 +65,22 @@ __device__ __forceinline__ void split3(float v, float& a, float& b, float& c) {
   c = r - b;  // (rounded where it is stored)
 }
 
+// v = a + b + c once more, with parts of v's own sign of which none is zero unless v is: a is the bf16 below v in
+// magnitude, b the one below v - a, c what is left (eight bits at most, or one).  So an infinite factor times the
+// parts gives infinities of one sign, as it does times v.  Without c the parts are at most 2^-14 of v short of it.
+__device__ __forceinline__ void split3_below(float v, float& a, float& b, float& c) {
+  const auto below = [](float x) {
+    const uint32_t u = __float_as_uint(x), m = u & 0x7FFFFFFFu;
+    return __uint_as_float(m ? (u & 0x80000000u) | ((m - 1) & 0xFFFF0000u) : u);
+  };
+  a = b = c = v;
+  if (!(fabsf(v) <= 3.4028235e38f)) return;
+  a = below(v);
+  const float r = v - a;
+  b = below(r);
+  c = r - b;
+}
+
 // ---- activations ----
 
 // s(v) = 1 / (1 + exp(-v)): for fp32 results with CUDA's full exponential and quotient, for bf16 with the
@@ -125,7 +141,8 @@ struct PackArgs {
 constexpr int kMaxPacks = 3;
 cudaError_t launch_expert_packs(const PackArgs* args, int count, cudaStream_t s);  // all fp32, or all bf16
 // [dg, du] of a gated block's backward, to rows of 2 * p.out
-cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, bool beside, cudaStream_t s);  // (planes: to's)
+// (planes: three, or two for bf16 rows and results)
+cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, bool beside, cudaStream_t s);
 
 struct MmArgs {
   MmOperand a, b;

@@ -137,11 +137,11 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
     if (gated) a.gu = p.d_gu, a.gu_ld = p.gu_ld;
     return launch_expert_mm_rows(a, s);
   }
-  // [dg, du], or dout; an fp32 gradient of bf16 weights takes all of dg and du, dx their first plane
+  // [dg, du], or dout; of bf16 rows an fp32 dw takes all planes of dg and du, dx and a bf16 dw two
   MmOperand d, xo, wo;
   const bool dx = p.d_dx && S > 0;
   if (S > 0) {
-    if (gated) d = packed(room, O, S, 1, 1, f32 || (p.d_dw && p.dw_dtype == EMB_F32) ? 3 : 1);
+    if (gated) d = packed(room, O, S, 1, 1, f32 || (p.d_dw && p.dw_dtype == EMB_F32) ? 3 : 2);
     else d = operand({p.d_dout, f, S, p.dout_ld, 0, 0, 1, 1, last}, f32, room, packs);
     if (dx) wo = operand({p.d_w, p.w_turned ? O : in, p.w_turned ? in : O, p.w_ld, 0, p.w_step, 1, p.experts}, f32, room, packs);
     if (p.d_dw) xo = operand(x, f32, room, packs);
@@ -150,7 +150,7 @@ cudaError_t product(const emb_product& p, ProductKind kind, Room& room, bool lau
   }
   if (dx) {
     a.a = d, a.b = wo;
-    if (!f32) a.a.planes = 1;
+    if (!f32) a.a.planes = gated ? 2 : 1;
     a.b_mn = p.w_turned == 0;
     a.N = (int)in, a.K = (int)O;
     a.out = p.d_dx, a.out_ld = p.dx_ld, a.out_bf16 = !f32;

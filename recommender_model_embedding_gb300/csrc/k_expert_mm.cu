@@ -26,7 +26,7 @@
 // and the six products a_i b_j with i + j <= 2 are added; what is left out is below 2^-24 of the product.
 // The three planes of 64 K lie in the ring side by side, so each is brought once for its six products (with three
 // products, for an fp32 gradient of bf16 weights, such threes hold the copies up: 2.2 ms for 524288 x 2048 x 512 instead of
-// 1.9, so there each product has a stage).  The tensor core adds in fp32 but does not round to nearest, so an
+// 1.9, so there, and with two, each product has a stage).  The tensor core adds in fp32 but does not round to nearest, so an
 // error would grow with the length of the sum: fp32 results are therefore summed over parts of K in
 // registers, the small products' apart from the large one's (8192 rows of bf16: 9.1e-6 off in the 2-norm in one sum, 4.8e-7 in parts of 512).  bf16 results take the accumulator as it is (its error, below 2^-12 at K = 65536, is inside
 // bf16's rounding).
@@ -67,7 +67,7 @@ constexpr int kMmCols = 512;
 struct MmParams {
   const int32_t* offsets;
   int E, S, N, K, nt, mt;
-  int terms;            // products of planes: 1, 3 or 6
+  int terms;            // products of planes: 1, 2, 3 or 6
   uint32_t terms_a, terms_b;  // planes of each, four bits
   int tile_n;           // columns of a tile: 256 or 128
   int stages;
@@ -327,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
   let_next_start();
   const uint32_t tmem = *tmem_slot;
   const int tiles = prefix[p.E];
-  const int terms = SIX ? 6 : p.terms, tile_n = p.tile_n, slots = terms == 1 ? 1 : 3, stage_bytes = mm_stage(tile_n);  // slots: stages of 64 K
+  const int terms = SIX ? 6 : p.terms, tile_n = p.tile_n, slots = terms == 6 ? 3 : terms, stage_bytes = mm_stage(tile_n);  // slots: stages of 64 K
   Walk walk{cuts, prefix};
 
   // blocks of 64 along a tile's contraction; WGRAD: and its rows [r0, r1)
@@ -357,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const int n0 = GATED ? n * (tile_n / 2) : n * tile_n + (int)rank * (tile_n / 2);
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
-          // six products: the planes of each 64 K side by side; three: a part's first products, then its second ..
+          // six products: the planes of each 64 K side by side; two or three: a part's first products, then its second ..
           const int outer = terms == 6 ? c1 - c0 : slots, inner = terms == 6 ? slots : c1 - c0;
           for (int u = 0; ok && u < outer; ++u)
             for (int v = 0; v < inner; ++v) {
@@ -800,10 +800,10 @@ MmParams params_of(const MmArgs& a) {
   // products of the operands' planes (a, b), small ones first
   if (a.a.planes > 1 && a.b.planes > 1) {  // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
     p.terms = 6, p.terms_a = 0x001012, p.terms_b = 0x010210;
-  } else if (a.a.planes > 1) {             // (2,0) (1,0) (0,0)
-    p.terms = 3, p.terms_a = 0x012;
+  } else if (a.a.planes > 1) {             // (2,0) (1,0) (0,0), or without the first
+    p.terms = a.a.planes, p.terms_a = p.terms == 3 ? 0x012 : 0x01;
   } else if (a.b.planes > 1) {
-    p.terms = 3, p.terms_b = 0x012;
+    p.terms = a.b.planes, p.terms_b = p.terms == 3 ? 0x012 : 0x01;
   }
   p.out = a.out, p.out_ld = a.out_ld, p.out_step = a.out_step;
   p.gu = a.gu, p.gu_ld = a.gu_ld;

@@ -7,8 +7,9 @@
 // instead, and infinities and NaN stand in v0 alone.
 //
 // Gated block: from h = act(g) u, dg = dh u act'(g) and du = dh act(g), side by side as the product's
-// operand, rounded to bf16 as the tensor cores take them (for fp32 results, dw among them: three planes, for a
-// gradient in fp32 of [dg, du] rounded to bf16 is 2.6e-3 off in the 2-norm).  Both kernels are bound by HBM bandwidth:
+// operand, in planes too: rounded to bf16 they would put dx 1.7e-3 off in the 2-norm beside its own rounding, which is as much,
+// and an fp32 dw 2.6e-3.  fp32 rows, and an fp32 dw of bf16 rows, take three planes, bf16 results two (2^-14 of each element is
+// left out, their own rounding is up to 2^-8).  Both kernels are bound by HBM bandwidth:
 // 524288 x 1024 in bf16 to three planes 9.7 GB in 1.50 ms (6.4 TB/s, 95% of the measured copy rate); the planes of
 // 8198 x 479 rows and 12 x 1280 x 479 weights in fp32 113 MB in 24 us (4.7 TB/s, in L2 for the most part).
 #include <algorithm>
@@ -80,7 +81,8 @@ __device__ __forceinline__ void load_piece(const T* p, float (&v)[EPU]) {
   }
 }
 
-template <int PLANES, int EPU>
+// BELOW: parts of one sign, for products with a single plane
+template <int PLANES, bool BELOW, int EPU>
 __device__ __forceinline__ void store_piece(__nv_bfloat16* to, int64_t plane, const float (&v)[EPU]) {
   if constexpr (PLANES == 1) {
     Pack<__nv_bfloat16, EPU> o;
@@ -89,12 +91,15 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* to, int64_t plane, co
   } else {
     float a[EPU], b[EPU], c[EPU];
 #pragma unroll
-    for (int i = 0; i < EPU; ++i) split3(v[i], a[i], b[i], c[i]);
+    for (int i = 0; i < EPU; ++i)
+      if (BELOW) split3_below(v[i], a[i], b[i], c[i]);
+      else split3(v[i], a[i], b[i], c[i]);
     Pack<__nv_bfloat16, EPU> o;
     o.set(a);
     o.store(to);
     o.set(b);
     o.store(to + plane);
+    if (PLANES == 2) return;
     o.set(c);
     o.store(to + 2 * plane);
   }
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_expert_pack(const __grid_const
     for (int u = sub; u < units; u += 1 << shift) {
       float v[8];
       load_any8<T>(from + u * 8, a.inner - u * 8, lo, hi, v);
-      store_piece<PLANES, 8>(out + u * 8, a.to_plane, v);
+      store_piece<PLANES, false, 8>(out + u * 8, a.to_plane, v);
     }
   }
 }
@@ -149,7 +154,7 @@ template <typename T, int PLANES, int ACT, int EPU>
 __global__ void __launch_bounds__(kPrepThreads)
     k_expert_gated_bwd(const T* dh, int64_t dh_ld, const T* gu, int64_t gu_ld, const int32_t* last, uint32_t S, int f,
                        int shift, __nv_bfloat16* to, int64_t to_ld, int64_t to_plane, int beside) {
-  constexpr bool F32 = PLANES == 3;  // what is to be of fp32's exactness
+  constexpr bool F32 = PLANES == 3, BELOW = sizeof(T) == 2;  // F32: what is to be of fp32's exactness
   if (!beside) wait_for_earlier();
   let_next_start();
   const uint32_t per = kPrepThreads >> shift;
@@ -170,8 +175,8 @@ __global__ void __launch_bounds__(kPrepThreads)
         gv[i] = dv[i] * uv[i] * slope;
         uv[i] = dv[i] * a;
       }
-      store_piece<PLANES, EPU>(out + c * EPU, to_plane, gv);
-      store_piece<PLANES, EPU>(out + f + c * EPU, to_plane, uv);
+      store_piece<PLANES, BELOW, EPU>(out + c * EPU, to_plane, gv);
+      store_piece<PLANES, BELOW, EPU>(out + f + c * EPU, to_plane, uv);
     }
   }
   if (beside) wait_for_earlier();
@@ -229,7 +234,7 @@ cudaError_t launch_expert_gated_bwd(const emb_product& p, const MmOperand& to, b
     float* f = nullptr;
     if (p.dtype == EMB_F32) return vec ? run(k_expert_gated_bwd<float, 3, A, 8>, f) : run(k_expert_gated_bwd<float, 3, A, 1>, f);
     if (to.planes == 3) return vec ? run(k_expert_gated_bwd<H, 3, A, 8>, h) : run(k_expert_gated_bwd<H, 3, A, 1>, h);
-    return vec ? run(k_expert_gated_bwd<H, 1, A, 8>, h) : run(k_expert_gated_bwd<H, 1, A, 1>, h);
+    return vec ? run(k_expert_gated_bwd<H, 2, A, 8>, h) : run(k_expert_gated_bwd<H, 2, A, 1>, h);
   };
   switch (p.act) {
     case EMB_ACT_SILU: return by_act(std::integral_constant<int, EMB_ACT_SILU>());
