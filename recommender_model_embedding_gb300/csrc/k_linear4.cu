@@ -14,7 +14,7 @@
 // A CTA takes 16 outputs of one expert and its (up to 8, 16 or 32) rows; its eight warps share the
 // contraction and add up through shared memory in a fixed order.  Where outputs are many, each warp takes tiles of its
 // own and streams their codes through shared memory (k_linear4_stream; with fewer, in fp32, a CTA two tiles), or, where codes do not start on the boundaries that
-// its copies need, loads them for 64 (fp32 with 32 rows: 32) outputs at a time.
+// its copies need, loads them for 64 (with 32 rows: 32) outputs at a time.
 //
 // Measured, groups of 64: one row for each of two of eight experts of 2048 x 1024 3.3 us a call; 64 experts of that
 // with a row each 30 us in bf16 (37% of the copy rate) and 38 in fp32 (34 and 65 with loads in place of the ring); 25
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
               int in, int out_dim, int q_vec, int per_group, int groups, T* out, int64_t out_ld, int tile0) {
   constexpr int PLANES = sizeof(T) == 4 ? 3 : 1, RT = 8 * NT, SPAN = 32 * W;  // SPAN: k of a step
   __shared__ float sums[kFewWarps][RT][16 * MT + 1];
+  static_assert(sizeof(sums) <= 48 * 1024, "shared memory of a fixed size");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   wait_for_earlier();
   let_next_start();
@@ -442,8 +443,9 @@ __global__ void __launch_bounds__(256)
 template <typename T, int W, int NT>
 cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
   constexpr bool F32 = sizeof(T) == 4;
-  // Tiles of a warp at a time where these fill the SMs, else eight warps share one.
-  constexpr int MT = F32 && NT == 4 ? 2 : 4;
+  // Tiles of a warp at a time where these fill the SMs, else eight warps share one.  (Four of 32 rows would be 66,560 bytes of
+  // sums, above the 48 KB that shared memory of a fixed size may take.)
+  constexpr int MT = NT == 4 ? 2 : 4;
   // Steps loaded ahead.  Shared tiles: two, and where a warp has more of them four in bf16 (with two steps a warp, four
   // take longer for the masks: 3.6 -> 4.3 us for a single request; in fp32 they leave room for one CTA an SM: 1 x
   // 7616 x 3664 29 -> 46 us).  Alone: what registers for two CTAs an SM hold.
