@@ -398,8 +398,8 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
  * distribution), relu, or sigmoid s(g) = 1 / (1 + exp(-g)).  Everything is of `dtype`; dw is of dw_dtype
  * (F32, or as dtype).  bf16: exact products, fp32 sums; the gated backward's dg, du enter an fp32 dw as they are (in
  * fp32), dx and a bf16 dw less 2^-14 of each at most.  F32: operands are split into three bf16 parts and the products of the
- * larger six pairs summed in fp32, about as exact as an fp32 product; an infinite element makes what it
- * enters non-finite (infinite or NaN).
+ * larger six pairs summed in fp32, about as exact as an fp32 product; infinite and NaN elements give what the
+ * formula gives (of elements not below 2^-126, which may count as zero beside an infinite one).
  * A weight matrix lies in rows of `in` elements (row step w_ld), or with w_turned in rows of `out` (2 out)
  * elements, one for each input; experts w_step elements apart (0: the same matrix).  dw likewise by dw_ld,
  * dw_turned, dw_step, its matrices apart.

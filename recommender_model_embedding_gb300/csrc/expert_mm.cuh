@@ -65,6 +65,13 @@ __device__ __forceinline__ void split3(float v, float& a, float& b, float& c) {
   c = r - b;  // (rounded where it is stored)
 }
 
+// What the products of the small parts add to that of the large ones, for fp32 operands.  An infinite or NaN element
+// stands in its large part alone, and the large parts' product is then what the definition gives (a large part is zero
+// only with its element); the small ones' is not, infinity times a part of zero is NaN: it is left out.
+__device__ __forceinline__ float with_small(float large, float small) {
+  return fabsf(large) <= 3.4028235e38f ? large + small : large;
+}
+
 // v = a + b + c once more, with parts of v's own sign of which none is zero unless v is: a is the bf16 below v in
 // magnitude, b the one below v - a, c what is left (eight bits at most, or one).  So an infinite factor times the
 // parts gives infinities of one sign, as it does times v.  Without c the parts are at most 2^-14 of v short of it.

@@ -38,20 +38,20 @@ struct FewParams {
 template <typename T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
 
-// Products of a step's fragments; fp32: all planes with i + j <= 2, small ones first, and their sum added in fp32 (the
-// matrix instruction does not round to nearest: summed in it alone 1487 elements were 1.3e-6 off).
+// Products of a step's fragments; fp32: all planes with i + j <= 2, the small ones' sum apart from the large one, and both
+// added in fp32 (the matrix instruction does not round to nearest: summed in it alone 1487 elements were 1.3e-6 off).
 template <int PLANES>
 __device__ __forceinline__ void few_mma(float (&c)[4], const uint32_t (&a)[PLANES][4], const uint32_t (&b)[PLANES][2]) {
   if constexpr (PLANES == 3) {
-    float d[4] = {};
+    float d[4] = {}, large[4] = {};
     mma16816(d, a[2], b[0][0], b[0][1]);
     mma16816(d, a[1], b[1][0], b[1][1]);
     mma16816(d, a[0], b[2][0], b[2][1]);
     mma16816(d, a[1], b[0][0], b[0][1]);
     mma16816(d, a[0], b[1][0], b[1][1]);
-    mma16816(d, a[0], b[0][0], b[0][1]);
+    mma16816(large, a[0], b[0][0], b[0][1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] += d[i];
+    for (int i = 0; i < 4; ++i) c[i] += with_small(large[i], d[i]);
   } else {
     mma16816(c, a[0], b[0][0], b[0][1]);
   }

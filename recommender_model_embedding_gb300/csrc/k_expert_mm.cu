@@ -483,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                 if (sa >= stages) sa -= stages;
                 if (sb >= stages) sb -= stages;
                 if (t == 5) {
-                  // the large sum's half is read last of a part
+                  // (the large sum's half, which is read first of a part)
                   if (left == part && !(ok = mbar_wait_bounded(dempty + 1, dphase))) break;
                   if (left > 64 && stages >= 6) {
                     // the next copies, waited for while the tensor core still has work (their stages are others)
@@ -572,8 +572,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
           ok = ok && mbar_wait_bounded(dfull + buf, dphase);
           tc_fence_after();
           __syncwarp();
-          // six products: the small ones' sum from the upper half, which is given back at once, then the large one's
-          for (int half = SIX; half >= 0; --half) {
+          // six products: the large one's sum from the lower half, then the small ones' from the upper
+#pragma unroll
+          for (int half = 0; half <= (int)SIX; ++half) {
             const uint32_t from = lanes + (SIX ? half : buf) * 256;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -581,7 +582,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
               float v[16];
               tmem_ld16(from + (i < 2 ? at0 : at1) + (i & 1) * 16, v);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) (i < 2 ? v0 : v1)[(i & 1) * 16 + j] += v[j];
+              for (int j = 0; j < 16; ++j) {
+                float& sum = (i < 2 ? v0 : v1)[(i & 1) * 16 + j];
+                sum = half ? with_small(sum, v[j]) : sum + v[j];
+              }
             }
             release(SIX ? 1 - half : buf);
           }
