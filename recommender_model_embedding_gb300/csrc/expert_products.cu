@@ -43,12 +43,13 @@ struct Packs {
   int count = 0;
 };
 
-// A matrix as the tensor cores take it: in place, or as a copy.
-MmOperand operand(const Source& m, bool f32, Room& room, Packs& packs) {
+// A matrix as the tensor cores take it: in place, or as a copy.  One matrix for all experts is one matrix.
+MmOperand operand(Source m, bool f32, Room& room, Packs& packs) {
   MmOperand o;
+  if (m.expert_step == 0) m.experts = 1;
   if (!f32 && reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && (m.rows <= 1 || (m.ld % 8 == 0 && m.ld >= m.inner)) &&
       (m.halves == 1 || (m.half_step % 8 == 0 && m.half_step > 0)) &&
-      (m.experts == 1 || (m.expert_step % 8 == 0 && m.expert_step > 0 && m.expert_step < (int64_t)1 << 38))) {
+      (m.experts == 1 || (m.expert_step % 8 == 0 && m.expert_step < (int64_t)1 << 38))) {
     o.p = static_cast<const __nv_bfloat16*>(m.p);
     o.inner = m.inner, o.rows = m.rows, o.ld = m.ld, o.half_step = m.half_step, o.expert_step = m.expert_step;
     o.halves = m.halves, o.experts = m.experts;

@@ -77,6 +77,7 @@ struct MmParams {
   int beside;           // starts beside the launch before it, and waits for that at its own end
   uint32_t idesc;
   int b_mn;
+  int b_each;           // rows product: every expert has a matrix of its own
   void* out;
   int64_t out_ld, out_step;
   void* gu;
@@ -384,13 +385,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                 tma_box(&bmap, b, bar, n0, k, 0, 0, pb);
                 if (tile_n > 128) tma_box(&bmap, b + 8192, bar, n0 + 64, k, 0, 0, pb);
               } else {
-                const int half = GATED ? (int)rank : 0;
+                const int half = GATED ? (int)rank : 0, of = p.b_each ? e : 0;
                 tma_box(&amap, a, bar, kb * 64, m0, 0, 0, pa);
                 if (p.b_mn) {
-                  tma_box(&bmap, b, bar, n0, kb * 64, half, e, pb);
-                  if (tile_n > 128) tma_box(&bmap, b + 8192, bar, n0 + 64, kb * 64, half, e, pb);
+                  tma_box(&bmap, b, bar, n0, kb * 64, half, of, pb);
+                  if (tile_n > 128) tma_box(&bmap, b + 8192, bar, n0 + 64, kb * 64, half, of, pb);
                 } else {
-                  tma_box(&bmap, b, bar, kb * 64, n0, half, e, pb);
+                  tma_box(&bmap, b, bar, kb * 64, n0, half, of, pb);
                 }
               }
               if (++stage == stages) stage = 0, phase ^= 1;
@@ -832,7 +833,7 @@ cudaError_t launch_expert_mm_rows(const MmArgs& a, cudaStream_t s) {
   p.tile_n = 5 * rounds(256) > 3 * rounds(128) ? 128 : 256;
   p.nt = (int)((N + p.tile_n - 1) / p.tile_n), p.mt = 1;
   if (gated) p.nt = (a.N + p.tile_n / 2 - 1) / (p.tile_n / 2);
-  p.b_mn = a.b_mn;
+  p.b_mn = a.b_mn, p.b_each = a.b.experts > 1;
   p.idesc = mm_idesc(false, a.b_mn, p.tile_n);
   p.chunk = a.f32 ? 8 : 1 << 20;
   const int64_t most = down * p.nt;
