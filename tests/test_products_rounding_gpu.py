@@ -85,3 +85,65 @@ def test_infinities_of_the_gated_backward(E, dw_type):
     dw[0, :, 11] = 0
     dw[1, :, 12] = 0
     assert dx.isfinite().all() and dw.isfinite().all()
+
+
+def rms(a, b, counts, by):
+    """Norm of the roots of the sums of the products' squares."""
+    return by(a.double() ** 2, b.double() ** 2, counts)[0].sqrt()
+
+
+def of_fp32(K):
+    """What a sum of K fp32 products is off by, of the root of their squares' sum: 2^-22 of each product left out; parts of
+    512, to which the tensor core adds 16 products at a time and cuts off up to a step of 2^-23 of the sum so far, half of
+    one on average (its own rounding a step at most); each part's and the last rounding, 2^-24."""
+    return 2.0 ** -22 + 32 * 2.0 ** -24 + (-(-K // 512) + 1) * 2.0 ** -24
+
+
+def of_bf16(K):
+    """One sum of K exact products: half a step of 2^-23 for each 16."""
+    return -(-K // 16) * 2.0 ** -24
+
+
+LONG = [([300, 0, 412], 96, 64), ([700], 8192, 72), ([257, 300], 2056, 8), ([8192], 64, 136), ([5000, 11000], 520, 40), ([2], 8192, 64), ([20, 9], 2056, 40)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=NAMES.get)
+@pytest.mark.parametrize("counts,i,o", LONG)
+def test_linear(E, counts, i, o, dtype):
+    """Both directions, an fp32 dw of bf16 rows among them (its parts are of 512 rows as well)."""
+    g, n, off = gen(23), sum(counts), offsets_of(counts)
+    of = of_fp32 if dtype == F32 else of_bf16
+    x, dout, w = rows(n, i, dtype, g), rows(n, o, dtype, g), weights(len(counts), o, i, dtype, g)
+    out, dx, dw = torch.empty_like(dout), torch.empty_like(x), torch.empty((len(counts), o, i), device="cuda")
+    E.expert_linear(x, w, out, offsets=off)
+    E.expert_linear_backward(dout, x, w, dx, dw, offsets=off)
+    wt = w.transpose(1, 2)
+    assert off_by(out, by_expert(x, w, counts)[0]) <= 2 * of(i) * rms(x, w, counts, by_expert).norm()
+    assert off_by(dx, by_expert(dout, wt, counts)[0]) <= 2 * of(o) * rms(dout, wt, counts, by_expert).norm()
+    assert off_by(dw, by_rows(dout, x, counts)[0]) <= 2 * of_fp32(max(counts)) * rms(dout, x, counts, by_rows).norm()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=NAMES.get)
+@pytest.mark.parametrize("counts", [[2], [300]], ids=["few", "many"])
+def test_longest_rows(E, counts, dtype):
+    """65536 inputs, as many as there can be: in bf16 the one sum's error, 2^-12, is still inside the result's rounding."""
+    test_linear(E, counts, 65536, 40, dtype)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("counts,i,f", [([300, 0, 412], 96, 64), ([700], 4096, 72), ([8192], 64, 136), ([20, 9], 2056, 40)])
+def test_gated_in_fp32(E, counts, i, f, act):
+    """h from g and u as they are (errors times |act'| |u| <= 1.13 |u| and |act|), the exponential's 2^-21; the gradients'
+    [dg, du] 2^-20 off."""
+    x, dh, gu, w, dgu = gated_case(counts, i, f, F32, 24, act)
+    off, h = offsets_of(counts), torch.empty_like(dh)
+    E.expert_gated(x, w, h, offsets=off, act=act)
+    y, q = by_expert(x, w, counts)[0], rms(x, w, counts, by_expert)
+    a, u = act64(act, y[:, :f])[0], y[:, f:]
+    d = of_fp32(i) * (1.13 * u.abs() * q[:, :f] + a.abs() * q[:, f:]) + 2.0 ** -21 * u.abs() * (a.abs() + 1e-3)
+    assert off_by(h, a * u) <= 2 * d.norm()
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    E.expert_gated_backward(dh, gu, x, w, dx, dw, offsets=off, act=act)
+    wt = w.transpose(1, 2)
+    assert off_by(dx, by_expert(dgu, wt, counts)[0]) <= 2 * (of_fp32(2 * f) + 2.0 ** -20) * rms(dgu, wt, counts, by_expert).norm()
+    assert off_by(dw, by_rows(dgu, x, counts)[0]) <= 2 * (of_fp32(max(counts)) + 2.0 ** -20) * rms(dgu, x, counts, by_rows).norm()
