@@ -384,8 +384,9 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
 /* Experts' products: rows sorted by expert (emb_expert_sort, emb_expert_dispatch) through each
  * expert's own weights, without the host learning how many rows an expert has.  Expert e's rows are
  * [offsets[e], offsets[e+1]) of x; d_offsets is int32 [experts + 1] as emb_expert_sort writes it, or
- * NULL for one dense layer (experts = 1, all rows).  Rows of no expert are neither read nor
- * written.  Offsets have to ascend within [0, rows]: others lead to unspecified results, but never outside
+ * NULL for one dense layer (experts = 1, all rows).  Rows of no expert are not written, and nothing of
+ * them reaches a result (they may be read).  No output may lie over an input, dx over x or dout among
+ * them.  Offsets have to ascend within [0, rows]: others lead to unspecified results, but never outside
  * the buffers.
  *
  *   linear  out[r] = W_e x[r]                              W_e [out][in]
@@ -396,15 +397,16 @@ emb_status emb_gated_norm_backward(const emb_norm* args, void* d_ws, int64_t ws_
  *
  * An expert without rows has dW_e = 0; dw is overwritten.  act: silu g s(g), gelu g P(g) (P the normal
  * distribution), relu, or sigmoid s(g) = 1 / (1 + exp(-g)).  Everything is of `dtype`; dw is of dw_dtype
- * (F32, or as dtype).  bf16: exact products, fp32 sums; the gated backward's dg, du enter an fp32 dw as they are (in
- * fp32), dx and a bf16 dw less 2^-14 of each at most.  F32: operands are split into three bf16 parts and the products of the
- * larger six pairs summed in fp32, about as exact as an fp32 product; infinite and NaN elements give what the
- * formula gives (of elements not below 2^-126, which may count as zero beside an infinite one).
+ * (F32, or as dtype).  bf16: exact products, fp32 sums; the gated backward's dg, du enter an fp32 dw as they
+ * are (in fp32), dx and a bf16 dw less 2^-14 of each at most.  F32: operands are split into three bf16 parts and
+ * the products of the larger six pairs summed in fp32, about as exact as an fp32 product; infinite and NaN
+ * elements give what the formula gives (an element below 2^-126 may count as zero beside an infinite one).
  * A weight matrix lies in rows of `in` elements (row step w_ld), or with w_turned in rows of `out` (2 out)
  * elements, one for each input; experts w_step elements apart (0: the same matrix).  dw likewise by dw_ld,
  * dw_turned, dw_step, its matrices apart.
- * Workspace: what has to be copied for the tensor cores (fp32 operands, and rows or weights not on 16-byte
- * boundaries), the gated backward's [dg, du], and parts of dw; from the same arguments, pointers among
+ * Workspace: what has to be copied for the tensor cores (fp32 operands, 6 bytes an element, and rows or weights not
+ * on 16-byte boundaries), the gated backward's [dg, du] (rows of 2 out; 6 bytes an element for F32 and for an F32 dw,
+ * else 4: 6.4 GB for 524288 rows and out = 1024), and parts of dw; from the same arguments, pointers among
  * them (only their alignment is looked at).
  * EMB_EINVAL: rows outside [0, 2^31 - 1024], experts outside [1, EMB_EXPERT_MAX] or not 1 without offsets, in or
  * out outside [1, EMB_EXPERT_MAX_DIM], bad types, act or steps, a missing buffer (d_dx or d_dw may be

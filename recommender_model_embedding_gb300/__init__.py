@@ -385,7 +385,8 @@ def expert_linear(x, w, out, offsets=None, workspace=None, stream=None):
     expert_sort, int32 [experts + 1]; None: one dense layer).  x [S, in] and out [S, out] float32 or
     bfloat16, rows any step apart; w [experts, out, in] (or [out, in]) of the same type, either its
     rows or its columns adjacent (so a transposed [experts, in, out] serves).  Rows of no expert
-    are left as they were.  The host does not wait for the offsets.  Asynchronous."""
+    are left as they were.  out may not lie over x (nor dx, below, over x or dout).  The host does not
+    wait for the offsets.  Asynchronous."""
     _tower.linear(x, w, out, offsets, workspace, stream)
 
 
@@ -406,7 +407,8 @@ def expert_gated(x, w, h, gu=None, offsets=None, act: str = "silu", workspace=No
 def expert_gated_backward(dh, gu, x, w, dx, dw, offsets=None, act: str = "silu", workspace=None,
                           stream=None):
     """Gradients of expert_gated from dh [S, f], and gu as the forward left it: dx [S, in], and dw
-    [experts, 2f, in] float32 or of w's type (overwritten).  Either may be None."""
+    [experts, 2f, in] float32 or of w's type (overwritten).  Either may be None.  The workspace holds
+    what dh makes of gu, 12 bytes for each element of dh (8 where x and dw, if any, are bfloat16)."""
     _tower.gated_backward(dh, gu, x, w, dx, dw, offsets, act, workspace, stream)
 
 

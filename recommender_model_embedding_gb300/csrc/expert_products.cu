@@ -95,7 +95,8 @@ void cut_wgrad(MmArgs& a, int64_t rows) {
 // every 32 rows of an expert, at a rate that falls with the rows it multiplies them by (64 experts of 1024 x
 // 512 in bf16: 15 us with 8 rows, 22 with 16, 32 with 32); the tiles' kernel takes longer to get going and
 // some 3 us for a tile, and reads them once for 256 rows (16 us for all three), for fp32 after copying them as
-// bf16 planes.
+// bf16 planes.  The host knows the rows' number and not whose they are, so all of it goes by the average: where most
+// rows are one expert's, this kernel reads that expert's weights (from L2) again for every 8, 16 or 32 of them.
 bool few(int64_t rows, int experts, int64_t outs, int64_t in, bool f32) {
   const int64_t each = (rows + experts - 1) / experts, passes = (each + 31) / 32;
   if (each > 128 || few_tiles(rows, experts, 8) > 65535) return false;

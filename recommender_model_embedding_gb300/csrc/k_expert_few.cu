@@ -13,8 +13,8 @@
 // the large kernel.
 //
 // Measured, one row for each of two of eight experts, 2 x 1024 x 512 bf16 weights: 2.9 us a call (8.9 through the large
-// kernel); 32 rows over eight experts of 512 x 1024: 3.7 us (11.0).  64 experts of 1024 x 512 with a row each, call after
-// call: 12.4 us for 67 MB of weights, 5.4 TB/s, much of it from L2, which can hold them.
+// kernel); 32 rows over eight experts of 512 x 1024: 3.7 us (11.0).  64 experts of 1024 x 512 with a row each, call
+// after call: 12.4 us for 67 MB of weights, 5.4 TB/s, much of it from L2, which can hold them.
 #include <algorithm>
 
 #include "expert_few.cuh"
@@ -38,8 +38,9 @@ struct FewParams {
 template <typename T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
 
-// Products of a step's fragments; fp32: all planes with i + j <= 2, the small ones' sum apart from the large one, and both
-// added in fp32 (the matrix instruction does not round to nearest: summed in it alone 1487 elements were 1.3e-6 off).
+// Products of a step's fragments; fp32: all planes with i + j <= 2, the small ones' sum apart from the large one, and
+// both added in fp32 (the matrix instruction does not round to nearest: summed in it alone 1487 elements were 1.3e-6
+// off).
 template <int PLANES>
 __device__ __forceinline__ void few_mma(float (&c)[4], const uint32_t (&a)[PLANES][4], const uint32_t (&b)[PLANES][2]) {
   if constexpr (PLANES == 3) {

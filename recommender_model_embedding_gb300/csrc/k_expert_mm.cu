@@ -25,18 +25,19 @@
 // fp32: each operand is split into three bf16 planes, v = v0 + v1 + v2 (eight significant bits each),
 // and the six products a_i b_j with i + j <= 2 are added; what is left out is below 2^-24 of the product.
 // The three planes of 64 K lie in the ring side by side, so each is brought once for its six products (with three
-// products, for an fp32 gradient of bf16 weights, such threes hold the copies up: 2.2 ms for 524288 x 2048 x 512 instead of
-// 1.9, so there, and with two, each product has a stage).  The tensor core adds in fp32 but does not round to nearest, so an
-// error would grow with the length of the sum: fp32 results are therefore summed over parts of K in
-// registers, the small products' apart from the large one's (8192 rows of bf16: 9.1e-6 off in the 2-norm in one sum, 4.8e-7 in parts of 512).  bf16 results take the accumulator as it is (its error, below 2^-12 at K = 65536, is inside
-// bf16's rounding).
+// products, for an fp32 gradient of bf16 weights, such threes hold the copies up: 2.2 ms for 524288 x 2048 x 512
+// instead of 1.9, so there, and with two, each product has a stage).  The tensor core adds in fp32 but does not round
+// to nearest, so an error would grow with the length of the sum: fp32 results are therefore summed over parts of K in
+// registers, the small products' apart from the large one's (8192 rows of bf16: 9.1e-6 off in the 2-norm in one sum,
+// 4.8e-7 in parts of 512).  bf16 results take the accumulator as it is (its error, below 2^-12 at K = 65536, is
+// inside bf16's rounding).
 //
 // Measured on bf16 rows of 64 experts: 524288 x 512 through 512 -> 2048 outputs gated, h alone 0.60 ms (1.8 PFLOP/s,
-// the products alone, nothing stored, 0.57), with g and u too 0.81 ms; 1024 -> 512 0.34 ms; dx 2048 -> 512
-// 0.69 ms; dW 2048 x 512 0.69 ms (1.6 PFLOP/s).  Those are a cool chip's: after seconds of such work the power
-// limit takes the clock from 2.07 to 1.5 GHz, and gated takes 0.67 and 0.95 ms, 1024 -> 512 0.38.  fp32, 65536 x 512 through
-// 1024 outputs: 0.29 ms.  With all operands in shared memory a stage takes the tensor
-// core 512 cycles and the loop 520; what is over that is waiting for copies while stores share the way to memory.
+// the products alone, nothing stored, 0.57), with g and u too 0.81 ms; 1024 -> 512 0.34 ms; a linear layer's dx 2048
+// -> 512 0.69 ms; dW 2048 x 512 0.69 ms (1.6 PFLOP/s).  Those are a cool chip's: after seconds of such work the power
+// limit takes the clock from 2.07 to 1.5 GHz, and gated takes 0.67 and 0.95 ms, 1024 -> 512 0.38.  fp32, 65536 x 512
+// through 1024 outputs: 0.29 ms.  With all operands in shared memory a stage takes the tensor core 512 cycles and the
+// loop 520; what is over that is waiting for copies while stores share the way to memory.
 #include <algorithm>
 #include <atomic>
 
@@ -184,8 +185,8 @@ struct Walk {
 // A warp's output: parts of 32 rows of 64 bytes (one row a lane: 32 bf16 or 16 fp32 values), staged in
 // its buffer.  Full parts of an output on 16-byte boundaries leave as one TMA copy each, which takes the
 // store out of the warp's hands (and out of the load-store pipe, which the tensor core's operands
-// share); parts at an expert's end go row by row, those at the last columns element by element.  Chunk c of row r lies at c ^ (r / 2 % 4), the
-// 64-byte swizzle, so that neither the lanes' writes nor reads collide.
+// share); parts at an expert's end go row by row, those at the last columns element by element.  Chunk c of row r
+// lies at c ^ (r / 2 % 4), the 64-byte swizzle, so that neither the lanes' writes nor reads collide.
 struct Writer {
   unsigned char* staging;
   int lane;
@@ -358,7 +359,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         const int n0 = GATED ? n * (tile_n / 2) : n * tile_n + (int)rank * (tile_n / 2);
         for (int c0 = 0; ok && c0 < blocks; c0 += p.chunk) {
           const int c1 = min(blocks, c0 + p.chunk);
-          // six products: the planes of each 64 K side by side; two or three: a part's first products, then its second ..
+          // six products: the planes of each 64 K side by side; two or three: a part's first products, then its
+          // second ..
           const int outer = terms == 6 ? c1 - c0 : slots, inner = terms == 6 ? slots : c1 - c0;
           for (int u = 0; ok && u < outer; ++u)
             for (int v = 0; v < inner; ++v) {

@@ -7,9 +7,9 @@
 // instead, and infinities and NaN stand in v0 alone.
 //
 // Gated block: from h = act(g) u, dg = dh u act'(g) and du = dh act(g), side by side as the product's
-// operand, in planes too: rounded to bf16 they would put dx 1.7e-3 off in the 2-norm beside its own rounding, which is as much,
-// and an fp32 dw 2.6e-3.  fp32 rows, and an fp32 dw of bf16 rows, take three planes, bf16 results two (2^-14 of each element is
-// left out, their own rounding is up to 2^-8).  Both kernels are bound by HBM bandwidth:
+// operand, in planes too: rounded to bf16 they would put dx 1.7e-3 off in the 2-norm beside its own rounding, which
+// is as much, and an fp32 dw 2.6e-3.  fp32 rows, and an fp32 dw of bf16 rows, take three planes, bf16 results two
+// (2^-14 of each element is left out, their own rounding is up to 2^-8).  Both kernels are bound by HBM bandwidth:
 // 524288 x 1024 in bf16 to three planes 9.7 GB in 1.50 ms (6.4 TB/s, 95% of the measured copy rate); the planes of
 // 8198 x 479 rows and 12 x 1280 x 479 weights in fp32 113 MB in 24 us (4.7 TB/s, in L2 for the most part).
 #include <algorithm>
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_expert_pack(const __grid_const
 }
 
 // EPU columns of each half at a time: eight, or where rows or halves are not on 16-byte boundaries one (neighbouring
-// lanes, neighbouring columns: pieces of eight of the shifted result cost more, 773 against some 390 us for 175347 x 471
-// gelu in bf16, for each column's activation comes twice).
+// lanes, neighbouring columns: pieces of eight of the shifted result cost more, 773 against some 390 us for 175347 x
+// 471 gelu in bf16, for each column's activation comes twice).
 template <typename T, int PLANES, int ACT, int EPU>
 __global__ void __launch_bounds__(kPrepThreads)
     k_expert_gated_bwd(const T* dh, int64_t dh_ld, const T* gu, int64_t gu_ld, const int32_t* last, uint32_t S, int f,

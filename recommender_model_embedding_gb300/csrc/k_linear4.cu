@@ -13,14 +13,15 @@
 //
 // A CTA takes 16 outputs of one expert and its (up to 8, 16 or 32) rows; its eight warps share the
 // contraction and add up through shared memory in a fixed order.  Where outputs are many, each warp takes tiles of its
-// own and streams their codes through shared memory (k_linear4_stream; with fewer, in fp32, a CTA two tiles), or, where codes do not start on the boundaries that
-// its copies need, loads them for 64 (with 32 rows: 32) outputs at a time.
+// own and streams their codes through shared memory (k_linear4_stream; with fewer, in fp32, a CTA two tiles), or,
+// where codes do not start on the boundaries that its copies need, loads them for 64 (with 32 rows: 32) outputs at a
+// time.
 //
 // Measured, groups of 64: one row for each of two of eight experts of 2048 x 1024 3.3 us a call; 64 experts of that
 // with a row each 30 us in bf16 (37% of the copy rate) and 38 in fp32 (34 and 65 with loads in place of the ring); 25
 // experts of 4200 x 5064, whose rows lie on 4-byte boundaries only, 130 and 173 (245 and 340).
-// An instruction is issued in 53 to 62% of the cycles there and DRAM busy for 23 to 32%: some 280 instructions for 128 codes
-// of 16 outputs, 140 of them for taking the codes apart and multiplying, hold it up before memory does.
+// An instruction is issued in 53 to 62% of the cycles there and DRAM busy for 23 to 32%: some 280 instructions for
+// 128 codes of 16 outputs, 140 of them for taking the codes apart and multiplying, hold it up before memory does.
 #include <algorithm>
 
 #include "expert_few.cuh"
@@ -85,8 +86,9 @@ __device__ __forceinline__ void load_codes(const uint8_t* q, int valid, bool vec
 }
 
 // W: words (of eight codes) that a lane takes of a step: 1, or 2 where groups of 64 and codes on
-// eight-byte boundaries allow it: the four lanes of an output stay inside a group.  NT: eights of rows.  U: steps loaded ahead.  share: warps
-// that share a tile's contraction; MT: tiles of 16 outputs of a warp, for which x is brought and split once.
+// eight-byte boundaries allow it: the four lanes of an output stay inside a group.  NT: eights of rows.  U: steps
+// loaded ahead.  share: warps that share a tile's contraction; MT: tiles of 16 outputs of a warp, for which x is
+// brought and split once.
 template <typename T, int W, int NT, int U, int share, int MT>
 __global__ void __launch_bounds__(kFewThreads, 2)
     k_linear4(const T* x, int64_t x_ld, int x_vec, const int32_t* offsets, int E, int S, const uint8_t* q, const float* scale,
@@ -184,10 +186,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 }
 
 // The same where outputs are many, codes start on a 16-byte boundary and their rows on 4-byte boundaries.  Each warp
-// has tiles of 16 outputs of its own, up to MT at a time, and streams their codes and scales through a ring in shared memory, four stages (of
-// 128 codes of 16 outputs) ahead of the one it multiplies; the CTA's rows of x lie beside them as the fragments they
-// are taken as, up to KC columns at a time, so that they are brought, and in fp32 split, once for all warps.  Codes come
-// in whole pieces of 16 bytes: four for an output's 64 bytes where rows start on such boundaries (WHOLE), else five.
+// has tiles of 16 outputs of its own, up to MT at a time, and streams their codes and scales through a ring in shared
+// memory, four stages (of 128 codes of 16 outputs) ahead of the one it multiplies; the CTA's rows of x lie beside
+// them as the fragments they are taken as, up to KC columns at a time, so that they are brought, and in fp32 split,
+// once for all warps.  Codes come in whole pieces of 16 bytes: four for an output's 64 bytes where rows start on such
+// boundaries (WHOLE), else five.
 constexpr int kRing4 = 5, kCodes4 = 128, kBytes4 = kCodes4 / 2;
 constexpr int kPitch4 = kBytes4 + 16;                     // from one output's codes to the next: eight rows meet no bank twice
 constexpr int kScales4 = 16 * kPitch4;                    // behind the codes, [step of 32 codes][output]
@@ -208,7 +211,8 @@ __device__ __forceinline__ void copy_ahead(uint32_t to, const void* from, int by
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 
-// SHARED: the CTA's tiles are all its warps', each of which takes every eighth stage of the columns; they add up at the end.
+// SHARED: the CTA's tiles are all its warps', each of which takes every eighth stage of the columns; they add up at
+// the end.
 template <typename T, int NT, bool WHOLE, bool SHARED>
 __global__ void __launch_bounds__(kFewThreads, 2)
     k_linear4_stream(const T* x, int64_t x_ld, int x_vec, const int32_t* offsets, int E, int S, const uint8_t* q, const float* scale,
@@ -443,8 +447,8 @@ __global__ void __launch_bounds__(256)
 template <typename T, int W, int NT>
 cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
   constexpr bool F32 = sizeof(T) == 4;
-  // Tiles of a warp at a time where these fill the SMs, else eight warps share one.  (Four of 32 rows would be 66,560 bytes of
-  // sums, above the 48 KB that shared memory of a fixed size may take.)
+  // Tiles of a warp at a time where these fill the SMs, else eight warps share one.  (Four of 32 rows would be 66,560
+  // bytes of sums, above the 48 KB that shared memory of a fixed size may take.)
   constexpr int MT = NT == 4 ? 2 : 4;
   // Steps loaded ahead.  Shared tiles: two, and where a warp has more of them four in bf16 (with two steps a warp, four
   // take longer for the masks: 3.6 -> 4.3 us for a single request; in fp32 they leave room for one CTA an SM: 1 x
@@ -480,13 +484,14 @@ cudaError_t run_linear4(const emb_product4& a, bool q_vec, cudaStream_t s) {
     if ((n <= C::MT || a.in <= C::KC) && cost(n) < cost(each)) each = n;
   const int row_bytes = (a.in + 1) / 2;
   const bool ring = reinterpret_cast<uintptr_t>(a.d_q) % 16 == 0 && row_bytes % 4 == 0;
-  // From six tiles an SM on.  At 3.4 (one expert of 8192 x 4096, groups of 32) the shared sum takes 17 us and the ring 21; at
-  // 6.7 (eight of 2048 x 1024) 11.3 and 8.7, with groups of 64 and eight rows each 9.3 and 10.4; at 13 (16 of 2048 x 512)
-  // 14.5 and 6.2.  In fp32 34 and 33, 20 and 12, 21 and 8.
+  // From six tiles an SM on.  At 3.4 (one expert of 8192 x 4096, groups of 32) the shared sum takes 17 us and the
+  // ring 21; at 6.7 (eight of 2048 x 1024) 11.3 and 8.7, with groups of 64 and eight rows each 9.3 and 10.4; at 13
+  // (16 of 2048 x 512) 14.5 and 6.2.  In fp32 34 and 33, 20 and 12, 21 and 8.
   const bool streams = ring && likely * across >= (int64_t)device_sms() * 6;
-  // Below that the ring's CTAs share their tiles, two at a time, where splitting rows of fp32 anew for each costs most: from two
-  // tiles an SM on (one expert of 8192 x 4096 37 us with the shared sum of single tiles and 26 with this, two of 2600 x 2600 25
-  // and 18; at 1.7, 4096 x 479, 4.1 and 4.5).  With 32 rows, and in bf16, it gains nothing (101 and 116, 12.7 and 14.6).
+  // Below that the ring's CTAs share their tiles, two at a time, where splitting rows of fp32 anew for each costs
+  // most: from two tiles an SM on (one expert of 8192 x 4096 37 us with the shared sum of single tiles and 26 with
+  // this, two of 2600 x 2600 25 and 18; at 1.7, 4096 x 479, 4.1 and 4.5).  With 32 rows, and in bf16, it gains
+  // nothing (101 and 116, 12.7 and 14.6).
   constexpr bool kPairs = F32 && NT <= 2;
   const bool shared = kPairs && ring && !streams && likely * across >= (int64_t)device_sms() * 2;
   if (shared) each = 2;

@@ -146,7 +146,10 @@ __device__ __forceinline__ float lanes_sum(float v, int tpr) {
 // therefore passes wait_for_earlier() before it touches anything that earlier work writes or
 // reads (it holds until that work has finished and its writes are visible; since every kernel
 // passes it, that covers all earlier work, not the last kernel's alone), and says
-// let_next_start() once its own CTAs may be joined.  Work of other kinds before or after such a
+// let_next_start() once its own CTAs may be joined.  A kernel that is launched `beside` the one
+// before it (of the same call, whose results it does not need) passes it at its end only: it starts
+// when every CTA of that kernel has said let_next_start(), which those say after their own wait, so all
+// work before that kernel has finished and is visible, and it ends after that kernel has.  Work of other kinds before or after such a
 // kernel (copies, kernels launched in the ordinary way) is ordered as always.
 __device__ __forceinline__ void wait_for_earlier() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
